@@ -61,7 +61,7 @@ typedef enum lm_status {
   LM_ERR_WORKSPACE = 7      /* workspace null or smaller than required */
 } lm_status;
 
-typedef enum lm_dtype { LM_F32 = 0, LM_I16 = 1, LM_F16 = 2 } lm_dtype;
+typedef enum lm_dtype { LM_F32 = 0, LM_I16 = 1, LM_F16 = 2, LM_BF16 = 3 } lm_dtype;
 
 typedef enum lm_pad_mode {
   LM_PAD_REFLECT = 0,   /* mirror about the edge sample, edge not repeated */
@@ -421,6 +421,237 @@ lm_status lm_mel_spectrogram_host(const lm_mel_plan *plan, const void *wave_host
                                   int64_t B, int64_t T, void *out_host, int32_t out_dtype,
                                   int64_t chunk_clips, void *workspace, size_t workspace_bytes,
                                   lm_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 4. linear layers (the source pages have no counterpart)                  */
+/* ------------------------------------------------------------------------ */
+
+typedef enum lm_activation {
+  LM_ACT_NONE = 0,
+  LM_ACT_RELU = 1,      /* max(z, 0) */
+  LM_ACT_GELU = 2,      /* z * (1 + erf(z / sqrt 2)) / 2 */
+  LM_ACT_GELU_TANH = 3, /* z * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))) / 2 */
+  LM_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} lm_activation;
+
+/*
+ * y = residual + scale * act(x W^T + bias), for features and states of a
+ * speech model that reads this library's log-mel frames.
+ *
+ *   x         device, [groups][rows][k], read through x_group_stride and
+ *             x_row_stride (elements, >= 0; k contiguous).  Rows may overlap:
+ *             a convolution over frames is a product with the windows of
+ *             [frames][n_mels] read in place, k = taps * n_mels and
+ *             x_row_stride = hop * n_mels.                      (read-only)
+ *   weight    device, [n][k], weight_row_stride elements apart. (read-only)
+ *   bias      device, [n] of bias_dtype, or NULL.               (read-only)
+ *   residual  device, [groups*rows][n] of dtype, residual_row_stride
+ *             elements apart, or NULL; may equal out (same row stride).
+ *   out       device, [groups*rows][n] of out_dtype, out_row_stride
+ *             elements apart; must not overlap the other inputs.
+ *   dtype     LM_F16 or LM_BF16: type of x, weight and residual.
+ *   bias_dtype  LM_F32 or dtype.
+ *   out_dtype   dtype or LM_F32.
+ *
+ * Products are summed in 32 bits; bias, activation, scale and residual are
+ * applied in 32 bits and rounded once to out_dtype.  k = 0 gives act(bias).
+ * Pointers are aligned to their element; where x and weight are 16-byte
+ * aligned with row and group strides that are multiples of 8 elements, tiles
+ * are fetched by TMA.
+ *
+ *   workspace device, >= lm_linear_workspace_size(args), 16-byte aligned,
+ *             filled with zeros before its first use; every call leaves the
+ *             counters in it at zero, so calls of this function in stream
+ *             order may share one.
+ *             Its first u32 is the device error word (lm_workspace_error).
+ *
+ * Errors: LM_ERR_INVALID_ARG (null, negative sizes or strides, unknown
+ * activation), LM_ERR_UNSUPPORTED (dtypes; n, k or groups*rows >= 2^31),
+ * LM_ERR_MISALIGNED, LM_ERR_WORKSPACE, LM_ERR_CUDA.  groups * rows * n == 0
+ * returns LM_OK and enqueues nothing.
+ */
+typedef struct lm_linear_args {
+  const void *x;
+  const void *weight;
+  const void *bias;
+  const void *residual;
+  void *out;
+  int64_t groups, rows, k, n;
+  int64_t x_group_stride, x_row_stride, weight_row_stride, residual_row_stride, out_row_stride;
+  int32_t dtype, bias_dtype, out_dtype, activation;
+  float scale;
+  int32_t reserved;
+} lm_linear_args;
+
+lm_status lm_linear_workspace_size(const lm_linear_args *args, size_t *bytes);
+lm_status lm_linear(const lm_linear_args *args, void *workspace, size_t workspace_bytes, lm_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 5. keys and values in 8 bits (the source pages have no counterpart)      */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A cache of keys and values for `rows` sequences (a clip's encoder frames,
+ * or a beam's tokens), held as signed 8-bit integers in blocks of `block`
+ * tokens, with one f32 scale per layer, block and head:
+ *     key = k8 * k_scale, value = v8 * v_scale.
+ * Row r's token t is in place t % block of block table[r][t / block].
+ *
+ *   k8, v8            device, [layers][blocks][heads][block][head_dim] int8,
+ *                     16-byte aligned
+ *   k_scale, v_scale  device, [layers][blocks][heads] f32
+ *   table             device, [rows][width] int32, block numbers.  An entry
+ *                     outside [0, blocks) counts as tokens that are absent;
+ *                     entries past a row's tokens are not used.
+ *   spare             device, [rows] int32, one block per row that no table
+ *                     entry names (lm_kv_reorder only; may be NULL otherwise)
+ *   lens              device, [rows] int32, tokens held before this step
+ *   head_dim          32, 64 or 128;  block 16, 32, 64 or 128
+ * Rows hold at most width * block tokens: what a step adds past that is
+ * dropped.  A negative length counts as 0.
+ */
+typedef struct lm_kv_cache {
+  int8_t *k8;
+  int8_t *v8;
+  float *k_scale;
+  float *v_scale;
+  int32_t *table;
+  int32_t *spare;
+  int32_t *lens;
+  int64_t blocks;
+  int32_t layers, rows, width, heads, head_dim, block;
+} lm_kv_cache;
+
+/*
+ * Appends tokens to one layer: row r's token i (i < counts[r], or < tokens
+ * where counts is NULL) goes to place lens[r] + i.  lens itself is not
+ * changed (every layer of a step appends at the same lengths).
+ *   scale' = max(scale of what the block holds, max |new| / 127), 1 where
+ *            that is 0;
+ *   what the block holds: q' = rint(q * (scale / scale')) where it grew;
+ *   new tokens:           q  = rint(x / scale').
+ * Ties round to even.  A NaN or infinity among a block's new tokens makes its
+ * scale infinite, so that the block's values read as NaN.
+ *
+ *   k, v     device, [rows][tokens][heads][head_dim] of dtype (LM_F16 or
+ *            LM_BF16), read through k_strides and v_strides: elements
+ *            between rows, tokens and heads; head_dim contiguous. (read-only)
+ *   counts   device, [rows] int32 new tokens, clamped to [0, tokens]; or NULL
+ *   k_values, v_values  both NULL, or device,
+ *            [rows][span][heads][head_dim] of dtype, 16-byte aligned, with
+ *            span = ((tokens - 1 + block - 1) / block + 1) * block:
+ *            what the cache then holds from the first token of the block that
+ *            lens[r] falls in; zeros past the row's last token.
+ * A row's blocks must not be shared with another row from the block that
+ * lens[r] falls in onwards.
+ *
+ * Errors: LM_ERR_INVALID_ARG, LM_ERR_UNSUPPORTED, LM_ERR_MISALIGNED,
+ * LM_ERR_CUDA.  rows == 0 or tokens == 0 enqueues nothing.
+ */
+lm_status lm_kv_append(const lm_kv_cache *cache, int32_t layer, const void *k, const void *v,
+                       const int64_t *k_strides, const int64_t *v_strides, int32_t tokens,
+                       const int32_t *counts, int32_t dtype, void *k_values, void *v_values,
+                       lm_stream_t stream);
+
+/*
+ * The values that tokens start .. start + count - 1 of every row stand for:
+ * k_out, v_out device, [layers or 1][rows][count][heads][head_dim] of dtype,
+ * 16-byte aligned; zeros from lens[r] on.  layer = -1 reads every layer.
+ * Errors as lm_kv_append.
+ */
+lm_status lm_kv_read(const lm_kv_cache *cache, int32_t layer, int32_t start, int32_t count, int32_t dtype,
+                     void *k_out, void *v_out, lm_stream_t stream);
+
+/*
+ * Attention over one layer of the cache, softmax(scale * q k^T) v per head.
+ *   q        device, [rows][tokens][q_heads][head_dim] of dtype (LM_F16,
+ *            LM_BF16), read through q_strides (rows, tokens, heads);
+ *            q_heads a multiple of the cache's heads: query head h reads
+ *            key head h / (q_heads / heads).                   (read-only)
+ *   counts   device, [rows] int32 or NULL: new tokens of this step that the
+ *            cache already holds past lens[r], clamped to [0, tokens];
+ *            NULL: new_tokens for every row.
+ *   causal   1: query i stands at token lens[r] + i and sees tokens up to
+ *            it; queries from counts[r] on see nothing.
+ *            0: every query sees the lens[r] + counts[r] tokens.
+ *   out      device, [rows][tokens][q_heads][head_dim] of dtype, contiguous,
+ *            16-byte aligned.  A query that sees nothing gives zeros.
+ *   workspace  device, >= lm_kv_attend_workspace_size(...), 16-byte aligned,
+ *            zeroed before its first use, left usable by every call (as for
+ *            lm_linear).
+ * Scores, softmax statistics and the sums are held in 32 bits.
+ * Errors as lm_kv_append, and LM_ERR_WORKSPACE.
+ */
+lm_status lm_kv_attend_workspace_size(const lm_kv_cache *cache, int32_t tokens, int32_t q_heads, size_t *bytes);
+lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const void *q, const int64_t *q_strides,
+                       int32_t tokens, int32_t q_heads, const int32_t *counts, int32_t new_tokens,
+                       int32_t causal, float scale, int32_t dtype, void *out, void *workspace,
+                       size_t workspace_bytes, lm_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 6. beam search (the source pages have no counterpart)                    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * One step of beam search: the `beams` best continuations of each clip.
+ * Beam i of a clip offers its tokens at
+ *     total = score[i] + ((x - max x) - log(sum exp(x - max x))),
+ * x the beam's logits; a finished beam offers eos alone, at its score.
+ * Best is the largest total; among equal totals the lower beam, then the
+ * larger logit, then the lower token.  A beam whose logits hold a NaN or
+ * +infinity, or nothing above -infinity, and a NaN total, count as -infinity
+ * (places that nothing better fills are taken by such continuations).
+ *
+ *   logits    device, [clips][beams][vocab] of dtype (LM_F32, LM_F16,
+ *             LM_BF16), rows row_stride elements apart.          (read-only)
+ *   scores    device, [clips][beams] f32                         (read-only)
+ *   finished  device, [clips][beams] u8 (0 or 1), or NULL: none  (read-only)
+ *   history   device, [clips][beams][width] int32, or NULL       (read-only)
+ *   length    place of the new token in the history, 0 <= length < width
+ *   eos       the token that ends a beam; -1: none
+ *   out_*     device, [clips][beams], best first: the totals f32, the tokens,
+ *             the beams they continue (0 .. beams-1), and whether they have
+ *             ended (u8): the continued beam had, or the token is eos.
+ *   out_history  [clips][beams][width]: the continued beam's history with
+ *             the token at `length` (NULL where history is); must not
+ *             overlap history.
+ *   beams     1..32;  vocab 1..2^31-1
+ *   workspace device, >= lm_beam_step_workspace_size(...), 16-byte aligned,
+ *             zeroed before its first use, left usable by every call.
+ * Errors as above.  clips == 0 enqueues nothing.
+ */
+typedef struct lm_beam_args {
+  const void *logits;
+  const float *scores;
+  const uint8_t *finished;
+  const int32_t *history;
+  float *out_scores;
+  int32_t *out_tokens;
+  int32_t *out_parents;
+  uint8_t *out_finished;
+  int32_t *out_history;
+  int64_t clips, vocab, row_stride, width, length, eos;
+  int32_t beams, dtype;
+} lm_beam_args;
+
+lm_status lm_beam_step_workspace_size(const lm_beam_args *args, size_t *bytes);
+lm_status lm_beam_step(const lm_beam_args *args, void *workspace, size_t workspace_bytes, lm_stream_t stream);
+
+/*
+ * Lets the cache follow a beam step: rows are clips * beams, and row (c, i)
+ * takes the tokens of row (c, parents[c][i]) (device, int32, each in
+ * [0, beams); others leave their row as it is).  Rows of a clip have the
+ * same length.  Whole blocks are shared by copying table entries; the block
+ * that the next token falls in, where it holds tokens, is copied for every
+ * layer into the row's spare block, which changes places with it.  A row
+ * that continues itself is left alone.
+ *   workspace device, >= 16 + 4 * clips bytes, 16-byte aligned, zeroed before
+ *             its first use, left usable by every call.
+ * Errors as above, and LM_ERR_INVALID_ARG where spare is NULL or rows is not
+ * a multiple of beams.
+ */
+lm_status lm_kv_reorder(const lm_kv_cache *cache, const int32_t *parents, int32_t beams, void *workspace,
+                        size_t workspace_bytes, lm_stream_t stream);
 
 #ifdef __cplusplus
 }

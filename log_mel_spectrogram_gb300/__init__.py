@@ -10,6 +10,9 @@ missing or the tensors are not on a CUDA device.
   from a complex STFT (KBench "audio_mel_spectrogram_fused" spec).
 * ``mel_spectrogram(wave, ...)`` / ``MelSpectrogram`` -- waveform to mel
   spectrogram with torchaudio-style arguments (flashmel page).
+* ``linear``, ``KvCache`` and ``beam_step`` (decode.py) -- what turns the
+  features into text: linear layers, attention over an 8-bit key/value cache,
+  beam search.
 """
 from __future__ import annotations
 
@@ -22,11 +25,12 @@ import torch
 
 from . import _native
 from ._native import LogmelError
+from .decode import BeamStep, KvCache, beam_step, linear
 
 __all__ = ["log_mel_from_stft", "log_mel_from_stft_workspace_size", "workspace_error", "LogmelError",
            "pack_mel_filters", "log_mel_from_stft_host", "log_mel_from_stft_host_workspace_size",
            "describe_log_mel_from_stft", "MelSpectrogram", "mel_spectrogram", "library_path",
-           "log_mel_from_stft_op", "mel_spectrogram_op"]
+           "log_mel_from_stft_op", "mel_spectrogram_op", "linear", "KvCache", "beam_step", "BeamStep"]
 
 
 def library_path():

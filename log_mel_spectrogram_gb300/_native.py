@@ -17,7 +17,7 @@ _lib = None
 LM_OK = 0
 STATUS_NAMES = {0: "LM_OK", 1: "LM_ERR_INVALID_ARG", 2: "LM_ERR_UNSUPPORTED", 3: "LM_ERR_MISALIGNED",
                 4: "LM_ERR_CUDA", 5: "LM_ERR_OUT_OF_MEMORY", 6: "LM_ERR_DEVICE_FAULT", 7: "LM_ERR_WORKSPACE"}
-DTYPES = {"f32": 0, "i16": 1, "f16": 2}
+DTYPES = {"f32": 0, "i16": 1, "f16": 2, "bf16": 3}
 PAD_MODES = {"reflect": 0, "constant": 1, "replicate": 2, "circular": 3}
 MEL_SCALES = {"htk": 0, "slaney": 1}
 
@@ -110,6 +110,25 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.lm_mel_spectrogram_host_workspace_size.restype = ctypes.c_int
     L.lm_mel_spectrogram_host.argtypes = [vp, vp, i32, i64, i64, vp, i32, i64, vp, sz, vp]
     L.lm_mel_spectrogram_host.restype = ctypes.c_int
+    # Argument structs of the entry points below are passed as packed bytes.
+    L.lm_linear_workspace_size.argtypes = [vp, vp]
+    L.lm_linear_workspace_size.restype = ctypes.c_int
+    L.lm_linear.argtypes = [vp, vp, sz, vp]
+    L.lm_linear.restype = ctypes.c_int
+    L.lm_kv_append.argtypes = [vp, i32, vp, vp, vp, vp, i32, vp, i32, vp, vp, vp]
+    L.lm_kv_append.restype = ctypes.c_int
+    L.lm_kv_read.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
+    L.lm_kv_read.restype = ctypes.c_int
+    L.lm_kv_attend_workspace_size.argtypes = [vp, i32, i32, vp]
+    L.lm_kv_attend_workspace_size.restype = ctypes.c_int
+    L.lm_kv_attend.argtypes = [vp, i32, vp, vp, i32, i32, vp, i32, i32, ctypes.c_float, i32, vp, vp, sz, vp]
+    L.lm_kv_attend.restype = ctypes.c_int
+    L.lm_kv_reorder.argtypes = [vp, vp, i32, vp, sz, vp]
+    L.lm_kv_reorder.restype = ctypes.c_int
+    L.lm_beam_step_workspace_size.argtypes = [vp, vp]
+    L.lm_beam_step_workspace_size.restype = ctypes.c_int
+    L.lm_beam_step.argtypes = [vp, vp, sz, vp]
+    L.lm_beam_step.restype = ctypes.c_int
     return L
 
 

@@ -1,56 +1,458 @@
-// linear.cu -- y = residual + scale * act(x W^T + bias).
+// linear.cu -- y = residual + scale * act(x W^T + bias) on the tensor cores.
 //
-// One thread per output element, operands through 16 x 16 tiles of shared
-// memory, sums in 32 bits.
+// A CTA computes tiles of 128 x bn outputs: one thread fetches 128 x 64 and
+// bn x 64 operand tiles by TMA into a ring of shared-memory stages, one thread
+// issues tcgen05.mma into tensor memory (32-bit sums), the other warps turn a
+// finished tile into outputs while the next one is summed into the other half
+// of the tensor memory.  CTAs are persistent: one per SM walks the tiles.
+//
+// The tile has two orientations.
+//  - rows of x along the 128 lanes: a lane holds 16 consecutive outputs of a
+//    row, i.e. whole 32-byte sectors per thread.  Taken where outputs (and the
+//    residual) can be accessed in 16-byte vectors and there are enough rows.
+//  - rows of W along the lanes: x fills the other side of the tile with
+//    exactly the rows there are (bn = 16 .. 256), so few rows do not waste
+//    products, and lanes are consecutive outputs, so odd row lengths still
+//    store whole lines.
+// Few tiles (decoding steps) split k over a cluster of CTAs, whose partial sums
+// meet in distributed shared memory in rank order: one launch, and the same
+// result on every call.
+//
+// Operands that TMA cannot address (rows off 16-byte boundaries) are first
+// copied into padded rows in the workspace.
 #include <climits>
+#include <cuda.h>
 
 #include "half.cuh"
 #include "internal.h"
 #include "ptx.cuh"
+#include "tcgen05.cuh"
 
 namespace lm {
 namespace {
 
-constexpr int kTile = 16;
+constexpr int kBk = 64;             // elements of k per stage: one 128-byte swizzle row
+constexpr int kLanes = 128;         // rows of the tile's lane side
+constexpr int kMaxBn = 256;
+constexpr int kMaxStages = 8;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;  // TMA, MMA, TMEM and one idle warp; then the epilogue
+constexpr int kSmemBudget = 227 * 1024 - 1024 - 4096;
 
-__device__ __forceinline__ float activate(float z, int act) {
-  switch (act) {
-    case LM_ACT_RELU: return fmaxf(z, 0.0f);
-    case LM_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    case LM_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-    case LM_ACT_SILU: return z / (1.0f + expf(-z));
-    default: return z;
+struct LinearParams {
+  const void *bias, *residual;
+  void *out;
+  int64_t out_row, res_row;
+  int64_t rows_total;         // rows of the output
+  int32_t rows, k, n;         // rows per group
+  int32_t bn, stages, kblocks, tmem_cols;
+  int32_t lane_tiles, col_tiles, tiles;  // tiles along the lanes and columns of one group, and in all
+  int32_t splits;             // CTAs that share a tile's k
+  int32_t bias_f32, out_f32, act, vec32;
+  uint32_t idesc;
+  float scale;
+  uint32_t *err;
+};
+
+struct Barriers {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+};
+
+// erf by formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
+// Functions: off by at most 1.5e-7.
+__device__ __forceinline__ float erf_as(float x) {
+  const float a = fabsf(x);
+  const float t = __fdividef(1.0f, fmaf(0.3275911f, a, 1.0f));
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  return copysignf(1.0f - p * t * __expf(-a * a), x);
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if (ACT == LM_ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays
+  if (ACT == LM_ACT_GELU) {
+    const float h = 0.5f * z;
+    return fmaf(h, erf_as(z * 0.70710678118654752f), h);
+  }
+  if (ACT == LM_ACT_GELU_TANH) {
+    // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
+    const float u = 0.79788456080286536f * fmaf(0.044715f * z * z, z, z);
+    return z * __fdividef(1.0f, 1.0f + __expf(-2.0f * u));
+  }
+  if (ACT == LM_ACT_SILU) return z * __fdividef(1.0f, 1.0f + __expf(-z));
+  return z;
+}
+
+__device__ __forceinline__ uint4 ldg_v4(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
+
+// 16 consecutive 16-bit values as f32, in 16-byte loads.
+template <typename T>
+__device__ __forceinline__ void load16(const T *p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 w = ldg_v4(p + 8 * i);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack2<T>(u[j]);
+      x[8 * i + 2 * j] = f.x;
+      x[8 * i + 2 * j + 1] = f.y;
+    }
+  }
+}
+
+__device__ __forceinline__ void store_v8(void *p, const uint32_t (&w)[8], bool vec32) {
+  if (vec32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
 template <typename T>
-__global__ void linear_kernel(const lm_linear_args a) {
-  __shared__ float xs[kTile][kTile + 1], ws[kTile][kTile + 1];
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kTile + threadIdx.x;
-  const int64_t m = static_cast<int64_t>(blockIdx.y) * kTile + threadIdx.y;
-  const int64_t rows = a.groups * a.rows;
-  const int64_t nl = static_cast<int64_t>(blockIdx.x) * kTile + threadIdx.y;
-  const T *const x = static_cast<const T *>(a.x) + m / a.rows * a.x_group_stride + m % a.rows * a.x_row_stride;
-  const T *const w = static_cast<const T *>(a.weight) + nl * a.weight_row_stride;
-  float s = 0.0f;
-  for (int64_t k0 = 0; k0 < a.k; k0 += kTile) {
-    const int64_t k = k0 + threadIdx.x;
-    xs[threadIdx.y][threadIdx.x] = m < rows && k < a.k ? to_f32(x[k]) : 0.0f;
-    ws[threadIdx.y][threadIdx.x] = nl < a.n && k < a.k ? to_f32(w[k]) : 0.0f;
-    __syncthreads();
-    for (int j = 0; j < kTile; ++j) s += xs[threadIdx.y][j] * ws[threadIdx.x][j];
-    __syncthreads();
-  }
-  if (m >= rows || n >= a.n) return;
-  if (a.bias)
-    s += a.bias_dtype == LM_F32 ? static_cast<const float *>(a.bias)[n] : to_f32(static_cast<const T *>(a.bias)[n]);
-  s = a.scale * activate(s, a.activation);
-  if (a.residual) s += to_f32(static_cast<const T *>(a.residual)[m * a.residual_row_stride + n]);
-  if (a.out_dtype == LM_F32) {
-    static_cast<float *>(a.out)[m * a.out_row_stride + n] = s;
+__device__ __forceinline__ float bias_at(const LinearParams &p, int n) {
+  if (!p.bias || n >= p.n) return 0.0f;
+  return p.bias_f32 ? static_cast<const float *>(p.bias)[n] : to_f32(static_cast<const T *>(p.bias)[n]);
+}
+
+// One output element of the lane = W orientation.
+template <typename T, int ACT>
+__device__ __forceinline__ void put(const LinearParams &p, float acc, float bias, int64_t row, int n) {
+  float y = p.scale * activate<ACT>(acc + bias);
+  if (p.residual) y += to_f32(static_cast<const T *>(p.residual)[row * p.res_row + n]);
+  if (p.out_f32) {
+    static_cast<float *>(p.out)[row * p.out_row + n] = y;
   } else {
-    static_cast<T *>(a.out)[m * a.out_row_stride + n] = from_f32<T>(s);
+    static_cast<T *>(p.out)[row * p.out_row + n] = from_f32<T>(y);
   }
+}
+
+// The 16 columns in `r` of a lane's tile row.
+template <typename T, int ACT, bool SWAP>
+__device__ __forceinline__ void finish16(const LinearParams &p, const uint32_t (&r)[16], const float *bias_s,
+                                         float lane_bias, int64_t group_row, int lane_at, int col_at) {
+  if (SWAP) {
+    if (lane_at >= p.n) return;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (col_at + j < p.rows) put<T, ACT>(p, __uint_as_float(r[j]), lane_bias, group_row + col_at + j, lane_at);
+    }
+    return;
+  }
+  if (lane_at >= p.rows || col_at >= p.n) return;
+  const int64_t row = group_row + lane_at;
+  float y[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) y[j] = p.scale * activate<ACT>(__uint_as_float(r[j]) + bias_s[j]);
+  if (col_at + 16 <= p.n) {
+    if (p.residual) {
+      float x[16];
+      load16(static_cast<const T *>(p.residual) + row * p.res_row + col_at, x);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[j] += x[j];
+    }
+    if (p.out_f32) {
+      float *const o = static_cast<float *>(p.out) + row * p.out_row + col_at;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(y[8 * i + j]);
+        store_v8(o + 8 * i, w, p.vec32);
+      }
+    } else {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = pack2<T>(y[2 * j], y[2 * j + 1]);
+      store_v8(static_cast<T *>(p.out) + row * p.out_row + col_at, w, p.vec32);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (col_at + j >= p.n) break;
+      float v = y[j];
+      if (p.residual) v += to_f32(static_cast<const T *>(p.residual)[row * p.res_row + col_at + j]);
+      if (p.out_f32) {
+        static_cast<float *>(p.out)[row * p.out_row + col_at + j] = v;
+      } else {
+        static_cast<T *>(p.out)[row * p.out_row + col_at + j] = from_f32<T>(v);
+      }
+    }
+  }
+}
+
+struct Tile {
+  int group, lane0, col0;
+};
+
+// Consecutive tiles share their rows along the lanes.
+__device__ __forceinline__ Tile tile_at(const LinearParams &p, int t) {
+  Tile o;
+  const int per = p.lane_tiles * p.col_tiles;
+  o.group = t / per;
+  const int u = t % per;
+  o.lane0 = u / p.col_tiles * kLanes;
+  o.col0 = u % p.col_tiles * p.bn;
+  return o;
+}
+
+// Turns tile `t` into outputs.  `acc` is the tile's tensor memory; warp e of
+// the epilogue reads lanes 32 * (e % 4) .. + 31 and every second 16 columns.
+template <typename T, int ACT, bool SWAP>
+__device__ __forceinline__ void epilogue(const LinearParams &p, const Tile &t, uint32_t acc, const float *bias_s, int e) {
+  const int lane = 32 * (e % 4) + static_cast<int>(threadIdx.x % 32);
+  const uint32_t base = acc + (static_cast<uint32_t>(32 * (e % 4)) << 16);
+  const int64_t group_row = static_cast<int64_t>(t.group) * p.rows;
+  const int at = t.lane0 + lane;
+  const float lane_bias = SWAP ? bias_at<T>(p, at) : 0.0f;
+  for (int c = e / 4 * 16; c < p.bn; c += kEpiWarps / 4 * 16) {
+    if (t.col0 + c >= (SWAP ? p.rows : p.n)) break;
+    uint32_t r[16];
+    if (p.kblocks > 0) {
+      tmem_ld16(base + c, r);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) r[j] = 0;
+    }
+    finish16<T, ACT, SWAP>(p, r, bias_s + c, lane_bias, group_row, at, t.col0 + c);
+  }
+}
+
+template <typename T, bool SWAP>
+__device__ __forceinline__ void epilogue_act(const LinearParams &p, const Tile &t, uint32_t acc, const float *bias_s,
+                                             int e) {
+  switch (p.act) {
+    case LM_ACT_RELU: epilogue<T, LM_ACT_RELU, SWAP>(p, t, acc, bias_s, e); break;
+    case LM_ACT_GELU: epilogue<T, LM_ACT_GELU, SWAP>(p, t, acc, bias_s, e); break;
+    case LM_ACT_GELU_TANH: epilogue<T, LM_ACT_GELU_TANH, SWAP>(p, t, acc, bias_s, e); break;
+    case LM_ACT_SILU: epilogue<T, LM_ACT_SILU, SWAP>(p, t, acc, bias_s, e); break;
+    default: epilogue<T, LM_ACT_NONE, SWAP>(p, t, acc, bias_s, e); break;
+  }
+}
+
+// The split form's outputs: columns of the tile are shared out over the
+// cluster's CTAs; every CTA's partial sums lie at the same place of its
+// shared memory, [column][lane].
+template <typename T, int ACT>
+__device__ __forceinline__ void finish_split(const LinearParams &p, const Tile &t, uint32_t partial, int rank, int tid,
+                                             int threads) {
+  const int64_t group_row = static_cast<int64_t>(t.group) * p.rows;
+  const int cols = min(p.bn, p.rows - t.col0);
+  for (int i = tid; i < kLanes * ((p.bn + p.splits - 1) / p.splits); i += threads) {
+    const int c = i / kLanes * p.splits + rank, lane = i % kLanes;
+    const int n = t.lane0 + lane;
+    if (c >= cols || n >= p.n) continue;
+    const uint32_t at = partial + static_cast<uint32_t>(c * kLanes + lane) * 4;
+    float s = 0.0f;
+    for (int r = 0; r < p.splits; ++r) s += __uint_as_float(ld_dsmem_u32(at, static_cast<uint32_t>(r)));
+    put<T, ACT>(p, s, bias_at<T>(p, n), group_row + t.col0 + c, n);
+  }
+}
+
+// Barrier of the epilogue's warps: whether `ok` holds for all their threads.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u), "n"(32 * kEpiWarps)
+      : "memory");
+  return r != 0;
+}
+
+template <typename T, bool SWAP, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap lane_map, const __grid_constant__ CUtensorMap col_map,
+                  const LinearParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  // Stages start on a 1024-byte boundary (the swizzle's period).
+  uint8_t *const ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int stage_bytes = kLanes * 128 + p.bn * 128;
+  Barriers &b = *reinterpret_cast<Barriers *>(ring + p.stages * stage_bytes);
+  float *const bias_s = reinterpret_cast<float *>(&b + 1);  // two tiles of bn
+  const int warp = threadIdx.x / 32;
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = SPLIT ? static_cast<int>(blockIdx.x) / p.splits : static_cast<int>(blockIdx.x);
+  const int step = SPLIT ? p.tiles : static_cast<int>(gridDim.x);
+  // This CTA's part of k.
+  const int k_begin = SPLIT ? static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / p.splits) : 0;
+  const int k_end = SPLIT ? static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / p.splits) : p.kblocks;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&b.full[i], 1);
+      mbar_init(&b.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.acc_full[i], 1);
+      mbar_init(&b.acc_empty[i], 32 * kEpiWarps);
+    }
+    mbar_init(&b.drain, 1);
+    b.abort = 0;
+    fence_mbar_init();
+    if (p.kblocks > 0) {
+      tma_prefetch_map(&lane_map);
+      tma_prefetch_map(&col_map);
+    }
+  }
+  if (warp == 2) {
+    tmem_alloc(&b.tmem, static_cast<uint32_t>(p.tmem_cols));
+    tmem_relinquish();
+  }
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  const uint32_t tmem = b.tmem;
+  volatile int *const abort = &b.abort;
+
+  if (warp == 0) {
+    if (threadIdx.x == 0) {
+      int fills = 0;
+      bool ok = true;
+      for (int t = first; t < p.tiles && ok; t += step) {
+        const Tile tile = tile_at(p, t);
+        for (int kb = k_begin; kb < k_end; ++kb, ++fills) {
+          const int s = fills % p.stages;
+          if (fills >= p.stages && !mbar_wait(&b.empty[s], (fills / p.stages - 1) & 1, abort, p.err)) {
+            ok = false;
+            break;
+          }
+          uint8_t *const dst = ring + s * stage_bytes;
+          mbar_arrive_expect_tx(&b.full[s], static_cast<uint32_t>(stage_bytes));
+          const int lane_z = SWAP ? 0 : tile.group, col_z = SWAP ? tile.group : 0;
+          tma_load_3d(dst, &lane_map, kb * kBk, tile.lane0, lane_z, &b.full[s]);
+          tma_load_3d(dst + kLanes * 128, &col_map, kb * kBk, tile.col0, col_z, &b.full[s]);
+        }
+      }
+      // No copy outlives the CTA, whatever the other warps did.
+      if (!ok) {
+        for (int f = fills > p.stages ? fills - p.stages : 0; f < fills; ++f)
+          mbar_wait_drain(&b.full[f % p.stages], (f / p.stages) & 1, p.err);
+      }
+    }
+  } else if (warp == 1) {
+    if (threadIdx.x == 32) {
+      int uses = 0, tiles = 0;
+      bool ok = true;
+      for (int t = first; t < p.tiles && ok; t += step, ++tiles) {
+        const int half = tiles & 1;
+        if (tiles >= 2 && !mbar_wait(&b.acc_empty[half], ((tiles >> 1) - 1) & 1, abort, p.err)) break;
+        tcgen05_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
+        for (int kb = k_begin; kb < k_end; ++kb, ++uses) {
+          const int s = uses % p.stages;
+          if (!mbar_wait(&b.full[s], (uses / p.stages) & 1, abort, p.err)) {
+            ok = false;
+            break;
+          }
+          tcgen05_fence_after();
+          const uint64_t a = smem_desc_k128(smem_u32(ring + s * stage_bytes));
+          const uint64_t c = smem_desc_k128(smem_u32(ring + s * stage_bytes + kLanes * 128));
+#pragma unroll
+          for (int i = 0; i < kBk / 16; ++i)
+            tcgen05_mma_f16(d, a + 2 * i, c + 2 * i, p.idesc, kb > k_begin || i > 0);
+          tcgen05_commit(&b.empty[s]);
+        }
+        if (ok) tcgen05_commit(&b.acc_full[half]);
+      }
+      if (*abort) {  // products in flight end before the tensor memory is given back
+        tcgen05_commit(&b.drain);
+        mbar_wait_drain(&b.drain, 0, p.err);
+      }
+    }
+  } else if (warp >= 4) {
+    const int e = warp - 4;
+    const int et = threadIdx.x - 128;
+    int tiles = 0;
+    for (int t = first; t < p.tiles; t += step, ++tiles) {
+      const Tile tile = tile_at(p, t);
+      const int half = tiles & 1;
+      float *const bs = bias_s + half * p.bn;
+      if (!SWAP) {
+        // Every epilogue warp has left the tile that used this half before:
+        // the barrier of the tile in between lies behind it.
+        for (int i = et; i < p.bn; i += 32 * kEpiWarps) bs[i] = bias_at<T>(p, tile.col0 + i);
+      }
+      bool ok = mbar_wait(&b.acc_full[half], (tiles >> 1) & 1, abort, p.err);
+      // One decision for all warps that meet at the barrier, and per warp
+      // elsewhere: tensor memory loads are executed by whole warps.
+      ok = SWAP ? __all_sync(0xffffffffu, ok) : epilogue_all(ok);
+      if (!ok) break;
+      tcgen05_fence_after();
+      const uint32_t acc = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
+      if (SPLIT) {
+        // Products are complete: the ring is free to hold the partial sums.
+        float *const partial = reinterpret_cast<float *>(ring);
+        const int lane = 32 * (e % 4) + static_cast<int>(threadIdx.x % 32);
+        for (int c = e / 4 * 16; c < p.bn; c += kEpiWarps / 4 * 16) {
+          uint32_t r[16];
+          tmem_ld16(acc + (static_cast<uint32_t>(32 * (e % 4)) << 16) + c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) partial[(c + j) * kLanes + lane] = __uint_as_float(r[j]);
+        }
+      } else {
+        epilogue_act<T, SWAP>(p, tile, acc, bs, e);
+        tcgen05_fence_before();
+        mbar_arrive(&b.acc_empty[half]);
+      }
+    }
+  }
+
+  __syncwarp();
+  if (SPLIT) {
+    __syncthreads();
+    cluster_sync_all();
+    if (!*abort && first < p.tiles) {
+      const Tile tile = tile_at(p, first);
+      const uint32_t partial = smem_u32(ring);
+      const int tid = threadIdx.x;
+      switch (p.act) {
+        case LM_ACT_RELU: finish_split<T, LM_ACT_RELU>(p, tile, partial, rank, tid, kThreads); break;
+        case LM_ACT_GELU: finish_split<T, LM_ACT_GELU>(p, tile, partial, rank, tid, kThreads); break;
+        case LM_ACT_GELU_TANH: finish_split<T, LM_ACT_GELU_TANH>(p, tile, partial, rank, tid, kThreads); break;
+        case LM_ACT_SILU: finish_split<T, LM_ACT_SILU>(p, tile, partial, rank, tid, kThreads); break;
+        default: finish_split<T, LM_ACT_NONE>(p, tile, partial, rank, tid, kThreads); break;
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its sums
+  }
+  tcgen05_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tcgen05_fence_after();
+    tmem_dealloc(tmem, static_cast<uint32_t>(p.tmem_cols));
+  }
+}
+
+// Copies rows off 16-byte boundaries into rows padded to 8 elements.
+struct PackParams {
+  const uint16_t *src;
+  uint4 *dst;
+  int64_t group_stride, row_stride, rows, k, vecs, total;  // vecs: 16-byte vectors a row
+};
+
+__global__ void __launch_bounds__(256) pack_kernel(const PackParams p) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= p.total) return;
+  const int64_t row = i / p.vecs, v = i % p.vecs;
+  const uint16_t *const s = p.src + row / p.rows * p.group_stride + row % p.rows * p.row_stride + v * 8;
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = v * 8 + j < p.k ? s[j] : 0u;
+  p.dst[i] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
 }
 
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -65,9 +467,133 @@ lm_status check(const lm_linear_args *a) {
   if ((a->bias && a->bias_dtype != LM_F32 && a->bias_dtype != a->dtype) ||
       (a->out_dtype != LM_F32 && a->out_dtype != a->dtype))
     return LM_ERR_UNSUPPORTED;
-  if (a->k > INT_MAX || a->n > INT_MAX || a->groups > INT_MAX || a->rows > INT_MAX ||
-      a->groups * a->rows > INT_MAX)
+  const int64_t most = INT_MAX - 512;
+  if (a->k > most || a->n > most || a->groups > most || a->rows > most ||
+      (a->rows > 0 && a->groups > most / a->rows))
     return LM_ERR_UNSUPPORTED;
+  return LM_OK;
+}
+
+// An operand as TMA sees it: [groups][rows][k], strides in elements.
+struct Operand {
+  const void *p;
+  int64_t groups, rows, group_stride, row_stride;
+  bool pack;       // copied into the workspace first
+  size_t bytes;    // of that copy
+};
+
+Operand operand(const void *p, int64_t groups, int64_t rows, int64_t k, int64_t group_stride, int64_t row_stride) {
+  Operand o{p, groups, rows, group_stride, row_stride, false, 0};
+  if (o.rows == 1 && o.groups > 1) {  // one row per group: the groups are the rows
+    o.rows = o.groups;
+    o.groups = 1;
+    o.row_stride = group_stride;
+  }
+  if (o.rows <= 1) o.row_stride = k;  // never used
+  if (o.groups <= 1) o.group_stride = o.rows * o.row_stride;
+  if (o.groups > 1 && o.group_stride == o.rows * o.row_stride) {
+    o.rows *= o.groups;
+    o.groups = 1;
+  }
+  // Strides that are in use must be multiples of 16 bytes, and not zero.
+  const bool rows_ok = o.rows <= 1 || (o.row_stride > 0 && o.row_stride % 8 == 0);
+  const bool groups_ok = o.groups <= 1 || (o.group_stride > 0 && o.group_stride % 8 == 0);
+  o.pack = k > 0 && !(aligned(p, 16) && rows_ok && groups_ok && o.row_stride < (1ll << 38) &&
+                      o.group_stride < (1ll << 38));
+  if (o.pack) o.bytes = static_cast<size_t>(o.groups) * o.rows * ((k + 7) / 8) * 16;
+  return o;
+}
+
+struct Plan {
+  Operand x, w;
+  size_t bytes;
+};
+
+Plan plan(const lm_linear_args &a) {
+  Plan p;
+  p.x = operand(a.x, a.groups, a.rows, a.k, a.x_group_stride, a.x_row_stride);
+  p.w = operand(a.weight, 1, a.n, a.k, 0, a.weight_row_stride);
+  p.bytes = 256 + (p.x.bytes + 255) / 256 * 256 + (p.w.bytes + 255) / 256 * 256;
+  return p;
+}
+
+lm_status pack(Operand *o, int64_t k, void *dst, cudaStream_t s) {
+  PackParams p;
+  p.src = static_cast<const uint16_t *>(o->p);
+  p.dst = static_cast<uint4 *>(dst);
+  p.group_stride = o->group_stride;
+  p.row_stride = o->row_stride;
+  p.rows = o->rows;
+  p.k = k;
+  p.vecs = (k + 7) / 8;
+  p.total = o->groups * o->rows * p.vecs;
+  const int64_t ctas = (p.total + 255) / 256;
+  if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
+  pack_kernel<<<static_cast<unsigned>(ctas), 256, 0, s>>>(p);
+  LM_CUDA_TRY(cudaGetLastError());
+  o->p = dst;
+  o->row_stride = p.vecs * 8;
+  o->group_stride = o->rows * o->row_stride;
+  return LM_OK;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// Tiles of `box_rows` rows x 64 elements of k, zeros outside.
+lm_status make_map(CUtensorMap *map, const Operand &o, int64_t k, int box_rows, bool bf16) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cuda_fail(cudaErrorNotSupported);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(o.rows),
+                              static_cast<cuuint64_t>(o.groups)};
+  // A stride that is not used still has to be a valid one.
+  const int64_t pad = (k + 7) / 8 * 8;
+  const int64_t rs = o.rows > 1 ? o.row_stride : pad;
+  const int64_t gs = o.groups > 1 ? o.group_stride : pad;
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(rs) * 2, static_cast<cuuint64_t>(gs) * 2};
+  const cuuint32_t box[3] = {kBk, static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
+  const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                        const_cast<void *>(o.p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? LM_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
+template <typename T>
+lm_status launch(const CUtensorMap &lanes, const CUtensorMap &cols, const LinearParams &p, bool swap, int grid,
+                 int smem, cudaStream_t s) {
+  auto *const kernel = !swap ? linear_kernel<T, false, false>
+                             : p.splits > 1 ? linear_kernel<T, true, true> : linear_kernel<T, true, false>;
+  if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  if (p.splits > 1) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+  LM_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, lanes, cols, p));
   return LM_OK;
 }
 
@@ -77,15 +603,14 @@ lm_status check(const lm_linear_args *a) {
 extern "C" lm_status lm_linear_workspace_size(const lm_linear_args *args, size_t *bytes) {
   if (!bytes) return LM_ERR_INVALID_ARG;
   if (lm_status st = lm::check(args); st != LM_OK) return st;
-  *bytes = lm::kWorkspaceHeaderBytes;
+  *bytes = lm::plan(*args).bytes;
   return LM_OK;
 }
 
 extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size_t workspace_bytes,
                                lm_stream_t stream) {
   using namespace lm;
-  size_t need = 0;
-  if (lm_status st = lm_linear_workspace_size(args, &need); st != LM_OK) return st;
+  if (lm_status st = check(args); st != LM_OK) return st;
   const lm_linear_args &a = *args;
   if (a.groups * a.rows == 0 || a.n == 0) return LM_OK;
   if (!a.out || (a.k > 0 && (!a.x || !a.weight))) return LM_ERR_INVALID_ARG;
@@ -93,16 +618,73 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
   if (!aligned(a.x, 2) || !aligned(a.weight, 2) || !aligned(a.bias, a.bias_dtype == LM_F32 ? 4 : 2) ||
       !aligned(a.residual, 2) || !aligned(a.out, out_size) || !aligned(workspace, 16))
     return LM_ERR_MISALIGNED;
-  if (!workspace || workspace_bytes < need) return LM_ERR_WORKSPACE;
-  const int64_t gx = (a.n + kTile - 1) / kTile, gy = (a.groups * a.rows + kTile - 1) / kTile;
-  if (gy > 65535) return LM_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(kTile, kTile);
+  Plan pl = plan(a);
+  if (!workspace || workspace_bytes < pl.bytes) return LM_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if (lm_status st = current_device_info(&dev); st != LM_OK) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (a.dtype == LM_F16) {
-    linear_kernel<__half><<<grid, block, 0, s>>>(a);
-  } else {
-    linear_kernel<__nv_bfloat16><<<grid, block, 0, s>>>(a);
+  char *const scratch = static_cast<char *>(workspace) + 256;
+  const size_t x_bytes = pl.x.bytes;
+  if (pl.x.pack)
+    if (lm_status st = pack(&pl.x, a.k, scratch, s); st != LM_OK) return st;
+  if (pl.w.pack)
+    if (lm_status st = pack(&pl.w, a.k, scratch + (x_bytes + 255) / 256 * 256, s); st != LM_OK) return st;
+
+  LinearParams p = {};
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.out = a.out;
+  p.rows_total = a.groups * a.rows;
+  p.out_row = a.out_row_stride;
+  p.res_row = a.residual_row_stride;
+  p.rows = static_cast<int32_t>(pl.x.rows);
+  p.k = static_cast<int32_t>(a.k);
+  p.n = static_cast<int32_t>(a.n);
+  p.kblocks = (p.k + kBk - 1) / kBk;
+  p.bias_f32 = a.bias_dtype == LM_F32;
+  p.out_f32 = a.out_dtype == LM_F32;
+  p.act = a.activation;
+  p.scale = a.scale;
+  p.err = static_cast<uint32_t *>(workspace);
+  const bool bf16 = a.dtype == LM_BF16;
+
+  // Outputs in 16-byte vectors, 16 of a row at a time.
+  const int64_t ov = 16 / static_cast<int64_t>(out_size);
+  const bool one_row = p.rows_total == 1;
+  const bool vec = aligned(a.out, 16) && (one_row || a.out_row_stride % ov == 0) &&
+                   (!a.residual || (aligned(a.residual, 16) && (one_row || a.residual_row_stride % 8 == 0)));
+  p.vec32 = aligned(a.out, 32) && (one_row || a.out_row_stride % (2 * ov) == 0);
+  const bool swap = !vec || p.rows <= 256;
+  const int64_t lane_rows = swap ? p.n : p.rows, col_rows = swap ? p.rows : p.n;
+  p.lane_tiles = static_cast<int32_t>((lane_rows + kLanes - 1) / kLanes);
+  // Columns in equal tiles of at most 256, a multiple of 16 each.
+  int64_t col_tiles = (col_rows + kMaxBn - 1) / kMaxBn;
+  p.bn = static_cast<int32_t>(((col_rows + col_tiles - 1) / col_tiles + 15) / 16 * 16);
+  if (!swap && static_cast<int64_t>(p.lane_tiles) * col_tiles * pl.x.groups < dev.sm_count && p.bn > 128) {
+    p.bn = 128;
   }
-  LM_CUDA_TRY(cudaGetLastError());
-  return LM_OK;
+  p.col_tiles = static_cast<int32_t>((col_rows + p.bn - 1) / p.bn);
+  const int64_t tiles = static_cast<int64_t>(p.lane_tiles) * p.col_tiles * pl.x.groups;
+  if (tiles > INT_MAX / 16) return LM_ERR_UNSUPPORTED;
+  p.tiles = static_cast<int32_t>(tiles);
+  p.splits = 1;
+  if (swap && p.bn <= 64) {
+    while (p.splits < 8 && tiles * p.splits * 2 <= dev.sm_count && p.kblocks >= p.splits * 2) p.splits *= 2;
+  }
+  p.tmem_cols = 32;
+  while (p.tmem_cols < 2 * p.bn) p.tmem_cols *= 2;
+  const int stage_bytes = kLanes * 128 + p.bn * 128;
+  p.stages = kSmemBudget / stage_bytes;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.idesc = idesc_f16(bf16, static_cast<uint32_t>(p.bn));
+  int smem = 1024 + p.stages * stage_bytes + static_cast<int>(sizeof(Barriers)) + 2 * p.bn * 4;
+
+  CUtensorMap lanes = {}, cols = {};
+  if (p.kblocks > 0) {
+    if (lm_status st = make_map(&lanes, swap ? pl.w : pl.x, a.k, kLanes, bf16); st != LM_OK) return st;
+    if (lm_status st = make_map(&cols, swap ? pl.x : pl.w, a.k, p.bn, bf16); st != LM_OK) return st;
+  }
+  const int grid = p.splits > 1 ? p.tiles * p.splits : p.tiles < dev.sm_count ? p.tiles : dev.sm_count;
+  return bf16 ? launch<__nv_bfloat16>(lanes, cols, p, swap, grid, smem, s)
+              : launch<__half>(lanes, cols, p, swap, grid, smem, s);
 }

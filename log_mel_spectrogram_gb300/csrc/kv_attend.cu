@@ -1,18 +1,56 @@
 // kv_attend.cu -- attention over the 8-bit key/value cache.
 //
-// One warp per query row and head walks the row's tokens with a running
-// maximum and sum; lanes hold head_dim / 32 elements each.
+// A CTA serves one row and key head: the row's queries that read that head
+// (tokens x group) fill tiles of 16 or 32 rows, and each of its four warps
+// walks its own tiles of 32 tokens with a running maximum and sum per row.  A
+// warp fetches keys and values -- contiguous pieces of a block -- by bulk
+// copies into a ring of its own, so warps never wait for one another until
+// the end, and only the bytes of the cache travel.
+//
+// Bytes become 16-bit floats exactly, in registers, on their way into
+// m16n8k16 products with 32-bit sums: decoding has few query rows and is bound by
+// the cache's bytes, so the products only have to keep up with those (16 query
+// rows at full memory speed are 0.2 PFLOP/s).
+//
+// The order of head elements in a product over k, and of tokens within 16, is
+// free: a thread takes contiguous bytes of its token as its part of k, and
+// every fourth token, which makes the shared-memory reads wide and free of
+// conflicts.
+//
+// Scales.  With s = scale * q k8 * k_scale * log2 e, a token's weight times its
+// value scale is 2^(s + log2 v_scale); the running maximum M is taken over
+// those exponents, so that the weights p = 2^(s + log2 v_scale - M) that
+// multiply v8 are at most 1 and keep their precision in 16 bits whatever the
+// block's scale; the softmax's sum is that of p / v_scale, in 32 bits.
+//
+// Long rows are split over CTAs; the last one to finish a row and head joins
+// the parts in order.
 #include <climits>
 
 #include "half.cuh"
 #include "internal.h"
 #include "kv_cache.cuh"
+#include "mma.cuh"
 #include "ptx.cuh"
 
 namespace lm {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTok = 32;              // tokens of a warp's tile
+constexpr int kMinChunk = 512;        // tokens below which a row is not split
+// Value scales count as at least 2^-90 (values of at most 1e-25, which are off
+// by as much): a weight divided by its scale then still has 23 bits below the
+// largest one in 32-bit floats, for scales of up to 2^13.
+constexpr float kMinScale = 8.0779357e-28f;
+
+// Bytes of one warp's stage (keys and values of kTok tokens), ring depth and
+// the CTAs that a full device holds: 64 KB of ring or less per CTA for
+// head_dim 32 and 64, 96 KB for 128.
+constexpr int stage_bytes(int d) { return 2 * kTok * d; }
+constexpr int ring_stages(int d) { return d == 128 ? 3 : d == 64 ? 4 : 6; }
+constexpr int full_ctas(int d) { return 152 * (d == 128 ? 2 : 3); }
 
 struct AttendParams {
   KvView c;
@@ -20,58 +58,439 @@ struct AttendParams {
   void *out;
   int64_t row_s, tok_s, head_s;
   const int32_t *counts;
-  int32_t tokens, q_heads, new_tokens, causal;
+  uint32_t *err, *done;          // done: per unit, parts that are ready
+  float2 *part_ml;               // [unit][split][rows]: maximum, sum
+  float *part_acc;               // [unit][split][rows][head_dim]
+  int32_t tokens, q_heads, new_tokens, causal, group, qrows, qtiles, splits, part_rows, qvec;
   float scale;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) {
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (u >= static_cast<int64_t>(p.c.rows) * p.tokens * p.q_heads) return;
-  const int hq = static_cast<int>(u % p.q_heads), i = static_cast<int>(u / p.q_heads % p.tokens);
-  const int r = static_cast<int>(u / p.q_heads / p.tokens);
-  const int h = hq / (p.q_heads / p.c.heads);
-  const int64_t cap = static_cast<int64_t>(p.c.width) * p.c.block;
-  const int64_t held = max(p.c.lens[r], 0);
-  const int fresh = min(max(p.counts ? p.counts[r] : p.new_tokens, 0), p.causal ? p.tokens : INT_MAX);
-  int64_t end = min(held + fresh, cap);
-  if (p.causal) end = i < fresh ? min(end, held + i + 1) : 0;
-  constexpr int N = D / 32;
-  float q[N], acc[N] = {}, m = -INFINITY, l = 0.0f;
-  const T *const qp = static_cast<const T *>(p.q) + r * p.row_s + i * p.tok_s + hq * p.head_s;
-  for (int j = 0; j < N; ++j) q[j] = to_f32(qp[lane * N + j]) * p.scale;
-  for (int64_t t = 0; t < end; ++t) {
-    const int blk = p.c.table[r * static_cast<int64_t>(p.c.width) + t / p.c.block];
-    if (blk < 0 || blk >= p.c.blocks) continue;
-    const int64_t tile = p.c.layer_tiles + static_cast<int64_t>(blk) * p.c.heads + h;
-    const int64_t at = (tile * p.c.block + t % p.c.block) * D + lane * N;
-    float s = 0.0f;
-    for (int j = 0; j < N; ++j) s += q[j] * p.c.k8[at + j];
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= p.c.k_scale[tile];
-    const float mn = fmaxf(m, s), a = m == mn ? 1.0f : expf(m - mn), w = expf(s - mn);
-    m = mn;
-    l = l * a + w;
-    for (int j = 0; j < N; ++j) acc[j] = acc[j] * a + w * (p.c.v8[at + j] * p.c.v_scale[tile]);
-  }
-  T *const o = static_cast<T *>(p.out) + u * D + lane * N;
-  for (int j = 0; j < N; ++j) o[j] = from_f32<T>(l == 0.0f ? 0.0f : acc[j] / l);
+// Shared memory: the rings (at the end the warps' partial results), then this.
+template <int R>
+struct Shared {
+  uint64_t full[kWarps][8];
+  float2 ml[kWarps][R];  // maximum and sum per warp and query row
+  int abort;
+  int last;
+};
+
+constexpr int big_bytes(int d, int mt) {
+  const int ring = kWarps * ring_stages(d) * stage_bytes(d), joined = kWarps * 16 * mt * d * 4;
+  return ring > joined ? ring : joined;
 }
 
-template <typename T>
-lm_status launch(const AttendParams &p, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(p.c.rows) * p.tokens * p.q_heads;
-  const int64_t ctas = (rows + kThreads / 32 - 1) / (kThreads / 32);
-  if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
-  const unsigned n = static_cast<unsigned>(ctas);
-  switch (p.c.head_dim) {
-    case 32: attend_kernel<T, 32><<<n, kThreads, 0, s>>>(p); break;
-    case 64: attend_kernel<T, 64><<<n, kThreads, 0, s>>>(p); break;
-    default: attend_kernel<T, 128><<<n, kThreads, 0, s>>>(p); break;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+// N 32-bit words of shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = lds_u32(a);
+  } else if constexpr (N == 2) {
+    const uint2 v = lds_v2(a);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = lds_v4(a + 16 * i);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
   }
-  LM_CUDA_TRY(cudaGetLastError());
-  return LM_OK;
+}
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) {
+  constexpr int STAGES = ring_stages(D);
+  constexpr int KW = D / 16;   // 32-bit words of a token's key per thread; also 16-element steps of k
+  constexpr int VB = D / 8;    // bytes of a token's value per thread; also 8-column tiles of the output
+  constexpr int R = 16 * MT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  Shared<R> &sh = *reinterpret_cast<Shared<R> *>(smem + big_bytes(D, MT));
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r8 = lane / 4, c4 = lane % 4;
+  int u = blockIdx.x;
+  const int split = u % p.splits;
+  u /= p.splits;
+  const int unit = u;
+  const int qt = u % p.qtiles;
+  u /= p.qtiles;
+  const int h = u % p.c.heads;
+  const int row = u / p.c.heads;
+
+  // How far this tile of queries sees.
+  const int cap = p.c.width * p.c.block;
+  const int held = min(max(p.c.lens[row], 0), cap);
+  int fresh = max(p.counts ? p.counts[row] : p.new_tokens, 0);
+  if (p.causal) fresh = min(fresh, p.tokens);
+  const int total = static_cast<int>(min(static_cast<int64_t>(held) + fresh, static_cast<int64_t>(cap)));
+  const int q_first = qt * R, q_rows = min(R, p.qrows - q_first);
+  int end = total;
+  if (p.causal) {
+    const int i_first = q_first / p.group, i_last = min((q_first + q_rows - 1) / p.group, fresh - 1);
+    end = i_first < fresh ? min(total, held + i_last + 1) : 0;
+  }
+  // Equal parts of whole CTA strides; a part that would be empty has no CTA.
+  int chunk = ((end + p.splits - 1) / p.splits + kWarps * kTok - 1) / (kWarps * kTok) * (kWarps * kTok);
+  chunk = max(chunk, kMinChunk);
+  const int parts = max((end + chunk - 1) / chunk, 1);
+  if (split >= parts) return;
+  const int begin = split * chunk, stop = min(end, begin + chunk);
+
+  if (threadIdx.x < kWarps)
+    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[threadIdx.x][i], 1);
+  if (threadIdx.x == 0) sh.abort = 0;
+  fence_mbar_init();
+  __syncthreads();
+
+  uint8_t *const ring = smem + warp * STAGES * stage_bytes(D);
+  const uint32_t ring_a = smem_u32(ring);
+  uint64_t *const full = sh.full[warp];
+  const int block_shift = 31 - __clz(p.c.block);
+  const int32_t *const table = p.c.table + static_cast<int64_t>(row) * p.c.width;
+  const int64_t tiles0 = p.c.layer_tiles + h;
+  // This warp's tiles: number j starts at token begin + (j * kWarps + warp) * kTok.
+  const int mine = max((stop - begin - warp * kTok + kWarps * kTok - 1) / (kWarps * kTok), 0);
+  auto token_of = [&](int j) { return begin + (j * kWarps + warp) * kTok; };
+  // The block of a tile's half (16 tokens), or -1.
+  auto block_of = [&](int j, int half) {
+    const int t = token_of(j) + 16 * half;
+    if (j >= mine || t >= stop) return -1;
+    const int b = __ldg(table + (t >> block_shift));
+    return b >= 0 && b < p.c.blocks ? b : -1;
+  };
+  int fb0 = -1, fb1 = -1;  // blocks of the 32 tiles that are fetched next, one per lane
+  auto fetch = [&](int j) {
+    if (j % 32 == 0) {
+      fb0 = block_of(j + lane, 0);
+      fb1 = block_of(j + lane, 1);
+    }
+    const int b0 = __shfl_sync(0xffffffffu, fb0, j % 32), b1 = __shfl_sync(0xffffffffu, fb1, j % 32);
+    if (lane == 0 && j < mine) {
+      const int s = j % STAGES;
+      const uint32_t bytes = 16 * D;
+      mbar_arrive_expect_tx(&full[s], ((b0 >= 0) + (b1 >= 0)) * 2 * bytes);
+      uint8_t *const k_at = ring + s * stage_bytes(D), *const v_at = k_at + kTok * D;
+      const int t = token_of(j), in = t & (p.c.block - 1);
+      const int64_t at0 = ((tiles0 + static_cast<int64_t>(b0) * p.c.heads) * p.c.block + in) * D;
+      if (b0 >= 0 && b0 == b1) {
+        bulk_g2s_plain(k_at, p.c.k8 + at0, 2 * bytes, &full[s]);
+        bulk_g2s_plain(v_at, p.c.v8 + at0, 2 * bytes, &full[s]);
+      } else {
+        if (b0 >= 0) {
+          bulk_g2s_plain(k_at, p.c.k8 + at0, bytes, &full[s]);
+          bulk_g2s_plain(v_at, p.c.v8 + at0, bytes, &full[s]);
+        }
+        if (b1 >= 0) {
+          const int64_t at1 =
+              ((tiles0 + static_cast<int64_t>(b1) * p.c.heads) * p.c.block + ((in + 16) & (p.c.block - 1))) * D;
+          bulk_g2s_plain(k_at + bytes, p.c.k8 + at1, bytes, &full[s]);
+          bulk_g2s_plain(v_at + bytes, p.c.v8 + at1, bytes, &full[s]);
+        }
+      }
+    }
+  };
+  int fetched = 0;
+  for (; fetched < min(mine, STAGES); ++fetched) fetch(fetched);
+
+  // Queries, k permuted: step s of the product over k takes elements
+  // c4 * D/4 + 4s .. + 3 of the head from this thread.
+  uint32_t q[MT][KW][4];
+  int limit[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int at = q_first + 16 * m + 8 * e + r8;
+      const bool in = at < p.qrows;
+      const int i = in ? at / p.group : 0, g = in ? at % p.group : 0;
+      limit[m][e] = !in ? INT_MAX : !p.causal ? total : i < fresh ? min(total, held + i + 1) : 0;
+      const T *const src = static_cast<const T *>(p.q) + row * p.row_s + i * p.tok_s +
+                           (static_cast<int64_t>(h) * p.group + g) * p.head_s + c4 * (D / 4);
+      uint32_t w[2 * KW];
+      if (!in) {
+#pragma unroll
+        for (int j = 0; j < 2 * KW; ++j) w[j] = 0;
+      } else if (p.qvec) {
+#pragma unroll
+        for (int j = 0; j < 2 * KW; j += 4) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(src + 2 * j);
+          w[j] = v.x;
+          w[j + 1] = v.y;
+          w[j + 2] = v.z;
+          w[j + 3] = v.w;
+        }
+      } else {
+        const uint16_t *const s16 = reinterpret_cast<const uint16_t *>(src);
+#pragma unroll
+        for (int j = 0; j < 2 * KW; ++j)
+          w[j] = s16[2 * j] | static_cast<uint32_t>(s16[2 * j + 1]) << 16;
+      }
+#pragma unroll
+      for (int s = 0; s < KW; ++s) {
+        q[m][s][e] = w[2 * s];
+        q[m][s][2 + e] = w[2 * s + 1];
+      }
+    }
+  }
+
+  float acc[MT][VB][4];
+  float top[MT][2], sum[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int j = 0; j < VB; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
+    top[m][0] = top[m][1] = -INFINITY;
+    sum[m][0] = sum[m][1] = 0.0f;
+  }
+
+  // Of the 32 tiles that are consumed next, one per lane and half: the score
+  // factor, log2 and inverse of the value scale; absent blocks are masked.
+  float f_s[2] = {0, 0}, l_s[2] = {0, 0}, i_s[2] = {0, 0};
+  const float log2e = 1.4426950408889634f;
+  int done = 0;
+  for (; done < mine; ++done) {
+    const int j = done;
+    if (j % 32 == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int b = block_of(j + lane, e);
+        f_s[e] = l_s[e] = i_s[e] = 0.0f;
+        if (b >= 0) {
+          const int64_t tile = tiles0 + static_cast<int64_t>(b) * p.c.heads;
+          const float vs = fmaxf(__ldg(p.c.v_scale + tile), kMinScale);
+          f_s[e] = __ldg(p.c.k_scale + tile) * p.scale * log2e;
+          l_s[e] = log2f(vs);
+          i_s[e] = 1.0f / vs;
+        } else {
+          i_s[e] = -1.0f;
+        }
+      }
+    }
+    const int t0 = token_of(j);
+    const int s = j % STAGES;
+    const uint32_t k_at = ring_a + s * stage_bytes(D), v_at = k_at + kTok * D;
+    if (!mbar_wait(&full[s], (j / STAGES) & 1, &sh.abort, p.err)) break;
+
+    // Scores: column n of 8-token tile n8 is token 16 (n8/2) + 8 (n8%2) + n/2 + 4 (n%2).
+    float sc[MT][4][4];
+#pragma unroll
+    for (int n8 = 0; n8 < 4; ++n8) {
+      const int tok = 16 * (n8 / 2) + 8 * (n8 & 1) + (r8 >> 1) + 4 * (r8 & 1);
+      uint32_t w[KW];
+      lds_words(k_at + tok * D + c4 * (D / 4), w);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) sc[m][n8][0] = sc[m][n8][1] = sc[m][n8][2] = sc[m][n8][3] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < KW; ++ks) {
+        const uint32_t b0 = bytes_to<T>(__byte_perm(w[ks], 0, 0x4140)), b1 = bytes_to<T>(__byte_perm(w[ks], 0, 0x4342));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) mma16816<T>(sc[m][n8], q[m][ks], b0, b1);
+      }
+    }
+    const float f0 = __shfl_sync(0xffffffffu, f_s[0], j % 32), f1 = __shfl_sync(0xffffffffu, f_s[1], j % 32);
+    const float l0 = __shfl_sync(0xffffffffu, l_s[0], j % 32), l1 = __shfl_sync(0xffffffffu, l_s[1], j % 32);
+    const float i0 = __shfl_sync(0xffffffffu, i_s[0], j % 32), i1 = __shfl_sync(0xffffffffu, i_s[1], j % 32);
+    const bool partial = i0 < 0.0f || i1 < 0.0f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int n8 = 0; n8 < 4; ++n8) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sc[m][n8][x] = fmaf(sc[m][n8][x], n8 < 2 ? f0 : f1, n8 < 2 ? l0 : l1);
+      }
+      // Tokens past a row's end, and absent ones.  (Selected, not added: their
+      // bytes and scales may be anything.)
+      const bool cut = t0 > limit[m][0] - kTok || t0 > limit[m][1] - kTok || partial;
+      if (__any_sync(0xffffffffu, cut)) {
+#pragma unroll
+        for (int n8 = 0; n8 < 4; ++n8) {
+          const bool absent = (n8 < 2 ? i0 : i1) < 0.0f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int tok = t0 + 16 * (n8 / 2) + 8 * (n8 & 1) + c4 + 4 * (x & 1);
+            if (absent || tok >= limit[m][x >> 1]) sc[m][n8][x] = -INFINITY;
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = top[m][e];
+#pragma unroll
+        for (int n8 = 0; n8 < 4; ++n8) t = fmaxf(t, fmaxf(sc[m][n8][2 * e], sc[m][n8][2 * e + 1]));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+        const float zero = t == -INFINITY ? 0.0f : t;
+        const float shrink = ex2(top[m][e] - zero);
+        top[m][e] = t;
+        sum[m][e] *= shrink;
+#pragma unroll
+        for (int n = 0; n < VB; ++n) {
+          acc[m][n][2 * e] *= shrink;
+          acc[m][n][2 * e + 1] *= shrink;
+        }
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int n8 = 0; n8 < 4; ++n8) {
+#pragma unroll
+          for (int x = 2 * e; x < 2 * e + 2; ++x) {
+            const float w = ex2(sc[m][n8][x] - zero);
+            sc[m][n8][x] = w;
+            if (n8 < 2) {
+              s0 += w;
+            } else {
+              s1 += w;
+            }
+          }
+        }
+        sum[m][e] = fmaf(s0, fabsf(i0), fmaf(s1, fabsf(i1), sum[m][e]));
+      }
+    }
+    // Values: this thread's bytes VB r8 .. + VB-1 of every fourth token.
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t a[MT][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        a[m][0] = pack2<__half>(sc[m][2 * half][0], sc[m][2 * half][1]);
+        a[m][1] = pack2<__half>(sc[m][2 * half][2], sc[m][2 * half][3]);
+        a[m][2] = pack2<__half>(sc[m][2 * half + 1][0], sc[m][2 * half + 1][1]);
+        a[m][3] = pack2<__half>(sc[m][2 * half + 1][2], sc[m][2 * half + 1][3]);
+      }
+      uint32_t w[4][VB / 4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds_words(v_at + (16 * half + 4 * i + c4) * D + VB * r8, w[i]);
+#pragma unroll
+      for (int n = 0; n < VB; ++n) {
+        // Byte n of tokens c4, c4 + 4 and of c4 + 8, c4 + 12, in the low byte of each half.
+        constexpr uint32_t pick[4] = {0x0400, 0x0501, 0x0602, 0x0703};
+        const uint32_t lo = __byte_perm(w[0][n / 4], w[1][n / 4], pick[n % 4]);
+        const uint32_t hi = __byte_perm(w[2][n / 4], w[3][n / 4], pick[n % 4]);
+        // The selectors above put byte n at positions 0 (first token) and 2 (second).
+        const uint32_t b0 = bytes_to_f16(lo), b1 = bytes_to_f16(hi);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) mma16816<__half>(acc[m][n], a[m], b0, b1);
+      }
+    }
+    __syncwarp();
+    if (fetched < mine) fetch(fetched++);
+  }
+  if (done < mine && lane == 0) {  // gave up: the copies in flight still have to land
+    for (int f = done; f < fetched; ++f) mbar_wait_drain(&full[f % STAGES], (f / STAGES) & 1, p.err);
+  }
+  __syncthreads();
+  if (sh.abort) return;
+
+  // The four warps' parts meet in the ring's memory.
+  float *const acc_s = reinterpret_cast<float *>(smem);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rr = 16 * m + 8 * e + r8;
+      float s = sum[m][e];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (c4 == 0) sh.ml[warp][rr] = make_float2(top[m][e], s);
+      if (rr < q_rows) {
+        float *const o = acc_s + (warp * R + rr) * D + c4 * (D / 4);
+#pragma unroll
+        for (int n = 0; n < VB; ++n) {
+          o[n] = acc[m][n][2 * e];
+          o[VB + n] = acc[m][n][2 * e + 1];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  const int64_t part0 = (static_cast<int64_t>(unit) * p.splits + split) * p.part_rows;
+  constexpr int PER = D / 4;  // 4-element vectors of a row
+  auto emit = [&](int rr, int d, float4 v, float l) {
+    const int at = q_first + rr, i = at / p.group, g = at % p.group;
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;
+    T *const o = static_cast<T *>(p.out) +
+                 ((static_cast<int64_t>(row) * p.tokens + i) * p.q_heads + h * p.group + g) * D + d;
+    *reinterpret_cast<uint2 *>(o) = make_uint2(pack2<T>(v.x * f, v.y * f), pack2<T>(v.z * f, v.w * f));
+  };
+  for (int x = threadIdx.x; x < q_rows * PER; x += kThreads) {
+    const int rr = x / PER, d = x % PER * 4;
+    float t = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) t = fmaxf(t, sh.ml[w][rr].x);
+    const float zero = t == -INFINITY ? 0.0f : t;
+    float4 v = make_float4(0, 0, 0, 0);
+    float l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 ml = sh.ml[w][rr];
+      const float f = ex2(ml.x - zero);
+      const float4 a = *reinterpret_cast<const float4 *>(acc_s + (w * R + rr) * D + d);
+      v.x = fmaf(a.x, f, v.x);
+      v.y = fmaf(a.y, f, v.y);
+      v.z = fmaf(a.z, f, v.z);
+      v.w = fmaf(a.w, f, v.w);
+      l = fmaf(ml.y, f, l);
+    }
+    if (parts == 1) {
+      emit(rr, d, v, l);
+    } else {
+      *reinterpret_cast<float4 *>(p.part_acc + (part0 + rr) * D + d) = v;
+      if (d == 0) p.part_ml[part0 + rr] = make_float2(t, l);
+    }
+  }
+  if (parts == 1) return;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    sh.last = atomicAdd(&p.done[unit], 1u) == static_cast<uint32_t>(parts - 1);
+  }
+  __syncthreads();
+  if (!sh.last) return;
+  __threadfence();
+  if (threadIdx.x == 0) p.done[unit] = 0;
+  const int64_t unit0 = static_cast<int64_t>(unit) * p.splits * p.part_rows;
+  for (int x = threadIdx.x; x < q_rows * PER; x += kThreads) {
+    const int rr = x / PER, d = x % PER * 4;
+    float t = -INFINITY;
+    for (int w = 0; w < parts; ++w) t = fmaxf(t, __ldcg(&p.part_ml[unit0 + w * p.part_rows + rr]).x);
+    const float zero = t == -INFINITY ? 0.0f : t;
+    float4 v = make_float4(0, 0, 0, 0);
+    float l = 0.0f;
+    for (int w = 0; w < parts; ++w) {
+      const float2 ml = __ldcg(&p.part_ml[unit0 + w * p.part_rows + rr]);
+      const float f = ex2(ml.x - zero);
+      const float4 a = __ldcg(reinterpret_cast<const float4 *>(p.part_acc + (unit0 + w * p.part_rows + rr) * D + d));
+      v.x = fmaf(a.x, f, v.x);
+      v.y = fmaf(a.y, f, v.y);
+      v.z = fmaf(a.z, f, v.z);
+      v.w = fmaf(a.w, f, v.w);
+      l = fmaf(ml.y, f, l);
+    }
+    emit(rr, d, v, l);
+  }
 }
 
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -79,7 +498,58 @@ bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 lm_status check(const lm_kv_cache *cache, int32_t tokens, int32_t q_heads) {
   if (lm_status st = kv_check(cache); st != LM_OK) return st;
   if (tokens < 0 || q_heads < 1 || q_heads % cache->heads != 0) return LM_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(tokens) * (q_heads / cache->heads) > INT_MAX - 64) return LM_ERR_UNSUPPORTED;
   return LM_OK;
+}
+
+// How a call is cut: query rows per tile, tiles, units (row, key head, tile)
+// and parts of the tokens.
+struct Cut {
+  int mt, qrows, qtiles, splits, part_rows;
+  int64_t units;
+  size_t done_bytes, ml_bytes, acc_bytes;
+};
+
+Cut cut(const lm_kv_cache *c, int32_t tokens, int32_t q_heads) {
+  Cut k;
+  k.qrows = tokens * (q_heads / c->heads);
+  k.mt = k.qrows <= 16 ? 1 : 2;
+  k.qtiles = (k.qrows + 16 * k.mt - 1) / (16 * k.mt);
+  k.part_rows = k.qrows < 16 * k.mt ? k.qrows : 16 * k.mt;
+  k.units = static_cast<int64_t>(c->rows) * c->heads * k.qtiles;
+  // As many parts as fill the device once, none below kMinChunk tokens.
+  const int64_t cap = static_cast<int64_t>(c->width) * c->block;
+  int64_t s = k.units > 0 ? full_ctas(c->head_dim) / k.units : 1;
+  const int64_t most = (cap + kMinChunk - 1) / kMinChunk;
+  if (s > most) s = most;
+  k.splits = static_cast<int>(s < 1 ? 1 : s);
+  const int64_t parts = k.splits > 1 ? k.units * k.splits * k.part_rows : 0;
+  // One place for the counters whatever the shape: calls of other shapes
+  // that share the workspace must not write over them.  Split units are at
+  // most half of full_ctas().
+  k.done_bytes = (full_ctas(32) / 2 * 4 + 255) / 256 * 256;
+  k.ml_bytes = (static_cast<size_t>(parts) * 8 + 255) / 256 * 256;
+  k.acc_bytes = static_cast<size_t>(parts) * c->head_dim * 4;
+  return k;
+}
+
+template <typename T, int D, int MT>
+lm_status launch(const AttendParams &p, int64_t ctas, cudaStream_t s) {
+  auto *const kernel = attend_kernel<T, D, MT>;
+  constexpr int smem = big_bytes(D, MT) + static_cast<int>(sizeof(Shared<16 * MT>));
+  if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
+  kernel<<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(p);
+  LM_CUDA_TRY(cudaGetLastError());
+  return LM_OK;
+}
+
+template <typename T>
+lm_status launch_dim(const AttendParams &p, int mt, int64_t ctas, cudaStream_t s) {
+  switch (p.c.head_dim) {
+    case 32: return mt == 1 ? launch<T, 32, 1>(p, ctas, s) : launch<T, 32, 2>(p, ctas, s);
+    case 64: return mt == 1 ? launch<T, 64, 1>(p, ctas, s) : launch<T, 64, 2>(p, ctas, s);
+    default: return mt == 1 ? launch<T, 128, 1>(p, ctas, s) : launch<T, 128, 2>(p, ctas, s);
+  }
 }
 
 }  // namespace
@@ -89,7 +559,8 @@ extern "C" lm_status lm_kv_attend_workspace_size(const lm_kv_cache *cache, int32
                                                  size_t *bytes) {
   if (!bytes) return LM_ERR_INVALID_ARG;
   if (lm_status st = lm::check(cache, tokens, q_heads); st != LM_OK) return st;
-  *bytes = lm::kWorkspaceHeaderBytes;
+  const lm::Cut k = lm::cut(cache, tokens, q_heads);
+  *bytes = 256 + k.done_bytes + k.ml_bytes + k.acc_bytes;
   return LM_OK;
 }
 
@@ -106,9 +577,11 @@ extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const
   for (int i = 0; i < 3; ++i)
     if (q_strides[i] < 0) return LM_ERR_INVALID_ARG;
   if (!aligned(q, 2) || !aligned(out, 16) || !aligned(workspace, 16)) return LM_ERR_MISALIGNED;
-  size_t need = 0;
-  lm_kv_attend_workspace_size(cache, tokens, q_heads, &need);
-  if (!workspace || workspace_bytes < need) return LM_ERR_WORKSPACE;
+  const Cut k = cut(cache, tokens, q_heads);
+  if (!workspace || workspace_bytes < 256 + k.done_bytes + k.ml_bytes + k.acc_bytes) return LM_ERR_WORKSPACE;
+  const int64_t ctas = k.units * k.splits;
+  if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
+  char *const w = static_cast<char *>(workspace);
   AttendParams p;
   p.c = kv_view(cache, layer);
   p.q = q;
@@ -117,11 +590,21 @@ extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const
   p.tok_s = q_strides[1];
   p.head_s = q_strides[2];
   p.counts = counts;
+  p.err = reinterpret_cast<uint32_t *>(w);
+  p.done = reinterpret_cast<uint32_t *>(w + 256);
+  p.part_ml = reinterpret_cast<float2 *>(w + 256 + k.done_bytes);
+  p.part_acc = reinterpret_cast<float *>(w + 256 + k.done_bytes + k.ml_bytes);
   p.tokens = tokens;
   p.q_heads = q_heads;
   p.new_tokens = new_tokens;
   p.causal = causal != 0;
+  p.group = q_heads / cache->heads;
+  p.qrows = k.qrows;
+  p.qtiles = k.qtiles;
+  p.splits = k.splits;
+  p.part_rows = k.part_rows;
+  p.qvec = aligned(q, 16) && q_strides[0] % 8 == 0 && q_strides[1] % 8 == 0 && q_strides[2] % 8 == 0;
   p.scale = scale;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return dtype == LM_F16 ? launch<__half>(p, s) : launch<__nv_bfloat16>(p, s);
+  return dtype == LM_F16 ? launch_dim<__half>(p, k.mt, ctas, s) : launch_dim<__nv_bfloat16>(p, k.mt, ctas, s);
 }

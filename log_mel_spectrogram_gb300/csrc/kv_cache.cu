@@ -307,7 +307,7 @@ lm_status kv_check(const lm_kv_cache *c) {
   if (c->blocks < 0 || c->layers < 1 || c->rows < 0 || c->width < 0 || c->heads < 1) return LM_ERR_INVALID_ARG;
   if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128) return LM_ERR_UNSUPPORTED;
   if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) return LM_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(c->width) * c->block > INT_MAX - 256 || c->blocks > INT_MAX) return LM_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->width) * c->block > INT_MAX - 65536 || c->blocks > INT_MAX) return LM_ERR_UNSUPPORTED;
   if (!aligned(c->k8, 16) || !aligned(c->v8, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
       !aligned(c->table, 4) || !aligned(c->lens, 4))
     return LM_ERR_MISALIGNED;

@@ -347,6 +347,24 @@ def test_strided_queries_streams_and_graphs(lm):
         assert torch.equal(out, want)
 
 
+def test_calls_of_many_shapes_share_their_scratch(lm):
+    """Rows long enough to be split, and row counts that change from call to call."""
+    shapes = [(1, 1, 9000, 1), (3, 2, 5000, 1), (1, 8, 4000, 4), (30, 4, 2000, 1), (2, 1, 20000, 2), (6, 6, 1500, 20)]
+    made = []
+    for i, (rows, heads, tokens, t) in enumerate(shapes):
+        c = filled(lm, rows, tokens, heads, 64, 32, torch.float16, seed=i)
+        c.lens.fill_(tokens - t)
+        made.append((c, gen(i)(rows, t, heads, 64).half()))
+    first = [c.attend(0, q) for c, q in made]
+    for c, q in made:
+        check_attend(c.attend(0, q), c, 0, q, [q.shape[1]] * c.rows, True)
+    for _ in range(3):
+        for (c, q), want in zip(reversed(made), reversed(first)):
+            assert torch.equal(c.attend(0, q), want)
+        for (c, q), want in zip(made, first):
+            assert torch.equal(c.attend(0, q), want)
+
+
 # ---- reorder --------------------------------------------------------------
 
 @pytest.mark.parametrize("block,layers", [(16, 1), (32, 3), (128, 2)])

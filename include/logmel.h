@@ -615,7 +615,7 @@ lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const void *q, c
  *   out_history  [clips][beams][width]: the continued beam's history with
  *             the token at `length` (NULL where history is); must not
  *             overlap history.
- *   beams     1..32;  vocab 1..2^31-1
+ *   beams     1..32;  vocab 1..2^24
  *   workspace device, >= lm_beam_step_workspace_size(...), 16-byte aligned,
  *             zeroed before its first use, left usable by every call.
  * Errors as above.  clips == 0 enqueues nothing.

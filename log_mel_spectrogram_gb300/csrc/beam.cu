@@ -292,22 +292,32 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p) {
     // ... its lists, one part after the other: n-way insertion of sorted lists.
     const uint64_t *const pk = p.part_keys + r * p.parts * n;
     uint64_t l = 0;
-    for (int i = 0; i < p.parts; ++i) {
-      const uint64_t k = lane < n ? __ldcg(reinterpret_cast<const unsigned long long *>(pk + i * n + lane)) : 0;
-      // Both sorted, one per lane: an entry's place is its own index plus the
-      // number of larger entries of the other list.
-      int pl = lane, pk_ = lane;
-      for (int j = 0; j < n; ++j) {
-        pl += __shfl_sync(0xffffffffu, k, j) > l;
-        pk_ += __shfl_sync(0xffffffffu, l, j) > k;
+    for (int i0 = 0; i0 < p.parts; i0 += 4) {
+      uint64_t next[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        next[i] = lane < n && i0 + i < p.parts
+                      ? __ldcg(reinterpret_cast<const unsigned long long *>(pk + (i0 + i) * n + lane))
+                      : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t k = next[i];
+        if (i0 + i >= p.parts) break;
+        // Both sorted, one per lane: an entry's place is its own index plus
+        // the number of larger entries of the other list.
+        int pl = lane, pn = lane;
+        for (int j = 0; j < n; ++j) {
+          pl += __shfl_sync(0xffffffffu, k, j) > l;
+          pn += __shfl_sync(0xffffffffu, l, j) > k;
+        }
+        uint64_t *const mine_s = keys + warp * n;
+        const int have = __popc(__ballot_sync(0xffffffffu, l != 0)) + __popc(__ballot_sync(0xffffffffu, k != 0));
+        __syncwarp();
+        if (lane < n && l != 0 && pl < n) mine_s[pl] = l;
+        if (lane < n && k != 0 && pn < n) mine_s[pn] = k;
+        __syncwarp();
+        l = lane < n && lane < have ? mine_s[lane] : 0;
       }
-      uint64_t *const mine_s = keys + warp * n;
-      __syncwarp();
-      if (lane < n && l != 0 && pl < n) mine_s[pl] = l;
-      if (lane < n && k != 0 && pk_ < n) mine_s[pk_] = k;
-      const int have = __popc(__ballot_sync(0xffffffffu, l != 0)) + __popc(__ballot_sync(0xffffffffu, k != 0));
-      __syncwarp();
-      l = lane < n && lane < have ? mine_s[lane] : 0;
     }
     if (lane < n) {
       float t = -INFINITY;
@@ -352,10 +362,23 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p) {
   }
   if (!a.history) return;
   __syncthreads();
-  for (int b = warp; b < n; b += kWarps) {
-    const int32_t *const from = a.history + (row0 + parents[b]) * a.width;
-    int32_t *const to = a.out_history + (row0 + b) * a.width;
-    for (int64_t i = lane; i < a.width; i += 32) to[i] = i == a.length ? tokens[b] : from[i];
+  const uint32_t width = static_cast<uint32_t>(a.width), all = n * width;
+  const int32_t *const from = a.history + row0 * a.width;
+  int32_t *const to = a.out_history + row0 * a.width;
+  for (uint32_t i0 = threadIdx.x; i0 < all; i0 += 8 * kThreads) {
+    int32_t t[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t i = i0 + u * kThreads;
+      if (i >= all) continue;
+      const uint32_t b = i / width, c = i - b * width;
+      t[u] = c == a.length ? tokens[b] : __ldg(from + parents[b] * static_cast<int64_t>(width) + c);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t i = i0 + u * kThreads;
+      if (i < all) to[i] = t[u];
+    }
   }
 }
 
@@ -369,6 +392,7 @@ lm_status check(const lm_beam_args *a) {
   if (a->beams > kMaxBeams || a->vocab > kMaxVocab || a->clips > INT_MAX / kMaxBeams) return LM_ERR_UNSUPPORTED;
   if ((a->history == nullptr) != (a->out_history == nullptr)) return LM_ERR_INVALID_ARG;
   if (a->history && (a->length < 0 || a->length >= a->width)) return LM_ERR_INVALID_ARG;
+  if (a->width > (1 << 24)) return LM_ERR_UNSUPPORTED;
   return LM_OK;
 }
 

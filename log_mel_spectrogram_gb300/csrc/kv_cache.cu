@@ -27,47 +27,76 @@ struct AppendParams {
   void *values[2];
   const int32_t *counts;
   int32_t tokens, spans;         // spans: blocks per row that a step can touch
-  int64_t units;                 // rows * spans * heads
+  uint32_t units;                // rows * spans * heads
   bool vec;                      // 16-byte loads of src are aligned
 };
-
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]) {
-  if (vec) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2<T>(u[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f32(p[i]);
-  }
-}
 
 __device__ __forceinline__ int byte_of(uint2 w, int i) {
   const uint32_t u = i < 4 ? w.x : w.y;
   return static_cast<int>(u << (24 - 8 * (i & 3))) >> 24;
 }
 
+// The largest |x| of two packed values and an earlier result; NaN stays NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w);
+template <>
+__device__ __forceinline__ uint32_t max_abs2<__half>(uint32_t m, uint32_t w) {
+  const __half2 r = __hmax2_nan(*reinterpret_cast<__half2 *>(&m), __habs2(*reinterpret_cast<__half2 *>(&w)));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t max_abs2<__nv_bfloat16>(uint32_t m, uint32_t w) {
+  const __nv_bfloat162 r =
+      __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&m), __habs2(*reinterpret_cast<__nv_bfloat162 *>(&w)));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// x / scale to the nearest integer, ties to even, as __fdiv_rn and rintf give
+// it, for eight values with |x / scale| <= 128, without the division: adding
+// 1.5 * 2^23 to x * (1 / scale) leaves the integer in the low bits.  The
+// product is within 2^-22 * 128 of the quotient, so that only values within
+// 2^-14 of a half can differ, and those take the division.
+__device__ __forceinline__ void quantise8(const float (&x)[8], float scale, float inv, float (&q)[8], uint2 &w) {
+  constexpr float kMagic = 12582912.0f;
+  float t[8], off = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    t[j] = fmaf(x[j], inv, kMagic);
+    q[j] = t[j] - kMagic;
+    off = fmaxf(off, fabsf(fmaf(x[j], inv, -q[j])));
+  }
+  // (An infinite or a subnormal scale has no inverse to go by.)
+  if (!(off < 0.5f - 6.2e-5f) || !(inv > 0.0f && inv < INFINITY)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      q[j] = static_cast<float>(static_cast<int>(rintf(__fdiv_rn(x[j], scale))));  // NaN as 0
+      t[j] = q[j] + kMagic;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t a = __byte_perm(__float_as_uint(t[4 * j]), __float_as_uint(t[4 * j + 1]), 0x0040);
+    const uint32_t b = __byte_perm(__float_as_uint(t[4 * j + 2]), __float_as_uint(t[4 * j + 3]), 0x0040);
+    (j ? w.y : w.x) = __byte_perm(a, b, 0x5410);
+  }
+}
+
 // One unit: row r's span s of head h.  D and BS are the head dimension and
 // the tokens of a block; NT threads work on the unit.
 template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams p) {
   constexpr int NT = BS * D / 64;
   constexpr int PER = kThreads / NT;  // units per CTA
   __shared__ float part[kThreads / 32];
   const int tid = threadIdx.x % NT;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * PER + threadIdx.x / NT;
+  const uint32_t unit = blockIdx.x * PER + threadIdx.x / NT;
   const int which = blockIdx.y;
   const bool in = unit < p.units;
-  const int64_t uu = in ? unit : 0;
-  const int h = static_cast<int>(uu % p.c.heads);
-  const int span = static_cast<int>(uu / p.c.heads % p.spans);
-  const int r = static_cast<int>(uu / p.c.heads / p.spans);
+  const uint32_t uu = in ? unit : 0;
+  const uint32_t rs = uu / static_cast<uint32_t>(p.c.heads);
+  const int h = static_cast<int>(uu - rs * p.c.heads);
+  const int r = static_cast<int>(rs / static_cast<uint32_t>(p.spans));
+  const int span = static_cast<int>(rs - static_cast<uint32_t>(r) * p.spans);
 
   const int held = min(max(p.c.lens[r], 0), p.c.width * BS);
   const int fresh = p.counts ? min(max(p.counts[r], 0), p.tokens) : p.tokens;
@@ -78,25 +107,50 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   const int blk = in && col < p.c.width ? p.c.table[static_cast<int64_t>(r) * p.c.width + col] : -1;
   const bool ok = blk >= 0 && blk < p.c.blocks && base < end;
   const int64_t tile = ok ? (static_cast<int64_t>(blk) * p.c.heads + h) : 0;
-  int8_t *const q8 = (which ? p.c.v8 : p.c.k8) + p.c.layer_tiles * BS * D + tile * BS * D;
+  int8_t *const q8 = (which ? p.c.v8 : p.c.k8) + (p.c.layer_tiles + tile) * BS * D;
   float *const qs = (which ? p.c.v_scale : p.c.k_scale) + p.c.layer_tiles + tile;
+  const bool had = ok && base < held;  // the block holds tokens already
+  const float before = had ? *qs : 0.0f;
 
+  // Vector i of this thread: token v / (D / 8), elements v % (D / 8) * 8, of
+  // v = i * NT + tid.  A new token's values, or an old one's bytes.
   const T *const src = static_cast<const T *>(p.src[which]) + r * p.row_s[which] + h * p.head_s[which];
-  float x[kVecs][8];
-  float top = 0.0f;
+  uint32_t x[kVecs][4];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int v = i * NT + tid;
     const int tok = base + v / (D / 8), d = v % (D / 8) * 8;
-    if (ok && tok >= held && tok < end) {
-      load8(src + static_cast<int64_t>(tok - held) * p.tok_s[which] + d, p.vec, x[i]);
+    x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
+    if (ok && tok < held) {
+      const uint2 w = *reinterpret_cast<const uint2 *>(q8 + (tok - base) * D + d);
+      x[i][0] = w.x;
+      x[i][1] = w.y;
+    } else if (ok && tok < end) {
+      const T *const s = src + static_cast<int64_t>(tok - held) * p.tok_s[which] + d;
+      if (p.vec) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(s));
+        x[i][0] = w.x;
+        x[i][1] = w.y;
+        x[i][2] = w.z;
+        x[i][3] = w.w;
+      } else {
+        const uint16_t *const s16 = reinterpret_cast<const uint16_t *>(s);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = fabsf(x[i][j]);
-        top = fmaxf(top, a <= 3.402823466e38f ? a : __int_as_float(0x7f800000));
+        for (int j = 0; j < 4; ++j) x[i][j] = s16[2 * j] | static_cast<uint32_t>(s16[2 * j + 1]) << 16;
       }
     }
   }
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int tok = base + (i * NT + tid) / (D / 8);
+    if (tok >= held)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) most = max_abs2<T>(most, x[i][j]);
+  }
+  const float2 m2 = unpack2<T>(most);
+  float top = fmaxf(m2.x, m2.y);
+  if (m2.x != m2.x || m2.y != m2.y) top = __int_as_float(0x7f800000);
   // The unit's maximum.
 #pragma unroll
   for (int o = (NT < 32 ? NT : 32) / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -107,91 +161,114 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, part[w0 + w]);
   }
-  const float before = ok && base < held ? *qs : 0.0f;
   float now = fmaxf(before, top * (1.0f / 127.0f));
   if (now == 0.0f) now = 1.0f;
-  const float shrink = before / now;
+  const float shrink = had ? before / now : 1.0f, inv = 1.0f / now;
   // Every thread of the unit has read the old scale before one writes it.
-  if (NT > 32) {
-    __syncthreads();
-  } else {
-    __syncwarp();
-  }
+  if (NT <= 32) __syncwarp();
   if (ok && tid == 0) *qs = now;
 
-  T *const out = p.values[which] ? static_cast<T *>(p.values[which]) : nullptr;
+  T *const out = static_cast<T *>(p.values[which]);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int v = i * NT + tid;
     const int tok = base + v / (D / 8), d = v % (D / 8) * 8;
-    float val[8] = {};
+    float q[8] = {};
     if (ok && tok < end) {
-      int q[8];
-      const bool is_new = tok >= held;
-      uint2 w = make_uint2(0, 0);
       uint2 *const at = reinterpret_cast<uint2 *>(q8 + (tok - base) * D + d);
-      if (is_new) {
+      if (tok >= held) {
+        float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = static_cast<int>(rintf(x[i][j] / now));
-      } else if (out || shrink != 1.0f) {
-        w = *at;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = static_cast<int>(rintf(static_cast<float>(byte_of(w, j)) * shrink));
-      }
-      if (is_new || shrink != 1.0f) {
-        w.x = (q[0] & 255) | (q[1] & 255) << 8 | (q[2] & 255) << 16 | static_cast<uint32_t>(q[3]) << 24;
-        w.y = (q[4] & 255) | (q[5] & 255) << 8 | (q[6] & 255) << 16 | static_cast<uint32_t>(q[7]) << 24;
+        for (int j = 0; j < 4; ++j) {
+          const float2 f2 = unpack2<T>(x[i][j]);
+          f[2 * j] = f2.x;
+          f[2 * j + 1] = f2.y;
+        }
+        uint2 w;
+        quantise8(f, now, inv, q, w);
         *at = w;
+      } else {
+        uint2 w = make_uint2(x[i][0], x[i][1]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = static_cast<float>(byte_of(w, j));
+        if (shrink != 1.0f) {
+          int n[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            n[j] = static_cast<int>(rintf(q[j] * shrink));
+            q[j] = static_cast<float>(n[j]);
+          }
+          w.x = (n[0] & 255) | (n[1] & 255) << 8 | (n[2] & 255) << 16 | static_cast<uint32_t>(n[3]) << 24;
+          w.y = (n[4] & 255) | (n[5] & 255) << 8 | (n[6] & 255) << 16 | static_cast<uint32_t>(n[7]) << 24;
+          *at = w;
+        }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) val[j] = static_cast<float>(q[j]) * now;
+      for (int j = 0; j < 8; ++j) q[j] *= now;
     }
     if (out && in) {
-      const int64_t at = ((static_cast<int64_t>(r) * p.spans * BS + span * BS + v / (D / 8)) * p.c.heads + h) * D + d;
-      *reinterpret_cast<uint4 *>(out + at) = make_uint4(pack2<T>(val[0], val[1]), pack2<T>(val[2], val[3]),
-                                                        pack2<T>(val[4], val[5]), pack2<T>(val[6], val[7]));
+      const int64_t to = (static_cast<int64_t>(rs) * BS + v / (D / 8)) * p.c.heads + h;
+      __stcs(reinterpret_cast<uint4 *>(out + to * D + d),
+             make_uint4(pack2<T>(q[0], q[1]), pack2<T>(q[2], q[3]), pack2<T>(q[4], q[5]), pack2<T>(q[6], q[7])));
     }
   }
 }
+
+constexpr int kReadVecs = 4;  // vectors of a thread
 
 struct ReadParams {
   KvView c;
   void *out[2];
-  int32_t start, count, layers;
-  int64_t vecs;  // layers * rows * count * heads * head_dim / 8
+  int32_t start, count, dim_shift;  // dim_shift: log2 of a head's 8-element vectors
+  uint32_t vecs;                    // of a row: count * heads * head_dim / 8
 };
 
+// Grid: (part of a row's vectors, row, layer and keys or values).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
-  const int64_t v = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (v >= p.vecs) return;
-  const int which = blockIdx.y;
-  const int per = p.c.head_dim / 8;
-  const int d = static_cast<int>(v % per) * 8;
-  int64_t u = v / per;
-  const int h = static_cast<int>(u % p.c.heads);
-  u /= p.c.heads;
-  const int64_t tok = p.start + u % p.count;
-  u /= p.count;
-  const int r = static_cast<int>(u % p.c.rows);
-  const int64_t layer = u / p.c.rows;
-  const int64_t col = tok / p.c.block;
-  uint4 w = make_uint4(0, 0, 0, 0);
-  if (tok < p.c.lens[r] && col < p.c.width) {
-    const int blk = p.c.table[static_cast<int64_t>(r) * p.c.width + col];
-    if (blk >= 0 && blk < p.c.blocks) {
-      const int64_t tile = p.c.layer_tiles + (layer * p.c.blocks + blk) * p.c.heads + h;
-      const float s = (which ? p.c.v_scale : p.c.k_scale)[tile];
-      const uint2 q = *reinterpret_cast<const uint2 *>((which ? p.c.v8 : p.c.k8) +
-                                                       (tile * p.c.block + tok % p.c.block) * p.c.head_dim + d);
-      float x[8];
+  const int which = blockIdx.z & 1, r = blockIdx.y;
+  const int64_t layer = blockIdx.z >> 1;
+  const int32_t *const table = p.c.table + static_cast<int64_t>(r) * p.c.width;
+  const int64_t tiles = p.c.layer_tiles + layer * p.c.blocks * p.c.heads;
+  const int8_t *const x8 = which ? p.c.v8 : p.c.k8;
+  const float *const xs = which ? p.c.v_scale : p.c.k_scale;
+  uint4 *const out =
+      reinterpret_cast<uint4 *>(p.out[which]) + (layer * p.c.rows + r) * static_cast<int64_t>(p.vecs);
+  const uint32_t per_token = static_cast<uint32_t>(p.c.heads) << p.dim_shift;
+  const int len = p.c.lens[r];
+  const int block_shift = 31 - __clz(p.c.block);
+  const uint32_t v0 = blockIdx.x * (kThreads * kReadVecs) + threadIdx.x;
+  uint2 q[kReadVecs];
+  float s[kReadVecs];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(byte_of(q, j)) * s;
-      w = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
-    }
+  for (int i = 0; i < kReadVecs; ++i) {
+    const uint32_t v = v0 + i * kThreads;
+    q[i] = make_uint2(0, 0);
+    s[i] = 0.0f;
+    if (v >= p.vecs) continue;
+    const uint32_t t = v / per_token, e = v - t * per_token;
+    const int64_t tok = static_cast<int64_t>(p.start) + t;
+    const int64_t col = tok >> block_shift;
+    if (tok >= len || col >= p.c.width) continue;
+    const int blk = __ldg(table + col);
+    if (blk < 0 || blk >= p.c.blocks) continue;
+    const int64_t tile = tiles + static_cast<int64_t>(blk) * p.c.heads + (e >> p.dim_shift);
+    s[i] = xs[tile];
+    q[i] = *reinterpret_cast<const uint2 *>(x8 + ((tile << block_shift) + (tok & (p.c.block - 1))) * p.c.head_dim +
+                                            (e & ((1u << p.dim_shift) - 1)) * 8);
   }
-  reinterpret_cast<uint4 *>(p.out[which])[v] = w;
+#pragma unroll
+  for (int i = 0; i < kReadVecs; ++i) {
+    const uint32_t v = v0 + i * kThreads;
+    if (v >= p.vecs) continue;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(byte_of(q[i], j)) * s[i];
+    __stcs(out + v, make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7])));
+  }
 }
+
+constexpr int kCopy = 4;  // vectors of keys and of values that a thread has in flight
 
 struct ReorderParams {
   KvView c;
@@ -222,14 +299,30 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
     const int from = p.c.table[from_row * width + col], to = p.c.spare[r];
     if (from >= 0 && from < p.c.blocks && to >= 0 && to < p.c.blocks) {
       // 16-byte vectors of a block's keys or values over all heads, per layer.
-      const int64_t vecs = static_cast<int64_t>(p.c.heads) * p.c.block * p.c.head_dim / 16;
-      const int64_t all = vecs * p.c.layers;
-      for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < all;
-           i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t layer = i / vecs, v = i % vecs;
-        const int64_t a = (layer * p.c.blocks + from) * vecs + v, b = (layer * p.c.blocks + to) * vecs + v;
-        reinterpret_cast<uint4 *>(p.c.k8)[b] = reinterpret_cast<const uint4 *>(p.c.k8)[a];
-        reinterpret_cast<uint4 *>(p.c.v8)[b] = reinterpret_cast<const uint4 *>(p.c.v8)[a];
+      const uint32_t vecs = static_cast<uint32_t>(p.c.heads) * p.c.block * p.c.head_dim / 16;
+      const uint32_t all = vecs * p.c.layers;
+      // Only the tokens that are held: a head's first `used` vectors.
+      const int head_vecs = p.c.block * p.c.head_dim / 16, used = len % p.c.block * p.c.head_dim / 16;
+      for (uint32_t i0 = blockIdx.x * kThreads + threadIdx.x; i0 < all; i0 += kCopy * gridDim.x * kThreads) {
+        uint4 x[kCopy][2];
+        int64_t at[kCopy];
+#pragma unroll
+        for (int u = 0; u < kCopy; ++u) {
+          const uint32_t i = i0 + u * gridDim.x * kThreads;
+          const uint32_t layer = i / vecs, v = i - layer * vecs;
+          at[u] = -1;
+          if (i >= all || static_cast<int>(v & (head_vecs - 1)) >= used) continue;
+          const int64_t a = (static_cast<int64_t>(layer) * p.c.blocks + from) * vecs + v;
+          at[u] = (static_cast<int64_t>(layer) * p.c.blocks + to) * vecs + v;
+          x[u][0] = reinterpret_cast<const uint4 *>(p.c.k8)[a];
+          x[u][1] = reinterpret_cast<const uint4 *>(p.c.v8)[a];
+        }
+#pragma unroll
+        for (int u = 0; u < kCopy; ++u) {
+          if (at[u] < 0) continue;
+          reinterpret_cast<uint4 *>(p.c.k8)[at[u]] = x[u][0];
+          reinterpret_cast<uint4 *>(p.c.v8)[at[u]] = x[u][1];
+        }
       }
       const int scales = p.c.heads * p.c.layers;
       for (int i = blockIdx.x * kThreads + threadIdx.x; i < scales; i += gridDim.x * kThreads) {
@@ -273,9 +366,8 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
 template <typename T, int D>
 lm_status append_block(const AppendParams &p, int block, cudaStream_t s) {
   const int nt = block * D / 64;
-  const int64_t ctas = (p.units * nt + kThreads - 1) / kThreads;
-  if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(ctas), 2);
+  const int per = kThreads / nt;
+  const dim3 grid((p.units + per - 1) / per, 2);
   switch (block) {
     case 16: append_kernel<T, D, 16><<<grid, kThreads, 0, s>>>(p); break;
     case 32: append_kernel<T, D, 32><<<grid, kThreads, 0, s>>>(p); break;
@@ -368,7 +460,9 @@ extern "C" lm_status lm_kv_append(const lm_kv_cache *cache, int32_t layer, const
   p.counts = counts;
   p.tokens = tokens;
   p.spans = (tokens - 1 + cache->block - 1) / cache->block + 1;
-  p.units = static_cast<int64_t>(cache->rows) * p.spans * cache->heads;
+  const int64_t units = static_cast<int64_t>(cache->rows) * p.spans * cache->heads;
+  if (units > INT_MAX - kThreads) return LM_ERR_UNSUPPORTED;
+  p.units = static_cast<uint32_t>(units);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dtype == LM_F16 ? append_dim<__half>(p, cache->head_dim, cache->block, s)
                          : append_dim<__nv_bfloat16>(p, cache->head_dim, cache->block, s);
@@ -389,11 +483,12 @@ extern "C" lm_status lm_kv_read(const lm_kv_cache *cache, int32_t layer, int32_t
   p.out[1] = v_out;
   p.start = start;
   p.count = count;
-  p.layers = layer < 0 ? cache->layers : 1;
-  p.vecs = static_cast<int64_t>(p.layers) * cache->rows * count * cache->heads * (cache->head_dim / 8);
-  const int64_t ctas = (p.vecs + kThreads - 1) / kThreads;
-  if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(ctas), 2);
+  const int layers = layer < 0 ? cache->layers : 1;
+  p.dim_shift = cache->head_dim == 32 ? 2 : cache->head_dim == 64 ? 3 : 4;
+  const int64_t vecs = (static_cast<int64_t>(count) * cache->heads) << p.dim_shift;
+  if (vecs > INT_MAX - kThreads * kReadVecs || cache->rows > 65535 || layers > 32767) return LM_ERR_UNSUPPORTED;
+  p.vecs = static_cast<uint32_t>(vecs);
+  const dim3 grid((p.vecs + kThreads * kReadVecs - 1) / (kThreads * kReadVecs), cache->rows, 2 * layers);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == LM_F16) {
     read_kernel<__half><<<grid, kThreads, 0, s>>>(p);
@@ -420,9 +515,13 @@ extern "C" lm_status lm_kv_reorder(const lm_kv_cache *cache, const int32_t *pare
   p.parents = parents;
   p.done = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + kWorkspaceHeaderBytes);
   p.beams = beams;
-  // 8 vectors of keys and of values per thread, within one wave of CTAs or so.
+  // kCopy vectors of keys and of values per thread, or one where that leaves
+  // most of the device idle.
   const int64_t vecs = static_cast<int64_t>(cache->layers) * cache->heads * cache->block * cache->head_dim / 16;
-  p.parts = static_cast<int32_t>(vecs / (8 * kThreads) > 0 ? (vecs / (8 * kThreads) < 64 ? vecs / (8 * kThreads) : 64) : 1);
+  if (vecs > INT_MAX / 2) return LM_ERR_UNSUPPORTED;
+  int64_t parts = (vecs + kCopy * kThreads - 1) / (kCopy * kThreads);
+  if (parts * cache->rows < 152) parts = (vecs + kThreads - 1) / kThreads;
+  p.parts = static_cast<int32_t>(parts < 256 ? parts : 256);
   reorder_kernel<<<dim3(p.parts, cache->rows), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   LM_CUDA_TRY(cudaGetLastError());
   return LM_OK;

@@ -22,6 +22,8 @@
 // copied into padded rows in the workspace.
 #include <climits>
 #include <cuda.h>
+#include <map>
+#include <mutex>
 
 #include "half.cuh"
 #include "internal.h"
@@ -35,8 +37,11 @@ constexpr int kBk = 64;             // elements of k per stage: one 128-byte swi
 constexpr int kLanes = 128;         // rows of the tile's lane side
 constexpr int kMaxBn = 256;
 constexpr int kMaxStages = 8;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 128 + 32 * kEpiWarps;  // TMA, MMA, TMEM and one idle warp; then the epilogue
+
+// Warps: TMA, MMA, TMEM and an idle one, then the epilogue's.  16 of those where
+// a tile is wide and the activation is computed on all of it, 8 else.
+constexpr int epi_warps(bool swap) { return swap ? 8 : 16; }
+constexpr int threads_of(bool swap) { return 128 + 32 * epi_warps(swap); }
 constexpr int kSmemBudget = 227 * 1024 - 1024 - 4096;
 
 struct LinearParams {
@@ -47,6 +52,7 @@ struct LinearParams {
   int32_t rows, k, n;         // rows per group
   int32_t bn, stages, kblocks, tmem_cols;
   int32_t lane_tiles, col_tiles, tiles;  // tiles along the lanes and columns of one group, and in all
+  int32_t lane_step;          // rows along the lanes of a tile: 128, or a pair's 256
   int32_t splits;             // CTAs that share a tile's k
   int32_t bias_f32, out_f32, act, vec32;
   uint32_t idesc;
@@ -54,7 +60,7 @@ struct LinearParams {
   uint32_t *err;
 };
 
-struct Barriers {
+struct alignas(16) Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
@@ -62,31 +68,52 @@ struct Barriers {
   int abort;
 };
 
-// erf by formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
-// Functions: off by at most 1.5e-7.
-__device__ __forceinline__ float erf_as(float x) {
-  const float a = fabsf(x);
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, a, 1.0f));
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  return copysignf(1.0f - p * t * __expf(-a * a), x);
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// max(x, 0), NaN for NaN.
+__device__ __forceinline__ float relu(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt 2) / 2, with erfc by formula
+// 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions
+// (erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), off by
+// at most 1.5e-7); the coefficients below are halved.  Past |z| = 20 the second
+// term is 0.
+__device__ __forceinline__ float gelu(float z) {
+  const float a = fminf(fabsf(z), 20.0f);
+  const float t = rcp(fmaf(0.3275911f * 0.70710678118654752f, a, 1.0f));
+  float q = fmaf(0.5f * 1.061405429f, t, -0.5f * 1.453152027f);
+  q = fmaf(q, t, 0.5f * 1.421413741f);
+  q = fmaf(q, t, -0.5f * 0.284496736f);
+  q = fmaf(q, t, 0.5f * 0.254829592f);
+  const float e = ex2(a * (a * (-0.5f * kLog2e)));
+  return fmaf(-a * t, q * e, relu(z));
 }
 
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
-  if (ACT == LM_ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays
-  if (ACT == LM_ACT_GELU) {
-    const float h = 0.5f * z;
-    return fmaf(h, erf_as(z * 0.70710678118654752f), h);
-  }
+  if (ACT == LM_ACT_RELU) return relu(z);
+  if (ACT == LM_ACT_GELU) return gelu(z);
   if (ACT == LM_ACT_GELU_TANH) {
     // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
-    const float u = 0.79788456080286536f * fmaf(0.044715f * z * z, z, z);
-    return z * __fdividef(1.0f, 1.0f + __expf(-2.0f * u));
+    const float u = fmaf(-2.0f * 0.79788456080286536f * kLog2e * 0.044715f * z * z, z,
+                         -2.0f * 0.79788456080286536f * kLog2e * z);
+    return z * rcp(1.0f + ex2(u));
   }
-  if (ACT == LM_ACT_SILU) return z * __fdividef(1.0f, 1.0f + __expf(-z));
+  if (ACT == LM_ACT_SILU) return z * rcp(1.0f + ex2(-kLog2e * z));
   return z;
 }
 
@@ -153,7 +180,13 @@ __device__ __forceinline__ void finish16(const LinearParams &p, const uint32_t (
   const int64_t row = group_row + lane_at;
   float y[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) y[j] = p.scale * activate<ACT>(__uint_as_float(r[j]) + bias_s[j]);
+  for (int j = 0; j < 16; j += 4) {
+    const float4 v = *reinterpret_cast<const float4 *>(bias_s + j);
+    y[j] = p.scale * activate<ACT>(__uint_as_float(r[j]) + v.x);
+    y[j + 1] = p.scale * activate<ACT>(__uint_as_float(r[j + 1]) + v.y);
+    y[j + 2] = p.scale * activate<ACT>(__uint_as_float(r[j + 2]) + v.z);
+    y[j + 3] = p.scale * activate<ACT>(__uint_as_float(r[j + 3]) + v.w);
+  }
   if (col_at + 16 <= p.n) {
     if (p.residual) {
       float x[16];
@@ -195,19 +228,21 @@ struct Tile {
   int group, lane0, col0;
 };
 
-// Consecutive tiles share their rows along the lanes.
-__device__ __forceinline__ Tile tile_at(const LinearParams &p, int t) {
+// Consecutive tiles share their rows along the lanes; of a pair's 256 rows
+// CTA `rank` has 128.
+__device__ __forceinline__ Tile tile_at(const LinearParams &p, int t, int rank) {
   Tile o;
   const int per = p.lane_tiles * p.col_tiles;
   o.group = t / per;
   const int u = t % per;
-  o.lane0 = u / p.col_tiles * kLanes;
+  o.lane0 = u / p.col_tiles * p.lane_step + rank * kLanes;
   o.col0 = u % p.col_tiles * p.bn;
   return o;
 }
 
 // Turns tile `t` into outputs.  `acc` is the tile's tensor memory; warp e of
-// the epilogue reads lanes 32 * (e % 4) .. + 31 and every second 16 columns.
+// the epilogue reads lanes 32 * (e % 4) .. + 31 and every second (fourth) 16
+// columns.
 template <typename T, int ACT, bool SWAP>
 __device__ __forceinline__ void epilogue(const LinearParams &p, const Tile &t, uint32_t acc, const float *bias_s, int e) {
   const int lane = 32 * (e % 4) + static_cast<int>(threadIdx.x % 32);
@@ -215,17 +250,21 @@ __device__ __forceinline__ void epilogue(const LinearParams &p, const Tile &t, u
   const int64_t group_row = static_cast<int64_t>(t.group) * p.rows;
   const int at = t.lane0 + lane;
   const float lane_bias = SWAP ? bias_at<T>(p, at) : 0.0f;
-  for (int c = e / 4 * 16; c < p.bn; c += kEpiWarps / 4 * 16) {
-    if (t.col0 + c >= (SWAP ? p.rows : p.n)) break;
-    uint32_t r[16];
-    if (p.kblocks > 0) {
-      tmem_ld16(base + c, r);
-      tmem_wait_ld();
-    } else {
+  // Columns that exist, 16 at a time; the next 16 are on their way from tensor
+  // memory while these are worked on.
+  constexpr int STEP = epi_warps(SWAP) / 4 * 16;
+  const int cols = min(p.bn, (SWAP ? p.rows : p.n) - t.col0);
+  int c = e / 4 * 16;
+  if (c >= cols) return;
+  uint32_t r[16];
+  tmem_ld16(base + c, r);
+  for (; c < cols; c += STEP) {
+    uint32_t now[16];
+    tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) r[j] = 0;
-    }
-    finish16<T, ACT, SWAP>(p, r, bias_s + c, lane_bias, group_row, at, t.col0 + c);
+    for (int j = 0; j < 16; ++j) now[j] = p.kblocks > 0 ? r[j] : 0u;
+    if (c + STEP < cols) tmem_ld16(base + c + STEP, r);
+    finish16<T, ACT, SWAP>(p, now, bias_s + c, lane_bias, group_row, at, t.col0 + c);
   }
 }
 
@@ -261,31 +300,44 @@ __device__ __forceinline__ void finish_split(const LinearParams &p, const Tile &
 }
 
 // Barrier of the epilogue's warps: whether `ok` holds for all their threads.
+template <int THREADS>
 __device__ __forceinline__ bool epilogue_all(bool ok) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(ok ? 1u : 0u), "n"(32 * kEpiWarps)
+      : "r"(ok ? 1u : 0u), "n"(THREADS)
       : "memory");
   return r != 0;
 }
 
-template <typename T, bool SWAP, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+enum class Form {
+  kOne,    // a CTA per tile of 128 lanes
+  kPair,   // two CTAs per tile of 256 lanes
+  kSplit,  // a cluster per tile, each CTA a part of k
+};
+
+template <typename T, bool SWAP, Form FORM>
+__global__ void __launch_bounds__(threads_of(SWAP), 1)
     linear_kernel(const __grid_constant__ CUtensorMap lane_map, const __grid_constant__ CUtensorMap col_map,
                   const LinearParams p) {
+  constexpr bool PAIR = FORM == Form::kPair, SPLIT = FORM == Form::kSplit;
+  constexpr int EPI = epi_warps(SWAP);
   extern __shared__ uint8_t smem_raw[];
   // Stages start on a 1024-byte boundary (the swizzle's period).
   uint8_t *const ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int stage_bytes = kLanes * 128 + p.bn * 128;
+  const int col_rows = PAIR ? p.bn / 2 : p.bn;  // rows of the column side that this CTA holds
+  const int stage_bytes = kLanes * 128 + col_rows * 128;
   Barriers &b = *reinterpret_cast<Barriers *>(ring + p.stages * stage_bytes);
   float *const bias_s = reinterpret_cast<float *>(&b + 1);  // two tiles of bn
-  const int warp = threadIdx.x / 32;
-  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
-  const int first = SPLIT ? static_cast<int>(blockIdx.x) / p.splits : static_cast<int>(blockIdx.x);
-  const int step = SPLIT ? p.tiles : static_cast<int>(gridDim.x);
+  // (The shuffle tells the compiler that the warp number is uniform.)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
+  const int rank = FORM != Form::kOne ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = SPLIT ? static_cast<int>(blockIdx.x) / p.splits
+                          : PAIR ? static_cast<int>(blockIdx.x) / 2 : static_cast<int>(blockIdx.x);
+  const int step = SPLIT ? p.tiles : PAIR ? static_cast<int>(gridDim.x) / 2 : static_cast<int>(gridDim.x);
+  const int lane_rank = PAIR ? rank : 0;
   // This CTA's part of k.
   const int k_begin = SPLIT ? static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / p.splits) : 0;
   const int k_end = SPLIT ? static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / p.splits) : p.kblocks;
@@ -297,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.acc_full[i], 1);
-      mbar_init(&b.acc_empty[i], 32 * kEpiWarps);
+      mbar_init(&b.acc_empty[i], PAIR ? 2 * EPI : EPI);
     }
     mbar_init(&b.drain, 1);
     b.abort = 0;
@@ -307,68 +359,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_map(&col_map);
     }
   }
-  if (warp == 2) {
-    tmem_alloc(&b.tmem, static_cast<uint32_t>(p.tmem_cols));
-    tmem_relinquish();
-  }
+  if (warp == 2) tmem_alloc<PAIR>(&b.tmem, static_cast<uint32_t>(p.tmem_cols));
   tcgen05_fence_before();
   __syncthreads();
+  __syncwarp();
+  if (PAIR) cluster_sync_all();  // both CTAs' barriers exist
   tcgen05_fence_after();
   const uint32_t tmem = b.tmem;
   volatile int *const abort = &b.abort;
 
   if (warp == 0) {
-    if (threadIdx.x == 0) {
-      int fills = 0;
-      bool ok = true;
-      for (int t = first; t < p.tiles && ok; t += step) {
-        const Tile tile = tile_at(p, t);
-        for (int kb = k_begin; kb < k_end; ++kb, ++fills) {
-          const int s = fills % p.stages;
-          if (fills >= p.stages && !mbar_wait(&b.empty[s], (fills / p.stages - 1) & 1, abort, p.err)) {
-            ok = false;
-            break;
-          }
+    int fills = 0, s = 0;
+    uint32_t phase = 1;  // of the stage's last release; the first round waits for nothing
+    bool ok = true;
+    for (int t = first; t < p.tiles && ok; t += step) {
+      const Tile tile = tile_at(p, t, lane_rank);
+      const int col0 = tile.col0 + (PAIR ? rank * col_rows : 0);
+      const int lane_z = SWAP ? 0 : tile.group, col_z = SWAP ? tile.group : 0;
+      for (int kb = k_begin; kb < k_end; ++kb) {
+        if (fills >= p.stages) ok = __all_sync(0xffffffffu, mbar_wait(&b.empty[s], phase, abort, p.err));
+        if (!ok) break;
+        if (elect_one()) {
           uint8_t *const dst = ring + s * stage_bytes;
-          mbar_arrive_expect_tx(&b.full[s], static_cast<uint32_t>(stage_bytes));
-          const int lane_z = SWAP ? 0 : tile.group, col_z = SWAP ? tile.group : 0;
-          tma_load_3d(dst, &lane_map, kb * kBk, tile.lane0, lane_z, &b.full[s]);
-          tma_load_3d(dst + kLanes * 128, &col_map, kb * kBk, tile.col0, col_z, &b.full[s]);
+          // A pair's copies all count on CTA 0's barrier, which expects both.
+          // (CTA 1's may be first: the phase still lacks CTA 0's arrival.)
+          uint32_t bar = smem_u32(&b.full[s]);
+          if (PAIR) bar = cluster_addr(bar, 0);
+          if (!PAIR || rank == 0)
+            mbar_arrive_expect_tx(&b.full[s], static_cast<uint32_t>(PAIR ? 2 * stage_bytes : stage_bytes));
+          tma_load_3d<PAIR>(dst, &lane_map, kb * kBk, tile.lane0, lane_z, bar);
+          tma_load_3d<PAIR>(dst + kLanes * 128, &col_map, kb * kBk, col0, col_z, bar);
+        }
+        __syncwarp();
+        ++fills;
+        if (++s == p.stages) {
+          s = 0;
+          phase ^= 1;
         }
       }
-      // No copy outlives the CTA, whatever the other warps did.
-      if (!ok) {
+    }
+    // No copy outlives the CTA, whatever the other warps did.
+    if (!ok) {
+      if (!PAIR || rank == 0) {
         for (int f = fills > p.stages ? fills - p.stages : 0; f < fills; ++f)
           mbar_wait_drain(&b.full[f % p.stages], (f / p.stages) & 1, p.err);
+      } else {  // counted on the other CTA's barriers: time enough for any copy
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 10000000ull) __nanosleep(1000);
       }
     }
   } else if (warp == 1) {
-    if (threadIdx.x == 32) {
-      int uses = 0, tiles = 0;
+    if (!PAIR || rank == 0) {
+      int s = 0, tiles = 0;
+      uint32_t phase = 0;
       bool ok = true;
+      const uint32_t ring_a = smem_u32(ring);
       for (int t = first; t < p.tiles && ok; t += step, ++tiles) {
         const int half = tiles & 1;
-        if (tiles >= 2 && !mbar_wait(&b.acc_empty[half], ((tiles >> 1) - 1) & 1, abort, p.err)) break;
+        if (tiles >= 2)
+          ok = __all_sync(0xffffffffu, mbar_wait(&b.acc_empty[half], ((tiles >> 1) - 1) & 1, abort, p.err));
         tcgen05_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
-        for (int kb = k_begin; kb < k_end; ++kb, ++uses) {
-          const int s = uses % p.stages;
-          if (!mbar_wait(&b.full[s], (uses / p.stages) & 1, abort, p.err)) {
-            ok = false;
-            break;
-          }
+        for (int kb = k_begin; kb < k_end && ok; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&b.full[s], phase, abort, p.err));
+          if (!ok) break;
           tcgen05_fence_after();
-          const uint64_t a = smem_desc_k128(smem_u32(ring + s * stage_bytes));
-          const uint64_t c = smem_desc_k128(smem_u32(ring + s * stage_bytes + kLanes * 128));
+          const uint64_t a = smem_desc_k128(ring_a + s * stage_bytes);
+          const uint64_t c = smem_desc_k128(ring_a + s * stage_bytes + kLanes * 128);
+          if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < kBk / 16; ++i)
-            tcgen05_mma_f16(d, a + 2 * i, c + 2 * i, p.idesc, kb > k_begin || i > 0);
-          tcgen05_commit(&b.empty[s]);
+            for (int i = 0; i < kBk / 16; ++i)
+              tcgen05_mma_f16<PAIR>(d, a + 2 * i, c + 2 * i, p.idesc, kb > k_begin || i > 0);
+            tcgen05_commit<PAIR>(&b.empty[s]);
+          }
+          __syncwarp();
+          if (++s == p.stages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
-        if (ok) tcgen05_commit(&b.acc_full[half]);
+        if (ok && elect_one()) tcgen05_commit<PAIR>(&b.acc_full[half]);
+        __syncwarp();
       }
-      if (*abort) {  // products in flight end before the tensor memory is given back
-        tcgen05_commit(&b.drain);
+      if (!ok) {  // products in flight end before the tensor memory is given back
+        if (elect_one()) tcgen05_commit<PAIR>(&b.drain);
         mbar_wait_drain(&b.drain, 0, p.err);
       }
     }
@@ -377,18 +451,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int et = threadIdx.x - 128;
     int tiles = 0;
     for (int t = first; t < p.tiles; t += step, ++tiles) {
-      const Tile tile = tile_at(p, t);
+      const Tile tile = tile_at(p, t, lane_rank);
       const int half = tiles & 1;
       float *const bs = bias_s + half * p.bn;
       if (!SWAP) {
         // Every epilogue warp has left the tile that used this half before:
         // the barrier of the tile in between lies behind it.
-        for (int i = et; i < p.bn; i += 32 * kEpiWarps) bs[i] = bias_at<T>(p, tile.col0 + i);
+        for (int i = et; i < p.bn; i += 32 * EPI) bs[i] = bias_at<T>(p, tile.col0 + i);
       }
       bool ok = mbar_wait(&b.acc_full[half], (tiles >> 1) & 1, abort, p.err);
       // One decision for all warps that meet at the barrier, and per warp
       // elsewhere: tensor memory loads are executed by whole warps.
-      ok = SWAP ? __all_sync(0xffffffffu, ok) : epilogue_all(ok);
+      ok = SWAP ? __all_sync(0xffffffffu, ok) : epilogue_all<32 * EPI>(ok);
       if (!ok) break;
       tcgen05_fence_after();
       const uint32_t acc = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
@@ -396,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Products are complete: the ring is free to hold the partial sums.
         float *const partial = reinterpret_cast<float *>(ring);
         const int lane = 32 * (e % 4) + static_cast<int>(threadIdx.x % 32);
-        for (int c = e / 4 * 16; c < p.bn; c += kEpiWarps / 4 * 16) {
+        for (int c = e / 4 * 16; c < p.bn; c += EPI / 4 * 16) {
           uint32_t r[16];
           tmem_ld16(acc + (static_cast<uint32_t>(32 * (e % 4)) << 16) + c, r);
           tmem_wait_ld();
@@ -406,7 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         epilogue_act<T, SWAP>(p, tile, acc, bs, e);
         tcgen05_fence_before();
-        mbar_arrive(&b.acc_empty[half]);
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) {
+          if (PAIR && rank != 0) {
+            mbar_arrive_cluster(cluster_addr(smem_u32(&b.acc_empty[half]), 0));
+          } else {
+            mbar_arrive(&b.acc_empty[half]);
+          }
+        }
       }
     }
   }
@@ -416,24 +497,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync_all();
     if (!*abort && first < p.tiles) {
-      const Tile tile = tile_at(p, first);
+      const Tile tile = tile_at(p, first, 0);
       const uint32_t partial = smem_u32(ring);
       const int tid = threadIdx.x;
+      constexpr int N = threads_of(SWAP);
       switch (p.act) {
-        case LM_ACT_RELU: finish_split<T, LM_ACT_RELU>(p, tile, partial, rank, tid, kThreads); break;
-        case LM_ACT_GELU: finish_split<T, LM_ACT_GELU>(p, tile, partial, rank, tid, kThreads); break;
-        case LM_ACT_GELU_TANH: finish_split<T, LM_ACT_GELU_TANH>(p, tile, partial, rank, tid, kThreads); break;
-        case LM_ACT_SILU: finish_split<T, LM_ACT_SILU>(p, tile, partial, rank, tid, kThreads); break;
-        default: finish_split<T, LM_ACT_NONE>(p, tile, partial, rank, tid, kThreads); break;
+        case LM_ACT_RELU: finish_split<T, LM_ACT_RELU>(p, tile, partial, rank, tid, N); break;
+        case LM_ACT_GELU: finish_split<T, LM_ACT_GELU>(p, tile, partial, rank, tid, N); break;
+        case LM_ACT_GELU_TANH: finish_split<T, LM_ACT_GELU_TANH>(p, tile, partial, rank, tid, N); break;
+        case LM_ACT_SILU: finish_split<T, LM_ACT_SILU>(p, tile, partial, rank, tid, N); break;
+        default: finish_split<T, LM_ACT_NONE>(p, tile, partial, rank, tid, N); break;
       }
     }
     cluster_sync_all();  // no CTA leaves while another reads its sums
   }
   tcgen05_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync_all();  // ... or its barriers and tensor memory are in use
   if (warp == 2) {
     tcgen05_fence_after();
-    tmem_dealloc(tmem, static_cast<uint32_t>(p.tmem_cols));
+    tmem_dealloc<PAIR>(tmem, static_cast<uint32_t>(p.tmem_cols));
   }
 }
 
@@ -574,27 +657,29 @@ lm_status make_map(CUtensorMap *map, const Operand &o, int64_t k, int box_rows, 
   return r == CUDA_SUCCESS ? LM_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-template <typename T>
-lm_status launch(const CUtensorMap &lanes, const CUtensorMap &cols, const LinearParams &p, bool swap, int grid,
-                 int smem, cudaStream_t s) {
-  auto *const kernel = !swap ? linear_kernel<T, false, false>
-                             : p.splits > 1 ? linear_kernel<T, true, true> : linear_kernel<T, true, false>;
-  if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  if (p.splits > 1) {
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const LinearParams);
+
+// Pairs of CTAs that the device holds at once (SMs that have no partner in
+// their group stay out), asked once per device.
+int resident_pairs(Kernel kernel, const cudaLaunchConfig_t &cfg, const DeviceInfo &dev) {
+  static std::mutex mu;
+  static std::map<int, int> known;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto it = known.find(dev.device);
+  if (it != known.end()) return it->second;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = dev.sm_count / 2;
   }
-  LM_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, lanes, cols, p));
-  return LM_OK;
+  return known[dev.device] = n < dev.sm_count / 2 ? n : dev.sm_count / 2;
+}
+
+template <typename T>
+Kernel kernel_of(bool swap, Form form) {
+  if (form == Form::kSplit) return linear_kernel<T, true, Form::kSplit>;
+  if (form == Form::kPair) return swap ? linear_kernel<T, true, Form::kPair> : linear_kernel<T, false, Form::kPair>;
+  return swap ? linear_kernel<T, true, Form::kOne> : linear_kernel<T, false, Form::kOne>;
 }
 
 }  // namespace
@@ -656,35 +741,76 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
   p.vec32 = aligned(a.out, 32) && (one_row || a.out_row_stride % (2 * ov) == 0);
   const bool swap = !vec || p.rows <= 256;
   const int64_t lane_rows = swap ? p.n : p.rows, col_rows = swap ? p.rows : p.n;
-  p.lane_tiles = static_cast<int32_t>((lane_rows + kLanes - 1) / kLanes);
+  const int64_t groups = pl.x.groups;
   // Columns in equal tiles of at most 256, a multiple of 16 each.
-  int64_t col_tiles = (col_rows + kMaxBn - 1) / kMaxBn;
-  p.bn = static_cast<int32_t>(((col_rows + col_tiles - 1) / col_tiles + 15) / 16 * 16);
-  if (!swap && static_cast<int64_t>(p.lane_tiles) * col_tiles * pl.x.groups < dev.sm_count && p.bn > 128) {
-    p.bn = 128;
+  auto columns = [&](int most, int unit) {
+    const int64_t n = (col_rows + most - 1) / most;
+    return static_cast<int32_t>(((col_rows + n - 1) / n + unit - 1) / unit * unit);
+  };
+  auto count = [&](int lanes, int bn) {
+    return (lane_rows + lanes - 1) / lanes * ((col_rows + bn - 1) / bn) * groups;
+  };
+  Form form = Form::kOne;
+  p.bn = columns(kMaxBn, 16);
+  const int32_t pair_bn = columns(kMaxBn, 32);
+  if (pair_bn >= 128 && count(2 * kLanes, pair_bn) >= dev.sm_count / 2) {
+    form = Form::kPair;
+    p.bn = pair_bn;
+  } else if (!swap && count(kLanes, p.bn) < dev.sm_count && p.bn > 128) {
+    p.bn = columns(128, 16);
   }
+  p.lane_step = form == Form::kPair ? 2 * kLanes : kLanes;
+  p.lane_tiles = static_cast<int32_t>((lane_rows + p.lane_step - 1) / p.lane_step);
   p.col_tiles = static_cast<int32_t>((col_rows + p.bn - 1) / p.bn);
-  const int64_t tiles = static_cast<int64_t>(p.lane_tiles) * p.col_tiles * pl.x.groups;
+  const int64_t tiles = count(p.lane_step, p.bn);
   if (tiles > INT_MAX / 16) return LM_ERR_UNSUPPORTED;
   p.tiles = static_cast<int32_t>(tiles);
   p.splits = 1;
-  if (swap && p.bn <= 64) {
+  if (swap && form == Form::kOne && p.bn <= 64) {
     while (p.splits < 8 && tiles * p.splits * 2 <= dev.sm_count && p.kblocks >= p.splits * 2) p.splits *= 2;
+    if (p.splits > 1) form = Form::kSplit;
   }
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.bn) p.tmem_cols *= 2;
-  const int stage_bytes = kLanes * 128 + p.bn * 128;
+  const int held_cols = form == Form::kPair ? p.bn / 2 : p.bn;
+  const int stage_bytes = kLanes * 128 + held_cols * 128;
   p.stages = kSmemBudget / stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.idesc = idesc_f16(bf16, static_cast<uint32_t>(p.bn));
-  int smem = 1024 + p.stages * stage_bytes + static_cast<int>(sizeof(Barriers)) + 2 * p.bn * 4;
+  p.idesc = idesc_f16(bf16, static_cast<uint32_t>(p.lane_step), static_cast<uint32_t>(p.bn));
+  const int smem = 1024 + p.stages * stage_bytes + static_cast<int>(sizeof(Barriers)) + 2 * p.bn * 4;
 
   CUtensorMap lanes = {}, cols = {};
   if (p.kblocks > 0) {
     if (lm_status st = make_map(&lanes, swap ? pl.w : pl.x, a.k, kLanes, bf16); st != LM_OK) return st;
-    if (lm_status st = make_map(&cols, swap ? pl.x : pl.w, a.k, p.bn, bf16); st != LM_OK) return st;
+    if (lm_status st = make_map(&cols, swap ? pl.x : pl.w, a.k, held_cols, bf16); st != LM_OK) return st;
   }
-  const int grid = p.splits > 1 ? p.tiles * p.splits : p.tiles < dev.sm_count ? p.tiles : dev.sm_count;
-  return bf16 ? launch<__nv_bfloat16>(lanes, cols, p, swap, grid, smem, s)
-              : launch<__half>(lanes, cols, p, swap, grid, smem, s);
+  const Kernel kernel = bf16 ? kernel_of<__nv_bfloat16>(swap, form) : kernel_of<__half>(swap, form);
+  if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(swap)));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  int cluster = 1, grid = p.tiles < dev.sm_count ? p.tiles : dev.sm_count;
+  if (form == Form::kSplit) {
+    cluster = p.splits;
+    grid = p.tiles * p.splits;
+  } else if (form == Form::kPair) {
+    cluster = 2;
+    grid = 2 * (p.tiles < dev.sm_count / 2 ? p.tiles : dev.sm_count / 2);
+  }
+  if (cluster > 1) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  if (form == Form::kPair) {
+    const int pairs = resident_pairs(kernel, cfg, dev);
+    if (grid > 2 * pairs) cfg.gridDim.x = static_cast<unsigned>(2 * pairs);
+  }
+  LM_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, lanes, cols, p));
+  return LM_OK;
 }

@@ -38,11 +38,17 @@ constexpr int kLanes = 128;         // rows of the tile's lane side
 constexpr int kMaxBn = 256;
 constexpr int kMaxStages = 8;
 
-// Warps: TMA, MMA, TMEM and an idle one, then the epilogue's.  16 of those where
-// a tile is wide and the activation is computed on all of it, 8 else.
-constexpr int epi_warps(bool swap) { return swap ? 8 : 16; }
-constexpr int threads_of(bool swap) { return 128 + 32 * epi_warps(swap); }
-constexpr int kSmemBudget = 227 * 1024 - 1024 - 4096;
+enum class Form {
+  kOne,    // a CTA per tile of 128 lanes
+  kPair,   // two CTAs per tile of 256 lanes
+  kSplit,  // a cluster per tile, each CTA a part of k
+};
+
+// Warps: TMA, MMA, TMEM and an idle one, then the epilogue's: 16, or 8 for the
+// split form's few columns.
+constexpr int epi_warps(Form f) { return f == Form::kSplit ? 8 : 16; }
+constexpr int threads_of(Form f) { return 128 + 32 * epi_warps(f); }
+constexpr int kStageOut = 32 * 32 * 2;  // a warp's 32 rows x 32 columns of 16 bits
 
 struct LinearParams {
   const void *bias, *residual;
@@ -55,6 +61,7 @@ struct LinearParams {
   int32_t lane_step;          // rows along the lanes of a tile: 128, or a pair's 256
   int32_t splits;             // CTAs that share a tile's k
   int32_t bias_f32, out_f32, act, vec32;
+  int32_t tma_out, stage_out; // outputs leave by TMA, through that many bytes of shared memory
   uint32_t idesc;
   float scale;
   uint32_t *err;
@@ -87,26 +94,58 @@ __device__ __forceinline__ float relu(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Two f32 in a 64-bit register: one instruction works on both.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt 2) / 2, with erfc by formula
 // 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions
 // (erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), off by
-// at most 1.5e-7); the coefficients below are halved.  Past |z| = 20 the second
-// term is 0.
-__device__ __forceinline__ float gelu(float z) {
-  const float a = fminf(fabsf(z), 20.0f);
-  const float t = rcp(fmaf(0.3275911f * 0.70710678118654752f, a, 1.0f));
-  float q = fmaf(0.5f * 1.061405429f, t, -0.5f * 1.453152027f);
-  q = fmaf(q, t, 0.5f * 1.421413741f);
-  q = fmaf(q, t, -0.5f * 0.284496736f);
-  q = fmaf(q, t, 0.5f * 0.254829592f);
-  const float e = ex2(a * (a * (-0.5f * kLog2e)));
-  return fmaf(-a * t, q * e, relu(z));
+// at most 1.5e-7); the coefficients below are halved and negated.  Past
+// |z| = 20 the second term is 0.
+__device__ __forceinline__ f32x2 gelu2(f32x2 z) {
+  const float2 zz = unpair(z);
+  const f32x2 a = pair(fminf(fabsf(zz.x), 20.0f), fminf(fabsf(zz.y), 20.0f));
+  const float2 den = unpair(fma2(both(0.3275911f * 0.70710678118654752f), a, both(1.0f)));
+  const f32x2 t = pair(rcp(den.x), rcp(den.y));
+  f32x2 q = fma2(both(-0.5f * 1.061405429f), t, both(0.5f * 1.453152027f));
+  q = fma2(q, t, both(-0.5f * 1.421413741f));
+  q = fma2(q, t, both(0.5f * 0.284496736f));
+  q = fma2(q, t, both(-0.5f * 0.254829592f));
+  const float2 arg = unpair(mul2(a, mul2(a, both(-0.5f * kLog2e))));
+  const f32x2 e = pair(ex2(arg.x), ex2(arg.y));
+  return fma2(mul2(a, t), mul2(q, e), pair(relu(zz.x), relu(zz.y)));
 }
 
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
   if (ACT == LM_ACT_RELU) return relu(z);
-  if (ACT == LM_ACT_GELU) return gelu(z);
+  if (ACT == LM_ACT_GELU) return unpair(gelu2(both(z))).x;
   if (ACT == LM_ACT_GELU_TANH) {
     // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
     const float u = fmaf(-2.0f * 0.79788456080286536f * kLog2e * 0.044715f * z * z, z,
@@ -115,6 +154,14 @@ __device__ __forceinline__ float activate(float z) {
   }
   if (ACT == LM_ACT_SILU) return z * rcp(1.0f + ex2(-kLog2e * z));
   return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ f32x2 activate2(f32x2 z) {
+  if (ACT == LM_ACT_NONE) return z;
+  if (ACT == LM_ACT_GELU) return gelu2(z);
+  const float2 f = unpair(z);
+  return pair(activate<ACT>(f.x), activate<ACT>(f.y));
 }
 
 __device__ __forceinline__ uint4 ldg_v4(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
@@ -167,7 +214,8 @@ __device__ __forceinline__ void put(const LinearParams &p, float acc, float bias
 // The 16 columns in `r` of a lane's tile row.
 template <typename T, int ACT, bool SWAP>
 __device__ __forceinline__ void finish16(const LinearParams &p, const uint32_t (&r)[16], const float *bias_s,
-                                         float lane_bias, int64_t group_row, int lane_at, int col_at) {
+                                         float lane_bias, int64_t group_row, int lane_at, int col_at,
+                                         uint32_t stage, uint32_t stage_at) {
   if (SWAP) {
     if (lane_at >= p.n) return;
 #pragma unroll
@@ -179,13 +227,40 @@ __device__ __forceinline__ void finish16(const LinearParams &p, const uint32_t (
   if (lane_at >= p.rows || col_at >= p.n) return;
   const int64_t row = group_row + lane_at;
   float y[16];
+  const f32x2 scale = both(p.scale);
 #pragma unroll
   for (int j = 0; j < 16; j += 4) {
     const float4 v = *reinterpret_cast<const float4 *>(bias_s + j);
-    y[j] = p.scale * activate<ACT>(__uint_as_float(r[j]) + v.x);
-    y[j + 1] = p.scale * activate<ACT>(__uint_as_float(r[j + 1]) + v.y);
-    y[j + 2] = p.scale * activate<ACT>(__uint_as_float(r[j + 2]) + v.z);
-    y[j + 3] = p.scale * activate<ACT>(__uint_as_float(r[j + 3]) + v.w);
+    const f32x2 z0 = add2(pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), pair(v.x, v.y));
+    const f32x2 z1 = add2(pair(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), pair(v.z, v.w));
+    const float2 y0 = unpair(mul2(scale, activate2<ACT>(z0))), y1 = unpair(mul2(scale, activate2<ACT>(z1)));
+    y[j] = y0.x;
+    y[j + 1] = y0.y;
+    y[j + 2] = y1.x;
+    y[j + 3] = y1.y;
+  }
+  if (p.tma_out) {
+    if (p.residual) {
+      if (col_at + 16 <= p.n) {
+        float x[16];
+        load16(static_cast<const T *>(p.residual) + row * p.res_row + col_at, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] += x[j];
+      } else {
+        for (int j = 0; j < 16 && col_at + j < p.n; ++j)
+          y[j] += to_f32(static_cast<const T *>(p.residual)[row * p.res_row + col_at + j]);
+      }
+    }
+    // Two 16-byte parts of a 64-byte row, in the 64-byte swizzle.
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t off = stage_at + 16 * i, to = stage + (off ^ ((off >> 3) & 0x30u));
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(pack2<T>(y[8 * i], y[8 * i + 1])),
+                   "r"(pack2<T>(y[8 * i + 2], y[8 * i + 3])), "r"(pack2<T>(y[8 * i + 4], y[8 * i + 5])),
+                   "r"(pack2<T>(y[8 * i + 6], y[8 * i + 7]))
+                   : "memory");
+    }
+    return;
   }
   if (col_at + 16 <= p.n) {
     if (p.residual) {
@@ -241,42 +316,68 @@ __device__ __forceinline__ Tile tile_at(const LinearParams &p, int t, int rank) 
 }
 
 // Turns tile `t` into outputs.  `acc` is the tile's tensor memory; warp e of
-// the epilogue reads lanes 32 * (e % 4) .. + 31 and every second (fourth) 16
-// columns.
+// the epilogue reads lanes 32 * (e % 4) .. + 31.  `stage`: the warp's shared
+// memory for outputs that leave by TMA.
 template <typename T, int ACT, bool SWAP>
-__device__ __forceinline__ void epilogue(const LinearParams &p, const Tile &t, uint32_t acc, const float *bias_s, int e) {
-  const int lane = 32 * (e % 4) + static_cast<int>(threadIdx.x % 32);
-  const uint32_t base = acc + (static_cast<uint32_t>(32 * (e % 4)) << 16);
+__device__ __forceinline__ void epilogue(const LinearParams &p, const CUtensorMap *out_map, const Tile &t, uint32_t acc,
+                                         const float *bias_s, int e, uint32_t stage) {
   const int64_t group_row = static_cast<int64_t>(t.group) * p.rows;
-  const int at = t.lane0 + lane;
-  const float lane_bias = SWAP ? bias_at<T>(p, at) : 0.0f;
-  // Columns that exist, 16 at a time; the next 16 are on their way from tensor
-  // memory while these are worked on.
-  constexpr int STEP = epi_warps(SWAP) / 4 * 16;
-  const int cols = min(p.bn, (SWAP ? p.rows : p.n) - t.col0);
-  int c = e / 4 * 16;
-  if (c >= cols) return;
-  uint32_t r[16];
-  tmem_ld16(base + c, r);
-  for (; c < cols; c += STEP) {
-    uint32_t now[16];
-    tmem_wait_ld();
+  const int lane = threadIdx.x % 32;
+  const uint32_t base = acc + (static_cast<uint32_t>(32 * (e % 4)) << 16);
+  const int at = t.lane0 + 32 * (e % 4) + lane;
+  const int end = min(p.bn, (SWAP ? p.rows : p.n) - t.col0);
+  uint32_t r[SWAP ? 1 : 2][16];
+  if constexpr (SWAP) {
+    // Every fourth 16 columns.
+    const float lane_bias = bias_at<T>(p, at);
+    for (int c = e / 4 * 16; c < end; c += 64) {
+      tmem_ld16(base + c, r[0]);
+      tmem_wait_ld();
+      if (p.kblocks == 0) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) now[j] = p.kblocks > 0 ? r[j] : 0u;
-    if (c + STEP < cols) tmem_ld16(base + c + STEP, r);
-    finish16<T, ACT, SWAP>(p, now, bias_s + c, lane_bias, group_row, at, t.col0 + c);
+        for (int j = 0; j < 16; ++j) r[0][j] = 0;
+      }
+      finish16<T, ACT, SWAP>(p, r[0], bias_s, lane_bias, group_row, at, t.col0 + c, 0, 0);
+    }
+  } else {
+    // Every fourth 32 columns.
+    for (int c = e / 4 * 32; c < end; c += 128) {
+      tmem_ld16(base + c, r[0]);
+      tmem_ld16(base + c + 16, r[1]);
+      if (p.tma_out) {  // the last outputs have left the stage
+        if (lane == 0) tma_store_wait_read();
+        __syncwarp();
+      }
+      tmem_wait_ld();
+      if (p.kblocks == 0) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[0][j] = r[1][j] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        finish16<T, ACT, SWAP>(p, r[i], bias_s + c + 16 * i, 0.0f, group_row, at, t.col0 + c + 16 * i, stage,
+                               static_cast<uint32_t>(lane * 64 + i * 32));
+      if (p.tma_out) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && t.lane0 + 32 * (e % 4) < p.rows) {
+          tma_store_3d(out_map, stage, t.col0 + c, t.lane0 + 32 * (e % 4), t.group);
+          tma_store_commit();
+        }
+      }
+    }
   }
 }
 
 template <typename T, bool SWAP>
-__device__ __forceinline__ void epilogue_act(const LinearParams &p, const Tile &t, uint32_t acc, const float *bias_s,
-                                             int e) {
+__device__ __forceinline__ void epilogue_act(const LinearParams &p, const CUtensorMap *out_map, const Tile &t,
+                                             uint32_t acc, const float *bias_s, int e, uint32_t stage) {
   switch (p.act) {
-    case LM_ACT_RELU: epilogue<T, LM_ACT_RELU, SWAP>(p, t, acc, bias_s, e); break;
-    case LM_ACT_GELU: epilogue<T, LM_ACT_GELU, SWAP>(p, t, acc, bias_s, e); break;
-    case LM_ACT_GELU_TANH: epilogue<T, LM_ACT_GELU_TANH, SWAP>(p, t, acc, bias_s, e); break;
-    case LM_ACT_SILU: epilogue<T, LM_ACT_SILU, SWAP>(p, t, acc, bias_s, e); break;
-    default: epilogue<T, LM_ACT_NONE, SWAP>(p, t, acc, bias_s, e); break;
+    case LM_ACT_RELU: epilogue<T, LM_ACT_RELU, SWAP>(p, out_map, t, acc, bias_s, e, stage); break;
+    case LM_ACT_GELU: epilogue<T, LM_ACT_GELU, SWAP>(p, out_map, t, acc, bias_s, e, stage); break;
+    case LM_ACT_GELU_TANH: epilogue<T, LM_ACT_GELU_TANH, SWAP>(p, out_map, t, acc, bias_s, e, stage); break;
+    case LM_ACT_SILU: epilogue<T, LM_ACT_SILU, SWAP>(p, out_map, t, acc, bias_s, e, stage); break;
+    default: epilogue<T, LM_ACT_NONE, SWAP>(p, out_map, t, acc, bias_s, e, stage); break;
   }
 }
 
@@ -312,24 +413,17 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
   return r != 0;
 }
 
-enum class Form {
-  kOne,    // a CTA per tile of 128 lanes
-  kPair,   // two CTAs per tile of 256 lanes
-  kSplit,  // a cluster per tile, each CTA a part of k
-};
-
 template <typename T, bool SWAP, Form FORM>
-__global__ void __launch_bounds__(threads_of(SWAP), 1)
+__global__ void __launch_bounds__(threads_of(FORM), 1)
     linear_kernel(const __grid_constant__ CUtensorMap lane_map, const __grid_constant__ CUtensorMap col_map,
-                  const LinearParams p) {
+                  const __grid_constant__ CUtensorMap out_map, const LinearParams p) {
   constexpr bool PAIR = FORM == Form::kPair, SPLIT = FORM == Form::kSplit;
-  constexpr int EPI = epi_warps(SWAP);
-  extern __shared__ uint8_t smem_raw[];
-  // Stages start on a 1024-byte boundary (the swizzle's period).
-  uint8_t *const ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  constexpr int EPI = epi_warps(FORM);
+  extern __shared__ __align__(1024) uint8_t ring[];  // stages on a boundary of the swizzle's period
   const int col_rows = PAIR ? p.bn / 2 : p.bn;  // rows of the column side that this CTA holds
   const int stage_bytes = kLanes * 128 + col_rows * 128;
-  Barriers &b = *reinterpret_cast<Barriers *>(ring + p.stages * stage_bytes);
+  uint8_t *const stage_s = ring + p.stages * stage_bytes;  // outputs on their way
+  Barriers &b = *reinterpret_cast<Barriers *>(stage_s + p.stage_out);
   float *const bias_s = reinterpret_cast<float *>(&b + 1);  // two tiles of bn
   // (The shuffle tells the compiler that the warp number is uniform.)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
@@ -450,6 +544,9 @@ __global__ void __launch_bounds__(threads_of(SWAP), 1)
     const int e = warp - 4;
     const int et = threadIdx.x - 128;
     int tiles = 0;
+    // A thread's column of the bias, fetched a tile ahead (bn <= threads).
+    float next_bias = 0.0f;
+    if (!SWAP && et < p.bn && first < p.tiles) next_bias = bias_at<T>(p, tile_at(p, first, lane_rank).col0 + et);
     for (int t = first; t < p.tiles; t += step, ++tiles) {
       const Tile tile = tile_at(p, t, lane_rank);
       const int half = tiles & 1;
@@ -457,7 +554,10 @@ __global__ void __launch_bounds__(threads_of(SWAP), 1)
       if (!SWAP) {
         // Every epilogue warp has left the tile that used this half before:
         // the barrier of the tile in between lies behind it.
-        for (int i = et; i < p.bn; i += 32 * EPI) bs[i] = bias_at<T>(p, tile.col0 + i);
+        if (et < p.bn) {
+          bs[et] = next_bias;
+          if (t + step < p.tiles) next_bias = bias_at<T>(p, tile_at(p, t + step, lane_rank).col0 + et);
+        }
       }
       bool ok = mbar_wait(&b.acc_full[half], (tiles >> 1) & 1, abort, p.err);
       // One decision for all warps that meet at the barrier, and per warp
@@ -478,7 +578,7 @@ __global__ void __launch_bounds__(threads_of(SWAP), 1)
           for (int j = 0; j < 16; ++j) partial[(c + j) * kLanes + lane] = __uint_as_float(r[j]);
         }
       } else {
-        epilogue_act<T, SWAP>(p, tile, acc, bs, e);
+        epilogue_act<T, SWAP>(p, &out_map, tile, acc, bs, e, smem_u32(stage_s) + e * kStageOut);
         tcgen05_fence_before();
         __syncwarp();
         if (threadIdx.x % 32 == 0) {
@@ -492,6 +592,7 @@ __global__ void __launch_bounds__(threads_of(SWAP), 1)
     }
   }
 
+  if (warp >= 4 && threadIdx.x % 32 == 0) tma_store_wait_read();
   __syncwarp();
   if (SPLIT) {
     __syncthreads();
@@ -500,7 +601,7 @@ __global__ void __launch_bounds__(threads_of(SWAP), 1)
       const Tile tile = tile_at(p, first, 0);
       const uint32_t partial = smem_u32(ring);
       const int tid = threadIdx.x;
-      constexpr int N = threads_of(SWAP);
+      constexpr int N = threads_of(FORM);
       switch (p.act) {
         case LM_ACT_RELU: finish_split<T, LM_ACT_RELU>(p, tile, partial, rank, tid, N); break;
         case LM_ACT_GELU: finish_split<T, LM_ACT_GELU>(p, tile, partial, rank, tid, N); break;
@@ -638,26 +739,28 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Tiles of `box_rows` rows x 64 elements of k, zeros outside.
-lm_status make_map(CUtensorMap *map, const Operand &o, int64_t k, int box_rows, bool bf16) {
+// Boxes of `box_rows` rows x `box_k` (64 or 32) elements in a swizzle of as
+// many bytes, zeros outside.
+lm_status make_map(CUtensorMap *map, const Operand &o, int64_t k, int box_rows, bool bf16, int box_k = kBk) {
   const EncodeFn fn = encode_fn();
   if (!fn) return cuda_fail(cudaErrorNotSupported);
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(o.rows),
                               static_cast<cuuint64_t>(o.groups)};
   // A stride that is not used still has to be a valid one.
   const int64_t pad = (k + 7) / 8 * 8;
+  // (A row that is alone may have any stride.)
   const int64_t rs = o.rows > 1 ? o.row_stride : pad;
   const int64_t gs = o.groups > 1 ? o.group_stride : pad;
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(rs) * 2, static_cast<cuuint64_t>(gs) * 2};
-  const cuuint32_t box[3] = {kBk, static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_k), static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
   const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                         const_cast<void *>(o.p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        box_k == kBk ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? LM_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const LinearParams);
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const LinearParams);
 
 // Pairs of CTAs that the device holds at once (SMs that have no partner in
 // their group stay out), asked once per device.
@@ -739,7 +842,9 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
   const bool vec = aligned(a.out, 16) && (one_row || a.out_row_stride % ov == 0) &&
                    (!a.residual || (aligned(a.residual, 16) && (one_row || a.residual_row_stride % 8 == 0)));
   p.vec32 = aligned(a.out, 32) && (one_row || a.out_row_stride % (2 * ov) == 0);
-  const bool swap = !vec || p.rows <= 256;
+  // Up to 512 rows, tiles that hold exactly the rows there are beat 128 or 256
+  // lanes of them (320 x 1024 onto 50048: 38 us against 42).
+  const bool swap = !vec || p.rows <= 512;
   const int64_t lane_rows = swap ? p.n : p.rows, col_rows = swap ? p.rows : p.n;
   const int64_t groups = pl.x.groups;
   // Columns in equal tiles of at most 256, a multiple of 16 each.
@@ -751,13 +856,16 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
     return (lane_rows + lanes - 1) / lanes * ((col_rows + bn - 1) / bn) * groups;
   };
   Form form = Form::kOne;
-  p.bn = columns(kMaxBn, 16);
+  const int unit = swap ? 16 : 32;
+  p.bn = columns(kMaxBn, unit);
   const int32_t pair_bn = columns(kMaxBn, 32);
-  if (pair_bn >= 128 && count(2 * kLanes, pair_bn) >= dev.sm_count / 2) {
+  // Pairs fetch a third less per product; their tiles are longer to fill and
+  // to empty, which shows where k is short (k = 240: 20.5 us against 18.5).
+  if (pair_bn >= 128 && p.kblocks >= 8 && count(2 * kLanes, pair_bn) >= dev.sm_count / 2) {
     form = Form::kPair;
     p.bn = pair_bn;
   } else if (!swap && count(kLanes, p.bn) < dev.sm_count && p.bn > 128) {
-    p.bn = columns(128, 16);
+    p.bn = columns(128, unit);
   }
   p.lane_step = form == Form::kPair ? 2 * kLanes : kLanes;
   p.lane_tiles = static_cast<int32_t>((lane_rows + p.lane_step - 1) / p.lane_step);
@@ -774,20 +882,27 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
   while (p.tmem_cols < 2 * p.bn) p.tmem_cols *= 2;
   const int held_cols = form == Form::kPair ? p.bn / 2 : p.bn;
   const int stage_bytes = kLanes * 128 + held_cols * 128;
-  p.stages = kSmemBudget / stage_bytes;
+  p.tma_out = !swap && !p.out_f32;
+  p.stage_out = p.tma_out ? epi_warps(form) * kStageOut : 0;
+  const int rest = p.stage_out + static_cast<int>(sizeof(Barriers)) + 2 * p.bn * 4;
+  p.stages = (227 * 1024 - rest) / stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.idesc = idesc_f16(bf16, static_cast<uint32_t>(p.lane_step), static_cast<uint32_t>(p.bn));
-  const int smem = 1024 + p.stages * stage_bytes + static_cast<int>(sizeof(Barriers)) + 2 * p.bn * 4;
+  const int smem = p.stages * stage_bytes + rest;
 
-  CUtensorMap lanes = {}, cols = {};
+  CUtensorMap lanes = {}, cols = {}, outs = {};
   if (p.kblocks > 0) {
     if (lm_status st = make_map(&lanes, swap ? pl.w : pl.x, a.k, kLanes, bf16); st != LM_OK) return st;
     if (lm_status st = make_map(&cols, swap ? pl.x : pl.w, a.k, held_cols, bf16); st != LM_OK) return st;
   }
+  if (p.tma_out) {
+    const Operand o{a.out, groups, p.rows, static_cast<int64_t>(p.rows) * a.out_row_stride, a.out_row_stride, false, 0};
+    if (lm_status st = make_map(&outs, o, a.n, 32, bf16, 32); st != LM_OK) return st;
+  }
   const Kernel kernel = bf16 ? kernel_of<__nv_bfloat16>(swap, form) : kernel_of<__half>(swap, form);
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(swap)));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(form)));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -811,6 +926,6 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
     const int pairs = resident_pairs(kernel, cfg, dev);
     if (grid > 2 * pairs) cfg.gridDim.x = static_cast<unsigned>(2 * pairs);
   }
-  LM_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, lanes, cols, p));
+  LM_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, lanes, cols, outs, p));
   return LM_OK;
 }

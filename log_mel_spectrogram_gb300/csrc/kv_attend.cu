@@ -26,6 +26,7 @@
 // Long rows are split over CTAs; the last one to finish a row and head joins
 // the parts in order.
 #include <climits>
+#include <type_traits>
 
 #include "half.cuh"
 #include "internal.h"
@@ -45,12 +46,13 @@ constexpr int kMinChunk = 512;        // tokens below which a row is not split
 // largest one in 32-bit floats, for scales of up to 2^13.
 constexpr float kMinScale = 8.0779357e-28f;
 
-// Bytes of one warp's stage (keys and values of kTok tokens), ring depth and
-// the CTAs that a full device holds: 64 KB of ring or less per CTA for
-// head_dim 32 and 64, 96 KB for 128.
+// Bytes of a stage (keys and values of kTok tokens), ring depth, and the CTAs
+// that an SM holds: shared memory (a ring per warp) and registers allow 4, 4
+// and 3 of head_dim 32, 64 and 128.
 constexpr int stage_bytes(int d) { return 2 * kTok * d; }
-constexpr int ring_stages(int d) { return d == 128 ? 3 : d == 64 ? 4 : 6; }
-constexpr int full_ctas(int d) { return 152 * (d == 128 ? 2 : 3); }
+constexpr int ring_stages(int d, bool shared) { return shared ? 4 : d == 128 ? 2 : d == 64 ? 3 : 6; }
+constexpr int resident_ctas(int d) { return d == 128 ? 3 : 4; }
+constexpr int full_ctas(int d) { return 152 * resident_ctas(d); }
 
 struct AttendParams {
   KvView c;
@@ -68,14 +70,14 @@ struct AttendParams {
 // Shared memory: the rings (at the end the warps' partial results), then this.
 template <int R>
 struct Shared {
-  uint64_t full[kWarps][8];
+  uint64_t full[kWarps][8], empty[8];
   float2 ml[kWarps][R];  // maximum and sum per warp and query row
   int abort;
   int last;
 };
 
-constexpr int big_bytes(int d, int mt) {
-  const int ring = kWarps * ring_stages(d) * stage_bytes(d), joined = kWarps * 16 * mt * d * 4;
+constexpr int big_bytes(int d, int mt, bool shared) {
+  const int ring = (shared ? 1 : kWarps) * ring_stages(d, shared) * stage_bytes(d), joined = kWarps * 16 * mt * d * 4;
   return ring > joined ? ring : joined;
 }
 
@@ -122,14 +124,17 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
   }
 }
 
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) {
-  constexpr int STAGES = ring_stages(D);
+// SHARED: the warps have 16 query rows each and go over the same tokens, in one
+// ring, instead of sharing out the tokens of 16 * MT rows.
+template <typename T, int D, int MT, bool SHARED>
+__global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) attend_kernel(const AttendParams p) {
+  constexpr int STAGES = ring_stages(D, SHARED);
   constexpr int KW = D / 16;   // 32-bit words of a token's key per thread; also 16-element steps of k
   constexpr int VB = D / 8;    // bytes of a token's value per thread; also 8-column tiles of the output
-  constexpr int R = 16 * MT;
+  constexpr int R = 16 * MT;            // query rows of a warp
+  constexpr int QT = SHARED ? kWarps * R : R;  // ... and of the CTA
   extern __shared__ __align__(128) uint8_t smem[];
-  Shared<R> &sh = *reinterpret_cast<Shared<R> *>(smem + big_bytes(D, MT));
+  Shared<R> &sh = *reinterpret_cast<Shared<R> *>(smem + big_bytes(D, MT, SHARED));
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r8 = lane / 4, c4 = lane % 4;
   int u = blockIdx.x;
@@ -147,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
   int fresh = max(p.counts ? p.counts[row] : p.new_tokens, 0);
   if (p.causal) fresh = min(fresh, p.tokens);
   const int total = static_cast<int>(min(static_cast<int64_t>(held) + fresh, static_cast<int64_t>(cap)));
-  const int q_first = qt * R, q_rows = min(R, p.qrows - q_first);
+  const int q_first = qt * QT, q_rows = min(QT, p.qrows - q_first);
   int end = total;
   if (p.causal) {
     const int i_first = q_first / p.group, i_last = min((q_first + q_rows - 1) / p.group, fresh - 1);
@@ -161,20 +166,25 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
   const int begin = split * chunk, stop = min(end, begin + chunk);
 
   if (threadIdx.x < kWarps)
-    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[threadIdx.x][i], 1);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&sh.full[threadIdx.x][i], 1);
+      if (threadIdx.x == 0) mbar_init(&sh.empty[i], kWarps);
+    }
   if (threadIdx.x == 0) sh.abort = 0;
   fence_mbar_init();
   __syncthreads();
 
-  uint8_t *const ring = smem + warp * STAGES * stage_bytes(D);
+  uint8_t *const ring = smem + (SHARED ? 0 : warp * STAGES * stage_bytes(D));
   const uint32_t ring_a = smem_u32(ring);
-  uint64_t *const full = sh.full[warp];
+  uint64_t *const full = sh.full[SHARED ? 0 : warp];
   const int block_shift = 31 - __clz(p.c.block);
   const int32_t *const table = p.c.table + static_cast<int64_t>(row) * p.c.width;
   const int64_t tiles0 = p.c.layer_tiles + h;
-  // This warp's tiles: number j starts at token begin + (j * kWarps + warp) * kTok.
-  const int mine = max((stop - begin - warp * kTok + kWarps * kTok - 1) / (kWarps * kTok), 0);
-  auto token_of = [&](int j) { return begin + (j * kWarps + warp) * kTok; };
+  // This warp's tiles: number j starts at token begin + (j * kWarps + warp) * kTok
+  // (SHARED: begin + j * kTok).
+  const int mine = SHARED ? (stop - begin + kTok - 1) / kTok
+                          : max((stop - begin - warp * kTok + kWarps * kTok - 1) / (kWarps * kTok), 0);
+  auto token_of = [&](int j) { return begin + (SHARED ? j : j * kWarps + warp) * kTok; };
   // The block of a tile's half (16 tokens), or -1.
   auto block_of = [&](int j, int half) {
     const int t = token_of(j) + 16 * half;
@@ -213,18 +223,25 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
       }
     }
   };
+  const bool fetches = !SHARED || warp == 0;
   int fetched = 0;
-  for (; fetched < min(mine, STAGES); ++fetched) fetch(fetched);
+  if (fetches)
+    for (; fetched < min(mine, STAGES); ++fetched) fetch(fetched);
 
   // Queries, k permuted: step s of the product over k takes elements
-  // c4 * D/4 + 4s .. + 3 of the head from this thread.
+  // c4 * D/4 + 4s .. + 3 of the head from this thread.  bf16 queries become f16
+  // times a power of two that puts the row's largest between 2^14 and 2^15:
+  // exact but for values below 2^-28 of that one, which are off by 2^-39 of
+  // it.  (Bytes turn into f16 in two instructions, into bf16 in three.)
   uint32_t q[MT][KW][4];
   int limit[MT][2];
+  float back[MT][2];  // the power's inverse, times scale and log2 e
+  const float log2e = 1.4426950408889634f;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int at = q_first + 16 * m + 8 * e + r8;
+      const int at = q_first + (SHARED ? warp * R : 0) + 16 * m + 8 * e + r8;
       const bool in = at < p.qrows;
       const int i = in ? at / p.group : 0, g = in ? at % p.group : 0;
       limit[m][e] = !in ? INT_MAX : !p.causal ? total : i < fresh ? min(total, held + i + 1) : 0;
@@ -249,6 +266,23 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
         for (int j = 0; j < 2 * KW; ++j)
           w[j] = s16[2 * j] | static_cast<uint32_t>(s16[2 * j + 1]) << 16;
       }
+      back[m][e] = p.scale * log2e;
+      if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+        uint32_t top = 0;  // |q| as integers
+#pragma unroll
+        for (int j = 0; j < 2 * KW; ++j) top = max(top, max(w[j] << 16 & 0x7fffffffu, w[j] & 0x7fff0000u));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        uint32_t ex = max(top >> 23, 15u);
+        if (ex == 255) ex = 141;  // infinity or NaN: as it is
+        const float up = __uint_as_float((268 - ex) << 23);
+        back[m][e] *= __uint_as_float((ex - 14) << 23);
+#pragma unroll
+        for (int j = 0; j < 2 * KW; ++j) {
+          const float2 f = unpack2<T>(w[j]);
+          w[j] = pack2<__half>(f.x * up, f.y * up);
+        }
+      }
 #pragma unroll
       for (int s = 0; s < KW; ++s) {
         q[m][s][e] = w[2 * s];
@@ -267,10 +301,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
     sum[m][0] = sum[m][1] = 0.0f;
   }
 
-  // Of the 32 tiles that are consumed next, one per lane and half: the score
-  // factor, log2 and inverse of the value scale; absent blocks are masked.
+  // Of the 32 tiles that are consumed next, one per lane and half: the key
+  // scale, log2 and inverse of the value scale; absent blocks are masked.
   float f_s[2] = {0, 0}, l_s[2] = {0, 0}, i_s[2] = {0, 0};
-  const float log2e = 1.4426950408889634f;
   int done = 0;
   for (; done < mine; ++done) {
     const int j = done;
@@ -282,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
         if (b >= 0) {
           const int64_t tile = tiles0 + static_cast<int64_t>(b) * p.c.heads;
           const float vs = fmaxf(__ldg(p.c.v_scale + tile), kMinScale);
-          f_s[e] = __ldg(p.c.k_scale + tile) * p.scale * log2e;
+          f_s[e] = __ldg(p.c.k_scale + tile);
           l_s[e] = log2f(vs);
           i_s[e] = 1.0f / vs;
         } else {
@@ -306,9 +339,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
       for (int m = 0; m < MT; ++m) sc[m][n8][0] = sc[m][n8][1] = sc[m][n8][2] = sc[m][n8][3] = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < KW; ++ks) {
-        const uint32_t b0 = bytes_to<T>(__byte_perm(w[ks], 0, 0x4140)), b1 = bytes_to<T>(__byte_perm(w[ks], 0, 0x4342));
+        const uint32_t b0 = bytes_to_f16(__byte_perm(w[ks], 0, 0x4140)), b1 = bytes_to_f16(__byte_perm(w[ks], 0, 0x4342));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) mma16816<T>(sc[m][n8], q[m][ks], b0, b1);
+        for (int m = 0; m < MT; ++m) mma16816(sc[m][n8], q[m][ks], b0, b1);
       }
     }
     const float f0 = __shfl_sync(0xffffffffu, f_s[0], j % 32), f1 = __shfl_sync(0xffffffffu, f_s[1], j % 32);
@@ -317,10 +350,12 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
     const bool partial = i0 < 0.0f || i1 < 0.0f;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+      const float g0[2] = {f0 * back[m][0], f0 * back[m][1]}, g1[2] = {f1 * back[m][0], f1 * back[m][1]};
 #pragma unroll
       for (int n8 = 0; n8 < 4; ++n8) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sc[m][n8][x] = fmaf(sc[m][n8][x], n8 < 2 ? f0 : f1, n8 < 2 ? l0 : l1);
+        for (int x = 0; x < 4; ++x)
+          sc[m][n8][x] = fmaf(sc[m][n8][x], n8 < 2 ? g0[x >> 1] : g1[x >> 1], n8 < 2 ? l0 : l1);
       }
       // Tokens past a row's end, and absent ones.  (Selected, not added: their
       // bytes and scales may be anything.)
@@ -336,22 +371,32 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
           }
         }
       }
+      float next[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float t = top[m][e];
 #pragma unroll
         for (int n8 = 0; n8 < 4; ++n8) t = fmaxf(t, fmaxf(sc[m][n8][2 * e], sc[m][n8][2 * e + 1]));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-        const float zero = t == -INFINITY ? 0.0f : t;
-        const float shrink = ex2(top[m][e] - zero);
-        top[m][e] = t;
-        sum[m][e] *= shrink;
+        next[e] = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      }
+      // Maxima rise ever more rarely along a row.
+      if (__any_sync(0xffffffffu, next[0] > top[m][0] || next[1] > top[m][1])) {
 #pragma unroll
-        for (int n = 0; n < VB; ++n) {
-          acc[m][n][2 * e] *= shrink;
-          acc[m][n][2 * e + 1] *= shrink;
+        for (int e = 0; e < 2; ++e) {
+          const float shrink = ex2(top[m][e] - (next[e] == -INFINITY ? 0.0f : next[e]));
+          top[m][e] = next[e];
+          sum[m][e] *= shrink;
+#pragma unroll
+          for (int n = 0; n < VB; ++n) {
+            acc[m][n][2 * e] *= shrink;
+            acc[m][n][2 * e + 1] *= shrink;
+          }
         }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float zero = top[m][e] == -INFINITY ? 0.0f : top[m][e];
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int n8 = 0; n8 < 4; ++n8) {
@@ -392,13 +437,24 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
         // The selectors above put byte n at positions 0 (first token) and 2 (second).
         const uint32_t b0 = bytes_to_f16(lo), b1 = bytes_to_f16(hi);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) mma16816<__half>(acc[m][n], a[m], b0, b1);
+        for (int m = 0; m < MT; ++m) mma16816(acc[m][n], a[m], b0, b1);
       }
     }
     __syncwarp();
-    if (fetched < mine) fetch(fetched++);
+    if (!SHARED) {
+      if (fetched < mine) fetch(fetched++);
+    } else {
+      if (lane == 0) mbar_arrive(&sh.empty[s]);
+      // The stage of the tile before, which the other warps have most likely
+      // left by now.
+      if (warp == 0 && j > 0 && fetched < mine) {
+        const int was = (j - 1) % STAGES;
+        if (!mbar_wait(&sh.empty[was], ((j - 1) / STAGES) & 1, &sh.abort, p.err)) break;
+        fetch(fetched++);
+      }
+    }
   }
-  if (done < mine && lane == 0) {  // gave up: the copies in flight still have to land
+  if (fetches && done < mine && lane == 0) {  // gave up: the copies in flight still have to land
     for (int f = done; f < fetched; ++f) mbar_wait_drain(&full[f % STAGES], (f / STAGES) & 1, p.err);
   }
   __syncthreads();
@@ -415,7 +471,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       if (c4 == 0) sh.ml[warp][rr] = make_float2(top[m][e], s);
-      if (rr < q_rows) {
+      if ((SHARED ? warp * R : 0) + rr < q_rows) {
         float *const o = acc_s + (warp * R + rr) * D + c4 * (D / 4);
 #pragma unroll
         for (int n = 0; n < VB; ++n) {
@@ -438,14 +494,16 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) 
   for (int x = threadIdx.x; x < q_rows * PER; x += kThreads) {
     const int rr = x / PER, d = x % PER * 4;
     float t = -INFINITY;
+    const float2 *const ml_s = &sh.ml[0][0];  // SHARED: row rr is in place rr; else in warp w's place rr
+    constexpr int FROM = SHARED ? 1 : kWarps;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) t = fmaxf(t, sh.ml[w][rr].x);
+    for (int w = 0; w < FROM; ++w) t = fmaxf(t, ml_s[w * R + rr].x);
     const float zero = t == -INFINITY ? 0.0f : t;
     float4 v = make_float4(0, 0, 0, 0);
     float l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = sh.ml[w][rr];
+    for (int w = 0; w < FROM; ++w) {
+      const float2 ml = ml_s[w * R + rr];
       const float f = ex2(ml.x - zero);
       const float4 a = *reinterpret_cast<const float4 *>(acc_s + (w * R + rr) * D + d);
       v.x = fmaf(a.x, f, v.x);
@@ -505,6 +563,7 @@ lm_status check(const lm_kv_cache *cache, int32_t tokens, int32_t q_heads) {
 // How a call is cut: query rows per tile, tiles, units (row, key head, tile)
 // and parts of the tokens.
 struct Cut {
+  bool shared;
   int mt, qrows, qtiles, splits, part_rows;
   int64_t units;
   size_t done_bytes, ml_bytes, acc_bytes;
@@ -513,42 +572,53 @@ struct Cut {
 Cut cut(const lm_kv_cache *c, int32_t tokens, int32_t q_heads) {
   Cut k;
   k.qrows = tokens * (q_heads / c->heads);
-  k.mt = k.qrows <= 16 ? 1 : 2;
-  k.qtiles = (k.qrows + 16 * k.mt - 1) / (16 * k.mt);
-  k.part_rows = k.qrows < 16 * k.mt ? k.qrows : 16 * k.mt;
+  k.shared = k.qrows > 32;
+  k.mt = k.qrows > 16 && !k.shared ? 2 : 1;
+  const int tile = k.shared ? 16 * kWarps : 16 * k.mt;
+  k.qtiles = (k.qrows + tile - 1) / tile;
+  k.part_rows = k.qrows < tile ? k.qrows : tile;
   k.units = static_cast<int64_t>(c->rows) * c->heads * k.qtiles;
-  // As many parts as fill the device once, none below kMinChunk tokens.
+  // As many parts as fill the device once.  Where the units alone come near
+  // that, parts are for balance between rows of unequal length: four rounds of
+  // them.  None below kMinChunk tokens.
   const int64_t cap = static_cast<int64_t>(c->width) * c->block;
-  int64_t s = k.units > 0 ? full_ctas(c->head_dim) / k.units : 1;
+  const int64_t slots = full_ctas(c->head_dim);
+  int64_t s = k.units == 0 ? 1 : 2 * k.units > slots ? (4 * slots + k.units - 1) / k.units : slots / k.units;
   const int64_t most = (cap + kMinChunk - 1) / kMinChunk;
   if (s > most) s = most;
   k.splits = static_cast<int>(s < 1 ? 1 : s);
   const int64_t parts = k.splits > 1 ? k.units * k.splits * k.part_rows : 0;
   // One place for the counters whatever the shape: calls of other shapes
-  // that share the workspace must not write over them.  Split units are at
-  // most half of full_ctas().
-  k.done_bytes = (full_ctas(32) / 2 * 4 + 255) / 256 * 256;
+  // that share the workspace must not write over them.  Units that are split
+  // are fewer than 4 * full_ctas().
+  k.done_bytes = (4 * full_ctas(32) * 4 + 255) / 256 * 256;
   k.ml_bytes = (static_cast<size_t>(parts) * 8 + 255) / 256 * 256;
   k.acc_bytes = static_cast<size_t>(parts) * c->head_dim * 4;
   return k;
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int MT, bool SHARED>
 lm_status launch(const AttendParams &p, int64_t ctas, cudaStream_t s) {
-  auto *const kernel = attend_kernel<T, D, MT>;
-  constexpr int smem = big_bytes(D, MT) + static_cast<int>(sizeof(Shared<16 * MT>));
+  auto *const kernel = attend_kernel<T, D, MT, SHARED>;
+  constexpr int smem = big_bytes(D, MT, SHARED) + static_cast<int>(sizeof(Shared<16 * MT>));
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
   kernel<<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(p);
   LM_CUDA_TRY(cudaGetLastError());
   return LM_OK;
 }
 
+template <typename T, int D>
+lm_status launch_form(const AttendParams &p, const Cut &k, int64_t ctas, cudaStream_t s) {
+  if (k.shared) return launch<T, D, 1, true>(p, ctas, s);
+  return k.mt == 1 ? launch<T, D, 1, false>(p, ctas, s) : launch<T, D, 2, false>(p, ctas, s);
+}
+
 template <typename T>
-lm_status launch_dim(const AttendParams &p, int mt, int64_t ctas, cudaStream_t s) {
+lm_status launch_dim(const AttendParams &p, const Cut &k, int64_t ctas, cudaStream_t s) {
   switch (p.c.head_dim) {
-    case 32: return mt == 1 ? launch<T, 32, 1>(p, ctas, s) : launch<T, 32, 2>(p, ctas, s);
-    case 64: return mt == 1 ? launch<T, 64, 1>(p, ctas, s) : launch<T, 64, 2>(p, ctas, s);
-    default: return mt == 1 ? launch<T, 128, 1>(p, ctas, s) : launch<T, 128, 2>(p, ctas, s);
+    case 32: return launch_form<T, 32>(p, k, ctas, s);
+    case 64: return launch_form<T, 64>(p, k, ctas, s);
+    default: return launch_form<T, 128>(p, k, ctas, s);
   }
 }
 
@@ -606,5 +676,5 @@ extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const
   p.qvec = aligned(q, 16) && q_strides[0] % 8 == 0 && q_strides[1] % 8 == 0 && q_strides[2] % 8 == 0;
   p.scale = scale;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return dtype == LM_F16 ? launch_dim<__half>(p, k.mt, ctas, s) : launch_dim<__nv_bfloat16>(p, k.mt, ctas, s);
+  return dtype == LM_F16 ? launch_dim<__half>(p, k, ctas, s) : launch_dim<__nv_bfloat16>(p, k, ctas, s);
 }

@@ -1,5 +1,5 @@
-// mma.cuh -- warp-level matrix products (m16n8k16, f32 sums) and the exact
-// conversion of signed bytes to 16-bit floats.
+// mma.cuh -- warp-level matrix products (m16n8k16, f16 operands, f32 sums) and
+// the exact conversion of signed bytes to f16.
 //
 // Fragments, with r = lane / 4 and c = lane % 4:
 //   A (16 x 16, rows x k): a[0] = (r; 2c, 2c+1), a[1] = (r+8; 2c, 2c+1),
@@ -9,16 +9,11 @@
 #pragma once
 
 #include <cstdint>
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 namespace lm {
 
-template <typename T>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
-
-template <>
-__device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
@@ -26,43 +21,13 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Bytes b0, b1 of `u` = 0x00 b1 00 b0 as two 16-bit floats.
-//  f16: with the sign bit flipped a byte is b + 128, and 0x6400 | that is
-//  1024 + 128 + b; subtracting 1152 is exact.
+// The bytes in the lower byte of each half of `u` as two f16: with the sign bit
+// flipped a byte is b + 128, and 0x6400 | that is 1024 + 128 + b; subtracting
+// 1152 is exact.
 __device__ __forceinline__ uint32_t bytes_to_f16(uint32_t u) {
   const uint32_t x = (u & 0x00ff00ffu) ^ 0x64806480u;
   const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x), __floats2half2_rn(1152.0f, 1152.0f));
   return *reinterpret_cast<const uint32_t *>(&d);
-}
-
-//  bf16 (8 significant bits): 0x4300 | the low seven bits is 128 + those; a
-//  negative byte is 128 less, and 0x4380 is 256.
-__device__ __forceinline__ uint32_t bytes_to_bf16(uint32_t u) {
-  const uint32_t x = (u & 0x007f007fu) | 0x43004300u, y = (u & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 d =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&y));
-  return *reinterpret_cast<const uint32_t *>(&d);
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t bytes_to(uint32_t u);
-template <>
-__device__ __forceinline__ uint32_t bytes_to<__half>(uint32_t u) {
-  return bytes_to_f16(u);
-}
-template <>
-__device__ __forceinline__ uint32_t bytes_to<__nv_bfloat16>(uint32_t u) {
-  return bytes_to_bf16(u);
 }
 
 }  // namespace lm

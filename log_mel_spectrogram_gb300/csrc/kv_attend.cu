@@ -41,6 +41,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = 32;              // tokens of a warp's tile
 constexpr int kMinChunk = 512;        // tokens below which a row is not split
+constexpr int kBalance = 2048;        // ... where parts are for balance only (512: 44 us, 1024: 39, none: 36 for
+                                      // 1024 units of up to 1500 tokens)
 // Value scales count as at least 2^-90 (values of at most 1e-25, which are off
 // by as much): a weight divided by its scale then still has 23 bits below the
 // largest one in 32-bit floats, for scales of up to 2^13.
@@ -63,7 +65,7 @@ struct AttendParams {
   uint32_t *err, *done;          // done: per unit, parts that are ready
   float2 *part_ml;               // [unit][split][rows]: maximum, sum
   float *part_acc;               // [unit][split][rows][head_dim]
-  int32_t tokens, q_heads, new_tokens, causal, group, qrows, qtiles, splits, part_rows, qvec;
+  int32_t tokens, q_heads, new_tokens, causal, group, qrows, qtiles, splits, part_rows, min_chunk, qvec;
   float scale;
 };
 
@@ -125,8 +127,10 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
 }
 
 // SHARED: the warps have 16 query rows each and go over the same tokens, in one
-// ring, instead of sharing out the tokens of 16 * MT rows.
-template <typename T, int D, int MT, bool SHARED>
+// ring, instead of sharing out the tokens of 16 * MT rows.  E = 1: at most
+// eight query rows, so that the lower half of a product's rows is left out of
+// the softmax (55 of 400 instructions a tile).
+template <typename T, int D, int MT, int E, bool SHARED>
 __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) attend_kernel(const AttendParams p) {
   constexpr int STAGES = ring_stages(D, SHARED);
   constexpr int KW = D / 16;   // 32-bit words of a token's key per thread; also 16-element steps of k
@@ -141,10 +145,11 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
   const int split = u % p.splits;
   u /= p.splits;
   const int unit = u;
-  const int qt = u % p.qtiles;
-  u /= p.qtiles;
+  // Later queries see more: their tiles go first.
   const int h = u % p.c.heads;
-  const int row = u / p.c.heads;
+  u /= p.c.heads;
+  const int row = u % p.c.rows;
+  const int qt = p.qtiles - 1 - u / p.c.rows;
 
   // How far this tile of queries sees.
   const int cap = p.c.width * p.c.block;
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
   }
   // Equal parts of whole CTA strides; a part that would be empty has no CTA.
   int chunk = ((end + p.splits - 1) / p.splits + kWarps * kTok - 1) / (kWarps * kTok) * (kWarps * kTok);
-  chunk = max(chunk, kMinChunk);
+  chunk = max(chunk, p.min_chunk);
   const int parts = max((end + chunk - 1) / chunk, 1);
   if (split >= parts) return;
   const int begin = split * chunk, stop = min(end, begin + chunk);
@@ -234,13 +239,13 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
   // exact but for values below 2^-28 of that one, which are off by 2^-39 of
   // it.  (Bytes turn into f16 in two instructions, into bf16 in three.)
   uint32_t q[MT][KW][4];
-  int limit[MT][2];
-  float back[MT][2];  // the power's inverse, times scale and log2 e
+  int limit[MT][E];
+  float back[MT][E];  // the power's inverse, times scale and log2 e
   const float log2e = 1.4426950408889634f;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < E; ++e) {
       const int at = q_first + (SHARED ? warp * R : 0) + 16 * m + 8 * e + r8;
       const bool in = at < p.qrows;
       const int i = in ? at / p.group : 0, g = in ? at % p.group : 0;
@@ -287,18 +292,22 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
       for (int s = 0; s < KW; ++s) {
         q[m][s][e] = w[2 * s];
         q[m][s][2 + e] = w[2 * s + 1];
+        if (E == 1) q[m][s][1] = q[m][s][3] = 0;
       }
     }
   }
 
   float acc[MT][VB][4];
-  float top[MT][2], sum[MT][2];
+  float top[MT][E], sum[MT][E];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
 #pragma unroll
     for (int j = 0; j < VB; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
-    top[m][0] = top[m][1] = -INFINITY;
-    sum[m][0] = sum[m][1] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      top[m][e] = -INFINITY;
+      sum[m][e] = 0.0f;
+    }
   }
 
   // Of the 32 tiles that are consumed next, one per lane and half: the key
@@ -316,8 +325,8 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
           const int64_t tile = tiles0 + static_cast<int64_t>(b) * p.c.heads;
           const float vs = fmaxf(__ldg(p.c.v_scale + tile), kMinScale);
           f_s[e] = __ldg(p.c.k_scale + tile);
-          l_s[e] = log2f(vs);
-          i_s[e] = 1.0f / vs;
+          l_s[e] = __log2f(vs);
+          i_s[e] = ex2(-l_s[e]);  // of the logarithm that the weight has: they cancel
         } else {
           i_s[e] = -1.0f;
         }
@@ -350,40 +359,46 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
     const bool partial = i0 < 0.0f || i1 < 0.0f;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const float g0[2] = {f0 * back[m][0], f0 * back[m][1]}, g1[2] = {f1 * back[m][0], f1 * back[m][1]};
+      bool cut = partial;
 #pragma unroll
-      for (int n8 = 0; n8 < 4; ++n8) {
+      for (int e = 0; e < E; ++e) {
+        const float g0 = f0 * back[m][e], g1 = f1 * back[m][e];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          sc[m][n8][x] = fmaf(sc[m][n8][x], n8 < 2 ? g0[x >> 1] : g1[x >> 1], n8 < 2 ? l0 : l1);
+        for (int n8 = 0; n8 < 4; ++n8) {
+#pragma unroll
+          for (int x = 2 * e; x < 2 * e + 2; ++x)
+            sc[m][n8][x] = fmaf(sc[m][n8][x], n8 < 2 ? g0 : g1, n8 < 2 ? l0 : l1);
+        }
+        cut = cut || t0 > limit[m][e] - kTok;
       }
       // Tokens past a row's end, and absent ones.  (Selected, not added: their
       // bytes and scales may be anything.)
-      const bool cut = t0 > limit[m][0] - kTok || t0 > limit[m][1] - kTok || partial;
       if (__any_sync(0xffffffffu, cut)) {
 #pragma unroll
         for (int n8 = 0; n8 < 4; ++n8) {
           const bool absent = (n8 < 2 ? i0 : i1) < 0.0f;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < 2 * E; ++x) {
             const int tok = t0 + 16 * (n8 / 2) + 8 * (n8 & 1) + c4 + 4 * (x & 1);
             if (absent || tok >= limit[m][x >> 1]) sc[m][n8][x] = -INFINITY;
           }
         }
       }
-      float next[2];
+      float next[E];
+      bool rise = false;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         float t = top[m][e];
 #pragma unroll
         for (int n8 = 0; n8 < 4; ++n8) t = fmaxf(t, fmaxf(sc[m][n8][2 * e], sc[m][n8][2 * e + 1]));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
         next[e] = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+        rise = rise || next[e] > top[m][e];
       }
       // Maxima rise ever more rarely along a row.
-      if (__any_sync(0xffffffffu, next[0] > top[m][0] || next[1] > top[m][1])) {
+      if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < E; ++e) {
           const float shrink = ex2(top[m][e] - (next[e] == -INFINITY ? 0.0f : next[e]));
           top[m][e] = next[e];
           sum[m][e] *= shrink;
@@ -395,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
         }
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         const float zero = top[m][e] == -INFINITY ? 0.0f : top[m][e];
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
@@ -421,9 +436,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         a[m][0] = pack2<__half>(sc[m][2 * half][0], sc[m][2 * half][1]);
-        a[m][1] = pack2<__half>(sc[m][2 * half][2], sc[m][2 * half][3]);
+        a[m][1] = E == 1 ? 0u : pack2<__half>(sc[m][2 * half][2], sc[m][2 * half][3]);
         a[m][2] = pack2<__half>(sc[m][2 * half + 1][0], sc[m][2 * half + 1][1]);
-        a[m][3] = pack2<__half>(sc[m][2 * half + 1][2], sc[m][2 * half + 1][3]);
+        a[m][3] = E == 1 ? 0u : pack2<__half>(sc[m][2 * half + 1][2], sc[m][2 * half + 1][3]);
       }
       uint32_t w[4][VB / 4];
 #pragma unroll
@@ -465,18 +480,19 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < E; ++e) {
       const int rr = 16 * m + 8 * e + r8;
       float s = sum[m][e];
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       if (c4 == 0) sh.ml[warp][rr] = make_float2(top[m][e], s);
       if ((SHARED ? warp * R : 0) + rr < q_rows) {
-        float *const o = acc_s + (warp * R + rr) * D + c4 * (D / 4);
+        float4 *const o = reinterpret_cast<float4 *>(acc_s + (warp * R + rr) * D + c4 * (D / 4));
 #pragma unroll
-        for (int n = 0; n < VB; ++n) {
-          o[n] = acc[m][n][2 * e];
-          o[VB + n] = acc[m][n][2 * e + 1];
+        for (int n = 0; n < VB; n += 4) {
+          o[n / 4] = make_float4(acc[m][n][2 * e], acc[m][n + 1][2 * e], acc[m][n + 2][2 * e], acc[m][n + 3][2 * e]);
+          o[(VB + n) / 4] = make_float4(acc[m][n][2 * e + 1], acc[m][n + 1][2 * e + 1], acc[m][n + 2][2 * e + 1],
+                                        acc[m][n + 3][2 * e + 1]);
         }
       }
     }
@@ -564,7 +580,7 @@ lm_status check(const lm_kv_cache *cache, int32_t tokens, int32_t q_heads) {
 // and parts of the tokens.
 struct Cut {
   bool shared;
-  int mt, qrows, qtiles, splits, part_rows;
+  int mt, qrows, qtiles, splits, part_rows, chunk;
   int64_t units;
   size_t done_bytes, ml_bytes, acc_bytes;
 };
@@ -580,11 +596,12 @@ Cut cut(const lm_kv_cache *c, int32_t tokens, int32_t q_heads) {
   k.units = static_cast<int64_t>(c->rows) * c->heads * k.qtiles;
   // As many parts as fill the device once.  Where the units alone come near
   // that, parts are for balance between rows of unequal length: four rounds of
-  // them.  None below kMinChunk tokens.
+  // them.  None below kMinChunk or kBalance tokens.
   const int64_t cap = static_cast<int64_t>(c->width) * c->block;
   const int64_t slots = full_ctas(c->head_dim);
   int64_t s = k.units == 0 ? 1 : 2 * k.units > slots ? (4 * slots + k.units - 1) / k.units : slots / k.units;
-  const int64_t most = (cap + kMinChunk - 1) / kMinChunk;
+  k.chunk = 2 * k.units > slots ? kBalance : kMinChunk;
+  const int64_t most = (cap + k.chunk - 1) / k.chunk;
   if (s > most) s = most;
   k.splits = static_cast<int>(s < 1 ? 1 : s);
   const int64_t parts = k.splits > 1 ? k.units * k.splits * k.part_rows : 0;
@@ -597,9 +614,9 @@ Cut cut(const lm_kv_cache *c, int32_t tokens, int32_t q_heads) {
   return k;
 }
 
-template <typename T, int D, int MT, bool SHARED>
+template <typename T, int D, int MT, int E, bool SHARED>
 lm_status launch(const AttendParams &p, int64_t ctas, cudaStream_t s) {
-  auto *const kernel = attend_kernel<T, D, MT, SHARED>;
+  auto *const kernel = attend_kernel<T, D, MT, E, SHARED>;
   constexpr int smem = big_bytes(D, MT, SHARED) + static_cast<int>(sizeof(Shared<16 * MT>));
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
   kernel<<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(p);
@@ -609,8 +626,9 @@ lm_status launch(const AttendParams &p, int64_t ctas, cudaStream_t s) {
 
 template <typename T, int D>
 lm_status launch_form(const AttendParams &p, const Cut &k, int64_t ctas, cudaStream_t s) {
-  if (k.shared) return launch<T, D, 1, true>(p, ctas, s);
-  return k.mt == 1 ? launch<T, D, 1, false>(p, ctas, s) : launch<T, D, 2, false>(p, ctas, s);
+  if (k.shared) return launch<T, D, 1, 2, true>(p, ctas, s);
+  if (k.qrows <= 8) return launch<T, D, 1, 1, false>(p, ctas, s);
+  return k.mt == 1 ? launch<T, D, 1, 2, false>(p, ctas, s) : launch<T, D, 2, 2, false>(p, ctas, s);
 }
 
 template <typename T>
@@ -673,6 +691,7 @@ extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const
   p.qtiles = k.qtiles;
   p.splits = k.splits;
   p.part_rows = k.part_rows;
+  p.min_chunk = k.chunk;
   p.qvec = aligned(q, 16) && q_strides[0] % 8 == 0 && q_strides[1] % 8 == 0 && q_strides[2] % 8 == 0;
   p.scale = scale;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

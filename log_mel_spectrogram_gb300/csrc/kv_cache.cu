@@ -51,40 +51,54 @@ __device__ __forceinline__ uint32_t max_abs2<__nv_bfloat16>(uint32_t m, uint32_t
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+struct Eight {
+  float x[8];
+};
+
+// The nearest integers of x / scale, ties to even, NaN as 0: the definition.
+__device__ __noinline__ Eight divide8(Eight v, float scale) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v.x[j] = static_cast<float>(static_cast<int>(rintf(__fdiv_rn(v.x[j], scale))));
+  return v;
+}
+
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves an integer in the low bits
+
+// Eight integers' low bytes.
+__device__ __forceinline__ uint2 pack_bytes(const float (&q)[8]) {
+  uint32_t t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t[j] = __float_as_uint(q[j] + kMagic);
+  return make_uint2(
+      __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
+      __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
+}
+
 // x / scale to the nearest integer, ties to even, as __fdiv_rn and rintf give
-// it, for eight values with |x / scale| <= 128, without the division: adding
-// 1.5 * 2^23 to x * (1 / scale) leaves the integer in the low bits.  The
-// product is within 2^-22 * 128 of the quotient, so that only values within
-// 2^-14 of a half can differ, and those take the division.
-__device__ __forceinline__ void quantise8(const float (&x)[8], float scale, float inv, float (&q)[8], uint2 &w) {
-  constexpr float kMagic = 12582912.0f;
-  float t[8], off = 0.0f;
+// it, for eight values with |x / scale| <= 128, without the division.  The
+// product with 1 / scale is within 2^-22 * 128 of the quotient, so that only
+// values within 2^-14 of a half can differ, and those take the division.
+__device__ __forceinline__ void quantise8(const float (&x)[8], float scale, float inv, bool plain, float (&q)[8]) {
+  float off = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    t[j] = fmaf(x[j], inv, kMagic);
-    q[j] = t[j] - kMagic;
+    q[j] = fmaf(x[j], inv, kMagic) - kMagic;
     off = fmaxf(off, fabsf(fmaf(x[j], inv, -q[j])));
   }
-  // (An infinite or a subnormal scale has no inverse to go by.)
-  if (!(off < 0.5f - 6.2e-5f) || !(inv > 0.0f && inv < INFINITY)) {
+  if (!(off < 0.5f - 6.2e-5f) || plain) {
+    Eight v;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      q[j] = static_cast<float>(static_cast<int>(rintf(__fdiv_rn(x[j], scale))));  // NaN as 0
-      t[j] = q[j] + kMagic;
-    }
-  }
+    for (int j = 0; j < 8; ++j) v.x[j] = x[j];
+    v = divide8(v, scale);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint32_t a = __byte_perm(__float_as_uint(t[4 * j]), __float_as_uint(t[4 * j + 1]), 0x0040);
-    const uint32_t b = __byte_perm(__float_as_uint(t[4 * j + 2]), __float_as_uint(t[4 * j + 3]), 0x0040);
-    (j ? w.y : w.x) = __byte_perm(a, b, 0x5410);
+    for (int j = 0; j < 8; ++j) q[j] = v.x[j];
   }
 }
 
 // One unit: row r's span s of head h.  D and BS are the head dimension and
 // the tokens of a block; NT threads work on the unit.
 template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams p) {
   constexpr int NT = BS * D / 64;
   constexpr int PER = kThreads / NT;  // units per CTA
   __shared__ float part[kThreads / 32];
@@ -112,21 +126,26 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams 
   const bool had = ok && base < held;  // the block holds tokens already
   const float before = had ? *qs : 0.0f;
 
-  // Vector i of this thread: token v / (D / 8), elements v % (D / 8) * 8, of
-  // v = i * NT + tid.  A new token's values, or an old one's bytes.
-  const T *const src = static_cast<const T *>(p.src[which]) + r * p.row_s[which] + h * p.head_s[which];
+  // Vector i of this thread: token tok0 + i * STEP of the block, elements d ..
+  // d + 7.  A new token's values, or an old one's bytes.
+  constexpr int STEP = NT / (D / 8);
+  const int tok0 = tid / (D / 8), d = tid % (D / 8) * 8;
+  const int old = ok ? min(held - base, BS) : 0, all = ok ? min(end - base, BS) : 0;  // tokens of the block
+  const T *const src = static_cast<const T *>(p.src[which]) + r * p.row_s[which] + h * p.head_s[which] +
+                       (static_cast<int64_t>(base) + tok0 - held) * p.tok_s[which] + d;
+  const int64_t src_step = STEP * p.tok_s[which];
+  int8_t *const dst = q8 + tok0 * D + d;
   uint32_t x[kVecs][4];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int v = i * NT + tid;
-    const int tok = base + v / (D / 8), d = v % (D / 8) * 8;
+    const int tok = tok0 + i * STEP;
     x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
-    if (ok && tok < held) {
-      const uint2 w = *reinterpret_cast<const uint2 *>(q8 + (tok - base) * D + d);
+    if (tok < old) {
+      const uint2 w = *reinterpret_cast<const uint2 *>(dst + i * STEP * D);
       x[i][0] = w.x;
       x[i][1] = w.y;
-    } else if (ok && tok < end) {
-      const T *const s = src + static_cast<int64_t>(tok - held) * p.tok_s[which] + d;
+    } else if (tok < all) {
+      const T *const s = src + i * src_step;
       if (p.vec) {
         const uint4 w = __ldg(reinterpret_cast<const uint4 *>(s));
         x[i][0] = w.x;
@@ -143,8 +162,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams 
   uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int tok = base + (i * NT + tid) / (D / 8);
-    if (tok >= held)
+    if (tok0 + i * STEP >= old)
 #pragma unroll
       for (int j = 0; j < 4; ++j) most = max_abs2<T>(most, x[i][j]);
   }
@@ -164,51 +182,46 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams 
   float now = fmaxf(before, top * (1.0f / 127.0f));
   if (now == 0.0f) now = 1.0f;
   const float shrink = had ? before / now : 1.0f, inv = 1.0f / now;
+  const bool plain = !(inv > 0.0f && inv < INFINITY);  // an infinite or subnormal scale has no inverse to go by
   // Every thread of the unit has read the old scale before one writes it.
   if (NT <= 32) __syncwarp();
   if (ok && tid == 0) *qs = now;
 
-  T *const out = static_cast<T *>(p.values[which]);
+  T *const values = static_cast<T *>(p.values[which]);
+  T *const out = values && in ? values + ((static_cast<int64_t>(rs) * BS + tok0) * p.c.heads + h) * D + d : nullptr;
+  const int64_t out_step = static_cast<int64_t>(STEP) * p.c.heads * D;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int v = i * NT + tid;
-    const int tok = base + v / (D / 8), d = v % (D / 8) * 8;
-    float q[8] = {};
-    if (ok && tok < end) {
-      uint2 *const at = reinterpret_cast<uint2 *>(q8 + (tok - base) * D + d);
-      if (tok >= held) {
-        float f[8];
+    const int tok = tok0 + i * STEP;
+    uint2 *const at = reinterpret_cast<uint2 *>(dst + i * STEP * D);
+    float q[8];
+    if (tok >= all) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f2 = unpack2<T>(x[i][j]);
-          f[2 * j] = f2.x;
-          f[2 * j + 1] = f2.y;
-        }
-        uint2 w;
-        quantise8(f, now, inv, q, w);
-        *at = w;
-      } else {
-        uint2 w = make_uint2(x[i][0], x[i][1]);
+      for (int j = 0; j < 8; ++j) q[j] = 0.0f;
+    } else if (tok >= old) {
+      float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = static_cast<float>(byte_of(w, j));
-        if (shrink != 1.0f) {
-          int n[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            n[j] = static_cast<int>(rintf(q[j] * shrink));
-            q[j] = static_cast<float>(n[j]);
-          }
-          w.x = (n[0] & 255) | (n[1] & 255) << 8 | (n[2] & 255) << 16 | static_cast<uint32_t>(n[3]) << 24;
-          w.y = (n[4] & 255) | (n[5] & 255) << 8 | (n[6] & 255) << 16 | static_cast<uint32_t>(n[7]) << 24;
-          *at = w;
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float2 f2 = unpack2<T>(x[i][j]);
+        f[2 * j] = f2.x;
+        f[2 * j + 1] = f2.y;
       }
+      quantise8(f, now, inv, plain, q);
+      *at = pack_bytes(q);
+    } else {
+      const uint2 w = make_uint2(x[i][0], x[i][1]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] *= now;
+      for (int j = 0; j < 8; ++j) q[j] = static_cast<float>(byte_of(w, j));
+      if (shrink != 1.0f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = static_cast<float>(static_cast<int>(rintf(q[j] * shrink)));
+        *at = pack_bytes(q);
+      }
     }
-    if (out && in) {
-      const int64_t to = (static_cast<int64_t>(rs) * BS + v / (D / 8)) * p.c.heads + h;
-      __stcs(reinterpret_cast<uint4 *>(out + to * D + d),
+    if (out) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = tok < all ? q[j] * now : 0.0f;
+      __stcs(reinterpret_cast<uint4 *>(out + i * out_step),
              make_uint4(pack2<T>(q[0], q[1]), pack2<T>(q[2], q[3]), pack2<T>(q[4], q[5]), pack2<T>(q[6], q[7])));
     }
   }

@@ -4,16 +4,18 @@
 // A warp holds a tile of a beam's logits in registers (32 lanes x 8 vectors of
 // 16 bytes, all in flight together: the pass is bound by reading the logits
 // once) and takes three things from it: the maximum, the sum of exponentials,
-// and its best `beams` continuations, a sorted list with one entry per lane.
-// The n-th largest of the lanes' maxima bounds the list from below, so that
-// only a few values ever reach the insertion.  A CTA joins its eight tiles; the
-// last CTA of a clip joins the parts of its beams, in order, and selects.
+// and its best `beams` continuations.  The n-th largest of the lanes' maxima
+// bounds those from below, so that hardly more than n values are ever gathered
+// and ranked.  A CTA joins its eight tiles; the last CTA of a clip joins the
+// parts of its beams, in order, and selects.  A few rows alone take tiles of 2
+// vectors, for the sake of latency.
 //
 // A continuation inside a beam is ordered by its key: the logit as an ordered
 // integer, then the lower token.  Keys are distinct, so that an entry's place
 // is the number of larger ones, whatever order it is found in.
 #include <climits>
 
+#include "f32x2.cuh"
 #include "half.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -25,8 +27,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxBeams = 32;
 constexpr int64_t kMaxVocab = 1 << 24;
-constexpr int kVecs = 8;              // 16-byte vectors of a lane
-constexpr int kTileVecs = 32 * kVecs;
+constexpr int kHistory = 4096;         // entries of a clip's histories that are fetched ahead
+constexpr int kGather = 64;           // keys that a warp gathers before it ranks them
 constexpr int kClips = 16384;         // clips of a launch: counters at the workspace's start
 constexpr size_t kCounterBytes = 4 * kClips;
 
@@ -35,7 +37,7 @@ struct BeamParams {
   uint32_t *done;       // per clip: parts that are ready
   float2 *part_ms;      // [row][part]: maximum, sum of exponentials against it
   uint64_t *part_keys;  // [row][part][beams], largest first, 0 = none
-  int32_t parts;
+  int32_t parts, tiles;  // CTAs of a row; tiles that each of their warps goes over
 };
 
 // Logits are compared as f32, -0 as 0; among equals the lower token is larger.
@@ -45,12 +47,6 @@ __device__ __forceinline__ uint64_t order_key(float x, int token) {
 __device__ __forceinline__ float key_logit(uint64_t k) { return ordered_to_float(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ int key_token(uint64_t k) {
   return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -81,69 +77,110 @@ __device__ __forceinline__ uint32_t bits_of<__nv_bfloat16>(__nv_bfloat16 x) {
   return __bfloat16_as_ushort(x);
 }
 
-// The 16 bytes that start Q words (and half a word, with HALF) into the eight
-// words w, x.
-template <int Q, bool HALF>
-__device__ __forceinline__ void shift_words(uint32_t (&w)[4], const uint32_t (&x)[4]) {
-  uint32_t c[8];
+// The 16 bytes that start `halves` 16-bit units into the eight words w, x.
+__device__ __forceinline__ void shift_words(uint32_t (&w)[4], const uint32_t (&x)[4], int halves) {
+  uint32_t c[8] = {w[0], w[1], w[2], w[3], x[0], x[1], x[2], x[3]};
+  if (halves & 4) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    c[j] = w[j];
-    c[4 + j] = x[j];
+    for (int j = 0; j < 6; ++j) c[j] = c[j + 2];
+  }
+  if (halves & 2) {
+#pragma unroll
+    for (int j = 0; j < 5; ++j) c[j] = c[j + 1];
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = HALF ? __funnelshift_r(c[j + Q], c[j + Q + 1], 16) : c[j + Q];
+  for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(c[j], c[j + 1], (halves & 1) * 16);
 }
 
-// Loads the aligned 16-byte vector `v` of a row that starts `skew` values into
-// its vector 0; values outside the row read as -infinity.
+// The aligned 16-byte vector that starts at value t0 of a row; values outside
+// the row read as -infinity.
 template <typename T>
-__device__ __forceinline__ void load_vec(const T *x, int64_t v, int skew, int vocab, uint32_t (&w)[4]) {
+__device__ __noinline__ uint4 load_edge(const T *x, int t0, int vocab) {
   constexpr int N = 16 / static_cast<int>(sizeof(T));
-  const int64_t t0 = v * N - skew;
-  if (t0 >= 0 && t0 + N <= vocab) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(x + t0));
-    w[0] = u.x;
-    w[1] = u.y;
-    w[2] = u.z;
-    w[3] = u.w;
-    return;
-  }
   const uint32_t none = bits_of<T>(from_f32<T>(-INFINITY));
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = sizeof(T) == 4 ? none : none | none << 16;
-  if (t0 >= vocab) return;
+  uint32_t w[4];
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    if (t0 + e >= 0 && t0 + e < vocab) {
-      const uint32_t b = bits_of<T>(x[t0 + e]);
-      if constexpr (sizeof(T) == 4) {
-        w[e] = b;
-      } else {
-        w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | b << 16 : (w[e / 2] & 0xffff0000u) | b;
-      }
+    const bool in = t0 + e >= 0 && t0 + e < vocab;
+    const uint32_t b = in ? bits_of<T>(x[t0 + e]) : none;
+    if constexpr (sizeof(T) == 4) {
+      w[e] = b;
+    } else {
+      w[e / 2] = e & 1 ? w[e / 2] | b << 16 : b;
     }
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The largest `n` of the distinct nonzero keys in[0 .. count), largest first,
-// into out[0 .. n) (0 where there are fewer); by `threads` threads.
-__device__ __forceinline__ void largest(const uint64_t *in, int count, int n, uint64_t *out, int tid, int threads) {
-  for (int i = tid; i < count; i += threads) {
-    const uint64_t k = in[i];
-    if (k == 0) continue;
-    int place = 0;
-    for (int j = 0; j < count; ++j) place += in[j] > k;
-    if (place < n) out[place] = k;
+// Ranks the `count` <= kGather keys that a warp has gathered (distinct, or 0 for
+// none): the largest `n` in order, then zeros up to n.  Returns how many there are;
+// *floor: the n-th.
+__device__ __noinline__ int rank_keys(uint64_t *keys, int count, int n, uint64_t *floor) {
+  const int lane = threadIdx.x % 32;
+  __syncwarp();
+  const uint64_t a = lane < count ? keys[lane] : 0, b = lane + 32 < count ? keys[lane + 32] : 0;
+  int pa = 0, pb = 0;
+#pragma unroll 4
+  for (int j = 0; j < count; ++j) {
+    const uint64_t k = keys[j];
+    pa += k > a;
+    pb += k > b;
   }
+  const int found = __popc(__ballot_sync(0xffffffffu, a != 0)) + __popc(__ballot_sync(0xffffffffu, b != 0));
+  const int left = found < n ? found : n;
+  __syncwarp();
+  if (a != 0 && pa < n) keys[pa] = a;
+  if (b != 0 && pb < n) keys[pb] = b;
+  if (lane >= left && lane < n) keys[lane] = 0;
+  __syncwarp();
+  *floor = keys[n - 1];
+  return left;
 }
 
+// A warp's shared memory: vectors that hold a value of interest, and keys.
+struct Gather {
+  uint64_t keys[kGather];
+  uint4 vecs[kGather];
+  int first[kGather];  // the first token of a vector
+};
+
+// Adds the values of `count` gathered vectors that reach `bound` to the keys.
+// Returns how many keys there are then; *floor as of rank_keys.
 template <typename T>
+__device__ __noinline__ int take_keys(Gather *g, int count, int keys, float bound, int vocab, int n, uint64_t *floor) {
+  constexpr int N = 16 / static_cast<int>(sizeof(T));
+  const int lane = threadIdx.x % 32;
+  uint64_t least = *floor;
+  __syncwarp();
+#pragma unroll 1
+  for (int i = lane; i - lane < count * N; i += 32) {
+    uint64_t key = 0;
+    if (i < count * N) {
+      const float v = to_f32(reinterpret_cast<const T *>(g->vecs)[i]);
+      const int t = g->first[i / N] + i % N;
+      if (v >= bound && t < vocab) key = order_key(v, t);
+    }
+    const uint32_t who = __ballot_sync(0xffffffffu, key > least);
+    if (who == 0) continue;
+    if (key > least) g->keys[keys + __popc(who & ((1u << lane) - 1))] = key;
+    keys += __popc(who);
+    if (keys > kGather - 32) keys = rank_keys(g->keys, keys, n, &least);
+  }
+  __syncwarp();
+  *floor = least;
+  return keys;
+}
+
+template <typename T, int kVecs>
 __global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p) {
   constexpr int N = 16 / static_cast<int>(sizeof(T));  // values of a vector
-  __shared__ uint64_t keys[kWarps * kMaxBeams];
+  constexpr int kTileVecs = 32 * kVecs;
+  __shared__ Gather gathered[kWarps];
   __shared__ float2 ms[kWarps];
-  __shared__ uint64_t best[kMaxBeams];
+  __shared__ float tot[kMaxBeams * kMaxBeams];
+  __shared__ int tok[kMaxBeams * kMaxBeams];
+  __shared__ int parents[kMaxBeams], tokens[kMaxBeams];
+  __shared__ int32_t history[kHistory];
   __shared__ bool last;
   const lm_beam_args &a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -151,109 +188,134 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p) {
   const int64_t row = blockIdx.x / p.parts;
   const int n = a.beams, vocab = static_cast<int>(a.vocab);
 
-  // This lane's tokens: vectors v0 + 32 i of the row.  A row that starts off
-  // a 16-byte boundary is read in the aligned vectors that hold it and moved
-  // into place between the lanes, so that results do not depend on where a row
-  // lies.
+  // A row that starts off a 16-byte boundary is read in the aligned vectors
+  // that hold it and moved into place between the lanes, so that results do not
+  // depend on where a row lies.
   const T *const x = static_cast<const T *>(a.logits) + row * a.row_stride;
   const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
-  const int64_t v0 = (static_cast<int64_t>(part) * kWarps + warp) * kTileVecs + lane;
-  uint32_t w[kVecs][4];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) load_vec(x, v0 + 32 * i, skew, vocab, w[i]);
-  if (skew != 0) {
-    uint32_t over[4];
-    load_vec(x, v0 + 32 * kVecs - lane, skew, vocab, over);  // one address: the vector past the tile
-    const int words = skew * static_cast<int>(sizeof(T)) / 4;
-    const bool odd = sizeof(T) == 2 && (skew & 1);
+  const int shift = skew * static_cast<int>(sizeof(T)) / 2;  // in half words
+  Gather &g = gathered[warp];
+  uint64_t *const list = g.keys;
+  uint64_t floor = 0;  // what a key has to beat
+  int count = 0;
+  float m = -INFINITY, z = 0.0f;
+  for (int k = 0; k < p.tiles; ++k) {
+    const int tile0 = ((part * p.tiles + k) * kWarps + warp) * kTileVecs * N;
+    if (tile0 >= vocab) break;
+    const int t0 = tile0 + lane * N;  // vector i holds the tokens from t0 + 32 N i on
+    uint32_t w[kVecs][4];
+    auto load = [&](int at) {
+      return at >= 0 && at + N <= vocab ? __ldg(reinterpret_cast<const uint4 *>(x + at)) : load_edge(x, at, vocab);
+    };
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      uint32_t next[4];
+      const uint4 u = load(t0 - skew + 32 * N * i);
+      w[i][0] = u.x;
+      w[i][1] = u.y;
+      w[i][2] = u.z;
+      w[i][3] = u.w;
+    }
+    if (skew != 0) {
+      const uint4 u = load(tile0 - skew + kTileVecs * N);  // one address: the vector past the tile
+      const uint32_t over[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t first = i + 1 < kVecs ? __shfl_sync(0xffffffffu, w[(i + 1) % kVecs][j], 0) : over[j];
-        next[j] = __shfl_down_sync(0xffffffffu, w[i][j], 1);
-        if (lane == 31) next[j] = first;
-      }
-      switch (words * 2 + odd) {
-        case 0: break;
-        case 1: shift_words<0, true>(w[i], next); break;
-        case 2: shift_words<1, false>(w[i], next); break;
-        case 3: shift_words<1, true>(w[i], next); break;
-        case 4: shift_words<2, false>(w[i], next); break;
-        case 5: shift_words<2, true>(w[i], next); break;
-        case 6: shift_words<3, false>(w[i], next); break;
-        default: shift_words<3, true>(w[i], next); break;
+      for (int i = 0; i < kVecs; ++i) {
+        uint32_t next[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // Lane 31 is followed by lane 0's next vector, which lane 0 hands round.
+          const uint32_t after = i + 1 < kVecs ? w[(i + 1) % kVecs][j] : over[j];
+          next[j] = __shfl_sync(0xffffffffu, lane == 0 ? after : w[i][j], (lane + 1) % 32);
+        }
+        shift_words(w[i], next, shift);
       }
     }
+    float vt[kVecs], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      vt[i] = value_of<T>(w[i], 0);
+#pragma unroll
+      for (int e = 1; e < N; ++e) vt[i] = fmaxf(vt[i], value_of<T>(w[i], e));
+      top = fmaxf(top, vt[i]);
+    }
+    const float before = m;
+    m = fmaxf(m, warp_max(top));
+    // A NaN or +infinity makes the sum NaN, which marks the beam.
+    const float base = m == -INFINITY ? 0.0f : m;
+    if (before != -INFINITY) z *= ex2((before - base) * kLog2e);
+    f32x2 z2 = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        const f32x2 x2 = pair(value_of<T>(w[i], e), value_of<T>(w[i], e + 1));
+        const float2 y = unpair(mul2(add2(x2, both(-base)), both(kLog2e)));
+        z2 = add2(z2, pair(ex2(y.x), ex2(y.y)));
+      }
+    z += unpair(z2).x + unpair(z2).y;
+
+    // A bound from below: the n-th best so far, or the n-th largest of the
+    // lanes' maxima.
+    float bound = key_logit(floor);
+    if (floor == 0) {
+      uint32_t mine = float_to_ordered(top), kth = 0;
+      for (int i = 0; i < n; ++i) {
+        kth = __reduce_max_sync(0xffffffffu, mine);
+        const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
+        if (lane == __ffs(who) - 1) mine = 0;
+      }
+      bound = kth == 0 ? -INFINITY : ordered_to_float(kth);
+    }
+    if (!__any_sync(0xffffffffu, top >= bound)) continue;
+    int queued = 0;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const uint32_t who = __ballot_sync(0xffffffffu, vt[i] >= bound);
+      if (who == 0) continue;
+      if (vt[i] >= bound) {
+        const int at = queued + __popc(who & ((1u << lane) - 1));
+        g.vecs[at] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        g.first[at] = t0 + 32 * N * i;
+      }
+      queued += __popc(who);
+      if (queued > kGather - 32) {
+        count = take_keys<T>(&g, queued, count, bound, vocab, n, &floor);
+        queued = 0;
+      }
+    }
+    count = take_keys<T>(&g, queued, count, bound, vocab, n, &floor);
+    if (k + 1 < p.tiles) count = rank_keys(list, count, n, &floor);
   }
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-    for (int e = 0; e < N; ++e) top = fmaxf(top, value_of<T>(w[i], e));
-  const float m = warp_max(top);
-  // A NaN or +infinity makes the sum NaN, which marks the beam.
-  const float base = m == -INFINITY ? 0.0f : m;
-  float z = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-    for (int e = 0; e < N; ++e) z += ex2((value_of<T>(w[i], e) - base) * kLog2e);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-
-  // The n-th largest of the lanes' maxima.
-  uint32_t mine = float_to_ordered(top), kth = 0;
-  for (int i = 0; i < n; ++i) {
-    kth = __reduce_max_sync(0xffffffffu, mine);
-    const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
-    if (lane == __ffs(who) - 1) mine = 0;
-  }
-  float bound = kth == 0 ? -INFINITY : ordered_to_float(kth);
-  uint64_t list = 0, floor = 0;  // lane i: the i-th best so far; the n-th
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    float vt = value_of<T>(w[i], 0);
-#pragma unroll
-    for (int e = 1; e < N; ++e) vt = fmaxf(vt, value_of<T>(w[i], e));
-    if (!__any_sync(0xffffffffu, vt >= bound)) continue;
-    const int64_t t0 = (v0 + 32 * i) * N;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float v = value_of<T>(w[i], e);
-      const int64_t t = t0 + e;
-      uint64_t key = v >= bound && t < vocab ? order_key(v, static_cast<int>(t)) : 0;
-      for (;;) {
-        const uint32_t who = __ballot_sync(0xffffffffu, key > floor);
-        if (who == 0) break;
-        const int from = __ffs(who) - 1;
-        const uint64_t k = __shfl_sync(0xffffffffu, key, from);
-        if (lane == from) key = 0;
-        const int place = __popc(__ballot_sync(0xffffffffu, list > k));
-        const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
-        list = lane < place ? list : lane == place ? k : up;
-        floor = __shfl_sync(0xffffffffu, list, n - 1);
-      }
-    }
-  }
-  if (lane < n) keys[warp * n + lane] = list;
+  rank_keys(list, count, n, &floor);
   if (lane == 0) ms[warp] = make_float2(m, z);
   __syncthreads();
 
-  // The CTA's eight tiles as one part.
-  if (threadIdx.x < n) best[threadIdx.x] = 0;
-  __syncthreads();
-  largest(keys, kWarps * n, n, best, threadIdx.x, kThreads);
-  __syncthreads();
-  if (threadIdx.x < n) p.part_keys[(row * p.parts + part) * n + threadIdx.x] = best[threadIdx.x];
-  if (threadIdx.x == 0) {
-    float mm = -INFINITY, zz = 0.0f;
-    for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ms[i].x);
-    const float bb = mm == -INFINITY ? 0.0f : mm;
-    for (int i = 0; i < kWarps; ++i)
-      zz += ms[i].x == -INFINITY ? ms[i].y : ms[i].y * ex2((ms[i].x - bb) * kLog2e);
-    p.part_ms[row * p.parts + part] = make_float2(mm, zz);
+  // The CTA's eight lists as one part.
+  uint64_t *const part_keys = p.part_keys + (row * p.parts + part) * n;
+  if (warp == kWarps - 1) {
+    const float2 v = lane < kWarps ? ms[lane] : make_float2(-INFINITY, 0.0f);
+    const float mm = warp_max(v.x), bb = mm == -INFINITY ? 0.0f : mm;
+    float zz = v.x == -INFINITY ? v.y : v.y * ex2((v.x - bb) * kLog2e);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) zz += __shfl_xor_sync(0xffffffffu, zz, o);
+    if (lane == 0) p.part_ms[row * p.parts + part] = make_float2(mm, zz);
+  }
+  // (Zeros fill up places that no key takes: they count what they follow.)
+  for (int i = threadIdx.x; i < kWarps * n; i += kThreads) {
+    const int of = i / n, at = i - of * n;
+    const uint64_t k = gathered[of].keys[at];
+    int place = 0;
+#pragma unroll 1
+    for (int u = 0; u < n; ++u) {
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) {
+        const uint64_t o = gathered[j].keys[u];
+        place += o > k || (o == k && j * n + u < i);
+      }
+    }
+    if (place < n) part_keys[place] = k;
   }
   __syncthreads();
   const int clip = static_cast<int>(row / n);
@@ -266,15 +328,32 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p) {
   __threadfence();
   if (threadIdx.x == 0) p.done[clip] = 0;
 
-  // The clip's last CTA.  A warp joins a beam's parts ...
-  __shared__ float tot[kMaxBeams * kMaxBeams];
-  __shared__ int tok[kMaxBeams * kMaxBeams];
-  __shared__ int parents[kMaxBeams], tokens[kMaxBeams];
+  // The clip's last CTA.  Its beams' histories are on their way meanwhile,
+  // where they fit ...
   const int places = vocab < n ? vocab : n;
   const int64_t row0 = static_cast<int64_t>(clip) * n;
+  const uint32_t width = static_cast<uint32_t>(a.width);
+  const uint32_t told = a.history ? n * width : 0;
+  const int32_t *const from = a.history + row0 * a.width;
+  int32_t *const to = a.out_history + row0 * a.width;
+  const bool ahead = told <= kHistory;
+  if (ahead) {
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < told; i += kThreads)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(history + i)), "l"(from + i) : "memory");
+  }
+  // ... and a warp joins a beam's parts.
   for (int b = warp; b < n; b += kWarps) {
     const int64_t r = row0 + b;
     const float2 *const pm = p.part_ms + r * p.parts;
+    const uint64_t *const pk = p.part_keys + r * p.parts * n;
+    const int all = p.parts * n;
+    const float score = a.scores[r];
+    const bool ended = a.finished && a.finished[r];
+    auto key_at = [&](int i) -> uint64_t {
+      return i < all ? __ldcg(reinterpret_cast<const unsigned long long *>(pk + i)) : 0;
+    };
+    const uint64_t k0 = key_at(lane), k1 = key_at(lane + 32);
     float mm = -INFINITY;
     for (int i = lane; i < p.parts; i += 32) mm = fmaxf(mm, __ldcg(pm + i).x);
     mm = warp_max(mm);
@@ -287,39 +366,19 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) zz += __shfl_xor_sync(0xffffffffu, zz, o);
     const bool dead = mm == -INFINITY || zz != zz;
-    const float logz = logf(zz), score = a.scores[r];
-    const bool ended = a.finished && a.finished[r];
-    // ... its lists, one part after the other: n-way insertion of sorted lists.
-    const uint64_t *const pk = p.part_keys + r * p.parts * n;
-    uint64_t l = 0;
-    for (int i0 = 0; i0 < p.parts; i0 += 4) {
-      uint64_t next[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        next[i] = lane < n && i0 + i < p.parts
-                      ? __ldcg(reinterpret_cast<const unsigned long long *>(pk + (i0 + i) * n + lane))
-                      : 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint64_t k = next[i];
-        if (i0 + i >= p.parts) break;
-        // Both sorted, one per lane: an entry's place is its own index plus
-        // the number of larger entries of the other list.
-        int pl = lane, pn = lane;
-        for (int j = 0; j < n; ++j) {
-          pl += __shfl_sync(0xffffffffu, k, j) > l;
-          pn += __shfl_sync(0xffffffffu, l, j) > k;
-        }
-        uint64_t *const mine_s = keys + warp * n;
-        const int have = __popc(__ballot_sync(0xffffffffu, l != 0)) + __popc(__ballot_sync(0xffffffffu, k != 0));
-        __syncwarp();
-        if (lane < n && l != 0 && pl < n) mine_s[pl] = l;
-        if (lane < n && k != 0 && pn < n) mine_s[pn] = k;
-        __syncwarp();
-        l = lane < n && lane < have ? mine_s[lane] : 0;
-      }
+    const float logz = logf(zz);
+    list[lane] = k0;
+    list[lane + 32] = k1;
+    count = rank_keys(list, all < kGather ? all : kGather, n, &floor);
+    for (int i = kGather; i < all; i += 32) {
+      const uint64_t k = key_at(i + lane);
+      const uint32_t who = __ballot_sync(0xffffffffu, k > floor);
+      if (who == 0) continue;
+      if (k > floor) list[n + __popc(who & ((1u << lane) - 1))] = k;
+      count = rank_keys(list, n + __popc(who), n, &floor);
     }
     if (lane < n) {
+      const uint64_t l = list[lane];
       float t = -INFINITY;
       int token = lane;
       if (ended) {
@@ -333,20 +392,29 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p) {
       tot[b * n + lane] = t;
       tok[b * n + lane] = token;
     }
+    __syncwarp();
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  // ... and all threads find each offer's place among the clip's.
+  // Then all threads find each offer's place among the clip's.
   for (int i = threadIdx.x; i < n * n; i += kThreads) {
     const int b = i / n, c = i % n;
     if (c >= places) continue;
     const float t = tot[i];
     int place = 0;
-    for (int j = 0; j < n && place < n; ++j) {
-      // Beam j's list is sorted: count what goes in front.
-      for (int k = 0; k < places; ++k) {
-        const float u = tot[j * n + k];
-        if (!(u > t || (u == t && j * n + k < i))) break;
-        ++place;
+    if (n <= 8 && places == n) {
+      for (int j = 0; j < n * n; ++j) {
+        const float u = tot[j];
+        place += u > t || (u == t && j < i);
+      }
+    } else {
+      for (int j = 0; j < n && place < n; ++j) {
+        // Beam j's list is sorted: count what goes in front.
+        for (int k = 0; k < places; ++k) {
+          const float u = tot[j * n + k];
+          if (!(u > t || (u == t && j * n + k < i))) break;
+          ++place;
+        }
       }
     }
     if (place < n) {
@@ -360,25 +428,13 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p) {
       tokens[place] = tok[i];
     }
   }
-  if (!a.history) return;
+  if (told == 0) return;
   __syncthreads();
-  const uint32_t width = static_cast<uint32_t>(a.width), all = n * width;
-  const int32_t *const from = a.history + row0 * a.width;
-  int32_t *const to = a.out_history + row0 * a.width;
-  for (uint32_t i0 = threadIdx.x; i0 < all; i0 += 8 * kThreads) {
-    int32_t t[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const uint32_t i = i0 + u * kThreads;
-      if (i >= all) continue;
-      const uint32_t b = i / width, c = i - b * width;
-      t[u] = c == a.length ? tokens[b] : __ldg(from + parents[b] * static_cast<int64_t>(width) + c);
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const uint32_t i = i0 + u * kThreads;
-      if (i < all) to[i] = t[u];
-    }
+#pragma unroll 1
+  for (uint32_t i = threadIdx.x; i < told; i += kThreads) {
+    const uint32_t b = i / width, c = i - b * width;
+    const int64_t at = parents[b] * static_cast<int64_t>(width) + c;
+    to[i] = c == a.length ? tokens[b] : ahead ? history[at] : __ldg(from + at);
   }
 }
 
@@ -396,17 +452,34 @@ lm_status check(const lm_beam_args *a) {
   return LM_OK;
 }
 
-// Parts of a row: eight warp tiles each.
-int64_t parts_of(const lm_beam_args &a) {
-  const int64_t n = kWarps * kTileVecs * (a.dtype == LM_F32 ? 4 : 8);
-  return (a.vocab + n - 1) / n;
+// How rows are cut: vectors of a lane (8, or 2 where that leaves SMs without a
+// CTA), CTAs of a row, and tiles that each of their warps goes over: as many as
+// leave the device one round of CTAs (four an SM).
+struct Cut {
+  int vecs, parts, tiles;
+};
+
+Cut cut(const lm_beam_args &a) {
+  const int64_t rows = a.clips * a.beams, values = kWarps * 32 * (a.dtype == LM_F32 ? 4 : 8);
+  Cut c;
+  const int64_t big = (a.vocab + 8 * values - 1) / (8 * values);
+  c.vecs = rows * big < 152 ? 2 : 8;
+  const int64_t all = (a.vocab + c.vecs * values - 1) / (c.vecs * values);
+  const int64_t parts = c.vecs == 2 ? all : 4 * 152 / rows > 1 ? 4 * 152 / rows : 1;
+  c.tiles = static_cast<int>(parts < all ? (all + parts - 1) / parts : 1);
+  c.parts = static_cast<int>((all + c.tiles - 1) / c.tiles);
+  return c;
 }
 
 template <typename T>
-lm_status launch(const BeamParams &p, cudaStream_t s) {
+lm_status launch(const BeamParams &p, int vecs, cudaStream_t s) {
   const int64_t ctas = p.a.clips * p.a.beams * p.parts;
   if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
-  beam_kernel<T><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(p);
+  if (vecs == 2) {
+    beam_kernel<T, 2><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(p);
+  } else {
+    beam_kernel<T, 8><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(p);
+  }
   LM_CUDA_TRY(cudaGetLastError());
   return LM_OK;
 }
@@ -418,8 +491,12 @@ extern "C" lm_status lm_beam_step_workspace_size(const lm_beam_args *args, size_
   using namespace lm;
   if (!bytes) return LM_ERR_INVALID_ARG;
   if (lm_status st = check(args); st != LM_OK) return st;
+  if (args->clips == 0) {
+    *bytes = 256;
+    return LM_OK;
+  }
   const size_t clips = static_cast<size_t>(args->clips < kClips ? args->clips : kClips);
-  *bytes = 256 + kCounterBytes + clips * args->beams * parts_of(*args) * (sizeof(float2) + 8 * args->beams);
+  *bytes = 256 + kCounterBytes + clips * args->beams * cut(*args).parts * (sizeof(float2) + 8 * args->beams);
   return LM_OK;
 }
 
@@ -439,7 +516,9 @@ extern "C" lm_status lm_beam_step(const lm_beam_args *args, void *workspace, siz
       !aligned(a.out_history, 4) || !aligned(workspace, 16))
     return LM_ERR_MISALIGNED;
   if (!workspace || workspace_bytes < need) return LM_ERR_WORKSPACE;
-  p.parts = static_cast<int32_t>(parts_of(a));
+  const Cut c = cut(a);  // of all clips, also where they take several launches
+  p.parts = c.parts;
+  p.tiles = c.tiles;
   char *const w = static_cast<char *>(workspace);
   p.done = reinterpret_cast<uint32_t *>(w + 256);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -460,9 +539,9 @@ extern "C" lm_status lm_beam_step(const lm_beam_args *args, void *workspace, siz
     a.out_history = args->out_history ? args->out_history + skip * a.width : nullptr;
     lm_status st;
     switch (a.dtype) {
-      case LM_F32: st = launch<float>(p, s); break;
-      case LM_F16: st = launch<__half>(p, s); break;
-      default: st = launch<__nv_bfloat16>(p, s); break;
+      case LM_F32: st = launch<float>(p, c.vecs, s); break;
+      case LM_F16: st = launch<__half>(p, c.vecs, s); break;
+      default: st = launch<__nv_bfloat16>(p, c.vecs, s); break;
     }
     if (st != LM_OK) return st;
   }

@@ -28,6 +28,7 @@
 #include <climits>
 #include <type_traits>
 
+#include "f32x2.cuh"
 #include "half.cuh"
 #include "internal.h"
 #include "kv_cache.cuh"
@@ -81,12 +82,6 @@ struct Shared {
 constexpr int big_bytes(int d, int mt, bool shared) {
   const int ring = (shared ? 1 : kWarps) * ring_stages(d, shared) * stage_bytes(d), joined = kWarps * 16 * mt * d * 4;
   return ring > joined ? ring : joined;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 __device__ __forceinline__ uint4 lds_v4(uint32_t a) {

@@ -235,7 +235,11 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
   // it.  (Bytes turn into f16 in two instructions, into bf16 in three.)
   uint32_t q[MT][KW][4];
   int limit[MT][E];
-  float back[MT][E];  // the power's inverse, times scale and log2 e
+  // Key bytes go in as (k + 128) * 2^-24, which takes half the instructions of
+  // k: a score is product * 2^24 - 128 * (sum of q).  (The sums are in 32 bits;
+  // 128 sum q is of the size of the largest scores the block's scale allows.)
+  float back[MT][E];  // the power's inverse, times scale, log2 e and 2^24
+  float bias[MT][E];  // 128 * 2^-24 * sum of q
   const float log2e = 1.4426950408889634f;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
         for (int j = 0; j < 2 * KW; ++j)
           w[j] = s16[2 * j] | static_cast<uint32_t>(s16[2 * j + 1]) << 16;
       }
-      back[m][e] = p.scale * log2e;
+      back[m][e] = p.scale * log2e * 16777216.0f;
       if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
         uint32_t top = 0;  // |q| as integers
 #pragma unroll
@@ -283,6 +287,15 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
           w[j] = pack2<__half>(f.x * up, f.y * up);
         }
       }
+      float total_q = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2 * KW; ++j) {
+        const float2 f = unpack2<__half>(w[j]);
+        total_q += f.x + f.y;
+      }
+      total_q += __shfl_xor_sync(0xffffffffu, total_q, 1);
+      total_q += __shfl_xor_sync(0xffffffffu, total_q, 2);
+      bias[m][e] = total_q * (128.0f / 16777216.0f);
 #pragma unroll
       for (int s = 0; s < KW; ++s) {
         q[m][s][e] = w[2 * s];
@@ -343,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
       for (int m = 0; m < MT; ++m) sc[m][n8][0] = sc[m][n8][1] = sc[m][n8][2] = sc[m][n8][3] = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < KW; ++ks) {
-        const uint32_t b0 = bytes_to_f16(__byte_perm(w[ks], 0, 0x4140)), b1 = bytes_to_f16(__byte_perm(w[ks], 0, 0x4342));
+        uint32_t b0, b1;
+        bytes_to_subnormal(w[ks], b0, b1);
 #pragma unroll
         for (int m = 0; m < MT; ++m) mma16816(sc[m][n8], q[m][ks], b0, b1);
       }
@@ -358,11 +372,12 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float g0 = f0 * back[m][e], g1 = f1 * back[m][e];
+        const float h0 = fmaf(-g0, bias[m][e], l0), h1 = fmaf(-g1, bias[m][e], l1);
 #pragma unroll
         for (int n8 = 0; n8 < 4; ++n8) {
 #pragma unroll
           for (int x = 2 * e; x < 2 * e + 2; ++x)
-            sc[m][n8][x] = fmaf(sc[m][n8][x], n8 < 2 ? g0 : g1, n8 < 2 ? l0 : l1);
+            sc[m][n8][x] = fmaf(sc[m][n8][x], n8 < 2 ? g0 : g1, n8 < 2 ? h0 : h1);
         }
         cut = cut || t0 > limit[m][e] - kTok;
       }

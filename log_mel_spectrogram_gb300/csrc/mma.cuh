@@ -30,4 +30,13 @@ __device__ __forceinline__ uint32_t bytes_to_f16(uint32_t u) {
   return *reinterpret_cast<const uint32_t *>(&d);
 }
 
+// The bytes of `w` (sign bits flipped: b + 128) as two pairs of f16, (b + 128) *
+// 2^-24 each: a byte in the low bits of an f16 is that subnormal number, which
+// products take exactly.
+__device__ __forceinline__ void bytes_to_subnormal(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  const uint32_t x = w ^ 0x80808080u;
+  lo = __byte_perm(x, 0, 0x4140);
+  hi = __byte_perm(x, 0, 0x4342);
+}
+
 }  // namespace lm

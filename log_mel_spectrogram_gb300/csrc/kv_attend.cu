@@ -126,7 +126,7 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
 // eight query rows, so that the lower half of a product's rows is left out of
 // the softmax (55 of 400 instructions a tile).
 template <typename T, int D, int MT, int E, bool SHARED>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) attend_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? resident_ctas(D) : 2) attend_kernel(const AttendParams p) {
   constexpr int STAGES = ring_stages(D, SHARED);
   constexpr int KW = D / 16;   // 32-bit words of a token's key per thread; also 16-element steps of k
   constexpr int VB = D / 8;    // bytes of a token's value per thread; also 8-column tiles of the output
@@ -136,35 +136,60 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
   Shared<R> &sh = *reinterpret_cast<Shared<R> *>(smem + big_bytes(D, MT, SHARED));
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r8 = lane / 4, c4 = lane % 4;
-  int u = blockIdx.x;
-  const int split = u % p.splits;
-  u /= p.splits;
-  const int unit = u;
-  // Later queries see more: their tiles go first.
-  const int h = u % p.c.heads;
-  u /= p.c.heads;
-  const int row = u % p.c.rows;
-  const int qt = p.qtiles - 1 - u / p.c.rows;
+  // Grid: (key heads and parts, row, tile of queries).  Later queries see more:
+  // their tiles go first.
+  const int split = p.splits > 1 ? static_cast<int>(blockIdx.x) / p.c.heads : 0;
+  const int h = static_cast<int>(blockIdx.x) - split * p.c.heads;
+  const int row = blockIdx.y;
+  const int qt = p.qtiles - 1 - static_cast<int>(blockIdx.z);
+  const int64_t unit = (static_cast<int64_t>(blockIdx.z) * p.c.rows + row) * p.c.heads + h;
 
-  // How far this tile of queries sees.
-  const int cap = p.c.width * p.c.block;
-  const int held = min(max(p.c.lens[row], 0), cap);
-  int fresh = max(p.counts ? p.counts[row] : p.new_tokens, 0);
-  if (p.causal) fresh = min(fresh, p.tokens);
-  const int total = static_cast<int>(min(static_cast<int64_t>(held) + fresh, static_cast<int64_t>(cap)));
-  const int q_first = qt * QT, q_rows = min(QT, p.qrows - q_first);
-  int end = total;
-  if (p.causal) {
-    const int i_first = q_first / p.group, i_last = min((q_first + q_rows - 1) / p.group, fresh - 1);
-    end = i_first < fresh ? min(total, held + i_last + 1) : 0;
+  // What no other load has to wait for goes out first: lengths, queries and,
+  // for the first part of a row (the only one, mostly), its blocks.
+  const int block_shift = 31 - __clz(p.c.block);
+  const int32_t *const table = p.c.table + static_cast<int64_t>(row) * p.c.width;
+  const int held_ = p.c.lens[row];
+  const int fresh_ = p.counts ? p.counts[row] : p.new_tokens;
+  int early[2] = {-1, -1};
+  if (split == 0 && p.c.width > 0) {
+    const int t = (SHARED ? lane : lane * kWarps + warp) * kTok;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) early[e] = __ldg(table + min((t + 16 * e) >> block_shift, p.c.width - 1));
   }
-  // Equal parts of whole CTA strides; a part that would be empty has no CTA.
-  int chunk = ((end + p.splits - 1) / p.splits + kWarps * kTok - 1) / (kWarps * kTok) * (kWarps * kTok);
-  chunk = max(chunk, p.min_chunk);
-  const int parts = max((end + chunk - 1) / chunk, 1);
-  if (split >= parts) return;
-  const int begin = split * chunk, stop = min(end, begin + chunk);
-
+  const int q_first = qt * QT, q_rows = min(QT, p.qrows - q_first);
+  uint32_t raw[MT][E][2 * KW];
+  int q_i[MT][E];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int at = q_first + (SHARED ? warp * R : 0) + 16 * m + 8 * e + r8;
+      const bool in = at < p.qrows;
+      const int i = !in ? 0 : p.group == 1 ? at : at / p.group, g = in ? at - i * p.group : 0;
+      q_i[m][e] = in ? i : -1;
+      const T *const src = static_cast<const T *>(p.q) + row * p.row_s + i * p.tok_s +
+                           (static_cast<int64_t>(h) * p.group + g) * p.head_s + c4 * (D / 4);
+      uint32_t *const w = raw[m][e];
+      if (!in) {
+#pragma unroll
+        for (int j = 0; j < 2 * KW; ++j) w[j] = 0;
+      } else if (p.qvec) {
+#pragma unroll
+        for (int j = 0; j < 2 * KW; j += 4) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + 2 * j));
+          w[j] = v.x;
+          w[j + 1] = v.y;
+          w[j + 2] = v.z;
+          w[j + 3] = v.w;
+        }
+      } else {
+        const uint16_t *const s16 = reinterpret_cast<const uint16_t *>(src);
+#pragma unroll
+        for (int j = 0; j < 2 * KW; ++j)
+          w[j] = s16[2 * j] | static_cast<uint32_t>(s16[2 * j + 1]) << 16;
+      }
+    }
+  }
   if (threadIdx.x < kWarps)
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&sh.full[threadIdx.x][i], 1);
@@ -174,11 +199,30 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
   fence_mbar_init();
   __syncthreads();
 
+  // How far this tile of queries sees.
+  const int cap = p.c.width * p.c.block;
+  const int held = min(max(held_, 0), cap);
+  int fresh = max(fresh_, 0);
+  if (p.causal) fresh = min(fresh, p.tokens);
+  const int total = static_cast<int>(min(static_cast<int64_t>(held) + fresh, static_cast<int64_t>(cap)));
+  int end = total;
+  if (p.causal) {
+    const int i_first = q_first / p.group, i_last = min((q_first + q_rows - 1) / p.group, fresh - 1);
+    end = i_first < fresh ? min(total, held + i_last + 1) : 0;
+  }
+  // Equal parts of whole CTA strides; a part that would be empty has no CTA.
+  int chunk = end, parts = 1;
+  if (p.splits > 1) {
+    chunk = ((end + p.splits - 1) / p.splits + kWarps * kTok - 1) / (kWarps * kTok) * (kWarps * kTok);
+    chunk = max(chunk, p.min_chunk);
+    parts = max((end + chunk - 1) / chunk, 1);
+  }
+  if (split >= parts) return;
+  const int begin = split * chunk, stop = min(end, begin + chunk);
+
   uint8_t *const ring = smem + (SHARED ? 0 : warp * STAGES * stage_bytes(D));
   const uint32_t ring_a = smem_u32(ring);
   uint64_t *const full = sh.full[SHARED ? 0 : warp];
-  const int block_shift = 31 - __clz(p.c.block);
-  const int32_t *const table = p.c.table + static_cast<int64_t>(row) * p.c.width;
   const int64_t tiles0 = p.c.layer_tiles + h;
   // This warp's tiles: number j starts at token begin + (j * kWarps + warp) * kTok
   // (SHARED: begin + j * kTok).
@@ -189,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
   auto block_of = [&](int j, int half) {
     const int t = token_of(j) + 16 * half;
     if (j >= mine || t >= stop) return -1;
-    const int b = __ldg(table + (t >> block_shift));
+    const int b = j < 32 && split == 0 ? early[half] : __ldg(table + (t >> block_shift));
     return b >= 0 && b < p.c.blocks ? b : -1;
   };
   int fb0 = -1, fb1 = -1;  // blocks of the 32 tiles that are fetched next, one per lane
@@ -245,31 +289,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
   for (int m = 0; m < MT; ++m) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int at = q_first + (SHARED ? warp * R : 0) + 16 * m + 8 * e + r8;
-      const bool in = at < p.qrows;
-      const int i = in ? at / p.group : 0, g = in ? at % p.group : 0;
-      limit[m][e] = !in ? INT_MAX : !p.causal ? total : i < fresh ? min(total, held + i + 1) : 0;
-      const T *const src = static_cast<const T *>(p.q) + row * p.row_s + i * p.tok_s +
-                           (static_cast<int64_t>(h) * p.group + g) * p.head_s + c4 * (D / 4);
-      uint32_t w[2 * KW];
-      if (!in) {
-#pragma unroll
-        for (int j = 0; j < 2 * KW; ++j) w[j] = 0;
-      } else if (p.qvec) {
-#pragma unroll
-        for (int j = 0; j < 2 * KW; j += 4) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(src + 2 * j);
-          w[j] = v.x;
-          w[j + 1] = v.y;
-          w[j + 2] = v.z;
-          w[j + 3] = v.w;
-        }
-      } else {
-        const uint16_t *const s16 = reinterpret_cast<const uint16_t *>(src);
-#pragma unroll
-        for (int j = 0; j < 2 * KW; ++j)
-          w[j] = s16[2 * j] | static_cast<uint32_t>(s16[2 * j + 1]) << 16;
-      }
+      const int i = q_i[m][e];
+      limit[m][e] = i < 0 ? INT_MAX : !p.causal ? total : i < fresh ? min(total, held + i + 1) : 0;
+      uint32_t *const w = raw[m][e];
       back[m][e] = p.scale * log2e * 16777216.0f;
       if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
         uint32_t top = 0;  // |q| as integers
@@ -508,10 +530,10 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
     }
   }
   __syncthreads();
-  const int64_t part0 = (static_cast<int64_t>(unit) * p.splits + split) * p.part_rows;
+  const int64_t part0 = (unit * p.splits + split) * p.part_rows;
   constexpr int PER = D / 4;  // 4-element vectors of a row
   auto emit = [&](int rr, int d, float4 v, float l) {
-    const int at = q_first + rr, i = at / p.group, g = at % p.group;
+    const int at = q_first + rr, i = p.group == 1 ? at : at / p.group, g = at - i * p.group;
     const float f = l == 0.0f ? 0.0f : 1.0f / l;
     T *const o = static_cast<T *>(p.out) +
                  ((static_cast<int64_t>(row) * p.tokens + i) * p.q_heads + h * p.group + g) * D + d;
@@ -555,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? resident_ctas(D) : 2) atte
   if (!sh.last) return;
   __threadfence();
   if (threadIdx.x == 0) p.done[unit] = 0;
-  const int64_t unit0 = static_cast<int64_t>(unit) * p.splits * p.part_rows;
+  const int64_t unit0 = unit * p.splits * p.part_rows;
   for (int x = threadIdx.x; x < q_rows * PER; x += kThreads) {
     const int rr = x / PER, d = x % PER * 4;
     float t = -INFINITY;
@@ -625,28 +647,28 @@ Cut cut(const lm_kv_cache *c, int32_t tokens, int32_t q_heads) {
 }
 
 template <typename T, int D, int MT, int E, bool SHARED>
-lm_status launch(const AttendParams &p, int64_t ctas, cudaStream_t s) {
+lm_status launch(const AttendParams &p, dim3 grid, cudaStream_t s) {
   auto *const kernel = attend_kernel<T, D, MT, E, SHARED>;
   constexpr int smem = big_bytes(D, MT, SHARED) + static_cast<int>(sizeof(Shared<16 * MT>));
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
-  kernel<<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(p);
+  kernel<<<grid, kThreads, smem, s>>>(p);
   LM_CUDA_TRY(cudaGetLastError());
   return LM_OK;
 }
 
 template <typename T, int D>
-lm_status launch_form(const AttendParams &p, const Cut &k, int64_t ctas, cudaStream_t s) {
-  if (k.shared) return launch<T, D, 1, 2, true>(p, ctas, s);
-  if (k.qrows <= 8) return launch<T, D, 1, 1, false>(p, ctas, s);
-  return k.mt == 1 ? launch<T, D, 1, 2, false>(p, ctas, s) : launch<T, D, 2, 2, false>(p, ctas, s);
+lm_status launch_form(const AttendParams &p, const Cut &k, dim3 grid, cudaStream_t s) {
+  if (k.shared) return launch<T, D, 1, 2, true>(p, grid, s);
+  if (k.qrows <= 8) return launch<T, D, 1, 1, false>(p, grid, s);
+  return k.mt == 1 ? launch<T, D, 1, 2, false>(p, grid, s) : launch<T, D, 2, 2, false>(p, grid, s);
 }
 
 template <typename T>
-lm_status launch_dim(const AttendParams &p, const Cut &k, int64_t ctas, cudaStream_t s) {
+lm_status launch_dim(const AttendParams &p, const Cut &k, dim3 grid, cudaStream_t s) {
   switch (p.c.head_dim) {
-    case 32: return launch_form<T, 32>(p, k, ctas, s);
-    case 64: return launch_form<T, 64>(p, k, ctas, s);
-    default: return launch_form<T, 128>(p, k, ctas, s);
+    case 32: return launch_form<T, 32>(p, k, grid, s);
+    case 64: return launch_form<T, 64>(p, k, grid, s);
+    default: return launch_form<T, 128>(p, k, grid, s);
   }
 }
 
@@ -677,8 +699,9 @@ extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const
   if (!aligned(q, 2) || !aligned(out, 16) || !aligned(workspace, 16)) return LM_ERR_MISALIGNED;
   const Cut k = cut(cache, tokens, q_heads);
   if (!workspace || workspace_bytes < 256 + k.done_bytes + k.ml_bytes + k.acc_bytes) return LM_ERR_WORKSPACE;
-  const int64_t ctas = k.units * k.splits;
-  if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
+  if (cache->rows > 65535 || k.qtiles > 65535 || static_cast<int64_t>(cache->heads) * k.splits > INT_MAX)
+    return LM_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(cache->heads) * k.splits, cache->rows, k.qtiles);
   char *const w = static_cast<char *>(workspace);
   AttendParams p;
   p.c = kv_view(cache, layer);
@@ -705,5 +728,5 @@ extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const
   p.qvec = aligned(q, 16) && q_strides[0] % 8 == 0 && q_strides[1] % 8 == 0 && q_strides[2] % 8 == 0;
   p.scale = scale;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return dtype == LM_F16 ? launch_dim<__half>(p, k, ctas, s) : launch_dim<__nv_bfloat16>(p, k, ctas, s);
+  return dtype == LM_F16 ? launch_dim<__half>(p, k, grid, s) : launch_dim<__nv_bfloat16>(p, k, grid, s);
 }

@@ -182,6 +182,8 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p) {
   __shared__ int parents[kMaxBeams], tokens[kMaxBeams];
   __shared__ int32_t history[kHistory];
   __shared__ bool last;
+  pdl_launch();
+  pdl_wait();
   const lm_beam_args &a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int part = blockIdx.x % p.parts;
@@ -475,13 +477,8 @@ template <typename T>
 lm_status launch(const BeamParams &p, int vecs, cudaStream_t s) {
   const int64_t ctas = p.a.clips * p.a.beams * p.parts;
   if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
-  if (vecs == 2) {
-    beam_kernel<T, 2><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(p);
-  } else {
-    beam_kernel<T, 8><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(p);
-  }
-  LM_CUDA_TRY(cudaGetLastError());
-  return LM_OK;
+  return launch_dependent(vecs == 2 ? beam_kernel<T, 2> : beam_kernel<T, 8>, dim3(static_cast<unsigned>(ctas)),
+                          kThreads, 0, s, 1, p);
 }
 
 }  // namespace

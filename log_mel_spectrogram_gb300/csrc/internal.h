@@ -34,6 +34,33 @@ lm_status cuda_fail(cudaError_t e);
 // Sets a kernel's dynamic shared memory limit once per (kernel, device).
 lm_status ensure_smem_attribute(const void *kernel, int bytes);
 
+// Launches `kernel` as a programmatic dependent of what precedes it on the
+// stream: its CTAs may start, and set up their shared memory, while the grid
+// before is still running; the kernel calls pdl_wait() before its first access
+// to global memory, and pdl_launch() to let the next grid do the same.
+template <typename... P, typename... A>
+lm_status launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                           A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  LM_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...));
+  return LM_OK;
+}
+
 // Every workspace starts with a 16-byte header whose first u32 is the
 // device error word (bit flags set by kernels whose bounded waits ran out).
 constexpr size_t kWorkspaceHeaderBytes = 16;

@@ -144,6 +144,16 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
   const int qt = p.qtiles - 1 - static_cast<int>(blockIdx.z);
   const int64_t unit = (static_cast<int64_t>(blockIdx.z) * p.c.rows + row) * p.c.heads + h;
 
+  if (threadIdx.x < kWarps)
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&sh.full[threadIdx.x][i], 1);
+      if (threadIdx.x == 0) mbar_init(&sh.empty[i], kWarps);
+    }
+  if (threadIdx.x == 0) sh.abort = 0;
+  fence_mbar_init();
+  pdl_launch();
+  pdl_wait();
+
   // What no other load has to wait for goes out first: lengths, queries and,
   // for the first part of a row (the only one, mostly), its blocks.
   const int block_shift = 31 - __clz(p.c.block);
@@ -190,13 +200,6 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
       }
     }
   }
-  if (threadIdx.x < kWarps)
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&sh.full[threadIdx.x][i], 1);
-      if (threadIdx.x == 0) mbar_init(&sh.empty[i], kWarps);
-    }
-  if (threadIdx.x == 0) sh.abort = 0;
-  fence_mbar_init();
   __syncthreads();
 
   // How far this tile of queries sees.
@@ -651,9 +654,7 @@ lm_status launch(const AttendParams &p, dim3 grid, cudaStream_t s) {
   auto *const kernel = attend_kernel<T, D, MT, E, SHARED>;
   constexpr int smem = big_bytes(D, MT, SHARED) + static_cast<int>(sizeof(Shared<16 * MT>));
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
-  kernel<<<grid, kThreads, smem, s>>>(p);
-  LM_CUDA_TRY(cudaGetLastError());
-  return LM_OK;
+  return launch_dependent(kernel, grid, kThreads, smem, s, 1, p);
 }
 
 template <typename T, int D>

@@ -102,6 +102,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
   constexpr int NT = BS * D / 64;
   constexpr int PER = kThreads / NT;  // units per CTA
   __shared__ float part[kThreads / 32];
+  pdl_launch();
+  pdl_wait();
   const int tid = threadIdx.x % NT;
   const uint32_t unit = blockIdx.x * PER + threadIdx.x / NT;
   const int which = blockIdx.y;
@@ -239,6 +241,8 @@ struct ReadParams {
 // Grid: (part of a row's vectors, row, layer and keys or values).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
+  pdl_launch();
+  pdl_wait();
   const int which = blockIdx.z & 1, r = blockIdx.y;
   const int64_t layer = blockIdx.z >> 1;
   const int32_t *const table = p.c.table + static_cast<int64_t>(r) * p.c.width;
@@ -301,6 +305,8 @@ __device__ __forceinline__ int parent_row(const ReorderParams &p, int r) {
 // The tables still show the old state meanwhile; the last CTA of a clip to
 // finish then rewrites them.
 __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p) {
+  pdl_launch();
+  pdl_wait();
   const int r = blockIdx.y;
   const int clip = r / p.beams;
   const int64_t width = p.c.width;
@@ -311,22 +317,22 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
   if (open && from_row != r) {
     const int from = p.c.table[from_row * width + col], to = p.c.spare[r];
     if (from >= 0 && from < p.c.blocks && to >= 0 && to < p.c.blocks) {
-      // 16-byte vectors of a block's keys or values over all heads, per layer.
-      const uint32_t vecs = static_cast<uint32_t>(p.c.heads) * p.c.block * p.c.head_dim / 16;
-      const uint32_t all = vecs * p.c.layers;
-      // Only the tokens that are held: a head's first `used` vectors.
-      const int head_vecs = p.c.block * p.c.head_dim / 16, used = len % p.c.block * p.c.head_dim / 16;
+      // The tokens that are held: a head's first `used` 16-byte vectors.
+      const uint32_t head_vecs = p.c.block * p.c.head_dim / 16, used = len % p.c.block * p.c.head_dim / 16;
+      const uint32_t vecs = p.c.heads * used, all = vecs * p.c.layers;
       for (uint32_t i0 = blockIdx.x * kThreads + threadIdx.x; i0 < all; i0 += kCopy * gridDim.x * kThreads) {
         uint4 x[kCopy][2];
         int64_t at[kCopy];
 #pragma unroll
         for (int u = 0; u < kCopy; ++u) {
           const uint32_t i = i0 + u * gridDim.x * kThreads;
-          const uint32_t layer = i / vecs, v = i - layer * vecs;
           at[u] = -1;
-          if (i >= all || static_cast<int>(v & (head_vecs - 1)) >= used) continue;
-          const int64_t a = (static_cast<int64_t>(layer) * p.c.blocks + from) * vecs + v;
-          at[u] = (static_cast<int64_t>(layer) * p.c.blocks + to) * vecs + v;
+          if (i >= all) continue;
+          const uint32_t tile = i / used, v = i - tile * used;  // (layer, head) and its vector
+          const uint32_t layer = tile / p.c.heads, head = tile - layer * p.c.heads;
+          const int64_t first = static_cast<int64_t>(layer) * p.c.blocks;
+          const int64_t a = ((first + from) * p.c.heads + head) * head_vecs + v;
+          at[u] = ((first + to) * p.c.heads + head) * head_vecs + v;
           x[u][0] = reinterpret_cast<const uint4 *>(p.c.k8)[a];
           x[u][1] = reinterpret_cast<const uint4 *>(p.c.v8)[a];
         }
@@ -382,13 +388,11 @@ lm_status append_block(const AppendParams &p, int block, cudaStream_t s) {
   const int per = kThreads / nt;
   const dim3 grid((p.units + per - 1) / per, 2);
   switch (block) {
-    case 16: append_kernel<T, D, 16><<<grid, kThreads, 0, s>>>(p); break;
-    case 32: append_kernel<T, D, 32><<<grid, kThreads, 0, s>>>(p); break;
-    case 64: append_kernel<T, D, 64><<<grid, kThreads, 0, s>>>(p); break;
-    default: append_kernel<T, D, 128><<<grid, kThreads, 0, s>>>(p); break;
+    case 16: return launch_dependent(append_kernel<T, D, 16>, grid, kThreads, 0, s, 1, p);
+    case 32: return launch_dependent(append_kernel<T, D, 32>, grid, kThreads, 0, s, 1, p);
+    case 64: return launch_dependent(append_kernel<T, D, 64>, grid, kThreads, 0, s, 1, p);
+    default: return launch_dependent(append_kernel<T, D, 128>, grid, kThreads, 0, s, 1, p);
   }
-  LM_CUDA_TRY(cudaGetLastError());
-  return LM_OK;
 }
 
 template <typename T>
@@ -503,13 +507,8 @@ extern "C" lm_status lm_kv_read(const lm_kv_cache *cache, int32_t layer, int32_t
   p.vecs = static_cast<uint32_t>(vecs);
   const dim3 grid((p.vecs + kThreads * kReadVecs - 1) / (kThreads * kReadVecs), cache->rows, 2 * layers);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == LM_F16) {
-    read_kernel<__half><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    read_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-  }
-  LM_CUDA_TRY(cudaGetLastError());
-  return LM_OK;
+  return dtype == LM_F16 ? launch_dependent(read_kernel<__half>, grid, kThreads, 0, s, 1, p)
+                         : launch_dependent(read_kernel<__nv_bfloat16>, grid, kThreads, 0, s, 1, p);
 }
 
 extern "C" lm_status lm_kv_reorder(const lm_kv_cache *cache, const int32_t *parents, int32_t beams, void *workspace,
@@ -535,7 +534,6 @@ extern "C" lm_status lm_kv_reorder(const lm_kv_cache *cache, const int32_t *pare
   int64_t parts = (vecs + kCopy * kThreads - 1) / (kCopy * kThreads);
   if (parts * cache->rows < 152) parts = (vecs + kThreads - 1) / kThreads;
   p.parts = static_cast<int32_t>(parts < 256 ? parts : 256);
-  reorder_kernel<<<dim3(p.parts, cache->rows), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  LM_CUDA_TRY(cudaGetLastError());
-  return LM_OK;
+  return launch_dependent(reorder_kernel, dim3(p.parts, cache->rows), kThreads, 0, reinterpret_cast<cudaStream_t>(stream),
+                          1, p);
 }

@@ -420,6 +420,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   __syncthreads();
   __syncwarp();
   if (PAIR) cluster_sync_all();  // both CTAs' barriers exist
+  pdl_launch();
+  pdl_wait();
   tcgen05_fence_after();
   const uint32_t tmem = b.tmem;
   volatile int *const abort = &b.abort;
@@ -592,6 +594,8 @@ struct PackParams {
 
 __global__ void __launch_bounds__(256) pack_kernel(const PackParams p) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  pdl_launch();
+  pdl_wait();
   if (i >= p.total) return;
   const int64_t row = i / p.vecs, v = i % p.vecs;
   const uint16_t *const s = p.src + row / p.rows * p.group_stride + row % p.rows * p.row_stride + v * 8;
@@ -675,8 +679,8 @@ lm_status pack(Operand *o, int64_t k, void *dst, cudaStream_t s) {
   p.total = o->groups * o->rows * p.vecs;
   const int64_t ctas = (p.total + 255) / 256;
   if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
-  pack_kernel<<<static_cast<unsigned>(ctas), 256, 0, s>>>(p);
-  LM_CUDA_TRY(cudaGetLastError());
+  if (lm_status st = launch_dependent(pack_kernel, dim3(static_cast<unsigned>(ctas)), 256, 0, s, 1, p); st != LM_OK)
+    return st;
   o->p = dst;
   o->row_stride = p.vecs * 8;
   o->group_stride = o->rows * o->row_stride;
@@ -726,12 +730,22 @@ using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
 
 // Pairs of CTAs that the device holds at once (SMs that have no partner in
 // their group stay out), asked once per device.
-int resident_pairs(Kernel kernel, const cudaLaunchConfig_t &cfg, const DeviceInfo &dev) {
+int resident_pairs(Kernel kernel, int threads, int smem, const DeviceInfo &dev) {
   static std::mutex mu;
   static std::map<int, int> known;
   std::lock_guard<std::mutex> lk(mu);
   const auto it = known.find(dev.device);
   if (it != known.end()) return it->second;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / 2 * 2));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
     (void)cudaGetLastError();
@@ -863,31 +877,15 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
   }
   const Kernel kernel = bf16 ? kernel_of<__nv_bfloat16>(swap, form) : kernel_of<__half>(swap, form);
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(form)));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
   int cluster = 1, grid = p.tiles < dev.sm_count ? p.tiles : dev.sm_count;
   if (form == Form::kSplit) {
     cluster = p.splits;
     grid = p.tiles * p.splits;
   } else if (form == Form::kPair) {
     cluster = 2;
-    grid = 2 * (p.tiles < dev.sm_count / 2 ? p.tiles : dev.sm_count / 2);
+    const int pairs = resident_pairs(kernel, threads_of(form), smem, dev);
+    grid = 2 * (p.tiles < pairs ? p.tiles : pairs);
   }
-  if (cluster > 1) {
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-  }
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  if (form == Form::kPair) {
-    const int pairs = resident_pairs(kernel, cfg, dev);
-    if (grid > 2 * pairs) cfg.gridDim.x = static_cast<unsigned>(2 * pairs);
-  }
-  LM_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, lanes, cols, outs, p));
-  return LM_OK;
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), threads_of(form), static_cast<size_t>(smem), s,
+                          cluster, lanes, cols, outs, p);
 }

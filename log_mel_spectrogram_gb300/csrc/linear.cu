@@ -180,9 +180,37 @@ __device__ __forceinline__ void finish16(const LinearParams &p, const uint32_t (
                                          uint32_t stage, uint32_t stage_at) {
   if (SWAP) {
     if (lane_at >= p.n) return;
+    const int count = min(16, p.rows - col_at);
+    const int64_t row = group_row + col_at;
+    float y[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (col_at + j < p.rows) put<T, ACT>(p, __uint_as_float(r[j]), lane_bias, group_row + col_at + j, lane_at);
+    for (int j = 0; j < 16; j += 2) {
+      const f32x2 z = add2(pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), both(lane_bias));
+      const float2 f = unpair(mul2(both(p.scale), activate2<ACT>(z)));
+      y[j] = f.x;
+      y[j + 1] = f.y;
+    }
+    if (p.residual) {
+      const T *x = static_cast<const T *>(p.residual) + row * p.res_row + lane_at;
+#pragma unroll
+      for (int j = 0; j < 16; ++j, x += p.res_row)
+        if (j < count) y[j] += to_f32(*x);
+    }
+    if (p.out_f32) {
+      float *o = static_cast<float *>(p.out) + row * p.out_row + lane_at;
+#pragma unroll
+      for (int j = 0; j < 16; ++j, o += p.out_row)
+        if (j < count) *o = y[j];
+    } else {
+      T *o = static_cast<T *>(p.out) + row * p.out_row + lane_at;
+      if (count == 16) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j, o += p.out_row) *o = from_f32<T>(y[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j, o += p.out_row)
+          if (j < count) *o = from_f32<T>(y[j]);
+      }
     }
     return;
   }

@@ -1,22 +1,38 @@
 // linear.cu -- y = residual + scale * act(x W^T + bias) on the tensor cores.
 //
-// A CTA computes tiles of 128 x bn outputs: one thread fetches 128 x 64 and
-// bn x 64 operand tiles by TMA into a ring of shared-memory stages, one thread
-// issues tcgen05.mma into tensor memory (32-bit sums), the other warps turn a
-// finished tile into outputs while the next one is summed into the other half
-// of the tensor memory.  CTAs are persistent: one per SM walks the tiles.
+// A CTA computes tiles of 128 outputs (rows of W, along the lanes of tensor
+// memory) by bn rows of x: one warp fetches 128 x 64 and bn x 64 operand tiles
+// by TMA into a ring of shared-memory stages, one warp issues tcgen05.mma into
+// tensor memory (32-bit sums), sixteen turn a finished tile into outputs while
+// the next one is summed into the other half of the tensor memory.  CTAs are
+// persistent: one per SM walks the tiles.
 //
-// The tile has two orientations.
-//  - rows of x along the 128 lanes: a lane holds 16 consecutive outputs of a
-//    row, i.e. whole 32-byte sectors per thread.  Taken where outputs (and the
-//    residual) can be accessed in 16-byte vectors and there are enough rows.
-//  - rows of W along the lanes: x fills the other side of the tile with
-//    exactly the rows there are (bn = 16 .. 256), so few rows do not waste
-//    products, and lanes are consecutive outputs, so odd row lengths still
-//    store whole lines.
-// Few tiles (decoding steps) split k over a cluster of CTAs, whose partial sums
-// meet in distributed shared memory in rank order: one launch, and the same
-// result on every call.
+// With W along the lanes, bn is any multiple of 16 up to 256, so that few rows
+// of x waste no products and the tiles of a medium problem can be cut to fill the
+// SMs once; and the lanes of a warp are consecutive outputs of a row, so that
+// stores are whole, whatever the row length's alignment.  (The other way round,
+// with outputs leaving by TMA, was equal at 24000 x 1024 x 4096 and up to 45%
+// slower between 100 and 6000 rows.)
+//
+// Three forms, chosen with bn by the estimate in best_cut():
+//  - a CTA per tile;
+//  - a pair of CTAs per tile of 256 lanes (cta_group::2): each fetches half of
+//    the rows of x and both use them, a third less traffic from L2, which is
+//    what bounds large problems (8192^3: 1.58 -> 1.79 PFLOP/s);
+//  - a cluster of 2 to 8 CTAs per tile, each with a part of k, for the few tiles
+//    of a decoding step: the partial sums meet in distributed shared memory in
+//    rank order, in the same launch and with the same result on every call.
+//
+// The issuing warps stay converged up to one elected lane: addresses and
+// descriptors then live in uniform registers, which the tensor instructions
+// take.  Issued from one divergent thread, a product of 128 x 256 x 16 took 172
+// to 237 cycles, in competition with the epilogue; now 130.
+//
+// Measured: 24000 x 1024 -> 4096 bf16 with bias and gelu 128 us (1.57 PFLOP/s;
+// bound by the tensor pipe and, at a quarter of it, the epilogue's arithmetic);
+// 320 x 1024 -> 50001 33 us against 20 us of memory traffic; windows of 8 x 3000
+// frames, 240 -> 512 with gelu, 15 us (epilogue); 5 x 1024 -> 1024 4.5 us a call in
+// a row of calls.
 //
 // Operands that TMA cannot address (rows off 16-byte boundaries) are first
 // copied into padded rows in the workspace.
@@ -35,9 +51,10 @@ namespace lm {
 namespace {
 
 constexpr int kBk = 64;             // elements of k per stage: one 128-byte swizzle row
-constexpr int kLanes = 128;         // rows of the tile's lane side
+constexpr int kLanes = 128;         // rows of W of a CTA's tile
 constexpr int kMaxBn = 256;
 constexpr int kMaxStages = 8;
+constexpr int kMaxSplits = 8;
 
 enum class Form {
   kOne,    // a CTA per tile of 128 lanes
@@ -49,20 +66,18 @@ enum class Form {
 // split form's few columns.
 constexpr int epi_warps(Form f) { return f == Form::kSplit ? 8 : 16; }
 constexpr int threads_of(Form f) { return 128 + 32 * epi_warps(f); }
-constexpr int kStageOut = 32 * 32 * 2;  // a warp's 32 rows x 32 columns of 16 bits
 
 struct LinearParams {
   const void *bias, *residual;
   void *out;
   int64_t out_row, res_row;
-  int64_t rows_total;         // rows of the output
-  int32_t rows, k, n;         // rows per group
+  int32_t rows, n;                       // rows of x per group; rows of W
   int32_t bn, stages, kblocks, tmem_cols;
-  int32_t lane_tiles, col_tiles, tiles;  // tiles along the lanes and columns of one group, and in all
-  int32_t lane_step;          // rows along the lanes of a tile: 128, or a pair's 256
-  int32_t splits;             // CTAs that share a tile's k
-  int32_t bias_f32, out_f32, act, vec32;
-  int32_t tma_out, stage_out; // outputs leave by TMA, through that many bytes of shared memory
+  int32_t lane_tiles, col_tiles, tiles;  // of one group, and in all
+  int32_t lane_step;                     // rows of W of a tile: 128, or a pair's 256
+  int32_t lanes_inside;                  // consecutive tiles share x, not W
+  int32_t splits;                        // CTAs that share a tile's k
+  int32_t bias_f32, out_f32, act;
   uint32_t idesc;
   float scale;
   uint32_t *err;
@@ -126,42 +141,13 @@ __device__ __forceinline__ f32x2 activate2(f32x2 z) {
   return pair(activate<ACT>(f.x), activate<ACT>(f.y));
 }
 
-__device__ __forceinline__ uint4 ldg_v4(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
-
-// 16 consecutive 16-bit values as f32, in 16-byte loads.
-template <typename T>
-__device__ __forceinline__ void load16(const T *p, float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 w = ldg_v4(p + 8 * i);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack2<T>(u[j]);
-      x[8 * i + 2 * j] = f.x;
-      x[8 * i + 2 * j + 1] = f.y;
-    }
-  }
-}
-
-__device__ __forceinline__ void store_v8(void *p, const uint32_t (&w)[8], bool vec32) {
-  if (vec32) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
-
 template <typename T>
 __device__ __forceinline__ float bias_at(const LinearParams &p, int n) {
   if (!p.bias || n >= p.n) return 0.0f;
   return p.bias_f32 ? static_cast<const float *>(p.bias)[n] : to_f32(static_cast<const T *>(p.bias)[n]);
 }
 
-// One output element of the lane = W orientation.
+// One output element.
 template <typename T, int ACT>
 __device__ __forceinline__ void put(const LinearParams &p, float acc, float bias, int64_t row, int n) {
   float y = p.scale * activate<ACT>(acc + bias);
@@ -173,118 +159,38 @@ __device__ __forceinline__ void put(const LinearParams &p, float acc, float bias
   }
 }
 
-// The 16 columns in `r` of a lane's tile row.
-template <typename T, int ACT, bool SWAP>
-__device__ __forceinline__ void finish16(const LinearParams &p, const uint32_t (&r)[16], const float *bias_s,
-                                         float lane_bias, int64_t group_row, int lane_at, int col_at,
-                                         uint32_t stage, uint32_t stage_at) {
-  if (SWAP) {
-    if (lane_at >= p.n) return;
-    const int count = min(16, p.rows - col_at);
-    const int64_t row = group_row + col_at;
-    float y[16];
+// Output n of `count` <= 16 rows from `row` on, from the lane's sums r.
+template <typename T, int ACT>
+__device__ __forceinline__ void put16(const LinearParams &p, const uint32_t (&r)[16], float bias, int64_t row, int count,
+                                      int n) {
+  float y[16];
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      const f32x2 z = add2(pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), both(lane_bias));
-      const float2 f = unpair(mul2(both(p.scale), activate2<ACT>(z)));
-      y[j] = f.x;
-      y[j + 1] = f.y;
-    }
-    if (p.residual) {
-      const T *x = static_cast<const T *>(p.residual) + row * p.res_row + lane_at;
+  for (int j = 0; j < 16; j += 2) {
+    const f32x2 z = add2(pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), both(bias));
+    const float2 f = unpair(mul2(both(p.scale), activate2<ACT>(z)));
+    y[j] = f.x;
+    y[j + 1] = f.y;
+  }
+  if (p.residual) {
+    const T *x = static_cast<const T *>(p.residual) + row * p.res_row + n;
 #pragma unroll
-      for (int j = 0; j < 16; ++j, x += p.res_row)
-        if (j < count) y[j] += to_f32(*x);
-    }
-    if (p.out_f32) {
-      float *o = static_cast<float *>(p.out) + row * p.out_row + lane_at;
+    for (int j = 0; j < 16; ++j, x += p.res_row)
+      if (j < count) y[j] += to_f32(*x);
+  }
+  if (p.out_f32) {
+    float *o = static_cast<float *>(p.out) + row * p.out_row + n;
+#pragma unroll
+    for (int j = 0; j < 16; ++j, o += p.out_row)
+      if (j < count) *o = y[j];
+  } else {
+    T *o = static_cast<T *>(p.out) + row * p.out_row + n;
+    if (count == 16) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j, o += p.out_row) *o = from_f32<T>(y[j]);
+    } else {
 #pragma unroll
       for (int j = 0; j < 16; ++j, o += p.out_row)
-        if (j < count) *o = y[j];
-    } else {
-      T *o = static_cast<T *>(p.out) + row * p.out_row + lane_at;
-      if (count == 16) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j, o += p.out_row) *o = from_f32<T>(y[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j, o += p.out_row)
-          if (j < count) *o = from_f32<T>(y[j]);
-      }
-    }
-    return;
-  }
-  if (lane_at >= p.rows || col_at >= p.n) return;
-  const int64_t row = group_row + lane_at;
-  float y[16];
-  const f32x2 scale = both(p.scale);
-#pragma unroll
-  for (int j = 0; j < 16; j += 4) {
-    const float4 v = *reinterpret_cast<const float4 *>(bias_s + j);
-    const f32x2 z0 = add2(pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), pair(v.x, v.y));
-    const f32x2 z1 = add2(pair(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), pair(v.z, v.w));
-    const float2 y0 = unpair(mul2(scale, activate2<ACT>(z0))), y1 = unpair(mul2(scale, activate2<ACT>(z1)));
-    y[j] = y0.x;
-    y[j + 1] = y0.y;
-    y[j + 2] = y1.x;
-    y[j + 3] = y1.y;
-  }
-  if (p.tma_out) {
-    if (p.residual) {
-      if (col_at + 16 <= p.n) {
-        float x[16];
-        load16(static_cast<const T *>(p.residual) + row * p.res_row + col_at, x);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] += x[j];
-      } else {
-        for (int j = 0; j < 16 && col_at + j < p.n; ++j)
-          y[j] += to_f32(static_cast<const T *>(p.residual)[row * p.res_row + col_at + j]);
-      }
-    }
-    // Two 16-byte parts of a 64-byte row, in the 64-byte swizzle.
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t off = stage_at + 16 * i, to = stage + (off ^ ((off >> 3) & 0x30u));
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(pack2<T>(y[8 * i], y[8 * i + 1])),
-                   "r"(pack2<T>(y[8 * i + 2], y[8 * i + 3])), "r"(pack2<T>(y[8 * i + 4], y[8 * i + 5])),
-                   "r"(pack2<T>(y[8 * i + 6], y[8 * i + 7]))
-                   : "memory");
-    }
-    return;
-  }
-  if (col_at + 16 <= p.n) {
-    if (p.residual) {
-      float x[16];
-      load16(static_cast<const T *>(p.residual) + row * p.res_row + col_at, x);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) y[j] += x[j];
-    }
-    if (p.out_f32) {
-      float *const o = static_cast<float *>(p.out) + row * p.out_row + col_at;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(y[8 * i + j]);
-        store_v8(o + 8 * i, w, p.vec32);
-      }
-    } else {
-      uint32_t w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = pack2<T>(y[2 * j], y[2 * j + 1]);
-      store_v8(static_cast<T *>(p.out) + row * p.out_row + col_at, w, p.vec32);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (col_at + j >= p.n) break;
-      float v = y[j];
-      if (p.residual) v += to_f32(static_cast<const T *>(p.residual)[row * p.res_row + col_at + j]);
-      if (p.out_f32) {
-        static_cast<float *>(p.out)[row * p.out_row + col_at + j] = v;
-      } else {
-        static_cast<T *>(p.out)[row * p.out_row + col_at + j] = from_f32<T>(v);
-      }
+        if (j < count) *o = from_f32<T>(y[j]);
     }
   }
 }
@@ -293,81 +199,37 @@ struct Tile {
   int group, lane0, col0;
 };
 
-// Consecutive tiles share their rows along the lanes; of a pair's 256 rows
-// CTA `rank` has 128.
+// Of a pair's 256 lanes CTA `rank` has 128.
 __device__ __forceinline__ Tile tile_at(const LinearParams &p, int t, int rank) {
   Tile o;
   const int per = p.lane_tiles * p.col_tiles;
   o.group = t / per;
-  const int u = t % per;
-  o.lane0 = u / p.col_tiles * p.lane_step + rank * kLanes;
-  o.col0 = u % p.col_tiles * p.bn;
+  const int u = t - o.group * per;
+  const int inside = p.lanes_inside ? p.lane_tiles : p.col_tiles;
+  const int outer = u / inside, inner = u - outer * inside;
+  o.lane0 = (p.lanes_inside ? inner : outer) * p.lane_step + rank * kLanes;
+  o.col0 = (p.lanes_inside ? outer : inner) * p.bn;
   return o;
 }
 
 // Turns tile `t` into outputs.  `acc` is the tile's tensor memory; warp e of
-// the epilogue reads lanes 32 * (e % 4) .. + 31.  `stage`: the warp's shared
-// memory for outputs that leave by TMA.
-template <typename T, int ACT, bool SWAP>
-__device__ __forceinline__ void epilogue(const LinearParams &p, const CUtensorMap *out_map, const Tile &t, uint32_t acc,
-                                         const float *bias_s, int e, uint32_t stage) {
-  const int64_t group_row = static_cast<int64_t>(t.group) * p.rows;
-  const int lane = threadIdx.x % 32;
+// the epilogue has lanes 32 * (e % 4) .. + 31 and every fourth 16 columns.
+template <typename T, int ACT>
+__device__ __forceinline__ void epilogue(const LinearParams &p, const Tile &t, uint32_t acc, int e) {
   const uint32_t base = acc + (static_cast<uint32_t>(32 * (e % 4)) << 16);
-  const int at = t.lane0 + 32 * (e % 4) + lane;
-  const int end = min(p.bn, (SWAP ? p.rows : p.n) - t.col0);
-  uint32_t r[SWAP ? 1 : 2][16];
-  if constexpr (SWAP) {
-    // Every fourth 16 columns.
-    const float lane_bias = bias_at<T>(p, at);
-    for (int c = e / 4 * 16; c < end; c += 64) {
-      tmem_ld16(base + c, r[0]);
-      tmem_wait_ld();
-      if (p.kblocks == 0) {
+  const int n = t.lane0 + 32 * (e % 4) + static_cast<int>(threadIdx.x % 32);
+  const int64_t row = static_cast<int64_t>(t.group) * p.rows + t.col0;
+  const int cols = min(p.bn, p.rows - t.col0);
+  const float bias = bias_at<T>(p, n);
+  for (int c = e / 4 * 16; c < cols; c += 64) {
+    uint32_t r[16];
+    tmem_ld16(base + c, r);
+    tmem_wait_ld();
+    if (p.kblocks == 0) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[0][j] = 0;
-      }
-      finish16<T, ACT, SWAP>(p, r[0], bias_s, lane_bias, group_row, at, t.col0 + c, 0, 0);
+      for (int j = 0; j < 16; ++j) r[j] = 0;
     }
-  } else {
-    // Every fourth 32 columns.
-    for (int c = e / 4 * 32; c < end; c += 128) {
-      tmem_ld16(base + c, r[0]);
-      tmem_ld16(base + c + 16, r[1]);
-      if (p.tma_out) {  // the last outputs have left the stage
-        if (lane == 0) tma_store_wait_read();
-        __syncwarp();
-      }
-      tmem_wait_ld();
-      if (p.kblocks == 0) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) r[0][j] = r[1][j] = 0;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        finish16<T, ACT, SWAP>(p, r[i], bias_s + c + 16 * i, 0.0f, group_row, at, t.col0 + c + 16 * i, stage,
-                               static_cast<uint32_t>(lane * 64 + i * 32));
-      if (p.tma_out) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && t.lane0 + 32 * (e % 4) < p.rows) {
-          tma_store_3d(out_map, stage, t.col0 + c, t.lane0 + 32 * (e % 4), t.group);
-          tma_store_commit();
-        }
-      }
-    }
-  }
-}
-
-template <typename T, bool SWAP>
-__device__ __forceinline__ void epilogue_act(const LinearParams &p, const CUtensorMap *out_map, const Tile &t,
-                                             uint32_t acc, const float *bias_s, int e, uint32_t stage) {
-  switch (p.act) {
-    case LM_ACT_RELU: epilogue<T, LM_ACT_RELU, SWAP>(p, out_map, t, acc, bias_s, e, stage); break;
-    case LM_ACT_GELU: epilogue<T, LM_ACT_GELU, SWAP>(p, out_map, t, acc, bias_s, e, stage); break;
-    case LM_ACT_GELU_TANH: epilogue<T, LM_ACT_GELU_TANH, SWAP>(p, out_map, t, acc, bias_s, e, stage); break;
-    case LM_ACT_SILU: epilogue<T, LM_ACT_SILU, SWAP>(p, out_map, t, acc, bias_s, e, stage); break;
-    default: epilogue<T, LM_ACT_NONE, SWAP>(p, out_map, t, acc, bias_s, e, stage); break;
+    if (n < p.n) put16<T, ACT>(p, r, bias, row + c, min(16, cols - c), n);
   }
 }
 
@@ -377,44 +239,58 @@ __device__ __forceinline__ void epilogue_act(const LinearParams &p, const CUtens
 template <typename T, int ACT>
 __device__ __forceinline__ void finish_split(const LinearParams &p, const Tile &t, uint32_t partial, int rank, int tid,
                                              int threads) {
-  const int64_t group_row = static_cast<int64_t>(t.group) * p.rows;
+  const int64_t row = static_cast<int64_t>(t.group) * p.rows + t.col0;
   const int cols = min(p.bn, p.rows - t.col0);
   for (int i = tid; i < kLanes * ((p.bn + p.splits - 1) / p.splits); i += threads) {
     const int c = i / kLanes * p.splits + rank, lane = i % kLanes;
     const int n = t.lane0 + lane;
     if (c >= cols || n >= p.n) continue;
     const uint32_t at = partial + static_cast<uint32_t>(c * kLanes + lane) * 4;
+    uint32_t v[kMaxSplits];
+#pragma unroll
+    for (int r = 0; r < kMaxSplits; ++r)
+      if (r < p.splits) v[r] = ld_dsmem_u32(at, static_cast<uint32_t>(r));
     float s = 0.0f;
-    for (int r = 0; r < p.splits; ++r) s += __uint_as_float(ld_dsmem_u32(at, static_cast<uint32_t>(r)));
-    put<T, ACT>(p, s, bias_at<T>(p, n), group_row + t.col0 + c, n);
+#pragma unroll
+    for (int r = 0; r < kMaxSplits; ++r)
+      if (r < p.splits) s += __uint_as_float(v[r]);
+    put<T, ACT>(p, s, bias_at<T>(p, n), row + c, n);
   }
 }
 
-// Barrier of the epilogue's warps: whether `ok` holds for all their threads.
-template <int THREADS>
-__device__ __forceinline__ bool epilogue_all(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(ok ? 1u : 0u), "n"(THREADS)
-      : "memory");
-  return r != 0;
+template <typename T>
+__device__ __forceinline__ void epilogue_act(const LinearParams &p, const Tile &t, uint32_t acc, int e) {
+  switch (p.act) {
+    case LM_ACT_RELU: epilogue<T, LM_ACT_RELU>(p, t, acc, e); break;
+    case LM_ACT_GELU: epilogue<T, LM_ACT_GELU>(p, t, acc, e); break;
+    case LM_ACT_GELU_TANH: epilogue<T, LM_ACT_GELU_TANH>(p, t, acc, e); break;
+    case LM_ACT_SILU: epilogue<T, LM_ACT_SILU>(p, t, acc, e); break;
+    default: epilogue<T, LM_ACT_NONE>(p, t, acc, e); break;
+  }
 }
 
-template <typename T, bool SWAP, Form FORM>
+template <typename T>
+__device__ __forceinline__ void finish_split_act(const LinearParams &p, const Tile &t, uint32_t partial, int rank,
+                                                 int tid, int threads) {
+  switch (p.act) {
+    case LM_ACT_RELU: finish_split<T, LM_ACT_RELU>(p, t, partial, rank, tid, threads); break;
+    case LM_ACT_GELU: finish_split<T, LM_ACT_GELU>(p, t, partial, rank, tid, threads); break;
+    case LM_ACT_GELU_TANH: finish_split<T, LM_ACT_GELU_TANH>(p, t, partial, rank, tid, threads); break;
+    case LM_ACT_SILU: finish_split<T, LM_ACT_SILU>(p, t, partial, rank, tid, threads); break;
+    default: finish_split<T, LM_ACT_NONE>(p, t, partial, rank, tid, threads); break;
+  }
+}
+
+template <typename T, Form FORM>
 __global__ void __launch_bounds__(threads_of(FORM), 1)
     linear_kernel(const __grid_constant__ CUtensorMap lane_map, const __grid_constant__ CUtensorMap col_map,
-                  const __grid_constant__ CUtensorMap out_map, const LinearParams p) {
+                  const LinearParams p) {
   constexpr bool PAIR = FORM == Form::kPair, SPLIT = FORM == Form::kSplit;
   constexpr int EPI = epi_warps(FORM);
   extern __shared__ __align__(1024) uint8_t ring[];  // stages on a boundary of the swizzle's period
   const int col_rows = PAIR ? p.bn / 2 : p.bn;  // rows of the column side that this CTA holds
   const int stage_bytes = kLanes * 128 + col_rows * 128;
-  uint8_t *const stage_s = ring + p.stages * stage_bytes;  // outputs on their way
-  Barriers &b = *reinterpret_cast<Barriers *>(stage_s + p.stage_out);
-  float *const bias_s = reinterpret_cast<float *>(&b + 1);  // two tiles of bn
+  Barriers &b = *reinterpret_cast<Barriers *>(ring + p.stages * stage_bytes);
   // (The shuffle tells the compiler that the warp number is uniform.)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
   const int rank = FORM != Form::kOne ? static_cast<int>(cluster_ctarank()) : 0;
@@ -461,7 +337,6 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     for (int t = first; t < p.tiles && ok; t += step) {
       const Tile tile = tile_at(p, t, lane_rank);
       const int col0 = tile.col0 + (PAIR ? rank * col_rows : 0);
-      const int lane_z = SWAP ? 0 : tile.group, col_z = SWAP ? tile.group : 0;
       for (int kb = k_begin; kb < k_end; ++kb) {
         if (fills >= p.stages) ok = __all_sync(0xffffffffu, mbar_wait(&b.empty[s], phase, abort, p.err));
         if (!ok) break;
@@ -473,8 +348,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
           if (PAIR) bar = cluster_addr(bar, 0);
           if (!PAIR || rank == 0)
             mbar_arrive_expect_tx(&b.full[s], static_cast<uint32_t>(PAIR ? 2 * stage_bytes : stage_bytes));
-          tma_load_3d<PAIR>(dst, &lane_map, kb * kBk, tile.lane0, lane_z, bar);
-          tma_load_3d<PAIR>(dst + kLanes * 128, &col_map, kb * kBk, col0, col_z, bar);
+          tma_load_3d<PAIR>(dst, &lane_map, kb * kBk, tile.lane0, 0, bar);
+          tma_load_3d<PAIR>(dst + kLanes * 128, &col_map, kb * kBk, col0, tile.group, bar);
         }
         __syncwarp();
         ++fills;
@@ -534,28 +409,12 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     }
   } else if (warp >= 4) {
     const int e = warp - 4;
-    const int et = threadIdx.x - 128;
     int tiles = 0;
-    // A thread's column of the bias, fetched a tile ahead (bn <= threads).
-    float next_bias = 0.0f;
-    if (!SWAP && et < p.bn && first < p.tiles) next_bias = bias_at<T>(p, tile_at(p, first, lane_rank).col0 + et);
     for (int t = first; t < p.tiles; t += step, ++tiles) {
       const Tile tile = tile_at(p, t, lane_rank);
       const int half = tiles & 1;
-      float *const bs = bias_s + half * p.bn;
-      if (!SWAP) {
-        // Every epilogue warp has left the tile that used this half before:
-        // the barrier of the tile in between lies behind it.
-        if (et < p.bn) {
-          bs[et] = next_bias;
-          if (t + step < p.tiles) next_bias = bias_at<T>(p, tile_at(p, t + step, lane_rank).col0 + et);
-        }
-      }
-      bool ok = mbar_wait(&b.acc_full[half], (tiles >> 1) & 1, abort, p.err);
-      // One decision for all warps that meet at the barrier, and per warp
-      // elsewhere: tensor memory loads are executed by whole warps.
-      ok = SWAP ? __all_sync(0xffffffffu, ok) : epilogue_all<32 * EPI>(ok);
-      if (!ok) break;
+      // One decision per warp: tensor memory loads are executed by whole warps.
+      if (!__all_sync(0xffffffffu, mbar_wait(&b.acc_full[half], (tiles >> 1) & 1, abort, p.err))) break;
       tcgen05_fence_after();
       const uint32_t acc = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
       if (SPLIT) {
@@ -570,7 +429,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
           for (int j = 0; j < 16; ++j) partial[(c + j) * kLanes + lane] = __uint_as_float(r[j]);
         }
       } else {
-        epilogue_act<T, SWAP>(p, &out_map, tile, acc, bs, e, smem_u32(stage_s) + e * kStageOut);
+        epilogue_act<T>(p, tile, acc, e);
         tcgen05_fence_before();
         __syncwarp();
         if (threadIdx.x % 32 == 0) {
@@ -584,23 +443,13 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     }
   }
 
-  if (warp >= 4 && threadIdx.x % 32 == 0) tma_store_wait_read();
   __syncwarp();
   if (SPLIT) {
     __syncthreads();
     cluster_sync_all();
     if (!*abort && first < p.tiles) {
       const Tile tile = tile_at(p, first, 0);
-      const uint32_t partial = smem_u32(ring);
-      const int tid = threadIdx.x;
-      constexpr int N = threads_of(FORM);
-      switch (p.act) {
-        case LM_ACT_RELU: finish_split<T, LM_ACT_RELU>(p, tile, partial, rank, tid, N); break;
-        case LM_ACT_GELU: finish_split<T, LM_ACT_GELU>(p, tile, partial, rank, tid, N); break;
-        case LM_ACT_GELU_TANH: finish_split<T, LM_ACT_GELU_TANH>(p, tile, partial, rank, tid, N); break;
-        case LM_ACT_SILU: finish_split<T, LM_ACT_SILU>(p, tile, partial, rank, tid, N); break;
-        default: finish_split<T, LM_ACT_NONE>(p, tile, partial, rank, tid, N); break;
-      }
+      finish_split_act<T>(p, tile, smem_u32(ring), rank, threadIdx.x, threads_of(FORM));
     }
     cluster_sync_all();  // no CTA leaves while another reads its sums
   }
@@ -733,9 +582,8 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Boxes of `box_rows` rows x `box_k` (64 or 32) elements in a swizzle of as
-// many bytes, zeros outside.
-lm_status make_map(CUtensorMap *map, const Operand &o, int64_t k, int box_rows, bool bf16, int box_k = kBk) {
+// Tiles of `box_rows` rows x 64 elements of k, zeros outside.
+lm_status make_map(CUtensorMap *map, const Operand &o, int64_t k, int box_rows, bool bf16) {
   const EncodeFn fn = encode_fn();
   if (!fn) return cuda_fail(cudaErrorNotSupported);
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(o.rows),
@@ -746,47 +594,123 @@ lm_status make_map(CUtensorMap *map, const Operand &o, int64_t k, int box_rows, 
   const int64_t rs = o.rows > 1 ? o.row_stride : pad;
   const int64_t gs = o.groups > 1 ? o.group_stride : pad;
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(rs) * 2, static_cast<cuuint64_t>(gs) * 2};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_k), static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {kBk, static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
   const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                         const_cast<void *>(o.p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        box_k == kBk ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? LM_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const LinearParams);
-
-// Pairs of CTAs that the device holds at once (SMs that have no partner in
-// their group stay out), asked once per device.
-int resident_pairs(Kernel kernel, int threads, int smem, const DeviceInfo &dev) {
-  static std::mutex mu;
-  static std::map<int, int> known;
-  std::lock_guard<std::mutex> lk(mu);
-  const auto it = known.find(dev.device);
-  if (it != known.end()) return it->second;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / 2 * 2));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-    (void)cudaGetLastError();
-    n = dev.sm_count / 2;
-  }
-  return known[dev.device] = n < dev.sm_count / 2 ? n : dev.sm_count / 2;
-}
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const LinearParams);
 
 template <typename T>
-Kernel kernel_of(bool swap, Form form) {
-  if (form == Form::kSplit) return linear_kernel<T, true, Form::kSplit>;
-  if (form == Form::kPair) return swap ? linear_kernel<T, true, Form::kPair> : linear_kernel<T, false, Form::kPair>;
-  return swap ? linear_kernel<T, true, Form::kOne> : linear_kernel<T, false, Form::kOne>;
+Kernel kernel_of(Form form) {
+  return form == Form::kSplit ? linear_kernel<T, Form::kSplit>
+         : form == Form::kPair ? linear_kernel<T, Form::kPair> : linear_kernel<T, Form::kOne>;
+}
+
+// Clusters of 2, 4 and 8 CTAs, one to an SM, that the device holds at once (SMs
+// that have no partner in their group stay out), asked once per device.
+struct Resident {
+  int pairs, split[kMaxSplits + 1];
+};
+
+lm_status resident_clusters(const DeviceInfo &dev, Resident *r) {
+  static std::mutex mu;
+  static std::map<int, Resident> known;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto it = known.find(dev.device);
+  if (it != known.end()) {
+    *r = it->second;
+    return LM_OK;
+  }
+  auto ask = [&](Kernel kernel, Form form, int size) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / size * size));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads_of(form)));
+    cfg.dynamicSmemBytes = 128 * 1024;  // more than half an SM's
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(size);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      n = dev.sm_count / (2 * size);
+    }
+    return n < dev.sm_count / size ? n : dev.sm_count / size;
+  };
+  Resident a = {};
+  const Kernel pair = kernel_of<__half>(Form::kPair), split = kernel_of<__half>(Form::kSplit);
+  for (const Kernel k : {pair, split})
+    if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(k), 128 * 1024); st != LM_OK) return st;
+  a.pairs = ask(pair, Form::kPair, 2);
+  for (int size = 2; size <= kMaxSplits; size *= 2) a.split[size] = ask(split, Form::kSplit, size);
+  *r = known[dev.device] = a;
+  return LM_OK;
+}
+
+// How a problem is cut into tiles.
+struct Cut {
+  Form form;
+  int bn, splits;
+  int64_t tiles;
+};
+
+// The cut with the least estimated time, in microseconds.  The constants are
+// fitted to 160 problems of 5 to 24000 rows, k of 256 to 4096 and 256 to 10000
+// outputs; the estimate's choice was within 7% of the best one of all cuts for
+// nine in ten of them.
+//   first tile: 3, a stage's latency or its traffic at 185 KB/us for each block
+//     of k, and the epilogue's 0.008 a column;
+//   each further round of tiles: the most of traffic (140 KB/us per SM with all
+//     of them fetching), products (0.0011 a column and block) and epilogue.
+Cut best_cut(int64_t n, int64_t rows, int64_t groups, int kblocks, bool activation, int sms, const Resident &held) {
+  Cut best = {Form::kOne, 16, 1, 0};
+  float least = 3.0e38f;
+  const float column = activation ? 0.0125f : 0.0085f;
+  auto consider = [&](Form form, int bn, int splits) {
+    const bool two = form == Form::kPair;
+    const int64_t lanes = two ? 2 * kLanes : kLanes;
+    const int64_t tiles = (n + lanes - 1) / lanes * ((rows + bn - 1) / bn) * groups;
+    const int64_t at_once = two ? held.pairs : splits > 1 ? held.split[splits] : sms;
+    if (splits > 1 && tiles > at_once) return;
+    const int64_t rounds = (tiles + at_once - 1) / at_once;
+    const int blocks = (kblocks + splits - 1) / splits;
+    const float kb = 16.0f + static_cast<float>(bn) / (two ? 16.0f : 8.0f);  // KB of a stage
+    const float stage = kb / 185.0f > 0.13f ? kb / 185.0f : 0.13f;
+    float t = (two ? 4.2f : 3.0f) + static_cast<float>(blocks) * stage;
+    if (splits > 1) {
+      t += 0.9f + 0.03f * static_cast<float>(bn) / static_cast<float>(splits) + 0.008f * static_cast<float>(bn);
+    } else {
+      t += column * static_cast<float>(bn);
+    }
+    if (rounds > 1) {
+      const float products = 0.0011f * static_cast<float>(bn), feed = kb / 140.0f;
+      const float main = static_cast<float>(blocks) * (products > feed ? products : feed);
+      const float epi = 0.5f + column * static_cast<float>(bn);
+      t += static_cast<float>(rounds - 1) * (main > epi ? main : epi);
+    }
+    if (t < least) {
+      least = t;
+      best = {form, bn, splits, tiles};
+    }
+  };
+  const int most = rows < kMaxBn ? static_cast<int>((rows + 15) / 16 * 16) : kMaxBn;
+  for (int bn = 16; bn <= most; bn += bn < 64 ? 16 : 32) {
+    consider(Form::kOne, bn, 1);
+    if (bn % 32 == 0) consider(Form::kPair, bn, 1);
+    for (int s = 2; s <= kMaxSplits && s <= kblocks; s *= 2) consider(Form::kSplit, bn, s);
+  }
+  // Exactly the rows there are, or equal shares of them.
+  const int64_t shares = (rows + kMaxBn - 1) / kMaxBn;
+  const int even = static_cast<int>(((rows + shares - 1) / shares + 15) / 16 * 16);
+  consider(Form::kOne, even, 1);
+  if (even % 32 == 0) consider(Form::kPair, even, 1);
+  return best;
 }
 
 }  // namespace
@@ -826,13 +750,11 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
   p.bias = a.bias;
   p.residual = a.residual;
   p.out = a.out;
-  p.rows_total = a.groups * a.rows;
   p.out_row = a.out_row_stride;
   p.res_row = a.residual_row_stride;
   p.rows = static_cast<int32_t>(pl.x.rows);
-  p.k = static_cast<int32_t>(a.k);
   p.n = static_cast<int32_t>(a.n);
-  p.kblocks = (p.k + kBk - 1) / kBk;
+  p.kblocks = static_cast<int32_t>((a.k + kBk - 1) / kBk);
   p.bias_f32 = a.bias_dtype == LM_F32;
   p.out_f32 = a.out_dtype == LM_F32;
   p.act = a.activation;
@@ -840,80 +762,42 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
   p.err = static_cast<uint32_t *>(workspace);
   const bool bf16 = a.dtype == LM_BF16;
 
-  // Outputs in 16-byte vectors, 16 of a row at a time.
-  const int64_t ov = 16 / static_cast<int64_t>(out_size);
-  const bool one_row = p.rows_total == 1;
-  const bool vec = aligned(a.out, 16) && (one_row || a.out_row_stride % ov == 0) &&
-                   (!a.residual || (aligned(a.residual, 16) && (one_row || a.residual_row_stride % 8 == 0)));
-  p.vec32 = aligned(a.out, 32) && (one_row || a.out_row_stride % (2 * ov) == 0);
-  // Up to 512 rows, tiles that hold exactly the rows there are beat 128 or 256
-  // lanes of them (320 x 1024 onto 50048: 38 us against 42).
-  const bool swap = !vec || p.rows <= 512;
-  const int64_t lane_rows = swap ? p.n : p.rows, col_rows = swap ? p.rows : p.n;
-  const int64_t groups = pl.x.groups;
-  // Columns in equal tiles of at most 256, a multiple of 16 each.
-  auto columns = [&](int most, int unit) {
-    const int64_t n = (col_rows + most - 1) / most;
-    return static_cast<int32_t>(((col_rows + n - 1) / n + unit - 1) / unit * unit);
-  };
-  auto count = [&](int lanes, int bn) {
-    return (lane_rows + lanes - 1) / lanes * ((col_rows + bn - 1) / bn) * groups;
-  };
-  Form form = Form::kOne;
-  const int unit = swap ? 16 : 32;
-  p.bn = columns(kMaxBn, unit);
-  const int32_t pair_bn = columns(kMaxBn, 32);
-  // Pairs fetch a third less per product; their tiles are longer to fill and
-  // to empty, which shows where k is short (k = 240: 20.5 us against 18.5).
-  if (pair_bn >= 128 && p.kblocks >= 8 && count(2 * kLanes, pair_bn) >= dev.sm_count / 2) {
-    form = Form::kPair;
-    p.bn = pair_bn;
-  } else if (!swap && count(kLanes, p.bn) < dev.sm_count && p.bn > 128) {
-    p.bn = columns(128, unit);
-  }
-  p.lane_step = form == Form::kPair ? 2 * kLanes : kLanes;
-  p.lane_tiles = static_cast<int32_t>((lane_rows + p.lane_step - 1) / p.lane_step);
-  p.col_tiles = static_cast<int32_t>((col_rows + p.bn - 1) / p.bn);
-  const int64_t tiles = count(p.lane_step, p.bn);
-  if (tiles > INT_MAX / 16) return LM_ERR_UNSUPPORTED;
-  p.tiles = static_cast<int32_t>(tiles);
-  p.splits = 1;
-  if (swap && form == Form::kOne && p.bn <= 64) {
-    while (p.splits < 8 && tiles * p.splits * 2 <= dev.sm_count && p.kblocks >= p.splits * 2) p.splits *= 2;
-    if (p.splits > 1) form = Form::kSplit;
-  }
+  Resident held;
+  if (lm_status st = resident_clusters(dev, &held); st != LM_OK) return st;
+  const Cut cut = best_cut(p.n, p.rows, pl.x.groups, p.kblocks, p.act > LM_ACT_RELU, dev.sm_count, held);
+  if (cut.tiles > INT_MAX / 16) return LM_ERR_UNSUPPORTED;
+  p.bn = cut.bn;
+  p.splits = cut.splits;
+  p.tiles = static_cast<int32_t>(cut.tiles);
+  p.lane_step = cut.form == Form::kPair ? 2 * kLanes : kLanes;
+  p.lane_tiles = (p.n + p.lane_step - 1) / p.lane_step;
+  p.col_tiles = (p.rows + p.bn - 1) / p.bn;
+  // The smaller operand goes round inside, out of L2, the larger passes once.
+  p.lanes_inside = p.n <= p.rows;
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.bn) p.tmem_cols *= 2;
-  const int held_cols = form == Form::kPair ? p.bn / 2 : p.bn;
+  const int held_cols = cut.form == Form::kPair ? p.bn / 2 : p.bn;
   const int stage_bytes = kLanes * 128 + held_cols * 128;
-  p.tma_out = !swap && !p.out_f32;
-  p.stage_out = p.tma_out ? epi_warps(form) * kStageOut : 0;
-  const int rest = p.stage_out + static_cast<int>(sizeof(Barriers)) + 2 * p.bn * 4;
-  p.stages = (227 * 1024 - rest) / stage_bytes;
+  p.stages = (227 * 1024 - static_cast<int>(sizeof(Barriers))) / stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.idesc = idesc_f16(bf16, static_cast<uint32_t>(p.lane_step), static_cast<uint32_t>(p.bn));
-  const int smem = p.stages * stage_bytes + rest;
+  const int smem = p.stages * stage_bytes + static_cast<int>(sizeof(Barriers));
 
-  CUtensorMap lanes = {}, cols = {}, outs = {};
+  CUtensorMap lanes = {}, cols = {};
   if (p.kblocks > 0) {
-    if (lm_status st = make_map(&lanes, swap ? pl.w : pl.x, a.k, kLanes, bf16); st != LM_OK) return st;
-    if (lm_status st = make_map(&cols, swap ? pl.x : pl.w, a.k, held_cols, bf16); st != LM_OK) return st;
+    if (lm_status st = make_map(&lanes, pl.w, a.k, kLanes, bf16); st != LM_OK) return st;
+    if (lm_status st = make_map(&cols, pl.x, a.k, held_cols, bf16); st != LM_OK) return st;
   }
-  if (p.tma_out) {
-    const Operand o{a.out, groups, p.rows, static_cast<int64_t>(p.rows) * a.out_row_stride, a.out_row_stride, false, 0};
-    if (lm_status st = make_map(&outs, o, a.n, 32, bf16, 32); st != LM_OK) return st;
-  }
-  const Kernel kernel = bf16 ? kernel_of<__nv_bfloat16>(swap, form) : kernel_of<__half>(swap, form);
+  const Kernel kernel = bf16 ? kernel_of<__nv_bfloat16>(cut.form) : kernel_of<__half>(cut.form);
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
   int cluster = 1, grid = p.tiles < dev.sm_count ? p.tiles : dev.sm_count;
-  if (form == Form::kSplit) {
+  if (cut.form == Form::kSplit) {
     cluster = p.splits;
     grid = p.tiles * p.splits;
-  } else if (form == Form::kPair) {
+  } else if (cut.form == Form::kPair) {
     cluster = 2;
-    const int pairs = resident_pairs(kernel, threads_of(form), smem, dev);
-    grid = 2 * (p.tiles < pairs ? p.tiles : pairs);
+    grid = 2 * (p.tiles < held.pairs ? p.tiles : held.pairs);
   }
-  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), threads_of(form), static_cast<size_t>(smem), s,
-                          cluster, lanes, cols, outs, p);
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), threads_of(cut.form), static_cast<size_t>(smem), s,
+                          cluster, lanes, cols, p);
 }

@@ -172,7 +172,7 @@ __device__ __noinline__ int take_keys(Gather *g, int count, int keys, float boun
 }
 
 template <typename T, int kVecs>
-__global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 2) beam_kernel(const BeamParams p) {
   constexpr int N = 16 / static_cast<int>(sizeof(T));  // values of a vector
   constexpr int kTileVecs = 32 * kVecs;
   __shared__ Gather gathered[kWarps];

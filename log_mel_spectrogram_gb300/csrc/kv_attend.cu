@@ -73,14 +73,16 @@ struct AttendParams {
 // Shared memory: the rings (at the end the warps' partial results), then this.
 template <int R>
 struct Shared {
-  uint64_t full[kWarps][8], empty[8];
+  uint64_t full[kWarps][8];
   float2 ml[kWarps][R];  // maximum and sum per warp and query row
   int abort;
   int last;
 };
 
 constexpr int big_bytes(int d, int mt, bool shared) {
-  const int ring = (shared ? 1 : kWarps) * ring_stages(d, shared) * stage_bytes(d), joined = kWarps * 16 * mt * d * 4;
+  // (Shared: and two tiles as f16.)
+  const int ring = (shared ? 1 : kWarps) * ring_stages(d, shared) * stage_bytes(d) + (shared ? 4 * stage_bytes(d) : 0);
+  const int joined = kWarps * 16 * mt * d * 4;
   return ring > joined ? ring : joined;
 }
 
@@ -93,6 +95,9 @@ __device__ __forceinline__ uint2 lds_v2(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
+}
+__device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
   uint32_t v;
@@ -121,12 +126,24 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
   }
 }
 
-// SHARED: the warps have 16 query rows each and go over the same tokens, in one
-// ring, instead of sharing out the tokens of 16 * MT rows.  E = 1: at most
+// Where row `row` of a tile of f16 (D elements a row) has its 16-byte piece
+// `piece`: pieces are permuted so that eight rows' pieces of one column lie in
+// different banks.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+  return static_cast<uint32_t>(row * D * 2 + ((piece ^ (D == 32 ? (row >> 1) & 3 : row & 7)) * 16));
+}
+
+// SHARED, for many query rows: the warps have 16 each and go over the same
+// tokens, in one ring, instead of sharing out the tokens of 16 * MT rows.  Each
+// warp turns a quarter of a tile into f16 in shared memory, laid out so that
+// ldmatrix gives all warps the operands that they would make of the bytes
+// themselves (250 instructions a tile and warp instead of 400).  E = 1: at most
 // eight query rows, so that the lower half of a product's rows is left out of
 // the softmax (55 of 400 instructions a tile).
 template <typename T, int D, int MT, int E, bool SHARED>
-__global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? resident_ctas(D) : 2) attend_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? resident_ctas(D) : 2)
+    attend_kernel(const AttendParams p) {
   constexpr int STAGES = ring_stages(D, SHARED);
   constexpr int KW = D / 16;   // 32-bit words of a token's key per thread; also 16-element steps of k
   constexpr int VB = D / 8;    // bytes of a token's value per thread; also 8-column tiles of the output
@@ -145,10 +162,7 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
   const int64_t unit = (static_cast<int64_t>(blockIdx.z) * p.c.rows + row) * p.c.heads + h;
 
   if (threadIdx.x < kWarps)
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&sh.full[threadIdx.x][i], 1);
-      if (threadIdx.x == 0) mbar_init(&sh.empty[i], kWarps);
-    }
+    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[threadIdx.x][i], 1);
   if (threadIdx.x == 0) sh.abort = 0;
   fence_mbar_init();
   pdl_launch();
@@ -343,6 +357,9 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
     }
   }
 
+  // Byte n of two words, in the low bytes of the halves.
+  constexpr uint32_t kPick[4] = {0x0400, 0x0501, 0x0602, 0x0703};
+  const uint32_t tiles_a = ring_a + STAGES * stage_bytes(D);  // SHARED: two tiles of f16 keys and values
   // Of the 32 tiles that are consumed next, one per lane and half: the key
   // scale, log2 and inverse of the value scale; absent blocks are masked.
   float f_s[2] = {0, 0}, l_s[2] = {0, 0}, i_s[2] = {0, 0};
@@ -368,23 +385,59 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
     const int t0 = token_of(j);
     const int s = j % STAGES;
     const uint32_t k_at = ring_a + s * stage_bytes(D), v_at = k_at + kTok * D;
-    if (!mbar_wait(&full[s], (j / STAGES) & 1, &sh.abort, p.err)) break;
+    bool ok = mbar_wait(&full[s], (j / STAGES) & 1, &sh.abort, p.err);
+    const uint32_t k16 = tiles_a + (j & 1) * 2 * stage_bytes(D), v16 = k16 + kTok * D * 2;
+    if constexpr (SHARED) {
+      if (ok) {
+        // Token r8 of this warp's eight: place 2 (r8 % 4) + r8 / 4 among them.
+        const int to = 8 * warp + 2 * (r8 & 3) + (r8 >> 2);
+        uint32_t w[KW];
+        lds_words(k_at + (8 * warp + r8) * D + c4 * (D / 4), w);
+#pragma unroll
+        for (int ks = 0; ks < KW; ++ks) {
+          uint32_t b0, b1;
+          bytes_to_subnormal(w[ks], b0, b1);
+          sts_u32(k16 + piece_at<D>(to, 2 * ks) + 4 * c4, b0);
+          sts_u32(k16 + piece_at<D>(to, 2 * ks + 1) + 4 * c4, b1);
+        }
+        lds_words(v_at + (8 * warp + r8) * D + c4 * (D / 4), w);
+#pragma unroll
+        for (int n = 0; n < VB; ++n)
+          sts_u32(v16 + piece_at<D>(to, n) + 4 * c4,
+                  bytes_to_f16(__byte_perm(w[n / 4], w[VB / 4 + n / 4], kPick[n % 4])));
+      }
+      // The tile is whole, and its bytes are no longer needed.
+      if (__syncthreads_or(!ok)) break;
+      if (fetches && fetched < mine) fetch(fetched++);
+    } else if (!ok) {
+      break;
+    }
 
     // Scores: column n of 8-token tile n8 is token 16 (n8/2) + 8 (n8%2) + n/2 + 4 (n%2).
     float sc[MT][4][4];
 #pragma unroll
     for (int n8 = 0; n8 < 4; ++n8) {
-      const int tok = 16 * (n8 / 2) + 8 * (n8 & 1) + (r8 >> 1) + 4 * (r8 & 1);
-      uint32_t w[KW];
-      lds_words(k_at + tok * D + c4 * (D / 4), w);
 #pragma unroll
       for (int m = 0; m < MT; ++m) sc[m][n8][0] = sc[m][n8][1] = sc[m][n8][2] = sc[m][n8][3] = 0.0f;
+      if constexpr (SHARED) {
 #pragma unroll
-      for (int ks = 0; ks < KW; ++ks) {
-        uint32_t b0, b1;
-        bytes_to_subnormal(w[ks], b0, b1);
+        for (int k2 = 0; k2 < KW / 2; ++k2) {
+          uint32_t b[4];
+          ldmatrix4<false>(b, k16 + piece_at<D>(8 * n8 + lane % 8, 4 * k2 + lane / 8));
+          mma16816(sc[0][n8], q[0][2 * k2], b[0], b[1]);
+          mma16816(sc[0][n8], q[0][2 * k2 + 1], b[2], b[3]);
+        }
+      } else {
+        const int tok = 16 * (n8 / 2) + 8 * (n8 & 1) + (r8 >> 1) + 4 * (r8 & 1);
+        uint32_t w[KW];
+        lds_words(k_at + tok * D + c4 * (D / 4), w);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) mma16816(sc[m][n8], q[m][ks], b0, b1);
+        for (int ks = 0; ks < KW; ++ks) {
+          uint32_t b0, b1;
+          bytes_to_subnormal(w[ks], b0, b1);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) mma16816(sc[m][n8], q[m][ks], b0, b1);
+        }
       }
     }
     const float f0 = __shfl_sync(0xffffffffu, f_s[0], j % 32), f1 = __shfl_sync(0xffffffffu, f_s[1], j % 32);
@@ -475,34 +528,30 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
         a[m][2] = pack2<__half>(sc[m][2 * half + 1][0], sc[m][2 * half + 1][1]);
         a[m][3] = E == 1 ? 0u : pack2<__half>(sc[m][2 * half + 1][2], sc[m][2 * half + 1][3]);
       }
-      uint32_t w[4][VB / 4];
+      if constexpr (SHARED) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lds_words(v_at + (16 * half + 4 * i + c4) * D + VB * r8, w[i]);
+        for (int n = 0; n < VB; n += 2) {
+          uint32_t b[4];
+          ldmatrix4<true>(b, v16 + piece_at<D>(16 * half + lane % 16, n + lane / 16));
+          mma16816(acc[0][n], a[0], b[0], b[1]);
+          mma16816(acc[0][n + 1], a[0], b[2], b[3]);
+        }
+      } else {
+        uint32_t w[4][VB / 4];
 #pragma unroll
-      for (int n = 0; n < VB; ++n) {
-        // Byte n of tokens c4, c4 + 4 and of c4 + 8, c4 + 12, in the low byte of each half.
-        constexpr uint32_t pick[4] = {0x0400, 0x0501, 0x0602, 0x0703};
-        const uint32_t lo = __byte_perm(w[0][n / 4], w[1][n / 4], pick[n % 4]);
-        const uint32_t hi = __byte_perm(w[2][n / 4], w[3][n / 4], pick[n % 4]);
-        // The selectors above put byte n at positions 0 (first token) and 2 (second).
-        const uint32_t b0 = bytes_to_f16(lo), b1 = bytes_to_f16(hi);
+        for (int i = 0; i < 4; ++i) lds_words(v_at + (16 * half + 4 * i + c4) * D + VB * r8, w[i]);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) mma16816(acc[m][n], a[m], b0, b1);
+        for (int n = 0; n < VB; ++n) {
+          // Byte n of tokens c4, c4 + 4 and of c4 + 8, c4 + 12.
+          const uint32_t b0 = bytes_to_f16(__byte_perm(w[0][n / 4], w[1][n / 4], kPick[n % 4]));
+          const uint32_t b1 = bytes_to_f16(__byte_perm(w[2][n / 4], w[3][n / 4], kPick[n % 4]));
+#pragma unroll
+          for (int m = 0; m < MT; ++m) mma16816(acc[m][n], a[m], b0, b1);
+        }
       }
     }
     __syncwarp();
-    if (!SHARED) {
-      if (fetched < mine) fetch(fetched++);
-    } else {
-      if (lane == 0) mbar_arrive(&sh.empty[s]);
-      // The stage of the tile before, which the other warps have most likely
-      // left by now.
-      if (warp == 0 && j > 0 && fetched < mine) {
-        const int was = (j - 1) % STAGES;
-        if (!mbar_wait(&sh.empty[was], ((j - 1) / STAGES) & 1, &sh.abort, p.err)) break;
-        fetch(fetched++);
-      }
-    }
+    if (!SHARED && fetched < mine) fetch(fetched++);
   }
   if (fetches && done < mine && lane == 0) {  // gave up: the copies in flight still have to land
     for (int f = done; f < fetched; ++f) mbar_wait_drain(&full[f % STAGES], (f / STAGES) & 1, p.err);

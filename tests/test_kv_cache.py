@@ -258,6 +258,28 @@ def test_an_offset_past_32_bits(lm):
     del c
 
 
+@pytest.mark.parametrize("dim", [32, 64, 128])
+@pytest.mark.parametrize("block", [16, 64])
+def test_a_prompt_over_a_long_row(lm, dim, block):
+    """Many queries and many tokens: tiles beyond the first 32, parts, ragged ends."""
+    c = filled(lm, 2, 3000, 1, dim, block, torch.float16, seed=dim)
+    c.lens.copy_(torch.tensor([2800, 1203]))
+    q = gen(dim)(2, 130, 2, dim).half()
+    new = torch.tensor([130, 77], dtype=torch.int32, device="cuda")
+    check_attend(c.attend(0, q, new), c, 0, q, new.tolist(), True)
+    check_attend(c.attend(0, q, new, causal=False), c, 0, q, new.tolist(), False)
+
+
+def test_results_repeat(lm):
+    """Parts are joined in order, whichever finishes last."""
+    c = filled(lm, 2, 30000, 2, 64, 32, torch.bfloat16, seed=3)
+    c.lens.copy_(torch.tensor([29000, 17001]))
+    q = gen(3)(2, 3, 4, 64).bfloat16()
+    first = c.attend(0, q, causal=False)
+    for _ in range(20):
+        assert torch.equal(first, c.attend(0, q, causal=False))
+
+
 def test_garbage_past_the_rows_does_not_matter(lm):
     c = filled(lm, 3, 200, 2, 64, 16, torch.float16, seed=7)
     c.lens.copy_(torch.tensor([50, 0, 97]))

@@ -185,3 +185,31 @@ def test_refusals(lm):
         lm.linear(x, w)
     with torch.no_grad():
         lm.linear(x, w)
+
+
+@pytest.mark.parametrize("m,k,n", [(3000, 1024, 4001), (1100, 4096, 2050), (6000, 130, 1000), (513, 2000, 9999),
+                                   (20, 4096, 300), (33, 4095, 520), (7, 2049, 130), (130, 5000, 260), (3000, 3000, 80),
+                                   (1, 8192, 64), (64, 640, 128)])
+def test_every_way_of_cutting(lm, m, k, n):
+    """Pairs of CTAs, several rounds of tiles, k split over clusters of 2, 4 and 8."""
+    x, w, b, r = make((m, k), n, torch.bfloat16, seed=m + n)
+    check(lm.linear(x, w, b, activation="silu", residual=r), x, w, b, "silu", r)
+    check(lm.linear(x, w, out_dtype=torch.float32), x, w)
+
+
+@pytest.mark.parametrize("bands", [80, 81])
+def test_windows_of_many_frames(lm, bands):
+    g = torch.Generator(device="cuda").manual_seed(8)
+    frames = torch.rand((5, 1502, bands), generator=g, device="cuda").half()
+    x = frames.as_strided((5, 1500, 3 * bands), (1502 * bands, bands, 1))
+    w = (torch.randn((512, 3 * bands), generator=g, device="cuda") / 16).half()
+    b = torch.randn(512, generator=g, device="cuda")
+    check(lm.linear(x, w, b, activation="gelu"), x, w, b, "gelu")
+
+
+def test_results_repeat(lm):
+    for m, k, n in ((5, 1024, 1024), (200, 4096, 512), (3000, 1024, 1024)):
+        x, w, b, r = make((m, k), n, torch.float16, seed=1)
+        first = lm.linear(x, w, b, activation="gelu", residual=r)
+        for _ in range(5):
+            assert torch.equal(first, lm.linear(x, w, b, activation="gelu", residual=r))

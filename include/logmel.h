@@ -1,7 +1,9 @@
 /*
  * logmel.h -- C ABI of liblogmel.so, the GB300 (sm_103a) log-mel front end.
  *
- * Two operations:
+ * Two operations (and, in sections 4 to 6, what turns their features into
+ * text: linear layers, an 8-bit key/value cache with its attention, and beam
+ * search):
  *
  *  1. lm_log_mel_from_stft: Whisper's log-mel spectrogram from a complex
  *     STFT, as defined by the KBench task spec "audio_mel_spectrogram_fused.py"
@@ -455,9 +457,8 @@ typedef enum lm_activation {
  *
  * Products are summed in 32 bits; bias, activation, scale and residual are
  * applied in 32 bits and rounded once to out_dtype.  k = 0 gives act(bias).
- * Pointers are aligned to their element; where x and weight are 16-byte
- * aligned with row and group strides that are multiples of 8 elements, tiles
- * are fetched by TMA.
+ * Pointers are aligned to their element.  An x or weight whose rows do not all
+ * start on 16 bytes is copied into the workspace first.
  *
  *   workspace device, >= lm_linear_workspace_size(args), 16-byte aligned,
  *             filled with zeros before its first use; every call leaves the
@@ -507,6 +508,7 @@ lm_status lm_linear(const lm_linear_args *args, void *workspace, size_t workspac
  *                     entry names (lm_kv_reorder only; may be NULL otherwise)
  *   lens              device, [rows] int32, tokens held before this step
  *   head_dim          32, 64 or 128;  block 16, 32, 64 or 128
+ *   rows              up to 65535 for lm_kv_read, lm_kv_attend and lm_kv_reorder
  * Rows hold at most width * block tokens: what a step adds past that is
  * dropped.  A negative length counts as 0.
  */
@@ -579,7 +581,9 @@ lm_status lm_kv_read(const lm_kv_cache *cache, int32_t layer, int32_t start, int
  *   workspace  device, >= lm_kv_attend_workspace_size(...), 16-byte aligned,
  *            zeroed before its first use, left usable by every call (as for
  *            lm_linear).
- * Scores, softmax statistics and the sums are held in 32 bits.
+ * Scores, softmax statistics and the sums are held in 32 bits; a token's weight
+ * is rounded to f16 (2^-11) on its way to the values.  Value scales count as at
+ * least 2^-90.
  * Errors as lm_kv_append, and LM_ERR_WORKSPACE.
  */
 lm_status lm_kv_attend_workspace_size(const lm_kv_cache *cache, int32_t tokens, int32_t q_heads, size_t *bytes);

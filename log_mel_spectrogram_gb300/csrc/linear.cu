@@ -36,10 +36,9 @@
 //
 // Operands that TMA cannot address (rows off 16-byte boundaries) are first
 // copied into padded rows in the workspace.
+#include <atomic>
 #include <climits>
 #include <cuda.h>
-#include <map>
-#include <mutex>
 
 #include "f32x2.cuh"
 #include "half.cuh"
@@ -161,8 +160,8 @@ __device__ __forceinline__ void put(const LinearParams &p, float acc, float bias
 
 // Output n of `count` <= 16 rows from `row` on, from the lane's sums r.
 template <typename T, int ACT>
-__device__ __forceinline__ void put16(const LinearParams &p, const uint32_t (&r)[16], float bias, int64_t row, int count,
-                                      int n) {
+__device__ __forceinline__ void put_rows(const LinearParams &p, const uint32_t (&r)[16], float bias, int64_t row,
+                                         int count, int n) {
   float y[16];
 #pragma unroll
   for (int j = 0; j < 16; j += 2) {
@@ -216,10 +215,10 @@ __device__ __forceinline__ Tile tile_at(const LinearParams &p, int t, int rank) 
 // the epilogue has lanes 32 * (e % 4) .. + 31 and every fourth 16 columns.
 template <typename T, int ACT>
 __device__ __forceinline__ void epilogue(const LinearParams &p, const Tile &t, uint32_t acc, int e) {
-  const uint32_t base = acc + (static_cast<uint32_t>(32 * (e % 4)) << 16);
   const int n = t.lane0 + 32 * (e % 4) + static_cast<int>(threadIdx.x % 32);
   const int64_t row = static_cast<int64_t>(t.group) * p.rows + t.col0;
   const int cols = min(p.bn, p.rows - t.col0);
+  const uint32_t base = acc + (static_cast<uint32_t>(32 * (e % 4)) << 16);
   const float bias = bias_at<T>(p, n);
   for (int c = e / 4 * 16; c < cols; c += 64) {
     uint32_t r[16];
@@ -229,7 +228,7 @@ __device__ __forceinline__ void epilogue(const LinearParams &p, const Tile &t, u
 #pragma unroll
       for (int j = 0; j < 16; ++j) r[j] = 0;
     }
-    if (n < p.n) put16<T, ACT>(p, r, bias, row + c, min(16, cols - c), n);
+    if (n < p.n) put_rows<T, ACT>(p, r, bias, row + c, min(16, cols - c), n);
   }
 }
 
@@ -611,18 +610,18 @@ Kernel kernel_of(Form form) {
 }
 
 // Clusters of 2, 4 and 8 CTAs, one to an SM, that the device holds at once (SMs
-// that have no partner in their group stay out), asked once per device.
+// that have no partner in their group stay out), asked once per device.  Two
+// threads that ask together get the same answer.
 struct Resident {
   int pairs, split[kMaxSplits + 1];
 };
+constexpr int kKnownDevices = 64;
+Resident g_resident[kKnownDevices];
+std::atomic<int> g_resident_state[kKnownDevices];  // 0: not known, 1: being written, 2: known
 
 lm_status resident_clusters(const DeviceInfo &dev, Resident *r) {
-  static std::mutex mu;
-  static std::map<int, Resident> known;
-  std::lock_guard<std::mutex> lk(mu);
-  const auto it = known.find(dev.device);
-  if (it != known.end()) {
-    *r = it->second;
+  if (dev.device < kKnownDevices && g_resident_state[dev.device].load(std::memory_order_acquire) == 2) {
+    *r = g_resident[dev.device];
     return LM_OK;
   }
   auto ask = [&](Kernel kernel, Form form, int size) {
@@ -649,7 +648,12 @@ lm_status resident_clusters(const DeviceInfo &dev, Resident *r) {
     if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(k), 128 * 1024); st != LM_OK) return st;
   a.pairs = ask(pair, Form::kPair, 2);
   for (int size = 2; size <= kMaxSplits; size *= 2) a.split[size] = ask(split, Form::kSplit, size);
-  *r = known[dev.device] = a;
+  *r = a;
+  int none = 0;
+  if (dev.device < kKnownDevices && g_resident_state[dev.device].compare_exchange_strong(none, 1)) {
+    g_resident[dev.device] = a;
+    g_resident_state[dev.device].store(2, std::memory_order_release);
+  }
   return LM_OK;
 }
 

@@ -31,9 +31,15 @@ struct AppendParams {
   bool vec;                      // 16-byte loads of src are aligned
 };
 
-__device__ __forceinline__ int byte_of(uint2 w, int i) {
-  const uint32_t u = i < 4 ? w.x : w.y;
-  return static_cast<int>(u << (24 - 8 * (i & 3))) >> 24;
+// Eight signed bytes as f32: with the sign bit flipped a byte is b + 128, and
+// 0x4b000000 | that is 2^23 + 128 + b.  (Conversion instructions run at an
+// eighth of this rate.)
+__device__ __forceinline__ void bytes_to_f32(uint2 w, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t u = (j < 4 ? w.x : w.y) ^ 0x80808080u;
+    x[j] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + (j & 3))) - 8388736.0f;
+  }
 }
 
 // The largest |x| of two packed values and an earlier result; NaN stays NaN.
@@ -64,25 +70,27 @@ __device__ __noinline__ Eight divide8(Eight v, float scale) {
 
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves an integer in the low bits
 
-// Eight integers' low bytes.
-__device__ __forceinline__ uint2 pack_bytes(const float (&q)[8]) {
-  uint32_t t[8];
+// The low bytes of eight integers q, given as q + kMagic.
+__device__ __forceinline__ uint2 pack_bytes(const float (&t)[8]) {
+  uint32_t u[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) t[j] = __float_as_uint(q[j] + kMagic);
+  for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(t[j]);
   return make_uint2(
-      __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
-      __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
+      __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410),
+      __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410));
 }
 
 // x / scale to the nearest integer, ties to even, as __fdiv_rn and rintf give
 // it, for eight values with |x / scale| <= 128, without the division.  The
 // product with 1 / scale is within 2^-22 * 128 of the quotient, so that only
 // values within 2^-14 of a half can differ, and those take the division.
-__device__ __forceinline__ void quantise8(const float (&x)[8], float scale, float inv, bool plain, float (&q)[8]) {
-  float off = 0.0f;
+// Returns the integers' bytes; q holds them as floats.
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale, float inv, bool plain, float (&q)[8]) {
+  float t[8], off = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    q[j] = fmaf(x[j], inv, kMagic) - kMagic;
+    t[j] = fmaf(x[j], inv, kMagic);
+    q[j] = t[j] - kMagic;
     off = fmaxf(off, fabsf(fmaf(x[j], inv, -q[j])));
   }
   if (!(off < 0.5f - 6.2e-5f) || plain) {
@@ -91,8 +99,28 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], float scale, floa
     for (int j = 0; j < 8; ++j) v.x[j] = x[j];
     v = divide8(v, scale);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = v.x[j];
+    for (int j = 0; j < 8; ++j) {
+      q[j] = v.x[j];
+      t[j] = q[j] + kMagic;
+    }
   }
+  return pack_bytes(t);
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint32_t (&w)[4], float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f2 = unpack2<T>(w[j]);
+    f[2 * j] = f2.x;
+    f[2 * j + 1] = f2.y;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&q)[8], float scale) {
+  return make_uint4(pack2<T>(q[0] * scale, q[1] * scale), pack2<T>(q[2] * scale, q[3] * scale),
+                    pack2<T>(q[4] * scale, q[5] * scale), pack2<T>(q[6] * scale, q[7] * scale));
 }
 
 // One unit: row r's span s of head h.  D and BS are the head dimension and
@@ -137,7 +165,20 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
                        (static_cast<int64_t>(base) + tok0 - held) * p.tok_s[which] + d;
   const int64_t src_step = STEP * p.tok_s[which];
   int8_t *const dst = q8 + tok0 * D + d;
+  // A block that the step fills from its first token, as most of a prompt's:
+  // no conditions on the tokens.
+  const bool full = old == 0 && all == BS && p.vec;
   uint32_t x[kVecs][4];
+  if (full) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + i * src_step));
+      x[i][0] = w.x;
+      x[i][1] = w.y;
+      x[i][2] = w.z;
+      x[i][3] = w.w;
+    }
+  } else
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int tok = tok0 + i * STEP;
@@ -192,40 +233,42 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
   T *const values = static_cast<T *>(p.values[which]);
   T *const out = values && in ? values + ((static_cast<int64_t>(rs) * BS + tok0) * p.c.heads + h) * D + d : nullptr;
   const int64_t out_step = static_cast<int64_t>(STEP) * p.c.heads * D;
+  if (full) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      float f[8], q[8];
+      unpack8<T>(x[i], f);
+      *reinterpret_cast<uint2 *>(dst + i * STEP * D) = quantise8(f, now, inv, plain, q);
+      if (out) __stcs(reinterpret_cast<uint4 *>(out + i * out_step), pack8<T>(q, now));
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int tok = tok0 + i * STEP;
     uint2 *const at = reinterpret_cast<uint2 *>(dst + i * STEP * D);
     float q[8];
     if (tok >= all) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = 0.0f;
-    } else if (tok >= old) {
+      if (out) __stcs(reinterpret_cast<uint4 *>(out + i * out_step), make_uint4(0, 0, 0, 0));
+      continue;
+    }
+    if (tok >= old) {
       float f[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f2 = unpack2<T>(x[i][j]);
-        f[2 * j] = f2.x;
-        f[2 * j + 1] = f2.y;
-      }
-      quantise8(f, now, inv, plain, q);
-      *at = pack_bytes(q);
+      unpack8<T>(x[i], f);
+      *at = quantise8(f, now, inv, plain, q);
     } else {
-      const uint2 w = make_uint2(x[i][0], x[i][1]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = static_cast<float>(byte_of(w, j));
+      bytes_to_f32(make_uint2(x[i][0], x[i][1]), q);
       if (shrink != 1.0f) {
+        float t[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = static_cast<float>(static_cast<int>(rintf(q[j] * shrink)));
-        *at = pack_bytes(q);
+        for (int j = 0; j < 8; ++j) {
+          t[j] = static_cast<float>(static_cast<int>(rintf(q[j] * shrink))) + kMagic;  // NaN as 0
+          q[j] = t[j] - kMagic;
+        }
+        *at = pack_bytes(t);
       }
     }
-    if (out) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = tok < all ? q[j] * now : 0.0f;
-      __stcs(reinterpret_cast<uint4 *>(out + i * out_step),
-             make_uint4(pack2<T>(q[0], q[1]), pack2<T>(q[2], q[3]), pack2<T>(q[4], q[5]), pack2<T>(q[6], q[7])));
-    }
+    if (out) __stcs(reinterpret_cast<uint4 *>(out + i * out_step), pack8<T>(q, now));
   }
 }
 
@@ -279,9 +322,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
     const uint32_t v = v0 + i * kThreads;
     if (v >= p.vecs) continue;
     float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(byte_of(q[i], j)) * s[i];
-    __stcs(out + v, make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7])));
+    bytes_to_f32(q[i], x);
+    __stcs(out + v, pack8<T>(x, s[i]));
   }
 }
 
@@ -362,22 +404,25 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
   __syncthreads();
   if (!last) return;
   if (threadIdx.x == 0) p.done[clip] = 0;
-  // A column at a time per thread: its entries of all beams are read before
-  // one is written.
+  // A thread per beam and column, whole columns at a time: all entries of a
+  // column are read before one is written.
   const int row0 = clip * p.beams;
   const int cols = static_cast<int>(min(static_cast<int64_t>(col) + (open ? 1 : 0), width));
-  for (int c = threadIdx.x; c < cols; c += kThreads) {
-    int32_t was[32];
-    for (int i = 0; i < p.beams; ++i) was[i] = p.c.table[(row0 + i) * width + c];
-    for (int i = 0; i < p.beams; ++i) {
-      const int from = parent_row(p, row0 + i) - row0;
-      if (from == i) continue;
-      if (c < col) {
-        p.c.table[(row0 + i) * width + c] = was[from];
-      } else {
-        p.c.table[(row0 + i) * width + c] = p.c.spare[row0 + i];
-        p.c.spare[row0 + i] = was[i];
-      }
+  const int step = kThreads / p.beams, i = threadIdx.x % p.beams, c0 = threadIdx.x / p.beams;
+  const int parent = parent_row(p, row0 + i);
+  const int mine = p.c.spare[row0 + i];
+  for (int c1 = 0; c1 < cols; c1 += step) {
+    const int c = c1 + c0;
+    const bool moves = c0 < step && c < cols && parent != row0 + i;
+    int next = 0, was = 0;
+    if (moves) {
+      was = p.c.table[(row0 + i) * width + c];
+      next = c < col ? p.c.table[parent * width + c] : mine;
+    }
+    __syncthreads();
+    if (moves) {
+      p.c.table[(row0 + i) * width + c] = next;
+      if (c == col) p.c.spare[row0 + i] = was;
     }
   }
 }
@@ -527,13 +572,11 @@ extern "C" lm_status lm_kv_reorder(const lm_kv_cache *cache, const int32_t *pare
   p.parents = parents;
   p.done = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + kWorkspaceHeaderBytes);
   p.beams = beams;
-  // kCopy vectors of keys and of values per thread, or one where that leaves
-  // most of the device idle.
+  // CTAs of a row: four an SM over all rows, and no more than a vector per thread needs.
   const int64_t vecs = static_cast<int64_t>(cache->layers) * cache->heads * cache->block * cache->head_dim / 16;
   if (vecs > INT_MAX / 2) return LM_ERR_UNSUPPORTED;
-  int64_t parts = (vecs + kCopy * kThreads - 1) / (kCopy * kThreads);
-  if (parts * cache->rows < 152) parts = (vecs + kThreads - 1) / kThreads;
-  p.parts = static_cast<int32_t>(parts < 256 ? parts : 256);
+  const int64_t most = (vecs + kThreads - 1) / kThreads, round = 4 * 152 / cache->rows;
+  p.parts = static_cast<int32_t>(round < 1 ? 1 : round < most ? round : most);
   return launch_dependent(reorder_kernel, dim3(p.parts, cache->rows), kThreads, 0, reinterpret_cast<cudaStream_t>(stream),
                           1, p);
 }

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
   int8_t *const dst = q8 + tok0 * D + d;
   // A block that the step fills from its first token, as most of a prompt's:
   // no conditions on the tokens.
-  const bool full = old == 0 && all == BS && p.vec;
+  const bool full = old <= 0 && all == BS && p.vec;
   uint32_t x[kVecs][4];
   if (full) {
 #pragma unroll

@@ -450,7 +450,7 @@ typedef enum lm_activation {
  *   residual  device, [groups*rows][n] of dtype, residual_row_stride
  *             elements apart, or NULL; may equal out (same row stride).
  *   out       device, [groups*rows][n] of out_dtype, out_row_stride
- *             elements apart; must not overlap the other inputs.
+ *             elements apart (>= n); must not overlap the other inputs.
  *   dtype     LM_F16 or LM_BF16: type of x, weight and residual.
  *   bias_dtype  LM_F32 or dtype.
  *   out_dtype   dtype or LM_F32.
@@ -467,7 +467,7 @@ typedef enum lm_activation {
  *             Its first u32 is the device error word (lm_workspace_error).
  *
  * Errors: LM_ERR_INVALID_ARG (null, negative sizes or strides, unknown
- * activation), LM_ERR_UNSUPPORTED (dtypes; n, k or groups*rows >= 2^31),
+ * activation, overlapping rows of out), LM_ERR_UNSUPPORTED (dtypes; n, k or groups*rows >= 2^31),
  * LM_ERR_MISALIGNED, LM_ERR_WORKSPACE, LM_ERR_CUDA.  groups * rows * n == 0
  * returns LM_OK and enqueues nothing.
  */

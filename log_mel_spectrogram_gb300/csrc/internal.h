@@ -65,6 +65,15 @@ lm_status launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t 
 // device error word (bit flags set by kernels whose bounded waits ran out).
 constexpr size_t kWorkspaceHeaderBytes = 16;
 
+// `count` rows of `size` bytes, `step` bytes apart.
+struct ByteRows {
+  const void *first;
+  int64_t count, step, size;
+};
+
+// Whether two of them have a byte in common.
+bool rows_meet(ByteRows a, ByteRows b);
+
 // Reads an environment override once; returns `fallback` when unset.
 const char *env_or(const char *name, const char *fallback);
 

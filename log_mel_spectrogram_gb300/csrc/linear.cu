@@ -543,6 +543,23 @@ Plan plan(const lm_linear_args &a) {
   return p;
 }
 
+// Whether the output's rows run into one another or into an input.  (Equal to
+// the residual it may be: an element is read before it is written.)
+bool out_meets_inputs(const lm_linear_args &a, const Plan &p, int64_t out_size) {
+  const int64_t rows = a.groups * a.rows;
+  if (rows > 1 && a.out_row_stride < a.n) return true;
+  const ByteRows out{a.out, rows, a.out_row_stride * out_size, a.n * out_size};
+  auto input = [&](const Operand &o) {
+    const ByteRows r{o.p, o.rows, o.row_stride * 2, a.k * 2};
+    if (o.groups == 1) return r;
+    return ByteRows{o.p, o.groups, o.group_stride * 2, (o.rows - 1) * r.step + r.size};
+  };
+  if (a.k > 0 && (rows_meet(out, input(p.x)) || rows_meet(out, input(p.w)))) return true;
+  if (a.bias && rows_meet(out, {a.bias, 1, 0, a.n * (a.bias_dtype == LM_F32 ? 4 : 2)})) return true;
+  const bool same = a.residual == a.out && out_size == 2 && (rows == 1 || a.residual_row_stride == a.out_row_stride);
+  return a.residual && !same && rows_meet(out, {a.residual, rows, a.residual_row_stride * 2, a.n * 2});
+}
+
 lm_status pack(Operand *o, int64_t k, void *dst, cudaStream_t s) {
   PackParams p;
   p.src = static_cast<const uint16_t *>(o->p);
@@ -739,6 +756,7 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
       !aligned(a.residual, 2) || !aligned(a.out, out_size) || !aligned(workspace, 16))
     return LM_ERR_MISALIGNED;
   Plan pl = plan(a);
+  if (out_meets_inputs(a, pl, static_cast<int64_t>(out_size))) return LM_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < pl.bytes) return LM_ERR_WORKSPACE;
   DeviceInfo dev;
   if (lm_status st = current_device_info(&dev); st != LM_OK) return st;

@@ -27,7 +27,7 @@ lm_status cuda_fail(cudaError_t e) {
   return LM_ERR_CUDA;
 }
 
-lm_status current_device_info(DeviceInfo *info) {
+lm_status current_device_info(DeviceInfo *info) try {
   int dev = 0;
   LM_CUDA_TRY(cudaGetDevice(&dev));
   {
@@ -46,9 +46,11 @@ lm_status current_device_info(DeviceInfo *info) {
   g_devices[dev] = d;
   *info = d;
   return LM_OK;
+} catch (...) {  // no exception leaves the library
+  return LM_ERR_OUT_OF_MEMORY;
 }
 
-lm_status ensure_smem_attribute(const void *kernel, int bytes) {
+lm_status ensure_smem_attribute(const void *kernel, int bytes) try {
   int dev = 0;
   LM_CUDA_TRY(cudaGetDevice(&dev));
   {
@@ -63,6 +65,39 @@ lm_status ensure_smem_attribute(const void *kernel, int bytes) {
   std::lock_guard<std::mutex> lk(g_mu);
   g_smem_set.insert({kernel, dev});
   return LM_OK;
+} catch (...) {
+  return LM_ERR_OUT_OF_MEMORY;
+}
+
+bool rows_meet(ByteRows a, ByteRows b) {
+  for (ByteRows *r : {&a, &b}) {
+    if (r->count <= 0 || r->size <= 0) return false;
+    if (r->step <= r->size) {  // no gaps
+      r->size += (r->count - 1) * r->step;
+      r->count = 1;
+    }
+    if (r->count == 1) r->step = r->size;
+  }
+  if (a.count > b.count) {
+    const ByteRows t = a;
+    a = b;
+    b = t;
+  }
+  const int64_t b0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.first));
+  int64_t x0 = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.first));
+  const int64_t x_end = x0 + (a.count - 1) * a.step + a.size, b_end = b0 + (b.count - 1) * b.step + b.size;
+  if (x_end <= b0 || b_end <= x0) return false;
+  if (a.count > 1 && a.step == b.step) {  // columns of one matrix
+    const int64_t d = ((b0 - x0) % a.step + a.step) % a.step;
+    return d < a.size || d + b.size > a.step;
+  }
+  for (int64_t i = 0; i < a.count; ++i, x0 += a.step) {
+    // The first row of b that ends past x0.
+    const int64_t past = x0 - b0 - b.size;
+    const int64_t j = past < 0 ? 0 : past / b.step + 1;
+    if (j < b.count && b0 + j * b.step < x0 + a.size) return true;
+  }
+  return false;
 }
 
 const char *env_or(const char *name, const char *fallback) {

@@ -68,7 +68,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     ``frames.as_strided((B, F - taps + 1, taps * M), (F * M, M, 1))`` against a
     [N, taps * M] weight).  bias [N] float32 or x's dtype; residual [..., N] of
     x's dtype.  activation: None, "relu", "gelu" (erf), "gelu_tanh" or "silu".
-    out_dtype: x's dtype (default) or float32; out may be residual itself."""
+    out_dtype: x's dtype (default) or float32; out may be residual itself, and
+    overlaps no other input."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear(x, weight, bias, activation=activation, residual=residual, scale=scale, out=out,
@@ -171,15 +172,18 @@ class KvCache:
         the cache from lens[r] on, and query i sees up to token lens[r] + i;
         queries past counts[r] see nothing.  Otherwise every query sees the
         lens[r] + counts[r] tokens (lens[r] where counts is None).  A query
-        that sees nothing gives zeros."""
+        that sees nothing gives zeros.  out does not overlap q."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.attend(layer, q, counts, causal=causal, scale=scale, out=out)
         return _checked((_ext or _binding()).kv_attend(*self._head, layer, q, counts, causal, scale, out),
                         "lm_kv_attend")
 
-    def advance(self, tokens) -> None:
+    def advance(self, tokens, *, stream=None) -> None:
         """Adds a step's tokens (a number, or a [rows] int32 tensor) to lens."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.advance(tokens)
         self._lens.add_(tokens)
 
     def read(self, layer: int | None, start: int, count: int, *, stream=None):

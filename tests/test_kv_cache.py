@@ -480,3 +480,15 @@ def test_refusals(lm):
             bad()
     with pytest.raises(RuntimeError, match="inference-only"):
         c.attend(0, k.requires_grad_())
+
+
+def test_outputs_that_overlap_queries(lm):
+    c = lm.KvCache(2, 64, 2, 64, dtype=torch.float16)
+    k = torch.randn((2, 3, 2, 64), device="cuda").half()
+    c.append(0, k, k)
+    q = k.clone()
+    with pytest.raises(lm.LogmelError, match="INVALID_ARG"):
+        c.attend(0, q, out=q)
+    both = torch.randn((2, 2, 3, 2, 64), device="cuda").half()
+    got = c.attend(0, both[0], out=both[1])
+    assert torch.equal(got, c.attend(0, both[0].clone()))

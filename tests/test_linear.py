@@ -213,3 +213,26 @@ def test_results_repeat(lm):
         first = lm.linear(x, w, b, activation="gelu", residual=r)
         for _ in range(5):
             assert torch.equal(first, lm.linear(x, w, b, activation="gelu", residual=r))
+
+
+def test_outputs_that_overlap_inputs(lm):
+    """Refused where a byte is shared; columns of one buffer, and out = residual, are not."""
+    for dtype in (torch.float16, torch.bfloat16):
+        buf = torch.randn((40, 200), device="cuda").to(dtype)
+        w = torch.randn((64, 64), device="cuda").to(dtype)
+        x = buf[:, :64]
+        for bad in (lambda: lm.linear(x, w, out=x), lambda: lm.linear(x, w, out=buf[:, 63:127]),
+                    lambda: lm.linear(buf[:, 8:72], w, out=buf[:, 64:128]),
+                    lambda: lm.linear(w, w, out=w), lambda: lm.linear(x, w, residual=buf[:, 100:164], out=buf[:, 104:168]),
+                    lambda: lm.linear(x, w, out=torch.empty((1, 64), device="cuda", dtype=dtype).expand(40, 64)),
+                    lambda: lm.linear(x, w, buf[3, 64:128], out=buf[:, 64:128])):
+            with pytest.raises(lm.LogmelError, match="INVALID_ARG"):
+                bad()
+        want = lm.linear(x.clone(), w, residual=buf[:, 136:].clone())
+        lm.linear(x, w, residual=buf[:, 136:], out=buf[:, 136:])
+        assert torch.equal(buf[:, 136:], want)
+        lm.linear(x, w, out=buf[:, 64:128])
+        assert torch.equal(buf[:, 64:128], lm.linear(x.clone(), w))
+        rows = torch.randn((16, 64), device="cuda").to(dtype)
+        got = lm.linear(rows[8:], w, out=rows[:8])
+        assert torch.equal(got, lm.linear(rows[8:].clone(), w))

@@ -1,6 +1,6 @@
 """GB300-native log-mel front end: a thin torch binding over liblogmel.so.
 
-Every step of both operations runs in the library's CUDA kernels; this module
+Every step of every operation runs in the library's CUDA kernels; this module
 only checks tensor arguments, allocates outputs and workspaces through torch
 and passes raw pointers plus torch's current stream to the C ABI
 (include/logmel.h).  There is no CPU fallback: calls fail when the library is

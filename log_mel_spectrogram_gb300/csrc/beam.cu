@@ -13,6 +13,11 @@
 // A continuation inside a beam is ordered by its key: the logit as an ordered
 // integer, then the lower token.  Keys are distinct, so that an entry's place
 // is the number of larger ones, whatever order it is found in.
+//
+// Measured: 64 clips of 5 beams over 50001 f32 logits 29.6 us, from L2 as from
+// memory (fetching a warp's next tiles ahead into L2: 30.1 and 31.6): seven tiles a
+// warp, each with one load's latency and a chain of warp reductions, then 8 us for
+// the joins.  One clip, bf16, 10.4 us, of which launch and joins are 8.
 #include <climits>
 
 #include "f32x2.cuh"
@@ -456,7 +461,7 @@ lm_status check(const lm_beam_args *a) {
 
 // How rows are cut: vectors of a lane (8, or 2 where that leaves SMs without a
 // CTA), CTAs of a row, and tiles that each of their warps goes over: as many as
-// leave the device one round of CTAs (four an SM).
+// leave the device one round of CTAs (at most four an SM).
 struct Cut {
   int vecs, parts, tiles;
 };

@@ -6,6 +6,11 @@
 // keys or of values: block * head_dim / 64 threads work on it, 64 elements
 // (eight 8-element vectors) each, so that a unit's new tokens stay in
 // registers between the maximum and the rounding and are read once.
+//
+// Measured: 64 rows of up to 1500 tokens, 16 heads of 64, with their values
+// read back, 131 us (6.3 TB/s, 94% of copy bandwidth).  One token of 320 rows,
+// values read back, 13.8 us against 9.1 of traffic: length, table and scale are
+// loads that wait for one another, in two rounds of CTAs.
 #include <climits>
 
 #include "half.cuh"
@@ -281,7 +286,9 @@ struct ReadParams {
   uint32_t vecs;                    // of a row: count * heads * head_dim / 8
 };
 
-// Grid: (part of a row's vectors, row, layer and keys or values).
+// Grid: (part of a row's vectors, row, layer and keys or values).  Bound by its
+// output: the open blocks of 320 rows, 4 layers of 16 heads of 64, 36.5 us (197
+// MB, 5.4 TB/s; 2 vectors a thread 39.3, 8 41.9).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
   pdl_launch();
@@ -345,7 +352,8 @@ __device__ __forceinline__ int parent_row(const ReorderParams &p, int r) {
 // Grid: (part, row).  Each CTA copies its part of the row's open block (over
 // layers, keys and values, heads) from the parent's to the row's spare one.
 // The tables still show the old state meanwhile; the last CTA of a clip to
-// finish then rewrites them.
+// finish then rewrites them.  The open blocks of 320 rows, 4 layers of 16 heads
+// of 64, 11.5 us with one CTA a row (eight: 16.5).
 __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p) {
   pdl_launch();
   pdl_wait();

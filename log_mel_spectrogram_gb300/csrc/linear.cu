@@ -28,11 +28,14 @@
 // take.  Issued from one divergent thread, a product of 128 x 256 x 16 took 172
 // to 237 cycles, in competition with the epilogue; now 130.
 //
-// Measured: 24000 x 1024 -> 4096 bf16 with bias and gelu 128 us (1.57 PFLOP/s;
-// bound by the tensor pipe and, at a quarter of it, the epilogue's arithmetic);
-// 320 x 1024 -> 50001 33 us against 20 us of memory traffic; windows of 8 x 3000
-// frames, 240 -> 512 with gelu, 15 us (epilogue); 5 x 1024 -> 1024 4.5 us a call in
-// a row of calls.
+// Measured, calls in a row: 24000 x 1024 -> 4096 bf16 with bias and gelu 123 us
+// alone (1.64 PFLOP/s) and 145 us in a second-long loop, where the power limit
+// lowers the clock; bound by the tensor pipe, then the epilogue's arithmetic.
+// 320 x 1024 -> 50001 36 us against 20 us of memory traffic: every SM fetches
+// and stores whole tiles in turn, and the last of 2.6 rounds is not full.
+// Windows of 8 x 3000 frames, 240 -> 512 with gelu, 14 us: four stages of k a
+// tile, so that the epilogue's arithmetic is most of it.  5 x 1024 -> 1024 4.5
+// us: a launch, one load's latency and the cluster's exchange.
 //
 // Operands that TMA cannot address (rows off 16-byte boundaries) are first
 // copied into padded rows in the workspace.
@@ -682,9 +685,9 @@ struct Cut {
 };
 
 // The cut with the least estimated time, in microseconds.  The constants are
-// fitted to 160 problems of 5 to 24000 rows, k of 256 to 4096 and 256 to 10000
-// outputs; the estimate's choice was within 7% of the best one of all cuts for
-// nine in ten of them.
+// fitted to 256 problems of 5 to 24000 rows, k of 256 to 4096 and 256 to 10000
+// outputs; the estimate's choice was 0.6% slower than the best of all cuts in the
+// geometric mean, and within 7% of it for 96 in 100.
 //   first tile: 3, a stage's latency or its traffic at 185 KB/us for each block
 //     of k, and the epilogue's 0.008 a column;
 //   each further round of tiles: the most of traffic (140 KB/us per SM with all

@@ -1,7 +1,7 @@
 // kv_attend.cu -- attention over the 8-bit key/value cache.
 //
 // A CTA serves one row and key head: the row's queries that read that head
-// (tokens x group) fill tiles of 16 or 32 rows, and each of its four warps
+// (tokens x group) fill tiles of 16 rows, and each of its four warps
 // walks its own tiles of 32 tokens with a running maximum and sum per row.  A
 // warp fetches keys and values -- contiguous pieces of a block -- by bulk
 // copies into a ring of its own, so warps never wait for one another until
@@ -26,7 +26,7 @@
 // Long rows are split over CTAs; the last one to finish a row and head joins
 // the parts in order.
 //
-// Prompts, with more than 32 query rows, take another form (SHARED below): four
+// Many prompts take another form (SHARED below): four
 // warps of 16 rows over the same tokens, whose bytes become f16 once per CTA
 // (223 causal queries over up to 448 tokens, 16 rows of 16 heads: 37 -> 33 us).
 //
@@ -52,6 +52,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = 32;              // tokens of a warp's tile
+constexpr int kRows = 16;             // query rows of a warp
 constexpr int kMinChunk = 512;        // tokens below which a row is not split
 constexpr int kBalance = 2048;        // ... where parts are for balance only (512: 44 us, 1024: 39, none: 36 for
                                       // 1024 units of up to 1500 tokens)
@@ -82,18 +83,17 @@ struct AttendParams {
 };
 
 // Shared memory: the rings (at the end the warps' partial results), then this.
-template <int R>
 struct Shared {
   uint64_t full[kWarps][8];
-  float2 ml[kWarps][R];  // maximum and sum per warp and query row
+  float2 ml[kWarps][kRows];  // maximum and sum per warp and query row
   int abort;
   int last;
 };
 
-constexpr int big_bytes(int d, int mt, bool shared) {
+constexpr int big_bytes(int d, bool shared) {
   // (Shared: and two tiles as f16.)
   const int ring = (shared ? 1 : kWarps) * ring_stages(d, shared) * stage_bytes(d) + (shared ? 4 * stage_bytes(d) : 0);
-  const int joined = kWarps * 16 * mt * d * 4;
+  const int joined = kWarps * kRows * d * 4;
   return ring > joined ? ring : joined;
 }
 
@@ -146,22 +146,22 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
 }
 
 // SHARED, for many query rows: the warps have 16 each and go over the same
-// tokens, in one ring, instead of sharing out the tokens of 16 * MT rows.  Each
+// tokens, in one ring, instead of sharing out the tokens of 16 rows.  Each
 // warp turns a quarter of a tile into f16 in shared memory, laid out so that
 // ldmatrix gives all warps the operands that they would make of the bytes
 // themselves (250 instructions a tile and warp instead of 400).  E = 1: at most
 // eight query rows, so that the lower half of a product's rows is left out of
-// the softmax (55 of 400 instructions a tile).
-template <typename T, int D, int MT, int E, bool SHARED>
-__global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? resident_ctas(D) : 2)
+// the softmax (55 of 400 instructions a tile; 5 queries of 64 rows over up to
+// 1500 tokens: 40.2 -> 38.6 us).
+template <typename T, int D, int E, bool SHARED>
+__global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : resident_ctas(D))
     attend_kernel(const AttendParams p) {
   constexpr int STAGES = ring_stages(D, SHARED);
   constexpr int KW = D / 16;   // 32-bit words of a token's key per thread; also 16-element steps of k
   constexpr int VB = D / 8;    // bytes of a token's value per thread; also 8-column tiles of the output
-  constexpr int R = 16 * MT;            // query rows of a warp
-  constexpr int QT = SHARED ? kWarps * R : R;  // ... and of the CTA
+  constexpr int QT = SHARED ? kWarps * kRows : kRows;  // query rows of the CTA
   extern __shared__ __align__(128) uint8_t smem[];
-  Shared<R> &sh = *reinterpret_cast<Shared<R> *>(smem + big_bytes(D, MT, SHARED));
+  Shared &sh = *reinterpret_cast<Shared *>(smem + big_bytes(D, SHARED));
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r8 = lane / 4, c4 = lane % 4;
   // Grid: (key heads and parts, row, tile of queries).  Later queries see more:
@@ -192,37 +192,34 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
     for (int e = 0; e < 2; ++e) early[e] = __ldg(table + min((t + 16 * e) >> block_shift, p.c.width - 1));
   }
   const int q_first = qt * QT, q_rows = min(QT, p.qrows - q_first);
-  uint32_t raw[MT][E][2 * KW];
-  int q_i[MT][E];
+  uint32_t raw[E][2 * KW];
+  int q_i[E];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int e = 0; e < E; ++e) {
+    const int at = q_first + (SHARED ? warp * kRows : 0) + 8 * e + r8;
+    const bool in = at < p.qrows;
+    const int i = !in ? 0 : p.group == 1 ? at : at / p.group, g = in ? at - i * p.group : 0;
+    q_i[e] = in ? i : -1;
+    const T *const src = static_cast<const T *>(p.q) + row * p.row_s + i * p.tok_s +
+                         (static_cast<int64_t>(h) * p.group + g) * p.head_s + c4 * (D / 4);
+    uint32_t *const w = raw[e];
+    if (!in) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int at = q_first + (SHARED ? warp * R : 0) + 16 * m + 8 * e + r8;
-      const bool in = at < p.qrows;
-      const int i = !in ? 0 : p.group == 1 ? at : at / p.group, g = in ? at - i * p.group : 0;
-      q_i[m][e] = in ? i : -1;
-      const T *const src = static_cast<const T *>(p.q) + row * p.row_s + i * p.tok_s +
-                           (static_cast<int64_t>(h) * p.group + g) * p.head_s + c4 * (D / 4);
-      uint32_t *const w = raw[m][e];
-      if (!in) {
+      for (int j = 0; j < 2 * KW; ++j) w[j] = 0;
+    } else if (p.qvec) {
 #pragma unroll
-        for (int j = 0; j < 2 * KW; ++j) w[j] = 0;
-      } else if (p.qvec) {
-#pragma unroll
-        for (int j = 0; j < 2 * KW; j += 4) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + 2 * j));
-          w[j] = v.x;
-          w[j + 1] = v.y;
-          w[j + 2] = v.z;
-          w[j + 3] = v.w;
-        }
-      } else {
-        const uint16_t *const s16 = reinterpret_cast<const uint16_t *>(src);
-#pragma unroll
-        for (int j = 0; j < 2 * KW; ++j)
-          w[j] = s16[2 * j] | static_cast<uint32_t>(s16[2 * j + 1]) << 16;
+      for (int j = 0; j < 2 * KW; j += 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + 2 * j));
+        w[j] = v.x;
+        w[j + 1] = v.y;
+        w[j + 2] = v.z;
+        w[j + 3] = v.w;
       }
+    } else {
+      const uint16_t *const s16 = reinterpret_cast<const uint16_t *>(src);
+#pragma unroll
+      for (int j = 0; j < 2 * KW; ++j)
+        w[j] = s16[2 * j] | static_cast<uint32_t>(s16[2 * j + 1]) << 16;
     }
   }
   __syncthreads();
@@ -305,67 +302,61 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
   // times a power of two that puts the row's largest between 2^14 and 2^15:
   // exact but for values below 2^-28 of that one, which are off by 2^-39 of
   // it.  (Bytes turn into f16 in two instructions, into bf16 in three.)
-  uint32_t q[MT][KW][4];
-  int limit[MT][E];
+  uint32_t q[KW][4];
+  int limit[E];
   // Key bytes go in as (k + 128) * 2^-24, which takes half the instructions of
   // k: a score is product * 2^24 - 128 * (sum of q).  (The sums are in 32 bits;
   // 128 sum q is of the size of the largest scores the block's scale allows.)
-  float back[MT][E];  // the power's inverse, times scale, log2 e and 2^24
-  float bias[MT][E];  // 128 * 2^-24 * sum of q
+  float back[E];  // the power's inverse, times scale, log2 e and 2^24
+  float bias[E];  // 128 * 2^-24 * sum of q
   const float log2e = 1.4426950408889634f;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int e = 0; e < E; ++e) {
+    const int i = q_i[e];
+    limit[e] = i < 0 ? INT_MAX : !p.causal ? total : i < fresh ? min(total, held + i + 1) : 0;
+    uint32_t *const w = raw[e];
+    back[e] = p.scale * log2e * 16777216.0f;
+    if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+      uint32_t top = 0;  // |q| as integers
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int i = q_i[m][e];
-      limit[m][e] = i < 0 ? INT_MAX : !p.causal ? total : i < fresh ? min(total, held + i + 1) : 0;
-      uint32_t *const w = raw[m][e];
-      back[m][e] = p.scale * log2e * 16777216.0f;
-      if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
-        uint32_t top = 0;  // |q| as integers
-#pragma unroll
-        for (int j = 0; j < 2 * KW; ++j) top = max(top, max(w[j] << 16 & 0x7fffffffu, w[j] & 0x7fff0000u));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        uint32_t ex = max(top >> 23, 15u);
-        if (ex == 255) ex = 141;  // infinity or NaN: as it is
-        const float up = __uint_as_float((268 - ex) << 23);
-        back[m][e] *= __uint_as_float((ex - 14) << 23);
-#pragma unroll
-        for (int j = 0; j < 2 * KW; ++j) {
-          const float2 f = unpack2<T>(w[j]);
-          w[j] = pack2<__half>(f.x * up, f.y * up);
-        }
-      }
-      float total_q = 0.0f;
+      for (int j = 0; j < 2 * KW; ++j) top = max(top, max(w[j] << 16 & 0x7fffffffu, w[j] & 0x7fff0000u));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      uint32_t ex = max(top >> 23, 15u);
+      if (ex == 255) ex = 141;  // infinity or NaN: as it is
+      const float up = __uint_as_float((268 - ex) << 23);
+      back[e] *= __uint_as_float((ex - 14) << 23);
 #pragma unroll
       for (int j = 0; j < 2 * KW; ++j) {
-        const float2 f = unpack2<__half>(w[j]);
-        total_q += f.x + f.y;
+        const float2 f = unpack2<T>(w[j]);
+        w[j] = pack2<__half>(f.x * up, f.y * up);
       }
-      total_q += __shfl_xor_sync(0xffffffffu, total_q, 1);
-      total_q += __shfl_xor_sync(0xffffffffu, total_q, 2);
-      bias[m][e] = total_q * (128.0f / 16777216.0f);
+    }
+    float total_q = 0.0f;
 #pragma unroll
-      for (int s = 0; s < KW; ++s) {
-        q[m][s][e] = w[2 * s];
-        q[m][s][2 + e] = w[2 * s + 1];
-        if (E == 1) q[m][s][1] = q[m][s][3] = 0;
-      }
+    for (int j = 0; j < 2 * KW; ++j) {
+      const float2 f = unpack2<__half>(w[j]);
+      total_q += f.x + f.y;
+    }
+    total_q += __shfl_xor_sync(0xffffffffu, total_q, 1);
+    total_q += __shfl_xor_sync(0xffffffffu, total_q, 2);
+    bias[e] = total_q * (128.0f / 16777216.0f);
+#pragma unroll
+    for (int s = 0; s < KW; ++s) {
+      q[s][e] = w[2 * s];
+      q[s][2 + e] = w[2 * s + 1];
+      if (E == 1) q[s][1] = q[s][3] = 0;
     }
   }
 
-  float acc[MT][VB][4];
-  float top[MT][E], sum[MT][E];
+  float acc[VB][4];
+  float top[E], sum[E];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int j = 0; j < VB; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < VB; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      top[m][e] = -INFINITY;
-      sum[m][e] = 0.0f;
-    }
+  for (int e = 0; e < E; ++e) {
+    top[e] = -INFINITY;
+    sum[e] = 0.0f;
   }
 
   // Byte n of two words, in the low bytes of the halves.
@@ -425,18 +416,17 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
     }
 
     // Scores: column n of 8-token tile n8 is token 16 (n8/2) + 8 (n8%2) + n/2 + 4 (n%2).
-    float sc[MT][4][4];
+    float sc[4][4];
 #pragma unroll
     for (int n8 = 0; n8 < 4; ++n8) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) sc[m][n8][0] = sc[m][n8][1] = sc[m][n8][2] = sc[m][n8][3] = 0.0f;
+      sc[n8][0] = sc[n8][1] = sc[n8][2] = sc[n8][3] = 0.0f;
       if constexpr (SHARED) {
 #pragma unroll
         for (int k2 = 0; k2 < KW / 2; ++k2) {
           uint32_t b[4];
           ldmatrix4<false>(b, k16 + piece_at<D>(8 * n8 + lane % 8, 4 * k2 + lane / 8));
-          mma16816(sc[0][n8], q[0][2 * k2], b[0], b[1]);
-          mma16816(sc[0][n8], q[0][2 * k2 + 1], b[2], b[3]);
+          mma16816(sc[n8], q[2 * k2], b[0], b[1]);
+          mma16816(sc[n8], q[2 * k2 + 1], b[2], b[3]);
         }
       } else {
         const int tok = 16 * (n8 / 2) + 8 * (n8 & 1) + (r8 >> 1) + 4 * (r8 & 1);
@@ -446,8 +436,7 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
         for (int ks = 0; ks < KW; ++ks) {
           uint32_t b0, b1;
           bytes_to_subnormal(w[ks], b0, b1);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) mma16816(sc[m][n8], q[m][ks], b0, b1);
+          mma16816(sc[n8], q[ks], b0, b1);
         }
       }
     }
@@ -455,97 +444,91 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
     const float l0 = __shfl_sync(0xffffffffu, l_s[0], j % 32), l1 = __shfl_sync(0xffffffffu, l_s[1], j % 32);
     const float i0 = __shfl_sync(0xffffffffu, i_s[0], j % 32), i1 = __shfl_sync(0xffffffffu, i_s[1], j % 32);
     const bool partial = i0 < 0.0f || i1 < 0.0f;
+    bool cut = partial;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      bool cut = partial;
+    for (int e = 0; e < E; ++e) {
+      const float g0 = f0 * back[e], g1 = f1 * back[e];
+      const float h0 = fmaf(-g0, bias[e], l0), h1 = fmaf(-g1, bias[e], l1);
+#pragma unroll
+      for (int n8 = 0; n8 < 4; ++n8) {
+#pragma unroll
+        for (int x = 2 * e; x < 2 * e + 2; ++x)
+          sc[n8][x] = fmaf(sc[n8][x], n8 < 2 ? g0 : g1, n8 < 2 ? h0 : h1);
+      }
+      cut = cut || t0 > limit[e] - kTok;
+    }
+    // Tokens past a row's end, and absent ones.  (Selected, not added: their
+    // bytes and scales may be anything.)
+    if (__any_sync(0xffffffffu, cut)) {
+#pragma unroll
+      for (int n8 = 0; n8 < 4; ++n8) {
+        const bool absent = (n8 < 2 ? i0 : i1) < 0.0f;
+#pragma unroll
+        for (int x = 0; x < 2 * E; ++x) {
+          const int tok = t0 + 16 * (n8 / 2) + 8 * (n8 & 1) + c4 + 4 * (x & 1);
+          if (absent || tok >= limit[x >> 1]) sc[n8][x] = -INFINITY;
+        }
+      }
+    }
+    float next[E];
+    bool rise = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float t = top[e];
+#pragma unroll
+      for (int n8 = 0; n8 < 4; ++n8) t = fmaxf(t, fmaxf(sc[n8][2 * e], sc[n8][2 * e + 1]));
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+      next[e] = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      rise = rise || next[e] > top[e];
+    }
+    // Maxima rise ever more rarely along a row.
+    if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float g0 = f0 * back[m][e], g1 = f1 * back[m][e];
-        const float h0 = fmaf(-g0, bias[m][e], l0), h1 = fmaf(-g1, bias[m][e], l1);
+        const float shrink = ex2(top[e] - (next[e] == -INFINITY ? 0.0f : next[e]));
+        top[e] = next[e];
+        sum[e] *= shrink;
 #pragma unroll
-        for (int n8 = 0; n8 < 4; ++n8) {
-#pragma unroll
-          for (int x = 2 * e; x < 2 * e + 2; ++x)
-            sc[m][n8][x] = fmaf(sc[m][n8][x], n8 < 2 ? g0 : g1, n8 < 2 ? h0 : h1);
+        for (int n = 0; n < VB; ++n) {
+          acc[n][2 * e] *= shrink;
+          acc[n][2 * e + 1] *= shrink;
         }
-        cut = cut || t0 > limit[m][e] - kTok;
       }
-      // Tokens past a row's end, and absent ones.  (Selected, not added: their
-      // bytes and scales may be anything.)
-      if (__any_sync(0xffffffffu, cut)) {
+    }
 #pragma unroll
-        for (int n8 = 0; n8 < 4; ++n8) {
-          const bool absent = (n8 < 2 ? i0 : i1) < 0.0f;
+    for (int e = 0; e < E; ++e) {
+      const float zero = top[e] == -INFINITY ? 0.0f : top[e];
+      float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-          for (int x = 0; x < 2 * E; ++x) {
-            const int tok = t0 + 16 * (n8 / 2) + 8 * (n8 & 1) + c4 + 4 * (x & 1);
-            if (absent || tok >= limit[m][x >> 1]) sc[m][n8][x] = -INFINITY;
+      for (int n8 = 0; n8 < 4; ++n8) {
+#pragma unroll
+        for (int x = 2 * e; x < 2 * e + 2; ++x) {
+          const float w = ex2(sc[n8][x] - zero);
+          sc[n8][x] = w;
+          if (n8 < 2) {
+            s0 += w;
+          } else {
+            s1 += w;
           }
         }
       }
-      float next[E];
-      bool rise = false;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float t = top[m][e];
-#pragma unroll
-        for (int n8 = 0; n8 < 4; ++n8) t = fmaxf(t, fmaxf(sc[m][n8][2 * e], sc[m][n8][2 * e + 1]));
-        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-        next[e] = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-        rise = rise || next[e] > top[m][e];
-      }
-      // Maxima rise ever more rarely along a row.
-      if (__any_sync(0xffffffffu, rise)) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float shrink = ex2(top[m][e] - (next[e] == -INFINITY ? 0.0f : next[e]));
-          top[m][e] = next[e];
-          sum[m][e] *= shrink;
-#pragma unroll
-          for (int n = 0; n < VB; ++n) {
-            acc[m][n][2 * e] *= shrink;
-            acc[m][n][2 * e + 1] *= shrink;
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float zero = top[m][e] == -INFINITY ? 0.0f : top[m][e];
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int n8 = 0; n8 < 4; ++n8) {
-#pragma unroll
-          for (int x = 2 * e; x < 2 * e + 2; ++x) {
-            const float w = ex2(sc[m][n8][x] - zero);
-            sc[m][n8][x] = w;
-            if (n8 < 2) {
-              s0 += w;
-            } else {
-              s1 += w;
-            }
-          }
-        }
-        sum[m][e] = fmaf(s0, fabsf(i0), fmaf(s1, fabsf(i1), sum[m][e]));
-      }
+      sum[e] = fmaf(s0, fabsf(i0), fmaf(s1, fabsf(i1), sum[e]));
     }
     // Values: this thread's bytes VB r8 .. + VB-1 of every fourth token.
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      uint32_t a[MT][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        a[m][0] = pack2<__half>(sc[m][2 * half][0], sc[m][2 * half][1]);
-        a[m][1] = E == 1 ? 0u : pack2<__half>(sc[m][2 * half][2], sc[m][2 * half][3]);
-        a[m][2] = pack2<__half>(sc[m][2 * half + 1][0], sc[m][2 * half + 1][1]);
-        a[m][3] = E == 1 ? 0u : pack2<__half>(sc[m][2 * half + 1][2], sc[m][2 * half + 1][3]);
-      }
+      uint32_t a[4];
+      a[0] = pack2<__half>(sc[2 * half][0], sc[2 * half][1]);
+      a[1] = E == 1 ? 0u : pack2<__half>(sc[2 * half][2], sc[2 * half][3]);
+      a[2] = pack2<__half>(sc[2 * half + 1][0], sc[2 * half + 1][1]);
+      a[3] = E == 1 ? 0u : pack2<__half>(sc[2 * half + 1][2], sc[2 * half + 1][3]);
       if constexpr (SHARED) {
 #pragma unroll
         for (int n = 0; n < VB; n += 2) {
           uint32_t b[4];
           ldmatrix4<true>(b, v16 + piece_at<D>(16 * half + lane % 16, n + lane / 16));
-          mma16816(acc[0][n], a[0], b[0], b[1]);
-          mma16816(acc[0][n + 1], a[0], b[2], b[3]);
+          mma16816(acc[n], a, b[0], b[1]);
+          mma16816(acc[n + 1], a, b[2], b[3]);
         }
       } else {
         uint32_t w[4][VB / 4];
@@ -556,8 +539,7 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
           // Byte n of tokens c4, c4 + 4 and of c4 + 8, c4 + 12.
           const uint32_t b0 = bytes_to_f16(__byte_perm(w[0][n / 4], w[1][n / 4], kPick[n % 4]));
           const uint32_t b1 = bytes_to_f16(__byte_perm(w[2][n / 4], w[3][n / 4], kPick[n % 4]));
-#pragma unroll
-          for (int m = 0; m < MT; ++m) mma16816(acc[m][n], a[m], b0, b1);
+          mma16816(acc[n], a, b0, b1);
         }
       }
     }
@@ -573,22 +555,19 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
   // The four warps' parts meet in the ring's memory.
   float *const acc_s = reinterpret_cast<float *>(smem);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int e = 0; e < E; ++e) {
+    const int rr = 8 * e + r8;
+    float s = sum[e];
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    if (c4 == 0) sh.ml[warp][rr] = make_float2(top[e], s);
+    if ((SHARED ? warp * kRows : 0) + rr < q_rows) {
+      float4 *const o = reinterpret_cast<float4 *>(acc_s + (warp * kRows + rr) * D + c4 * (D / 4));
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int rr = 16 * m + 8 * e + r8;
-      float s = sum[m][e];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      if (c4 == 0) sh.ml[warp][rr] = make_float2(top[m][e], s);
-      if ((SHARED ? warp * R : 0) + rr < q_rows) {
-        float4 *const o = reinterpret_cast<float4 *>(acc_s + (warp * R + rr) * D + c4 * (D / 4));
-#pragma unroll
-        for (int n = 0; n < VB; n += 4) {
-          o[n / 4] = make_float4(acc[m][n][2 * e], acc[m][n + 1][2 * e], acc[m][n + 2][2 * e], acc[m][n + 3][2 * e]);
-          o[(VB + n) / 4] = make_float4(acc[m][n][2 * e + 1], acc[m][n + 1][2 * e + 1], acc[m][n + 2][2 * e + 1],
-                                        acc[m][n + 3][2 * e + 1]);
-        }
+      for (int n = 0; n < VB; n += 4) {
+        o[n / 4] = make_float4(acc[n][2 * e], acc[n + 1][2 * e], acc[n + 2][2 * e], acc[n + 3][2 * e]);
+        o[(VB + n) / 4] = make_float4(acc[n][2 * e + 1], acc[n + 1][2 * e + 1], acc[n + 2][2 * e + 1],
+                                      acc[n + 3][2 * e + 1]);
       }
     }
   }
@@ -608,15 +587,15 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : MT == 1 ? re
     const float2 *const ml_s = &sh.ml[0][0];  // SHARED: row rr is in place rr; else in warp w's place rr
     constexpr int FROM = SHARED ? 1 : kWarps;
 #pragma unroll
-    for (int w = 0; w < FROM; ++w) t = fmaxf(t, ml_s[w * R + rr].x);
+    for (int w = 0; w < FROM; ++w) t = fmaxf(t, ml_s[w * kRows + rr].x);
     const float zero = t == -INFINITY ? 0.0f : t;
     float4 v = make_float4(0, 0, 0, 0);
     float l = 0.0f;
 #pragma unroll
     for (int w = 0; w < FROM; ++w) {
-      const float2 ml = ml_s[w * R + rr];
+      const float2 ml = ml_s[w * kRows + rr];
       const float f = ex2(ml.x - zero);
-      const float4 a = *reinterpret_cast<const float4 *>(acc_s + (w * R + rr) * D + d);
+      const float4 a = *reinterpret_cast<const float4 *>(acc_s + (w * kRows + rr) * D + d);
       v.x = fmaf(a.x, f, v.x);
       v.y = fmaf(a.y, f, v.y);
       v.z = fmaf(a.z, f, v.z);
@@ -671,11 +650,20 @@ lm_status check(const lm_kv_cache *cache, int32_t tokens, int32_t q_heads) {
   return LM_OK;
 }
 
+// Key heads and tiles of 64 query rows from which the SHARED form is taken, where
+// at most a fifth of those tiles is empty.  It takes 1.2 to 1.8 times less time a
+// query row on a full device, but a CTA of it walks all tokens alone.  Both in us,
+// SHARED last: 64 rows x 16 heads over 1500 tokens, 64 queries 114 / 109, 128
+// 207 / 174, 96 (a third of two tiles empty) 160 / 176; 16 rows x 16 heads over
+// 448, 128 queries (512 tiles) 29.1 / 26.4, 64 (256 tiles) 18.0 / 21.6; 8 rows x
+// 8 heads, 448 queries (448) 43 / 29, 223 (256) 25.5 / 25.9, 64 (64) 11.4 / 20.
+constexpr int64_t kSharedTiles = 400;
+
 // How a call is cut: query rows per tile, tiles, units (row, key head, tile)
 // and parts of the tokens.
 struct Cut {
   bool shared;
-  int mt, qrows, qtiles, splits, part_rows, chunk;
+  int qrows, qtiles, splits, part_rows, chunk;
   int64_t units;
   size_t done_bytes, ml_bytes, acc_bytes;
 };
@@ -683,9 +671,9 @@ struct Cut {
 Cut cut(const lm_kv_cache *c, int32_t tokens, int32_t q_heads) {
   Cut k;
   k.qrows = tokens * (q_heads / c->heads);
-  k.shared = k.qrows > 32;
-  k.mt = k.qrows > 16 && !k.shared ? 2 : 1;
-  const int tile = k.shared ? 16 * kWarps : 16 * k.mt;
+  const int64_t big = (static_cast<int64_t>(k.qrows) + kWarps * kRows - 1) / (kWarps * kRows);
+  k.shared = big * c->rows * c->heads >= kSharedTiles && 5 * static_cast<int64_t>(k.qrows) >= 4 * big * kWarps * kRows;
+  const int tile = k.shared ? kWarps * kRows : kRows;
   k.qtiles = (k.qrows + tile - 1) / tile;
   k.part_rows = k.qrows < tile ? k.qrows : tile;
   k.units = static_cast<int64_t>(c->rows) * c->heads * k.qtiles;
@@ -709,19 +697,18 @@ Cut cut(const lm_kv_cache *c, int32_t tokens, int32_t q_heads) {
   return k;
 }
 
-template <typename T, int D, int MT, int E, bool SHARED>
+template <typename T, int D, int E, bool SHARED>
 lm_status launch(const AttendParams &p, dim3 grid, cudaStream_t s) {
-  auto *const kernel = attend_kernel<T, D, MT, E, SHARED>;
-  constexpr int smem = big_bytes(D, MT, SHARED) + static_cast<int>(sizeof(Shared<16 * MT>));
+  auto *const kernel = attend_kernel<T, D, E, SHARED>;
+  constexpr int smem = big_bytes(D, SHARED) + static_cast<int>(sizeof(Shared));
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
   return launch_dependent(kernel, grid, kThreads, smem, s, 1, p);
 }
 
 template <typename T, int D>
 lm_status launch_form(const AttendParams &p, const Cut &k, dim3 grid, cudaStream_t s) {
-  if (k.shared) return launch<T, D, 1, 2, true>(p, grid, s);
-  if (k.qrows <= 8) return launch<T, D, 1, 1, false>(p, grid, s);
-  return k.mt == 1 ? launch<T, D, 1, 2, false>(p, grid, s) : launch<T, D, 2, 2, false>(p, grid, s);
+  if (k.shared) return launch<T, D, 2, true>(p, grid, s);
+  return k.qrows <= 8 ? launch<T, D, 1, false>(p, grid, s) : launch<T, D, 2, false>(p, grid, s);
 }
 
 template <typename T>

@@ -17,7 +17,7 @@
 // Measured: 64 clips of 5 beams over 50001 f32 logits 29.6 us, from L2 as from
 // memory (fetching a warp's next tiles ahead into L2: 30.1 and 31.6): seven tiles a
 // warp, each with one load's latency and a chain of warp reductions, then 8 us for
-// the joins.  One clip, bf16, 10.4 us, of which launch and joins are 8.
+// the joins.  One clip, bf16, 10.8 us, of which launch and joins are 8.
 #include <climits>
 
 #include "f32x2.cuh"
@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 2) beam_kernel(
   __shared__ float tot[kMaxBeams * kMaxBeams];
   __shared__ int tok[kMaxBeams * kMaxBeams];
   __shared__ int parents[kMaxBeams], tokens[kMaxBeams];
+  __shared__ bool over[kMaxBeams];
   __shared__ int32_t history[kHistory];
   __shared__ bool last;
   pdl_launch();
@@ -396,44 +397,50 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 2) beam_kernel(
         token = key_token(l);
       }
       if (!(t == t)) t = -INFINITY;
-      tot[b * n + lane] = t;
+      tot[b * n + lane] = t + 0.0f;  // -0 as 0
       tok[b * n + lane] = token;
+      if (lane == 0) over[b] = ended;
     }
     __syncwarp();
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  // Then all threads find each offer's place among the clip's.
-  for (int i = threadIdx.x; i < n * n; i += kThreads) {
-    const int b = i / n, c = i % n;
-    if (c >= places) continue;
-    const float t = tot[i];
-    int place = 0;
-    if (n <= 8 && places == n) {
+  // Offer i takes its place.
+  auto select = [&](int i, int place) {
+    const int b = i / n;
+    const int64_t at = row0 + place;
+    a.out_scores[at] = tot[i];
+    a.out_tokens[at] = tok[i];
+    a.out_parents[at] = b;
+    a.out_finished[at] = over[b] || tok[i] == a.eos;
+    parents[place] = b;
+    tokens[place] = tok[i];
+  };
+  if (n <= 8 && places == n) {
+    // A thread per offer counts those in front of it.
+    const int i = threadIdx.x;
+    if (i < n * n) {
+      const float t = tot[i];
+      int place = 0;
       for (int j = 0; j < n * n; ++j) {
         const float u = tot[j];
         place += u > t || (u == t && j < i);
       }
-    } else {
-      for (int j = 0; j < n && place < n; ++j) {
-        // Beam j's list is sorted: count what goes in front.
-        for (int k = 0; k < places; ++k) {
-          const float u = tot[j * n + k];
-          if (!(u > t || (u == t && j * n + k < i))) break;
-          ++place;
-        }
-      }
+      if (place < n) select(i, place);
     }
-    if (place < n) {
-      const int64_t at = row0 + place;
-      const bool was = a.finished && a.finished[row0 + b];
-      a.out_scores[at] = t;
-      a.out_tokens[at] = tok[i];
-      a.out_parents[at] = b;
-      a.out_finished[at] = was || tok[i] == a.eos;
-      parents[place] = b;
-      tokens[place] = tok[i];
+  } else if (warp == 0) {
+    // A beam's offers are in order: a lane per beam, and the best head n times
+    // (5 beams of 1000 logits 7.8 us so, 7.1 by counting; 16 beams 12.6 and 15.6).
+    int next = 0, mine = 0;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t head = lane < n && next < places ? float_to_ordered(tot[lane * n + next]) : 0;
+      const uint32_t best = __reduce_max_sync(0xffffffffu, head);
+      const int who = __ffs(__ballot_sync(0xffffffffu, head == best)) - 1;
+      const int offer = who * n + __shfl_sync(0xffffffffu, next, who);
+      if (lane == i) mine = offer;
+      next += lane == who;
     }
+    if (lane < n) select(mine, lane);
   }
   if (told == 0) return;
   __syncthreads();
@@ -459,9 +466,12 @@ lm_status check(const lm_beam_args *a) {
   return LM_OK;
 }
 
-// How rows are cut: vectors of a lane (8, or 2 where that leaves SMs without a
-// CTA), CTAs of a row, and tiles that each of their warps goes over: as many as
-// leave the device one round of CTAs (at most four an SM).
+// How rows are cut: vectors of a lane, CTAs of a row, and tiles that each of their
+// warps goes over: as many as leave the device one round of CTAs (at most four an
+// SM).  Two vectors instead of eight where SMs would else have no CTA, as long as
+// a row's parts have no more keys than are ranked at once (one clip of 5 beams,
+// 10001 bf16 logits: 8.1 against 8.4 us; 16 beams, 15.6 against 17.0 for 1000
+// logits, but 26.1 against 19.9 for 50001, which are 13 parts).
 struct Cut {
   int vecs, parts, tiles;
 };
@@ -470,7 +480,8 @@ Cut cut(const lm_beam_args &a) {
   const int64_t rows = a.clips * a.beams, values = kWarps * 32 * (a.dtype == LM_F32 ? 4 : 8);
   Cut c;
   const int64_t big = (a.vocab + 8 * values - 1) / (8 * values);
-  c.vecs = rows * big < 152 ? 2 : 8;
+  const int64_t small = (a.vocab + 2 * values - 1) / (2 * values);
+  c.vecs = rows * big < 152 && small * a.beams <= kGather ? 2 : 8;
   const int64_t all = (a.vocab + c.vecs * values - 1) / (c.vecs * values);
   const int64_t parts = c.vecs == 2 ? all : 4 * 152 / rows > 1 ? 4 * 152 / rows : 1;
   c.tiles = static_cast<int>(parts < all ? (all + parts - 1) / parts : 1);

@@ -30,8 +30,8 @@
 // warps of 16 rows over the same tokens, whose bytes become f16 once per CTA
 // (223 causal queries over up to 448 tokens, 16 rows of 16 heads: 37 -> 33 us).
 //
-// Measured: 5 queries of 64 rows over up to 1500 tokens, 16 heads of 64, 37 us
-// (3.3 TB/s: 1024 CTAs in two rounds, each 4 us of start-up and end, then per
+// Measured: 5 queries of 64 rows over up to 1500 tokens, 16 heads of 64, 36 us
+// (3.4 TB/s: 1024 CTAs in two rounds, each 4 us of start-up and end, then per
 // tile the issue of about 400 instructions a warp); two rows of 131000 tokens,
 // 8 heads of 128, 95 us (5.7 TB/s, 85% of copy bandwidth); a step of 5 rows of
 // up to 448 tokens, 6.4 us (launch, three dependent loads, the join of 4 warps).

@@ -28,12 +28,13 @@
 // take.  Issued from one divergent thread, a product of 128 x 256 x 16 took 172
 // to 237 cycles, in competition with the epilogue; now 130.
 //
-// Measured, calls in a row: 24000 x 1024 -> 4096 bf16 with bias and gelu 123 us
-// alone (1.64 PFLOP/s) and 145 us in a second-long loop, where the power limit
-// lowers the clock; bound by the tensor pipe, then the epilogue's arithmetic.
+// Measured, calls in a row: 24000 x 1024 -> 4096 bf16 with bias and gelu 122 us
+// alone (1.65 PFLOP/s; 112 without gelu) and 144 us in a second-long loop, where
+// the power limit lowers the clock; bound by the tensor pipe, then the epilogue's
+// arithmetic.
 // 320 x 1024 -> 50001 36 us against 20 us of memory traffic: every SM fetches
 // and stores whole tiles in turn, and the last of 5.2 rounds is not full.
-// Windows of 8 x 3000 frames, 240 -> 512 with gelu, 14 us: four stages of k a
+// Windows of 8 x 3000 frames, 240 -> 512 with gelu, 13 us: four stages of k a
 // tile, so that the epilogue's arithmetic is most of it.  5 x 1024 -> 1024 4.5
 // us: a launch, one load's latency and the cluster's exchange.
 //

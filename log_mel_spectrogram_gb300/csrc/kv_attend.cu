@@ -745,14 +745,14 @@ extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const
   for (int i = 0; i < 3; ++i)
     if (q_strides[i] < 0) return LM_ERR_INVALID_ARG;
   if (!aligned(q, 2) || !aligned(out, 16) || !aligned(workspace, 16)) return LM_ERR_MISALIGNED;
+  const Cut k = cut(cache, tokens, q_heads);
+  if (!workspace || workspace_bytes < 256 + k.done_bytes + k.ml_bytes + k.acc_bytes) return LM_ERR_WORKSPACE;
   // A part of a row may still read queries when another writes its output.
   const int64_t head_bytes = 2 * cache->head_dim;
   const int64_t row_bytes = 2 * ((tokens - 1) * q_strides[1] + (q_heads - 1) * q_strides[2]) + head_bytes;
   if (rows_meet({q, cache->rows, 2 * q_strides[0], row_bytes},
                 {out, 1, 0, static_cast<int64_t>(cache->rows) * tokens * q_heads * head_bytes}))
     return LM_ERR_INVALID_ARG;
-  const Cut k = cut(cache, tokens, q_heads);
-  if (!workspace || workspace_bytes < 256 + k.done_bytes + k.ml_bytes + k.acc_bytes) return LM_ERR_WORKSPACE;
   if (cache->rows > 65535 || k.qtiles > 65535 || static_cast<int64_t>(cache->heads) * k.splits > INT_MAX)
     return LM_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(cache->heads) * k.splits, cache->rows, k.qtiles);

@@ -14,10 +14,10 @@
 // integer, then the lower token.  Keys are distinct, so that an entry's place
 // is the number of larger ones, whatever order it is found in.
 //
-// Measured: 64 clips of 5 beams over 50001 f32 logits 29.6 us, from L2 as from
-// memory (fetching a warp's next tiles ahead into L2: 30.1 and 31.6): seven tiles a
-// warp, each with one load's latency and a chain of warp reductions, then 8 us for
-// the joins.  One clip, bf16, 10.8 us, of which launch and joins are 8.
+// Measured: 64 clips of 5 beams over 50001 f32 logits 27.8 us where the linear
+// layer left them in L2, 31 from memory (fetching a warp's next tiles ahead into L2
+// only cost time): seven tiles a warp, each with one load's latency and a chain
+// of warp reductions, then 8 us for the joins.  One clip, bf16, 10.8 us, of which launch and joins are 8.
 #include <climits>
 
 #include "f32x2.cuh"
@@ -82,19 +82,26 @@ __device__ __forceinline__ uint32_t bits_of<__nv_bfloat16>(__nv_bfloat16 x) {
   return __bfloat16_as_ushort(x);
 }
 
-// The 16 bytes that start `halves` 16-bit units into the eight words w, x.
-__device__ __forceinline__ void shift_words(uint32_t (&w)[4], const uint32_t (&x)[4], int halves) {
-  uint32_t c[8] = {w[0], w[1], w[2], w[3], x[0], x[1], x[2], x[3]};
-  if (halves & 4) {
+// Moves what a warp's lanes hold (vector i of lane l: the 16 bytes at 512 i + 16 l)
+// down by S words and, if ODD, a half: `over` comes after the last vector.
+template <int S, bool ODD, int kVecs>
+__device__ __forceinline__ void move_down(uint32_t (&w)[kVecs][4], const uint32_t (&over)[4], int lane) {
 #pragma unroll
-    for (int j = 0; j < 6; ++j) c[j] = c[j + 2];
+  for (int i = 0; i < kVecs; ++i) {
+    uint32_t c[5];
+#pragma unroll
+    for (int j = 0; j < 4 + ODD; ++j) {
+      if (j + S < 4) {
+        c[j] = w[i][j + S];
+      } else {
+        // Lane 31 is followed by lane 0's next vector, which lane 0 hands round.
+        const uint32_t after = i + 1 < kVecs ? w[(i + 1) % kVecs][j + S - 4] : over[j + S - 4];
+        c[j] = __shfl_sync(0xffffffffu, lane == 0 ? after : w[i][j + S - 4], (lane + 1) % 32);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[i][j] = ODD ? __funnelshift_r(c[j], c[j + 1], 16) : c[j];
   }
-  if (halves & 2) {
-#pragma unroll
-    for (int j = 0; j < 5; ++j) c[j] = c[j + 1];
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(c[j], c[j + 1], (halves & 1) * 16);
 }
 
 // The aligned 16-byte vector that starts at value t0 of a row; values outside
@@ -201,7 +208,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 2) beam_kernel(
   // depend on where a row lies.
   const T *const x = static_cast<const T *>(a.logits) + row * a.row_stride;
   const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
-  const int shift = skew * static_cast<int>(sizeof(T)) / 2;  // in half words
   Gather &g = gathered[warp];
   uint64_t *const list = g.keys;
   uint64_t floor = 0;  // what a key has to beat
@@ -226,16 +232,22 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 2) beam_kernel(
     if (skew != 0) {
       const uint4 u = load(tile0 - skew + kTileVecs * N);  // one address: the vector past the tile
       const uint32_t over[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        uint32_t next[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // Lane 31 is followed by lane 0's next vector, which lane 0 hands round.
-          const uint32_t after = i + 1 < kVecs ? w[(i + 1) % kVecs][j] : over[j];
-          next[j] = __shfl_sync(0xffffffffu, lane == 0 ? after : w[i][j], (lane + 1) % 32);
+      if constexpr (sizeof(T) == 4) {
+        switch (skew) {
+          case 1: move_down<1, false>(w, over, lane); break;
+          case 2: move_down<2, false>(w, over, lane); break;
+          default: move_down<3, false>(w, over, lane); break;
         }
-        shift_words(w[i], next, shift);
+      } else {
+        switch (skew) {
+          case 1: move_down<0, true>(w, over, lane); break;
+          case 2: move_down<1, false>(w, over, lane); break;
+          case 3: move_down<1, true>(w, over, lane); break;
+          case 4: move_down<2, false>(w, over, lane); break;
+          case 5: move_down<2, true>(w, over, lane); break;
+          case 6: move_down<3, false>(w, over, lane); break;
+          default: move_down<3, true>(w, over, lane); break;
+        }
       }
     }
     float vt[kVecs], top = -INFINITY;
@@ -292,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 2) beam_kernel(
       }
     }
     count = take_keys<T>(&g, queued, count, bound, vocab, n, &floor);
-    if (k + 1 < p.tiles) count = rank_keys(list, count, n, &floor);
+    // A first bound, or room for more.
+    if (k + 1 < p.tiles && (floor == 0 || count > kGather - 32)) count = rank_keys(list, count, n, &floor);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);

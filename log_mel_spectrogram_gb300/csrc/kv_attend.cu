@@ -154,7 +154,7 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
 // the softmax (55 of 400 instructions a tile; 5 queries of 64 rows over up to
 // 1500 tokens: 40.2 -> 38.6 us).
 template <typename T, int D, int E, bool SHARED>
-__global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : resident_ctas(D))
+__global__ void __launch_bounds__(kThreads, resident_ctas(D))
     attend_kernel(const AttendParams p) {
   constexpr int STAGES = ring_stages(D, SHARED);
   constexpr int KW = D / 16;   // 32-bit words of a token's key per thread; also 16-element steps of k
@@ -365,6 +365,33 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : resident_cta
   // Of the 32 tiles that are consumed next, one per lane and half: the key
   // scale, log2 and inverse of the value scale; absent blocks are masked.
   float f_s[2] = {0, 0}, l_s[2] = {0, 0}, i_s[2] = {0, 0};
+  // SHARED: this warp's quarter of tile j as f16.
+  auto convert = [&](int j) {
+    if (j >= mine) return true;
+    const int s = j % STAGES;
+    if (!mbar_wait(&full[s], (j / STAGES) & 1, &sh.abort, p.err)) return false;
+    const uint32_t k_at = ring_a + s * stage_bytes(D), v_at = k_at + kTok * D;
+    const uint32_t k16 = tiles_a + (j & 1) * 2 * stage_bytes(D), v16 = k16 + kTok * D * 2;
+    // Token r8 of this warp's eight: place 2 (r8 % 4) + r8 / 4 among them.
+    const int to = 8 * warp + 2 * (r8 & 3) + (r8 >> 2);
+    uint32_t w[KW];
+    lds_words(k_at + (8 * warp + r8) * D + c4 * (D / 4), w);
+#pragma unroll
+    for (int ks = 0; ks < KW; ++ks) {
+      uint32_t b0, b1;
+      bytes_to_subnormal(w[ks], b0, b1);
+      sts_u32(k16 + piece_at<D>(to, 2 * ks) + 4 * c4, b0);
+      sts_u32(k16 + piece_at<D>(to, 2 * ks + 1) + 4 * c4, b1);
+    }
+    lds_words(v_at + (8 * warp + r8) * D + c4 * (D / 4), w);
+#pragma unroll
+    for (int n = 0; n < VB; ++n)
+      sts_u32(v16 + piece_at<D>(to, n) + 4 * c4,
+              bytes_to_f16(__byte_perm(w[n / 4], w[VB / 4 + n / 4], kPick[n % 4])));
+    return true;
+  };
+  bool ok = true;
+  if constexpr (SHARED) ok = convert(0);
   int done = 0;
   for (; done < mine; ++done) {
     const int j = done;
@@ -387,32 +414,14 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : resident_cta
     const int t0 = token_of(j);
     const int s = j % STAGES;
     const uint32_t k_at = ring_a + s * stage_bytes(D), v_at = k_at + kTok * D;
-    bool ok = mbar_wait(&full[s], (j / STAGES) & 1, &sh.abort, p.err);
     const uint32_t k16 = tiles_a + (j & 1) * 2 * stage_bytes(D), v16 = k16 + kTok * D * 2;
     if constexpr (SHARED) {
-      if (ok) {
-        // Token r8 of this warp's eight: place 2 (r8 % 4) + r8 / 4 among them.
-        const int to = 8 * warp + 2 * (r8 & 3) + (r8 >> 2);
-        uint32_t w[KW];
-        lds_words(k_at + (8 * warp + r8) * D + c4 * (D / 4), w);
-#pragma unroll
-        for (int ks = 0; ks < KW; ++ks) {
-          uint32_t b0, b1;
-          bytes_to_subnormal(w[ks], b0, b1);
-          sts_u32(k16 + piece_at<D>(to, 2 * ks) + 4 * c4, b0);
-          sts_u32(k16 + piece_at<D>(to, 2 * ks + 1) + 4 * c4, b1);
-        }
-        lds_words(v_at + (8 * warp + r8) * D + c4 * (D / 4), w);
-#pragma unroll
-        for (int n = 0; n < VB; ++n)
-          sts_u32(v16 + piece_at<D>(to, n) + 4 * c4,
-                  bytes_to_f16(__byte_perm(w[n / 4], w[VB / 4 + n / 4], kPick[n % 4])));
-      }
       // The tile is whole, and its bytes are no longer needed.
       if (__syncthreads_or(!ok)) break;
       if (fetches && fetched < mine) fetch(fetched++);
-    } else if (!ok) {
-      break;
+    } else {
+      ok = mbar_wait(&full[s], (j / STAGES) & 1, &sh.abort, p.err);
+      if (!ok) break;
     }
 
     // Scores: column n of 8-token tile n8 is token 16 (n8/2) + 8 (n8%2) + n/2 + 4 (n%2).
@@ -514,6 +523,9 @@ __global__ void __launch_bounds__(kThreads, SHARED && D < 128 ? 5 : resident_cta
       }
       sum[e] = fmaf(s0, fabsf(i0), fmaf(s1, fabsf(i1), sum[e]));
     }
+    // The next tile, in the shadow of this one's weights and products (223 queries
+    // over 1500 tokens 282 -> 275 us; before the weights 284).
+    if constexpr (SHARED) ok = convert(j + 1);
     // Values: this thread's bytes VB r8 .. + VB-1 of every fourth token.
 #pragma unroll
     for (int half = 0; half < 2; ++half) {

@@ -360,7 +360,7 @@ __device__ __forceinline__ int parent_row(const ReorderParams &p, int r) {
 // layers, keys and values, heads) from the parent's to the row's spare one.
 // The tables still show the old state meanwhile; the last CTA of a clip to
 // finish then rewrites them.  The open blocks of 320 rows, 4 layers of 16 heads
-// of 64, 11.5 us with one CTA a row (eight: 16.5).
+// of 64, 10.4 us with two CTAs a row (one 11.6, three 12.0, eight 16.5).
 __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p) {
   pdl_launch();
   pdl_wait();
@@ -590,10 +590,11 @@ extern "C" lm_status lm_kv_reorder(const lm_kv_cache *cache, const int32_t *pare
   p.parents = parents;
   p.done = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + kWorkspaceHeaderBytes);
   p.beams = beams;
-  // CTAs of a row: four an SM over all rows, and no more than a vector per thread needs.
+  // CTAs of a row: about four an SM over all rows, and no more than a vector per thread
+  // needs.
   const int64_t vecs = static_cast<int64_t>(cache->layers) * cache->heads * cache->block * cache->head_dim / 16;
   if (vecs > INT_MAX / 2) return LM_ERR_UNSUPPORTED;
-  const int64_t most = (vecs + kThreads - 1) / kThreads, round = 4 * 152 / cache->rows;
+  const int64_t most = (vecs + kThreads - 1) / kThreads, round = (4 * 152 + cache->rows / 2) / cache->rows;
   p.parts = static_cast<int32_t>(round < 1 ? 1 : round < most ? round : most);
   return launch_dependent(reorder_kernel, dim3(p.parts, cache->rows), kThreads, 0, reinterpret_cast<cudaStream_t>(stream),
                           1, p);

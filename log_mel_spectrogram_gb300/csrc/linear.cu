@@ -29,8 +29,8 @@
 // take.  Issued from one divergent thread, a product of 128 x 256 x 16 took 172
 // to 237 cycles, in competition with the epilogue; now 130.
 //
-// Measured, calls in a row: 24000 x 1024 -> 4096 bf16 with bias and gelu 118 us
-// alone (1.71 PFLOP/s; 113 without gelu) and 137 us in a second-long loop, where
+// Measured, calls in a row: 24000 x 1024 -> 4096 bf16 with bias and gelu 113 to 118
+// us alone (1.71 to 1.78 PFLOP/s; 111 without gelu) and 134 us in a second-long loop, where
 // the power limit lowers the clock; bound by the tensor pipe, then the epilogue's
 // arithmetic.
 // 320 x 1024 -> 50001 36 us against 20 us of memory traffic: every SM fetches

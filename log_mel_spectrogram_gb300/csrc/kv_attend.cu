@@ -2,7 +2,8 @@
 //
 // A CTA serves one row and key head: the row's queries that read that head
 // (tokens x group) fill tiles of 16 rows, and each of its four warps
-// walks its own tiles of 32 tokens with a running maximum and sum per row.  A
+// walks its own tiles of 32 tokens with a running maximum and sum per row (enum Mode
+// has two other ways, for many rows of few tokens and for many queries).  A
 // warp fetches keys and values -- contiguous pieces of a block -- by bulk
 // copies into a ring of its own, so warps never wait for one another until
 // the end, and only the bytes of the cache travel.
@@ -26,16 +27,13 @@
 // Long rows are split over CTAs; the last one to finish a row and head joins
 // the parts in order.
 //
-// Many prompts take another form (SHARED below): four
-// warps of 16 rows over the same tokens, whose bytes become f16 once per CTA
-// (223 causal queries over up to 448 tokens, 16 rows of 16 heads: 37 -> 33 us).
-//
 // Measured: 5 queries of 64 rows over up to 1500 tokens, 16 heads of 64, 36 us
 // (3.4 TB/s: 1024 CTAs in two rounds, each 4 us of start-up and end, then per
 // tile the issue of about 400 instructions a warp); two rows of 131000 tokens,
 // 8 heads of 128, 95 us (5.7 TB/s, 85% of copy bandwidth); a step of 5 rows of
 // up to 448 tokens, 6.4 us (launch, three dependent loads, the join of 4 warps).
-// Prompts are bound by start-up and end of a CTA that has at most 14 tiles.
+// 223 causal queries over up to 448 tokens, 16 rows of 16 heads, 33 us: start-up and
+// end of CTAs that have at most 14 tiles.
 #include <climits>
 #include <type_traits>
 
@@ -93,7 +91,7 @@ struct Shared {
 constexpr int big_bytes(int d, bool shared) {
   // (Shared: and two tiles as f16.)
   const int ring = (shared ? 1 : kWarps) * ring_stages(d, shared) * stage_bytes(d) + (shared ? 4 * stage_bytes(d) : 0);
-  const int joined = kWarps * kRows * d * 4;
+  const int joined = kWarps * (shared ? kRows * d * 4 : ring_stages(d, shared) * stage_bytes(d));
   return ring > joined ? ring : joined;
 }
 
@@ -145,18 +143,25 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
   return static_cast<uint32_t>(row * D * 2 + ((piece ^ (D == 32 ? (row >> 1) & 3 : row & 7)) * 16));
 }
 
-// SHARED, for many query rows: the warps have 16 each and go over the same
-// tokens, in one ring, instead of sharing out the tokens of 16 rows.  Each
-// warp turns a quarter of a tile into f16 in shared memory, laid out so that
-// ldmatrix gives all warps the operands that they would make of the bytes
-// themselves (250 instructions a tile and warp instead of 400).  E = 1: at most
-// eight query rows, so that the lower half of a product's rows is left out of
-// the softmax (55 of 400 instructions a tile; 5 queries of 64 rows over up to
-// 1500 tokens: 40.2 -> 38.6 us).
-template <typename T, int D, int E, bool SHARED>
+// How the four warps share the work (see cut() for the choice):
+//  - kTokens: 16 query rows of one head, every fourth tile of tokens each;
+//  - kHeads, where there are many rows of few tokens: 16 query rows of a head of
+//    its own each, no joins and a fourth of the CTAs;
+//  - kQueries, for many query rows: 16 of 64 query rows each, all over the same
+//    tokens in one ring.  Each warp turns a quarter of a tile into f16 in shared
+//    memory, laid out so that ldmatrix gives all warps the operands that they would
+//    make of the bytes themselves (250 instructions a tile and warp instead of 400).
+// E = 1: at most eight query rows, so that the lower half of a product's rows is
+// left out of the softmax (55 of 400 instructions a tile; 5 queries of 64 rows over
+// up to 1500 tokens: 40.2 -> 38.6 us).
+enum class Mode { kTokens, kHeads, kQueries };
+
+template <typename T, int D, int E, Mode MODE>
 __global__ void __launch_bounds__(kThreads, resident_ctas(D))
     attend_kernel(const AttendParams p) {
+  constexpr bool SHARED = MODE == Mode::kQueries, ALONE = MODE == Mode::kHeads;
   constexpr int STAGES = ring_stages(D, SHARED);
+  constexpr int JOIN = SHARED ? kRows * D * 4 : STAGES * stage_bytes(D);  // bytes between the warps' results
   constexpr int KW = D / 16;   // 32-bit words of a token's key per thread; also 16-element steps of k
   constexpr int VB = D / 8;    // bytes of a token's value per thread; also 8-column tiles of the output
   constexpr int QT = SHARED ? kWarps * kRows : kRows;  // query rows of the CTA
@@ -167,7 +172,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   // Grid: (key heads and parts, row, tile of queries).  Later queries see more:
   // their tiles go first.
   const int split = p.splits > 1 ? static_cast<int>(blockIdx.x) / p.c.heads : 0;
-  const int h = static_cast<int>(blockIdx.x) - split * p.c.heads;
+  const int head = ALONE ? static_cast<int>(blockIdx.x) * kWarps + warp : static_cast<int>(blockIdx.x) - split * p.c.heads;
+  const int h = ALONE ? min(head, p.c.heads - 1) : head;
   const int row = blockIdx.y;
   const int qt = p.qtiles - 1 - static_cast<int>(blockIdx.z);
   const int64_t unit = (static_cast<int64_t>(blockIdx.z) * p.c.rows + row) * p.c.heads + h;
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   const int fresh_ = p.counts ? p.counts[row] : p.new_tokens;
   int early[2] = {-1, -1};
   if (split == 0 && p.c.width > 0) {
-    const int t = (SHARED ? lane : lane * kWarps + warp) * kTok;
+    const int t = (MODE != Mode::kTokens ? lane : lane * kWarps + warp) * kTok;
 #pragma unroll
     for (int e = 0; e < 2; ++e) early[e] = __ldg(table + min((t + 16 * e) >> block_shift, p.c.width - 1));
   }
@@ -249,11 +255,11 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   const uint32_t ring_a = smem_u32(ring);
   uint64_t *const full = sh.full[SHARED ? 0 : warp];
   const int64_t tiles0 = p.c.layer_tiles + h;
-  // This warp's tiles: number j starts at token begin + (j * kWarps + warp) * kTok
-  // (SHARED: begin + j * kTok).
-  const int mine = SHARED ? (stop - begin + kTok - 1) / kTok
-                          : max((stop - begin - warp * kTok + kWarps * kTok - 1) / (kWarps * kTok), 0);
-  auto token_of = [&](int j) { return begin + (SHARED ? j : j * kWarps + warp) * kTok; };
+  // This warp's tiles: number j starts at token begin + j * kTok, or of kTokens
+  // begin + (j * kWarps + warp) * kTok.
+  const int mine = MODE != Mode::kTokens ? (head < p.c.heads ? (stop - begin + kTok - 1) / kTok : 0)
+                                         : max((stop - begin - warp * kTok + kWarps * kTok - 1) / (kWarps * kTok), 0);
+  auto token_of = [&](int j) { return begin + (MODE != Mode::kTokens ? j : j * kWarps + warp) * kTok; };
   // The block of a tile's half (16 tokens), or -1.
   auto block_of = [&](int j, int half) {
     const int t = token_of(j) + 16 * half;
@@ -561,11 +567,9 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   if (fetches && done < mine && lane == 0) {  // gave up: the copies in flight still have to land
     for (int f = done; f < fetched; ++f) mbar_wait_drain(&full[f % STAGES], (f / STAGES) & 1, p.err);
   }
-  __syncthreads();
-  if (sh.abort) return;
-
-  // The four warps' parts meet in the ring's memory.
-  float *const acc_s = reinterpret_cast<float *>(smem);
+  if (SHARED) __syncthreads();  // the ring and the tiles are free
+  // Every warp's sums, in its own ring's memory.
+  float *const acc_s = reinterpret_cast<float *>(smem + warp * JOIN);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int rr = 8 * e + r8;
@@ -573,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
     s += __shfl_xor_sync(0xffffffffu, s, 1);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     if (c4 == 0) sh.ml[warp][rr] = make_float2(top[e], s);
-    if ((SHARED ? warp * kRows : 0) + rr < q_rows) {
-      float4 *const o = reinterpret_cast<float4 *>(acc_s + (warp * kRows + rr) * D + c4 * (D / 4));
+    if ((SHARED ? warp * kRows : 0) + rr < q_rows && (MODE != Mode::kTokens || mine > 0 || warp == 0)) {
+      float4 *const o = reinterpret_cast<float4 *>(acc_s + rr * D + c4 * (D / 4));
 #pragma unroll
       for (int n = 0; n < VB; n += 4) {
         o[n / 4] = make_float4(acc[n][2 * e], acc[n + 1][2 * e], acc[n + 2][2 * e], acc[n + 3][2 * e]);
@@ -583,8 +587,6 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
       }
     }
   }
-  __syncthreads();
-  const int64_t part0 = (unit * p.splits + split) * p.part_rows;
   constexpr int PER = D / 4;  // 4-element vectors of a row
   auto emit = [&](int rr, int d, float4 v, float l) {
     const int at = q_first + rr, i = p.group == 1 ? at : at / p.group, g = at - i * p.group;
@@ -593,21 +595,38 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
                  ((static_cast<int64_t>(row) * p.tokens + i) * p.q_heads + h * p.group + g) * D + d;
     *reinterpret_cast<uint2 *>(o) = make_uint2(pack2<T>(v.x * f, v.y * f), pack2<T>(v.z * f, v.w * f));
   };
+  if constexpr (ALONE) {
+    __syncwarp();
+    if (head >= p.c.heads || done < mine) return;
+    for (int x = lane; x < q_rows * PER; x += 32) {
+      const int rr = x / PER, d = x % PER * 4;
+      emit(rr, d, *reinterpret_cast<const float4 *>(acc_s + rr * D + d), sh.ml[warp][rr].y);
+    }
+    return;
+  }
+  __syncthreads();
+  if (sh.abort) return;
+  const int64_t part0 = (unit * p.splits + split) * p.part_rows;
+  const float2 *const ml_s = &sh.ml[0][0];  // SHARED: row rr is in place rr; else in warp w's place rr
+  // Warps that had a tile.
+  const int from = SHARED ? 1 : min(max((stop - begin + kTok - 1) / kTok, 1), kWarps);
   for (int x = threadIdx.x; x < q_rows * PER; x += kThreads) {
     const int rr = x / PER, d = x % PER * 4;
-    float t = -INFINITY;
-    const float2 *const ml_s = &sh.ml[0][0];  // SHARED: row rr is in place rr; else in warp w's place rr
-    constexpr int FROM = SHARED ? 1 : kWarps;
+    auto sums_at = [&](int w) {
+      return *reinterpret_cast<const float4 *>(smem + w * JOIN + (rr * D + d) * 4);
+    };
+    constexpr int MOST = SHARED ? 1 : kWarps;
+    float t = ml_s[rr].x;
 #pragma unroll
-    for (int w = 0; w < FROM; ++w) t = fmaxf(t, ml_s[w * kRows + rr].x);
+    for (int w = 1; w < MOST; ++w) t = fmaxf(t, ml_s[w * kRows + rr].x);
     const float zero = t == -INFINITY ? 0.0f : t;
     float4 v = make_float4(0, 0, 0, 0);
     float l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < FROM; ++w) {
+    for (int w = 0; w < MOST; ++w) {
       const float2 ml = ml_s[w * kRows + rr];
       const float f = ex2(ml.x - zero);
-      const float4 a = *reinterpret_cast<const float4 *>(acc_s + (w * kRows + rr) * D + d);
+      const float4 a = w < from ? sums_at(w) : make_float4(0, 0, 0, 0);
       v.x = fmaf(a.x, f, v.x);
       v.y = fmaf(a.y, f, v.y);
       v.z = fmaf(a.z, f, v.z);
@@ -631,25 +650,69 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   if (!sh.last) return;
   __threadfence();
   if (threadIdx.x == 0) p.done[unit] = 0;
+  // Eight threads a row find each part's factor and the sum of weights ...
   const int64_t unit0 = unit * p.splits * p.part_rows;
-  for (int x = threadIdx.x; x < q_rows * PER; x += kThreads) {
-    const int rr = x / PER, d = x % PER * 4;
-    float t = -INFINITY;
-    for (int w = 0; w < parts; ++w) t = fmaxf(t, __ldcg(&p.part_ml[unit0 + w * p.part_rows + rr]).x);
+  float *const factor = reinterpret_cast<float *>(smem);  // [row][part]; cut() sees that it fits
+  for (int r0 = 0; r0 < q_rows; r0 += kThreads / 8) {
+    const int rr = r0 + static_cast<int>(threadIdx.x) / 8, l8 = threadIdx.x % 8;
+    const bool in = rr < q_rows;
+    const float2 *const ml = p.part_ml + unit0 + (in ? rr : 0);
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    const float2 first = in && l8 < parts ? __ldcg(&ml[l8 * p.part_rows]) : none;
+    float t = first.x;
+#pragma unroll 4
+    for (int w = l8 + 8; w < parts; w += 8) t = fmaxf(t, __ldcg(&ml[w * p.part_rows]).x);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
     const float zero = t == -INFINITY ? 0.0f : t;
-    float4 v = make_float4(0, 0, 0, 0);
     float l = 0.0f;
-    for (int w = 0; w < parts; ++w) {
-      const float2 ml = __ldcg(&p.part_ml[unit0 + w * p.part_rows + rr]);
-      const float f = ex2(ml.x - zero);
-      const float4 a = __ldcg(reinterpret_cast<const float4 *>(p.part_acc + (unit0 + w * p.part_rows + rr) * D + d));
-      v.x = fmaf(a.x, f, v.x);
-      v.y = fmaf(a.y, f, v.y);
-      v.z = fmaf(a.z, f, v.z);
-      v.w = fmaf(a.w, f, v.w);
-      l = fmaf(ml.y, f, l);
+#pragma unroll 4
+    for (int w = l8; w < parts; w += 8) {
+      const float2 m = w < 8 ? first : __ldcg(&ml[w * p.part_rows]);
+      const float f = ex2(m.x - zero);
+      if (in) factor[rr * parts + w] = f;
+      l = fmaf(m.y, f, l);
     }
-    emit(rr, d, v, l);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (in && l8 == 0) sh.ml[rr / kRows][rr % kRows].y = l;
+  }
+  __syncthreads();
+  // ... and groups of threads add up every `groups`-th part.
+  const int items = q_rows * PER, groups = max(kThreads / items, 1);
+  float4 *const group_sums = reinterpret_cast<float4 *>(smem + big_bytes(D, SHARED) - kThreads * 16);
+  for (int x0 = 0; x0 < items; x0 += kThreads) {
+    const int g = groups == 1 ? 0 : threadIdx.x / items;
+    const int x = x0 + (groups == 1 ? threadIdx.x : threadIdx.x - g * items);
+    const bool in = x < items && g < groups;
+    const int rr = x / PER, d = x % PER * 4;
+    float4 v = make_float4(0, 0, 0, 0);
+    if (in) {
+      const float *const acc_p = p.part_acc + (unit0 + rr) * D + d;
+#pragma unroll 8
+      for (int w = g; w < parts; w += groups) {
+        const float f = factor[rr * parts + w];
+        const float4 a = __ldcg(reinterpret_cast<const float4 *>(acc_p + static_cast<int64_t>(w) * p.part_rows * D));
+        v.x = fmaf(a.x, f, v.x);
+        v.y = fmaf(a.y, f, v.y);
+        v.z = fmaf(a.z, f, v.z);
+        v.w = fmaf(a.w, f, v.w);
+      }
+    }
+    if (groups > 1) {
+      group_sums[threadIdx.x] = v;
+      __syncthreads();
+      if (in && g == 0) {
+        for (int i = 1; i < groups; ++i) {
+          const float4 a = group_sums[threadIdx.x + i * items];
+          v.x += a.x;
+          v.y += a.y;
+          v.z += a.z;
+          v.w += a.w;
+        }
+      }
+    }
+    if (in && g == 0) emit(rr, d, v, sh.ml[rr / kRows][rr % kRows].y);
   }
 }
 
@@ -662,43 +725,64 @@ lm_status check(const lm_kv_cache *cache, int32_t tokens, int32_t q_heads) {
   return LM_OK;
 }
 
-// Key heads and tiles of 64 query rows from which the SHARED form is taken, where
-// at most a fifth of those tiles is empty.  It takes 1.2 to 1.8 times less time a
-// query row on a full device, but a CTA of it walks all tokens alone.  Both in us,
-// SHARED last: 64 rows x 16 heads over 1500 tokens, 64 queries 114 / 109, 128
-// 207 / 174, 96 (a third of two tiles empty) 160 / 176; 16 rows x 16 heads over
-// 448, 128 queries (512 tiles) 29.1 / 26.4, 64 (256 tiles) 18.0 / 21.6; 8 rows x
-// 8 heads, 448 queries (448) 43 / 29, 223 (256) 25.5 / 25.9, 64 (64) 11.4 / 20.
-constexpr int64_t kSharedTiles = 400;
-
-// How a call is cut: query rows per tile, tiles, units (row, key head, tile)
-// and parts of the tokens.
+// How a call is cut: the warps' mode, query rows per tile, tiles, units (row, key
+// head, tile) and parts of the tokens.
 struct Cut {
-  bool shared;
+  Mode mode;
   int qrows, qtiles, splits, part_rows, chunk;
   int64_t units;
   size_t done_bytes, ml_bytes, acc_bytes;
 };
 
+// The mode with the least estimated time: rounds of CTAs, times 5 for a CTA's start
+// and end and 1 for each tile of tokens that a warp goes over (a unit is about a
+// microsecond).  Rows are mostly of unequal length, which the modes with long walks
+// cannot even out: a tenth in favour of kTokens, and a fourth on the walks where all
+// CTAs run at once.  Measured, in us, kTokens / kQueries / kHeads: 320 rows x 16 heads
+// of 64, one query over up to 448 tokens 60 / - / 47, over 128 34 / - / 19; 157 rows x
+// 10 heads, 30 over 30 25 / 16 / 13; 64 rows x 16 heads, 20 over 1500 62 / 95 / 70, 96
+// over 448 85 / 74 / 60, 448 over 1500 615 / 450 / -; 8 rows x 8 heads, 448 over 448
+// 43 / 29 / -, 64 over 448 11 / 20 / -.
 Cut cut(const lm_kv_cache *c, int32_t tokens, int32_t q_heads) {
-  Cut k;
-  k.qrows = tokens * (q_heads / c->heads);
-  const int64_t big = (static_cast<int64_t>(k.qrows) + kWarps * kRows - 1) / (kWarps * kRows);
-  k.shared = big * c->rows * c->heads >= kSharedTiles && 5 * static_cast<int64_t>(k.qrows) >= 4 * big * kWarps * kRows;
-  const int tile = k.shared ? kWarps * kRows : kRows;
-  k.qtiles = (k.qrows + tile - 1) / tile;
-  k.part_rows = k.qrows < tile ? k.qrows : tile;
-  k.units = static_cast<int64_t>(c->rows) * c->heads * k.qtiles;
-  // As many parts as fill the device once.  Where the units alone come near
-  // that, parts are for balance between rows of unequal length: four rounds of
-  // them.  None below kMinChunk or kBalance tokens.
-  const int64_t cap = static_cast<int64_t>(c->width) * c->block;
+  Cut k = {};
+  const int qrows = tokens * (q_heads / c->heads);
+  const int64_t cap = static_cast<int64_t>(c->width) * c->block, tiles = (cap + kTok - 1) / kTok;
   const int64_t slots = full_ctas(c->head_dim);
-  int64_t s = k.units == 0 ? 1 : 2 * k.units > slots ? (4 * slots + k.units - 1) / k.units : slots / k.units;
-  k.chunk = 2 * k.units > slots ? kBalance : kMinChunk;
-  const int64_t most = (cap + k.chunk - 1) / k.chunk;
-  if (s > most) s = most;
-  k.splits = static_cast<int>(s < 1 ? 1 : s);
+  double least = 0.0;
+  for (const Mode mode : {Mode::kTokens, Mode::kQueries, Mode::kHeads}) {
+    Cut m = {};
+    m.mode = mode;
+    m.qrows = qrows;
+    const int tile = mode == Mode::kQueries ? kWarps * kRows : kRows;
+    if (mode == Mode::kQueries && qrows <= kRows) continue;
+    m.qtiles = static_cast<int>((static_cast<int64_t>(qrows) + tile - 1) / tile);
+    m.part_rows = qrows < tile ? qrows : tile;
+    m.units = static_cast<int64_t>(c->rows) * c->heads * m.qtiles;
+    // As many parts as fill the device once.  Where the units alone come near
+    // that, parts are for balance between rows of unequal length: four rounds of
+    // them.  None below kMinChunk or kBalance tokens, nor more than the join's
+    // factors have room for.
+    // (kTokens only: the others have units enough.)
+    int64_t s = m.units == 0 || mode != Mode::kTokens ? 1
+                : 2 * m.units > slots                 ? (4 * slots + m.units - 1) / m.units
+                                                      : slots / m.units;
+    m.chunk = 2 * m.units > slots ? kBalance : kMinChunk;
+    const int64_t most = (cap + m.chunk - 1) / m.chunk;
+    const int64_t room = (big_bytes(c->head_dim, false) - kThreads * 16) / (4 * kRows);
+    s = s < most ? s : most;
+    s = s < room ? s : room;
+    m.splits = static_cast<int>(s < 1 ? 1 : s);
+    const int64_t ctas = mode == Mode::kHeads ? static_cast<int64_t>(c->rows) * ((c->heads + kWarps - 1) / kWarps) * m.qtiles
+                                              : m.units * m.splits;
+    const double walked = static_cast<double>(tiles) / m.splits / (mode == Mode::kTokens ? kWarps : 1);
+    const int64_t rounds = (ctas + slots - 1) / slots;
+    const double tile_time = mode != Mode::kTokens && rounds <= 1 ? 1.25 : 1.0;
+    const double time = (mode == Mode::kTokens ? 0.9 : 1.0) * static_cast<double>(rounds) * (5.0 + tile_time * walked);
+    if (mode == Mode::kTokens || time < least) {
+      least = time;
+      k = m;
+    }
+  }
   const int64_t parts = k.splits > 1 ? k.units * k.splits * k.part_rows : 0;
   // One place for the counters whatever the shape: calls of other shapes
   // that share the workspace must not write over them.  Units that are split
@@ -709,18 +793,20 @@ Cut cut(const lm_kv_cache *c, int32_t tokens, int32_t q_heads) {
   return k;
 }
 
-template <typename T, int D, int E, bool SHARED>
+template <typename T, int D, int E, Mode MODE>
 lm_status launch(const AttendParams &p, dim3 grid, cudaStream_t s) {
-  auto *const kernel = attend_kernel<T, D, E, SHARED>;
-  constexpr int smem = big_bytes(D, SHARED) + static_cast<int>(sizeof(Shared));
+  auto *const kernel = attend_kernel<T, D, E, MODE>;
+  constexpr int smem = big_bytes(D, MODE == Mode::kQueries) + static_cast<int>(sizeof(Shared));
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
   return launch_dependent(kernel, grid, kThreads, smem, s, 1, p);
 }
 
 template <typename T, int D>
 lm_status launch_form(const AttendParams &p, const Cut &k, dim3 grid, cudaStream_t s) {
-  if (k.shared) return launch<T, D, 2, true>(p, grid, s);
-  return k.qrows <= 8 ? launch<T, D, 1, false>(p, grid, s) : launch<T, D, 2, false>(p, grid, s);
+  if (k.mode == Mode::kQueries) return launch<T, D, 2, Mode::kQueries>(p, grid, s);
+  if (k.mode == Mode::kHeads)
+    return k.qrows <= 8 ? launch<T, D, 1, Mode::kHeads>(p, grid, s) : launch<T, D, 2, Mode::kHeads>(p, grid, s);
+  return k.qrows <= 8 ? launch<T, D, 1, Mode::kTokens>(p, grid, s) : launch<T, D, 2, Mode::kTokens>(p, grid, s);
 }
 
 template <typename T>
@@ -767,7 +853,9 @@ extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const
     return LM_ERR_INVALID_ARG;
   if (cache->rows > 65535 || k.qtiles > 65535 || static_cast<int64_t>(cache->heads) * k.splits > INT_MAX)
     return LM_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(cache->heads) * k.splits, cache->rows, k.qtiles);
+  const unsigned across = k.mode == Mode::kHeads ? (cache->heads + kWarps - 1) / kWarps
+                                                 : static_cast<unsigned>(cache->heads) * k.splits;
+  const dim3 grid(across, cache->rows, k.qtiles);
   char *const w = static_cast<char *>(workspace);
   AttendParams p;
   p.c = kv_view(cache, layer);

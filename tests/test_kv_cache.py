@@ -492,3 +492,42 @@ def test_outputs_that_overlap_queries(lm):
     both = torch.randn((2, 2, 3, 2, 64), device="cuda").half()
     got = c.attend(0, both[0], out=both[1])
     assert torch.equal(got, c.attend(0, both[0].clone()))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows,heads,dim,tokens,t,group,causal", [
+    (160, 5, 64, 70, 1, 1, True), (200, 6, 32, 40, 1, 2, False), (130, 7, 128, 100, 1, 1, True),
+    (120, 9, 64, 33, 5, 4, False), (90, 13, 128, 17, 5, 8, False), (321, 3, 64, 200, 1, 1, True), (150, 6, 32, 64, 17, 1, True)])
+def test_many_rows_of_few_tokens(lm, dtype, rows, heads, dim, tokens, t, group, causal):
+    """More rows and heads than the device has room for: heads need not fill a CTA's four warps."""
+    c = filled(lm, rows, tokens, heads, dim, 16, dtype, seed=rows)
+    c.lens.copy_(torch.arange(rows) * 7 % (tokens - t + 1))
+    q = gen(heads)(rows, t, heads * group, dim).to(dtype)
+    out = c.attend(0, q, causal=causal)
+    check_attend(out, c, 0, q, [t] * rows if causal else [0] * rows, causal)
+    assert torch.equal(out, c.attend(0, q, causal=causal))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows,heads,dim,tokens,t,group,causal", [
+    (48, 10, 64, 160, 64, 1, True), (50, 12, 32, 100, 50, 1, False), (30, 12, 128, 150, 130, 1, True),
+    (60, 8, 64, 90, 16, 4, True), (40, 11, 128, 40, 7, 8, False), (20, 16, 64, 448, 223, 1, True)])
+def test_many_queries_of_many_rows(lm, dtype, rows, heads, dim, tokens, t, group, causal):
+    """Tiles of 64 queries that fill the device, and their ragged ends."""
+    c = filled(lm, rows, tokens, heads, dim, 32, dtype, seed=rows)
+    c.lens.copy_(torch.arange(rows) * 5 % (tokens - t + 1))
+    counts = torch.tensor([t if r % 7 else r % 3 for r in range(rows)], dtype=torch.int32, device="cuda")
+    q = gen(heads)(rows, t, heads * group, dim).to(dtype)
+    out = c.attend(0, q, counts if causal else None, causal=causal)
+    check_attend(out, c, 0, q, counts.tolist() if causal else [0] * rows, causal)
+
+
+@pytest.mark.parametrize("rows,heads,group,dim,t", [(1, 1, 1, 64, 1), (1, 1, 4, 32, 1), (2, 1, 8, 128, 2), (1, 2, 3, 64, 11)])
+def test_rows_of_many_parts(lm, rows, heads, group, dim, t):
+    """One or two units over the whole device: more parts than a warp has lanes."""
+    c = filled(lm, rows, 90000, heads, dim, 64, torch.float16, seed=dim)
+    c.lens.copy_(torch.tensor([89000, 40001][:rows]))
+    q = gen(t)(rows, t, heads * group, dim).half()
+    out = c.attend(0, q)
+    check_attend(out, c, 0, q, [t] * rows, True)
+    assert torch.equal(out, c.attend(0, q))

@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
     s += __shfl_xor_sync(0xffffffffu, s, 1);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     if (c4 == 0) sh.ml[warp][rr] = make_float2(top[e], s);
-    if ((SHARED ? warp * kRows : 0) + rr < q_rows && (MODE != Mode::kTokens || mine > 0 || warp == 0)) {
+    if ((SHARED ? warp * kRows : 0) + rr < q_rows) {
       float4 *const o = reinterpret_cast<float4 *>(acc_s + rr * D + c4 * (D / 4));
 #pragma unroll
       for (int n = 0; n < VB; n += 4) {
@@ -608,25 +608,20 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   if (sh.abort) return;
   const int64_t part0 = (unit * p.splits + split) * p.part_rows;
   const float2 *const ml_s = &sh.ml[0][0];  // SHARED: row rr is in place rr; else in warp w's place rr
-  // Warps that had a tile.
-  const int from = SHARED ? 1 : min(max((stop - begin + kTok - 1) / kTok, 1), kWarps);
+  constexpr int FROM = SHARED ? 1 : kWarps;
   for (int x = threadIdx.x; x < q_rows * PER; x += kThreads) {
     const int rr = x / PER, d = x % PER * 4;
-    auto sums_at = [&](int w) {
-      return *reinterpret_cast<const float4 *>(smem + w * JOIN + (rr * D + d) * 4);
-    };
-    constexpr int MOST = SHARED ? 1 : kWarps;
     float t = ml_s[rr].x;
 #pragma unroll
-    for (int w = 1; w < MOST; ++w) t = fmaxf(t, ml_s[w * kRows + rr].x);
+    for (int w = 1; w < FROM; ++w) t = fmaxf(t, ml_s[w * kRows + rr].x);
     const float zero = t == -INFINITY ? 0.0f : t;
     float4 v = make_float4(0, 0, 0, 0);
     float l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < MOST; ++w) {
+    for (int w = 0; w < FROM; ++w) {
       const float2 ml = ml_s[w * kRows + rr];
       const float f = ex2(ml.x - zero);
-      const float4 a = w < from ? sums_at(w) : make_float4(0, 0, 0, 0);
+      const float4 a = *reinterpret_cast<const float4 *>(smem + w * JOIN + (rr * D + d) * 4);
       v.x = fmaf(a.x, f, v.x);
       v.y = fmaf(a.y, f, v.y);
       v.z = fmaf(a.z, f, v.z);

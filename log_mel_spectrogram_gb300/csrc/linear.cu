@@ -30,7 +30,7 @@
 // to 237 cycles, in competition with the epilogue; now 130.
 //
 // Measured, calls in a row: 24000 x 1024 -> 4096 bf16 with bias and gelu 113 to 118
-// us alone (1.71 to 1.78 PFLOP/s; 111 without gelu) and 134 us in a second-long loop, where
+// us alone (1.71 to 1.78 PFLOP/s; 111 without gelu) and 135 us in a second-long loop, where
 // the power limit lowers the clock; bound by the tensor pipe, then the epilogue's
 // arithmetic.
 // 320 x 1024 -> 50001 36 us against 20 us of memory traffic: every SM fetches

@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
       uint8_t *const k_at = ring + s * stage_bytes(D), *const v_at = k_at + kTok * D;
       const int t = token_of(j), in = t & (p.c.block - 1);
       const int64_t at0 = ((tiles0 + static_cast<int64_t>(b0) * p.c.heads) * p.c.block + in) * D;
-      if (b0 >= 0 && b0 == b1) {
+      // (A row may name one block of 16 tokens in two columns: then the halves are equal, not
+      // consecutive.)
+      if (b0 >= 0 && b0 == b1 && p.c.block >= kTok) {
         bulk_g2s_plain(k_at, p.c.k8 + at0, 2 * bytes, &full[s]);
         bulk_g2s_plain(v_at, p.c.v8 + at0, 2 * bytes, &full[s]);
       } else {

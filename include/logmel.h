@@ -592,6 +592,18 @@ lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const void *q, c
                        int32_t causal, float scale, int32_t dtype, void *out, void *workspace,
                        size_t workspace_bytes, lm_stream_t stream);
 
+/* Fault injection for tests of the bounded waits: lm_kv_attend, except that
+ * the first tile of tokens that CTA `withheld_cta` (>= 0, counted over the
+ * grid) fetches never counts as complete, and that waits give up after
+ * wait_ns (1e5 .. 2e9; 2 s otherwise).  A CTA whose wait runs out sets bit 1
+ * of the workspace's error word, waits (bounded) for its copies and ends; the
+ * outputs of its row, heads and queries are not written. */
+lm_status lm_debug_kv_attend_withhold(const lm_kv_cache *cache, int32_t layer, const void *q, const int64_t *q_strides,
+                                      int32_t tokens, int32_t q_heads, const int32_t *counts, int32_t new_tokens,
+                                      int32_t causal, float scale, int32_t dtype, void *out, void *workspace,
+                                      size_t workspace_bytes, int64_t withheld_cta, uint64_t wait_ns,
+                                      lm_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* 6. beam search (the source pages have no counterpart)                    */
 /* ------------------------------------------------------------------------ */

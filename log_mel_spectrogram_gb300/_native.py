@@ -123,6 +123,9 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.lm_kv_attend_workspace_size.restype = ctypes.c_int
     L.lm_kv_attend.argtypes = [vp, i32, vp, vp, i32, i32, vp, i32, i32, ctypes.c_float, i32, vp, vp, sz, vp]
     L.lm_kv_attend.restype = ctypes.c_int
+    L.lm_debug_kv_attend_withhold.argtypes = [vp, i32, vp, vp, i32, i32, vp, i32, i32, ctypes.c_float, i32, vp, vp, sz,
+                                              i64, ctypes.c_uint64, vp]
+    L.lm_debug_kv_attend_withhold.restype = ctypes.c_int
     L.lm_kv_reorder.argtypes = [vp, vp, i32, vp, sz, vp]
     L.lm_kv_reorder.restype = ctypes.c_int
     L.lm_beam_step_workspace_size.argtypes = [vp, vp]

@@ -43,6 +43,7 @@
 #include "kv_cache.cuh"
 #include "mma.cuh"
 #include "ptx.cuh"
+#include "waits.cuh"
 
 namespace lm {
 namespace {
@@ -78,6 +79,8 @@ struct AttendParams {
   float *part_acc;               // [unit][split][rows][head_dim]
   int32_t tokens, q_heads, new_tokens, causal, group, qrows, qtiles, splits, part_rows, min_chunk, qvec;
   float scale;
+  uint64_t wait_ns;              // limit of a wait
+  int64_t withheld;              // CTA whose first stage never fills (tests), or -1
 };
 
 // Shared memory: the rings (at the end the warps' partial results), then this.
@@ -178,8 +181,10 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   const int qt = p.qtiles - 1 - static_cast<int>(blockIdx.z);
   const int64_t unit = (static_cast<int64_t>(blockIdx.z) * p.c.rows + row) * p.c.heads + h;
 
-  if (threadIdx.x < kWarps)
-    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[threadIdx.x][i], 1);
+  if (threadIdx.x < kWarps) {
+    const int64_t cta = (static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[threadIdx.x][i], threadIdx.x + i == 0 && cta == p.withheld ? 2 : 1);
+  }
   if (threadIdx.x == 0) sh.abort = 0;
   fence_mbar_init();
   pdl_launch();
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   auto convert = [&](int j) {
     if (j >= mine) return true;
     const int s = j % STAGES;
-    if (!mbar_wait(&full[s], (j / STAGES) & 1, &sh.abort, p.err)) return false;
+    if (!mbar_wait_warp(&full[s], (j / STAGES) & 1, p.wait_ns, &sh.abort, p.err)) return false;
     const uint32_t k_at = ring_a + s * stage_bytes(D), v_at = k_at + kTok * D;
     const uint32_t k16 = tiles_a + (j & 1) * 2 * stage_bytes(D), v16 = k16 + kTok * D * 2;
     // Token r8 of this warp's eight: place 2 (r8 % 4) + r8 / 4 among them.
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
       if (__syncthreads_or(!ok)) break;
       if (fetches && fetched < mine) fetch(fetched++);
     } else {
-      ok = mbar_wait(&full[s], (j / STAGES) & 1, &sh.abort, p.err);
+      ok = mbar_wait_warp(&full[s], (j / STAGES) & 1, p.wait_ns, &sh.abort, p.err);
       if (!ok) break;
     }
 
@@ -567,8 +572,9 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
     if (!SHARED && fetched < mine) fetch(fetched++);
   }
   if (fetches && done < mine && lane == 0) {  // gave up: the copies in flight still have to land
-    for (int f = done; f < fetched; ++f) mbar_wait_drain(&full[f % STAGES], (f / STAGES) & 1, p.err);
+    for (int f = done; f < fetched; ++f) mbar_drain(&full[f % STAGES], (f / STAGES) & 1, p.wait_ns, p.err);
   }
+  __syncwarp();
   if (SHARED) __syncthreads();  // the ring and the tiles are free
   // Every warp's sums, in its own ring's memory.
   float *const acc_s = reinterpret_cast<float *>(smem + warp * JOIN);
@@ -815,23 +821,10 @@ lm_status launch_dim(const AttendParams &p, const Cut &k, dim3 grid, cudaStream_
   }
 }
 
-}  // namespace
-}  // namespace lm
-
-extern "C" lm_status lm_kv_attend_workspace_size(const lm_kv_cache *cache, int32_t tokens, int32_t q_heads,
-                                                 size_t *bytes) {
-  if (!bytes) return LM_ERR_INVALID_ARG;
-  if (lm_status st = lm::check(cache, tokens, q_heads); st != LM_OK) return st;
-  const lm::Cut k = lm::cut(cache, tokens, q_heads);
-  *bytes = 256 + k.done_bytes + k.ml_bytes + k.acc_bytes;
-  return LM_OK;
-}
-
-extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const void *q, const int64_t *q_strides,
-                                  int32_t tokens, int32_t q_heads, const int32_t *counts, int32_t new_tokens,
-                                  int32_t causal, float scale, int32_t dtype, void *out, void *workspace,
-                                  size_t workspace_bytes, lm_stream_t stream) {
-  using namespace lm;
+// lm_kv_attend; `fault` is null outside tests.
+lm_status attend(const lm_kv_cache *cache, int32_t layer, const void *q, const int64_t *q_strides, int32_t tokens,
+                 int32_t q_heads, const int32_t *counts, int32_t new_tokens, int32_t causal, float scale, int32_t dtype,
+                 void *out, void *workspace, size_t workspace_bytes, cudaStream_t s, const WaitFault *fault) {
   if (lm_status st = check(cache, tokens, q_heads); st != LM_OK) return st;
   if (layer < 0 || layer >= cache->layers || !q_strides || new_tokens < 0) return LM_ERR_INVALID_ARG;
   if (dtype != LM_F16 && dtype != LM_BF16) return LM_ERR_UNSUPPORTED;
@@ -878,6 +871,38 @@ extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const
   p.min_chunk = k.chunk;
   p.qvec = aligned(q, 16) && q_strides[0] % 8 == 0 && q_strides[1] % 8 == 0 && q_strides[2] % 8 == 0;
   p.scale = scale;
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  p.wait_ns = fault ? fault->wait_ns : kWaitTimeoutNs;
+  p.withheld = fault ? fault->withheld_cta : -1;
   return dtype == LM_F16 ? launch_dim<__half>(p, k, grid, s) : launch_dim<__nv_bfloat16>(p, k, grid, s);
+}
+
+}  // namespace
+}  // namespace lm
+
+extern "C" lm_status lm_kv_attend_workspace_size(const lm_kv_cache *cache, int32_t tokens, int32_t q_heads,
+                                                 size_t *bytes) {
+  if (!bytes) return LM_ERR_INVALID_ARG;
+  if (lm_status st = lm::check(cache, tokens, q_heads); st != LM_OK) return st;
+  const lm::Cut k = lm::cut(cache, tokens, q_heads);
+  *bytes = 256 + k.done_bytes + k.ml_bytes + k.acc_bytes;
+  return LM_OK;
+}
+
+extern "C" lm_status lm_kv_attend(const lm_kv_cache *cache, int32_t layer, const void *q, const int64_t *q_strides,
+                                  int32_t tokens, int32_t q_heads, const int32_t *counts, int32_t new_tokens,
+                                  int32_t causal, float scale, int32_t dtype, void *out, void *workspace,
+                                  size_t workspace_bytes, lm_stream_t stream) {
+  return lm::attend(cache, layer, q, q_strides, tokens, q_heads, counts, new_tokens, causal, scale, dtype, out,
+                    workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream), nullptr);
+}
+
+extern "C" lm_status lm_debug_kv_attend_withhold(const lm_kv_cache *cache, int32_t layer, const void *q,
+                                                 const int64_t *q_strides, int32_t tokens, int32_t q_heads,
+                                                 const int32_t *counts, int32_t new_tokens, int32_t causal, float scale,
+                                                 int32_t dtype, void *out, void *workspace, size_t workspace_bytes,
+                                                 int64_t withheld_cta, uint64_t wait_ns, lm_stream_t stream) {
+  if (withheld_cta < 0 || wait_ns < 100000ull || wait_ns > lm::kWaitTimeoutNs) return LM_ERR_INVALID_ARG;
+  const lm::WaitFault fault{withheld_cta, wait_ns};
+  return lm::attend(cache, layer, q, q_strides, tokens, q_heads, counts, new_tokens, causal, scale, dtype, out,
+                    workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream), &fault);
 }

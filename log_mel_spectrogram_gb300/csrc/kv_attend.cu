@@ -52,6 +52,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = 32;              // tokens of a warp's tile
 constexpr int kRows = 16;             // query rows of a warp
+constexpr uint32_t kGaveUp = 1 << 16;  // more than a unit's parts
 constexpr int kMinChunk = 512;        // tokens below which a row is not split
 constexpr int kBalance = 2048;        // ... where parts are for balance only (512: 44 us, 1024: 39, none: 36 for
                                       // 1024 units of up to 1500 tokens)
@@ -74,7 +75,7 @@ struct AttendParams {
   void *out;
   int64_t row_s, tok_s, head_s;
   const int32_t *counts;
-  uint32_t *err, *done;          // done: per unit, parts that are ready
+  uint32_t *err, *done;          // done: per unit, parts that are ready, and kGaveUp for each that gave up
   float2 *part_ml;               // [unit][split][rows]: maximum, sum
   float *part_acc;               // [unit][split][rows][head_dim]
   int32_t tokens, q_heads, new_tokens, causal, group, qrows, qtiles, splits, part_rows, min_chunk, qvec;
@@ -88,7 +89,8 @@ struct Shared {
   uint64_t full[kWarps][8];
   float2 ml[kWarps][kRows];  // maximum and sum per warp and query row
   int abort;
-  int last;
+  int last;    // of a unit's parts
+  int failed;  // one of them gave up
 };
 
 constexpr int big_bytes(int d, bool shared) {
@@ -613,11 +615,11 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
     return;
   }
   __syncthreads();
-  if (sh.abort) return;
+  const bool gave_up = sh.abort;
   const int64_t part0 = (unit * p.splits + split) * p.part_rows;
   const float2 *const ml_s = &sh.ml[0][0];  // SHARED: row rr is in place rr; else in warp w's place rr
   constexpr int FROM = SHARED ? 1 : kWarps;
-  for (int x = threadIdx.x; x < q_rows * PER; x += kThreads) {
+  for (int x = threadIdx.x; x < (gave_up ? 0 : q_rows * PER); x += kThreads) {
     const int rr = x / PER, d = x % PER * 4;
     float t = ml_s[rr].x;
 #pragma unroll
@@ -647,12 +649,17 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    sh.last = atomicAdd(&p.done[unit], 1u) == static_cast<uint32_t>(parts - 1);
+    // A part that gave up counts as well, so that the counter goes back to zero; the unit is
+    // then not joined.
+    const uint32_t before = atomicAdd(&p.done[unit], gave_up ? 1 + kGaveUp : 1u);
+    sh.last = before % kGaveUp == static_cast<uint32_t>(parts - 1);
+    sh.failed = gave_up || before >= kGaveUp;
   }
   __syncthreads();
   if (!sh.last) return;
   __threadfence();
   if (threadIdx.x == 0) p.done[unit] = 0;
+  if (sh.failed) return;
   // Eight threads a row find each part's factor and the sum of weights ...
   const int64_t unit0 = unit * p.splits * p.part_rows;
   float *const factor = reinterpret_cast<float *>(smem);  // [row][part]; cut() sees that it fits

@@ -83,6 +83,26 @@ def test_a_withheld_tile_ends_its_cta(lm, rows, heads, dim, tokens, t, own_heads
     assert torch.equal(attend(c, q, ws), want) and error(ws) == 0
 
 
+@pytest.mark.parametrize("withheld", [0, 1, 2, 5])
+@pytest.mark.parametrize("rows,heads,dim,tokens,t", [(2, 2, 64, 9000, 1), (1, 2, 128, 20000, 3), (3, 2, 32, 5000, 16)])
+def test_a_part_that_gave_up_leaves_no_count(lm, withheld, rows, heads, dim, tokens, t):
+    """CTA x of a row is part x / heads of head x % heads.  The unit of the part that gave up is not joined, and the
+    next call finds the workspace as the first one did."""
+    c = kv.filled(lm, rows, tokens, heads, dim, 64, torch.float16, seed=rows)
+    c.lens.fill_(tokens - t)
+    q = kv.gen(dim)(rows, t, heads, dim).half()
+    ws = workspace(c, q)
+    want = attend(c, q, ws)
+    for _ in range(2):
+        got = attend(c, q, ws, withheld=withheld)
+        assert error(ws) & MBAR_TIMEOUT_BIT
+        head = withheld % heads
+        assert torch.equal(got[1:], want[1:]) and torch.equal(got[0, :, 1 - head], want[0, :, 1 - head])
+        assert (got[0, :, head] == 7).all()
+        ws[:4] = 0
+        assert torch.equal(attend(c, q, ws), want) and error(ws) == 0
+
+
 def test_refusals(lm):
     c = kv.filled(lm, 1, 64, 1, 64, 32, torch.float16)
     q = torch.zeros((1, 1, 1, 64), device="cuda", dtype=torch.float16)

@@ -487,6 +487,22 @@ typedef struct lm_linear_args {
 lm_status lm_linear_workspace_size(const lm_linear_args *args, size_t *bytes);
 lm_status lm_linear(const lm_linear_args *args, void *workspace, size_t workspace_bytes, lm_stream_t stream);
 
+/* Synchronises `stream`, then reads the bits (those of lm_workspace_error)
+ * that lm_linear and lm_kv_attend have reported on the current device, on any
+ * stream and with any workspace, since the word was last cleared; clears it
+ * where `clear` is nonzero.  Where it is not zero, some call's output is not
+ * whole.  Returns LM_ERR_DEVICE_FAULT when a bit was set,
+ * LM_ERR_INVALID_ARG for a null pointer, LM_ERR_CUDA when a CUDA call failed. */
+lm_status lm_decode_error(uint32_t *device_error, int32_t clear, lm_stream_t stream);
+
+/* Fault injection for tests of the bounded waits: lm_linear, except that the
+ * first tile of operands that CTA `withheld_cta` (>= 0) fetches never counts as
+ * complete, and that waits give up after wait_ns (1e5 .. 2e9; 2 s otherwise).
+ * The CTA sets bit 1 of the workspace's error word and ends; its outputs (and,
+ * where CTAs share a tile's k, those of its tile) are incomplete. */
+lm_status lm_debug_linear_withhold(const lm_linear_args *args, void *workspace, size_t workspace_bytes,
+                                   int64_t withheld_cta, uint64_t wait_ns, lm_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* 5. keys and values in 8 bits (the source pages have no counterpart)      */
 /* ------------------------------------------------------------------------ */

@@ -25,12 +25,13 @@ import torch
 
 from . import _native
 from ._native import LogmelError
-from .decode import BeamStep, KvCache, beam_step, linear
+from .decode import BeamStep, KvCache, beam_step, decode_error, linear
 
 __all__ = ["log_mel_from_stft", "log_mel_from_stft_workspace_size", "workspace_error", "LogmelError",
            "pack_mel_filters", "log_mel_from_stft_host", "log_mel_from_stft_host_workspace_size",
            "describe_log_mel_from_stft", "MelSpectrogram", "mel_spectrogram", "library_path",
-           "log_mel_from_stft_op", "mel_spectrogram_op", "linear", "KvCache", "beam_step", "BeamStep"]
+           "log_mel_from_stft_op", "mel_spectrogram_op", "linear", "KvCache", "beam_step", "BeamStep",
+           "decode_error"]
 
 
 def library_path():

@@ -115,6 +115,10 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.lm_linear_workspace_size.restype = ctypes.c_int
     L.lm_linear.argtypes = [vp, vp, sz, vp]
     L.lm_linear.restype = ctypes.c_int
+    L.lm_decode_error.argtypes = [vp, i32, vp]
+    L.lm_decode_error.restype = ctypes.c_int
+    L.lm_debug_linear_withhold.argtypes = [vp, vp, sz, i64, ctypes.c_uint64, vp]
+    L.lm_debug_linear_withhold.restype = ctypes.c_int
     L.lm_kv_append.argtypes = [vp, i32, vp, vp, vp, vp, i32, vp, i32, vp, vp, vp]
     L.lm_kv_append.restype = ctypes.c_int
     L.lm_kv_read.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]

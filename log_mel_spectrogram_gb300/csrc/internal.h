@@ -86,6 +86,13 @@ const char *env_or(const char *name, const char *fallback);
 // baked into a graph would repeat on every replay) or when the query fails.
 uint64_t call_token(cudaStream_t stream);
 
+// --- decoding operations ---------------------------------------------------
+
+// What the kernels of linear.cu and kv_attend.cu have reported on the current device since it was last
+// cleared, added to *value.
+lm_status linear_error(uint32_t *value, bool clear, cudaStream_t stream);
+lm_status attend_error(uint32_t *value, bool clear, cudaStream_t stream);
+
 // --- log_mel_from_stft -----------------------------------------------------
 
 // Workspace bytes of lm_log_mel_from_stft for this shape.

@@ -69,6 +69,8 @@ constexpr int ring_stages(int d, bool shared) { return shared ? 4 : d == 128 ? 2
 constexpr int resident_ctas(int d) { return d == 128 ? 3 : 4; }
 constexpr int full_ctas(int d) { return 152 * resident_ctas(d); }
 
+__device__ uint32_t g_attend_error;  // bits of every call on the device, whatever its workspace
+
 struct AttendParams {
   KvView c;
   const void *q;
@@ -607,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   };
   if constexpr (ALONE) {
     __syncwarp();
+    if (done < mine && lane == 0) atomicOr(&g_attend_error, kErrMbarTimeout);
     if (head >= p.c.heads || done < mine) return;
     for (int x = lane; x < q_rows * PER; x += 32) {
       const int rr = x / PER, d = x % PER * 4;
@@ -616,6 +619,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   }
   __syncthreads();
   const bool gave_up = sh.abort;
+  if (gave_up && threadIdx.x == 0) atomicOr(&g_attend_error, kErrMbarTimeout);
   const int64_t part0 = (unit * p.splits + split) * p.part_rows;
   const float2 *const ml_s = &sh.ml[0][0];  // SHARED: row rr is in place rr; else in warp w's place rr
   constexpr int FROM = SHARED ? 1 : kWarps;
@@ -884,6 +888,9 @@ lm_status attend(const lm_kv_cache *cache, int32_t layer, const void *q, const i
 }
 
 }  // namespace
+
+lm_status attend_error(uint32_t *value, bool clear, cudaStream_t s) { return read_sticky(g_attend_error, value, clear, s); }
+
 }  // namespace lm
 
 extern "C" lm_status lm_kv_attend_workspace_size(const lm_kv_cache *cache, int32_t tokens, int32_t q_heads,

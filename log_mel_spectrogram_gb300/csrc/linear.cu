@@ -50,6 +50,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
+#include "waits.cuh"
 
 namespace lm {
 namespace {
@@ -85,7 +86,11 @@ struct LinearParams {
   uint32_t idesc;
   float scale;
   uint32_t *err;
+  uint64_t wait_ns;                      // limit of a wait
+  int32_t withheld;                      // CTA whose first stage never fills (tests), or -1
 };
+
+__device__ uint32_t g_linear_error;  // bits of every call on the device, whatever its workspace
 
 struct alignas(16) Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&b.full[i], 1);
+      mbar_init(&b.full[i], i == 0 && static_cast<int>(blockIdx.x) == p.withheld ? 2 : 1);
       mbar_init(&b.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       const Tile tile = tile_at(p, t, lane_rank);
       const int col0 = tile.col0 + (PAIR ? rank * col_rows : 0);
       for (int kb = k_begin; kb < k_end; ++kb) {
-        if (fills >= p.stages) ok = __all_sync(0xffffffffu, mbar_wait(&b.empty[s], phase, abort, p.err));
+        if (fills >= p.stages) ok = mbar_wait_warp(&b.empty[s], phase, p.wait_ns, abort, p.err);
         if (!ok) break;
         if (elect_one()) {
           uint8_t *const dst = ring + s * stage_bytes;
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     if (!ok) {
       if (!PAIR || rank == 0) {
         for (int f = fills > p.stages ? fills - p.stages : 0; f < fills; ++f)
-          mbar_wait_drain(&b.full[f % p.stages], (f / p.stages) & 1, p.err);
+          mbar_drain(&b.full[f % p.stages], (f / p.stages) & 1, p.wait_ns, p.err);
       } else {  // counted on the other CTA's barriers: time enough for any copy
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 10000000ull) __nanosleep(1000);
@@ -400,12 +405,11 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       const uint32_t ring_a = smem_u32(ring);
       for (int t = first; t < p.tiles && ok; t += step, ++tiles) {
         const int half = tiles & 1;
-        if (tiles >= 2)
-          ok = __all_sync(0xffffffffu, mbar_wait(&b.acc_empty[half], ((tiles >> 1) - 1) & 1, abort, p.err));
+        if (tiles >= 2) ok = mbar_wait_warp(&b.acc_empty[half], ((tiles >> 1) - 1) & 1, p.wait_ns, abort, p.err);
         tcgen05_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
         for (int kb = k_begin; kb < k_end && ok; ++kb) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&b.full[s], phase, abort, p.err));
+          ok = mbar_wait_warp(&b.full[s], phase, p.wait_ns, abort, p.err);
           if (!ok) break;
           tcgen05_fence_after();
           const uint64_t a = smem_desc_k128(ring_a + s * stage_bytes);
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       }
       if (!ok) {  // products in flight end before the tensor memory is given back
         if (elect_one()) tcgen05_commit<PAIR>(&b.drain);
-        mbar_wait_drain(&b.drain, 0, p.err);
+        mbar_drain(&b.drain, 0, p.wait_ns, p.err);
       }
     }
   } else if (warp >= 4) {
@@ -446,7 +450,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                            tile.lane0 + 32 * (e % 4) + static_cast<int>(threadIdx.x % 32));
       }
       // One decision per warp: tensor memory loads are executed by whole warps.
-      if (!__all_sync(0xffffffffu, mbar_wait(&b.acc_full[half], (tiles >> 1) & 1, abort, p.err))) break;
+      if (!mbar_wait_warp(&b.acc_full[half], (tiles >> 1) & 1, p.wait_ns, abort, p.err)) break;
       tcgen05_fence_after();
       const uint32_t acc = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
       if (SPLIT) {
@@ -491,6 +495,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   }
   tcgen05_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort) atomicOr(&g_linear_error, kErrMbarTimeout);
   if (PAIR) cluster_sync_all();  // ... or its barriers and tensor memory are in use
   if (warp == 2) {
     tcgen05_fence_after();
@@ -771,19 +776,9 @@ Cut best_cut(int64_t n, int64_t rows, int64_t groups, int kblocks, bool activati
   return best;
 }
 
-}  // namespace
-}  // namespace lm
-
-extern "C" lm_status lm_linear_workspace_size(const lm_linear_args *args, size_t *bytes) {
-  if (!bytes) return LM_ERR_INVALID_ARG;
-  if (lm_status st = lm::check(args); st != LM_OK) return st;
-  *bytes = lm::plan(*args).bytes;
-  return LM_OK;
-}
-
-extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size_t workspace_bytes,
-                               lm_stream_t stream) {
-  using namespace lm;
+// lm_linear; `fault` is null outside tests.
+lm_status run(const lm_linear_args *args, void *workspace, size_t workspace_bytes, cudaStream_t s,
+              const WaitFault *fault) {
   if (lm_status st = check(args); st != LM_OK) return st;
   const lm_linear_args &a = *args;
   if (a.groups * a.rows == 0 || a.n == 0) return LM_OK;
@@ -797,7 +792,6 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
   if (out_meets_inputs(a, pl, static_cast<int64_t>(out_size))) return LM_ERR_INVALID_ARG;
   DeviceInfo dev;
   if (lm_status st = current_device_info(&dev); st != LM_OK) return st;
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *const scratch = static_cast<char *>(workspace) + 256;
   const size_t x_bytes = pl.x.bytes;
   if (pl.x.pack)
@@ -819,6 +813,8 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
   p.act = a.activation;
   p.scale = a.scale;
   p.err = static_cast<uint32_t *>(workspace);
+  p.wait_ns = fault ? fault->wait_ns : kWaitTimeoutNs;
+  p.withheld = fault ? static_cast<int32_t>(fault->withheld_cta) : -1;
   const bool bf16 = a.dtype == LM_BF16;
 
   Resident held;
@@ -859,4 +855,30 @@ extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size
   }
   return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), threads_of(cut.form), static_cast<size_t>(smem), s,
                           cluster, lanes, cols, p);
+}
+
+}  // namespace
+
+lm_status linear_error(uint32_t *value, bool clear, cudaStream_t s) { return read_sticky(g_linear_error, value, clear, s); }
+
+}  // namespace lm
+
+extern "C" lm_status lm_linear_workspace_size(const lm_linear_args *args, size_t *bytes) {
+  if (!bytes) return LM_ERR_INVALID_ARG;
+  if (lm_status st = lm::check(args); st != LM_OK) return st;
+  *bytes = lm::plan(*args).bytes;
+  return LM_OK;
+}
+
+extern "C" lm_status lm_linear(const lm_linear_args *args, void *workspace, size_t workspace_bytes,
+                               lm_stream_t stream) {
+  return lm::run(args, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream), nullptr);
+}
+
+extern "C" lm_status lm_debug_linear_withhold(const lm_linear_args *args, void *workspace, size_t workspace_bytes,
+                                              int64_t withheld_cta, uint64_t wait_ns, lm_stream_t stream) {
+  if (withheld_cta < 0 || withheld_cta > INT_MAX || wait_ns < 100000ull || wait_ns > lm::kWaitTimeoutNs)
+    return LM_ERR_INVALID_ARG;
+  const lm::WaitFault fault{withheld_cta, wait_ns};
+  return lm::run(args, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream), &fault);
 }

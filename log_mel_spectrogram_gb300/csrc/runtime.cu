@@ -142,6 +142,17 @@ extern "C" int lm_last_cuda_error(void) { return lm::g_last_cuda_error; }
 
 extern "C" int lm_version(void) { return 100; }
 
+extern "C" lm_status lm_decode_error(uint32_t *device_error, int32_t clear, lm_stream_t stream) {
+  if (!device_error) return LM_ERR_INVALID_ARG;
+  uint32_t v = 0;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  *device_error = 0;
+  if (lm_status st = lm::linear_error(&v, clear != 0, s); st != LM_OK) return st;
+  if (lm_status st = lm::attend_error(&v, clear != 0, s); st != LM_OK) return st;
+  *device_error = v;
+  return v ? LM_ERR_DEVICE_FAULT : LM_OK;
+}
+
 extern "C" lm_status lm_workspace_error(const void *workspace, size_t workspace_bytes, uint32_t *device_error,
                                         lm_stream_t stream) {
   if (!workspace || !device_error) return LM_ERR_INVALID_ARG;

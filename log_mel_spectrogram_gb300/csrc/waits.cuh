@@ -1,6 +1,7 @@
 // waits.cuh -- bounded mbarrier waits of whole warps, with a limit that the launch gives.
 #pragma once
 
+#include "internal.h"
 #include "ptx.cuh"
 
 namespace lm {
@@ -46,6 +47,20 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, u
 // Waits for copies that are in flight, whatever the other warps did (no abort flag).
 __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity, uint64_t limit_ns, uint32_t *err_word) {
   mbar_wait_limited(smem_u32(bar), parity, limit_ns, nullptr, err_word);
+}
+
+// Host side of a translation unit's sticky word: reads the current device's into *value (bits are
+// added to it), and clears it where `clear` says so.
+template <typename Word>
+lm_status read_sticky(const Word &word, uint32_t *value, bool clear, cudaStream_t s) {
+  void *at = nullptr;
+  uint32_t v = 0;
+  LM_CUDA_TRY(cudaGetSymbolAddress(&at, word));
+  LM_CUDA_TRY(cudaMemcpyAsync(&v, at, sizeof(v), cudaMemcpyDeviceToHost, s));
+  if (clear) LM_CUDA_TRY(cudaMemsetAsync(at, 0, sizeof(v), s));
+  LM_CUDA_TRY(cudaStreamSynchronize(s));
+  *value |= v;
+  return LM_OK;
 }
 
 }  // namespace lm

@@ -7,11 +7,13 @@ its attention, and beam search, over the same C ABI (include/logmel.h).
   block of tokens and head: ``append``, ``attend``, ``advance``, ``read`` and
   ``reorder``.
 * ``beam_step(logits, scores, ...)`` -- the best continuations of every clip.
+* ``decode_error()`` -- whether a wait inside a kernel of these has run out.
 
 Inference only, CUDA only, on torch's current stream unless `stream` is given.
 """
 from __future__ import annotations
 
+import ctypes
 import importlib.util
 import struct
 from typing import NamedTuple
@@ -21,7 +23,7 @@ import torch
 from . import _native
 from . import build as _build
 
-__all__ = ["linear", "KvCache", "beam_step", "BeamStep"]
+__all__ = ["linear", "KvCache", "beam_step", "BeamStep", "decode_error"]
 
 _HALF = {torch.float16: _native.DTYPES["f16"], torch.bfloat16: _native.DTYPES["bf16"]}
 _FLOAT = {torch.float32: _native.DTYPES["f32"], **_HALF}
@@ -51,6 +53,20 @@ def _checked(r, what: str):
     if type(r) is int:
         _native.check(r, what)
     return r
+
+
+def decode_error(device=None, *, clear: bool = True) -> int:
+    """Waits for the device and returns the error bits that linear() and
+    KvCache.attend() have reported on it since the last call (0: none), replayed
+    graphs included.  Every wait inside their kernels is bounded; one that runs out
+    ends the kernel, sets a bit here, and leaves outputs that are not whole."""
+    v = ctypes.c_uint32()
+    with torch.cuda.device(device):
+        torch.cuda.synchronize()
+        rc = _native.lib().lm_decode_error(ctypes.byref(v), int(clear), torch.cuda.current_stream().cuda_stream)
+    if v.value == 0:
+        _native.check(rc, "lm_decode_error")
+    return v.value
 
 
 # ---------------------------------------------------------------------------

@@ -117,7 +117,8 @@ class KvCache:
 
     Tokens past max_tokens (rounded up to whole blocks) are dropped.  The
     tensors k8, v8 [layers, blocks, heads, block, head_dim], k_scale, v_scale
-    [layers, blocks, heads], table, spare and lens may be written in place."""
+    [layers, blocks, heads], table, spare and lens may be written in place.
+    copy.deepcopy and pickle give a cache of its own with the same contents."""
 
     def __init__(self, rows: int, max_tokens: int, heads: int, head_dim: int, *, layers: int = 1, block: int = 32,
                  dtype: torch.dtype = torch.bfloat16, device=None):
@@ -149,10 +150,25 @@ class KvCache:
         self._spare = order[rows * width:]
         self._lens = torch.zeros(rows, dtype=torch.int32, device=dev)
         self._code = _HALF[dtype]
-        self._args = struct.pack("7Pq6i", *(t.data_ptr() for t in (self._k8, self._v8, self._k_scale, self._v_scale,
-                                                                  self._table, self._spare, self._lens)),
-                                 blocks, layers, rows, width, heads, head_dim, block)
-        self._head = (self._args, dev.index, self._code)
+        self._bind()
+
+    def _bind(self):
+        """The C struct of this object's own tensors."""
+        tensors = (self._k8, self._v8, self._k_scale, self._v_scale, self._table, self._spare, self._lens)
+        if len({t.device for t in tensors}) != 1 or not self._k8.is_cuda:
+            raise ValueError("a KvCache's tensors must be on one CUDA device")
+        self.device = self._k8.device
+        self._args = struct.pack("7Pq6i", *(t.data_ptr() for t in tensors), self.blocks, self.layers, self.rows,
+                                 self.width, self.heads, self.head_dim, self.block)
+        self._head = (self._args, self.device.index, self._code)
+
+    # Copies and pickles hold tensors of their own (copy.copy shares them), and their addresses.
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k not in ("_args", "_head")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._bind()
 
     k8 = property(lambda self: self._k8)
     v8 = property(lambda self: self._v8)

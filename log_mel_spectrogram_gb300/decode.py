@@ -4,8 +4,8 @@ its attention, and beam search, over the same C ABI (include/logmel.h).
 * ``linear(x, weight, bias, ...)`` -- act(x W^T + bias), scaled, plus residual;
   x may be overlapping windows of feature frames, read in place.
 * ``KvCache`` -- keys and values of a model's rows in 8 bits, one scale per
-  block of tokens and head: ``append``, ``attend``, ``advance``, ``read`` and
-  ``reorder``.
+  block of tokens and head: ``append``, ``attend``, ``advance``, ``read``,
+  ``reorder`` and ``reset``.
 * ``beam_step(logits, scores, ...)`` -- the best continuations of every clip.
 * ``decode_error()`` -- whether a wait inside a kernel of these has run out.
 
@@ -118,7 +118,12 @@ class KvCache:
     Tokens past max_tokens (rounded up to whole blocks) are dropped.  The
     tensors k8, v8 [layers, blocks, heads, block, head_dim], k_scale, v_scale
     [layers, blocks, heads], table, spare and lens may be written in place.
-    copy.deepcopy and pickle give a cache of its own with the same contents."""
+    copy.deepcopy and pickle give a cache of its own with the same contents.
+
+    A row's blocks from the one that lens[r] falls in onwards must be its own, or
+    two rows write one block at once.  ``reorder`` lets the rows of a clip share the
+    blocks in front of that one: after it lens must not be set back, and a cache
+    that takes other sequences is emptied by ``reset`` first."""
 
     def __init__(self, rows: int, max_tokens: int, heads: int, head_dim: int, *, layers: int = 1, block: int = 32,
                  dtype: torch.dtype = torch.bfloat16, device=None):
@@ -217,6 +222,17 @@ class KvCache:
             with torch.cuda.stream(stream):
                 return self.advance(tokens)
         self._lens.add_(tokens)
+
+    def reset(self, *, stream=None) -> None:
+        """Empties the cache: no tokens, and every row has blocks of its own again
+        (table and spare as at construction)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.reset()
+        own = self.rows * self.width
+        torch.arange(own, dtype=torch.int32, device=self.device, out=self._table.view(-1))
+        torch.arange(own, self.blocks, dtype=torch.int32, device=self.device, out=self._spare)
+        self._lens.zero_()
 
     def read(self, layer: int | None, start: int, count: int, *, stream=None):
         """(k, v), the values that tokens start .. start + count - 1 stand for:

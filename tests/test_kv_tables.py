@@ -15,6 +15,52 @@ def lm():
     return log_mel_spectrogram_gb300
 
 
+def search(lm, c, seed, steps, clips, beams):
+    """Steps of append, attend, advance and reorder; the attentions' outputs."""
+    r, outs = kv.gen(seed), []
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for _ in range(steps):
+        q, k, v = (r(c.rows, 1, c.heads, c.head_dim).to(c.dtype) for _ in range(3))
+        c.append(0, k, v)
+        outs.append(c.attend(0, q))
+        c.advance(1)
+        c.reorder(torch.randint(0, beams, (clips, beams), generator=g, device="cuda", dtype=torch.int32))
+    return torch.stack(outs)
+
+
+@pytest.mark.parametrize("block,steps", [(16, 40), (32, 33), (16, 7)])
+def test_a_cache_is_used_again(lm, block, steps):
+    clips, beams = 2, 3
+    c = lm.KvCache(clips * beams, 48, 2, 64, block=block, dtype=torch.float16)
+    first = search(lm, c, 1, steps, clips, beams)
+    if steps > block:
+        assert c.table[:, 0].unique().numel() < c.rows  # rows share blocks that the next search writes
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c.reset(stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    names = torch.cat([c.table.flatten(), c.spare])
+    assert torch.equal(names.sort().values, torch.arange(c.blocks, device="cuda", dtype=torch.int32))
+    assert not c.lens.any()
+    again = search(lm, c, 2, steps, clips, beams)
+    fresh = lm.KvCache(clips * beams, 48, 2, 64, block=block, dtype=torch.float16)
+    assert torch.equal(again, search(lm, fresh, 2, steps, clips, beams))
+    c.reset()
+    assert torch.equal(first, search(lm, c, 1, steps, clips, beams))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.reset()
+    g.replay()
+    assert torch.equal(again, search(lm, c, 2, steps, clips, beams))
+
+
+def test_reset_of_empty_caches(lm):
+    for rows, tokens in ((0, 64), (3, 0)):
+        c = lm.KvCache(rows, tokens, 2, 64)
+        c.reset()
+        assert c.table.shape == (rows, -(-tokens // 32)) and c.spare.tolist() == list(range(rows * c.width, c.blocks))
+
+
 @pytest.mark.parametrize("block", [16, 32])
 @pytest.mark.parametrize("rows,heads,dim,tokens,t", [(3, 2, 64, 90, 1), (2, 1, 128, 75, 3), (1, 2, 32, 9000, 1),
                                                      (160, 5, 64, 70, 1), (48, 10, 64, 160, 64)])

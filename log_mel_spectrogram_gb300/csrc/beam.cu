@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 2) beam_kernel(
     const int t0 = tile0 + lane * N;  // vector i holds the tokens from t0 + 32 N i on
     uint32_t w[kVecs][4];
     auto load = [&](int at) {
-      return at >= 0 && at + N <= vocab ? __ldg(reinterpret_cast<const uint4 *>(x + at)) : load_edge(x, at, vocab);
+      return at >= 0 && at + N <= vocab ? *reinterpret_cast<const uint4 *>(x + at) : load_edge(x, at, vocab);
     };
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 2) beam_kernel(
   for (uint32_t i = threadIdx.x; i < told; i += kThreads) {
     const uint32_t b = i / width, c = i - b * width;
     const int64_t at = parents[b] * static_cast<int64_t>(width) + c;
-    to[i] = c == a.length ? tokens[b] : ahead ? history[at] : __ldg(from + at);
+    to[i] = c == a.length ? tokens[b] : ahead ? history[at] : from[at];
   }
 }
 

@@ -37,7 +37,10 @@ lm_status ensure_smem_attribute(const void *kernel, int bytes);
 // Launches `kernel` as a programmatic dependent of what precedes it on the
 // stream: its CTAs may start, and set up their shared memory, while the grid
 // before is still running; the kernel calls pdl_wait() before its first access
-// to global memory, and pdl_launch() to let the next grid do the same.
+// to global memory, and pdl_launch() to let the next grid do the same.  Such a
+// kernel lives while the one before still writes, so it reads global memory
+// through plain loads: a non-coherent one (__ldg) promises that nobody writes
+// while the kernel lives, and pdl_wait() does not hold it back.
 template <typename... P, typename... A>
 lm_status launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
                            A &&...args) {

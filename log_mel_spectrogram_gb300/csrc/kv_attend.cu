@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   if (split == 0 && p.c.width > 0) {
     const int t = (MODE != Mode::kTokens ? lane : lane * kWarps + warp) * kTok;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) early[e] = __ldg(table + min((t + 16 * e) >> block_shift, p.c.width - 1));
+    for (int e = 0; e < 2; ++e) early[e] = table[min((t + 16 * e) >> block_shift, p.c.width - 1)];
   }
   const int q_first = qt * QT, q_rows = min(QT, p.qrows - q_first);
   uint32_t raw[E][2 * KW];
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
     } else if (p.qvec) {
 #pragma unroll
       for (int j = 0; j < 2 * KW; j += 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + 2 * j));
+        const uint4 v = *reinterpret_cast<const uint4 *>(src + 2 * j);
         w[j] = v.x;
         w[j + 1] = v.y;
         w[j + 2] = v.z;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   auto block_of = [&](int j, int half) {
     const int t = token_of(j) + 16 * half;
     if (j >= mine || t >= stop) return -1;
-    const int b = j < 32 && split == 0 ? early[half] : __ldg(table + (t >> block_shift));
+    const int b = j < 32 && split == 0 ? early[half] : table[t >> block_shift];
     return b >= 0 && b < p.c.blocks ? b : -1;
   };
   int fb0 = -1, fb1 = -1;  // blocks of the 32 tiles that are fetched next, one per lane
@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
         f_s[e] = l_s[e] = i_s[e] = 0.0f;
         if (b >= 0) {
           const int64_t tile = tiles0 + static_cast<int64_t>(b) * p.c.heads;
-          const float vs = fmaxf(__ldg(p.c.v_scale + tile), kMinScale);
-          f_s[e] = __ldg(p.c.k_scale + tile);
+          const float vs = fmaxf(p.c.v_scale[tile], kMinScale);
+          f_s[e] = p.c.k_scale[tile];
           l_s[e] = __log2f(vs);
           i_s[e] = ex2(-l_s[e]);  // of the logarithm that the weight has: they cancel
         } else {

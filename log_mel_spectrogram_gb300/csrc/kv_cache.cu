@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
   if (full) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + i * src_step));
+      const uint4 w = *reinterpret_cast<const uint4 *>(src + i * src_step);
       x[i][0] = w.x;
       x[i][1] = w.y;
       x[i][2] = w.z;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
     } else if (tok < all) {
       const T *const s = src + i * src_step;
       if (p.vec) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(s));
+        const uint4 w = *reinterpret_cast<const uint4 *>(s);
         x[i][0] = w.x;
         x[i][1] = w.y;
         x[i][2] = w.z;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
     const uint32_t tok = static_cast<uint32_t>(p.start) + t0 + i;
     if (i == 0 || (tok & in_block) == 0) {
       const uint32_t col = tok >> block_shift;
-      const int blk = tok < len && col < static_cast<uint32_t>(p.c.width) ? __ldg(table + col) : -1;
+      const int blk = tok < len && col < static_cast<uint32_t>(p.c.width) ? table[col] : -1;
       block = nullptr;
       scale = 0.0f;
       if (blk >= 0 && blk < p.c.blocks) {

@@ -321,18 +321,18 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
   // it.  (Bytes turn into f16 in two instructions, into bf16 in three.)
   uint32_t q[KW][4];
   int limit[E];
-  // Key bytes go in as (k + 128) * 2^-24, which takes half the instructions of
-  // k: a score is product * 2^24 - 128 * (sum of q).  (The sums are in 32 bits;
-  // 128 sum q is of the size of the largest scores the block's scale allows.)
-  float back[E];  // the power's inverse, times scale, log2 e and 2^24
-  float bias[E];  // 128 * 2^-24 * sum of q
+  // Key bytes go in as they are, whole numbers in f16.  (As k + 128, in subnormal f16, they take
+  // three instructions a word instead of five -- two rows of 131000 tokens 94.2 us, so 96.9 -- but
+  // 128 sum q has to be taken off again, and a score is then off by the rounding of the largest one
+  // that the block's scale allows: too much where one element of the head is an outlier.)
+  float back[E];  // the power's inverse, times scale and log2 e
   const float log2e = 1.4426950408889634f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int i = q_i[e];
     limit[e] = i < 0 ? INT_MAX : !p.causal ? total : i < fresh ? min(total, held + i + 1) : 0;
     uint32_t *const w = raw[e];
-    back[e] = p.scale * log2e * 16777216.0f;
+    back[e] = p.scale * log2e;
     if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
       uint32_t top = 0;  // |q| as integers
 #pragma unroll
@@ -349,15 +349,6 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
         w[j] = pack2<__half>(f.x * up, f.y * up);
       }
     }
-    float total_q = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 2 * KW; ++j) {
-      const float2 f = unpack2<__half>(w[j]);
-      total_q += f.x + f.y;
-    }
-    total_q += __shfl_xor_sync(0xffffffffu, total_q, 1);
-    total_q += __shfl_xor_sync(0xffffffffu, total_q, 2);
-    bias[e] = total_q * (128.0f / 16777216.0f);
 #pragma unroll
     for (int s = 0; s < KW; ++s) {
       q[s][e] = w[2 * s];
@@ -396,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
 #pragma unroll
     for (int ks = 0; ks < KW; ++ks) {
       uint32_t b0, b1;
-      bytes_to_subnormal(w[ks], b0, b1);
+      word_to_f16(w[ks], b0, b1);
       sts_u32(k16 + piece_at<D>(to, 2 * ks) + 4 * c4, b0);
       sts_u32(k16 + piece_at<D>(to, 2 * ks + 1) + 4 * c4, b1);
     }
@@ -461,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
 #pragma unroll
         for (int ks = 0; ks < KW; ++ks) {
           uint32_t b0, b1;
-          bytes_to_subnormal(w[ks], b0, b1);
+          word_to_f16(w[ks], b0, b1);
           mma16816(sc[n8], q[ks], b0, b1);
         }
       }
@@ -474,12 +465,11 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float g0 = f0 * back[e], g1 = f1 * back[e];
-      const float h0 = fmaf(-g0, bias[e], l0), h1 = fmaf(-g1, bias[e], l1);
 #pragma unroll
       for (int n8 = 0; n8 < 4; ++n8) {
 #pragma unroll
         for (int x = 2 * e; x < 2 * e + 2; ++x)
-          sc[n8][x] = fmaf(sc[n8][x], n8 < 2 ? g0 : g1, n8 < 2 ? h0 : h1);
+          sc[n8][x] = fmaf(sc[n8][x], n8 < 2 ? g0 : g1, n8 < 2 ? l0 : l1);
       }
       cut = cut || t0 > limit[e] - kTok;
     }

@@ -676,7 +676,9 @@ lm_status lm_beam_step(const lm_beam_args *args, void *workspace, size_t workspa
  * same length.  Whole blocks are shared by copying table entries; the block
  * that the next token falls in, where it holds tokens, is copied for every
  * layer into the row's spare block, which changes places with it.  A row
- * that continues itself is left alone.
+ * that continues itself is left alone.  An absent open block (table entry
+ * outside [0, blocks)) stays absent in the rows that continue its row; a row
+ * whose own is absent gives that entry to its spare when it continues another.
  *   workspace device, >= 16 + 4 * clips bytes, 16-byte aligned, zeroed before
  *             its first use, left usable by every call.
  * Errors as above, and LM_ERR_INVALID_ARG where spare is NULL or rows is not

@@ -430,14 +430,17 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const ReorderParams p
     const int c = c1 + c0;
     const bool moves = c0 < step && c < cols && parent != row0 + i;
     int next = 0, was = 0;
+    bool copied = false;
     if (moves) {
       was = p.c.table[(row0 + i) * width + c];
-      next = c < col ? p.c.table[parent * width + c] : mine;
+      next = p.c.table[parent * width + c];
+      copied = c == col && next >= 0 && next < p.c.blocks;  // (an absent block stays absent)
+      if (copied) next = mine;
     }
     __syncthreads();
     if (moves) {
       p.c.table[(row0 + i) * width + c] = next;
-      if (c == col) p.c.spare[row0 + i] = was;
+      if (copied) p.c.spare[row0 + i] = was;
     }
   }
 }

@@ -61,6 +61,33 @@ def test_reset_of_empty_caches(lm):
         assert c.table.shape == (rows, -(-tokens // 32)) and c.spare.tolist() == list(range(rows * c.width, c.blocks))
 
 
+@pytest.mark.parametrize("absent", [-1, 2 ** 31 - 1])
+@pytest.mark.parametrize("beams", [2, 5])
+def test_an_absent_open_block_stays_absent(lm, absent, beams):
+    """Rows that continue a row without its open block have the tokens that it has, and keep their spare block."""
+    c = kv.filled(lm, beams, 64, 1, 64, 32, torch.float16, seed=3)
+    c.lens.fill_(40)
+    c.table[0, 1] = absent
+    spare = c.spare.clone()
+    q = kv.gen(3)(1, 1, 1, 64).half().expand(beams, -1, -1, -1)
+    want = c.attend(0, q, causal=False)[0].clone()
+    c.reorder(torch.zeros((1, beams), dtype=torch.int32, device="cuda"))
+    assert torch.equal(c.attend(0, q, causal=False), want.expand(beams, -1, -1, -1))
+    assert (c.table[:, 1] == absent).all() and torch.equal(c.spare, spare)
+    assert not c.read(0, 32, 8)[0].any()
+
+
+def test_a_row_without_its_open_block_takes_another(lm):
+    c = kv.filled(lm, 2, 64, 2, 64, 32, torch.float16, seed=4)
+    c.lens.fill_(40)
+    c.table[1, 1] = -1
+    mine = int(c.spare[1])
+    c.reorder(torch.zeros((1, 2), dtype=torch.int32, device="cuda"))
+    k, v = c.read(0, 0, 40)
+    assert torch.equal(k[0], k[1]) and torch.equal(v[0], v[1]) and k.any()
+    assert int(c.table[1, 1]) == mine and int(c.spare[1]) == -1
+
+
 @pytest.mark.parametrize("block", [16, 32])
 @pytest.mark.parametrize("rows,heads,dim,tokens,t", [(3, 2, 64, 90, 1), (2, 1, 128, 75, 3), (1, 2, 32, 9000, 1),
                                                      (160, 5, 64, 70, 1), (48, 10, 64, 160, 64)])

@@ -56,10 +56,17 @@ const Tensor *on(PyObject *o, const char *name, int dev) {
   return t;
 }
 
+// Neither direction of differentiation passes through these operations.  (Tangents exist under
+// no_grad, too.)
 void no_grad(std::initializer_list<const Tensor *> ts) {
-  if (!c10::GradMode::is_enabled()) return;
+  const bool backward = c10::GradMode::is_enabled();
   for (const Tensor *t : ts)
-    if (t && t->requires_grad()) throw GradError{};
+    if (t && ((backward && t->requires_grad()) || t->_fw_grad(0).defined())) throw GradError{};
+}
+
+// What a user's tensor holds has changed: a graph that saved it finds out.
+void written(const Tensor *t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
 
 int half_code(at::ScalarType t) { return t == at::kHalf ? LM_F16 : t == at::kBFloat16 ? LM_BF16 : -1; }
@@ -123,7 +130,7 @@ PyObject *linear(PyObject *const *a) {
   const Tensor *w = on(a[1], "weight", dev), *bias = on(a[2], "bias", dev), *res = on(a[4], "residual", dev),
                *given = on(a[6], "out", dev);
   if (!w) refuse("weight must be a CUDA tensor");
-  no_grad({&x, w, bias, res});
+  no_grad({&x, w, bias, res, given});
   const int64_t dims = x.dim(), k = x.size(-1);
   if (w->scalar_type() != x.scalar_type() || w->dim() != 2 || w->size(1) != k)
     refuse("weight must be [N, K] of x's dtype and last dimension");
@@ -204,7 +211,9 @@ PyObject *linear(PyObject *const *a) {
     const Tensor ws = workspace(kLinear, dev, s, need);
     rc = lm_linear(&p, ws.data_ptr(), static_cast<size_t>(ws.numel()), reinterpret_cast<lm_stream_t>(s));
   }
-  return rc == LM_OK ? THPVariable_Wrap(out) : status(rc);
+  if (rc != LM_OK) return status(rc);
+  written(given);
+  return THPVariable_Wrap(out);
 }
 
 // ---- the cache: args, device, dtype come first ----
@@ -288,7 +297,6 @@ PyObject *kv_attend(PyObject *const *a) {
   const int layer = layer_of(c, a[3]);
   int64_t qs[3];
   const Tensor &q = tokens_of(c, a[4], "q", -1, qs);
-  no_grad({&q});
   const int64_t t = q.size(1), hq = q.size(2);
   if (hq == 0 || hq % c.c.heads) refuse("q must have a multiple of " + std::to_string(c.c.heads) + " heads");
   if (t > INT32_MAX || hq > INT32_MAX) return status(LM_ERR_UNSUPPORTED);
@@ -299,6 +307,7 @@ PyObject *kv_attend(PyObject *const *a) {
   if (PyErr_Occurred()) return nullptr;
   const c10::cuda::OptionalCUDAGuard guard(q.device());
   const Tensor *given = on(a[8], "out", c.dev);
+  no_grad({&q, given});
   if (given && (given->scalar_type() != q.scalar_type() || given->sizes() != q.sizes() || !given->is_contiguous()))
     refuse("out must be contiguous, of q's dtype and shape");
   Tensor out = given ? *given : make(q.sizes(), q.scalar_type(), c.dev);
@@ -311,7 +320,9 @@ PyObject *kv_attend(PyObject *const *a) {
                       causal ? static_cast<int32_t>(t) : 0, causal, static_cast<float>(scale), c.code, out.data_ptr(),
                       ws.data_ptr(), static_cast<size_t>(ws.numel()), reinterpret_cast<lm_stream_t>(s));
   }
-  return rc == LM_OK ? THPVariable_Wrap(out) : status(rc);
+  if (rc != LM_OK) return status(rc);
+  written(given);
+  return THPVariable_Wrap(out);
 }
 
 // kv_read(args, device, dtype, layer or -1, start, count)
@@ -446,8 +457,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     PyErr_SetString(PyExc_ValueError, e.what());
   } catch (const GradError &) {
     PyErr_SetString(PyExc_RuntimeError,
-                    "log_mel_spectrogram_gb300 ops are inference-only: inputs must not require grad "
-                    "(use torch.no_grad() or detach())");
+                    "log_mel_spectrogram_gb300 ops are inference-only: tensors must not require grad (use "
+                    "torch.no_grad() or detach()) or carry a tangent");
   } catch (const std::exception &e) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {

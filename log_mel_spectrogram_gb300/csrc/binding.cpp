@@ -79,22 +79,53 @@ Tensor make(at::IntArrayRef shape, at::ScalarType type, int dev) {
 
 enum Op { kLinear, kAttend, kBeam, kReorder };
 
+constexpr int64_t kLeastBytes = 1 << 16;  // of a workspace that is kept
+constexpr size_t kMostKept = 128;         // workspaces; past that the one whose last use is longest ago goes
+
 // A zeroed workspace.  An operation's kernels leave its counters at zero, so
 // one per operation, device and stream serves every call on it; a call that a
-// graph captures gets one of its own, cleared on each replay.
+// graph captures gets one of its own, cleared on each replay.  Streams go by
+// their ids: a handle comes back after its stream is destroyed, whose work may
+// still be under way.
+//
+// linear has no counters, and needs much where it copies an operand off 16-byte
+// boundaries (128 MB for a weight of 50001 x 1023): what is more than the least is that call's
+// alone, and nothing is cleared.
 Tensor workspace(Op op, int dev, cudaStream_t stream, size_t bytes) {
+  struct Kept {
+    Tensor t;
+    uint64_t used = 0;
+  };
+  using Key = std::tuple<int, int, unsigned long long>;
   static std::mutex mu;
-  static auto *const all = new std::map<std::tuple<int, int, cudaStream_t>, Tensor>;  // outlives the interpreter's end
+  static auto *const all = new std::map<Key, Kept>;  // outlives the interpreter's end
+  static uint64_t uses = 0;
   const auto options = at::TensorOptions().dtype(at::kByte).device(at::Device(at::kCUDA, dev));
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) (void)cudaGetLastError();
-  if (cs != cudaStreamCaptureStatusNone) return at::zeros({static_cast<int64_t>(bytes)}, options);
+  const bool captured = cs != cudaStreamCaptureStatusNone;
+  if (op == kLinear && (captured || bytes > static_cast<size_t>(kLeastBytes)))
+    return at::empty({static_cast<int64_t>(bytes)}, options);
+  if (captured) return at::zeros({static_cast<int64_t>(bytes)}, options);
+  unsigned long long id = 0;
+  if (const cudaError_t e = cudaStreamGetId(stream, &id); e != cudaSuccess) {
+    (void)cudaGetLastError();
+    throw std::runtime_error(std::string("cudaStreamGetId: ") + cudaGetErrorString(e));
+  }
   std::lock_guard<std::mutex> lk(mu);
-  Tensor &t = (*all)[std::make_tuple(static_cast<int>(op), dev, stream)];
-  if (!t.defined() || static_cast<size_t>(t.numel()) < bytes) {
-    int64_t size = 1 << 16;
+  Kept &k = (*all)[std::make_tuple(static_cast<int>(op), dev, id)];
+  k.used = ++uses;
+  if (!k.t.defined() || static_cast<size_t>(k.t.numel()) < bytes) {
+    int64_t size = kLeastBytes;
     while (static_cast<size_t>(size) < bytes) size *= 2;
-    t = at::zeros({size}, options);
+    k.t = at::zeros({size}, options);
+  }
+  const Tensor t = k.t;
+  if (all->size() > kMostKept) {
+    auto oldest = all->begin();
+    for (auto i = all->begin(); i != all->end(); ++i)
+      if (i->second.used < oldest->second.used) oldest = i;
+    all->erase(oldest);
   }
   return t;
 }

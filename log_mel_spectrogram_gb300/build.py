@@ -120,7 +120,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         binding = None if checked else ex.submit(_compile_binding, verbose)
         objs = list(ex.map(compile_one, sources()))
     tmp = out_dir / f"{lib.stem}.{os.getpid()}.so"
-    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", f"-soname={lib.name}", "-o", str(tmp), *map(str, objs)]
+    # (No soname: a program that links the library by its path then finds it there.)
+    cmd = [nvcc, *ARCH, "-shared", "-o", str(tmp), *map(str, objs)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

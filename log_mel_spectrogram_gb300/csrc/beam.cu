@@ -23,6 +23,7 @@
 #include "f32x2.cuh"
 #include "half.cuh"
 #include "internal.h"
+#include "pdl.cuh"
 #include "ptx.cuh"
 
 namespace lm {

@@ -42,6 +42,7 @@
 #include "internal.h"
 #include "kv_cache.cuh"
 #include "mma.cuh"
+#include "pdl.cuh"
 #include "ptx.cuh"
 #include "waits.cuh"
 

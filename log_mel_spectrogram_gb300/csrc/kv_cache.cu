@@ -16,6 +16,7 @@
 #include "half.cuh"
 #include "internal.h"
 #include "kv_cache.cuh"
+#include "pdl.cuh"
 #include "ptx.cuh"
 
 namespace lm {

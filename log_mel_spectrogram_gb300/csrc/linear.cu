@@ -48,6 +48,7 @@
 #include "f32x2.cuh"
 #include "half.cuh"
 #include "internal.h"
+#include "pdl.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 #include "waits.cuh"

@@ -544,8 +544,9 @@ typedef struct lm_kv_cache {
  * Appends tokens to one layer: row r's token i (i < counts[r], or < tokens
  * where counts is NULL) goes to place lens[r] + i.  lens itself is not
  * changed (every layer of a step appends at the same lengths).
- *   scale' = max(scale of what the block holds, max |new| / 127), 1 where
- *            that is 0;
+ *   scale' = max(scale of what the block holds, max |new| * c), 1 where that
+ *            is 0, with c the f32 nearest to 1 / 127 (so that scale' may be one
+ *            unit in the last place off max |new| / 127);
  *   what the block holds: q' = rint(q * (scale / scale')) where it grew;
  *   new tokens:           q  = rint(x / scale').
  * Ties round to even.  A NaN or infinity among a block's new tokens makes its

@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, part[w0 + w]);
   }
+  // (A product by definition, as in logmel.h: one in twenty maxima gives one unit in the last
+  // place more or less than top / 127.)
   float now = fmaxf(before, top * (1.0f / 127.0f));
   if (now == 0.0f) now = 1.0f;
   const float shrink = had ? before / now : 1.0f, inv = 1.0f / now;

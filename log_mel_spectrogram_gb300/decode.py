@@ -187,8 +187,8 @@ class KvCache:
                values: bool = False, stream=None):
         """Appends k, v [rows, tokens, heads, head_dim] to one layer, row r's
         first counts[r] tokens (all, where counts is None) at lens[r] on.  A
-        block's scale grows to its largest value / 127; where it grows, what
-        the block held is rounded anew.  lens stays as it is (see advance).
+        block's scale grows to its largest value times float32(1 / 127); where it
+        grows, what the block held is rounded anew.  lens stays as it is (see advance).
 
         values=True returns (k, v) as the cache then holds them: [rows, span,
         heads, head_dim] from the first token of the block that lens[r] falls

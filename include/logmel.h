@@ -588,8 +588,10 @@ lm_status lm_kv_read(const lm_kv_cache *cache, int32_t layer, int32_t start, int
  *            q_heads a multiple of the cache's heads: query head h reads
  *            key head h / (q_heads / heads).                   (read-only)
  *   counts   device, [rows] int32 or NULL: new tokens of this step that the
- *            cache already holds past lens[r], clamped to [0, tokens];
- *            NULL: new_tokens for every row.
+ *            cache already holds past lens[r], at least 0, and at most
+ *            `tokens` where causal is 1 (where it is 0, as many as the table
+ *            holds: queries need not be those tokens'); NULL: new_tokens for
+ *            every row.
  *   causal   1: query i stands at token lens[r] + i and sees tokens up to
  *            it; queries from counts[r] on see nothing.
  *            0: every query sees the lens[r] + counts[r] tokens.

@@ -498,8 +498,8 @@ lm_status lm_decode_error(uint32_t *device_error, int32_t clear, lm_stream_t str
 /* Fault injection for tests of the bounded waits: lm_linear, except that the
  * first tile of operands that CTA `withheld_cta` (>= 0) fetches never counts as
  * complete, and that waits give up after wait_ns (1e5 .. 2e9; 2 s otherwise).
- * The CTA sets bit 1 of the workspace's error word and ends; its outputs (and,
- * where CTAs share a tile's k, those of its tile) are incomplete. */
+ * The CTA sets bit 1 of the workspace's error word and ends; its outputs are
+ * not written (where CTAs share a tile's k, those of its tile are not right). */
 lm_status lm_debug_linear_withhold(const lm_linear_args *args, void *workspace, size_t workspace_bytes,
                                    int64_t withheld_cta, uint64_t wait_ns, lm_stream_t stream);
 

@@ -10,7 +10,8 @@ against liblogmel.so.
 
 ``build(checked=True)`` makes the bounds-checked debug variant
 ``_build/checked/liblogmel_checked.so`` (-DLOGMEL_CHECKED): the same sources
-with every computed global-memory index tested against its buffer.
+with every computed global-memory index of the STFT and waveform kernels tested
+against its buffer (the decoding kernels carry no such tests).
 """
 from __future__ import annotations
 

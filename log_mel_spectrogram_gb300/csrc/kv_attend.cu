@@ -27,13 +27,14 @@
 // Long rows are split over CTAs; the last one to finish a row and head joins
 // the parts in order.
 //
-// Measured: 5 queries of 64 rows over up to 1500 tokens, 16 heads of 64, 36 us
-// (3.4 TB/s: 1024 CTAs in two rounds, each 4 us of start-up and end, then per
-// tile the issue of about 400 instructions a warp); two rows of 131000 tokens,
-// 8 heads of 128, 95 us (5.7 TB/s, 85% of copy bandwidth); a step of 5 rows of
-// up to 448 tokens, 6.4 us (launch, three dependent loads, the join of 4 warps).
-// 223 causal queries over up to 448 tokens, 16 rows of 16 heads, 33 us: start-up and
-// end of CTAs that have at most 14 tiles.
+// Measured: 5 queries of 64 rows over up to 1500 tokens, 16 heads of 64, 36.6 us
+// (3.3 TB/s: 1024 CTAs in two rounds, each 4 us of start-up and end; in between
+// latency, as a warp's products, maxima, exponentials and products follow one another:
+// 0.48 instructions a cycle from 21% of the warps, which is what registers allow); two rows of
+// 131000 tokens, 8 heads of 128, 97 us (5.5 TB/s, 83% of copy bandwidth); a step of 5 rows of
+// up to 448 tokens, 6.3 us (launch, three dependent loads, the join of 4 warps).
+// 223 causal queries over up to 448 tokens, 16 rows of 16 heads, 33.4 us (74 TFLOP/s):
+// start-up and end of CTAs that have at most 14 tiles, and the tensor pipe at 22%.
 #include <climits>
 #include <type_traits>
 
@@ -55,7 +56,7 @@ constexpr int kTok = 32;              // tokens of a warp's tile
 constexpr int kRows = 16;             // query rows of a warp
 constexpr uint32_t kGaveUp = 1 << 16;  // more than a unit's parts
 constexpr int kMinChunk = 512;        // tokens below which a row is not split
-constexpr int kBalance = 2048;        // ... where parts are for balance only (512: 44 us, 1024: 39, none: 36 for
+constexpr int kBalance = 2048;        // ... where parts are for balance only (512: 43 us, 1024: 39, none: 36 for
                                       // 1024 units of up to 1500 tokens)
 // Value scales count as at least 2^-90 (values of at most 1e-25, which are off
 // by as much): a weight divided by its scale then still has 23 bits below the
@@ -161,7 +162,7 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
 //    make of the bytes themselves (250 instructions a tile and warp instead of 400).
 // E = 1: at most eight query rows, so that the lower half of a product's rows is
 // left out of the softmax (55 of 400 instructions a tile; 5 queries of 64 rows over
-// up to 1500 tokens: 40.2 -> 38.6 us).
+// up to 1500 tokens: 38.0 -> 36.2 us).
 enum class Mode { kTokens, kHeads, kQueries };
 
 template <typename T, int D, int E, Mode MODE>
@@ -531,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
       }
       sum[e] = fmaf(s0, fabsf(i0), fmaf(s1, fabsf(i1), sum[e]));
     }
-    // The next tile, in the shadow of this one's weights and products (223 queries
-    // over 1500 tokens 282 -> 275 us; before the weights 284).
+    // The next tile, in the shadow of this one's weights and products (223 queries over
+    // 1500 tokens 2.5% faster; before the weights 1% slower).
     if constexpr (SHARED) ok = convert(j + 1);
     // Values: this thread's bytes VB r8 .. + VB-1 of every fourth token.
 #pragma unroll
@@ -743,11 +744,11 @@ struct Cut {
 // and end and 1 for each tile of tokens that a warp goes over (a unit is about a
 // microsecond).  Rows are mostly of unequal length, which the modes with long walks
 // cannot even out: a tenth in favour of kTokens, and a fourth on the walks where all
-// CTAs run at once.  Measured, in us, kTokens / kQueries / kHeads: 320 rows x 16 heads
-// of 64, one query over up to 448 tokens 60 / - / 47, over 128 34 / - / 19; 157 rows x
-// 10 heads, 30 over 30 25 / 16 / 13; 64 rows x 16 heads, 20 over 1500 62 / 95 / 70, 96
-// over 448 85 / 74 / 60, 448 over 1500 615 / 450 / -; 8 rows x 8 heads, 448 over 448
-// 43 / 29 / -, 64 over 448 11 / 20 / -.
+// CTAs run at once.  Measured, in us, kTokens / kQueries / kHeads, heads of 64: rows of unequal
+// length, 320 x 16 heads, one query over up to 448 tokens 57 / - / 47, over 128 31 / - / 18; 64 x 16,
+// 20 over up to 1500, not causal 62 / 100 / 81; rows of one length, causal, 157 x 10, 30 over 30
+// 24 / 15 / 12; 64 x 16, 96 over 448 95 / 85 / 73; 8 x 8, 64 over 448 11 / 16 / 15, 448 over 448
+// 22 / 25 / 27 (here the estimate takes kQueries); not causal, 64 x 16, 448 over 1052 804 / 600 / 693.
 Cut cut(const lm_kv_cache *c, int32_t tokens, int32_t q_heads) {
   Cut k = {};
   const int qrows = tokens * (q_heads / c->heads);

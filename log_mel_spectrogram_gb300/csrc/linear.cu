@@ -18,26 +18,27 @@
 //  - a CTA per tile;
 //  - a pair of CTAs per tile of 256 lanes (cta_group::2): each fetches half of
 //    the rows of x and both use them, a third less traffic from L2, which is
-//    what bounds large problems (8192^3: 1.58 -> 1.79 PFLOP/s);
+//    what bounds large problems (8192^3, calls in a row: 1.48 -> 1.65 PFLOP/s);
 //  - a cluster of 2 to 8 CTAs per tile, each with a part of k, for the few tiles
 //    of a decoding step: the partial sums meet in distributed shared memory in
 //    rank order, in the same launch and with the same result on every call (5 x
-//    1024 x 1024: a CTA a tile 5.0 us, clusters of two 5.6, of eight 4.4).
+//    1024 x 1024 in a graph: a CTA a tile 4.8 us, clusters of two 4.6, of eight 4.0).
 //
 // The issuing warps stay converged up to one elected lane: addresses and
 // descriptors then live in uniform registers, which the tensor instructions
 // take.  Issued from one divergent thread, a product of 128 x 256 x 16 took 172
 // to 237 cycles, in competition with the epilogue; now 130.
 //
-// Measured, calls in a row: 24000 x 1024 -> 4096 bf16 with bias and gelu 113 to 118
-// us alone (1.71 to 1.78 PFLOP/s; 111 without gelu) and 135 us in a second-long loop, where
-// the power limit lowers the clock; bound by the tensor pipe, then the epilogue's
-// arithmetic.
-// 320 x 1024 -> 50001 36 us against 20 us of memory traffic: every SM fetches
-// and stores whole tiles in turn, and the last of 5.2 rounds is not full.
-// Windows of 8 x 3000 frames, 240 -> 512 with gelu, 13 us: four stages of k a
-// tile, so that the epilogue's arithmetic is most of it.  5 x 1024 -> 1024 4.5
-// us: a launch, one load's latency and the cluster's exchange.
+// Measured, calls in a row: 24000 x 1024 -> 4096 bf16 with bias and gelu 127 to 134
+// us (1.50 to 1.58 PFLOP/s; the tensor pipe is active 92% of the time, at the clock that the
+// power limit allows).
+// 320 x 1024 -> 50001 34 to 35 us against 20 us of memory traffic; no unit is near its
+// rate (tensor pipe 53%, L2 41%, DRAM half), and best_cut()'s model gives 23.  Off 16-byte
+// boundaries (k = 1023) 74 us, most of it the copy of W.
+// Windows of 8 x 3000 frames, 240 -> 512 with gelu, 13.3 us, without 10.9: four stages of
+// k a tile, each tile fetching its part of W anew.  24000 x 1024 -> 1024 with a residual 42 us,
+// without 37.  5 x 1024 -> 1024 4.6 to 5.9 us from the host, 4.0 in a graph: a launch, one load's
+// latency and the cluster's exchange.
 //
 // Operands that TMA cannot address (rows off 16-byte boundaries) are first
 // copied into padded rows in the workspace.
@@ -235,7 +236,7 @@ __device__ __forceinline__ Tile tile_at(const LinearParams &p, int t, int rank) 
 // Turns tile `t` into outputs.  `acc` is the tile's tensor memory; warp e of
 // the epilogue has lanes 32 * (e % 4) .. + 31 and every fourth 16 columns.
 // RES: `residual` has that of the first 16 columns; the next ones' travels while they
-// are worked on (2642 x 144 x 12143 66 -> 40 us, 24000 x 1024 x 1024 57 -> 40).
+// are worked on (2642 x 144 x 12143 66 -> 38 us, 24000 x 1024 x 1024 57 -> 42).
 template <typename T, int ACT, bool RES>
 __device__ __forceinline__ void epilogue(const LinearParams &p, const Tile &t, uint32_t acc, int e, T (&residual)[16]) {
   const int n = t.lane0 + 32 * (e % 4) + static_cast<int>(threadIdx.x % 32);

@@ -281,7 +281,8 @@ def beam_step(logits: torch.Tensor, scores: torch.Tensor, finished: torch.Tensor
     the lower token.  A finished beam (finished [clips, beams] bool; needs eos)
     offers eos alone, at its score.  A score of -inf marks a beam that is not
     in use (all but the first, in the first step).  history [clips, beams,
-    width] int32 follows its beams and gets the token at place `length`."""
+    width] int32 follows its beams and gets the token at place `length`, a number of
+    the host's: a captured call writes at that place on every replay."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return beam_step(logits, scores, finished, history, length, eos=eos)

@@ -568,7 +568,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D))
     if (!SHARED && fetched < mine) fetch(fetched++);
   }
   if (fetches && done < mine && lane == 0) {  // gave up: the copies in flight still have to land
-    for (int f = done; f < fetched; ++f) mbar_drain(&full[f % STAGES], (f / STAGES) & 1, p.wait_ns, p.err);
+    for (int f = done; f < fetched; ++f)
+      if (!mbar_drain(&full[f % STAGES], (f / STAGES) & 1, p.wait_ns, p.err)) break;
   }
   __syncwarp();
   if (SHARED) __syncthreads();  // the ring and the tiles are free

@@ -389,15 +389,15 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         }
       }
     }
-    // No copy outlives the CTA, whatever the other warps did.
-    if (!ok) {
-      if (!PAIR || rank == 0) {
-        for (int f = fills > p.stages ? fills - p.stages : 0; f < fills; ++f)
-          mbar_drain(&b.full[f % p.stages], (f / p.stages) & 1, p.wait_ns, p.err);
-      } else {  // counted on the other CTA's barriers: time enough for any copy
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 10000000ull) __nanosleep(1000);
-      }
+    // No copy outlives the CTA, whatever the other warps did: also where all of them are issued
+    // and the products give up.  (Of a pair, CTA 0's barriers count both CTAs' copies, and CTA 1
+    // stays until CTA 0 leaves.)
+    if (!PAIR || rank == 0) {
+      for (int f = fills > p.stages ? fills - p.stages : 0; f < fills; ++f)
+        if (!mbar_drain(&b.full[f % p.stages], (f / p.stages) & 1, p.wait_ns, p.err)) break;
+    } else if (!ok) {  // CTA 0 may not have come as far: time enough for any copy
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 10000000ull) __nanosleep(1000);
     }
   } else if (warp == 1) {
     if (!PAIR || rank == 0) {

@@ -44,9 +44,10 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, u
   return __all_sync(0xffffffffu, ok);
 }
 
-// Waits for copies that are in flight, whatever the other warps did (no abort flag).
-__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity, uint64_t limit_ns, uint32_t *err_word) {
-  mbar_wait_limited(smem_u32(bar), parity, limit_ns, nullptr, err_word);
+// Waits for copies that are in flight, whatever the other warps did (no abort flag).  Returns
+// false where the limit ran out: other copies of the thread's have had as long by then.
+__device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity, uint64_t limit_ns, uint32_t *err_word) {
+  return mbar_wait_limited(smem_u32(bar), parity, limit_ns, nullptr, err_word);
 }
 
 // Host side of a translation unit's sticky word: reads the current device's into *value (bits are

@@ -76,6 +76,20 @@ def test_attention_reports(lm, rows, heads, tokens, t):
     assert torch.equal(c.attend(0, q), want) and lm.decode_error() == 0
 
 
+def test_a_wait_that_runs_out_is_waited_for_once(lm):
+    """A CTA that gives up waits for all of its copies in flight, together no longer than one limit."""
+    x, w = (torch.ones(s, device="cuda").half() for s in ((5, 8192), (256, 8192)))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    linear(x, w, ws)
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    linear(x, w, ws, withheld=0, wait_ns=100_000_000)
+    b.record()
+    torch.cuda.synchronize()
+    assert lm.decode_error() & MBAR_TIMEOUT_BIT
+    assert 100 <= a.elapsed_time(b) < 350  # the wait, the copies' and its neighbours'
+
+
 def test_refusals(lm):
     v = ctypes.c_uint32()
     assert waits.lib().lm_decode_error(None, 0, None) == 1

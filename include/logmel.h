@@ -690,6 +690,209 @@ lm_status lm_beam_step(const lm_beam_args *args, void *workspace, size_t workspa
 lm_status lm_kv_reorder(const lm_kv_cache *cache, const int32_t *parents, int32_t beams, void *workspace,
                         size_t workspace_bytes, lm_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* 7. layer norm (the source pages have no counterpart)                     */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * y = (x - mean) / sqrt(var + eps) * weight + bias over the last dimension of
+ * x [rows][width], with mean and var (the mean square of x - mean) of each row.
+ *
+ *   x        device, rows x_row_stride elements apart (>= 0: rows may overlap),
+ *            of dtype LM_F32, LM_F16 or LM_BF16.                (read-only)
+ *   weight, bias  device, [width], of weight_dtype and bias_dtype: LM_F32 or
+ *            dtype; NULL: 1 and 0.                               (read-only)
+ *   out      device, [rows][width] of dtype, rows out_row_stride elements
+ *            apart; may be x itself (same stride), and meets no other input.
+ *   stats    device, [3][rows] f32, or NULL: for lm_layer_norm_backward, the
+ *            mean, what its rounding to f32 left off, and 1 / sqrt(var + eps).
+ *   eps      >= 0
+ * Sums are held in 32 bits, the deviations' taken about the rounded mean and put
+ * right by theirs; y is rounded once.  A NaN or infinity in a row makes the row NaN.
+ *
+ * Errors: LM_ERR_INVALID_ARG, LM_ERR_UNSUPPORTED (dtypes, sizes of 2^31 and
+ * more), LM_ERR_MISALIGNED (pointers are aligned to their element), LM_ERR_CUDA.
+ * rows * width == 0 enqueues nothing.
+ */
+typedef struct lm_norm_args {
+  const void *x;
+  const void *weight;
+  const void *bias;
+  void *out;
+  float *stats;
+  int64_t rows, width, x_row_stride, out_row_stride;
+  int32_t dtype, weight_dtype, bias_dtype;
+  float eps;
+} lm_norm_args;
+
+lm_status lm_layer_norm(const lm_norm_args *args, lm_stream_t stream);
+
+/*
+ * The gradients of lm_layer_norm.  With n = (x - mean) / sqrt(var + eps) and
+ * h = grad * weight, row by row:
+ *   dx = (h - avg(h) - n * avg(h * n)) / sqrt(var + eps)
+ *   dweight = sum over rows of grad * n,   dbias = sum over rows of grad
+ *
+ *   x, weight, stats  as for (and from) lm_layer_norm
+ *   grad     device, [rows][width] of dtype, rows grad_row_stride apart
+ *   dx       device, [rows][width] of dtype, contiguous, or NULL: not wanted
+ *   dweight  device, [width] of weight_dtype, or NULL
+ *   dbias    device, [width] of bias_dtype, or NULL
+ *   workspace  device, >= lm_layer_norm_backward_workspace_size(...), 16-byte
+ *            aligned; its contents on entry do not matter.
+ * Sums over rows are taken in 32 bits, in an order that depends on the sizes
+ * alone, and rounded once.  Outputs meet no input and not one another.
+ * Errors as lm_layer_norm, and LM_ERR_WORKSPACE.  rows == 0 sets dweight and
+ * dbias to zero.
+ */
+typedef struct lm_norm_backward_args {
+  const void *x;
+  const void *weight;
+  const float *stats;
+  const void *grad;
+  void *dx;
+  void *dweight;
+  void *dbias;
+  int64_t rows, width, x_row_stride, grad_row_stride;
+  int32_t dtype, weight_dtype, bias_dtype, reserved;
+} lm_norm_backward_args;
+
+lm_status lm_layer_norm_backward_workspace_size(const lm_norm_backward_args *args, size_t *bytes);
+lm_status lm_layer_norm_backward(const lm_norm_backward_args *args, void *workspace, size_t workspace_bytes,
+                                 lm_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 8. gated linear layers (the source pages have no counterpart)            */
+/* ------------------------------------------------------------------------ */
+
+#define LM_ACT_SIGMOID 5 /* 1 / (1 + exp(-z)); lm_gated_linear only */
+
+/*
+ * y = act(x Wg^T + bg) * (x Wu^T + bu): the first half of a gated feed-forward
+ * block, both products, the activation and the product in one kernel.
+ *
+ *   x        device, [rows][k] of dtype (LM_F16, LM_BF16), rows x_row_stride
+ *            elements apart (>= 0: rows may overlap), k contiguous. (read-only)
+ *   w_gate, w_up  device, [n][k] of dtype, rows gate_row_stride and
+ *            up_row_stride elements apart.                      (read-only)
+ *   b_gate, b_up  device, [n] of bias_dtype (LM_F32 or dtype), or NULL each.
+ *   out      device, [rows][n] of dtype, rows out_row_stride elements apart;
+ *            meets no input.
+ *   activation  one of lm_activation, or LM_ACT_SIGMOID
+ * Products are summed in 32 bits, the rest is computed in 32 bits and rounded
+ * once.  Operands whose rows do not all start on 16 bytes are copied into the
+ * workspace first.
+ *   workspace  device, >= lm_gated_linear_workspace_size(args), 16-byte aligned;
+ *            its contents on entry do not matter but for the first u32, the
+ *            device error word (lm_workspace_error), to which bits are added.
+ *
+ * Errors: LM_ERR_INVALID_ARG, LM_ERR_UNSUPPORTED (dtypes, sizes),
+ * LM_ERR_MISALIGNED, LM_ERR_WORKSPACE, LM_ERR_CUDA.  rows * n == 0 enqueues
+ * nothing.
+ */
+typedef struct lm_gated_args {
+  const void *x;
+  const void *w_gate;
+  const void *w_up;
+  const void *b_gate;
+  const void *b_up;
+  void *out;
+  int64_t rows, k, n, x_row_stride, gate_row_stride, up_row_stride, out_row_stride;
+  int32_t dtype, bias_dtype, activation, reserved;
+} lm_gated_args;
+
+lm_status lm_gated_linear_workspace_size(const lm_gated_args *args, size_t *bytes);
+lm_status lm_gated_linear(const lm_gated_args *args, void *workspace, size_t workspace_bytes, lm_stream_t stream);
+
+/*
+ * The gradients of lm_gated_linear.  With a = x Wg^T + bg and b = x Wu^T + bu,
+ * computed anew (nothing is kept from the forward pass but its inputs):
+ *   da = grad * b * act'(a),   db = grad * act(a)
+ *   dx = da Wg + db Wu,  dWg = da^T x,  dWu = db^T x,
+ *   dbg, dbu = sums of da, db over rows
+ * da and db are computed and, for the biases, summed in 32 bits, and rounded to dtype as operands of
+ * the products.  relu's derivative at 0 is 0.
+ *
+ *   forward  the inputs and sizes of lm_gated_linear (out and out_row_stride
+ *            are not used)
+ *   grad     device, [rows][n] of dtype, rows grad_row_stride elements apart
+ *   dx [rows][k], dw_gate, dw_up [n][k] of dtype, db_gate, db_up [n] of
+ *            bias_dtype: device, contiguous, each NULL where not wanted; they
+ *            meet no input and not one another.
+ *   workspace  as for lm_gated_linear, >= lm_gated_linear_backward_workspace_size(...)
+ * Errors as lm_gated_linear.
+ */
+typedef struct lm_gated_backward_args {
+  lm_gated_args forward;
+  const void *grad;
+  void *dx;
+  void *dw_gate;
+  void *dw_up;
+  void *db_gate;
+  void *db_up;
+  int64_t grad_row_stride;
+} lm_gated_backward_args;
+
+lm_status lm_gated_linear_backward_workspace_size(const lm_gated_backward_args *args, size_t *bytes);
+lm_status lm_gated_linear_backward(const lm_gated_backward_args *args, void *workspace, size_t workspace_bytes,
+                                   lm_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 9. weights in 4 bits (the source pages have no counterpart)              */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A weight [n][k] as whole numbers of -8 .. 7 and one f32 scale for each row
+ * and `group` consecutive k:  w[i][j] = q[i][j] * s[i][j / group].
+ *   packed   device, ceil(n / 16) * ceil(k / 64) tiles of 512 bytes, 16-byte
+ *            aligned; a tile is 16 rows by 64 k, tiles run along k first.
+ *            Bytes 16 l .. 16 l + 15 of a tile hold rows l / 4 and l / 4 + 8
+ *            at k = 16 (l % 4) .. + 15, as two little-endian u32 a row, each of
+ *            eight k in order 0 2 4 6 1 3 5 7 from its lowest nibble; a nibble
+ *            is q + 8.  Places past n or k hold q = 0.
+ *   scale    device, [ceil(n / 16)][ceil(k / group)][16] f32, 16-byte aligned
+ *   group    32, 64 or 128
+ */
+typedef struct lm_weight4 {
+  const void *packed;
+  const float *scale;
+  int64_t n, k;
+  int32_t group, reserved;
+} lm_weight4;
+
+/* Bytes of `packed` and `scale` for a weight of n, k and group. */
+lm_status lm_weight4_size(const lm_weight4 *w, size_t *packed_bytes, size_t *scale_bytes);
+
+/* Lays out q (device, int8 [n][k], contiguous, values clamped to -8 .. 7) and
+ * scales (device, f32 [n][ceil(k / group)], contiguous) in w->packed and w->scale. */
+lm_status lm_weight4_pack(const lm_weight4 *w, const int8_t *q, const float *scales, lm_stream_t stream);
+
+/* Rounds weight (device, [n][k] of dtype LM_F32, LM_F16 or LM_BF16, rows
+ * row_stride elements apart): s = max |w| of the group / 7 (1 where that is 0),
+ * q = rint(w / s), ties to even.  A group with a NaN or infinity gets a scale of NaN or
+ * infinity. */
+lm_status lm_weight4_quantize(const lm_weight4 *w, const void *weight, int64_t row_stride, int32_t dtype,
+                              lm_stream_t stream);
+
+/* The values q * s, rounded to dtype (LM_F32, LM_F16, LM_BF16): out [n][k],
+ * rows row_stride elements apart. */
+lm_status lm_weight4_values(const lm_weight4 *w, void *out, int64_t row_stride, int32_t dtype, lm_stream_t stream);
+
+/*
+ * lm_linear with such a weight: args as there, but for weight and
+ * weight_row_stride, which are not used; args->n and args->k are the weight's.
+ * A group's products q * x are summed in 32 bits, the sums multiplied by its
+ * scale.  For many rows (lm_linear4_expands) the values are rounded to dtype
+ * and expanded into the workspace, and lm_linear's products take them.
+ *   workspace  as for lm_linear, >= lm_linear4_workspace_size(...)
+ * Errors as lm_linear.
+ */
+lm_status lm_linear4_workspace_size(const lm_linear_args *args, const lm_weight4 *w, size_t *bytes);
+lm_status lm_linear4(const lm_linear_args *args, const lm_weight4 *w, void *workspace, size_t workspace_bytes,
+                     lm_stream_t stream);
+/* 1 where a call with these sizes expands the weight, 0 where it reads the 4 bits in its products. */
+int lm_linear4_expands(int64_t rows, int64_t n, int64_t k);
+
 #ifdef __cplusplus
 }
 #endif

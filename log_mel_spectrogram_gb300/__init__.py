@@ -13,6 +13,8 @@ missing or the tensors are not on a CUDA device.
 * ``linear``, ``KvCache`` and ``beam_step`` (decode.py) -- what turns the
   features into text: linear layers, attention over an 8-bit key/value cache,
   beam search.
+* ``layer_norm``, ``gated_linear`` (with gradients) and ``Weight4`` (linear layers'
+  weights in 4 bits, decode.py) -- the rest of such a model's layers.
 """
 from __future__ import annotations
 
@@ -25,13 +27,14 @@ import torch
 
 from . import _native
 from ._native import LogmelError
-from .decode import BeamStep, KvCache, beam_step, decode_error, linear
+from .decode import (BeamStep, KvCache, Weight4, beam_step, decode_error, gated_linear, layer_norm, linear,
+                     quantize_weight)
 
 __all__ = ["log_mel_from_stft", "log_mel_from_stft_workspace_size", "workspace_error", "LogmelError",
            "pack_mel_filters", "log_mel_from_stft_host", "log_mel_from_stft_host_workspace_size",
            "describe_log_mel_from_stft", "MelSpectrogram", "mel_spectrogram", "library_path",
            "log_mel_from_stft_op", "mel_spectrogram_op", "linear", "KvCache", "beam_step", "BeamStep",
-           "decode_error"]
+           "decode_error", "layer_norm", "gated_linear", "Weight4", "quantize_weight"]
 
 
 def library_path():

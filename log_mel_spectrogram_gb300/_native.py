@@ -132,6 +132,34 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.lm_debug_kv_attend_withhold.restype = ctypes.c_int
     L.lm_kv_reorder.argtypes = [vp, vp, i32, vp, sz, vp]
     L.lm_kv_reorder.restype = ctypes.c_int
+    L.lm_layer_norm.argtypes = [vp, vp]
+    L.lm_layer_norm.restype = ctypes.c_int
+    L.lm_layer_norm_backward_workspace_size.argtypes = [vp, vp]
+    L.lm_layer_norm_backward_workspace_size.restype = ctypes.c_int
+    L.lm_layer_norm_backward.argtypes = [vp, vp, sz, vp]
+    L.lm_layer_norm_backward.restype = ctypes.c_int
+    L.lm_gated_linear_workspace_size.argtypes = [vp, vp]
+    L.lm_gated_linear_workspace_size.restype = ctypes.c_int
+    L.lm_gated_linear.argtypes = [vp, vp, sz, vp]
+    L.lm_gated_linear.restype = ctypes.c_int
+    L.lm_gated_linear_backward_workspace_size.argtypes = [vp, vp]
+    L.lm_gated_linear_backward_workspace_size.restype = ctypes.c_int
+    L.lm_gated_linear_backward.argtypes = [vp, vp, sz, vp]
+    L.lm_gated_linear_backward.restype = ctypes.c_int
+    L.lm_weight4_size.argtypes = [vp, vp, vp]
+    L.lm_weight4_size.restype = ctypes.c_int
+    L.lm_weight4_pack.argtypes = [vp, vp, vp, vp]
+    L.lm_weight4_pack.restype = ctypes.c_int
+    L.lm_weight4_quantize.argtypes = [vp, vp, i64, i32, vp]
+    L.lm_weight4_quantize.restype = ctypes.c_int
+    L.lm_weight4_values.argtypes = [vp, vp, i64, i32, vp]
+    L.lm_weight4_values.restype = ctypes.c_int
+    L.lm_linear4_workspace_size.argtypes = [vp, vp, vp]
+    L.lm_linear4_workspace_size.restype = ctypes.c_int
+    L.lm_linear4.argtypes = [vp, vp, vp, sz, vp]
+    L.lm_linear4.restype = ctypes.c_int
+    L.lm_linear4_expands.argtypes = [i64, i64, i64]
+    L.lm_linear4_expands.restype = ctypes.c_int
     L.lm_beam_step_workspace_size.argtypes = [vp, vp]
     L.lm_beam_step_workspace_size.restype = ctypes.c_int
     L.lm_beam_step.argtypes = [vp, vp, sz, vp]

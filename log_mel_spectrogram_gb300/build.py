@@ -4,7 +4,7 @@ Each ``csrc/*.cu`` file is compiled by nvcc for sm_103a in parallel, then
 linked into ``log_mel_spectrogram_gb300/_build/liblogmel.so``.  The build is
 skipped when the library is newer than every source and header.
 
-The torch binding of the decoding operations, ``csrc/binding.cpp``, becomes the
+The torch binding of the decoding operations and layers, ``csrc/*.cpp``, becomes the
 Python module ``_build/_decode.so`` beside it (g++, torch's headers), linked
 against liblogmel.so.
 
@@ -62,28 +62,28 @@ def _torch_dir() -> pathlib.Path:
     return pathlib.Path(torch.__file__).resolve().parent
 
 
-def _compile_binding(verbose: bool) -> pathlib.Path:
-    """binding.cpp against torch's headers."""
+def _compile_binding(src: pathlib.Path, verbose: bool) -> pathlib.Path:
+    """A source of the binding against torch's headers."""
     inc = _torch_dir() / "include"
     cuda = pathlib.Path(_nvcc()).resolve().parents[1] / "include"
-    obj = OUT_DIR / "binding.o"
+    obj = OUT_DIR / (src.stem + ".binding.o")
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", f"-I{INCLUDE}",
            f"-I{sysconfig.get_path('include')}", "-isystem", str(inc), "-isystem",
-           str(inc / "torch" / "csrc" / "api" / "include"), "-isystem", str(cuda), "-c", str(CSRC / "binding.cpp"),
+           str(inc / "torch" / "csrc" / "api" / "include"), "-isystem", str(cuda), "-c", str(src),
            "-o", str(obj)]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on {src.name}:\n{r.stdout}\n{r.stderr}")
     return obj
 
 
-def _link_binding(obj: pathlib.Path) -> None:
+def _link_binding(objs: list[pathlib.Path]) -> None:
     lib = _torch_dir() / "lib"
     cuda = pathlib.Path(_nvcc()).resolve().parents[1] / "lib64"
     tmp = OUT_DIR / f"_decode.{os.getpid()}.so"
-    cmd = ["g++", "-shared", "-o", str(tmp), str(obj), f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+    cmd = ["g++", "-shared", "-o", str(tmp), *map(str, objs), f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
            "-lc10", f"-L{OUT_DIR}", "-l:liblogmel.so", f"-L{cuda}", "-lcudart", f"-Wl,-rpath,{lib}",
            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{cuda}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -117,8 +117,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             print(r.stderr, flush=True)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources()) + 1) as ex:
-        binding = None if checked else ex.submit(_compile_binding, verbose)
+    bindings = [] if checked else sorted(CSRC.glob("*.cpp"))
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources()) + len(bindings)) as ex:
+        binding = [ex.submit(_compile_binding, src, verbose) for src in bindings]
         objs = list(ex.map(compile_one, sources()))
     tmp = out_dir / f"{lib.stem}.{os.getpid()}.so"
     # (No soname: a program that links the library by its path then finds it there.)
@@ -127,8 +128,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
-    if binding is not None:
-        _link_binding(binding.result())
+    if binding:
+        _link_binding([b.result() for b in binding])
     return lib
 
 

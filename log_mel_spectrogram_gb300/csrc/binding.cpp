@@ -1,86 +1,22 @@
 // binding.cpp -- the torch side of linear, the key/value cache and the beam
-// step: checks of arguments, outputs and workspaces, and the C call, without
+// step (layers.cpp has that of the norm, the gated layer and weights in 4 bits): checks of arguments, outputs and workspaces, and the C call, without
 // the interpreter in between (a decoding step makes dozens of these calls, and
 // each takes a few microseconds on the GPU).
 //
 // The C ABI (include/logmel.h) does the work.  A status other than LM_OK is
 // returned as an int, for the Python module to raise.
-#include <Python.h>
+#include "binding.h"
 
-#include <cstring>
 #include <map>
 #include <mutex>
-#include <stdexcept>
-#include <string>
 #include <tuple>
-#include <vector>
 
-#include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/zeros.h>
-#include <c10/core/GradMode.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-#include <cuda_runtime.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include "logmel.h"
+namespace lm_binding {
 
 namespace {
-
-using at::Tensor;
-
-struct GradError {};
-
-// Another operation's refusal, as the ValueError that it becomes.
-[[noreturn]] void refuse(const std::string &what) { throw std::invalid_argument(what); }
-
-const Tensor *tensor_or_null(PyObject *o, const char *name) {
-  if (o == Py_None) return nullptr;
-  if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a CUDA tensor");
-  return &THPVariable_Unpack(o);
-}
-
-const Tensor &tensor(PyObject *o, const char *name) {
-  const Tensor *t = tensor_or_null(o, name);
-  if (!t || !t->is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
-  return *t;
-}
-
-// An optional or required tensor on device `dev`.
-const Tensor *on(PyObject *o, const char *name, int dev) {
-  const Tensor *t = tensor_or_null(o, name);
-  if (!t) return nullptr;
-  if (!t->is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
-  if (t->get_device() != dev) refuse(std::string(name) + " must be on the same device as the other inputs");
-  return t;
-}
-
-// Neither direction of differentiation passes through these operations.  (Tangents exist under
-// no_grad, too.)
-void no_grad(std::initializer_list<const Tensor *> ts) {
-  const bool backward = c10::GradMode::is_enabled();
-  for (const Tensor *t : ts)
-    if (t && ((backward && t->requires_grad()) || t->_fw_grad(0).defined())) throw GradError{};
-}
-
-// What a user's tensor holds has changed: a graph that saved it finds out.
-void written(const Tensor *t) {
-  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
-}
-
-int half_code(at::ScalarType t) { return t == at::kHalf ? LM_F16 : t == at::kBFloat16 ? LM_BF16 : -1; }
-int float_code(at::ScalarType t) { return t == at::kFloat ? LM_F32 : half_code(t); }
-at::ScalarType type_of(int code) { return code == LM_F32 ? at::kFloat : code == LM_F16 ? at::kHalf : at::kBFloat16; }
-
-Tensor make(at::IntArrayRef shape, at::ScalarType type, int dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, dev)));
-}
-
-enum Op { kLinear, kAttend, kBeam, kReorder };
-
 constexpr int64_t kLeastBytes = 1 << 16;  // of a workspace that is kept
 constexpr size_t kMostKept = 128;         // workspaces; past that the one whose last use is longest ago goes
+}  // namespace
 
 // A zeroed workspace.  An operation's kernels leave its counters at zero, so
 // one per operation, device and stream serves every call on it; a call that a
@@ -130,27 +66,10 @@ Tensor workspace(Op op, int dev, cudaStream_t stream, size_t bytes) {
   return t;
 }
 
-PyObject *status(int rc) { return PyLong_FromLong(rc); }
+namespace {
 
-// The stride of a tensor's rows when its leading dimensions are one.
-int64_t row_stride(const Tensor &t, const char *name) {
-  const auto sz = t.sizes(), st = t.strides();
-  const int64_t d = t.dim();
-  if (d == 1 || t.numel() == 0) return sz[d - 1];
-  int64_t row = st[d - 2], n = sz[d - 2];
-  for (int64_t i = d - 3; i >= 0; --i) {
-    if (sz[i] == 1) continue;
-    if (n == 1) {
-      row = st[i];
-    } else if (st[i] != row * n) {
-      refuse(std::string(name) + "'s leading dimensions must be evenly spaced rows");
-    }
-    n *= sz[i];
-  }
-  return row;
-}
-
-// linear(x, weight, bias, activation, residual, scale, out, out_dtype or -1)
+// linear(x, weight, bias, activation, residual, scale, out, out_dtype or -1); weight is a tensor, or the
+// tuple of one in 4 bits
 PyObject *linear(PyObject *const *a) {
   const Tensor &x = tensor(a[0], "x");
   if (x.dim() < 1) refuse("x must be a CUDA tensor [..., K]");
@@ -158,20 +77,28 @@ PyObject *linear(PyObject *const *a) {
   const c10::cuda::OptionalCUDAGuard guard(x.device());
   const int code = half_code(x.scalar_type());
   if (code < 0) refuse("x must be float16 or bfloat16");
-  const Tensor *w = on(a[1], "weight", dev), *bias = on(a[2], "bias", dev), *res = on(a[4], "residual", dev),
-               *given = on(a[6], "out", dev);
-  if (!w) refuse("weight must be a CUDA tensor");
+  const bool four = PyTuple_Check(a[1]);
+  const Tensor *w = four ? nullptr : on(a[1], "weight", dev), *bias = on(a[2], "bias", dev),
+               *res = on(a[4], "residual", dev), *given = on(a[6], "out", dev);
+  Weight4 w4;
+  if (four) {
+    w4 = weight4_of(a[1]);
+    if (w4.dev != dev) refuse("weight must be on the same device as the other inputs");
+  } else if (!w) {
+    refuse("weight must be a CUDA tensor");
+  }
   no_grad({&x, w, bias, res, given});
   const int64_t dims = x.dim(), k = x.size(-1);
-  if (w->scalar_type() != x.scalar_type() || w->dim() != 2 || w->size(1) != k)
+  if (four ? w4.code != code || w4.c.k != k
+           : w->scalar_type() != x.scalar_type() || w->dim() != 2 || w->size(1) != k)
     refuse("weight must be [N, K] of x's dtype and last dimension");
-  const int64_t n = w->size(0);
-  if (k > 1 && (x.stride(-1) != 1 || w->stride(1) != 1))
+  const int64_t n = four ? w4.c.n : w->size(0);
+  if (k > 1 && (x.stride(-1) != 1 || (!four && w->stride(1) != 1)))
     refuse("the last dimension of x and weight must be contiguous");
   lm_linear_args p = {};
   p.k = k;
   p.n = n;
-  p.weight_row_stride = w->stride(0);
+  p.weight_row_stride = four ? 0 : w->stride(0);
   p.dtype = code;
   p.activation = static_cast<int32_t>(PyLong_AsLong(a[3]));
   p.scale = static_cast<float>(PyFloat_AsDouble(a[5]));
@@ -233,14 +160,15 @@ PyObject *linear(PyObject *const *a) {
     p.residual_row_stride = row_stride(*res, "residual");
   }
   p.x = x.data_ptr();
-  p.weight = w->data_ptr();
+  p.weight = four ? nullptr : w->data_ptr();
   p.out = out.data_ptr();
   size_t need = 0;
-  int rc = lm_linear_workspace_size(&p, &need);
+  int rc = four ? lm_linear4_workspace_size(&p, &w4.c, &need) : lm_linear_workspace_size(&p, &need);
   if (rc == LM_OK) {
     const cudaStream_t s = c10::cuda::getCurrentCUDAStream(dev).stream();
     const Tensor ws = workspace(kLinear, dev, s, need);
-    rc = lm_linear(&p, ws.data_ptr(), static_cast<size_t>(ws.numel()), reinterpret_cast<lm_stream_t>(s));
+    rc = four ? lm_linear4(&p, &w4.c, ws.data_ptr(), static_cast<size_t>(ws.numel()), reinterpret_cast<lm_stream_t>(s))
+              : lm_linear(&p, ws.data_ptr(), static_cast<size_t>(ws.numel()), reinterpret_cast<lm_stream_t>(s));
   }
   if (rc != LM_OK) return status(rc);
   written(given);
@@ -475,34 +403,6 @@ PyObject *beam_step(PyObject *const *a) {
                        THPVariable_Wrap(ended), last);
 }
 
-// No C++ exception leaves the module.
-template <PyObject *(*F)(PyObject *const *), int ARGS>
-PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  if (n != ARGS) {
-    PyErr_Format(PyExc_TypeError, "%d arguments expected, got %zd", ARGS, n);
-    return nullptr;
-  }
-  try {
-    return F(args);
-  } catch (const std::invalid_argument &e) {
-    PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (const GradError &) {
-    PyErr_SetString(PyExc_RuntimeError,
-                    "log_mel_spectrogram_gb300 ops are inference-only: tensors must not require grad (use "
-                    "torch.no_grad() or detach()) or carry a tangent");
-  } catch (const std::exception &e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
-  } catch (...) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
-  }
-  return nullptr;
-}
-
-template <PyObject *(*F)(PyObject *const *), int ARGS>
-PyCFunction fast() {
-  return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, ARGS>));
-}
-
 PyMethodDef kMethods[] = {
     {"linear", fast<linear, 8>(), METH_FASTCALL, nullptr},
     {"kv_append", fast<kv_append, 8>(), METH_FASTCALL, nullptr},
@@ -517,5 +417,13 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_decode", "linear, the key/value 
                        nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
+}  // namespace lm_binding
 
-PyMODINIT_FUNC PyInit__decode(void) { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__decode(void) {
+  PyObject *const m = PyModule_Create(&lm_binding::kModule);
+  if (m && PyModule_AddFunctions(m, lm_binding::kLayerMethods) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -91,6 +91,9 @@ uint64_t call_token(cudaStream_t stream);
 
 // --- decoding operations ---------------------------------------------------
 
+// Argument rules of lm_linear that need no pointers.
+lm_status linear_check(const lm_linear_args *args);
+
 // What the kernels of linear.cu and kv_attend.cu have reported on the current device since it was last
 // cleared, added to *value.
 lm_status linear_error(uint32_t *value, bool clear, cudaStream_t stream);

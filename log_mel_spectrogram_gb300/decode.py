@@ -2,14 +2,17 @@
 its attention, and beam search, over the same C ABI (include/logmel.h).
 
 * ``linear(x, weight, bias, ...)`` -- act(x W^T + bias), scaled, plus residual;
-  x may be overlapping windows of feature frames, read in place.
+  x may be overlapping windows of feature frames, read in place.  The weight may be
+  a ``Weight4``, in 4 bits (``quantize_weight``).
+* ``layer_norm(x, weight, bias)`` and ``gated_linear(x, w_gate, w_up, ...)``, the
+  norm and the gated block of a layer; these two have gradients.
 * ``KvCache`` -- keys and values of a model's rows in 8 bits, one scale per
   block of tokens and head: ``append``, ``attend``, ``advance``, ``read``,
   ``reorder`` and ``reset``.
 * ``beam_step(logits, scores, ...)`` -- the best continuations of every clip.
 * ``decode_error()`` -- whether a wait inside a kernel of these has run out.
 
-Inference only, CUDA only, on torch's current stream unless `stream` is given.
+Inference only but for layer_norm and gated_linear, CUDA only, on torch's current stream unless `stream` is given.
 """
 from __future__ import annotations
 
@@ -23,11 +26,12 @@ import torch
 from . import _native
 from . import build as _build
 
-__all__ = ["linear", "KvCache", "beam_step", "BeamStep", "decode_error"]
+__all__ = ["linear", "Weight4", "quantize_weight", "layer_norm", "gated_linear", "KvCache", "beam_step", "BeamStep", "decode_error"]
 
 _HALF = {torch.float16: _native.DTYPES["f16"], torch.bfloat16: _native.DTYPES["bf16"]}
 _FLOAT = {torch.float32: _native.DTYPES["f32"], **_HALF}
 _ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+_GATES = {**_ACTIVATIONS, "sigmoid": 5}
 
 _DTYPE_CODES = {None: -1, **_FLOAT}
 _ext = None
@@ -73,7 +77,7 @@ def decode_error(device=None, *, clear: bool = True) -> int:
 # linear
 # ---------------------------------------------------------------------------
 
-def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, *,
+def linear(x: torch.Tensor, weight: torch.Tensor | Weight4, bias: torch.Tensor | None = None, *,
            activation: str | None = None, residual: torch.Tensor | None = None, scale: float = 1.0,
            out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
     """residual + scale * act(x @ weight.T + bias), rounded once.
@@ -85,7 +89,10 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     [N, taps * M] weight).  bias [N] float32 or x's dtype; residual [..., N] of
     x's dtype.  activation: None, "relu", "gelu" (erf), "gelu_tanh" or "silu".
     out_dtype: x's dtype (default) or float32; out may be residual itself, and
-    overlaps no other input."""
+    overlaps no other input.
+
+    A Weight4 as weight is read in its 4 bits where x has few rows; for
+    many its values are rounded to x's dtype first, in each call."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear(x, weight, bias, activation=activation, residual=residual, scale=scale, out=out,
@@ -95,7 +102,117 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
         raise ValueError(f"activation must be one of {[a for a in _ACTIVATIONS if a]} or None")
     if code is None:
         raise ValueError("out_dtype must be x's dtype or float32")
+    if type(weight) is Weight4:
+        return _checked((_ext or _binding()).linear(x, weight._head(), bias, act, residual, scale, out, code),
+                        "lm_linear4")
     return _checked((_ext or _binding()).linear(x, weight, bias, act, residual, scale, out, code), "lm_linear")
+
+
+class Weight4:
+    """A linear layer's weight [N, K] as whole numbers of -8 .. 7, with one float32 scale for each row and
+    `group` consecutive k: value = q * scale.  ``quantize_weight`` rounds a weight to one, ``Weight4.pack`` takes
+    numbers and scales that are at hand; ``linear`` takes it as its weight, for x of `dtype`.
+
+    The tensors packed [ceil(N / 16), ceil(K / 64), 512] uint8 and scale [ceil(N / 16), ceil(K / group), 16]
+    float32 hold it in the order of include/logmel.h (lm_weight4)."""
+
+    def __init__(self, packed: torch.Tensor, scale: torch.Tensor, shape, group: int, dtype: torch.dtype):
+        self.packed, self.scale, self.shape, self.group, self.dtype = packed, scale, tuple(shape), group, dtype
+
+    device = property(lambda self: self.packed.device)
+
+    def _head(self):
+        return (self.packed, self.scale, self.shape[0], self.shape[1], self.group, _HALF[self.dtype])
+
+    @staticmethod
+    def _check(group, dtype):
+        if dtype not in _HALF:
+            raise ValueError("dtype must be torch.float16 or torch.bfloat16")
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+
+    @staticmethod
+    def pack(q: torch.Tensor, scale: torch.Tensor, *, group: int | None = None, dtype: torch.dtype = torch.bfloat16,
+             stream=None) -> Weight4:
+        """Lays out q [N, K] int8 (clamped to -8 .. 7) and scale [N, ceil(K / group)] float32.  group
+        is the one of 32, 64 and 128 that fits scale's shape (any of those that do, where a row has one scale)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return Weight4.pack(q, scale, group=group, dtype=dtype)
+        if group is None:
+            fits = [g for g in (32, 64, 128) if q.dim() == 2 == scale.dim() and -(-q.shape[1] // g) == scale.shape[1]]
+            if not fits:
+                raise ValueError("scale must be [N, ceil(K / group)] with a group of 32, 64 or 128")
+            group = fits[-1]
+        Weight4._check(group, dtype)
+        return Weight4(*_checked(_binding().weight4_pack(q, scale, group), "lm_weight4_pack"), q.shape, group, dtype)
+
+    def values(self, dtype: torch.dtype | None = None, *, stream=None) -> torch.Tensor:
+        """The weight [N, K] that it stands for, rounded to dtype (its own; float32 is exact to one rounding)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.values(dtype)
+        code = _FLOAT.get(dtype or self.dtype)
+        if code is None:
+            raise ValueError("dtype must be float32, float16 or bfloat16")
+        return _checked(_binding().weight4_values(self._head(), code), "lm_weight4_values")
+
+
+def quantize_weight(weight: torch.Tensor, group: int = 64, *, dtype: torch.dtype | None = None, stream=None) -> Weight4:
+    """Rounds weight [N, K] (float32, float16 or bfloat16) to 4 bits: scale = max |w| of a row's group / 7, q =
+    w / scale to the nearest whole number (ties to even).  dtype: of the x that linear will take (weight's own,
+    bfloat16 for float32)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_weight(weight, group, dtype=dtype)
+    if dtype is None:
+        dtype = torch.bfloat16 if weight.dtype == torch.float32 else weight.dtype
+    Weight4._check(group, dtype)
+    return Weight4(*_checked(_binding().weight4_quantize(weight, group), "lm_weight4_quantize"), weight.shape, group,
+                   dtype)
+
+
+# ---------------------------------------------------------------------------
+# the rest of a layer
+# ---------------------------------------------------------------------------
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
+               eps: float = 1e-5, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """(x - mean) / sqrt(var + eps) * weight + bias over the last dimension, rounded once.
+
+    x [..., width] float32, float16 or bfloat16, the last dimension contiguous and
+    the others evenly spaced rows; weight and bias [width] float32 or x's dtype.
+    out may be x itself, and overlaps no other input; it goes without gradients.
+
+    The gradients of x, weight and bias are those of the formula (first derivatives only);
+    sums over rows are taken in 32 bits and in one order."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm(x, weight, bias, eps=eps, out=out)
+    return _checked((_ext or _binding()).layer_norm(x, weight, bias, eps, out), "lm_layer_norm")
+
+
+def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, b_gate: torch.Tensor | None = None,
+                 b_up: torch.Tensor | None = None, *, activation: str | None = "silu", out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """act(x @ w_gate.T + b_gate) * (x @ w_up.T + b_up), rounded once: the gated block of a
+    feed-forward layer in one kernel.
+
+    x [..., K], w_gate and w_up [N, K] float16 or bfloat16 with K contiguous, x's other dimensions
+    evenly spaced rows; b_gate and b_up [N] float32 or x's dtype, one for both.  activation: "silu",
+    "gelu" (erf), "gelu_tanh", "relu", "sigmoid" or None.  out overlaps no input and goes without
+    gradients.
+
+    The gradients of all inputs are those of the formula (first derivatives only), from both
+    projections computed anew: the forward pass keeps nothing but its inputs.  The projections' own
+    gradients are rounded to x's dtype on their way into the products."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_linear(x, w_gate, w_up, b_gate, b_up, activation=activation, out=out)
+    act = _GATES.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {[a for a in _GATES if a]} or None")
+    return _checked((_ext or _binding()).gated_linear(x, w_gate, w_up, b_gate, b_up, act, out), "lm_gated_linear")
 
 
 # ---------------------------------------------------------------------------

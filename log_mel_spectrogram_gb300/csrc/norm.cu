@@ -6,6 +6,15 @@
 // Backward, with h = grad * weight:
 //   dx = (h - avg(h) - n avg(h n)) / sqrt(var + eps),
 //   dweight = sum over rows of grad n,  dbias = sum over rows of grad.
+//
+// Memory bounds both: a row is read once and stays in the registers of its team, 8
+// to 512 threads with 8, 16 or 32 elements each; teams walk the rows with the next row
+// on its way.  Backward, a thread adds its columns'
+// parts of dweight and dbias up over all rows of its team; a CTA's teams meet in
+// shared memory, and a second kernel joins the CTAs' sums in their order.
+//
+// Rows wider than a team can hold are read again for each pass, out of L2 (the kernels
+// at the end).
 #include <climits>
 
 #include "half.cuh"
@@ -15,16 +24,17 @@
 namespace lm {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMostChunks = 304;  // parts of the rows whose sums are joined at the end
+constexpr int kMostParts = 512;  // CTAs whose sums over rows are joined
+constexpr int kLoopThreads = 256;
+constexpr size_t kScratch = 2 * 32 * sizeof(float2);  // of a CTA's shared memory
 
 struct NormParams {
   const void *x, *weight, *bias, *grad;
   void *out;              // y, or dx
   float *stats;           // [3][rows]
-  float *partial;         // [chunks][2][width]
+  float *partial;         // [parts][2][width], or null
   int64_t rows, width, x_row, grad_row, out_row;
-  int32_t weight_f32, bias_f32, chunks;
+  int32_t weight_f32, bias_f32, parts;
   float eps;
 };
 
@@ -34,6 +44,382 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+template <typename T>
+__device__ __forceinline__ float param_at(const void *p, int f32, int64_t i, float otherwise) {
+  if (!p) return otherwise;
+  return f32 ? static_cast<const float *>(p)[i] : to_f32(static_cast<const T *>(p)[i]);
+}
+
+// Sums over a team's threads, for each of them.  A team of several warps has a barrier of its own
+// and two places for its warps' sums in turn, so that one wait a sum is enough.
+template <int TEAM>
+struct TeamSum {
+  float2 (*scratch)[32];  // [2][32], warps of the CTA
+  int turn = 0;
+
+  __device__ __forceinline__ float2 operator()(float a, float b) {
+#pragma unroll
+    for (int o = (TEAM < 32 ? TEAM : 32) / 2; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if constexpr (TEAM > 32) {
+      const int warp = static_cast<int>(threadIdx.x) / 32, team = static_cast<int>(threadIdx.x) / TEAM;
+      float2 *const at = scratch[turn];
+      turn ^= 1;
+      if (threadIdx.x % 32 == 0) at[warp] = make_float2(a, b);
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TEAM) : "memory");
+      a = b = 0.0f;
+#pragma unroll
+      for (int i = 0; i < TEAM / 32; ++i) {
+        const float2 v = at[team * (TEAM / 32) + i];
+        a += v.x;
+        b += v.y;
+      }
+    }
+    return make_float2(a, b);
+  }
+};
+
+// A thread's elements of a row: vectors of 16 bytes, TEAM vectors apart, or (rows off
+// 16-byte boundaries) single elements TEAM apart.
+template <typename T, int TEAM, int NE, bool VECTORS>
+struct Part {
+  static constexpr int kEach = VECTORS ? 16 / static_cast<int>(sizeof(T)) : 1;
+  static constexpr int kWords = VECTORS ? NE * static_cast<int>(sizeof(T)) / 4 : NE;
+  uint32_t w[kWords];
+
+  // Place j of thread t in the row.
+  static __device__ __forceinline__ int place(int j, int t) { return (j / kEach * TEAM + t) * kEach + j % kEach; }
+
+  __device__ __forceinline__ void load(const T *row, int width, int t, bool any) {
+    if constexpr (VECTORS) {
+#pragma unroll
+      for (int v = 0; v < NE / kEach; ++v) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (any && place(v * kEach, t) < width) u = *reinterpret_cast<const uint4 *>(row + place(v * kEach, t));
+        w[4 * v] = u.x;
+        w[4 * v + 1] = u.y;
+        w[4 * v + 2] = u.z;
+        w[4 * v + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NE; ++j) {
+        w[j] = 0;
+        if (any && place(j, t) < width) {
+          if constexpr (sizeof(T) == 4) {
+            w[j] = *reinterpret_cast<const uint32_t *>(row + place(j, t));
+          } else {
+            w[j] = *reinterpret_cast<const uint16_t *>(row + place(j, t));
+          }
+        }
+      }
+    }
+  }
+
+  // Elements j and j + 1.
+  __device__ __forceinline__ float2 two(int j) const {
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
+    else if constexpr (VECTORS) return unpack2<T>(w[j / 2]);
+    else return make_float2(unpack2<T>(w[j]).x, unpack2<T>(w[j + 1]).x);
+  }
+
+  __device__ __forceinline__ void set(int j, float a, float b) {
+    if constexpr (sizeof(T) == 4) {
+      w[j] = __float_as_uint(a);
+      w[j + 1] = __float_as_uint(b);
+    } else if constexpr (VECTORS) {
+      w[j / 2] = pack2<T>(a, b);
+    } else {
+      const uint32_t p = pack2<T>(a, b);
+      w[j] = p & 0xffffu;
+      w[j + 1] = p >> 16;
+    }
+  }
+
+  __device__ __forceinline__ void store(T *row, int width, int t) const {
+    if constexpr (VECTORS) {
+#pragma unroll
+      for (int v = 0; v < NE / kEach; ++v)
+        if (place(v * kEach, t) < width)
+          *reinterpret_cast<uint4 *>(row + place(v * kEach, t)) = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NE; ++j) {
+        if (place(j, t) >= width) continue;
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<uint32_t *>(row + place(j, t)) = w[j];
+        } else {
+          *reinterpret_cast<uint16_t *>(row + place(j, t)) = static_cast<uint16_t>(w[j]);
+        }
+      }
+    }
+  }
+};
+
+// Threads of a CTA that is alone on its SM, for so many registers a thread: whole teams, at most 15
+// of several warps (a CTA has 16 barriers).
+constexpr int threads_for(int team, int regs) {
+  const int most = 65536 / ((regs + 7) / 8 * 8) / 32 * 32;
+  const int teams = (most < 1024 ? most : 1024) / team;
+  return teams < 1 ? team : team > 32 && teams > 15 ? 15 * team : (teams * team) / 32 * 32;
+}
+
+// ---- forward ----
+
+// The weight and bias stay in registers where a thread has 8 elements, else in shared memory.
+template <typename P, int NE>
+constexpr int forward_regs() { return 56 + 2 * P::kWords + (NE == 8 ? 16 : 0); }
+template <typename P, int TEAM, int NE>
+constexpr int forward_threads() { return TEAM <= 32 ? 256 : TEAM; }
+template <typename P, int TEAM, int NE>
+constexpr int forward_ctas() {
+  const int n = threads_for(32, forward_regs<P, NE>()) / forward_threads<P, TEAM, NE>();
+  return n < 1 ? 1 : n;
+}
+
+template <typename T, int TEAM, int NE, bool VECTORS>
+__global__ void __launch_bounds__(forward_threads<Part<T, TEAM, NE, VECTORS>, TEAM, NE>(),
+                                  forward_ctas<Part<T, TEAM, NE, VECTORS>, TEAM, NE>()) norm_rows(const NormParams p) {
+  using P = Part<T, TEAM, NE, VECTORS>;
+  constexpr bool HOLD = NE == 8;
+  extern __shared__ float4 dynamic[];  // the sums' places; then weight and bias of two elements, [NE / 2][TEAM]
+  TeamSum<TEAM> sum{reinterpret_cast<float2(*)[32]>(dynamic)};
+  float4 *const params = dynamic + kScratch / sizeof(float4);
+  const int t = static_cast<int>(threadIdx.x) % TEAM, width = static_cast<int>(p.width);
+  const int64_t teams = static_cast<int64_t>(gridDim.x) * (blockDim.x / TEAM);
+  const int64_t team = static_cast<int64_t>(blockIdx.x) * (blockDim.x / TEAM) + threadIdx.x / TEAM;
+  const int64_t lead = TEAM < 32 ? team - threadIdx.x % 32 / TEAM : team;  // the warp's first
+  const float inv = 1.0f / static_cast<float>(width);
+  pdl_launch();
+  pdl_wait();
+  P now, next;
+  now.load(static_cast<const T *>(p.x) + team * p.x_row, width, t, team < p.rows);
+  auto param = [&](int j, int thread) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int i = P::place(j, thread), k = P::place(j + 1, thread);
+    if (i < width) {
+      v.x = param_at<T>(p.weight, p.weight_f32, i, 1.0f);
+      v.y = param_at<T>(p.bias, p.bias_f32, i, 0.0f);
+    }
+    if (k < width) {
+      v.z = param_at<T>(p.weight, p.weight_f32, k, 1.0f);
+      v.w = param_at<T>(p.bias, p.bias_f32, k, 0.0f);
+    }
+    return v;
+  };
+  float4 held[HOLD ? NE / 2 : 1];
+  if (HOLD) {
+#pragma unroll
+    for (int j = 0; j < NE; j += 2) held[HOLD ? j / 2 : 0] = param(j, t);
+  } else {
+    for (int i = threadIdx.x; i < NE / 2 * TEAM; i += blockDim.x) params[i] = param(i / TEAM * 2, i % TEAM);
+    __syncthreads();
+  }
+  for (int64_t row = team, first = lead; first < p.rows; row += teams, first += teams) {
+    const bool any = row < p.rows;
+    next.load(static_cast<const T *>(p.x) + (row + teams) * p.x_row, width, t, row + teams < p.rows);
+    float s = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NE; j += 2) {
+      const float2 v = now.two(j);
+      s += v.x + v.y;
+    }
+    const float mean = sum(s, 0.0f).x * inv;
+    s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NE; j += 2) {
+      const float2 v = now.two(j);
+      const float d0 = P::place(j, t) < width ? v.x - mean : 0.0f, d1 = P::place(j + 1, t) < width ? v.y - mean : 0.0f;
+      s += d0 + d1;
+      q = fmaf(d0, d0, fmaf(d1, d1, q));
+    }
+    const float2 u = sum(s, q);
+    const float off = u.x * inv, var = u.y * inv - off * off;
+    const float r = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + p.eps);
+    if (p.stats && t == 0 && any) {
+      p.stats[row] = mean;
+      p.stats[p.rows + row] = off;
+      p.stats[2 * p.rows + row] = r;
+    }
+#pragma unroll
+    for (int j = 0; j < NE; j += 2) {
+      const float2 v = now.two(j);
+      const float4 c = HOLD ? held[HOLD ? j / 2 : 0] : params[j / 2 * TEAM + t];
+      const float n0 = ((v.x - mean) - off) * r, n1 = ((v.y - mean) - off) * r;
+      now.set(j, fmaf(n0, c.x, c.y), fmaf(n1, c.z, c.w));
+    }
+    if (any) now.store(static_cast<T *>(p.out) + row * p.out_row, width, t);
+    now = next;
+  }
+}
+
+// ---- backward ----
+
+// The next row's elements have registers unless a team of 512 needs them all.
+template <typename P, int TEAM>
+constexpr bool backward_ahead() { return TEAM < 512 || P::kWords < 16; }
+template <typename P, int TEAM, int NE>
+constexpr int backward_threads() {
+  return threads_for(TEAM, 62 + 2 * NE + (backward_ahead<P, TEAM>() ? 4 : 2) * P::kWords);
+}
+
+template <typename T, int TEAM, int NE, bool VECTORS>
+__global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, TEAM, NE>(), 1)
+    norm_backward(const NormParams p) {
+  using P = Part<T, TEAM, NE, VECTORS>;
+  constexpr bool AHEAD = backward_ahead<P, TEAM>();
+  constexpr int PLACES = NE * TEAM;
+  extern __shared__ float4 dynamic[];  // the sums' places; the weight of two elements, [NE / 2][TEAM]; [..][NE][TEAM]
+  TeamSum<TEAM> sum{reinterpret_cast<float2(*)[32]>(dynamic)};
+  float2 *const shared = reinterpret_cast<float2 *>(dynamic + kScratch / sizeof(float4));
+  const int t = static_cast<int>(threadIdx.x) % TEAM, width = static_cast<int>(p.width);
+  const int64_t teams = static_cast<int64_t>(gridDim.x) * (blockDim.x / TEAM);
+  const int64_t team = static_cast<int64_t>(blockIdx.x) * (blockDim.x / TEAM) + threadIdx.x / TEAM;
+  const int64_t lead = TEAM < 32 ? team - threadIdx.x % 32 / TEAM : team;
+  const float inv = 1.0f / static_cast<float>(width);
+  float dw[NE], db[NE];
+#pragma unroll
+  for (int j = 0; j < NE; ++j) dw[j] = db[j] = 0.0f;
+  pdl_launch();
+  pdl_wait();
+  P x, g, next_x, next_g;
+  x.load(static_cast<const T *>(p.x) + team * p.x_row, width, t, team < p.rows);
+  g.load(static_cast<const T *>(p.grad) + team * p.grad_row, width, t, team < p.rows);
+  for (int i = threadIdx.x; i < PLACES / 2; i += blockDim.x) {
+    const int a = P::place(i / TEAM * 2, i % TEAM), b = P::place(i / TEAM * 2 + 1, i % TEAM);
+    shared[i] = make_float2(a < width ? param_at<T>(p.weight, p.weight_f32, a, 1.0f) : 0.0f,
+                            b < width ? param_at<T>(p.weight, p.weight_f32, b, 1.0f) : 0.0f);
+  }
+  __syncthreads();
+  for (int64_t row = team, first = lead; first < p.rows; row += teams, first += teams) {
+    const bool any = row < p.rows, more = row + teams < p.rows;
+    float mean = 0.0f, off = 0.0f, r = 0.0f;
+    if (any) {
+      mean = p.stats[row];
+      off = p.stats[p.rows + row];
+      r = p.stats[2 * p.rows + row];
+    }
+    if (AHEAD) {
+      next_x.load(static_cast<const T *>(p.x) + (row + teams) * p.x_row, width, t, more);
+      next_g.load(static_cast<const T *>(p.grad) + (row + teams) * p.grad_row, width, t, more);
+    }
+    float s = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NE; j += 2) {
+      const float2 v = x.two(j), e = g.two(j), w = shared[j / 2 * TEAM + t];
+      const float n0 = ((v.x - mean) - off) * r, n1 = ((v.y - mean) - off) * r;
+      // (A place past the width has no part, whatever its n.)
+      if (P::place(j, t) < width) {
+        const float h = e.x * w.x;
+        s += h;
+        q = fmaf(h, n0, q);
+        dw[j] = fmaf(e.x, n0, dw[j]);
+        db[j] += e.x;
+      }
+      if (P::place(j + 1, t) < width) {
+        const float h = e.y * w.y;
+        s += h;
+        q = fmaf(h, n1, q);
+        dw[j + 1] = fmaf(e.y, n1, dw[j + 1]);
+        db[j + 1] += e.y;
+      }
+    }
+    const float2 u = sum(s, q);
+    if (p.out) {
+      const float c1 = u.x * inv, c2 = u.y * inv;
+#pragma unroll
+      for (int j = 0; j < NE; j += 2) {
+        const float2 v = x.two(j), e = g.two(j), w = shared[j / 2 * TEAM + t];
+        const float n0 = ((v.x - mean) - off) * r, n1 = ((v.y - mean) - off) * r;
+        x.set(j, fmaf(-n0, c2, fmaf(e.x, w.x, -c1)) * r, fmaf(-n1, c2, fmaf(e.y, w.y, -c1)) * r);
+      }
+      if (any) x.store(static_cast<T *>(p.out) + row * p.out_row, width, t);
+    }
+    if (AHEAD) {
+      x = next_x;
+      g = next_g;
+    } else {
+      x.load(static_cast<const T *>(p.x) + (row + teams) * p.x_row, width, t, more);
+      g.load(static_cast<const T *>(p.grad) + (row + teams) * p.grad_row, width, t, more);
+    }
+  }
+  if (!p.partial) return;
+  // A warp's teams join by shuffles; then the upper half of the groups (teams, or warps of smaller ones) hand
+  // their sums to the lower, until one is left.
+  constexpr int GROUP = TEAM < 32 ? 32 : TEAM;
+#pragma unroll
+  for (int o = 16; o >= TEAM; o >>= 1)
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], o);
+      db[j] += __shfl_xor_sync(0xffffffffu, db[j], o);
+    }
+  const int group = static_cast<int>(threadIdx.x) / GROUP;
+  const bool mine = static_cast<int>(threadIdx.x) % GROUP < TEAM;
+  float2 *const slots = shared + PLACES / 2;
+  for (int n = static_cast<int>(blockDim.x) / GROUP; n > 1;) {
+    const int half = (n + 1) / 2;
+    if (group >= half && group < n && mine) {
+#pragma unroll
+      for (int j = 0; j < NE; ++j) slots[(group - half) * PLACES + j * TEAM + t] = make_float2(dw[j], db[j]);
+    }
+    __syncthreads();
+    if (group < n - half && mine) {
+#pragma unroll
+      for (int j = 0; j < NE; ++j) {
+        const float2 v = slots[group * PLACES + j * TEAM + t];
+        dw[j] += v.x;
+        db[j] += v.y;
+      }
+    }
+    __syncthreads();
+    n = half;
+  }
+  if (group != 0 || !mine) return;
+  float *const to = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * width;
+#pragma unroll
+  for (int j = 0; j < NE; ++j) {
+    const int at = P::place(j, t);
+    if (at >= width) continue;
+    to[at] = dw[j];
+    to[width + at] = db[j];
+  }
+}
+
+// Joins the parts: a CTA has 32 columns, its warps every eighth part; then the warps in their order.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_join(const float *partial, int parts, int64_t width, void *dweight,
+                                                 int weight_f32, void *dbias, int bias_f32) {
+  __shared__ float sums[8][32];
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float s = 0.0f;
+  if (i < 2 * width) {
+#pragma unroll 8
+    for (int c = warp; c < parts; c += 8) s += partial[static_cast<int64_t>(c) * 2 * width + i];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || i >= 2 * width) return;
+  s = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) s += sums[c][lane];
+  void *const to = i < width ? dweight : dbias;
+  if (!to) return;
+  const int64_t at = i < width ? i : i - width;
+  if (i < width ? weight_f32 : bias_f32) {
+    static_cast<float *>(to)[at] = s;
+  } else {
+    static_cast<T *>(to)[at] = from_f32<T>(s);
+  }
+}
+
+// ---- rows that no team holds ----
+
 // The sums of two values over the CTA, for every thread.
 __device__ __forceinline__ float2 cta_sum2(float a, float b, float2 *scratch) {
   a = warp_sum(a);
@@ -42,7 +428,7 @@ __device__ __forceinline__ float2 cta_sum2(float a, float b, float2 *scratch) {
   if (threadIdx.x % 32 == 0) scratch[threadIdx.x / 32] = make_float2(a, b);
   __syncthreads();
   float2 s = make_float2(0.0f, 0.0f);
-  for (int i = 0; i < kThreads / 32; ++i) {
+  for (int i = 0; i < kLoopThreads / 32; ++i) {
     s.x += scratch[i].x;
     s.y += scratch[i].y;
   }
@@ -50,14 +436,8 @@ __device__ __forceinline__ float2 cta_sum2(float a, float b, float2 *scratch) {
 }
 
 template <typename T>
-__device__ __forceinline__ float param_at(const void *p, int f32, int64_t i, float otherwise) {
-  if (!p) return otherwise;
-  return f32 ? static_cast<const float *>(p)[i] : to_f32(static_cast<const T *>(p)[i]);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_rows(const NormParams p) {
-  __shared__ float2 scratch[kThreads / 32];
+__global__ void __launch_bounds__(kLoopThreads) norm_rows_loop(const NormParams p) {
+  __shared__ float2 scratch[kLoopThreads / 32];
   pdl_launch();
   pdl_wait();
   const int64_t row = blockIdx.x;
@@ -65,10 +445,10 @@ __global__ void __launch_bounds__(kThreads) norm_rows(const NormParams p) {
   T *const out = static_cast<T *>(p.out) + row * p.out_row;
   const float inv = 1.0f / static_cast<float>(p.width);
   float s = 0.0f, q = 0.0f;
-  for (int64_t i = threadIdx.x; i < p.width; i += kThreads) s += to_f32(x[i]);
+  for (int64_t i = threadIdx.x; i < p.width; i += kLoopThreads) s += to_f32(x[i]);
   const float mean = cta_sum2(s, 0.0f, scratch).x * inv;
   s = 0.0f;
-  for (int64_t i = threadIdx.x; i < p.width; i += kThreads) {
+  for (int64_t i = threadIdx.x; i < p.width; i += kLoopThreads) {
     const float d = to_f32(x[i]) - mean;
     s += d;
     q += d * d;
@@ -81,15 +461,15 @@ __global__ void __launch_bounds__(kThreads) norm_rows(const NormParams p) {
     p.stats[p.rows + row] = off;
     p.stats[2 * p.rows + row] = r;
   }
-  for (int64_t i = threadIdx.x; i < p.width; i += kThreads) {
+  for (int64_t i = threadIdx.x; i < p.width; i += kLoopThreads) {
     const float n = ((to_f32(x[i]) - mean) - off) * r;
     out[i] = from_f32<T>(n * param_at<T>(p.weight, p.weight_f32, i, 1.0f) + param_at<T>(p.bias, p.bias_f32, i, 0.0f));
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_backward_rows(const NormParams p) {
-  __shared__ float2 scratch[kThreads / 32];
+__global__ void __launch_bounds__(kLoopThreads) norm_backward_rows_loop(const NormParams p) {
+  __shared__ float2 scratch[kLoopThreads / 32];
   pdl_launch();
   pdl_wait();
   const int64_t row = blockIdx.x;
@@ -99,14 +479,14 @@ __global__ void __launch_bounds__(kThreads) norm_backward_rows(const NormParams 
   const float mean = p.stats[row], off = p.stats[p.rows + row], r = p.stats[2 * p.rows + row];
   const float inv = 1.0f / static_cast<float>(p.width);
   float s = 0.0f, q = 0.0f;
-  for (int64_t i = threadIdx.x; i < p.width; i += kThreads) {
+  for (int64_t i = threadIdx.x; i < p.width; i += kLoopThreads) {
     const float n = ((to_f32(x[i]) - mean) - off) * r;
     const float h = to_f32(g[i]) * param_at<T>(p.weight, p.weight_f32, i, 1.0f);
     s += h;
     q += h * n;
   }
   const float2 t = cta_sum2(s, q, scratch);
-  for (int64_t i = threadIdx.x; i < p.width; i += kThreads) {
+  for (int64_t i = threadIdx.x; i < p.width; i += kLoopThreads) {
     const float n = ((to_f32(x[i]) - mean) - off) * r;
     const float h = to_f32(g[i]) * param_at<T>(p.weight, p.weight_f32, i, 1.0f);
     out[i] = from_f32<T>((h - t.x * inv - n * (t.y * inv)) * r);
@@ -115,12 +495,12 @@ __global__ void __launch_bounds__(kThreads) norm_backward_rows(const NormParams 
 
 // Sums over a part of the rows (blockIdx.y) for a thread's column.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_backward_columns(const NormParams p) {
+__global__ void __launch_bounds__(kLoopThreads) norm_backward_columns_loop(const NormParams p) {
   pdl_launch();
   pdl_wait();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kLoopThreads + threadIdx.x;
   if (i >= p.width) return;
-  const int64_t first = p.rows * blockIdx.y / p.chunks, end = p.rows * (blockIdx.y + 1) / p.chunks;
+  const int64_t first = p.rows * blockIdx.y / p.parts, end = p.rows * (blockIdx.y + 1) / p.parts;
   float dw = 0.0f, db = 0.0f;
   for (int64_t row = first; row < end; ++row) {
     const float g = to_f32(static_cast<const T *>(p.grad)[row * p.grad_row + i]);
@@ -131,26 +511,6 @@ __global__ void __launch_bounds__(kThreads) norm_backward_columns(const NormPara
   float *const to = p.partial + static_cast<int64_t>(blockIdx.y) * 2 * p.width + i;
   to[0] = dw;
   to[p.width] = db;
-}
-
-// Joins the parts in their order.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_join(const float *partial, int chunks, int64_t width, void *dweight,
-                                                      int weight_f32, void *dbias, int bias_f32) {
-  pdl_launch();
-  pdl_wait();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= 2 * width) return;
-  float s = 0.0f;
-  for (int c = 0; c < chunks; ++c) s += partial[static_cast<int64_t>(c) * 2 * width + i];
-  void *const to = i < width ? dweight : dbias;
-  if (!to) return;
-  const int64_t at = i < width ? i : i - width;
-  if (i < width ? weight_f32 : bias_f32) {
-    static_cast<float *>(to)[at] = s;
-  } else {
-    static_cast<T *>(to)[at] = from_f32<T>(s);
-  }
 }
 
 int64_t size_of(int32_t dtype) { return dtype == LM_F32 ? 4 : 2; }
@@ -170,28 +530,147 @@ lm_status check_sizes(int64_t rows, int64_t width, int64_t x_row, int64_t other_
   return LM_OK;
 }
 
-template <typename T>
-lm_status forward(const NormParams &p, cudaStream_t s) {
-  return launch_dependent(norm_rows<T>, dim3(static_cast<unsigned>(p.rows)), kThreads, 0, s, 1, p);
+int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// Whether rows and their step are whole vectors of 16 bytes.
+bool vectors(const void *p, int64_t step, int64_t rows, int64_t size) {
+  return aligned(p, 16) && (rows == 1 || step * size % 16 == 0);
 }
 
-int chunks_of(int64_t rows) { return rows < kMostChunks ? static_cast<int>(rows) : kMostChunks; }
+// Threads a row and elements a thread.
+struct Shape {
+  int team, each;
+};
+
+// Few rows are shared out among many threads, for the least time of one; of many, a warp holds up
+// to 1024 elements, because its sums need no barrier.
+Shape forward_shape(int64_t rows, int64_t width, int sms) {
+  const bool few = rows <= 4 * sms;
+  auto each = [&](int team) { return width <= 8 * team ? 8 : width <= 16 * team ? 16 : 32; };
+  if (width > 512 * 32) return {0, 0};
+  if (width <= 64) return {8, 8};
+  if (width <= (few ? 256 : 1024)) return {32, each(32)};
+  if (width <= (few ? 1024 : 4096)) return {128, each(128)};
+  return {512, each(512) < 16 ? 16 : each(512)};
+}
+
+// At most 16 elements a thread: it also holds their sums over rows.
+Shape backward_shape(int64_t width) {
+  if (width > 512 * 16) return {0, 0};
+  if (width <= 64) return {8, 8};
+  if (width <= 256) return {32, 8};
+  int team = 32;
+  while (team * 16 < width) team *= 2;
+  return {team, 16};
+}
+
+// Threads of a CTA of whole teams, at most `most`: few enough for every SM to have some.
+int spread(int team, int64_t rows, int most, int sms) {
+  const int unit = team < 32 ? 32 : team;
+  const int64_t units = (rows * team + unit - 1) / unit;
+  return unit * static_cast<int>(least(most / unit, (units + sms - 1) / sms));
+}
+
+template <typename T, int TEAM, int NE, bool VECTORS>
+lm_status forward_as(const NormParams &p, int sms, cudaStream_t s) {
+  using P = Part<T, TEAM, NE, VECTORS>;
+  constexpr int most = forward_threads<P, TEAM, NE>();
+  const int threads = spread(TEAM, p.rows, most, sms);
+  const int64_t ctas = (p.rows + threads / TEAM - 1) / (threads / TEAM);
+  const int64_t held = static_cast<int64_t>(sms) * forward_ctas<P, TEAM, NE>() * (most / threads);
+  const auto kernel = norm_rows<T, TEAM, NE, VECTORS>;
+  const size_t shared = kScratch + (NE == 8 ? 0 : sizeof(float4) * NE / 2 * TEAM);
+  if (shared > 40 * 1024)
+    if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), static_cast<int>(shared)); st != LM_OK)
+      return st;
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(least(ctas, held))), threads, shared, s, 1, p);
+}
+
+template <typename T, int TEAM, int NE, bool VECTORS>
+lm_status backward_as(NormParams &p, int sms, cudaStream_t s) {
+  using P = Part<T, TEAM, NE, VECTORS>;
+  const int threads = spread(TEAM, p.rows, backward_threads<P, TEAM, NE>(), sms);
+  const int64_t ctas = (p.rows + threads / TEAM - 1) / (threads / TEAM);
+  p.parts = static_cast<int>(least(least(ctas, kMostParts), sms));
+  const int groups = threads / (TEAM < 32 ? 32 : TEAM);
+  const size_t shared = kScratch + sizeof(float2) * TEAM * NE / 2 + sizeof(float2) * TEAM * NE * static_cast<size_t>(groups / 2);
+  const auto kernel = norm_backward<T, TEAM, NE, VECTORS>;
+  if (shared > 40 * 1024)
+    if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), static_cast<int>(shared)); st != LM_OK)
+      return st;
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(p.parts)), threads, shared, s, 1, p);
+}
+
+template <typename T, bool VECTORS>
+lm_status forward_shaped(const NormParams &p, Shape h, int sms, cudaStream_t s) {
+  if (h.team == 8) return forward_as<T, 8, 8, VECTORS>(p, sms, s);
+  if (h.team == 32)
+    return h.each == 8 ? forward_as<T, 32, 8, VECTORS>(p, sms, s) : h.each == 16 ? forward_as<T, 32, 16, VECTORS>(p, sms, s)
+                                                                                 : forward_as<T, 32, 32, VECTORS>(p, sms, s);
+  if (h.team == 128)
+    return h.each == 8    ? forward_as<T, 128, 8, VECTORS>(p, sms, s)
+           : h.each == 16 ? forward_as<T, 128, 16, VECTORS>(p, sms, s)
+                          : forward_as<T, 128, 32, VECTORS>(p, sms, s);
+  return h.each == 16 ? forward_as<T, 512, 16, VECTORS>(p, sms, s) : forward_as<T, 512, 32, VECTORS>(p, sms, s);
+}
+
+template <typename T, bool VECTORS>
+lm_status backward_shaped(NormParams &p, Shape h, int sms, cudaStream_t s) {
+  switch (h.team) {
+    case 8: return backward_as<T, 8, 8, VECTORS>(p, sms, s);
+    case 32: return h.each == 8 ? backward_as<T, 32, 8, VECTORS>(p, sms, s) : backward_as<T, 32, 16, VECTORS>(p, sms, s);
+    case 64: return backward_as<T, 64, 16, VECTORS>(p, sms, s);
+    case 128: return backward_as<T, 128, 16, VECTORS>(p, sms, s);
+    case 256: return backward_as<T, 256, 16, VECTORS>(p, sms, s);
+    default: return backward_as<T, 512, 16, VECTORS>(p, sms, s);
+  }
+}
+
+template <typename T>
+lm_status forward(const NormParams &p, cudaStream_t s) {
+  DeviceInfo dev;
+  if (lm_status st = current_device_info(&dev); st != LM_OK) return st;
+  const Shape h = forward_shape(p.rows, p.width, dev.sm_count);
+  if (h.team == 0)
+    return launch_dependent(norm_rows_loop<T>, dim3(static_cast<unsigned>(p.rows)), kLoopThreads, 0, s, 1, p);
+  const int64_t size = sizeof(T);
+  const bool v = p.width * size % 16 == 0 && vectors(p.x, p.x_row, p.rows, size) && vectors(p.out, p.out_row, p.rows, size);
+  return v ? forward_shaped<T, true>(p, h, dev.sm_count, s) : forward_shaped<T, false>(p, h, dev.sm_count, s);
+}
 
 template <typename T>
 lm_status backward(NormParams p, void *dweight, void *dbias, cudaStream_t s) {
-  if (p.out && p.rows > 0)
-    if (lm_status st = launch_dependent(norm_backward_rows<T>, dim3(static_cast<unsigned>(p.rows)), kThreads, 0, s, 1, p);
-        st != LM_OK)
-      return st;
-  if (!dweight && !dbias) return LM_OK;
-  const unsigned across = static_cast<unsigned>((p.width + kThreads - 1) / kThreads);
-  if (p.chunks > 0)
-    if (lm_status st = launch_dependent(norm_backward_columns<T>, dim3(across, static_cast<unsigned>(p.chunks)), kThreads,
-                                        0, s, 1, p);
-        st != LM_OK)
-      return st;
-  return launch_dependent(norm_join<T>, dim3(static_cast<unsigned>((2 * p.width + kThreads - 1) / kThreads)), kThreads, 0,
-                          s, 1, p.partial, p.chunks, p.width, dweight, p.weight_f32, dbias, p.bias_f32);
+  if (!dweight && !dbias) p.partial = nullptr;
+  float *const partial = p.partial;
+  if (p.rows > 0) {
+    DeviceInfo dev;
+    if (lm_status st = current_device_info(&dev); st != LM_OK) return st;
+    const Shape h = backward_shape(p.width);
+    const int64_t size = sizeof(T);
+    if (h.team != 0) {
+      const bool v = p.width * size % 16 == 0 && vectors(p.x, p.x_row, p.rows, size) &&
+                     vectors(p.grad, p.grad_row, p.rows, size) && vectors(p.out, p.out_row, p.rows, size);
+      if (lm_status st = v ? backward_shaped<T, true>(p, h, dev.sm_count, s) : backward_shaped<T, false>(p, h, dev.sm_count, s);
+          st != LM_OK)
+        return st;
+    } else {
+      if (p.out)
+        if (lm_status st = launch_dependent(norm_backward_rows_loop<T>, dim3(static_cast<unsigned>(p.rows)), kLoopThreads, 0,
+                                            s, 1, p);
+            st != LM_OK)
+          return st;
+      p.parts = static_cast<int>(least(p.rows, 256));
+      const unsigned across = static_cast<unsigned>((p.width + kLoopThreads - 1) / kLoopThreads);
+      if (partial)
+        if (lm_status st = launch_dependent(norm_backward_columns_loop<T>, dim3(across, static_cast<unsigned>(p.parts)),
+                                            kLoopThreads, 0, s, 1, p);
+            st != LM_OK)
+          return st;
+    }
+  }
+  if (!partial) return LM_OK;
+  return launch_dependent(norm_join<T>, dim3(static_cast<unsigned>((2 * p.width + 31) / 32)), 256, 0, s, 1,
+                          static_cast<const float *>(partial), p.parts, p.width, dweight, p.weight_f32, dbias, p.bias_f32);
 }
 
 }  // namespace
@@ -249,7 +728,7 @@ extern "C" lm_status lm_layer_norm_backward_workspace_size(const lm_norm_backwar
           check_sizes(a->rows, a->width, a->x_row_stride, a->grad_row_stride, a->dtype, a->weight_dtype, a->bias_dtype);
       st != LM_OK)
     return st;
-  *bytes = 256 + static_cast<size_t>(chunks_of(a->rows)) * 8 * static_cast<size_t>(a->width);
+  *bytes = 256 + static_cast<size_t>(a->rows < lm::kMostParts ? a->rows : lm::kMostParts) * 8 * static_cast<size_t>(a->width);
   return LM_OK;
 }
 
@@ -292,7 +771,6 @@ extern "C" lm_status lm_layer_norm_backward(const lm_norm_backward_args *a, void
   p.out_row = a->width;
   p.weight_f32 = a->weight_dtype == LM_F32;
   p.bias_f32 = a->bias_dtype == LM_F32;
-  p.chunks = chunks_of(a->rows);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return a->dtype == LM_F32   ? backward<float>(p, a->dweight, a->dbias, s)
          : a->dtype == LM_F16 ? backward<__half>(p, a->dweight, a->dbias, s)

@@ -488,7 +488,7 @@ lm_status lm_linear_workspace_size(const lm_linear_args *args, size_t *bytes);
 lm_status lm_linear(const lm_linear_args *args, void *workspace, size_t workspace_bytes, lm_stream_t stream);
 
 /* Synchronises `stream`, then reads the bits (those of lm_workspace_error)
- * that lm_linear and lm_kv_attend have reported on the current device, on any
+ * that lm_linear, lm_gated_linear (and its backward pass) and lm_kv_attend have reported on the current device, on any
  * stream and with any workspace, since the word was last cleared; clears it
  * where `clear` is nonzero.  Where it is not zero, some call's output is not
  * whole.  Returns LM_ERR_DEVICE_FAULT when a bit was set,
@@ -836,6 +836,15 @@ typedef struct lm_gated_backward_args {
 lm_status lm_gated_linear_backward_workspace_size(const lm_gated_backward_args *args, size_t *bytes);
 lm_status lm_gated_linear_backward(const lm_gated_backward_args *args, void *workspace, size_t workspace_bytes,
                                    lm_stream_t stream);
+
+/* Fault injection for tests of the bounded waits, as lm_debug_linear_withhold:
+ * in each kernel of the call the first tile of operands that CTA
+ * `withheld_cta` (>= 0) fetches never counts as complete. */
+lm_status lm_debug_gated_linear_withhold(const lm_gated_args *args, void *workspace, size_t workspace_bytes,
+                                         int64_t withheld_cta, uint64_t wait_ns, lm_stream_t stream);
+lm_status lm_debug_gated_linear_backward_withhold(const lm_gated_backward_args *args, void *workspace,
+                                                  size_t workspace_bytes, int64_t withheld_cta, uint64_t wait_ns,
+                                                  lm_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* 9. weights in 4 bits (the source pages have no counterpart)              */

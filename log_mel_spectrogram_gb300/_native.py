@@ -146,6 +146,10 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.lm_gated_linear_backward_workspace_size.restype = ctypes.c_int
     L.lm_gated_linear_backward.argtypes = [vp, vp, sz, vp]
     L.lm_gated_linear_backward.restype = ctypes.c_int
+    L.lm_debug_gated_linear_withhold.argtypes = [vp, vp, sz, i64, ctypes.c_uint64, vp]
+    L.lm_debug_gated_linear_withhold.restype = ctypes.c_int
+    L.lm_debug_gated_linear_backward_withhold.argtypes = [vp, vp, sz, i64, ctypes.c_uint64, vp]
+    L.lm_debug_gated_linear_backward_withhold.restype = ctypes.c_int
     L.lm_weight4_size.argtypes = [vp, vp, vp]
     L.lm_weight4_size.restype = ctypes.c_int
     L.lm_weight4_pack.argtypes = [vp, vp, vp, vp]

@@ -94,9 +94,18 @@ uint64_t call_token(cudaStream_t stream);
 // Argument rules of lm_linear that need no pointers.
 lm_status linear_check(const lm_linear_args *args);
 
-// What the kernels of linear.cu and kv_attend.cu have reported on the current device since it was last
+// Clusters of 2, 4 and 8 CTAs, one to an SM, that the device holds at once (SMs
+// that have no partner in their group stay out).
+constexpr int kMaxSplits = 8;
+struct Resident {
+  int pairs, split[kMaxSplits + 1];
+};
+lm_status resident_clusters(const DeviceInfo &dev, Resident *r);
+
+// What the kernels of linear.cu, gated.cu and kv_attend.cu have reported on the current device since it was last
 // cleared, added to *value.
 lm_status linear_error(uint32_t *value, bool clear, cudaStream_t stream);
+lm_status gated_error(uint32_t *value, bool clear, cudaStream_t stream);
 lm_status attend_error(uint32_t *value, bool clear, cudaStream_t stream);
 
 // --- log_mel_from_stft -----------------------------------------------------

@@ -50,6 +50,7 @@
 #include "f32x2.cuh"
 #include "half.cuh"
 #include "internal.h"
+#include "operand.cuh"
 #include "pdl.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
@@ -62,7 +63,6 @@ constexpr int kBk = 64;             // elements of k per stage: one 128-byte swi
 constexpr int kLanes = 128;         // rows of W of a CTA's tile
 constexpr int kMaxBn = 256;
 constexpr int kMaxStages = 8;
-constexpr int kMaxSplits = 8;
 
 enum class Form {
   kOne,    // a CTA per tile of 128 lanes
@@ -455,28 +455,6 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   }
 }
 
-// Copies rows off 16-byte boundaries into rows padded to 8 elements.
-struct PackParams {
-  const uint16_t *src;
-  uint4 *dst;
-  int64_t group_stride, row_stride, rows, k, vecs, total;  // vecs: 16-byte vectors a row
-};
-
-__global__ void __launch_bounds__(256) pack_kernel(const PackParams p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  pdl_launch();
-  pdl_wait();
-  if (i >= p.total) return;
-  const int64_t row = i / p.vecs, v = i % p.vecs;
-  const uint16_t *const s = p.src + row / p.rows * p.group_stride + row % p.rows * p.row_stride + v * 8;
-  uint32_t w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = v * 8 + j < p.k ? s[j] : 0u;
-  p.dst[i] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-}
-
-bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 lm_status check(const lm_linear_args *a) {
   if (!a || a->groups < 0 || a->rows < 0 || a->k < 0 || a->n < 0) return LM_ERR_INVALID_ARG;
   if (a->x_group_stride < 0 || a->x_row_stride < 0 || a->weight_row_stride < 0 || a->residual_row_stride < 0 ||
@@ -492,36 +470,6 @@ lm_status check(const lm_linear_args *a) {
       (a->rows > 0 && a->groups > most / a->rows))
     return LM_ERR_UNSUPPORTED;
   return LM_OK;
-}
-
-// An operand as TMA sees it: [groups][rows][k], strides in elements.
-struct Operand {
-  const void *p;
-  int64_t groups, rows, group_stride, row_stride;
-  bool pack;       // copied into the workspace first
-  size_t bytes;    // of that copy
-};
-
-Operand operand(const void *p, int64_t groups, int64_t rows, int64_t k, int64_t group_stride, int64_t row_stride) {
-  Operand o{p, groups, rows, group_stride, row_stride, false, 0};
-  if (o.rows == 1 && o.groups > 1) {  // one row per group: the groups are the rows
-    o.rows = o.groups;
-    o.groups = 1;
-    o.row_stride = group_stride;
-  }
-  if (o.rows <= 1) o.row_stride = k;  // never used
-  if (o.groups <= 1) o.group_stride = o.rows * o.row_stride;
-  if (o.groups > 1 && o.group_stride == o.rows * o.row_stride) {
-    o.rows *= o.groups;
-    o.groups = 1;
-  }
-  // Strides that are in use must be multiples of 16 bytes, and not zero.
-  const bool rows_ok = o.rows <= 1 || (o.row_stride > 0 && o.row_stride % 8 == 0);
-  const bool groups_ok = o.groups <= 1 || (o.group_stride > 0 && o.group_stride % 8 == 0);
-  o.pack = k > 0 && !(aligned(p, 16) && rows_ok && groups_ok && o.row_stride < (1ll << 38) &&
-                      o.group_stride < (1ll << 38));
-  if (o.pack) o.bytes = static_cast<size_t>(o.groups) * o.rows * ((k + 7) / 8) * 16;
-  return o;
 }
 
 struct Plan {
@@ -554,64 +502,6 @@ bool out_meets_inputs(const lm_linear_args &a, const Plan &p, int64_t out_size) 
   return a.residual && !same && rows_meet(out, {a.residual, rows, a.residual_row_stride * 2, a.n * 2});
 }
 
-lm_status pack(Operand *o, int64_t k, void *dst, cudaStream_t s) {
-  PackParams p;
-  p.src = static_cast<const uint16_t *>(o->p);
-  p.dst = static_cast<uint4 *>(dst);
-  p.group_stride = o->group_stride;
-  p.row_stride = o->row_stride;
-  p.rows = o->rows;
-  p.k = k;
-  p.vecs = (k + 7) / 8;
-  p.total = o->groups * o->rows * p.vecs;
-  const int64_t ctas = (p.total + 255) / 256;
-  if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
-  if (lm_status st = launch_dependent(pack_kernel, dim3(static_cast<unsigned>(ctas)), 256, 0, s, 1, p); st != LM_OK)
-    return st;
-  o->p = dst;
-  o->row_stride = p.vecs * 8;
-  o->group_stride = o->rows * o->row_stride;
-  return LM_OK;
-}
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      (void)cudaGetLastError();
-      f = nullptr;
-    }
-    return reinterpret_cast<EncodeFn>(f);
-  }();
-  return fn;
-}
-
-// Tiles of `box_rows` rows x 64 elements of k, zeros outside.
-lm_status make_map(CUtensorMap *map, const Operand &o, int64_t k, int box_rows, bool bf16) {
-  const EncodeFn fn = encode_fn();
-  if (!fn) return cuda_fail(cudaErrorNotSupported);
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(o.rows),
-                              static_cast<cuuint64_t>(o.groups)};
-  // A stride that is not used still has to be a valid one.
-  const int64_t pad = (k + 7) / 8 * 8;
-  // (A row that is alone may have any stride.)
-  const int64_t rs = o.rows > 1 ? o.row_stride : pad;
-  const int64_t gs = o.groups > 1 ? o.group_stride : pad;
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(rs) * 2, static_cast<cuuint64_t>(gs) * 2};
-  const cuuint32_t box[3] = {kBk, static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
-  const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                        const_cast<void *>(o.p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? LM_OK : cuda_fail(cudaErrorInvalidValue);
-}
-
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const LinearParams);
 
 template <typename T>
@@ -620,17 +510,12 @@ Kernel kernel_of(Form form) {
          : form == Form::kPair ? linear_kernel<T, Form::kPair> : linear_kernel<T, Form::kOne>;
 }
 
-// Clusters of 2, 4 and 8 CTAs, one to an SM, that the device holds at once (SMs
-// that have no partner in their group stay out), asked once per device.  Two
-// threads that ask together get the same answer.
-struct Resident {
-  int pairs, split[kMaxSplits + 1];
-};
+// Asked once per device.  Two threads that ask together get the same answer.
 constexpr int kKnownDevices = 64;
 Resident g_resident[kKnownDevices];
 std::atomic<int> g_resident_state[kKnownDevices];  // 0: not known, 1: being written, 2: known
 
-lm_status resident_clusters(const DeviceInfo &dev, Resident *r) {
+lm_status ask_resident_clusters(const DeviceInfo &dev, Resident *r) {
   if (dev.device < kKnownDevices && g_resident_state[dev.device].load(std::memory_order_acquire) == 2) {
     *r = g_resident[dev.device];
     return LM_OK;
@@ -770,7 +655,7 @@ lm_status run(const lm_linear_args *args, void *workspace, size_t workspace_byte
   const bool bf16 = a.dtype == LM_BF16;
 
   Resident held;
-  if (lm_status st = resident_clusters(dev, &held); st != LM_OK) return st;
+  if (lm_status st = ask_resident_clusters(dev, &held); st != LM_OK) return st;
   const Cut cut = best_cut(p.n, p.rows, pl.x.groups, p.kblocks, p.act > LM_ACT_RELU, dev.sm_count, held);
   if (cut.tiles > INT_MAX / 16) return LM_ERR_UNSUPPORTED;
   p.bn = cut.bn;
@@ -812,6 +697,8 @@ lm_status run(const lm_linear_args *args, void *workspace, size_t workspace_byte
 }  // namespace
 
 lm_status linear_check(const lm_linear_args *args) { return check(args); }
+
+lm_status resident_clusters(const DeviceInfo &dev, Resident *r) { return ask_resident_clusters(dev, r); }
 
 lm_status linear_error(uint32_t *value, bool clear, cudaStream_t s) { return read_sticky(g_linear_error, value, clear, s); }
 

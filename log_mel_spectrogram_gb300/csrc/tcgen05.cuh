@@ -102,6 +102,15 @@ __device__ __forceinline__ uint64_t smem_desc_k128(uint32_t addr) {
   return (static_cast<uint64_t>(addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// ... whose contraction index K runs along the rows instead: rows of 64 elements of M or N, one for each k, 1024 bytes
+// to the next eight; the next 64 elements of M or N are 8192 bytes away.  16 further along K is 2048 bytes: +128.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t addr) {
+  return (static_cast<uint64_t>(addr & 0x3ffffu) >> 4) | (512ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Bits of the instruction descriptor: A and B have K along the rows.
+constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
+
 // Instruction descriptor of kind::f16 with f32 sums: bf16 operands or f16,
 // both K-major, m = 128 or (pair) 256 rows of A, n rows of B (a multiple of 16,
 // of 32 for a pair; at most 256).
@@ -120,7 +129,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
       : "r"(addr));
 }
 
-// The registers of earlier tmem_ld16 calls hold their values.
+// ... and of 8.
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+
+// The registers of earlier tmem_ld16 and tmem_ld8 calls hold their values.
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // The address that `local` has in CTA `rank` of the cluster.

@@ -60,8 +60,8 @@ def _checked(r, what: str):
 
 
 def decode_error(device=None, *, clear: bool = True) -> int:
-    """Waits for the device and returns the error bits that linear() and
-    KvCache.attend() have reported on it since the last call (0: none), replayed
+    """Waits for the device and returns the error bits that linear(), gated_linear()
+    (and its backward pass) and KvCache.attend() have reported on it since the last call (0: none), replayed
     graphs included.  Every wait inside their kernels is bounded; one that runs out
     ends the kernel, sets a bit here, and leaves outputs that are not whole."""
     v = ctypes.c_uint32()

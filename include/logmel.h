@@ -855,10 +855,10 @@ lm_status lm_debug_gated_linear_backward_withhold(const lm_gated_backward_args *
  * and `group` consecutive k:  w[i][j] = q[i][j] * s[i][j / group].
  *   packed   device, ceil(n / 16) * ceil(k / 64) tiles of 512 bytes, 16-byte
  *            aligned; a tile is 16 rows by 64 k, tiles run along k first.
- *            Bytes 16 l .. 16 l + 15 of a tile hold rows l / 4 and l / 4 + 8
- *            at k = 16 (l % 4) .. + 15, as two little-endian u32 a row, each of
- *            eight k in order 0 2 4 6 1 3 5 7 from its lowest nibble; a nibble
- *            is q + 8.  Places past n or k hold q = 0.
+ *            Bytes 16 l .. 16 l + 15 of a tile are four little-endian u32 of
+ *            eight k each: row l / 4 at k = 8 (l % 4) .. + 7 and 32 + 8 (l % 4) .. + 7,
+ *            then row l / 4 + 8 at the same.  From a u32's lowest nibble the eight
+ *            are in order 0 2 4 6 1 3 5 7; a nibble is q + 8.  Places past n or k hold q = 0.
  *   scale    device, [ceil(n / 16)][ceil(k / group)][16] f32, 16-byte aligned
  *   group    32, 64 or 128
  */

@@ -488,7 +488,7 @@ lm_status lm_linear_workspace_size(const lm_linear_args *args, size_t *bytes);
 lm_status lm_linear(const lm_linear_args *args, void *workspace, size_t workspace_bytes, lm_stream_t stream);
 
 /* Synchronises `stream`, then reads the bits (those of lm_workspace_error)
- * that lm_linear, lm_gated_linear (and its backward pass) and lm_kv_attend have reported on the current device, on any
+ * that lm_linear, lm_linear4, lm_gated_linear, its backward pass and lm_kv_attend have reported on the current device, on any
  * stream and with any workspace, since the word was last cleared; clears it
  * where `clear` is nonzero.  Where it is not zero, some call's output is not
  * whole.  Returns LM_ERR_DEVICE_FAULT when a bit was set,
@@ -853,13 +853,15 @@ lm_status lm_debug_gated_linear_backward_withhold(const lm_gated_backward_args *
 /*
  * A weight [n][k] as whole numbers of -8 .. 7 and one f32 scale for each row
  * and `group` consecutive k:  w[i][j] = q[i][j] * s[i][j / group].
- *   packed   device, ceil(n / 16) * ceil(k / 64) tiles of 512 bytes, 16-byte
- *            aligned; a tile is 16 rows by 64 k, tiles run along k first.
+ *   packed   device, 16-byte aligned, blocks of 128 rows by 64 k: ceil(n / 128) *
+ *            ceil(k / 64) blocks of 4096 bytes, along k first.  A block is eight
+ *            tiles of 16 rows, 512 bytes each.
  *            Bytes 16 l .. 16 l + 15 of a tile are four little-endian u32 of
  *            eight k each: row l / 4 at k = 8 (l % 4) .. + 7 and 32 + 8 (l % 4) .. + 7,
  *            then row l / 4 + 8 at the same.  From a u32's lowest nibble the eight
- *            are in order 0 2 4 6 1 3 5 7; a nibble is q + 8.  Places past n or k hold q = 0.
- *   scale    device, [ceil(n / 16)][ceil(k / group)][16] f32, 16-byte aligned
+ *            are in order 0 2 4 6 1 3 5 7; a nibble is q + 8.  Places past n or k
+ *            hold q = 0.
+ *   scale    device, [ceil(n / 128)][ceil(k / group)][128] f32, 16-byte aligned
  *   group    32, 64 or 128
  */
 typedef struct lm_weight4 {
@@ -899,6 +901,9 @@ lm_status lm_weight4_values(const lm_weight4 *w, void *out, int64_t row_stride, 
 lm_status lm_linear4_workspace_size(const lm_linear_args *args, const lm_weight4 *w, size_t *bytes);
 lm_status lm_linear4(const lm_linear_args *args, const lm_weight4 *w, void *workspace, size_t workspace_bytes,
                      lm_stream_t stream);
+/* Fault injection for tests of the bounded waits, as lm_debug_linear_withhold. */
+lm_status lm_debug_linear4_withhold(const lm_linear_args *args, const lm_weight4 *w, void *workspace,
+                                    size_t workspace_bytes, int64_t withheld_cta, uint64_t wait_ns, lm_stream_t stream);
 /* 1 where a call with these sizes expands the weight, 0 where it reads the 4 bits in its products. */
 int lm_linear4_expands(int64_t rows, int64_t n, int64_t k);
 

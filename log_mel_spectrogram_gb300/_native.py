@@ -162,6 +162,8 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.lm_linear4_workspace_size.restype = ctypes.c_int
     L.lm_linear4.argtypes = [vp, vp, vp, sz, vp]
     L.lm_linear4.restype = ctypes.c_int
+    L.lm_debug_linear4_withhold.argtypes = [vp, vp, vp, sz, i64, ctypes.c_uint64, vp]
+    L.lm_debug_linear4_withhold.restype = ctypes.c_int
     L.lm_linear4_expands.argtypes = [i64, i64, i64]
     L.lm_linear4_expands.restype = ctypes.c_int
     L.lm_beam_step_workspace_size.argtypes = [vp, vp]

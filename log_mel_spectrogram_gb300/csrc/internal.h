@@ -102,10 +102,11 @@ struct Resident {
 };
 lm_status resident_clusters(const DeviceInfo &dev, Resident *r);
 
-// What the kernels of linear.cu, gated.cu and kv_attend.cu have reported on the current device since it was last
+// What the kernels of linear.cu, linear4.cu, gated.cu and kv_attend.cu have reported on the current device since it was last
 // cleared, added to *value.
 lm_status linear_error(uint32_t *value, bool clear, cudaStream_t stream);
 lm_status gated_error(uint32_t *value, bool clear, cudaStream_t stream);
+lm_status linear4_error(uint32_t *value, bool clear, cudaStream_t stream);
 lm_status attend_error(uint32_t *value, bool clear, cudaStream_t stream);
 
 // --- log_mel_from_stft -----------------------------------------------------

@@ -372,9 +372,9 @@ PyObject *new_weight4(int64_t n, int64_t k, int group, int dev, lm_weight4 *c, T
   c->group = group;
   size_t pb = 0, sb = 0;
   if (const int rc = lm_weight4_size(c, &pb, &sb); rc != LM_OK) return status(rc);
-  const int64_t ntiles = (n + 15) / 16, ktiles = (k + 63) / 64, groups = (k + group - 1) / group;
-  *packed = make({ntiles, ktiles, 512}, at::kByte, dev);
-  *scale = make({ntiles, groups, 16}, at::kFloat, dev);
+  const int64_t blocks = (n + 127) / 128, ktiles = (k + 63) / 64, groups = (k + group - 1) / group;
+  *packed = make({blocks, ktiles, 4096}, at::kByte, dev);
+  *scale = make({blocks, groups, 128}, at::kFloat, dev);
   c->packed = packed->data_ptr();
   c->scale = scale->data_ptr<float>();
   return nullptr;

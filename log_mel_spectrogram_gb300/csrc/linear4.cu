@@ -12,6 +12,7 @@
 // Many rows: products bound it, and the legacy matrix instruction with them.  The values are expanded into
 // the workspace, rounded to x's type, and linear.cu's kernel takes them.
 #include <climits>
+#include <type_traits>
 
 #include "activate.cuh"
 #include "half.cuh"
@@ -19,11 +20,15 @@
 #include "mma.cuh"
 #include "operand.cuh"
 #include "pdl.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+#include "waits.cuh"
 
 namespace lm {
 namespace {
 
-constexpr int kTileBytes = 512;  // 16 rows by 64 k
+constexpr int kTileBytes = 512;    // 16 rows by 64 k
+constexpr int kBlockBytes = 4096;  // eight of them: 128 rows by 64 k
 
 struct Weight {
   const uint32_t *packed;
@@ -37,11 +42,12 @@ __host__ __device__ inline int64_t up(int64_t a, int64_t b) { return (a + b - 1)
 // The word of `packed` that holds row i, k j .. j + 7 (j a multiple of 8).
 __device__ __forceinline__ int64_t word_at(const Weight &w, int64_t i, int64_t j) {
   const int r = static_cast<int>(i % 16), c = static_cast<int>(j % 64);
-  return (i / 16 * w.ktiles + j / 64) * (kTileBytes / 4) + (r % 8 * 4 + c % 32 / 8) * 4 + r / 8 * 2 + c / 32;
+  return ((i / 128 * w.ktiles + j / 64) * 8 + i % 128 / 16) * (kTileBytes / 4) + (r % 8 * 4 + c % 32 / 8) * 4 + r / 8 * 2 +
+         c / 32;
 }
 
 __device__ __forceinline__ int64_t scale_at(const Weight &w, int64_t i, int64_t g) {
-  return (i / 16 * w.groups + g) * 16 + i % 16;
+  return (i / 128 * w.groups + g) * 128 + i % 128;
 }
 
 // q of k j + e in a word.
@@ -130,11 +136,13 @@ struct ProductParams {
   void *out;
   int64_t x_group, x_row, res_row, out_row;
   int32_t rows, group_rows, ntiles, parts;  // parts: warps that share out a tile's k
+  int32_t group_tiles;  // log2 of a group's tiles of k
   int32_t bias_f32, out_f32, act;
   float scale;
 };
 
-constexpr int kWarps = 8;
+constexpr int kMostWarps = 16;  // of a CTA
+constexpr int kSide = 2;  // tiles of 16 outputs that a warp works on
 
 __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) { return (w & mask) | bits; }
 
@@ -176,6 +184,10 @@ __device__ __forceinline__ uint4 load_once(const uint32_t *p) {
   return v;
 }
 
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 // Eight elements of a row from k on, zeros past its end.
 template <typename T>
 __device__ __forceinline__ uint4 load8(const T *row, int k, int end) {
@@ -203,105 +215,543 @@ __device__ __forceinline__ void put(const ProductParams &p, float s, int row, in
 }
 
 // NT: blocks of eight rows of x; blockIdx.y counts such tiles.  SMALL: groups of 32, two to a tile.
+// A warp has two tiles of 16 outputs side by side, which share its operands of x and give it products
+// that do not wait for one another.
 template <typename T, int NT, bool SMALL>
-__global__ void __launch_bounds__(32 * kWarps) product_kernel(const ProductParams p) {
-  constexpr int AHEAD = NT <= 2 ? 4 : 2;  // tiles whose bytes are on their way
+__global__ void __launch_bounds__(32 * kMostWarps, 1) product_kernel(const ProductParams p) {
+  constexpr int AHEAD = NT == 1 ? 4 : 2;  // tiles whose bytes are on their way
   constexpr int SCALES = SMALL ? 2 : 1;
-  __shared__ float sums[kWarps][8 * NT][16 + 1];
+  constexpr int PITCH = 16 * kSide + 1;
+  extern __shared__ float sums[];  // [warps][8 * NT][PITCH]
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, r = lane / 4, c = lane % 4;
-  const int part = warp % p.parts, per = kWarps / p.parts;
-  const int tile = static_cast<int>(blockIdx.x) * per + warp / p.parts;
+  const int part = warp % p.parts, per = static_cast<int>(blockDim.x) / 32 / p.parts;
+  const int tile = (static_cast<int>(blockIdx.x) * per + warp / p.parts) * kSide;
   const int row0 = static_cast<int>(blockIdx.y) * 8 * NT, k = static_cast<int>(p.w.k);
   const bool any = tile < p.ntiles;
   const int begin = any ? static_cast<int>(static_cast<int64_t>(p.w.ktiles) * part / p.parts) : 0;
   const int end = any ? static_cast<int>(static_cast<int64_t>(p.w.ktiles) * (part + 1) / p.parts) : 0;
   pdl_launch();
   pdl_wait();
-  const uint32_t *const packed = p.w.packed + static_cast<int64_t>(tile) * p.w.ktiles * (kTileBytes / 4) + lane * 4;
-  const float *const scales = p.w.scale + static_cast<int64_t>(tile) * p.w.groups * 16 + r;
+  // (A row past the last reads the first; its sums are not written.)
+  const uint32_t *const packed =
+      p.w.packed + (static_cast<int64_t>(tile / 8) * p.w.ktiles * 8 + tile % 8) * (kTileBytes / 4) + lane * 4;
+  const float *const scales = p.w.scale + static_cast<int64_t>(tile / 8) * p.w.groups * 128 + tile % 8 * 16 + r;
   const T *x[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int row = row0 + 8 * t + r;
-    x[t] = row < p.rows ? static_cast<const T *>(p.x) + row / p.group_rows * p.x_group + row % p.group_rows * p.x_row
-                        : nullptr;
+    const int row = row0 + 8 * t + r < p.rows ? row0 + 8 * t + r : row0;
+    x[t] = static_cast<const T *>(p.x) + row / p.group_rows * p.x_group + row % p.group_rows * p.x_row + 8 * c;
   }
-  float total[NT][4];
+  float total[NT][kSide][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) total[t][j] = 0.0f;
-
-  uint4 w[AHEAD];
-  float s[AHEAD][SCALES][2];
-  auto fetch = [&](int u, int kt) {
-    w[u] = load_once(packed + static_cast<int64_t>(kt) * (kTileBytes / 4));
+    for (int m = 0; m < kSide; ++m)
 #pragma unroll
-    for (int h = 0; h < SCALES; ++h) {
-      int g = SMALL ? 2 * kt + h : kt * 64 / p.w.group;
-      if (SMALL && g >= p.w.groups) g = p.w.groups - 1;  // (its half of the tile is zeros)
-      s[u][h][0] = scales[g * 16];
-      s[u][h][1] = scales[g * 16 + 8];
+      for (int j = 0; j < 4; ++j) total[t][m][j] = 0.0f;
+
+  uint4 w[AHEAD][kSide];
+  float s[AHEAD][kSide][SCALES][2];
+  auto fetch = [&](int u, int kt) {
+#pragma unroll
+    for (int m = 0; m < kSide; ++m) {
+      w[u][m] = load_once(packed + m * (kTileBytes / 4) + static_cast<int64_t>(kt) * (kBlockBytes / 4));
+#pragma unroll
+      for (int h = 0; h < SCALES; ++h) {
+        int g = SMALL ? 2 * kt + h : kt >> p.group_tiles;
+        if (SMALL && g >= p.w.groups) g = p.w.groups - 1;  // (its half of the tile is zeros)
+        s[u][m][h][0] = scales[m * 16 + static_cast<int64_t>(g) * 128];
+        s[u][m][h][1] = scales[m * 16 + static_cast<int64_t>(g) * 128 + 8];
+      }
     }
+  };
+  uint4 b[2][NT][2];
+  auto fetch_x = [&](uint4 (&to)[NT][2], int kt) {
+    const bool whole = (kt + 1) * 64 <= k;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        to[t][h] = whole ? *reinterpret_cast<const uint4 *>(x[t] + kt * 64 + 32 * h)
+                         : load8<T>(x[t] - 8 * c, kt * 64 + 32 * h + 8 * c, k);
   };
 #pragma unroll
   for (int u = 0; u < AHEAD; ++u)
     if (begin + u < end) fetch(u, begin + u);
+  if (begin < end) fetch_x(b[0], begin);
   for (int base = begin; base < end; base += AHEAD) {
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       const int kt = base + u;
       if (kt >= end) break;
-      uint32_t v[4][4];  // words: row r, the tile's first and second half of k; row r + 8
-      widen<T>(w[u].x, v[0]);
-      widen<T>(w[u].y, v[1]);
-      widen<T>(w[u].z, v[2]);
-      widen<T>(w[u].w, v[3]);
-      float f[SCALES][2];
+      if (kt + 1 < end) fetch_x(b[(u + 1) % 2], kt + 1);
 #pragma unroll
-      for (int h = 0; h < SCALES; ++h) {
-        f[h][0] = s[u][h][0];
-        f[h][1] = s[u][h][1];
-      }
-      if (kt + AHEAD < end) fetch(u, kt + AHEAD);
+      for (int m = 0; m < kSide; ++m) {
+        uint32_t v[4][4];  // words: row r, the tile's first and second half of k; row r + 8
+        widen<T>(w[u][m].x, v[0]);
+        widen<T>(w[u][m].y, v[1]);
+        widen<T>(w[u][m].z, v[2]);
+        widen<T>(w[u][m].w, v[3]);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < NT; ++t) {
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 b = load8<T>(x[t], kt * 64 + 32 * h + 8 * c, k);
-          const uint32_t a0[4] = {v[h][0], v[h + 2][0], v[h][1], v[h + 2][1]};
-          const uint32_t a1[4] = {v[h][2], v[h + 2][2], v[h][3], v[h + 2][3]};
-          mma16816<T>(d, a0, b.x, b.y);
-          mma16816<T>(d, a1, b.z, b.w);
-          if (SMALL || h == 1) {
-            const int g = SMALL ? h : 0;
-            total[t][0] = fmaf(f[g][0], d[0], total[t][0]);
-            total[t][1] = fmaf(f[g][0], d[1], total[t][1]);
-            total[t][2] = fmaf(f[g][1], d[2], total[t][2]);
-            total[t][3] = fmaf(f[g][1], d[3], total[t][3]);
-            d[0] = d[1] = d[2] = d[3] = 0.0f;
+          for (int h = 0; h < 2; ++h) {
+            const uint4 &o = b[u % 2][t][h];
+            const uint32_t a0[4] = {v[h][0], v[h + 2][0], v[h][1], v[h + 2][1]};
+            const uint32_t a1[4] = {v[h][2], v[h + 2][2], v[h][3], v[h + 2][3]};
+            mma16816<T>(d, a0, o.x, o.y);
+            mma16816<T>(d, a1, o.z, o.w);
+            if (SMALL || h == 1) {
+              const float *const f = s[u][m][SMALL ? h : 0];
+              total[t][m][0] = fmaf(f[0], d[0], total[t][m][0]);
+              total[t][m][1] = fmaf(f[0], d[1], total[t][m][1]);
+              total[t][m][2] = fmaf(f[1], d[2], total[t][m][2]);
+              total[t][m][3] = fmaf(f[1], d[3], total[t][m][3]);
+              d[0] = d[1] = d[2] = d[3] = 0.0f;
+            }
           }
         }
       }
+      if (kt + AHEAD < end) fetch(u, kt + AHEAD);
     }
   }
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    sums[warp][8 * t + 2 * c][r] = total[t][0];
-    sums[warp][8 * t + 2 * c + 1][r] = total[t][1];
-    sums[warp][8 * t + 2 * c][r + 8] = total[t][2];
-    sums[warp][8 * t + 2 * c + 1][r + 8] = total[t][3];
-  }
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int m = 0; m < kSide; ++m) {
+      float *const to = sums + (warp * 8 * NT + 8 * t + 2 * c) * PITCH + 16 * m + r;
+      to[0] = total[t][m][0];
+      to[PITCH] = total[t][m][1];
+      to[8] = total[t][m][2];
+      to[PITCH + 8] = total[t][m][3];
+    }
   __syncthreads();
-  const int wide = 16 * per, rows = min(8 * NT, p.rows - row0);
+  constexpr int WIDE = 16 * kSide;
+  const int wide = WIDE * per, rows = min(8 * NT, p.rows - row0);
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * wide;
-  for (int i = threadIdx.x; i < rows * wide; i += 32 * kWarps) {
+  for (int i = threadIdx.x; i < rows * wide; i += blockDim.x) {
     const int row = i / wide, at = i % wide;
     if (n0 + at >= p.w.n) continue;
     float sum = 0.0f;
-    for (int q = 0; q < p.parts; ++q) sum += sums[at / 16 * p.parts + q][row][at % 16];
+    for (int q = 0; q < p.parts; ++q) sum += sums[((at / WIDE * p.parts + q) * 8 * NT + row) * PITCH + at % WIDE];
     put<T>(p, sum, row0 + row, static_cast<int>(n0) + at);
+  }
+}
+
+// ---- more rows: tcgen05 ----
+
+constexpr int kBk = 64;
+constexpr int kLanes = 128;
+constexpr int kOperandBytes = kLanes * kBk * 2;
+constexpr int kMaxBn = 128, kTurnBn = 64;     // up to kTurnBn columns, the adding warps' groups take turns
+constexpr int kMaxStages = 8, kMaxSums = 8, kMaxRaw = 16;
+constexpr int kScaleSlots = 32;                // ... of 512 bytes: a stage's scales take one, or two of groups of 32
+constexpr int kWiden = 8, kAdd = 8;            // warps
+// A stage's way through a warp takes a few hundred cycles of waiting for one another.  So groups of warps widen
+// several stages at once, in turn, and (of up to 64 columns) two groups add up two sums.  A wait tells whether the phase
+// before was the last to end, not which one it was; a group's own last fill shows that what came as
+// many fills before as there are stages has been used, which is enough where there are no more groups than stages.
+constexpr int widen_groups(bool turns) { return turns ? 4 : 2; }
+constexpr int kThreads = 32 * (4 + kWiden + kAdd);
+
+struct TileParams {
+  ProductParams o;                             // bias, residual, out, ...; rows: of one group
+  int32_t bn, stages, sums, raw, blocks, tmem_cols, sum_cols, sum_planes;
+  int32_t lane_tiles, col_tiles, tiles, splits;
+  uint32_t idesc;
+  uint32_t *err;
+  uint64_t wait_ns;
+  int32_t withheld;
+};
+
+__device__ uint32_t g_linear4_error;
+
+struct alignas(16) Barriers {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t sum_full[kMaxSums], sum_empty[kMaxSums];
+  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
+  uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+};
+
+struct Place {
+  int group, lane_tile, col0;
+};
+
+__device__ __forceinline__ Place place_at(const TileParams &p, int t) {
+  Place o;
+  const int per = p.lane_tiles * p.col_tiles;
+  o.group = t / per;
+  const int u = t - o.group * per;
+  o.lane_tile = u / p.col_tiles;  // a tile of W's columns go round inside: its bytes come from L2
+  o.col0 = (u - o.lane_tile * p.col_tiles) * p.bn;
+  return o;
+}
+
+// A ring's position.
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n, int by = 1) {
+    at += by;
+    while (at >= n) {
+      at -= n;
+      phase ^= 1;
+    }
+  }
+};
+
+// The sums of a tile's columns `first`, first + step, ... of `cols` at lane `at` of a [column][lane] array, or of the
+// arrays of a cluster's CTAs, into outputs.
+template <typename T, int ACT, bool SPLIT>
+__device__ __forceinline__ void finish(const TileParams &p, uint32_t sums, const Place &tile, int at, int first, int step,
+                                       int cols) {
+  const ProductParams &o = p.o;
+  const int n = tile.lane_tile * kLanes + at;
+  if (n >= o.w.n) return;
+  float bias = 0.0f;
+  if (o.bias) bias = o.bias_f32 ? static_cast<const float *>(o.bias)[n] : to_f32(static_cast<const T *>(o.bias)[n]);
+#pragma unroll 4
+  for (int c = first; c < cols; c += step) {
+    const uint32_t from = sums + static_cast<uint32_t>(c * kLanes + at) * 4;
+    float z = 0.0f;
+    if (SPLIT) {
+      uint32_t v[kMaxSplits];
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r)
+        if (r < p.splits) v[r] = ld_dsmem_u32(from, static_cast<uint32_t>(r));
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r)
+        if (r < p.splits) z += __uint_as_float(v[r]);
+      if (p.bn <= kTurnBn) {
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r)
+          if (r < p.splits) v[r] = ld_dsmem_u32(from + static_cast<uint32_t>(p.bn * kLanes) * 4, static_cast<uint32_t>(r));
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r)
+          if (r < p.splits) z += __uint_as_float(v[r]);
+      }
+    } else {
+      z = lds_f32(from);
+      if (p.bn <= kTurnBn) z += lds_f32(from + static_cast<uint32_t>(p.bn * kLanes) * 4);
+    }
+    const int64_t row = static_cast<int64_t>(tile.group) * o.rows + tile.col0 + c;
+    float y = o.scale * activate<ACT>(z + bias);
+    if (o.residual) y += to_f32(static_cast<const T *>(o.residual)[row * o.res_row + n]);
+    if (o.out_f32) {
+      static_cast<float *>(o.out)[row * o.out_row + n] = y;
+    } else {
+      static_cast<T *>(o.out)[row * o.out_row + n] = from_f32<T>(y);
+    }
+  }
+}
+
+template <typename T, bool SPLIT>
+__device__ __forceinline__ void finish_any(const TileParams &p, uint32_t sums, const Place &tile, int at, int first,
+                                           int step, int cols) {
+  switch (p.o.act) {
+    case LM_ACT_RELU: finish<T, LM_ACT_RELU, SPLIT>(p, sums, tile, at, first, step, cols); break;
+    case LM_ACT_GELU: finish<T, LM_ACT_GELU, SPLIT>(p, sums, tile, at, first, step, cols); break;
+    case LM_ACT_GELU_TANH: finish<T, LM_ACT_GELU_TANH, SPLIT>(p, sums, tile, at, first, step, cols); break;
+    case LM_ACT_SILU: finish<T, LM_ACT_SILU, SPLIT>(p, sums, tile, at, first, step, cols); break;
+    default: finish<T, LM_ACT_NONE, SPLIT>(p, sums, tile, at, first, step, cols); break;
+  }
+}
+
+// As linear.cu's kernel, W along the lanes, but for W's tiles: bulk copies bring their packed bytes and scales, eight
+// warps turn the bytes into the whole numbers q in the operand's swizzled layout, and the tensor memory holds one sum
+// of q x for each stage (two where groups are of 32); eight more warps multiply it by the lanes' scales and add
+// it up in registers, 32 bits, so that no scaled weight is ever rounded.
+// TURNS: up to kTurnBn columns.
+template <typename T, bool SPLIT, bool SMALL, bool TURNS>
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap col_map, const TileParams p) {
+  constexpr int UNITS = SMALL ? 2 : 1;  // sums a stage
+  constexpr int GROUPS = widen_groups(TURNS), GROUP_WARPS = kWiden / GROUPS, TILES = 8 / GROUP_WARPS;
+  constexpr int WIDEST = TURNS ? kTurnBn : kMaxBn / 2;  // columns of an adding warp
+  constexpr int SCALE_BYTES = 512 * UNITS, SCALES = kScaleSlots / UNITS;
+  extern __shared__ __align__(1024) uint8_t ring[];
+  const int stage_bytes = kOperandBytes + p.bn * 128;
+  uint8_t *const raw = ring + p.stages * stage_bytes;
+  uint8_t *const scales = raw + p.raw * kBlockBytes;
+  float *const sums = reinterpret_cast<float *>(scales + kScaleSlots * 512);  // [sum_planes][bn][kLanes]
+  Barriers &b = *reinterpret_cast<Barriers *>(sums + p.sum_planes * p.bn * kLanes);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = SPLIT ? static_cast<int>(blockIdx.x) / p.splits : static_cast<int>(blockIdx.x);
+  const int step = SPLIT ? p.tiles : static_cast<int>(gridDim.x);
+  const int k_begin = SPLIT ? static_cast<int>(static_cast<int64_t>(p.blocks) * rank / p.splits) : 0;
+  const int k_end = SPLIT ? static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / p.splits) : p.blocks;
+  const Weight &w = p.o.w;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&b.full[i], 1 + GROUP_WARPS + (i == 0 && static_cast<int>(blockIdx.x) == p.withheld ? 1 : 0));
+      mbar_init(&b.empty[i], 1);
+    }
+    for (int i = 0; i < p.sums; ++i) {
+      mbar_init(&b.sum_full[i], 1);
+      mbar_init(&b.sum_empty[i], TURNS ? kAdd / 2 : kAdd);
+    }
+    for (int i = 0; i < p.raw; ++i) {
+      mbar_init(&b.raw_full[i], 1);
+      mbar_init(&b.raw_empty[i], GROUP_WARPS);
+    }
+    for (int i = 0; i < SCALES; ++i) {
+      mbar_init(&b.scale_full[i], 1);
+      mbar_init(&b.scale_empty[i], TURNS ? kAdd / 2 : kAdd);
+    }
+    mbar_init(&b.drain, 1);
+    b.abort = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&col_map);
+  }
+  if (warp == 2) tmem_alloc<false>(&b.tmem, static_cast<uint32_t>(p.tmem_cols));
+  tcgen05_fence_before();
+  __syncthreads();
+  __syncwarp();
+  pdl_launch();
+  pdl_wait();
+  tcgen05_fence_after();
+  const uint32_t tmem = b.tmem;
+  volatile int *const abort = &b.abort;
+
+  if (warp == 0) {  // tiles of x
+    Ring s;
+    int fills = 0;
+    bool ok = true;
+    for (int t = first; t < p.tiles && ok; t += step) {
+      const Place tile = place_at(p, t);
+      for (int kb = k_begin; kb < k_end; ++kb) {
+        if (fills >= p.stages) ok = mbar_wait_warp(&b.empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&b.full[s.at], static_cast<uint32_t>(p.bn * 128));
+          tma_load_3d<false>(ring + s.at * stage_bytes + kOperandBytes, &col_map, kb * kBk, tile.col0, tile.group,
+                             smem_u32(&b.full[s.at]));
+        }
+        __syncwarp();
+        ++fills;
+        s.next(p.stages);
+      }
+    }
+    // No copy outlives the CTA, whatever the other warps did.
+    for (int f = fills > p.stages ? fills - p.stages : 0; f < fills; ++f)
+      if (!mbar_drain(&b.full[f % p.stages], (f / p.stages) & 1, p.wait_ns, p.err)) break;
+  } else if (warp == 3) {  // packed bytes and scales
+    Ring s, c;
+    int fills = 0;
+    bool ok = true;
+    for (int t = first; t < p.tiles && ok; t += step) {
+      const int lane_tile = place_at(p, t).lane_tile;
+      const uint8_t *const bytes =
+          reinterpret_cast<const uint8_t *>(w.packed) + static_cast<int64_t>(lane_tile) * w.ktiles * kBlockBytes;
+      const float *const factors = w.scale + static_cast<int64_t>(lane_tile) * w.groups * kLanes;
+      for (int kb = k_begin; kb < k_end; ++kb) {
+        if (fills >= p.raw) ok = mbar_wait_warp(&b.raw_empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err);
+        if (ok && fills >= SCALES) ok = mbar_wait_warp(&b.scale_empty[c.at], c.phase ^ 1, p.wait_ns, abort, p.err);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&b.raw_full[s.at], kBlockBytes);
+          bulk_g2s_plain(raw + s.at * kBlockBytes, bytes + static_cast<int64_t>(kb) * kBlockBytes, kBlockBytes,
+                         &b.raw_full[s.at]);
+          const int g = SMALL ? 2 * kb : kb >> p.o.group_tiles;
+          // (The last tile of groups of 32 may have one.)
+          const uint32_t size = SMALL && g + 1 < w.groups ? 1024u : 512u;
+          mbar_arrive_expect_tx(&b.scale_full[c.at], size);
+          bulk_g2s_plain(scales + c.at * SCALE_BYTES, factors + static_cast<int64_t>(g) * kLanes, size, &b.scale_full[c.at]);
+        }
+        __syncwarp();
+        ++fills;
+        s.next(p.raw);
+        c.next(SCALES);
+      }
+    }
+    for (int f = fills > p.raw ? fills - p.raw : 0; f < fills; ++f)
+      if (!mbar_drain(&b.raw_full[f % p.raw], (f / p.raw) & 1, p.wait_ns, p.err)) break;
+    for (int f = fills > SCALES ? fills - SCALES : 0; f < fills; ++f)
+      if (!mbar_drain(&b.scale_full[f % SCALES], (f / SCALES) & 1, p.wait_ns, p.err)) break;
+  } else if (warp == 1) {  // products
+    Ring s, a;
+    int units = 0;
+    bool ok = true;
+    const uint32_t ring_a = smem_u32(ring);
+    for (int t = first; t < p.tiles && ok; t += step) {
+      for (int kb = k_begin; kb < k_end && ok; ++kb) {
+        ok = mbar_wait_warp(&b.full[s.at], s.phase, p.wait_ns, abort, p.err);
+        if (!ok) break;
+        const uint64_t da = smem_desc_k128(ring_a + s.at * stage_bytes);
+        const uint64_t dc = smem_desc_k128(ring_a + s.at * stage_bytes + kOperandBytes);
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          if (ok && units >= p.sums) ok = mbar_wait_warp(&b.sum_empty[a.at], a.phase ^ 1, p.wait_ns, abort, p.err);
+          tcgen05_fence_after();
+          if (ok && elect_one()) {
+            const uint32_t d = tmem + static_cast<uint32_t>(a.at * p.sum_cols);
+#pragma unroll
+            for (int i = 0; i < kBk / 16 / UNITS; ++i) {
+              const int k16 = u * (kBk / 16 / UNITS) + i;
+              tcgen05_mma_f16<false>(d, da + 2 * k16, dc + 2 * k16, p.idesc, i > 0);
+            }
+            tcgen05_commit<false>(&b.sum_full[a.at]);
+            if (u == UNITS - 1) tcgen05_commit<false>(&b.empty[s.at]);
+          }
+          __syncwarp();
+          ++units;
+          a.next(p.sums);
+        }
+        s.next(p.stages);
+      }
+    }
+    if (!ok) {  // products in flight end before the tensor memory is given back
+      if (elect_one()) tcgen05_commit<false>(&b.drain);
+      mbar_drain(&b.drain, 0, p.wait_ns, p.err);
+    }
+  } else if (warp >= 4 && warp < 4 + kWiden) {
+    // Of a tile of 16 rows lane 4 r + c has rows r and r + 8 at k 8 c .. + 7 and 32 + 8 c .. + 7, chunks c
+    // and 4 + c of 16 bytes in a row of 128.  Odd rows store their second chunk first: eight lanes then
+    // meet every bank once.
+    const int e = warp - 4, group = e / GROUP_WARPS, r = lane / 4, c = lane % 4, odd = r & 1;
+    const int tile0 = e % GROUP_WARPS * TILES;
+    const uint32_t low = static_cast<uint32_t>((16 * tile0 + r) * 128 + (((odd ? 4 + c : c) ^ r) * 16));
+    const uint32_t high = static_cast<uint32_t>((16 * tile0 + r) * 128 + (((odd ? c : 4 + c) ^ r) * 16));
+    const uint32_t ring_a = smem_u32(ring);
+    const uint4 *const from = reinterpret_cast<const uint4 *>(raw + tile0 * kTileBytes) + lane;
+    const int mine = first < p.tiles ? (p.tiles - first + step - 1) / step * (k_end - k_begin) : 0;
+    Ring s, q;
+    s.next(p.stages, group);
+    q.next(p.raw, group);
+    for (int i = group; i < mine; i += GROUPS) {
+      if (!mbar_wait_warp(&b.raw_full[q.at], q.phase, p.wait_ns, abort, p.err)) break;
+      uint4 v[TILES];
+#pragma unroll
+      for (int j = 0; j < TILES; ++j) v[j] = from[q.at * (kBlockBytes / 16) + j * (kTileBytes / 16)];
+      if (i >= p.stages && !mbar_wait_warp(&b.empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err)) break;
+      const uint32_t to = ring_a + s.at * stage_bytes;
+#pragma unroll
+      for (int j = 0; j < TILES; ++j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // rows r and r + 8
+          uint32_t x[4], y[4];
+          widen<T>(h ? v[j].z : v[j].x, x);
+          widen<T>(h ? v[j].w : v[j].y, y);
+          const uint32_t at = to + j * 2048 + h * 1024;
+          sts_v4(at + low, odd ? y[0] : x[0], odd ? y[1] : x[1], odd ? y[2] : x[2], odd ? y[3] : x[3]);
+          sts_v4(at + high, odd ? x[0] : y[0], odd ? x[1] : y[1], odd ? x[2] : y[2], odd ? x[3] : y[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&b.full[s.at]);
+        mbar_arrive(&b.raw_empty[q.at]);
+      }
+      s.next(p.stages, GROUPS);
+      q.next(p.raw, GROUPS);
+    }
+  } else if (warp >= 4 + kWiden) {
+    const int e = warp - 4 - kWiden, quarter = e % 4;
+    const int wide = TURNS ? p.bn : p.bn / 2, col = TURNS ? 0 : e / 4 * wide;  // this warp's columns
+    const int turn = TURNS ? e / 4 : 0;                                       // ... and stages
+    constexpr int every = TURNS ? 2 : 1;
+    const uint32_t base = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + static_cast<uint32_t>(col);
+    const int at = 32 * quarter + lane;
+    const float *const factor = reinterpret_cast<const float *>(scales) + at;
+    float *const mine = sums + turn * p.bn * kLanes + at;
+    Ring a, q;
+    a.next(p.sums, turn * UNITS);
+    q.next(SCALES, turn);
+    int fill = turn, past = 0;  // the stage, counted over all tiles; those of the tiles before
+    bool ok = true;
+    // (Warps that have given up still come to the barriers.)
+    for (int t = first; t < p.tiles; t += step) {
+      const Place tile = place_at(p, t);
+      f32x2 total[WIDEST / 2];
+#pragma unroll
+      for (int i = 0; i < WIDEST / 2; ++i) total[i] = both(0.0f);
+      const int end = past + (k_end - k_begin);
+      for (; fill < end && ok; fill += every) {
+        const int kb = k_begin + fill - past;
+        ok = mbar_wait_warp(&b.scale_full[q.at], q.phase, p.wait_ns, abort, p.err);
+        if (!ok) break;
+        f32x2 f[UNITS];
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          // (The second group that a tile lacks has zeros for weights.)
+          const bool there = u == 0 || 2 * kb + u < w.groups;
+          f[u] = both(there ? factor[q.at * (SCALE_BYTES / 4) + u * kLanes] : 0.0f);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.scale_empty[q.at]);
+        q.next(SCALES, every);
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          if (ok) ok = mbar_wait_warp(&b.sum_full[a.at], a.phase, p.wait_ns, abort, p.err);
+          if (!ok) break;
+          tcgen05_fence_after();
+          const uint32_t d = base + static_cast<uint32_t>(a.at * p.sum_cols);
+#pragma unroll
+          for (int c = 0; c < WIDEST; c += 16) {
+            if (c < wide) {
+              uint32_t r[16];
+              tmem_ld16(d + c, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; j += 2)
+                total[(c + j) / 2] = fma2(f[u], pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), total[(c + j) / 2]);
+            }
+          }
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b.sum_empty[a.at]);
+          a.next(p.sums, u == UNITS - 1 ? 1 + (every - 1) * UNITS : 1);
+        }
+      }
+      past = end;
+      // Through shared memory: outputs by a short loop.  (From registers, every column a copy of the epilogue,
+      // the instructions' way from L2 took microseconds.)
+      if (!SPLIT && TURNS) asm volatile("bar.sync 1, 256;" ::: "memory");  // the last tile's sums have been read
+#pragma unroll
+      for (int c = 0; c < WIDEST; c += 2)
+        if (c < wide) {
+          const float2 v = unpair(total[c / 2]);
+          mine[(col + c) * kLanes] = v.x;
+          mine[(col + c + 1) * kLanes] = v.y;
+        }
+      if (!SPLIT) {
+        if (TURNS) {
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+        } else {
+          __syncwarp();
+        }
+        if (ok && !*abort)
+          finish_any<T, false>(p, smem_u32(sums), tile, at, TURNS ? turn : col, every,
+                               min(TURNS ? p.bn : col + wide, p.o.rows - tile.col0));
+      }
+    }
+  }
+
+  __syncwarp();
+  if (SPLIT) {
+    __syncthreads();
+    cluster_sync_all();
+    if (!*abort && first < p.tiles) {
+      const Place tile = place_at(p, first);
+      // Columns are shared out over the cluster's CTAs, and over groups of 128 threads.
+      const int part = static_cast<int>(threadIdx.x) / kLanes * p.splits + rank;
+      finish_any<T, true>(p, smem_u32(sums), tile, threadIdx.x % kLanes, part, kThreads / kLanes * p.splits,
+                          min(p.bn, p.o.rows - tile.col0));
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its sums
+  }
+  tcgen05_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort) atomicOr(&g_linear4_error, kErrMbarTimeout);
+  if (warp == 2) {
+    tcgen05_fence_after();
+    tmem_dealloc<false>(tmem, static_cast<uint32_t>(p.tmem_cols));
   }
 }
 
@@ -319,8 +769,11 @@ lm_status view(const lm_weight4 *a, Weight *w) {
   return LM_OK;
 }
 
+// Rows that the warps' products take.
+constexpr int64_t kFewRows = 16;
+
 // From this many rows on the products cost more than expanding the weight.
-bool expands(int64_t rows, int64_t, int64_t) { return rows > 128; }
+bool expands(int64_t rows, int64_t, int64_t) { return rows > 512; }
 
 // ... of a weight with contents.
 lm_status whole(const Weight &w) {
@@ -330,7 +783,7 @@ lm_status whole(const Weight &w) {
 
 template <typename T, bool GIVEN>
 lm_status fill(const Weight &w, const T *src, int64_t row_stride, const float *scales, cudaStream_t s) {
-  const int64_t units = up(w.n, 16) * 16 * w.groups;
+  const int64_t units = up(w.n, 128) * 128 * w.groups;
   if (up(units, 8) > INT_MAX) return LM_ERR_UNSUPPORTED;
   return launch_dependent(fill_kernel<T, GIVEN>, dim3(static_cast<unsigned>(up(units, 8))), 256, 0, s, 1, w,
                           const_cast<uint32_t *>(w.packed), const_cast<float *>(w.scale), src, row_stride, scales, units);
@@ -351,9 +804,9 @@ extern "C" lm_status lm_weight4_size(const lm_weight4 *a, size_t *packed_bytes, 
   lm::Weight w;
   if (!packed_bytes || !scale_bytes) return LM_ERR_INVALID_ARG;
   if (lm_status st = lm::view(a, &w); st != LM_OK) return st;
-  const size_t ntiles = static_cast<size_t>(lm::up(w.n, 16));
-  *packed_bytes = ntiles * static_cast<size_t>(w.ktiles) * lm::kTileBytes;
-  *scale_bytes = ntiles * static_cast<size_t>(w.groups) * 64;
+  const size_t blocks = static_cast<size_t>(lm::up(w.n, 128));
+  *packed_bytes = blocks * static_cast<size_t>(w.ktiles) * lm::kBlockBytes;
+  *scale_bytes = blocks * static_cast<size_t>(w.groups) * 512;
   return LM_OK;
 }
 
@@ -433,24 +886,111 @@ lm_status sizes(const lm_linear_args &a, size_t *first, size_t *all) {
   return LM_OK;
 }
 
+// CTAs of four warps or, where more share out a tile's k, of those: small ones even out over the SMs.
 template <typename T, int NT>
-lm_status product_as(const ProductParams &p, dim3 grid, cudaStream_t s) {
-  return launch_dependent(p.w.group == 32 ? product_kernel<T, NT, true> : product_kernel<T, NT, false>, grid, 32 * kWarps,
-                          0, s, 1, p);
+lm_status product_as(ProductParams p, int sms, cudaStream_t s) {
+  const int64_t pairs = up(p.ntiles, kSide), blocks = up(p.rows, 8 * NT);
+  // As many parts of k as give every SM eight warps.
+  p.parts = 1;
+  while (p.parts < kMostWarps && 2 * p.parts <= p.w.ktiles && pairs * blocks * p.parts < 8ll * sms) p.parts *= 2;
+  const int warps = p.parts > 4 ? p.parts : 4;
+  const dim3 grid(static_cast<unsigned>(up(pairs, warps / p.parts)), static_cast<unsigned>(blocks));
+  const auto kernel = p.w.group == 32 ? product_kernel<T, NT, true> : product_kernel<T, NT, false>;
+  const int shared = warps * 8 * NT * (16 * kSide + 1) * 4;
+  return launch_dependent(kernel, grid, 32 * warps, static_cast<size_t>(shared), s, 1, p);
 }
 
 template <typename T>
-lm_status product(ProductParams p, int sms, cudaStream_t s) {
-  const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : p.rows <= 32 ? 4 : 8;
-  const int64_t blocks = up(p.rows, 8 * nt);
-  // As many parts of k as give every SM a dozen warps.
-  p.parts = 1;
-  while (p.parts < kWarps && 2 * p.parts <= p.w.ktiles && p.ntiles * blocks * p.parts < 12ll * sms) p.parts *= 2;
-  const dim3 grid(static_cast<unsigned>(up(p.ntiles, kWarps / p.parts)), static_cast<unsigned>(blocks));
-  return nt == 1   ? product_as<T, 1>(p, grid, s)
-         : nt == 2 ? product_as<T, 2>(p, grid, s)
-         : nt == 4 ? product_as<T, 4>(p, grid, s)
-                   : product_as<T, 8>(p, grid, s);
+lm_status product(const ProductParams &p, int sms, cudaStream_t s) {
+  return p.rows <= 8 ? product_as<T, 1>(p, sms, s) : product_as<T, 2>(p, sms, s);
+}
+
+// How the tiles' kernel cuts a call.
+struct Cut {
+  int bn, splits;
+  int64_t tiles;
+};
+
+// The cut with the least estimated time, in microseconds: per stage the slowest of widening W, products,
+// and adding up.
+Cut best_cut(int64_t n, int64_t rows, int64_t groups, int blocks, bool small, int sms, const Resident &held) {
+  Cut best = {16, 1, 0};
+  float least = 3.0e38f;
+  for (int bn = 16; bn <= kMaxBn; bn += bn < 64 ? 16 : 32) {
+    const int64_t tiles = up(n, kLanes) * up(rows, bn) * groups;
+    for (int splits = 1; splits <= kMaxSplits && (splits == 1 || splits <= blocks); splits *= 2) {
+      if (splits > 1 && tiles > held.split[splits]) continue;
+      const int64_t rounds = up(tiles, splits > 1 ? held.split[splits] : sms);
+      const float add = (small ? 2.0f : 1.0f) * (0.02f + 0.0007f * static_cast<float>(bn));
+      const float products = 0.0011f * static_cast<float>(bn);
+      float stage = 0.085f;
+      if (add > stage) stage = add;
+      if (products > stage) stage = products;
+      float t = 3.5f + static_cast<float>(rounds * up(blocks, splits)) * stage;
+      t += splits > 1 ? 0.9f + 0.03f * static_cast<float>(bn) / static_cast<float>(splits) + 0.008f * static_cast<float>(bn)
+                      : 0.012f * static_cast<float>(bn) * static_cast<float>(rounds);
+      if (t < least) {
+        least = t;
+        best = {bn, splits, tiles};
+      }
+    }
+    if (bn >= rows) break;
+  }
+  return best;
+}
+
+template <typename T, bool TURNS>
+auto tile_kernel_of(bool split, bool small) {
+  return split ? (small ? tile_kernel<T, true, true, TURNS> : tile_kernel<T, true, false, TURNS>)
+               : (small ? tile_kernel<T, false, true, TURNS> : tile_kernel<T, false, false, TURNS>);
+}
+
+template <typename T>
+lm_status tiles(const ProductParams &o, const Operand &x, const DeviceInfo &dev, void *workspace, const WaitFault *fault,
+                cudaStream_t s) {
+  TileParams p = {};
+  p.o = o;
+  p.o.rows = static_cast<int32_t>(x.rows);
+  p.blocks = o.w.ktiles;
+  Resident held;
+  if (lm_status st = resident_clusters(dev, &held); st != LM_OK) return st;
+  const bool small = o.w.group == 32, bf16 = std::is_same<T, __nv_bfloat16>::value;
+  const Cut cut = best_cut(o.w.n, x.rows, x.groups, p.blocks, small, dev.sm_count, held);
+  if (cut.tiles > INT_MAX / 16) return LM_ERR_UNSUPPORTED;
+  p.bn = cut.bn;
+  p.splits = cut.splits;
+  p.tiles = static_cast<int32_t>(cut.tiles);
+  p.lane_tiles = static_cast<int32_t>(up(o.w.n, kLanes));
+  p.col_tiles = static_cast<int32_t>(up(x.rows, p.bn));
+  p.sum_cols = 32;
+  while (p.sum_cols < p.bn) p.sum_cols *= 2;
+  p.sums = 512 / p.sum_cols < kMaxSums ? 512 / p.sum_cols : kMaxSums;
+  p.tmem_cols = p.sums * p.sum_cols;
+  const bool turns = p.bn <= kTurnBn;
+  p.sum_planes = turns ? 2 : 1;
+  // Shared memory: eight blocks of packed bytes at least, more where the operands' stages leave space.
+  const int stage_bytes = kOperandBytes + p.bn * 128;
+  const int room = 227 * 1024 - static_cast<int>(sizeof(Barriers)) - kScaleSlots * 512 - p.sum_planes * p.bn * kLanes * 4;
+  p.stages = (room - 8 * kBlockBytes) / stage_bytes;
+  if (p.stages > 6) p.stages = 6;
+  p.raw = (room - p.stages * stage_bytes) / kBlockBytes / 4 * 4;  // (every group comes back to its own slots)
+  if (p.raw > kMaxRaw) p.raw = kMaxRaw;
+  if (p.stages < widen_groups(turns) || p.raw < widen_groups(turns)) return LM_ERR_UNSUPPORTED;
+  p.idesc = idesc_f16(bf16, kLanes, static_cast<uint32_t>(p.bn));
+  p.err = static_cast<uint32_t *>(workspace);
+  p.wait_ns = fault ? fault->wait_ns : kWaitTimeoutNs;
+  p.withheld = fault ? static_cast<int32_t>(fault->withheld_cta) : -1;
+  CUtensorMap cols = {};
+  if (p.blocks > 0)
+    if (lm_status st = make_map(&cols, x, o.w.k, p.bn, bf16); st != LM_OK) return st;
+  const int smem = p.stages * stage_bytes + p.raw * kBlockBytes + kScaleSlots * 512 + p.sum_planes * p.bn * kLanes * 4 +
+                   static_cast<int>(sizeof(Barriers));
+  const bool split = p.splits > 1;
+  const auto kernel = turns ? tile_kernel_of<T, true>(split, small) : tile_kernel_of<T, false>(split, small);
+  if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
+  const int grid = split ? p.tiles * p.splits : p.tiles < dev.sm_count ? p.tiles : dev.sm_count;
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), kThreads, static_cast<size_t>(smem), s,
+                          split ? p.splits : 1, cols, p);
 }
 
 }  // namespace
@@ -464,9 +1004,11 @@ extern "C" lm_status lm_linear4_workspace_size(const lm_linear_args *args, const
   return lm::sizes(*args, &first, bytes);
 }
 
-extern "C" lm_status lm_linear4(const lm_linear_args *args, const lm_weight4 *weight, void *workspace,
-                                size_t workspace_bytes, lm_stream_t stream) {
-  using namespace lm;
+namespace lm {
+namespace {
+
+lm_status run(const lm_linear_args *args, const lm_weight4 *weight, void *workspace, size_t workspace_bytes,
+              lm_stream_t stream, const WaitFault *fault) {
   Weight w;
   size_t first = 0, need = 0;
   if (lm_status st = check4(args, weight, &w); st != LM_OK) return st;
@@ -534,11 +1076,34 @@ extern "C" lm_status lm_linear4(const lm_linear_args *args, const lm_weight4 *we
   p.res_row = a.residual_row_stride;
   p.out_row = a.out_row_stride;
   p.ntiles = static_cast<int32_t>(up(a.n, 16));
+  p.group_tiles = w.group == 128 ? 1 : 0;
   p.bias_f32 = a.bias_dtype == LM_F32;
   p.out_f32 = a.out_dtype == LM_F32;
   p.act = a.activation;
   p.scale = a.scale;
   DeviceInfo dev;
   if (lm_status st = current_device_info(&dev); st != LM_OK) return st;
-  return half ? product<__half>(p, dev.sm_count, s) : product<__nv_bfloat16>(p, dev.sm_count, s);
+  if (rows <= kFewRows || a.k == 0)
+    return half ? product<__half>(p, dev.sm_count, s) : product<__nv_bfloat16>(p, dev.sm_count, s);
+  return half ? tiles<__half>(p, x, dev, workspace, fault, s) : tiles<__nv_bfloat16>(p, x, dev, workspace, fault, s);
+}
+
+}  // namespace
+
+lm_status linear4_error(uint32_t *value, bool clear, cudaStream_t s) { return read_sticky(g_linear4_error, value, clear, s); }
+
+}  // namespace lm
+
+extern "C" lm_status lm_linear4(const lm_linear_args *args, const lm_weight4 *weight, void *workspace,
+                                size_t workspace_bytes, lm_stream_t stream) {
+  return lm::run(args, weight, workspace, workspace_bytes, stream, nullptr);
+}
+
+extern "C" lm_status lm_debug_linear4_withhold(const lm_linear_args *args, const lm_weight4 *weight, void *workspace,
+                                               size_t workspace_bytes, int64_t withheld_cta, uint64_t wait_ns,
+                                               lm_stream_t stream) {
+  if (withheld_cta < 0 || withheld_cta > INT_MAX || wait_ns < 100000ull || wait_ns > lm::kWaitTimeoutNs)
+    return LM_ERR_INVALID_ARG;
+  const lm::WaitFault fault{withheld_cta, wait_ns};
+  return lm::run(args, weight, workspace, workspace_bytes, stream, &fault);
 }

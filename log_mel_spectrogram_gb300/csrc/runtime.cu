@@ -149,6 +149,7 @@ extern "C" lm_status lm_decode_error(uint32_t *device_error, int32_t clear, lm_s
   *device_error = 0;
   if (lm_status st = lm::linear_error(&v, clear != 0, s); st != LM_OK) return st;
   if (lm_status st = lm::gated_error(&v, clear != 0, s); st != LM_OK) return st;
+  if (lm_status st = lm::linear4_error(&v, clear != 0, s); st != LM_OK) return st;
   if (lm_status st = lm::attend_error(&v, clear != 0, s); st != LM_OK) return st;
   *device_error = v;
   return v ? LM_ERR_DEVICE_FAULT : LM_OK;

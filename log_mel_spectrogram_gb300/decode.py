@@ -113,7 +113,7 @@ class Weight4:
     `group` consecutive k: value = q * scale.  ``quantize_weight`` rounds a weight to one, ``Weight4.pack`` takes
     numbers and scales that are at hand; ``linear`` takes it as its weight, for x of `dtype`.
 
-    The tensors packed [ceil(N / 16), ceil(K / 64), 512] uint8 and scale [ceil(N / 16), ceil(K / group), 16]
+    The tensors packed [ceil(N / 128), ceil(K / 64), 4096] uint8 and scale [ceil(N / 128), ceil(K / group), 128]
     float32 hold it in the order of include/logmel.h (lm_weight4)."""
 
     def __init__(self, packed: torch.Tensor, scale: torch.Tensor, shape, group: int, dtype: torch.dtype):

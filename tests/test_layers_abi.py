@@ -118,7 +118,7 @@ def test_gated_backward(L):
 def test_weight4(L):
     a, b = ctypes.c_size_t(), ctypes.c_size_t()
     assert L.lm_weight4_size(weight(n=17, k=65, group=32), ctypes.byref(a), ctypes.byref(b)) == 0
-    assert a.value == 2 * 2 * 512 and b.value == 2 * 3 * 64
+    assert a.value == 2 * 4096 and b.value == 3 * 512
     assert L.lm_weight4_size(None, ctypes.byref(a), ctypes.byref(b)) == 1
     assert L.lm_weight4_size(weight(n=-1), ctypes.byref(a), ctypes.byref(b)) == 1
     assert L.lm_weight4_size(weight(group=16), ctypes.byref(a), ctypes.byref(b)) == 2

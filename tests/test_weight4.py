@@ -79,6 +79,15 @@ def test_sizes(lm, m, k, n, group, dtype):
     check(lm.linear(x, w4, b, activation="gelu", residual=res, scale=0.5), x, w, b, "gelu", res, 0.5)
 
 
+@pytest.mark.parametrize("m", [16, 17, 40, 64, 70, 96, 128, 200, 300])
+@pytest.mark.parametrize("group", [32, 128])
+def test_more_tiles_than_multiprocessors(lm, m, group):
+    """CTAs that go through several tiles, and come round in their rings more than once."""
+    q, s = numbers(20001, 700, group, seed=m)
+    x = torch.randn((m, 700), device="cuda", generator=torch.Generator(device="cuda").manual_seed(m)).half()
+    check(lm.linear(x, lm.Weight4.pack(q, s, group=group, dtype=torch.float16)), x, value64(q, s, group))
+
+
 @pytest.mark.parametrize("act", [None, "relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("m", [7, 20, 300])
@@ -214,7 +223,7 @@ def test_refusals(lm):
                 lambda: lm.Weight4.pack(q, s, group=48), lambda: lm.Weight4.pack(q, s, group=32),
                 lambda: lm.Weight4.pack(q, s, dtype=torch.float32), lambda: lm.quantize_weight(x, 16),
                 lambda: lm.quantize_weight(x.t()), lambda: lm.quantize_weight(x.double()), lambda: w4.values(torch.int8),
-                lambda: lm.linear(x, lm.Weight4(w4.packed[:1], w4.scale, w4.shape, 64, torch.float16)),
+                lambda: lm.linear(x, lm.Weight4(w4.packed[:, :1], w4.scale, w4.shape, 64, torch.float16)),
                 lambda: lm.linear(x, lm.Weight4(w4.packed, w4.scale, (1 << 20, 128), 64, torch.float16))):
         with pytest.raises(ValueError):
             bad()

@@ -892,9 +892,10 @@ lm_status lm_weight4_values(const lm_weight4 *w, void *out, int64_t row_stride, 
 /*
  * lm_linear with such a weight: args as there, but for weight and
  * weight_row_stride, which are not used; args->n and args->k are the weight's.
- * A group's products q * x are summed in 32 bits, the sums multiplied by its
- * scale.  For many rows (lm_linear4_expands) the values are rounded to dtype
- * and expanded into the workspace, and lm_linear's products take them.
+ * Up to 16 rows, a group's products q * x are summed in 32 bits and the sums
+ * multiplied by its scale.  For more the values are rounded to dtype (as
+ * lm_weight4_values) on their way into the products; for many
+ * (lm_linear4_expands) they are expanded into the workspace for lm_linear.
  *   workspace  as for lm_linear, >= lm_linear4_workspace_size(...)
  * Errors as lm_linear.
  */

@@ -17,6 +17,7 @@
 #include "activate.cuh"
 #include "half.cuh"
 #include "internal.h"
+#include "linear_epilogue.cuh"
 #include "mma.cuh"
 #include "operand.cuh"
 #include "pdl.cuh"
@@ -106,8 +107,8 @@ __global__ void __launch_bounds__(256) fill_kernel(const Weight w, uint32_t *pac
   }
 }
 
-// A thread a word: eight values.  WHOLE: rows of 16-byte vectors, zeros past k.
-template <typename T, bool WHOLE>
+// A thread a word: eight values.
+template <typename T>
 __global__ void __launch_bounds__(256) values_kernel(const Weight w, T *out, int64_t row_stride, int64_t words) {
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   pdl_launch();
@@ -117,17 +118,8 @@ __global__ void __launch_bounds__(256) values_kernel(const Weight w, T *out, int
   const int64_t i = t / per, j = t % per * 8;
   const uint32_t word = w.packed[word_at(w, i, j)];
   const float s = w.scale[scale_at(w, i, j / w.group)];
-  if constexpr (WHOLE) {
-    uint32_t v[4];
-#pragma unroll
-    for (int e = 0; e < 8; e += 2)
-      v[e / 2] = pack2<T>(j + e < w.k ? static_cast<float>(nibble(word, e)) * s : 0.0f,
-                          j + e + 1 < w.k ? static_cast<float>(nibble(word, e + 1)) * s : 0.0f);
-    *reinterpret_cast<uint4 *>(out + i * row_stride + j) = make_uint4(v[0], v[1], v[2], v[3]);
-  } else {
-    for (int e = 0; e < 8 && j + e < w.k; ++e)
-      out[i * row_stride + j + e] = from_f32<T>(static_cast<float>(nibble(word, e)) * s);
-  }
+  for (int e = 0; e < 8 && j + e < w.k; ++e)
+    out[i * row_stride + j + e] = from_f32<T>(static_cast<float>(nibble(word, e)) * s);
 }
 
 struct ProductParams {
@@ -203,7 +195,7 @@ __device__ __forceinline__ uint4 load8(const T *row, int k, int end) {
 
 // One output element.
 template <typename T>
-__device__ __forceinline__ void put(const ProductParams &p, float s, int row, int n) {
+__device__ __forceinline__ void put_any(const ProductParams &p, float s, int row, int n) {
   if (p.bias) s += p.bias_f32 ? static_cast<const float *>(p.bias)[n] : to_f32(static_cast<const T *>(p.bias)[n]);
   float y = p.scale * activate_any(s, p.act);
   if (p.residual) y += to_f32(static_cast<const T *>(p.residual)[row * p.res_row + n]);
@@ -335,61 +327,34 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) product_kernel(const Produ
     if (n0 + at >= p.w.n) continue;
     float sum = 0.0f;
     for (int q = 0; q < p.parts; ++q) sum += sums[((at / WIDE * p.parts + q) * 8 * NT + row) * PITCH + at % WIDE];
-    put<T>(p, sum, row0 + row, static_cast<int>(n0) + at);
+    put_any<T>(p, sum, row0 + row, static_cast<int>(n0) + at);
   }
 }
 
 // ---- more rows: tcgen05 ----
 
-constexpr int kBk = 64;
-constexpr int kLanes = 128;
-constexpr int kOperandBytes = kLanes * kBk * 2;
-constexpr int kMaxBn = 128, kTurnBn = 64;     // up to kTurnBn columns, the adding warps' groups take turns
-constexpr int kMaxStages = 8, kMaxSums = 8, kMaxRaw = 16;
-constexpr int kScaleSlots = 32;                // ... of 512 bytes: a stage's scales take one, or two of groups of 32
-constexpr int kWiden = 8, kAdd = 8;            // warps
-// A stage's way through a warp takes a few hundred cycles of waiting for one another.  So groups of warps widen
-// several stages at once, in turn, and (of up to 64 columns) two groups add up two sums.  A wait tells whether the phase
-// before was the last to end, not which one it was; a group's own last fill shows that what came as
-// many fills before as there are stages has been used, which is enough where there are no more groups than stages.
-constexpr int widen_groups(bool turns) { return turns ? 4 : 2; }
-constexpr int kThreads = 32 * (4 + kWiden + kAdd);
+constexpr int kMaxStages = 8, kMaxRaw = 16;
+constexpr int kSlotBytes = kBlockBytes + 1024;  // a block's packed bytes and its scales, of one group or two
+constexpr int kWiden = 16, kEpilogue = 8;       // warps
+constexpr int kThreads = 32 * (4 + kWiden + kEpilogue);
 
 struct TileParams {
-  ProductParams o;                             // bias, residual, out, ...; rows: of one group
-  int32_t bn, stages, sums, raw, blocks, tmem_cols, sum_cols, sum_planes;
-  int32_t lane_tiles, col_tiles, tiles, splits;
-  uint32_t idesc;
-  uint32_t *err;
-  uint64_t wait_ns;
-  int32_t withheld;
+  LinearParams l;
+  const uint8_t *packed;
+  const float *scale;
+  int32_t groups, small, group_tiles, raw;
 };
 
 __device__ uint32_t g_linear4_error;
 
 struct alignas(16) Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t sum_full[kMaxSums], sum_empty[kMaxSums];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
-  uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
+  uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem;
   int abort;
 };
-
-struct Place {
-  int group, lane_tile, col0;
-};
-
-__device__ __forceinline__ Place place_at(const TileParams &p, int t) {
-  Place o;
-  const int per = p.lane_tiles * p.col_tiles;
-  o.group = t / per;
-  const int u = t - o.group * per;
-  o.lane_tile = u / p.col_tiles;  // a tile of W's columns go round inside: its bytes come from L2
-  o.col0 = (u - o.lane_tile * p.col_tiles) * p.bn;
-  return o;
-}
 
 // A ring's position.
 struct Ring {
@@ -404,109 +369,86 @@ struct Ring {
   }
 };
 
-// The sums of a tile's columns `first`, first + step, ... of `cols` at lane `at` of a [column][lane] array, or of the
-// arrays of a cluster's CTAs, into outputs.
-template <typename T, int ACT, bool SPLIT>
-__device__ __forceinline__ void finish(const TileParams &p, uint32_t sums, const Place &tile, int at, int first, int step,
-                                       int cols) {
-  const ProductParams &o = p.o;
-  const int n = tile.lane_tile * kLanes + at;
-  if (n >= o.w.n) return;
-  float bias = 0.0f;
-  if (o.bias) bias = o.bias_f32 ? static_cast<const float *>(o.bias)[n] : to_f32(static_cast<const T *>(o.bias)[n]);
-#pragma unroll 4
-  for (int c = first; c < cols; c += step) {
-    const uint32_t from = sums + static_cast<uint32_t>(c * kLanes + at) * 4;
-    float z = 0.0f;
-    if (SPLIT) {
-      uint32_t v[kMaxSplits];
+// The eight values of a word: whole numbers times the scale in 32 bits, rounded once (as lm_weight4_values).
+template <typename T>
+__device__ __forceinline__ void widen_scaled(uint32_t word, float s, uint32_t (&v)[4]) {
+  widen<T>(word, v);
 #pragma unroll
-      for (int r = 0; r < kMaxSplits; ++r)
-        if (r < p.splits) v[r] = ld_dsmem_u32(from, static_cast<uint32_t>(r));
-#pragma unroll
-      for (int r = 0; r < kMaxSplits; ++r)
-        if (r < p.splits) z += __uint_as_float(v[r]);
-      if (p.bn <= kTurnBn) {
-#pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r)
-          if (r < p.splits) v[r] = ld_dsmem_u32(from + static_cast<uint32_t>(p.bn * kLanes) * 4, static_cast<uint32_t>(r));
-#pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r)
-          if (r < p.splits) z += __uint_as_float(v[r]);
-      }
-    } else {
-      z = lds_f32(from);
-      if (p.bn <= kTurnBn) z += lds_f32(from + static_cast<uint32_t>(p.bn * kLanes) * 4);
-    }
-    const int64_t row = static_cast<int64_t>(tile.group) * o.rows + tile.col0 + c;
-    float y = o.scale * activate<ACT>(z + bias);
-    if (o.residual) y += to_f32(static_cast<const T *>(o.residual)[row * o.res_row + n]);
-    if (o.out_f32) {
-      static_cast<float *>(o.out)[row * o.out_row + n] = y;
-    } else {
-      static_cast<T *>(o.out)[row * o.out_row + n] = from_f32<T>(y);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float2 q = unpack2<T>(v[i]);
+    v[i] = pack2<T>(q.x * s, q.y * s);
   }
 }
 
-template <typename T, bool SPLIT>
-__device__ __forceinline__ void finish_any(const TileParams &p, uint32_t sums, const Place &tile, int at, int first,
-                                           int step, int cols) {
-  switch (p.o.act) {
-    case LM_ACT_RELU: finish<T, LM_ACT_RELU, SPLIT>(p, sums, tile, at, first, step, cols); break;
-    case LM_ACT_GELU: finish<T, LM_ACT_GELU, SPLIT>(p, sums, tile, at, first, step, cols); break;
-    case LM_ACT_GELU_TANH: finish<T, LM_ACT_GELU_TANH, SPLIT>(p, sums, tile, at, first, step, cols); break;
-    case LM_ACT_SILU: finish<T, LM_ACT_SILU, SPLIT>(p, sums, tile, at, first, step, cols); break;
-    default: finish<T, LM_ACT_NONE, SPLIT>(p, sums, tile, at, first, step, cols); break;
+// The values of all blocks in rows of `pitch` (a multiple of 8) elements, zeros past k: a warp a tile of 16 rows,
+// a lane four vectors of 16 bytes.
+template <typename T>
+__global__ void __launch_bounds__(256) expand_kernel(const Weight w, T *out, int pitch) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+  const int64_t block = blockIdx.y;
+  const int kb = blockIdx.x, small = w.group == 32 ? 1 : 0;
+  const int g = small ? 2 * kb : kb * 64 / w.group;
+  pdl_launch();
+  pdl_wait();
+  const uint4 v = load_once(w.packed + ((block * w.ktiles + kb) * 8 + warp) * (kTileBytes / 4) + lane * 4);
+  const float *const s = w.scale + (block * w.groups + g) * 128 + 16 * warp + r;
+  const bool there = !small || g + 1 < w.groups;
+  const int j = kb * 64 + 8 * c;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t row = block * 128 + 16 * warp + r + 8 * h;
+    if (row >= w.n) break;
+    uint32_t x[4];
+    T *const to = out + row * pitch + j;
+    widen_scaled<T>(h ? v.z : v.x, s[8 * h], x);
+    if (j < pitch) *reinterpret_cast<uint4 *>(to) = make_uint4(x[0], x[1], x[2], x[3]);
+    widen_scaled<T>(h ? v.w : v.y, there ? s[8 * h + 128 * small] : 0.0f, x);
+    if (j + 32 < pitch) *reinterpret_cast<uint4 *>(to + 32) = make_uint4(x[0], x[1], x[2], x[3]);
   }
 }
 
-// As linear.cu's kernel, W along the lanes, but for W's tiles: bulk copies bring their packed bytes and scales, eight
-// warps turn the bytes into the whole numbers q in the operand's swizzled layout, and the tensor memory holds one sum
-// of q x for each stage (two where groups are of 32); eight more warps multiply it by the lanes' scales and add
-// it up in registers, 32 bits, so that no scaled weight is ever rounded.
-// TURNS: up to kTurnBn columns.
-template <typename T, bool SPLIT, bool SMALL, bool TURNS>
-__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap col_map, const TileParams p) {
-  constexpr int UNITS = SMALL ? 2 : 1;  // sums a stage
-  constexpr int GROUPS = widen_groups(TURNS), GROUP_WARPS = kWiden / GROUPS, TILES = 8 / GROUP_WARPS;
-  constexpr int WIDEST = TURNS ? kTurnBn : kMaxBn / 2;  // columns of an adding warp
-  constexpr int SCALE_BYTES = 512 * UNITS, SCALES = kScaleSlots / UNITS;
+// linear.cu's kernel (a CTA a tile, or a cluster that shares out k), but for W's tiles: bulk copies bring their packed
+// bytes and scales, and eight warps turn them into the operand's swizzled layout.
+//
+// A stage's way through a warp takes several hundred cycles of waiting for one another, so that GROUPS groups
+// of warps widen as many stages at once, in turn.  A wait tells whether the phase before was the last to
+// end, not which one it was; a group's own last fill shows that what came as many fills before as there are stages
+// has been used, which is enough where there are no more groups than stages.
+template <typename T, bool SPLIT, int GROUPS>
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap col_map, const TileParams tp) {
+  constexpr int GROUP_WARPS = kWiden / GROUPS, TILES = 8 / GROUP_WARPS;
+  const LinearParams &p = tp.l;
   extern __shared__ __align__(1024) uint8_t ring[];
-  const int stage_bytes = kOperandBytes + p.bn * 128;
+  const int stage_bytes = kLanes * 128 + p.bn * 128;
   uint8_t *const raw = ring + p.stages * stage_bytes;
-  uint8_t *const scales = raw + p.raw * kBlockBytes;
-  float *const sums = reinterpret_cast<float *>(scales + kScaleSlots * 512);  // [sum_planes][bn][kLanes]
-  Barriers &b = *reinterpret_cast<Barriers *>(sums + p.sum_planes * p.bn * kLanes);
+  Barriers &b = *reinterpret_cast<Barriers *>(raw + tp.raw * kSlotBytes);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
   const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
   const int first = SPLIT ? static_cast<int>(blockIdx.x) / p.splits : static_cast<int>(blockIdx.x);
   const int step = SPLIT ? p.tiles : static_cast<int>(gridDim.x);
-  const int k_begin = SPLIT ? static_cast<int>(static_cast<int64_t>(p.blocks) * rank / p.splits) : 0;
-  const int k_end = SPLIT ? static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / p.splits) : p.blocks;
-  const Weight &w = p.o.w;
+  const int k_begin = SPLIT ? static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / p.splits) : 0;
+  const int k_end = SPLIT ? static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / p.splits) : p.kblocks;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&b.full[i], 1 + GROUP_WARPS + (i == 0 && static_cast<int>(blockIdx.x) == p.withheld ? 1 : 0));
-      mbar_init(&b.empty[i], 1);
+  // (By many threads: one thread took a microsecond for all of them.)
+  if (warp == 0) {
+    if (lane < p.stages) {
+      mbar_init(&b.full[lane], 1 + GROUP_WARPS + (lane == 0 && static_cast<int>(blockIdx.x) == p.withheld ? 1 : 0));
+      mbar_init(&b.empty[lane], 1);
     }
-    for (int i = 0; i < p.sums; ++i) {
-      mbar_init(&b.sum_full[i], 1);
-      mbar_init(&b.sum_empty[i], TURNS ? kAdd / 2 : kAdd);
+    if (lane < tp.raw) {
+      mbar_init(&b.raw_full[lane], 1);
+      mbar_init(&b.raw_empty[lane], GROUP_WARPS);
     }
-    for (int i = 0; i < p.raw; ++i) {
-      mbar_init(&b.raw_full[i], 1);
-      mbar_init(&b.raw_empty[i], GROUP_WARPS);
+    if (lane < 2) {
+      mbar_init(&b.acc_full[lane], 1);
+      mbar_init(&b.acc_empty[lane], kEpilogue);
     }
-    for (int i = 0; i < SCALES; ++i) {
-      mbar_init(&b.scale_full[i], 1);
-      mbar_init(&b.scale_empty[i], TURNS ? kAdd / 2 : kAdd);
+    if (lane == 0) {
+      mbar_init(&b.drain, 1);
+      b.abort = 0;
+      tma_prefetch_map(&col_map);
     }
-    mbar_init(&b.drain, 1);
-    b.abort = 0;
     fence_mbar_init();
-    tma_prefetch_map(&col_map);
   }
   if (warp == 2) tmem_alloc<false>(&b.tmem, static_cast<uint32_t>(p.tmem_cols));
   tcgen05_fence_before();
@@ -523,13 +465,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     int fills = 0;
     bool ok = true;
     for (int t = first; t < p.tiles && ok; t += step) {
-      const Place tile = place_at(p, t);
+      const Tile tile = tile_at(p, t, 0);
       for (int kb = k_begin; kb < k_end; ++kb) {
         if (fills >= p.stages) ok = mbar_wait_warp(&b.empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err);
         if (!ok) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&b.full[s.at], static_cast<uint32_t>(p.bn * 128));
-          tma_load_3d<false>(ring + s.at * stage_bytes + kOperandBytes, &col_map, kb * kBk, tile.col0, tile.group,
+          tma_load_3d<false>(ring + s.at * stage_bytes + kLanes * 128, &col_map, kb * kBk, tile.col0, tile.group,
                              smem_u32(&b.full[s.at]));
         }
         __syncwarp();
@@ -541,69 +483,60 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     for (int f = fills > p.stages ? fills - p.stages : 0; f < fills; ++f)
       if (!mbar_drain(&b.full[f % p.stages], (f / p.stages) & 1, p.wait_ns, p.err)) break;
   } else if (warp == 3) {  // packed bytes and scales
-    Ring s, c;
+    Ring s;
     int fills = 0;
     bool ok = true;
     for (int t = first; t < p.tiles && ok; t += step) {
-      const int lane_tile = place_at(p, t).lane_tile;
-      const uint8_t *const bytes =
-          reinterpret_cast<const uint8_t *>(w.packed) + static_cast<int64_t>(lane_tile) * w.ktiles * kBlockBytes;
-      const float *const factors = w.scale + static_cast<int64_t>(lane_tile) * w.groups * kLanes;
+      const int64_t block = tile_at(p, t, 0).lane0 / kLanes;
+      const uint8_t *const bytes = tp.packed + block * p.kblocks * kBlockBytes;
+      const float *const scales = tp.scale + block * tp.groups * kLanes;
       for (int kb = k_begin; kb < k_end; ++kb) {
-        if (fills >= p.raw) ok = mbar_wait_warp(&b.raw_empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err);
-        if (ok && fills >= SCALES) ok = mbar_wait_warp(&b.scale_empty[c.at], c.phase ^ 1, p.wait_ns, abort, p.err);
+        if (fills >= tp.raw) ok = mbar_wait_warp(&b.raw_empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err);
         if (!ok) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&b.raw_full[s.at], kBlockBytes);
-          bulk_g2s_plain(raw + s.at * kBlockBytes, bytes + static_cast<int64_t>(kb) * kBlockBytes, kBlockBytes,
+          const int g = tp.small ? 2 * kb : kb >> tp.group_tiles;
+          // (The last block of groups of 32 may have one.)
+          const uint32_t size = tp.small && g + 1 < tp.groups ? 1024u : 512u;
+          mbar_arrive_expect_tx(&b.raw_full[s.at], kBlockBytes + size);
+          bulk_g2s_plain(raw + s.at * kSlotBytes, bytes + static_cast<int64_t>(kb) * kBlockBytes, kBlockBytes,
                          &b.raw_full[s.at]);
-          const int g = SMALL ? 2 * kb : kb >> p.o.group_tiles;
-          // (The last tile of groups of 32 may have one.)
-          const uint32_t size = SMALL && g + 1 < w.groups ? 1024u : 512u;
-          mbar_arrive_expect_tx(&b.scale_full[c.at], size);
-          bulk_g2s_plain(scales + c.at * SCALE_BYTES, factors + static_cast<int64_t>(g) * kLanes, size, &b.scale_full[c.at]);
+          bulk_g2s_plain(raw + s.at * kSlotBytes + kBlockBytes, scales + static_cast<int64_t>(g) * kLanes, size,
+                         &b.raw_full[s.at]);
         }
         __syncwarp();
         ++fills;
-        s.next(p.raw);
-        c.next(SCALES);
+        s.next(tp.raw);
       }
     }
-    for (int f = fills > p.raw ? fills - p.raw : 0; f < fills; ++f)
-      if (!mbar_drain(&b.raw_full[f % p.raw], (f / p.raw) & 1, p.wait_ns, p.err)) break;
-    for (int f = fills > SCALES ? fills - SCALES : 0; f < fills; ++f)
-      if (!mbar_drain(&b.scale_full[f % SCALES], (f / SCALES) & 1, p.wait_ns, p.err)) break;
+    for (int f = fills > tp.raw ? fills - tp.raw : 0; f < fills; ++f)
+      if (!mbar_drain(&b.raw_full[f % tp.raw], (f / tp.raw) & 1, p.wait_ns, p.err)) break;
   } else if (warp == 1) {  // products
-    Ring s, a;
-    int units = 0;
+    Ring s;
+    int tiles = 0;
     bool ok = true;
     const uint32_t ring_a = smem_u32(ring);
-    for (int t = first; t < p.tiles && ok; t += step) {
+    for (int t = first; t < p.tiles && ok; t += step, ++tiles) {
+      const int half = tiles & 1;
+      if (tiles >= 2) ok = mbar_wait_warp(&b.acc_empty[half], ((tiles >> 1) - 1) & 1, p.wait_ns, abort, p.err);
+      tcgen05_fence_after();
+      const uint32_t d = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
       for (int kb = k_begin; kb < k_end && ok; ++kb) {
         ok = mbar_wait_warp(&b.full[s.at], s.phase, p.wait_ns, abort, p.err);
         if (!ok) break;
-        const uint64_t da = smem_desc_k128(ring_a + s.at * stage_bytes);
-        const uint64_t dc = smem_desc_k128(ring_a + s.at * stage_bytes + kOperandBytes);
+        tcgen05_fence_after();
+        const uint64_t a = smem_desc_k128(ring_a + s.at * stage_bytes);
+        const uint64_t c = smem_desc_k128(ring_a + s.at * stage_bytes + kLanes * 128);
+        if (elect_one()) {
 #pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          if (ok && units >= p.sums) ok = mbar_wait_warp(&b.sum_empty[a.at], a.phase ^ 1, p.wait_ns, abort, p.err);
-          tcgen05_fence_after();
-          if (ok && elect_one()) {
-            const uint32_t d = tmem + static_cast<uint32_t>(a.at * p.sum_cols);
-#pragma unroll
-            for (int i = 0; i < kBk / 16 / UNITS; ++i) {
-              const int k16 = u * (kBk / 16 / UNITS) + i;
-              tcgen05_mma_f16<false>(d, da + 2 * k16, dc + 2 * k16, p.idesc, i > 0);
-            }
-            tcgen05_commit<false>(&b.sum_full[a.at]);
-            if (u == UNITS - 1) tcgen05_commit<false>(&b.empty[s.at]);
-          }
-          __syncwarp();
-          ++units;
-          a.next(p.sums);
+          for (int i = 0; i < kBk / 16; ++i)
+            tcgen05_mma_f16<false>(d, a + 2 * i, c + 2 * i, p.idesc, kb > k_begin || i > 0);
+          tcgen05_commit<false>(&b.empty[s.at]);
         }
+        __syncwarp();
         s.next(p.stages);
       }
+      if (ok && elect_one()) tcgen05_commit<false>(&b.acc_full[half]);
+      __syncwarp();
     }
     if (!ok) {  // products in flight end before the tensor memory is given back
       if (elect_one()) tcgen05_commit<false>(&b.drain);
@@ -618,16 +551,30 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     const uint32_t low = static_cast<uint32_t>((16 * tile0 + r) * 128 + (((odd ? 4 + c : c) ^ r) * 16));
     const uint32_t high = static_cast<uint32_t>((16 * tile0 + r) * 128 + (((odd ? c : 4 + c) ^ r) * 16));
     const uint32_t ring_a = smem_u32(ring);
-    const uint4 *const from = reinterpret_cast<const uint4 *>(raw + tile0 * kTileBytes) + lane;
     const int mine = first < p.tiles ? (p.tiles - first + step - 1) / step * (k_end - k_begin) : 0;
+    int kb = k_begin + group;  // (of groups of 32: the block's place in k)
     Ring s, q;
     s.next(p.stages, group);
-    q.next(p.raw, group);
+    q.next(tp.raw, group);
     for (int i = group; i < mine; i += GROUPS) {
+      while (kb >= k_end) kb -= k_end - k_begin;
       if (!mbar_wait_warp(&b.raw_full[q.at], q.phase, p.wait_ns, abort, p.err)) break;
+      const uint8_t *const slot = raw + q.at * kSlotBytes;
+      const float *const scales = reinterpret_cast<const float *>(slot + kBlockBytes) + 16 * tile0 + r;
+      // A second group that the block lacks has zeros for numbers, whatever lies in its scales' place.
+      const int other = tp.small ? kLanes : 0;
+      const bool there = !tp.small || 2 * kb + 1 < tp.groups;
       uint4 v[TILES];
+      float f[TILES][2][2];
 #pragma unroll
-      for (int j = 0; j < TILES; ++j) v[j] = from[q.at * (kBlockBytes / 16) + j * (kTileBytes / 16)];
+      for (int j = 0; j < TILES; ++j) {
+        v[j] = reinterpret_cast<const uint4 *>(slot + (tile0 + j) * kTileBytes)[lane];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f[j][h][0] = scales[16 * j + 8 * h];
+          f[j][h][1] = there ? scales[other + 16 * j + 8 * h] : 0.0f;
+        }
+      }
       if (i >= p.stages && !mbar_wait_warp(&b.empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err)) break;
       const uint32_t to = ring_a + s.at * stage_bytes;
 #pragma unroll
@@ -635,8 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // rows r and r + 8
           uint32_t x[4], y[4];
-          widen<T>(h ? v[j].z : v[j].x, x);
-          widen<T>(h ? v[j].w : v[j].y, y);
+          widen_scaled<T>(h ? v[j].z : v[j].x, f[j][h][0], x);
+          widen_scaled<T>(h ? v[j].w : v[j].y, f[j][h][1], y);
           const uint32_t at = to + j * 2048 + h * 1024;
           sts_v4(at + low, odd ? y[0] : x[0], odd ? y[1] : x[1], odd ? y[2] : x[2], odd ? y[3] : x[3]);
           sts_v4(at + high, odd ? x[0] : y[0], odd ? x[1] : y[1], odd ? x[2] : y[2], odd ? x[3] : y[3]);
@@ -649,86 +596,47 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         mbar_arrive(&b.raw_empty[q.at]);
       }
       s.next(p.stages, GROUPS);
-      q.next(p.raw, GROUPS);
+      q.next(tp.raw, GROUPS);
+      kb += GROUPS;
     }
   } else if (warp >= 4 + kWiden) {
-    const int e = warp - 4 - kWiden, quarter = e % 4;
-    const int wide = TURNS ? p.bn : p.bn / 2, col = TURNS ? 0 : e / 4 * wide;  // this warp's columns
-    const int turn = TURNS ? e / 4 : 0;                                       // ... and stages
-    constexpr int every = TURNS ? 2 : 1;
-    const uint32_t base = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + static_cast<uint32_t>(col);
-    const int at = 32 * quarter + lane;
-    const float *const factor = reinterpret_cast<const float *>(scales) + at;
-    float *const mine = sums + turn * p.bn * kLanes + at;
-    Ring a, q;
-    a.next(p.sums, turn * UNITS);
-    q.next(SCALES, turn);
-    int fill = turn, past = 0;  // the stage, counted over all tiles; those of the tiles before
-    bool ok = true;
-    // (Warps that have given up still come to the barriers.)
-    for (int t = first; t < p.tiles; t += step) {
-      const Place tile = place_at(p, t);
-      f32x2 total[WIDEST / 2];
+    const int e = warp - 4 - kWiden;
+    int tiles = 0;
+    for (int t = first; t < p.tiles; t += step, ++tiles) {
+      const Tile tile = tile_at(p, t, 0);
+      const int half = tiles & 1;
+      T residual[16];
+      if (!SPLIT && p.residual) {
 #pragma unroll
-      for (int i = 0; i < WIDEST / 2; ++i) total[i] = both(0.0f);
-      const int end = past + (k_end - k_begin);
-      for (; fill < end && ok; fill += every) {
-        const int kb = k_begin + fill - past;
-        ok = mbar_wait_warp(&b.scale_full[q.at], q.phase, p.wait_ns, abort, p.err);
-        if (!ok) break;
-        f32x2 f[UNITS];
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          // (The second group that a tile lacks has zeros for weights.)
-          const bool there = u == 0 || 2 * kb + u < w.groups;
-          f[u] = both(there ? factor[q.at * (SCALE_BYTES / 4) + u * kLanes] : 0.0f);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b.scale_empty[q.at]);
-        q.next(SCALES, every);
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          if (ok) ok = mbar_wait_warp(&b.sum_full[a.at], a.phase, p.wait_ns, abort, p.err);
-          if (!ok) break;
-          tcgen05_fence_after();
-          const uint32_t d = base + static_cast<uint32_t>(a.at * p.sum_cols);
-#pragma unroll
-          for (int c = 0; c < WIDEST; c += 16) {
-            if (c < wide) {
-              uint32_t r[16];
-              tmem_ld16(d + c, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 16; j += 2)
-                total[(c + j) / 2] = fma2(f[u], pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), total[(c + j) / 2]);
-            }
-          }
-          tcgen05_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&b.sum_empty[a.at]);
-          a.next(p.sums, u == UNITS - 1 ? 1 + (every - 1) * UNITS : 1);
-        }
+        for (int j = 0; j < 16; ++j) residual[j] = from_f32<T>(0.0f);
+        const int c = e / 4 * 16, cols = min(p.bn, p.rows - tile.col0);
+        if (c < cols)
+          residual_rows<T>(p, residual, static_cast<int64_t>(tile.group) * p.rows + tile.col0 + c, min(16, cols - c),
+                           tile.lane0 + 32 * (e % 4) + lane);
       }
-      past = end;
-      // Through shared memory: outputs by a short loop.  (From registers, every column a copy of the epilogue,
-      // the instructions' way from L2 took microseconds.)
-      if (!SPLIT && TURNS) asm volatile("bar.sync 1, 256;" ::: "memory");  // the last tile's sums have been read
+      // One decision per warp: tensor memory loads are executed by whole warps.
+      if (!mbar_wait_warp(&b.acc_full[half], (tiles >> 1) & 1, p.wait_ns, abort, p.err)) break;
+      tcgen05_fence_after();
+      const uint32_t acc = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
+      if (SPLIT) {
+        // Products are complete: the ring is free to hold the partial sums.
+        float *const partial = reinterpret_cast<float *>(ring);
+        for (int c = e / 4 * 16; c < p.bn; c += 4 * kEpilogue) {
+          uint32_t r[16];
+          tmem_ld16(acc + (static_cast<uint32_t>(32 * (e % 4)) << 16) + c, r);
+          tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < WIDEST; c += 2)
-        if (c < wide) {
-          const float2 v = unpair(total[c / 2]);
-          mine[(col + c) * kLanes] = v.x;
-          mine[(col + c + 1) * kLanes] = v.y;
+          for (int j = 0; j < 16; ++j) partial[(c + j) * kLanes + 32 * (e % 4) + lane] = __uint_as_float(r[j]);
         }
-      if (!SPLIT) {
-        if (TURNS) {
-          asm volatile("bar.sync 1, 256;" ::: "memory");
+      } else {
+        if (p.residual) {
+          epilogue_act<T, true, kEpilogue>(p, tile, acc, e, residual);
         } else {
-          __syncwarp();
+          epilogue_act<T, false, kEpilogue>(p, tile, acc, e, residual);
         }
-        if (ok && !*abort)
-          finish_any<T, false>(p, smem_u32(sums), tile, at, TURNS ? turn : col, every,
-                               min(TURNS ? p.bn : col + wide, p.o.rows - tile.col0));
+        tcgen05_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.acc_empty[half]);
       }
     }
   }
@@ -737,13 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   if (SPLIT) {
     __syncthreads();
     cluster_sync_all();
-    if (!*abort && first < p.tiles) {
-      const Place tile = place_at(p, first);
-      // Columns are shared out over the cluster's CTAs, and over groups of 128 threads.
-      const int part = static_cast<int>(threadIdx.x) / kLanes * p.splits + rank;
-      finish_any<T, true>(p, smem_u32(sums), tile, threadIdx.x % kLanes, part, kThreads / kLanes * p.splits,
-                          min(p.bn, p.o.rows - tile.col0));
-    }
+    if (!*abort && first < p.tiles)
+      finish_split_act<T>(p, tile_at(p, first, 0), smem_u32(ring), rank, threadIdx.x, kThreads);
     cluster_sync_all();  // no CTA leaves while another reads its sums
   }
   tcgen05_fence_before();
@@ -773,7 +676,7 @@ lm_status view(const lm_weight4 *a, Weight *w) {
 constexpr int64_t kFewRows = 16;
 
 // From this many rows on the products cost more than expanding the weight.
-bool expands(int64_t rows, int64_t, int64_t) { return rows > 512; }
+bool expands(int64_t rows, int64_t n, int64_t) { return rows > 768 && n <= 65535 * 128; }
 
 // ... of a weight with contents.
 lm_status whole(const Weight &w) {
@@ -793,7 +696,7 @@ template <typename T>
 lm_status values(const Weight &w, void *out, int64_t row_stride, cudaStream_t s) {
   const int64_t words = w.n * up(w.k, 8);
   if (up(words, 256) > INT_MAX) return LM_ERR_UNSUPPORTED;
-  return launch_dependent(values_kernel<T, false>, dim3(static_cast<unsigned>(up(words, 256))), 256, 0, s, 1, w,
+  return launch_dependent(values_kernel<T>, dim3(static_cast<unsigned>(up(words, 256))), 256, 0, s, 1, w,
                           static_cast<T *>(out), row_stride, words);
 }
 
@@ -911,86 +814,96 @@ struct Cut {
   int64_t tiles;
 };
 
-// The cut with the least estimated time, in microseconds: per stage the slowest of widening W, products,
-// and adding up.
-Cut best_cut(int64_t n, int64_t rows, int64_t groups, int blocks, bool small, int sms, const Resident &held) {
+// The cut with the least estimated time, in microseconds: linear.cu's model, with a stage of at least 0.14 for the
+// widening.
+Cut best_cut(int64_t n, int64_t rows, int64_t groups, int kblocks, bool activation, int sms, const Resident &held) {
   Cut best = {16, 1, 0};
   float least = 3.0e38f;
-  for (int bn = 16; bn <= kMaxBn; bn += bn < 64 ? 16 : 32) {
+  const float column = activation ? 0.017f : 0.013f;
+  auto consider = [&](int bn, int splits) {
     const int64_t tiles = up(n, kLanes) * up(rows, bn) * groups;
-    for (int splits = 1; splits <= kMaxSplits && (splits == 1 || splits <= blocks); splits *= 2) {
-      if (splits > 1 && tiles > held.split[splits]) continue;
-      const int64_t rounds = up(tiles, splits > 1 ? held.split[splits] : sms);
-      const float add = (small ? 2.0f : 1.0f) * (0.02f + 0.0007f * static_cast<float>(bn));
-      const float products = 0.0011f * static_cast<float>(bn);
-      float stage = 0.085f;
-      if (add > stage) stage = add;
-      if (products > stage) stage = products;
-      float t = 3.5f + static_cast<float>(rounds * up(blocks, splits)) * stage;
-      t += splits > 1 ? 0.9f + 0.03f * static_cast<float>(bn) / static_cast<float>(splits) + 0.008f * static_cast<float>(bn)
-                      : 0.012f * static_cast<float>(bn) * static_cast<float>(rounds);
-      if (t < least) {
-        least = t;
-        best = {bn, splits, tiles};
-      }
+    if (splits > 1 && tiles > held.split[splits]) return;
+    const int64_t rounds = up(tiles, splits > 1 ? held.split[splits] : sms);
+    const float products = 0.0011f * static_cast<float>(bn), stage = products > 0.14f ? products : 0.14f;
+    const float blocks = static_cast<float>(up(kblocks, splits)) * stage;
+    float t = 3.5f + blocks;
+    t += splits > 1 ? 0.9f + 0.03f * static_cast<float>(bn) / static_cast<float>(splits) + 0.008f * static_cast<float>(bn)
+                    : column * static_cast<float>(bn);
+    const float epi = 0.5f + column * static_cast<float>(bn);
+    t += static_cast<float>(rounds - 1) * (blocks > epi ? blocks : epi);
+    if (t < least) {
+      least = t;
+      best = {bn, splits, tiles};
     }
-    if (bn >= rows) break;
-  }
+  };
+  const int most = rows < kMaxBn ? static_cast<int>(up(rows, 16) * 16) : kMaxBn;
+  auto splits = [&](int bn) {
+    for (int s = 1; s <= kMaxSplits && (s == 1 || s <= kblocks); s *= 2) consider(bn, s);
+  };
+  for (int bn = 16; bn <= most; bn += bn < 64 ? 16 : 32) splits(bn);
+  splits(static_cast<int>(up(up(rows, up(rows, kMaxBn)), 16) * 16));
   return best;
 }
 
-template <typename T, bool TURNS>
-auto tile_kernel_of(bool split, bool small) {
-  return split ? (small ? tile_kernel<T, true, true, TURNS> : tile_kernel<T, true, false, TURNS>)
-               : (small ? tile_kernel<T, false, true, TURNS> : tile_kernel<T, false, false, TURNS>);
-}
-
 template <typename T>
-lm_status tiles(const ProductParams &o, const Operand &x, const DeviceInfo &dev, void *workspace, const WaitFault *fault,
-                cudaStream_t s) {
-  TileParams p = {};
-  p.o = o;
-  p.o.rows = static_cast<int32_t>(x.rows);
-  p.blocks = o.w.ktiles;
+lm_status tiles(const lm_linear_args &a, const Weight &w, const Operand &x, const DeviceInfo &dev, void *workspace,
+                const WaitFault *fault, cudaStream_t s) {
+  TileParams tp = {};
+  LinearParams &p = tp.l;
+  tp.packed = reinterpret_cast<const uint8_t *>(w.packed);
+  tp.scale = w.scale;
+  tp.groups = w.groups;
+  tp.small = w.group == 32;
+  tp.group_tiles = w.group == 128 ? 1 : 0;
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.out = a.out;
+  p.out_row = a.out_row_stride;
+  p.res_row = a.residual_row_stride;
+  p.rows = static_cast<int32_t>(x.rows);
+  p.n = static_cast<int32_t>(a.n);
+  p.kblocks = w.ktiles;
+  p.bias_f32 = a.bias_dtype == LM_F32;
+  p.out_f32 = a.out_dtype == LM_F32;
+  p.act = a.activation;
+  p.scale = a.scale;
+  p.err = static_cast<uint32_t *>(workspace);
+  p.wait_ns = fault ? fault->wait_ns : kWaitTimeoutNs;
+  p.withheld = fault ? static_cast<int32_t>(fault->withheld_cta) : -1;
   Resident held;
   if (lm_status st = resident_clusters(dev, &held); st != LM_OK) return st;
-  const bool small = o.w.group == 32, bf16 = std::is_same<T, __nv_bfloat16>::value;
-  const Cut cut = best_cut(o.w.n, x.rows, x.groups, p.blocks, small, dev.sm_count, held);
+  const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  const Cut cut = best_cut(a.n, x.rows, x.groups, p.kblocks, p.act > LM_ACT_RELU, dev.sm_count, held);
   if (cut.tiles > INT_MAX / 16) return LM_ERR_UNSUPPORTED;
   p.bn = cut.bn;
   p.splits = cut.splits;
   p.tiles = static_cast<int32_t>(cut.tiles);
-  p.lane_tiles = static_cast<int32_t>(up(o.w.n, kLanes));
-  p.col_tiles = static_cast<int32_t>(up(x.rows, p.bn));
-  p.sum_cols = 32;
-  while (p.sum_cols < p.bn) p.sum_cols *= 2;
-  p.sums = 512 / p.sum_cols < kMaxSums ? 512 / p.sum_cols : kMaxSums;
-  p.tmem_cols = p.sums * p.sum_cols;
-  const bool turns = p.bn <= kTurnBn;
-  p.sum_planes = turns ? 2 : 1;
+  p.lane_step = kLanes;
+  p.lane_tiles = static_cast<int32_t>(up(p.n, kLanes));
+  p.col_tiles = static_cast<int32_t>(up(p.rows, p.bn));
+  p.lanes_inside = 0;  // a tile of W's columns go round inside: its bytes come from L2
+  p.tmem_cols = 32;
+  while (p.tmem_cols < 2 * p.bn) p.tmem_cols *= 2;
   // Shared memory: eight blocks of packed bytes at least, more where the operands' stages leave space.
-  const int stage_bytes = kOperandBytes + p.bn * 128;
-  const int room = 227 * 1024 - static_cast<int>(sizeof(Barriers)) - kScaleSlots * 512 - p.sum_planes * p.bn * kLanes * 4;
-  p.stages = (room - 8 * kBlockBytes) / stage_bytes;
-  if (p.stages > 6) p.stages = 6;
-  p.raw = (room - p.stages * stage_bytes) / kBlockBytes / 4 * 4;  // (every group comes back to its own slots)
-  if (p.raw > kMaxRaw) p.raw = kMaxRaw;
-  if (p.stages < widen_groups(turns) || p.raw < widen_groups(turns)) return LM_ERR_UNSUPPORTED;
+  const int stage_bytes = kLanes * 128 + p.bn * 128;
+  const int room = 227 * 1024 - static_cast<int>(sizeof(Barriers));
+  p.stages = (room - 8 * kSlotBytes) / stage_bytes;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  tp.raw = (room - p.stages * stage_bytes) / kSlotBytes / 4 * 4;  // (every group comes back to its own slots)
+  if (tp.raw > kMaxRaw) tp.raw = kMaxRaw;
+  const bool four = p.stages >= 4;
+  if (p.stages < (four ? 4 : 2) || tp.raw < 4) return LM_ERR_UNSUPPORTED;
   p.idesc = idesc_f16(bf16, kLanes, static_cast<uint32_t>(p.bn));
-  p.err = static_cast<uint32_t *>(workspace);
-  p.wait_ns = fault ? fault->wait_ns : kWaitTimeoutNs;
-  p.withheld = fault ? static_cast<int32_t>(fault->withheld_cta) : -1;
   CUtensorMap cols = {};
-  if (p.blocks > 0)
-    if (lm_status st = make_map(&cols, x, o.w.k, p.bn, bf16); st != LM_OK) return st;
-  const int smem = p.stages * stage_bytes + p.raw * kBlockBytes + kScaleSlots * 512 + p.sum_planes * p.bn * kLanes * 4 +
-                   static_cast<int>(sizeof(Barriers));
+  if (lm_status st = make_map(&cols, x, a.k, p.bn, bf16); st != LM_OK) return st;
+  const int smem = p.stages * stage_bytes + tp.raw * kSlotBytes + static_cast<int>(sizeof(Barriers));
   const bool split = p.splits > 1;
-  const auto kernel = turns ? tile_kernel_of<T, true>(split, small) : tile_kernel_of<T, false>(split, small);
+  const auto kernel = split ? (four ? tile_kernel<T, true, 4> : tile_kernel<T, true, 2>)
+                            : (four ? tile_kernel<T, false, 4> : tile_kernel<T, false, 2>);
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
   const int grid = split ? p.tiles * p.splits : p.tiles < dev.sm_count ? p.tiles : dev.sm_count;
   return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), kThreads, static_cast<size_t>(smem), s,
-                          split ? p.splits : 1, cols, p);
+                          split ? p.splits : 1, cols, tp);
 }
 
 }  // namespace
@@ -1048,13 +961,12 @@ lm_status run(const lm_linear_args *args, const lm_weight4 *weight, void *worksp
   if (expands(rows, a.n, a.k)) {
     void *const to = static_cast<char *>(workspace) + first;
     if (a.k > 0) {
-      const int64_t words = a.n * up(a.k, 8), ctas = up(words, 256);
-      if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
-      const dim3 grid(static_cast<unsigned>(ctas));
-      if (lm_status st = half ? launch_dependent(values_kernel<__half, true>, grid, 256, 0, s, 1, w,
-                                                 static_cast<__half *>(to), up(a.k, 8) * 8, words)
-                              : launch_dependent(values_kernel<__nv_bfloat16, true>, grid, 256, 0, s, 1, w,
-                                                 static_cast<__nv_bfloat16 *>(to), up(a.k, 8) * 8, words);
+      if (up(a.n, 128) > 65535) return LM_ERR_UNSUPPORTED;
+      const dim3 grid(static_cast<unsigned>(w.ktiles), static_cast<unsigned>(up(a.n, 128)));
+      const int pitch = static_cast<int>(up(a.k, 8) * 8);
+      if (lm_status st = half ? launch_dependent(expand_kernel<__half>, grid, 256, 0, s, 1, w, static_cast<__half *>(to), pitch)
+                              : launch_dependent(expand_kernel<__nv_bfloat16>, grid, 256, 0, s, 1, w,
+                                                 static_cast<__nv_bfloat16 *>(to), pitch);
           st != LM_OK)
         return st;
     }
@@ -1085,7 +997,7 @@ lm_status run(const lm_linear_args *args, const lm_weight4 *weight, void *worksp
   if (lm_status st = current_device_info(&dev); st != LM_OK) return st;
   if (rows <= kFewRows || a.k == 0)
     return half ? product<__half>(p, dev.sm_count, s) : product<__nv_bfloat16>(p, dev.sm_count, s);
-  return half ? tiles<__half>(p, x, dev, workspace, fault, s) : tiles<__nv_bfloat16>(p, x, dev, workspace, fault, s);
+  return half ? tiles<__half>(a, w, x, dev, workspace, fault, s) : tiles<__nv_bfloat16>(a, w, x, dev, workspace, fault, s);
 }
 
 }  // namespace

@@ -209,9 +209,9 @@ __device__ __forceinline__ void put_any(const ProductParams &p, float s, int row
 // NT: blocks of eight rows of x; blockIdx.y counts such tiles.  SMALL: groups of 32, two to a tile.
 // A warp has two tiles of 16 outputs side by side, which share its operands of x and give it products
 // that do not wait for one another.
-template <typename T, int NT, bool SMALL>
-__global__ void __launch_bounds__(32 * kMostWarps, 1) product_kernel(const ProductParams p) {
-  constexpr int AHEAD = NT == 1 ? 4 : 2;  // tiles whose bytes are on their way
+// MOST: warps of a CTA, at most; with 8 the registers are held to what lets three such CTAs share an SM.
+template <typename T, int NT, bool SMALL, int MOST>
+__global__ void __launch_bounds__(32 * MOST, MOST == 8 ? (NT == 1 ? 3 : 2) : 1) product_kernel(const ProductParams p) {
   constexpr int SCALES = SMALL ? 2 : 1;
   constexpr int PITCH = 16 * kSide + 1;
   extern __shared__ float sums[];  // [warps][8 * NT][PITCH]
@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) product_kernel(const Produ
 #pragma unroll
       for (int j = 0; j < 4; ++j) total[t][m][j] = 0.0f;
 
-  uint4 w[AHEAD][kSide];
-  float s[AHEAD][kSide][SCALES][2];
+  uint4 w[2][kSide], b[2][NT][2];
+  float s[2][kSide][SCALES][2];
   auto fetch = [&](int u, int kt) {
 #pragma unroll
     for (int m = 0; m < kSide; ++m) {
@@ -252,60 +252,63 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) product_kernel(const Produ
       for (int h = 0; h < SCALES; ++h) {
         int g = SMALL ? 2 * kt + h : kt >> p.group_tiles;
         if (SMALL && g >= p.w.groups) g = p.w.groups - 1;  // (its half of the tile is zeros)
-        s[u][m][h][0] = scales[m * 16 + static_cast<int64_t>(g) * 128];
-        s[u][m][h][1] = scales[m * 16 + static_cast<int64_t>(g) * 128 + 8];
+        const float *const at = scales + m * 16 + static_cast<int64_t>(g) * 128;
+        s[u][m][h][0] = at[0];
+        s[u][m][h][1] = at[8];
       }
     }
+    if ((kt + 1) * 64 <= k) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) b[u][t][h] = *reinterpret_cast<const uint4 *>(x[t] + kt * 64 + 32 * h);
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) b[u][t][h] = load8<T>(x[t] - 8 * c, kt * 64 + 32 * h + 8 * c, k);
+    }
   };
-  uint4 b[2][NT][2];
-  auto fetch_x = [&](uint4 (&to)[NT][2], int kt) {
-    const bool whole = (kt + 1) * 64 <= k;
+  auto multiply = [&](int u) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int m = 0; m < kSide; ++m) {
+      uint32_t v[4][4];  // words: row r, the tile's first and second half of k; row r + 8
+      widen<T>(w[u][m].x, v[0]);
+      widen<T>(w[u][m].y, v[1]);
+      widen<T>(w[u][m].z, v[2]);
+      widen<T>(w[u][m].w, v[3]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        to[t][h] = whole ? *reinterpret_cast<const uint4 *>(x[t] + kt * 64 + 32 * h)
-                         : load8<T>(x[t] - 8 * c, kt * 64 + 32 * h + 8 * c, k);
-  };
+      for (int t = 0; t < NT; ++t) {
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int u = 0; u < AHEAD; ++u)
-    if (begin + u < end) fetch(u, begin + u);
-  if (begin < end) fetch_x(b[0], begin);
-  for (int base = begin; base < end; base += AHEAD) {
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      const int kt = base + u;
-      if (kt >= end) break;
-      if (kt + 1 < end) fetch_x(b[(u + 1) % 2], kt + 1);
-#pragma unroll
-      for (int m = 0; m < kSide; ++m) {
-        uint32_t v[4][4];  // words: row r, the tile's first and second half of k; row r + 8
-        widen<T>(w[u][m].x, v[0]);
-        widen<T>(w[u][m].y, v[1]);
-        widen<T>(w[u][m].z, v[2]);
-        widen<T>(w[u][m].w, v[3]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 &o = b[u % 2][t][h];
-            const uint32_t a0[4] = {v[h][0], v[h + 2][0], v[h][1], v[h + 2][1]};
-            const uint32_t a1[4] = {v[h][2], v[h + 2][2], v[h][3], v[h + 2][3]};
-            mma16816<T>(d, a0, o.x, o.y);
-            mma16816<T>(d, a1, o.z, o.w);
-            if (SMALL || h == 1) {
-              const float *const f = s[u][m][SMALL ? h : 0];
-              total[t][m][0] = fmaf(f[0], d[0], total[t][m][0]);
-              total[t][m][1] = fmaf(f[0], d[1], total[t][m][1]);
-              total[t][m][2] = fmaf(f[1], d[2], total[t][m][2]);
-              total[t][m][3] = fmaf(f[1], d[3], total[t][m][3]);
-              d[0] = d[1] = d[2] = d[3] = 0.0f;
-            }
+        for (int h = 0; h < 2; ++h) {
+          const uint4 &o = b[u][t][h];
+          const uint32_t a0[4] = {v[h][0], v[h + 2][0], v[h][1], v[h + 2][1]};
+          const uint32_t a1[4] = {v[h][2], v[h + 2][2], v[h][3], v[h + 2][3]};
+          mma16816<T>(d, a0, o.x, o.y);
+          mma16816<T>(d, a1, o.z, o.w);
+          if (SMALL || h == 1) {
+            const float *const f = s[u][m][SMALL ? h : 0];
+            total[t][m][0] = fmaf(f[0], d[0], total[t][m][0]);
+            total[t][m][1] = fmaf(f[0], d[1], total[t][m][1]);
+            total[t][m][2] = fmaf(f[1], d[2], total[t][m][2]);
+            total[t][m][3] = fmaf(f[1], d[3], total[t][m][3]);
+            d[0] = d[1] = d[2] = d[3] = 0.0f;
           }
         }
       }
-      if (kt + AHEAD < end) fetch(u, kt + AHEAD);
+    }
+  };
+  // Two tiles on their way.
+  if (begin < end) fetch(0, begin);
+  if (begin + 1 < end) fetch(1, begin + 1);
+#pragma unroll 1
+  for (int kt = begin; kt < end; kt += 2) {
+    multiply(0);
+    if (kt + 2 < end) fetch(0, kt + 2);
+    if (kt + 1 < end) {
+      multiply(1);
+      if (kt + 3 < end) fetch(1, kt + 3);
     }
   }
 #pragma unroll
@@ -333,9 +336,10 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) product_kernel(const Produ
 
 // ---- more rows: tcgen05 ----
 
-constexpr int kMaxStages = 8, kMaxRaw = 16;
-constexpr int kSlotBytes = kBlockBytes + 1024;  // a block's packed bytes and its scales, of one group or two
-constexpr int kWiden = 16, kEpilogue = 8;       // warps
+constexpr int kMaxStages = 8, kMaxRaw = 4;
+constexpr int kChunk = 4;                       // blocks of k that are fetched at once
+constexpr int kSlotBytes = kChunk * (kBlockBytes + 1024);  // their packed bytes, then their scales
+constexpr int kWiden = 8, kEpilogue = 8;        // warps
 constexpr int kThreads = 32 * (4 + kWiden + kEpilogue);
 
 struct TileParams {
@@ -356,13 +360,16 @@ struct alignas(16) Barriers {
   int abort;
 };
 
+// The group that block kb of k starts with.
+__device__ __forceinline__ int group_at(const TileParams &p, int kb) { return p.small ? 2 * kb : kb >> p.group_tiles; }
+
 // A ring's position.
 struct Ring {
   int at = 0;
   uint32_t phase = 0;
   __device__ __forceinline__ void next(int n, int by = 1) {
     at += by;
-    while (at >= n) {
+    if (at >= n) {
       at -= n;
       phase ^= 1;
     }
@@ -407,6 +414,86 @@ __global__ void __launch_bounds__(256) expand_kernel(const Weight w, T *out, int
   }
 }
 
+// A scale as two 16-bit floats, twice each: its rounded value and what that leaves off.
+template <typename T>
+struct Scale {
+  uint32_t high, low;
+};
+
+template <typename T>
+__device__ __forceinline__ Scale<T> split_scale(float s) {
+  Scale<T> o;
+  o.high = pack2<T>(s, s);
+  const float rest = s - unpack2<T>(o.high).x, low = fabsf(s) < 3.0e38f ? rest : 0.0f;
+  o.low = pack2<T>(low, low);
+  return o;
+}
+
+// The eight values of a word, two instructions a pair: q * high + (q * low rounded), rounded once.  In bf16 the
+// parts lose 2^-17 of the value, 2^-8 of the last rounding; in f16, whose least step is 2^-24, 8 * 2^-25 for scales
+// down to 2^-10, a sixteenth of it (smaller scales go through 32 bits).
+__device__ __forceinline__ __half2 as2(uint32_t v, __half) { return *reinterpret_cast<const __half2 *>(&v); }
+__device__ __forceinline__ __nv_bfloat162 as2(uint32_t v, __nv_bfloat16) {
+  return *reinterpret_cast<const __nv_bfloat162 *>(&v);
+}
+template <typename T>
+__device__ __forceinline__ void widen_scaled(uint32_t word, const Scale<T> &s, uint32_t (&v)[4]) {
+  widen<T>(word, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto q = as2(v[i], T()), y = __hfma2(q, as2(s.high, T()), __hmul2(q, as2(s.low, T())));
+    v[i] = *reinterpret_cast<const uint32_t *>(&y);
+  }
+}
+
+// TILES tiles of 16 rows of a block into the operand at `to`.
+template <typename T, int TILES>
+__device__ __forceinline__ void widen_stage(const uint8_t *slot, const float *scales, int other, bool there, uint32_t to,
+                                            uint32_t low, uint32_t high, bool odd, int lane) {
+  // (Odd rows' halves change places here.)
+  uint4 v[TILES];
+  float f[TILES][2][2];
+  bool tiny = false;
+#pragma unroll
+  for (int j = 0; j < TILES; ++j) {
+    const uint4 u = reinterpret_cast<const uint4 *>(slot + j * kTileBytes)[lane];
+    v[j] = odd ? make_uint4(u.y, u.x, u.w, u.z) : u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float first = scales[16 * j + 8 * h], second = there ? scales[other + 16 * j + 8 * h] : 0.0f;
+      f[j][h][0] = odd ? second : first;
+      f[j][h][1] = odd ? first : second;
+      tiny = tiny || fabsf(f[j][h][0]) < 0x1p-10f || fabsf(f[j][h][1]) < 0x1p-10f;
+    }
+  }
+  if (std::is_same<T, __half>::value && __any_sync(0xffffffffu, tiny)) {
+#pragma unroll 1
+    for (int h = 0; h < 2 * TILES; ++h) {
+      const uint4 u = reinterpret_cast<const uint4 *>(slot + h / 2 * kTileBytes)[lane];
+      const float first = scales[8 * h], second = there ? scales[other + 8 * h] : 0.0f;
+      uint32_t x[4], y[4];
+      widen_scaled<T>(h % 2 ? u.z : u.x, first, x);
+      widen_scaled<T>(h % 2 ? u.w : u.y, second, y);
+      const uint32_t at = to + h * 1024;
+      sts_v4(at + (odd ? high : low), x[0], x[1], x[2], x[3]);
+      sts_v4(at + (odd ? low : high), y[0], y[1], y[2], y[3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // rows r and r + 8
+        uint32_t x[4];
+        const uint32_t at = to + j * 2048 + h * 1024;
+        widen_scaled<T>(h ? v[j].z : v[j].x, split_scale<T>(f[j][h][0]), x);
+        sts_v4(at + low, x[0], x[1], x[2], x[3]);
+        widen_scaled<T>(h ? v[j].w : v[j].y, split_scale<T>(f[j][h][1]), x);
+        sts_v4(at + high, x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+}
+
 // linear.cu's kernel (a CTA a tile, or a cluster that shares out k), but for W's tiles: bulk copies bring their packed
 // bytes and scales, and eight warps turn them into the operand's swizzled layout.
 //
@@ -437,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
     if (lane < tp.raw) {
       mbar_init(&b.raw_full[lane], 1);
-      mbar_init(&b.raw_empty[lane], GROUP_WARPS);
+      mbar_init(&b.raw_empty[lane], kWiden);
     }
     if (lane < 2) {
       mbar_init(&b.acc_full[lane], 1);
@@ -482,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     // No copy outlives the CTA, whatever the other warps did.
     for (int f = fills > p.stages ? fills - p.stages : 0; f < fills; ++f)
       if (!mbar_drain(&b.full[f % p.stages], (f / p.stages) & 1, p.wait_ns, p.err)) break;
-  } else if (warp == 3) {  // packed bytes and scales
+  } else if (warp == 3) {  // packed bytes and scales, several blocks at once: issuing a copy takes some 200 cycles
     Ring s;
     int fills = 0;
     bool ok = true;
@@ -490,18 +577,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       const int64_t block = tile_at(p, t, 0).lane0 / kLanes;
       const uint8_t *const bytes = tp.packed + block * p.kblocks * kBlockBytes;
       const float *const scales = tp.scale + block * tp.groups * kLanes;
-      for (int kb = k_begin; kb < k_end; ++kb) {
+      for (int kb = k_begin; kb < k_end; kb += kChunk) {
         if (fills >= tp.raw) ok = mbar_wait_warp(&b.raw_empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err);
         if (!ok) break;
         if (elect_one()) {
-          const int g = tp.small ? 2 * kb : kb >> tp.group_tiles;
-          // (The last block of groups of 32 may have one.)
-          const uint32_t size = tp.small && g + 1 < tp.groups ? 1024u : 512u;
-          mbar_arrive_expect_tx(&b.raw_full[s.at], kBlockBytes + size);
-          bulk_g2s_plain(raw + s.at * kSlotBytes, bytes + static_cast<int64_t>(kb) * kBlockBytes, kBlockBytes,
-                         &b.raw_full[s.at]);
-          bulk_g2s_plain(raw + s.at * kSlotBytes + kBlockBytes, scales + static_cast<int64_t>(g) * kLanes, size,
-                         &b.raw_full[s.at]);
+          const int end = min(kb + kChunk, k_end), g = group_at(tp, kb), g_end = min(group_at(tp, end - 1) + 1 + tp.small, tp.groups);
+          const uint32_t size = static_cast<uint32_t>(end - kb) * kBlockBytes, factors = static_cast<uint32_t>(g_end - g) * 512;
+          uint8_t *const to = raw + s.at * kSlotBytes;
+          mbar_arrive_expect_tx(&b.raw_full[s.at], size + factors);
+          bulk_g2s_plain(to, bytes + static_cast<int64_t>(kb) * kBlockBytes, size, &b.raw_full[s.at]);
+          bulk_g2s_plain(to + kChunk * kBlockBytes, scales + static_cast<int64_t>(g) * kLanes, factors, &b.raw_full[s.at]);
         }
         __syncwarp();
         ++fills;
@@ -551,54 +636,36 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     const uint32_t low = static_cast<uint32_t>((16 * tile0 + r) * 128 + (((odd ? 4 + c : c) ^ r) * 16));
     const uint32_t high = static_cast<uint32_t>((16 * tile0 + r) * 128 + (((odd ? c : 4 + c) ^ r) * 16));
     const uint32_t ring_a = smem_u32(ring);
-    const int mine = first < p.tiles ? (p.tiles - first + step - 1) / step * (k_end - k_begin) : 0;
-    int kb = k_begin + group;  // (of groups of 32: the block's place in k)
+    // Every warp waits for every chunk of blocks and gives it back; the stages are the groups' in turn.
     Ring s, q;
     s.next(p.stages, group);
-    q.next(tp.raw, group);
-    for (int i = group; i < mine; i += GROUPS) {
-      while (kb >= k_end) kb -= k_end - k_begin;
-      if (!mbar_wait_warp(&b.raw_full[q.at], q.phase, p.wait_ns, abort, p.err)) break;
-      const uint8_t *const slot = raw + q.at * kSlotBytes;
-      const float *const scales = reinterpret_cast<const float *>(slot + kBlockBytes) + 16 * tile0 + r;
-      // A second group that the block lacks has zeros for numbers, whatever lies in its scales' place.
-      const int other = tp.small ? kLanes : 0;
-      const bool there = !tp.small || 2 * kb + 1 < tp.groups;
-      uint4 v[TILES];
-      float f[TILES][2][2];
-#pragma unroll
-      for (int j = 0; j < TILES; ++j) {
-        v[j] = reinterpret_cast<const uint4 *>(slot + (tile0 + j) * kTileBytes)[lane];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          f[j][h][0] = scales[16 * j + 8 * h];
-          f[j][h][1] = there ? scales[other + 16 * j + 8 * h] : 0.0f;
+    int fill = 0;
+    bool ok = true;
+    for (int t = first; t < p.tiles && ok; t += step)
+      for (int chunk = k_begin; chunk < k_end && ok; chunk += kChunk) {
+        ok = mbar_wait_warp(&b.raw_full[q.at], q.phase, p.wait_ns, abort, p.err);
+        const int end = min(chunk + kChunk, k_end);
+        for (int kb = chunk; kb < end && ok; ++kb, ++fill) {
+          if (fill % GROUPS != group) continue;
+          const uint8_t *const slot = raw + q.at * kSlotBytes + (kb - chunk) * kBlockBytes;
+          const int g = group_at(tp, kb) - group_at(tp, chunk);
+          const float *const scales =
+              reinterpret_cast<const float *>(raw + q.at * kSlotBytes + kChunk * kBlockBytes) + g * kLanes + 16 * tile0 + r;
+          // A second group that the block lacks has zeros for numbers, whatever lies in its scales' place.
+          const int other = tp.small ? kLanes : 0;
+          const bool there = !tp.small || 2 * kb + 1 < tp.groups;
+          if (fill >= p.stages) ok = mbar_wait_warp(&b.empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err);
+          if (!ok) break;
+          widen_stage<T, TILES>(slot + tile0 * kTileBytes, scales, other, there, ring_a + s.at * stage_bytes, low, high, odd, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b.full[s.at]);
+          s.next(p.stages, GROUPS);
         }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&b.raw_empty[q.at]);
+        q.next(tp.raw);
       }
-      if (i >= p.stages && !mbar_wait_warp(&b.empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err)) break;
-      const uint32_t to = ring_a + s.at * stage_bytes;
-#pragma unroll
-      for (int j = 0; j < TILES; ++j) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // rows r and r + 8
-          uint32_t x[4], y[4];
-          widen_scaled<T>(h ? v[j].z : v[j].x, f[j][h][0], x);
-          widen_scaled<T>(h ? v[j].w : v[j].y, f[j][h][1], y);
-          const uint32_t at = to + j * 2048 + h * 1024;
-          sts_v4(at + low, odd ? y[0] : x[0], odd ? y[1] : x[1], odd ? y[2] : x[2], odd ? y[3] : x[3]);
-          sts_v4(at + high, odd ? x[0] : y[0], odd ? x[1] : y[1], odd ? x[2] : y[2], odd ? x[3] : y[3]);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&b.full[s.at]);
-        mbar_arrive(&b.raw_empty[q.at]);
-      }
-      s.next(p.stages, GROUPS);
-      q.next(tp.raw, GROUPS);
-      kb += GROUPS;
-    }
   } else if (warp >= 4 + kWiden) {
     const int e = warp - 4 - kWiden;
     int tiles = 0;
@@ -793,12 +860,13 @@ lm_status sizes(const lm_linear_args &a, size_t *first, size_t *all) {
 template <typename T, int NT>
 lm_status product_as(ProductParams p, int sms, cudaStream_t s) {
   const int64_t pairs = up(p.ntiles, kSide), blocks = up(p.rows, 8 * NT);
-  // As many parts of k as give every SM eight warps.
+  // As many parts of k as give every SM two dozen warps.
   p.parts = 1;
-  while (p.parts < kMostWarps && 2 * p.parts <= p.w.ktiles && pairs * blocks * p.parts < 8ll * sms) p.parts *= 2;
+  while (p.parts < kMostWarps && 2 * p.parts <= p.w.ktiles && pairs * blocks * p.parts < 24ll * sms) p.parts *= 2;
   const int warps = p.parts > 4 ? p.parts : 4;
   const dim3 grid(static_cast<unsigned>(up(pairs, warps / p.parts)), static_cast<unsigned>(blocks));
-  const auto kernel = p.w.group == 32 ? product_kernel<T, NT, true> : product_kernel<T, NT, false>;
+  const auto kernel = warps > 8 ? (p.w.group == 32 ? product_kernel<T, NT, true, 16> : product_kernel<T, NT, false, 16>)
+                                : (p.w.group == 32 ? product_kernel<T, NT, true, 8> : product_kernel<T, NT, false, 8>);
   const int shared = warps * 8 * NT * (16 * kSide + 1) * 4;
   return launch_dependent(kernel, grid, 32 * warps, static_cast<size_t>(shared), s, 1, p);
 }
@@ -884,15 +952,14 @@ lm_status tiles(const lm_linear_args &a, const Weight &w, const Operand &x, cons
   p.lanes_inside = 0;  // a tile of W's columns go round inside: its bytes come from L2
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.bn) p.tmem_cols *= 2;
-  // Shared memory: eight blocks of packed bytes at least, more where the operands' stages leave space.
   const int stage_bytes = kLanes * 128 + p.bn * 128;
   const int room = 227 * 1024 - static_cast<int>(sizeof(Barriers));
-  p.stages = (room - 8 * kSlotBytes) / stage_bytes;
+  p.stages = (room - 3 * kSlotBytes) / stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  tp.raw = (room - p.stages * stage_bytes) / kSlotBytes / 4 * 4;  // (every group comes back to its own slots)
+  tp.raw = (room - p.stages * stage_bytes) / kSlotBytes;
   if (tp.raw > kMaxRaw) tp.raw = kMaxRaw;
   const bool four = p.stages >= 4;
-  if (p.stages < (four ? 4 : 2) || tp.raw < 4) return LM_ERR_UNSUPPORTED;
+  if (p.stages < (four ? 4 : 2) || tp.raw < 2) return LM_ERR_UNSUPPORTED;
   p.idesc = idesc_f16(bf16, kLanes, static_cast<uint32_t>(p.bn));
   CUtensorMap cols = {};
   if (lm_status st = make_map(&cols, x, a.k, p.bn, bf16); st != LM_OK) return st;

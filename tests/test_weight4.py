@@ -2,7 +2,10 @@
 
 Tolerance of linear: that of tests/test_linear.py with w = q s; the scale enters after a group's sum, which is
 one more rounding of 2^-24 of each group.  For more than 16 rows each value is first rounded to
-x's type: half a step, 2^-8 (bf16) or 2^-11 (f16, 2^-25 where subnormal), of every |x w|.
+x's type: half a step, 2^-8 (bf16) or 2^-11 (f16, 2^-25 where subnormal), of every |x w|, and up to a sixteenth of
+that for a scale in two parts: q * high + (q * low rounded), high and low of x's type.  In bf16 low's rounding and
+its product's take 2^-17 of the value, 2^-9 of 2^-8; in f16 with scales from 2^-10 on low is off by at most 2^-25 (half
+the least step), times |q| <= 8, against half a step of 2^-21 |q| at the least.
 """
 import copy
 import math
@@ -49,7 +52,7 @@ def check(y, x, w, bias=None, act=None, residual=None, scale=1.0):
         ref = ref + residual.double()
     off = 1.13 * (k + 16) * 2.0 ** -23 * mag
     if rows > 16:
-        off = off + 1.13 * (UNIT[x.dtype] * mag + 2.0 ** -25 * xd.abs().sum(-1, keepdim=True))
+        off = off + 1.13 * (17 / 16 * UNIT[x.dtype] * mag + 2.0 ** -25 * xd.abs().sum(-1, keepdim=True))
     tol = abs(scale) * (off + 2.0 ** -20 * (z.abs() + 1)) + UNIT[y.dtype] * (ref.abs() + 2.0 ** -14)
     assert y.shape == ref.shape
     gap = (y.double() - ref).abs() - tol
@@ -135,6 +138,16 @@ def test_what_is_not_finite(lm, rows):
     x[0, 100] = float("inf")
     y = lm.linear(x, lm.Weight4.pack(q, s, dtype=torch.float16))
     assert not y[0].isfinite().any() and torch.equal(y[1:], ref[1:])
+
+
+@pytest.mark.parametrize("rows", [5, 16, 100, 1000])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size", [2.0 ** -18, 2.0 ** -12, -1.0, 2.0 ** 10])
+def test_scales_of_any_size(lm, rows, dtype, size):
+    q, s = numbers(150, 200, 32, seed=rows)
+    x = torch.randn((rows, 200), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(dtype)
+    w4 = lm.Weight4.pack(q, s * size, group=32, dtype=dtype)
+    check(lm.linear(x, w4, out_dtype=torch.float32), x, value64(q, s * size, 32))
 
 
 @pytest.mark.parametrize("rows", [16, 500])

@@ -17,6 +17,7 @@
 // at the end).
 #include <climits>
 
+#include "f32x2.cuh"
 #include "half.cuh"
 #include "internal.h"
 #include "pdl.cuh"
@@ -119,20 +120,23 @@ struct Part {
   }
 
   // Elements j and j + 1.
-  __device__ __forceinline__ float2 two(int j) const {
-    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
-    else if constexpr (VECTORS) return unpack2<T>(w[j / 2]);
-    else return make_float2(unpack2<T>(w[j]).x, unpack2<T>(w[j + 1]).x);
+  __device__ __forceinline__ f32x2 two(int j) const {
+    float2 v;
+    if constexpr (sizeof(T) == 4) v = make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
+    else if constexpr (VECTORS) v = unpack2<T>(w[j / 2]);
+    else v = make_float2(unpack2<T>(w[j]).x, unpack2<T>(w[j + 1]).x);
+    return pair(v.x, v.y);
   }
 
-  __device__ __forceinline__ void set(int j, float a, float b) {
+  __device__ __forceinline__ void set(int j, f32x2 v) {
+    const float2 f = unpair(v);
     if constexpr (sizeof(T) == 4) {
-      w[j] = __float_as_uint(a);
-      w[j + 1] = __float_as_uint(b);
+      w[j] = __float_as_uint(f.x);
+      w[j + 1] = __float_as_uint(f.y);
     } else if constexpr (VECTORS) {
-      w[j / 2] = pack2<T>(a, b);
+      w[j / 2] = pack2<T>(f.x, f.y);
     } else {
-      const uint32_t p = pack2<T>(a, b);
+      const uint32_t p = pack2<T>(f.x, f.y);
       w[j] = p & 0xffffu;
       w[j + 1] = p >> 16;
     }
@@ -158,6 +162,19 @@ struct Part {
   }
 };
 
+// Two elements, zeros for what lies past the width.
+template <typename P, bool FULL>
+__device__ __forceinline__ f32x2 within(f32x2 v, int j, int t, int width) {
+  if (FULL) return v;
+  const float2 f = unpair(v);
+  return pair(P::place(j, t) < width ? f.x : 0.0f, P::place(j + 1, t) < width ? f.y : 0.0f);
+}
+
+__device__ __forceinline__ float joined(f32x2 v) {
+  const float2 f = unpair(v);
+  return f.x + f.y;
+}
+
 // Threads of a CTA that is alone on its SM, for so many registers a thread: whole teams, at most 15
 // of several warps (a CTA has 16 barriers).
 constexpr int threads_for(int team, int regs) {
@@ -170,7 +187,7 @@ constexpr int threads_for(int team, int regs) {
 
 // The weight and bias stay in registers where a thread has 8 elements, else in shared memory.
 template <typename P, int NE>
-constexpr int forward_regs() { return 56 + 2 * P::kWords + (NE == 8 ? 16 : 0); }
+constexpr int forward_regs() { return 52 + P::kWords + NE + (NE == 8 ? 16 : 0); }
 template <typename P, int TEAM, int NE>
 constexpr int forward_threads() { return TEAM <= 32 ? 256 : TEAM; }
 template <typename P, int TEAM, int NE>
@@ -179,7 +196,8 @@ constexpr int forward_ctas() {
   return n < 1 ? 1 : n;
 }
 
-template <typename T, int TEAM, int NE, bool VECTORS>
+// FULL: the width is what a team holds.
+template <typename T, int TEAM, int NE, bool VECTORS, bool FULL>
 __global__ void __launch_bounds__(forward_threads<Part<T, TEAM, NE, VECTORS>, TEAM, NE>(),
                                   forward_ctas<Part<T, TEAM, NE, VECTORS>, TEAM, NE>()) norm_rows(const NormParams p) {
   using P = Part<T, TEAM, NE, VECTORS>;
@@ -187,24 +205,24 @@ __global__ void __launch_bounds__(forward_threads<Part<T, TEAM, NE, VECTORS>, TE
   extern __shared__ float4 dynamic[];  // the sums' places; then weight and bias of two elements, [NE / 2][TEAM]
   TeamSum<TEAM> sum{reinterpret_cast<float2(*)[32]>(dynamic)};
   float4 *const params = dynamic + kScratch / sizeof(float4);
-  const int t = static_cast<int>(threadIdx.x) % TEAM, width = static_cast<int>(p.width);
+  const int t = static_cast<int>(threadIdx.x) % TEAM, width = FULL ? TEAM * NE : static_cast<int>(p.width);
   const int64_t teams = static_cast<int64_t>(gridDim.x) * (blockDim.x / TEAM);
   const int64_t team = static_cast<int64_t>(blockIdx.x) * (blockDim.x / TEAM) + threadIdx.x / TEAM;
   const int64_t lead = TEAM < 32 ? team - threadIdx.x % 32 / TEAM : team;  // the warp's first
   const float inv = 1.0f / static_cast<float>(width);
   pdl_launch();
   pdl_wait();
-  P now, next;
-  now.load(static_cast<const T *>(p.x) + team * p.x_row, width, t, team < p.rows);
+  P next;
+  next.load(static_cast<const T *>(p.x) + team * p.x_row, width, t, team < p.rows);
   auto param = [&](int j, int thread) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const int i = P::place(j, thread), k = P::place(j + 1, thread);
     if (i < width) {
       v.x = param_at<T>(p.weight, p.weight_f32, i, 1.0f);
-      v.y = param_at<T>(p.bias, p.bias_f32, i, 0.0f);
+      v.z = param_at<T>(p.bias, p.bias_f32, i, 0.0f);
     }
     if (k < width) {
-      v.z = param_at<T>(p.weight, p.weight_f32, k, 1.0f);
+      v.y = param_at<T>(p.weight, p.weight_f32, k, 1.0f);
       v.w = param_at<T>(p.bias, p.bias_f32, k, 0.0f);
     }
     return v;
@@ -219,23 +237,23 @@ __global__ void __launch_bounds__(forward_threads<Part<T, TEAM, NE, VECTORS>, TE
   }
   for (int64_t row = team, first = lead; first < p.rows; row += teams, first += teams) {
     const bool any = row < p.rows;
+    f32x2 v[NE / 2], s = both(0.0f), q = both(0.0f);
+#pragma unroll
+    for (int j = 0; j < NE; j += 2) {
+      v[j / 2] = next.two(j);
+      s = add2(s, v[j / 2]);
+    }
     next.load(static_cast<const T *>(p.x) + (row + teams) * p.x_row, width, t, row + teams < p.rows);
-    float s = 0.0f, q = 0.0f;
+    const float mean = sum(joined(s), 0.0f).x * inv;
+    s = both(0.0f);
 #pragma unroll
     for (int j = 0; j < NE; j += 2) {
-      const float2 v = now.two(j);
-      s += v.x + v.y;
+      const f32x2 d = within<P, FULL>(add2(v[j / 2], both(-mean)), j, t, width);
+      v[j / 2] = d;
+      s = add2(s, d);
+      q = fma2(d, d, q);
     }
-    const float mean = sum(s, 0.0f).x * inv;
-    s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NE; j += 2) {
-      const float2 v = now.two(j);
-      const float d0 = P::place(j, t) < width ? v.x - mean : 0.0f, d1 = P::place(j + 1, t) < width ? v.y - mean : 0.0f;
-      s += d0 + d1;
-      q = fmaf(d0, d0, fmaf(d1, d1, q));
-    }
-    const float2 u = sum(s, q);
+    const float2 u = sum(joined(s), joined(q));
     const float off = u.x * inv, var = u.y * inv - off * off;
     const float r = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + p.eps);
     if (p.stats && t == 0 && any) {
@@ -243,15 +261,15 @@ __global__ void __launch_bounds__(forward_threads<Part<T, TEAM, NE, VECTORS>, TE
       p.stats[p.rows + row] = off;
       p.stats[2 * p.rows + row] = r;
     }
+    if (!any) continue;
+    P out;
+    const f32x2 r2 = both(r), c2 = both(-off * r);
 #pragma unroll
     for (int j = 0; j < NE; j += 2) {
-      const float2 v = now.two(j);
       const float4 c = HOLD ? held[HOLD ? j / 2 : 0] : params[j / 2 * TEAM + t];
-      const float n0 = ((v.x - mean) - off) * r, n1 = ((v.y - mean) - off) * r;
-      now.set(j, fmaf(n0, c.x, c.y), fmaf(n1, c.z, c.w));
+      out.set(j, fma2(fma2(v[j / 2], r2, c2), pair(c.x, c.y), pair(c.z, c.w)));
     }
-    if (any) now.store(static_cast<T *>(p.out) + row * p.out_row, width, t);
-    now = next;
+    out.store(static_cast<T *>(p.out) + row * p.out_row, width, t);
   }
 }
 
@@ -262,10 +280,10 @@ template <typename P, int TEAM>
 constexpr bool backward_ahead() { return TEAM < 512 || P::kWords < 16; }
 template <typename P, int TEAM, int NE>
 constexpr int backward_threads() {
-  return threads_for(TEAM, 62 + 2 * NE + (backward_ahead<P, TEAM>() ? 4 : 2) * P::kWords);
+  return threads_for(TEAM, 66 + 4 * NE + (backward_ahead<P, TEAM>() ? 2 : 0) * P::kWords);
 }
 
-template <typename T, int TEAM, int NE, bool VECTORS>
+template <typename T, int TEAM, int NE, bool VECTORS, bool FULL>
 __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, TEAM, NE>(), 1)
     norm_backward(const NormParams p) {
   using P = Part<T, TEAM, NE, VECTORS>;
@@ -274,19 +292,28 @@ __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, T
   extern __shared__ float4 dynamic[];  // the sums' places; the weight of two elements, [NE / 2][TEAM]; [..][NE][TEAM]
   TeamSum<TEAM> sum{reinterpret_cast<float2(*)[32]>(dynamic)};
   float2 *const shared = reinterpret_cast<float2 *>(dynamic + kScratch / sizeof(float4));
-  const int t = static_cast<int>(threadIdx.x) % TEAM, width = static_cast<int>(p.width);
+  const int t = static_cast<int>(threadIdx.x) % TEAM, width = FULL ? TEAM * NE : static_cast<int>(p.width);
   const int64_t teams = static_cast<int64_t>(gridDim.x) * (blockDim.x / TEAM);
   const int64_t team = static_cast<int64_t>(blockIdx.x) * (blockDim.x / TEAM) + threadIdx.x / TEAM;
   const int64_t lead = TEAM < 32 ? team - threadIdx.x % 32 / TEAM : team;
   const float inv = 1.0f / static_cast<float>(width);
-  float dw[NE], db[NE];
+  f32x2 dw2[NE / 2], db2[NE / 2];
 #pragma unroll
-  for (int j = 0; j < NE; ++j) dw[j] = db[j] = 0.0f;
+  for (int j = 0; j < NE / 2; ++j) dw2[j] = db2[j] = both(0.0f);
   pdl_launch();
   pdl_wait();
-  P x, g, next_x, next_g;
-  x.load(static_cast<const T *>(p.x) + team * p.x_row, width, t, team < p.rows);
-  g.load(static_cast<const T *>(p.grad) + team * p.grad_row, width, t, team < p.rows);
+  P next_x, next_g;
+  float mean = 0.0f, off = 0.0f, r = 0.0f;
+  auto load = [&](int64_t row) {
+    next_x.load(static_cast<const T *>(p.x) + row * p.x_row, width, t, row < p.rows);
+    next_g.load(static_cast<const T *>(p.grad) + row * p.grad_row, width, t, row < p.rows);
+    if (row < p.rows) {
+      mean = p.stats[row];
+      off = p.stats[p.rows + row];
+      r = p.stats[2 * p.rows + row];
+    }
+  };
+  load(team);
   for (int i = threadIdx.x; i < PLACES / 2; i += blockDim.x) {
     const int a = P::place(i / TEAM * 2, i % TEAM), b = P::place(i / TEAM * 2 + 1, i % TEAM);
     shared[i] = make_float2(a < width ? param_at<T>(p.weight, p.weight_f32, a, 1.0f) : 0.0f,
@@ -294,58 +321,43 @@ __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, T
   }
   __syncthreads();
   for (int64_t row = team, first = lead; first < p.rows; row += teams, first += teams) {
-    const bool any = row < p.rows, more = row + teams < p.rows;
-    float mean = 0.0f, off = 0.0f, r = 0.0f;
-    if (any) {
-      mean = p.stats[row];
-      off = p.stats[p.rows + row];
-      r = p.stats[2 * p.rows + row];
-    }
-    if (AHEAD) {
-      next_x.load(static_cast<const T *>(p.x) + (row + teams) * p.x_row, width, t, more);
-      next_g.load(static_cast<const T *>(p.grad) + (row + teams) * p.grad_row, width, t, more);
-    }
-    float s = 0.0f, q = 0.0f;
+    f32x2 n[NE / 2], h[NE / 2], s = both(0.0f), q = both(0.0f);
+    const f32x2 m2 = both(-mean), r2 = both(r), o2 = both(-off * r);
+    const float scale = r;
 #pragma unroll
     for (int j = 0; j < NE; j += 2) {
-      const float2 v = x.two(j), e = g.two(j), w = shared[j / 2 * TEAM + t];
-      const float n0 = ((v.x - mean) - off) * r, n1 = ((v.y - mean) - off) * r;
-      // (A place past the width has no part, whatever its n.)
-      if (P::place(j, t) < width) {
-        const float h = e.x * w.x;
-        s += h;
-        q = fmaf(h, n0, q);
-        dw[j] = fmaf(e.x, n0, dw[j]);
-        db[j] += e.x;
-      }
-      if (P::place(j + 1, t) < width) {
-        const float h = e.y * w.y;
-        s += h;
-        q = fmaf(h, n1, q);
-        dw[j + 1] = fmaf(e.y, n1, dw[j + 1]);
-        db[j + 1] += e.y;
-      }
+      const float2 w = shared[j / 2 * TEAM + t];
+      // (A place past the width has no part, whatever its row.)
+      const f32x2 g = next_g.two(j), u = within<P, FULL>(fma2(add2(next_x.two(j), m2), r2, o2), j, t, width);
+      n[j / 2] = u;
+      h[j / 2] = mul2(g, pair(w.x, w.y));
+      s = add2(s, h[j / 2]);
+      q = fma2(h[j / 2], u, q);
+      dw2[j / 2] = fma2(g, u, dw2[j / 2]);
+      db2[j / 2] = add2(db2[j / 2], g);
     }
-    const float2 u = sum(s, q);
-    if (p.out) {
-      const float c1 = u.x * inv, c2 = u.y * inv;
+    if (AHEAD) load(row + teams);
+    const float2 u = sum(joined(s), joined(q));
+    if (p.out && row < p.rows) {
+      // dx = h r - avg(h) r - n avg(h n) r
+      const f32x2 k = both(scale), c1 = both(-(u.x * inv) * scale), c2 = both(-(u.y * inv) * scale);
+      P out;
 #pragma unroll
-      for (int j = 0; j < NE; j += 2) {
-        const float2 v = x.two(j), e = g.two(j), w = shared[j / 2 * TEAM + t];
-        const float n0 = ((v.x - mean) - off) * r, n1 = ((v.y - mean) - off) * r;
-        x.set(j, fmaf(-n0, c2, fmaf(e.x, w.x, -c1)) * r, fmaf(-n1, c2, fmaf(e.y, w.y, -c1)) * r);
-      }
-      if (any) x.store(static_cast<T *>(p.out) + row * p.out_row, width, t);
+      for (int j = 0; j < NE; j += 2) out.set(j, fma2(n[j / 2], c2, fma2(h[j / 2], k, c1)));
+      out.store(static_cast<T *>(p.out) + row * p.out_row, width, t);
     }
-    if (AHEAD) {
-      x = next_x;
-      g = next_g;
-    } else {
-      x.load(static_cast<const T *>(p.x) + (row + teams) * p.x_row, width, t, more);
-      g.load(static_cast<const T *>(p.grad) + (row + teams) * p.grad_row, width, t, more);
-    }
+    if (!AHEAD) load(row + teams);
   }
   if (!p.partial) return;
+  float dw[NE], db[NE];
+#pragma unroll
+  for (int j = 0; j < NE; j += 2) {
+    const float2 a = unpair(dw2[j / 2]), b = unpair(db2[j / 2]);
+    dw[j] = a.x;
+    dw[j + 1] = a.y;
+    db[j] = b.x;
+    db[j + 1] = b.y;
+  }
   // A warp's teams join by shuffles; then the upper half of the groups (teams, or warps of smaller ones) hand
   // their sums to the lower, until one is left.
   constexpr int GROUP = TEAM < 32 ? 32 : TEAM;
@@ -388,28 +400,26 @@ __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, T
   }
 }
 
-// Joins the parts: a CTA has 32 columns, its warps every eighth part; then the warps in their order.
+// Joins the parts: a CTA has 32 columns, warp w parts w, w + 32, ..., and then one column.
 template <typename T>
-__global__ void __launch_bounds__(256) norm_join(const float *partial, int parts, int64_t width, void *dweight,
-                                                 int weight_f32, void *dbias, int bias_f32) {
-  __shared__ float sums[8][32];
+__global__ void __launch_bounds__(1024) norm_join(const float *partial, int parts, int64_t width, void *dweight,
+                                                  int weight_f32, void *dbias, int bias_f32) {
+  __shared__ float sums[32][33];
   pdl_launch();
   pdl_wait();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.0f;
   if (i < 2 * width) {
 #pragma unroll 8
-    for (int c = warp; c < parts; c += 8) s += partial[static_cast<int64_t>(c) * 2 * width + i];
+    for (int c = warp; c < parts; c += 32) s += partial[static_cast<int64_t>(c) * 2 * width + i];
   }
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp != 0 || i >= 2 * width) return;
-  s = 0.0f;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) s += sums[c][lane];
+  s = warp_sum(sums[lane][warp]);
+  i = static_cast<int64_t>(blockIdx.x) * 32 + warp;
   void *const to = i < width ? dweight : dbias;
-  if (!to) return;
+  if (lane != 0 || i >= 2 * width || !to) return;
   const int64_t at = i < width ? i : i - width;
   if (i < width ? weight_f32 : bias_f32) {
     static_cast<float *>(to)[at] = s;
@@ -578,7 +588,7 @@ lm_status forward_as(const NormParams &p, int sms, cudaStream_t s) {
   const int threads = spread(TEAM, p.rows, most, sms);
   const int64_t ctas = (p.rows + threads / TEAM - 1) / (threads / TEAM);
   const int64_t held = static_cast<int64_t>(sms) * forward_ctas<P, TEAM, NE>() * (most / threads);
-  const auto kernel = norm_rows<T, TEAM, NE, VECTORS>;
+  const auto kernel = VECTORS && p.width == TEAM * NE ? norm_rows<T, TEAM, NE, VECTORS, VECTORS> : norm_rows<T, TEAM, NE, VECTORS, false>;
   const size_t shared = kScratch + (NE == 8 ? 0 : sizeof(float4) * NE / 2 * TEAM);
   if (shared > 40 * 1024)
     if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), static_cast<int>(shared)); st != LM_OK)
@@ -594,7 +604,8 @@ lm_status backward_as(NormParams &p, int sms, cudaStream_t s) {
   p.parts = static_cast<int>(least(least(ctas, kMostParts), sms));
   const int groups = threads / (TEAM < 32 ? 32 : TEAM);
   const size_t shared = kScratch + sizeof(float2) * TEAM * NE / 2 + sizeof(float2) * TEAM * NE * static_cast<size_t>(groups / 2);
-  const auto kernel = norm_backward<T, TEAM, NE, VECTORS>;
+  const auto kernel =
+      VECTORS && p.width == TEAM * NE ? norm_backward<T, TEAM, NE, VECTORS, VECTORS> : norm_backward<T, TEAM, NE, VECTORS, false>;
   if (shared > 40 * 1024)
     if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), static_cast<int>(shared)); st != LM_OK)
       return st;
@@ -669,7 +680,7 @@ lm_status backward(NormParams p, void *dweight, void *dbias, cudaStream_t s) {
     }
   }
   if (!partial) return LM_OK;
-  return launch_dependent(norm_join<T>, dim3(static_cast<unsigned>((2 * p.width + 31) / 32)), 256, 0, s, 1,
+  return launch_dependent(norm_join<T>, dim3(static_cast<unsigned>((2 * p.width + 31) / 32)), 1024, 0, s, 1,
                           static_cast<const float *>(partial), p.parts, p.width, dweight, p.weight_f32, dbias, p.bias_f32);
 }
 

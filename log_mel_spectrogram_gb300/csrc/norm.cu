@@ -162,6 +162,71 @@ struct Part {
   }
 };
 
+// Rows on their way: in shared memory, by asynchronous copies of 16 bytes that each thread makes for itself (three
+// rows of 16-bit elements, two of 32), or where rows are off 16-byte boundaries one row in registers.
+template <typename P, typename T, int NE, bool VECTORS>
+struct Feed {
+  static constexpr int kVectors = VECTORS ? NE * static_cast<int>(sizeof(T)) / 16 : 0;
+  static constexpr int kSlots = VECTORS ? (sizeof(T) == 2 ? 4 : 3) : 2;
+  static constexpr int kAhead = kSlots - 1;
+  uint32_t base, step;  // this thread's first vector, and from vector to vector
+  uint32_t in, out, last;
+  P held;
+
+  // Bytes a thread takes.
+  static constexpr size_t kBytes = static_cast<size_t>(VECTORS ? kSlots * kVectors * 16 : 0);
+
+  __device__ __forceinline__ Feed(void *shared) {
+    base = static_cast<uint32_t>(__cvta_generic_to_shared(shared)) + threadIdx.x * 16;
+    step = blockDim.x * 16;
+    in = out = base;
+    last = base + (kSlots - 1) * kVectors * step;
+  }
+
+  __device__ __forceinline__ void push(const T *row, int width, int t, bool any) {
+    if constexpr (VECTORS) {
+#pragma unroll
+      for (int v = 0; v < kVectors; ++v) {
+        const bool there = any && P::place(v * P::kEach, t) < width;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(in + static_cast<uint32_t>(v) * step),
+                     "l"(there ? row + P::place(v * P::kEach, t) : row), "r"(there ? 16 : 0)
+                     : "memory");
+      }
+      in = in == last ? base : in + kVectors * step;
+    } else {
+      held.load(row, width, t, any);
+    }
+  }
+
+  // The oldest row; its place is written again by the second push from here.
+  __device__ __forceinline__ P pop() {
+    P r;
+    if constexpr (VECTORS) {
+#pragma unroll
+      for (int v = 0; v < kVectors; ++v)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.w[4 * v]), "=r"(r.w[4 * v + 1]), "=r"(r.w[4 * v + 2]), "=r"(r.w[4 * v + 3])
+                     : "r"(out + static_cast<uint32_t>(v) * step)
+                     : "memory");
+      out = out == last ? base : out + kVectors * step;
+    } else {
+      r = held;
+    }
+    return r;
+  }
+
+  static __device__ __forceinline__ void commit() {
+    if constexpr (VECTORS) asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // All but the last kAhead - 1 rows are there.
+  static __device__ __forceinline__ void wait() {
+    if constexpr (VECTORS) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+  }
+  static __device__ __forceinline__ void drain() {
+    if constexpr (VECTORS) asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+};
+
 // Two elements, zeros for what lies past the width.
 template <typename P, bool FULL>
 __device__ __forceinline__ f32x2 within(f32x2 v, int j, int t, int width) {
@@ -185,9 +250,10 @@ constexpr int threads_for(int team, int regs) {
 
 // ---- forward ----
 
-// The weight and bias stay in registers where a thread has 8 elements, else in shared memory.
+// The weight and bias stay in registers where a thread has 8 elements, else in shared memory; for teams of 512 with 32
+// elements, whose rows take it all, they are read from the L1 each time.
 template <typename P, int NE>
-constexpr int forward_regs() { return 52 + P::kWords + NE + (NE == 8 ? 16 : 0); }
+constexpr int forward_regs() { return 62 + P::kWords / 2 + NE + (NE == 8 ? 16 : 0); }
 template <typename P, int TEAM, int NE>
 constexpr int forward_threads() { return TEAM <= 32 ? 256 : TEAM; }
 template <typename P, int TEAM, int NE>
@@ -201,7 +267,7 @@ template <typename T, int TEAM, int NE, bool VECTORS, bool FULL>
 __global__ void __launch_bounds__(forward_threads<Part<T, TEAM, NE, VECTORS>, TEAM, NE>(),
                                   forward_ctas<Part<T, TEAM, NE, VECTORS>, TEAM, NE>()) norm_rows(const NormParams p) {
   using P = Part<T, TEAM, NE, VECTORS>;
-  constexpr bool HOLD = NE == 8;
+  constexpr bool HOLD = NE == 8, SHARED = !HOLD && TEAM * NE <= 8192;
   extern __shared__ float4 dynamic[];  // the sums' places; then weight and bias of two elements, [NE / 2][TEAM]
   TeamSum<TEAM> sum{reinterpret_cast<float2(*)[32]>(dynamic)};
   float4 *const params = dynamic + kScratch / sizeof(float4);
@@ -212,8 +278,18 @@ __global__ void __launch_bounds__(forward_threads<Part<T, TEAM, NE, VECTORS>, TE
   const float inv = 1.0f / static_cast<float>(width);
   pdl_launch();
   pdl_wait();
-  P next;
-  next.load(static_cast<const T *>(p.x) + team * p.x_row, width, t, team < p.rows);
+  Feed<P, T, NE, VECTORS> feed(params + (SHARED ? NE / 2 * TEAM : 0));
+  const int64_t x_step = teams * p.x_row;
+  const T *x = static_cast<const T *>(p.x) + team * p.x_row;
+  int64_t fetched = team;  // the row to fetch next
+  auto push = [&]() {
+    feed.push(fetched < p.rows ? x : static_cast<const T *>(p.x), width, t, fetched < p.rows);
+    feed.commit();
+    x += x_step;
+    fetched += teams;
+  };
+#pragma unroll
+  for (int i = 0; i < feed.kAhead; ++i) push();
   auto param = [&](int j, int thread) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const int i = P::place(j, thread), k = P::place(j + 1, thread);
@@ -231,19 +307,21 @@ __global__ void __launch_bounds__(forward_threads<Part<T, TEAM, NE, VECTORS>, TE
   if (HOLD) {
 #pragma unroll
     for (int j = 0; j < NE; j += 2) held[HOLD ? j / 2 : 0] = param(j, t);
-  } else {
+  } else if (SHARED) {
     for (int i = threadIdx.x; i < NE / 2 * TEAM; i += blockDim.x) params[i] = param(i / TEAM * 2, i % TEAM);
     __syncthreads();
   }
   for (int64_t row = team, first = lead; first < p.rows; row += teams, first += teams) {
     const bool any = row < p.rows;
     f32x2 v[NE / 2], s = both(0.0f), q = both(0.0f);
+    feed.wait();
+    const P now = feed.pop();
+    push();
 #pragma unroll
     for (int j = 0; j < NE; j += 2) {
-      v[j / 2] = next.two(j);
+      v[j / 2] = now.two(j);
       s = add2(s, v[j / 2]);
     }
-    next.load(static_cast<const T *>(p.x) + (row + teams) * p.x_row, width, t, row + teams < p.rows);
     const float mean = sum(joined(s), 0.0f).x * inv;
     s = both(0.0f);
 #pragma unroll
@@ -266,30 +344,28 @@ __global__ void __launch_bounds__(forward_threads<Part<T, TEAM, NE, VECTORS>, TE
     const f32x2 r2 = both(r), c2 = both(-off * r);
 #pragma unroll
     for (int j = 0; j < NE; j += 2) {
-      const float4 c = HOLD ? held[HOLD ? j / 2 : 0] : params[j / 2 * TEAM + t];
+      const float4 c = HOLD ? held[HOLD ? j / 2 : 0] : SHARED ? params[j / 2 * TEAM + t] : param(j, t);
       out.set(j, fma2(fma2(v[j / 2], r2, c2), pair(c.x, c.y), pair(c.z, c.w)));
     }
     out.store(static_cast<T *>(p.out) + row * p.out_row, width, t);
   }
+  feed.drain();
 }
 
 // ---- backward ----
 
-// The next row's elements have registers unless a team of 512 needs them all.
-template <typename P, int TEAM>
-constexpr bool backward_ahead() { return TEAM < 512 || P::kWords < 16; }
+// Registers that a thread needs, and shared memory for its rows.
 template <typename P, int TEAM, int NE>
-constexpr int backward_threads() {
-  return threads_for(TEAM, 66 + 4 * NE + (backward_ahead<P, TEAM>() ? 2 : 0) * P::kWords);
-}
+constexpr int backward_threads() { return threads_for(TEAM, 58 + 4 * NE + (P::kEach == 1 ? 2 * P::kWords : 0)); }
 
 template <typename T, int TEAM, int NE, bool VECTORS, bool FULL>
 __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, TEAM, NE>(), 1)
     norm_backward(const NormParams p) {
   using P = Part<T, TEAM, NE, VECTORS>;
-  constexpr bool AHEAD = backward_ahead<P, TEAM>();
   constexpr int PLACES = NE * TEAM;
-  extern __shared__ float4 dynamic[];  // the sums' places; the weight of two elements, [NE / 2][TEAM]; [..][NE][TEAM]
+  using Rows = Feed<P, T, NE, VECTORS>;
+  // The sums' places; the weight of two elements, [NE / 2][TEAM]; rows of x and of the gradient, later [..][NE][TEAM].
+  extern __shared__ float4 dynamic[];
   TeamSum<TEAM> sum{reinterpret_cast<float2(*)[32]>(dynamic)};
   float2 *const shared = reinterpret_cast<float2 *>(dynamic + kScratch / sizeof(float4));
   const int t = static_cast<int>(threadIdx.x) % TEAM, width = FULL ? TEAM * NE : static_cast<int>(p.width);
@@ -302,18 +378,30 @@ __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, T
   for (int j = 0; j < NE / 2; ++j) dw2[j] = db2[j] = both(0.0f);
   pdl_launch();
   pdl_wait();
-  P next_x, next_g;
-  float mean = 0.0f, off = 0.0f, r = 0.0f;
-  auto load = [&](int64_t row) {
-    next_x.load(static_cast<const T *>(p.x) + row * p.x_row, width, t, row < p.rows);
-    next_g.load(static_cast<const T *>(p.grad) + row * p.grad_row, width, t, row < p.rows);
-    if (row < p.rows) {
-      mean = p.stats[row];
-      off = p.stats[p.rows + row];
-      r = p.stats[2 * p.rows + row];
-    }
+  char *const rows = reinterpret_cast<char *>(shared + PLACES / 2);
+  Rows feed_x(rows), feed_g(rows + Rows::kBytes * blockDim.x);
+  const int64_t x_step = teams * p.x_row, g_step = teams * p.grad_row;
+  const T *from_x = static_cast<const T *>(p.x) + team * p.x_row, *from_g = static_cast<const T *>(p.grad) + team * p.grad_row;
+  int64_t fetched = team;  // the row to fetch next
+  auto push = [&]() {
+    const bool there = fetched < p.rows;
+    feed_x.push(there ? from_x : static_cast<const T *>(p.x), width, t, there);
+    feed_g.push(there ? from_g : static_cast<const T *>(p.grad), width, t, there);
+    Rows::commit();
+    from_x += x_step;
+    from_g += g_step;
+    fetched += teams;
   };
-  load(team);
+#pragma unroll
+  for (int i = 0; i < Rows::kAhead; ++i) push();
+  float mean = 0.0f, off = 0.0f, r = 0.0f;
+  auto load_stats = [&](int64_t row) {
+    if (row >= p.rows) return;
+    mean = p.stats[row];
+    off = p.stats[p.rows + row];
+    r = p.stats[2 * p.rows + row];
+  };
+  load_stats(team);
   for (int i = threadIdx.x; i < PLACES / 2; i += blockDim.x) {
     const int a = P::place(i / TEAM * 2, i % TEAM), b = P::place(i / TEAM * 2 + 1, i % TEAM);
     shared[i] = make_float2(a < width ? param_at<T>(p.weight, p.weight_f32, a, 1.0f) : 0.0f,
@@ -324,11 +412,15 @@ __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, T
     f32x2 n[NE / 2], h[NE / 2], s = both(0.0f), q = both(0.0f);
     const f32x2 m2 = both(-mean), r2 = both(r), o2 = both(-off * r);
     const float scale = r;
+    Rows::wait();
+    const P x = feed_x.pop(), e = feed_g.pop();
+    push();
+    load_stats(row + teams);
 #pragma unroll
     for (int j = 0; j < NE; j += 2) {
       const float2 w = shared[j / 2 * TEAM + t];
       // (A place past the width has no part, whatever its row.)
-      const f32x2 g = next_g.two(j), u = within<P, FULL>(fma2(add2(next_x.two(j), m2), r2, o2), j, t, width);
+      const f32x2 g = e.two(j), u = within<P, FULL>(fma2(add2(x.two(j), m2), r2, o2), j, t, width);
       n[j / 2] = u;
       h[j / 2] = mul2(g, pair(w.x, w.y));
       s = add2(s, h[j / 2]);
@@ -336,7 +428,6 @@ __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, T
       dw2[j / 2] = fma2(g, u, dw2[j / 2]);
       db2[j / 2] = add2(db2[j / 2], g);
     }
-    if (AHEAD) load(row + teams);
     const float2 u = sum(joined(s), joined(q));
     if (p.out && row < p.rows) {
       // dx = h r - avg(h) r - n avg(h n) r
@@ -346,9 +437,10 @@ __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, T
       for (int j = 0; j < NE; j += 2) out.set(j, fma2(n[j / 2], c2, fma2(h[j / 2], k, c1)));
       out.store(static_cast<T *>(p.out) + row * p.out_row, width, t);
     }
-    if (!AHEAD) load(row + teams);
   }
+  Rows::drain();
   if (!p.partial) return;
+  __syncthreads();  // the rows' places are free
   float dw[NE], db[NE];
 #pragma unroll
   for (int j = 0; j < NE; j += 2) {
@@ -370,7 +462,7 @@ __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, T
     }
   const int group = static_cast<int>(threadIdx.x) / GROUP;
   const bool mine = static_cast<int>(threadIdx.x) % GROUP < TEAM;
-  float2 *const slots = shared + PLACES / 2;
+  float2 *const slots = reinterpret_cast<float2 *>(rows);
   for (int n = static_cast<int>(blockDim.x) / GROUP; n > 1;) {
     const int half = (n + 1) / 2;
     if (group >= half && group < n && mine) {
@@ -559,6 +651,7 @@ Shape forward_shape(int64_t rows, int64_t width, int sms) {
   auto each = [&](int team) { return width <= 8 * team ? 8 : width <= 16 * team ? 16 : 32; };
   if (width > 512 * 32) return {0, 0};
   if (width <= 64) return {8, 8};
+  if (width <= 128) return {16, 8};
   if (width <= (few ? 256 : 1024)) return {32, each(32)};
   if (width <= (few ? 1024 : 4096)) return {128, each(128)};
   return {512, each(512) < 16 ? 16 : each(512)};
@@ -568,6 +661,7 @@ Shape forward_shape(int64_t rows, int64_t width, int sms) {
 Shape backward_shape(int64_t width) {
   if (width > 512 * 16) return {0, 0};
   if (width <= 64) return {8, 8};
+  if (width <= 128) return {16, 8};
   if (width <= 256) return {32, 8};
   int team = 32;
   while (team * 16 < width) team *= 2;
@@ -587,13 +681,16 @@ lm_status forward_as(const NormParams &p, int sms, cudaStream_t s) {
   constexpr int most = forward_threads<P, TEAM, NE>();
   const int threads = spread(TEAM, p.rows, most, sms);
   const int64_t ctas = (p.rows + threads / TEAM - 1) / (threads / TEAM);
-  const int64_t held = static_cast<int64_t>(sms) * forward_ctas<P, TEAM, NE>() * (most / threads);
+  const size_t shared = kScratch + (NE == 8 || TEAM * NE > 8192 ? 0 : sizeof(float4) * NE / 2 * TEAM) +
+                        Feed<P, T, NE, VECTORS>::kBytes * static_cast<size_t>(threads);
+  int64_t each = forward_ctas<P, TEAM, NE>() * (most / threads);  // CTAs of an SM
+  each = least(each, static_cast<int64_t>(222 * 1024 / (shared + 1024)));
+  if (each < 1) each = 1;
   const auto kernel = VECTORS && p.width == TEAM * NE ? norm_rows<T, TEAM, NE, VECTORS, VECTORS> : norm_rows<T, TEAM, NE, VECTORS, false>;
-  const size_t shared = kScratch + (NE == 8 ? 0 : sizeof(float4) * NE / 2 * TEAM);
   if (shared > 40 * 1024)
     if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), static_cast<int>(shared)); st != LM_OK)
       return st;
-  return launch_dependent(kernel, dim3(static_cast<unsigned>(least(ctas, held))), threads, shared, s, 1, p);
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(least(ctas, sms * each))), threads, shared, s, 1, p);
 }
 
 template <typename T, int TEAM, int NE, bool VECTORS>
@@ -603,7 +700,9 @@ lm_status backward_as(NormParams &p, int sms, cudaStream_t s) {
   const int64_t ctas = (p.rows + threads / TEAM - 1) / (threads / TEAM);
   p.parts = static_cast<int>(least(least(ctas, kMostParts), sms));
   const int groups = threads / (TEAM < 32 ? 32 : TEAM);
-  const size_t shared = kScratch + sizeof(float2) * TEAM * NE / 2 + sizeof(float2) * TEAM * NE * static_cast<size_t>(groups / 2);
+  const size_t rows = 2 * Feed<P, T, NE, VECTORS>::kBytes * static_cast<size_t>(threads);
+  const size_t sums = sizeof(float2) * TEAM * NE * static_cast<size_t>(groups / 2);
+  const size_t shared = kScratch + sizeof(float2) * TEAM * NE / 2 + (rows > sums ? rows : sums);
   const auto kernel =
       VECTORS && p.width == TEAM * NE ? norm_backward<T, TEAM, NE, VECTORS, VECTORS> : norm_backward<T, TEAM, NE, VECTORS, false>;
   if (shared > 40 * 1024)
@@ -615,6 +714,7 @@ lm_status backward_as(NormParams &p, int sms, cudaStream_t s) {
 template <typename T, bool VECTORS>
 lm_status forward_shaped(const NormParams &p, Shape h, int sms, cudaStream_t s) {
   if (h.team == 8) return forward_as<T, 8, 8, VECTORS>(p, sms, s);
+  if (h.team == 16) return forward_as<T, 16, 8, VECTORS>(p, sms, s);
   if (h.team == 32)
     return h.each == 8 ? forward_as<T, 32, 8, VECTORS>(p, sms, s) : h.each == 16 ? forward_as<T, 32, 16, VECTORS>(p, sms, s)
                                                                                  : forward_as<T, 32, 32, VECTORS>(p, sms, s);
@@ -629,6 +729,7 @@ template <typename T, bool VECTORS>
 lm_status backward_shaped(NormParams &p, Shape h, int sms, cudaStream_t s) {
   switch (h.team) {
     case 8: return backward_as<T, 8, 8, VECTORS>(p, sms, s);
+    case 16: return backward_as<T, 16, 8, VECTORS>(p, sms, s);
     case 32: return h.each == 8 ? backward_as<T, 32, 8, VECTORS>(p, sms, s) : backward_as<T, 32, 16, VECTORS>(p, sms, s);
     case 64: return backward_as<T, 64, 16, VECTORS>(p, sms, s);
     case 128: return backward_as<T, 128, 16, VECTORS>(p, sms, s);

@@ -712,14 +712,8 @@ lm_status start(const lm_gated_args &a, Plan *pl, void *workspace, const WaitFau
   l->fault = fault;
   l->stream = s;
   l->bf16 = a.dtype == LM_BF16;
-  char *to = static_cast<char *>(workspace) + pl->copies;
-  for (Operand *o : {&pl->x, &pl->gate, &pl->up_}) {
-    const size_t bytes = o->bytes;
-    if (o->pack)
-      if (lm_status st = pack(o, a.k, to, s); st != LM_OK) return st;
-    to += padded(bytes);
-  }
-  return LM_OK;
+  Operand *const operands[3] = {&pl->x, &pl->gate, &pl->up_};
+  return pack_three(operands, a.k, static_cast<char *>(workspace) + pl->copies, s);
 }
 
 template <typename T>

@@ -18,17 +18,40 @@ struct PackParams {
   int64_t group_stride, row_stride, rows, k, vecs, total;  // vecs: 16-byte vectors a row
 };
 
-__global__ void __launch_bounds__(256) pack_kernel(const PackParams p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  pdl_launch();
-  pdl_wait();
-  if (i >= p.total) return;
+// Vector i of the copy.
+__device__ __forceinline__ void pack_vector(const PackParams &p, int64_t i) {
   const int64_t row = i / p.vecs, v = i % p.vecs;
   const uint16_t *const s = p.src + row / p.rows * p.group_stride + row % p.rows * p.row_stride + v * 8;
   uint32_t w[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) w[j] = v * 8 + j < p.k ? s[j] : 0u;
   p.dst[i] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+}
+
+__global__ void __launch_bounds__(256) pack_kernel(const PackParams p) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  pdl_launch();
+  pdl_wait();
+  if (i < p.total) pack_vector(p, i);
+}
+
+// Three of them in one launch; one that is not wanted has no vectors.
+struct PackThree {
+  PackParams p[3];
+};
+
+__global__ void __launch_bounds__(256) pack_three_kernel(const PackThree a) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  pdl_launch();
+  pdl_wait();
+  const int64_t second = i - a.p[0].total, third = second - a.p[1].total;
+  if (second < 0) {
+    pack_vector(a.p[0], i);
+  } else if (third < 0) {
+    pack_vector(a.p[1], second);
+  } else if (third < a.p[2].total) {
+    pack_vector(a.p[2], third);
+  }
 }
 
 inline bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -63,7 +86,8 @@ inline Operand operand(const void *p, int64_t groups, int64_t rows, int64_t k, i
   return o;
 }
 
-inline lm_status pack(Operand *o, int64_t k, void *dst, cudaStream_t s) {
+// The copy of an operand, which it stands for from then on.
+inline PackParams pack_params(Operand *o, int64_t k, void *dst) {
   PackParams p;
   p.src = static_cast<const uint16_t *>(o->p);
   p.dst = static_cast<uint4 *>(dst);
@@ -73,14 +97,33 @@ inline lm_status pack(Operand *o, int64_t k, void *dst, cudaStream_t s) {
   p.k = k;
   p.vecs = (k + 7) / 8;
   p.total = o->groups * o->rows * p.vecs;
-  const int64_t ctas = (p.total + 255) / 256;
-  if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
-  if (lm_status st = launch_dependent(pack_kernel, dim3(static_cast<unsigned>(ctas)), 256, 0, s, 1, p); st != LM_OK)
-    return st;
   o->p = dst;
   o->row_stride = p.vecs * 8;
   o->group_stride = o->rows * o->row_stride;
-  return LM_OK;
+  return p;
+}
+
+inline lm_status pack(Operand *o, int64_t k, void *dst, cudaStream_t s) {
+  const PackParams p = pack_params(o, k, dst);
+  const int64_t ctas = (p.total + 255) / 256;
+  if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
+  return launch_dependent(pack_kernel, dim3(static_cast<unsigned>(ctas)), 256, 0, s, 1, p);
+}
+
+// Those of three operands that have to be copied, into dst one after the other, on boundaries of 256 bytes.
+inline lm_status pack_three(Operand *const (&o)[3], int64_t k, char *dst, cudaStream_t s) {
+  PackThree a = {};
+  int64_t total = 0;
+  for (int i = 0; i < 3; ++i) {
+    const size_t bytes = o[i]->bytes;
+    if (o[i]->pack) a.p[i] = pack_params(o[i], k, dst);
+    total += a.p[i].total;
+    dst += (bytes + 255) / 256 * 256;
+  }
+  const int64_t ctas = (total + 255) / 256;
+  if (ctas > INT_MAX) return LM_ERR_UNSUPPORTED;
+  if (ctas == 0) return LM_OK;
+  return launch_dependent(pack_three_kernel, dim3(static_cast<unsigned>(ctas)), 256, 0, s, 1, a);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,

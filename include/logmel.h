@@ -892,9 +892,10 @@ lm_status lm_weight4_values(const lm_weight4 *w, void *out, int64_t row_stride, 
 /*
  * lm_linear with such a weight: args as there, but for weight and
  * weight_row_stride, which are not used; args->n and args->k are the weight's.
- * Up to 16 rows, a group's products q * x are summed in 32 bits and the sums
- * multiplied by its scale.  For more the values are rounded to dtype (as
- * lm_weight4_values) on their way into the products; for many
+ * For few rows (up to 16; up to 64 where n is small) a group's products q * x
+ * are summed in 32 bits and the sums multiplied by its scale.  For more the
+ * values are rounded to dtype on their way into the products (to within 17/16
+ * of half a step: the scale is taken in two parts of dtype); for many
  * (lm_linear4_expands) they are expanded into the workspace for lm_linear.
  *   workspace  as for lm_linear, >= lm_linear4_workspace_size(...)
  * Errors as lm_linear.

@@ -739,8 +739,10 @@ lm_status view(const lm_weight4 *a, Weight *w) {
   return LM_OK;
 }
 
-// Rows that the warps' products take.
-constexpr int64_t kFewRows = 16;
+// Whether the warps' products take a call: up to 16 rows read the weight once, more read it from L2 for every 16
+// (17 to 32 rows x 1024 -> 4096: 6.0 us, 6.7 on tcgen05; 64 x 4096 -> 1024: 5.5, 8.1; but 48 x 1024 -> 4096 8.9, 7.2, and 32
+// x 1024 -> 50001 29, 19).
+bool few(int64_t rows, int64_t n) { return rows <= 16 || (rows <= 64 && up(rows, 16) * n <= 8192); }
 
 // From this many rows on the products cost more than expanding the weight.
 bool expands(int64_t rows, int64_t n, int64_t) { return rows > 768 && n <= 65535 * 128; }
@@ -882,8 +884,9 @@ struct Cut {
   int64_t tiles;
 };
 
-// The cut with the least estimated time, in microseconds: linear.cu's model, with a stage of at least 0.14 for the
-// widening.
+// The cut with the least estimated time, in microseconds: linear.cu's model, with a stage of at least 0.25 for the
+// widening.  Of eleven problems (32 to 700 rows, k 512 to 4096, 512 to 50001 outputs) its choice is within 4% of the best
+// of all cuts.
 Cut best_cut(int64_t n, int64_t rows, int64_t groups, int kblocks, bool activation, int sms, const Resident &held) {
   Cut best = {16, 1, 0};
   float least = 3.0e38f;
@@ -892,7 +895,7 @@ Cut best_cut(int64_t n, int64_t rows, int64_t groups, int kblocks, bool activati
     const int64_t tiles = up(n, kLanes) * up(rows, bn) * groups;
     if (splits > 1 && tiles > held.split[splits]) return;
     const int64_t rounds = up(tiles, splits > 1 ? held.split[splits] : sms);
-    const float products = 0.0011f * static_cast<float>(bn), stage = products > 0.14f ? products : 0.14f;
+    const float products = 0.0011f * static_cast<float>(bn), stage = products > 0.25f ? products : 0.25f;
     const float blocks = static_cast<float>(up(kblocks, splits)) * stage;
     float t = 3.5f + blocks;
     t += splits > 1 ? 0.9f + 0.03f * static_cast<float>(bn) / static_cast<float>(splits) + 0.008f * static_cast<float>(bn)
@@ -1062,7 +1065,7 @@ lm_status run(const lm_linear_args *args, const lm_weight4 *weight, void *worksp
   p.scale = a.scale;
   DeviceInfo dev;
   if (lm_status st = current_device_info(&dev); st != LM_OK) return st;
-  if (rows <= kFewRows || a.k == 0)
+  if (few(rows, a.n) || a.k == 0)
     return half ? product<__half>(p, dev.sm_count, s) : product<__nv_bfloat16>(p, dev.sm_count, s);
   return half ? tiles<__half>(a, w, x, dev, workspace, fault, s) : tiles<__nv_bfloat16>(a, w, x, dev, workspace, fault, s);
 }

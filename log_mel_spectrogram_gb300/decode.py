@@ -91,8 +91,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor | Weight4, bias: torch.Tensor |
     out_dtype: x's dtype (default) or float32; out may be residual itself, and
     overlaps no other input.
 
-    A Weight4 as weight is read in its 4 bits where x has few rows; for
-    many its values are rounded to x's dtype first, in each call."""
+    A Weight4 as weight is multiplied as it is where x has few rows (a decoding step);
+    for more its values are rounded to x's dtype on their way, in each call."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear(x, weight, bias, activation=activation, residual=residual, scale=scale, out=out,

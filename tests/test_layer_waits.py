@@ -91,7 +91,7 @@ def test_gated_linear_backward(lm, m, k, n, withheld):
     recovers(lm, call, ws, withheld, True)
 
 
-@pytest.mark.parametrize("m,k,n,group,shared", [(40, 200, 900, 64, True), (200, 2048, 300, 32, True),
+@pytest.mark.parametrize("m,k,n,group,shared", [(90, 200, 900, 64, True), (200, 2048, 300, 32, True),
                                                 (60, 300, 25000, 128, False), (256, 640, 20001, 32, False)])
 @pytest.mark.parametrize("withheld", [0, 1])
 def test_linear4(lm, m, k, n, group, shared, withheld):

@@ -13,7 +13,10 @@ makes.  Steps, with this package's part of each:
   next tokens                         linear onto the vocabulary, beam_step,
                                       KvCache.reorder
 
-    python examples/transcribe.py [--clips 2] [--seconds 3] [--beams 5] [--tokens 24]
+Every layer starts with layer_norm; with --gated the feed-forward layers are gated_linear and linear, and
+with --four-bits the decoder's linear layers have weights in 4 bits (quantize_weight).
+
+    python examples/transcribe.py [--clips 2] [--seconds 3] [--beams 5] [--tokens 24] [--gated] [--four-bits]
 """
 from __future__ import annotations
 
@@ -34,7 +37,7 @@ MELS, TAPS = 80, 3
 class Layer:
     """Weights of one block: attention (and, in a decoder, attention over the encoder), feed-forward."""
 
-    def __init__(self, width: int, cross: bool, rand):
+    def __init__(self, width: int, cross: bool, rand, gated: bool):
         def dense(n, k):
             return rand(n, k) / math.sqrt(k)
         self.qkv, self.qkv_bias = dense(3 * width, width), torch.zeros(3 * width, device="cuda")
@@ -42,11 +45,20 @@ class Layer:
         self.cross_q, self.cross_kv, self.cross_out = (dense(n * width, width) if cross else None for n in (1, 2, 1))
         self.up, self.up_bias = dense(4 * width, width), torch.zeros(4 * width, device="cuda")
         self.down = dense(width, 4 * width)
+        self.gate = dense(4 * width, width) if gated else None
+
+    def in_four_bits(self):
+        """The linear layers' weights rounded to 4 bits (those of a gated layer stay as they are)."""
+        for name in ("qkv", "out", "cross_q", "cross_kv", "cross_out", "down", *(("up",) if self.gate is None else ())):
+            w = getattr(self, name)
+            if w is not None:
+                setattr(self, name, lm.quantize_weight(w))
+        return self
 
 
 class Model:
     def __init__(self, width: int = 256, heads: int = 4, encoder: int = 2, decoder: int = 2, vocab: int = 1009,
-                 dtype: torch.dtype = torch.bfloat16, seed: int = 0):
+                 dtype: torch.dtype = torch.bfloat16, seed: int = 0, gated: bool = False, four_bits: bool = False):
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def rand(*shape):
@@ -54,14 +66,25 @@ class Model:
         self.width, self.heads, self.dim, self.vocab, self.dtype = width, heads, width // heads, vocab, dtype
         self.stem = rand(width, TAPS * MELS) / math.sqrt(TAPS * MELS)
         self.stem_bias = torch.zeros(width, device="cuda")
-        self.encoder = [Layer(width, False, rand) for _ in range(encoder)]
-        self.decoder = [Layer(width, True, rand) for _ in range(decoder)]
+        self.encoder = [Layer(width, False, rand, gated) for _ in range(encoder)]
+        self.decoder = [Layer(width, True, rand, gated) for _ in range(decoder)]
         self.tokens = rand(vocab, width)
         self.head = 3 * rand(vocab, width) / math.sqrt(width)
+        if four_bits:
+            self.decoder = [layer.in_four_bits() for layer in self.decoder]
+            self.head = lm.quantize_weight(self.head)
         self.mel = lm.MelSpectrogram(n_fft=400, hop_length=160, n_mels=MELS, f_max=8000.0, log_mel=True)
 
     def norm(self, x):
-        return F.layer_norm(x, (self.width,))
+        return lm.layer_norm(x)
+
+    def feed_forward(self, layer: Layer, x: torch.Tensor) -> torch.Tensor:
+        h = self.norm(x)
+        if layer.gate is not None:
+            h = lm.gated_linear(h, layer.gate, layer.up)
+        else:
+            h = lm.linear(h, layer.up, layer.up_bias, activation="gelu")
+        return lm.linear(h, layer.down, residual=x)
 
     def split(self, x, parts: int):
         """[rows, tokens, parts * width] as `parts` views [rows, tokens, heads, dim]."""
@@ -80,9 +103,7 @@ class Model:
             cache.append(i, k, v)
             seen = torch.full((clips,), n, dtype=torch.int32, device="cuda")
             a = cache.attend(i, q, seen, causal=False)
-            x = lm.linear(a.flatten(2), layer.out, residual=x)
-            h = lm.linear(self.norm(x), layer.up, layer.up_bias, activation="gelu")
-            x = lm.linear(h, layer.down, residual=x)
+            x = self.feed_forward(layer, lm.linear(a.flatten(2), layer.out, residual=x))
         return self.norm(x)
 
     def remember(self, x: torch.Tensor) -> lm.KvCache:
@@ -104,8 +125,7 @@ class Model:
             q = lm.linear(self.norm(x), layer.cross_q).view(clips, beams, self.heads, self.dim)
             a = frames.attend(i, q, causal=False)  # a clip's beams are the queries of one row
             x = lm.linear(a.view(clips * beams, 1, self.width), layer.cross_out, residual=x)
-            h = lm.linear(self.norm(x), layer.up, layer.up_bias, activation="gelu")
-            x = lm.linear(h, layer.down, residual=x)
+            x = self.feed_forward(layer, x)
         own.advance(1)
         return lm.linear(self.norm(x), self.head, out_dtype=torch.float32).view(clips, beams, self.vocab)
 
@@ -134,9 +154,11 @@ def main():
     ap.add_argument("--seconds", type=float, default=3.0)
     ap.add_argument("--beams", type=int, default=5)
     ap.add_argument("--tokens", type=int, default=24)
+    ap.add_argument("--gated", action="store_true")
+    ap.add_argument("--four-bits", action="store_true")
     a = ap.parse_args()
     wave = torch.randn(a.clips, int(16000 * a.seconds), device="cuda") * 0.1
-    scores, tokens = transcribe(Model(), wave, a.beams, a.tokens)
+    scores, tokens = transcribe(Model(gated=a.gated, four_bits=a.four_bits), wave, a.beams, a.tokens)
     for c in range(a.clips):
         print(f"clip {c}: {scores[c, 0].item():.2f}  {' '.join(map(str, tokens[c, 0].tolist()))}")
 

@@ -28,6 +28,7 @@ def lm():
 
 def recovers(lm, call, ws, withheld, shared):
     """call(withheld or None) -> outputs, filled with 7 before."""
+    lm.decode_error()  # what other tests have left
     want = call(None)
     assert lm.decode_error() == 0 and waits.error(ws) == 0
     t0 = time.perf_counter()

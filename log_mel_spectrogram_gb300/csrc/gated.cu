@@ -10,7 +10,8 @@
 // computes four products, all with 128 lanes a CTA and bn columns:
 //   forward   lanes are outputs n, columns rows of x; a stage holds a tile of Wg and of Wu
 //             and one of x, the tensor memory both sums, which meet in registers
-//   grads     the same, with da and db for outputs and their column sums
+//   grads     the same, with da and db for outputs; for a layer with biases (grad sums) also
+//             their sums over columns, from products that are added up in registers every 256 of k
 //   input     dx: lanes are k, columns rows; W is summed over n, along its rows (an
 //             operand whose contiguous index is not summed over, "MN-major")
 //   weight    dWg and dWu: lanes are k, columns n; x and da or db are both summed over rows
@@ -40,18 +41,22 @@ constexpr int kBoxBytes = 64 * kBk * 2;  // 64 elements of a contiguous index by
 constexpr int kMaxStages = 8;
 
 enum class Form { kOne, kPair, kSplit };
-enum class Kind { kForward, kGrads, kInput, kWeight };
+enum class Kind { kForward, kGrads, kGradSums, kInput, kWeight };
 
-constexpr bool dual(Kind k) { return k == Kind::kForward || k == Kind::kGrads; }
+constexpr bool dual(Kind k) { return k == Kind::kForward || k == Kind::kGrads || k == Kind::kGradSums; }
 constexpr int epi_warps(Form f) { return f == Form::kSplit ? 8 : 16; }
 constexpr int threads_of(Form f) { return 128 + 32 * epi_warps(f); }
+// Blocks of k after which sums that have to be right to 32 bits go from tensor memory into registers: it loses a
+// little towards zero with each of its additions (measured at k = 912: 7e-7 of the result, systematically, where
+// additions that round are 2e-7 off), which a sum of thousands of da keeps.
+constexpr int kSumBlocks = 4;
 // Parts of a tile's columns whose sums of da and db are kept apart.
 constexpr int kColumnParts = epi_warps(Form::kOne) / 4;
 
 struct GatedParams {
   const void *bg, *bu, *grad;
   void *out[2];       // forward: y; grads: da, db; input: dx; weight: dWg, dWu
-  float *columns;     // [column tiles * kColumnParts][2][n], sums of da and db, or null
+  float *columns;     // [column tiles * kColumnParts][2][n], sums of da and db (Kind::kGradSums)
   int64_t out_row, grad_row;
   int32_t rows, n;    // columns and lanes of a group's outputs
   int32_t bn, stages, blocks, half_blocks, tmem_cols;
@@ -149,6 +154,13 @@ __device__ __forceinline__ void put_dual(const GatedParams &p, const uint32_t (&
   }
 }
 
+// The sums of da and db of a warp's columns in a tile.
+__device__ __forceinline__ void put_columns(const GatedParams &p, const Tile &t, int e, int n, float2 sums) {
+  float *const to = p.columns + (static_cast<int64_t>(t.col_tile) * kColumnParts + e / 4) * 2 * p.n + n;
+  to[0] = sums.x;
+  to[p.n] = sums.y;
+}
+
 // Turns a tile of both sums into outputs: warp e has lanes 32 * (e % 4) .. + 31 and every fourth 8 columns.
 template <typename T, Kind KIND, int ACT>
 __device__ __forceinline__ void dual_epilogue(const GatedParams &p, const Tile &t, uint32_t acc, int e, T (&grad)[8]) {
@@ -176,11 +188,30 @@ __device__ __forceinline__ void dual_epilogue(const GatedParams &p, const Tile &
     }
     if (in) put_dual<T, KIND, ACT>(p, ra, rb, now, bg, bu, sums, row + c, min(8, cols - c), n);
   }
-  if (KIND == Kind::kGrads && p.columns && in) {
-    float *const to = p.columns + (static_cast<int64_t>(t.col_tile) * kColumnParts + e / 4) * 2 * p.n + n;
-    to[0] = sums.x;
-    to[p.n] = sums.y;
+}
+
+// ... from a lane's sums of 16 columns in registers, from column 16 * (e / 4) on (Kind::kGradSums).
+template <typename T, int ACT>
+__device__ __forceinline__ void held_epilogue(const GatedParams &p, const Tile &t, int e, const float (&a)[16],
+                                              const float (&b)[16], const T (&grad)[2][8]) {
+  const int n = t.lane0 + 32 * (e % 4) + static_cast<int>(threadIdx.x % 32), c = e / 4 * 16;
+  const int cols = min(p.bn, p.rows - t.col0) - c;
+  if (n >= p.n) return;
+  const float bg = bias_of<T>(p.bg, p.bias_f32, n), bu = bias_of<T>(p.bu, p.bias_f32, n);
+  float2 sums = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t ra[8], rb[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      ra[j] = __float_as_uint(a[8 * h + j]);
+      rb[j] = __float_as_uint(b[8 * h + j]);
+    }
+    if (8 * h < cols)
+      put_dual<T, Kind::kGradSums, ACT>(p, ra, rb, grad[h], bg, bu, sums, static_cast<int64_t>(t.col0) + c + 8 * h,
+                                        min(8, cols - 8 * h), n);
   }
+  if (p.columns) put_columns(p, t, e, n, sums);
 }
 
 template <typename T, Kind KIND>
@@ -192,6 +223,19 @@ __device__ __forceinline__ void dual_epilogue_act(const GatedParams &p, const Ti
     case LM_ACT_SILU: dual_epilogue<T, KIND, LM_ACT_SILU>(p, t, acc, e, grad); break;
     case LM_ACT_SIGMOID: dual_epilogue<T, KIND, LM_ACT_SIGMOID>(p, t, acc, e, grad); break;
     default: dual_epilogue<T, KIND, LM_ACT_NONE>(p, t, acc, e, grad); break;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void held_epilogue_act(const GatedParams &p, const Tile &t, int e, const float (&a)[16],
+                                                  const float (&b)[16], const T (&grad)[2][8]) {
+  switch (p.act) {
+    case LM_ACT_RELU: held_epilogue<T, LM_ACT_RELU>(p, t, e, a, b, grad); break;
+    case LM_ACT_GELU: held_epilogue<T, LM_ACT_GELU>(p, t, e, a, b, grad); break;
+    case LM_ACT_GELU_TANH: held_epilogue<T, LM_ACT_GELU_TANH>(p, t, e, a, b, grad); break;
+    case LM_ACT_SILU: held_epilogue<T, LM_ACT_SILU>(p, t, e, a, b, grad); break;
+    case LM_ACT_SIGMOID: held_epilogue<T, LM_ACT_SIGMOID>(p, t, e, a, b, grad); break;
+    default: held_epilogue<T, LM_ACT_NONE>(p, t, e, a, b, grad); break;
   }
 }
 
@@ -252,6 +296,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     gated_kernel(const __grid_constant__ CUtensorMap gate_map, const __grid_constant__ CUtensorMap up_map,
                  const __grid_constant__ CUtensorMap col_map, const GatedParams p) {
   constexpr bool PAIR = FORM == Form::kPair, SPLIT = FORM == Form::kSplit, DUAL = dual(KIND);
+  constexpr bool CHUNKED = KIND == Kind::kGradSums;
   constexpr int EPI = epi_warps(FORM);
   constexpr int LANE_BYTES = DUAL ? 2 * kTileBytes : kTileBytes;
   extern __shared__ __align__(1024) uint8_t ring[];
@@ -352,46 +397,103 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     }
   } else if (warp == 1) {
     if (!PAIR || rank == 0) {
-      int s = 0, tiles = 0;
+      int s = 0, turns = 0;  // stages; halves of the tensor memory, filled in turn
       uint32_t phase = 0;
       bool ok = true;
       const uint32_t ring_a = smem_u32(ring);
-      for (int t = first; t < p.tiles && ok; t += step, ++tiles) {
-        const int half = tiles & 1;
-        if (tiles >= 2) ok = mbar_wait_warp(&b.acc_empty[half], ((tiles >> 1) - 1) & 1, p.wait_ns, abort, p.err);
-        tcgen05_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
-        for (int kb = k_begin; kb < k_end && ok; ++kb) {
-          ok = mbar_wait_warp(&b.full[s], phase, p.wait_ns, abort, p.err);
-          if (!ok) break;
+      for (int t = first; t < p.tiles && ok; t += step) {
+        int kb = k_begin;
+        do {  // a tile, or (CHUNKED) kSumBlocks of its blocks
+          const int half = turns & 1, begin = kb, end = CHUNKED ? min(kb + kSumBlocks, k_end) : k_end;
+          if (turns >= 2) ok = mbar_wait_warp(&b.acc_empty[half], ((turns >> 1) - 1) & 1, p.wait_ns, abort, p.err);
           tcgen05_fence_after();
-          const uint32_t at = ring_a + s * stage_bytes;
-          const uint64_t a = DUAL ? smem_desc_k128(at) : smem_desc_mn128(at);
-          const uint64_t c = KIND == Kind::kWeight ? smem_desc_mn128(at + LANE_BYTES) : smem_desc_k128(at + LANE_BYTES);
-          constexpr int A_STEP = DUAL ? 2 : 128, C_STEP = KIND == Kind::kWeight ? 128 : 2;  // 16 further in the sum
-          if (elect_one()) {
+          const uint32_t d = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
+          for (; kb < end && ok; ++kb) {
+            ok = mbar_wait_warp(&b.full[s], phase, p.wait_ns, abort, p.err);
+            if (!ok) break;
+            tcgen05_fence_after();
+            const uint32_t at = ring_a + s * stage_bytes;
+            const uint64_t a = DUAL ? smem_desc_k128(at) : smem_desc_mn128(at);
+            const uint64_t c = KIND == Kind::kWeight ? smem_desc_mn128(at + LANE_BYTES) : smem_desc_k128(at + LANE_BYTES);
+            constexpr int A_STEP = DUAL ? 2 : 128, C_STEP = KIND == Kind::kWeight ? 128 : 2;  // 16 further in the sum
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < kBk / 16; ++i) {
-              tcgen05_mma_f16<PAIR>(d, a + A_STEP * i, c + C_STEP * i, p.idesc, kb > k_begin || i > 0);
-              if (DUAL)
-                tcgen05_mma_f16<PAIR>(d + p.tmem_cols / 4, a + (kTileBytes >> 4) + A_STEP * i, c + C_STEP * i, p.idesc,
-                                      kb > k_begin || i > 0);
+              for (int i = 0; i < kBk / 16; ++i) {
+                tcgen05_mma_f16<PAIR>(d, a + A_STEP * i, c + C_STEP * i, p.idesc, kb > begin || i > 0);
+                if (DUAL)
+                  tcgen05_mma_f16<PAIR>(d + p.tmem_cols / 4, a + (kTileBytes >> 4) + A_STEP * i, c + C_STEP * i, p.idesc,
+                                        kb > begin || i > 0);
+              }
+              tcgen05_commit<PAIR>(&b.empty[s]);
             }
-            tcgen05_commit<PAIR>(&b.empty[s]);
+            __syncwarp();
+            if (++s == p.stages) {
+              s = 0;
+              phase ^= 1;
+            }
           }
+          if (ok && elect_one()) tcgen05_commit<PAIR>(&b.acc_full[half]);
           __syncwarp();
-          if (++s == p.stages) {
-            s = 0;
-            phase ^= 1;
-          }
-        }
-        if (ok && elect_one()) tcgen05_commit<PAIR>(&b.acc_full[half]);
-        __syncwarp();
+          ++turns;
+        } while (kb < k_end && ok);
       }
       if (!ok) {  // products in flight end before the tensor memory is given back
         if (elect_one()) tcgen05_commit<PAIR>(&b.drain);
         mbar_drain(&b.drain, 0, p.wait_ns, p.err);
       }
+    }
+  } else if (CHUNKED && warp >= 4) {
+    const int e = warp - 4, c = e / 4 * 16;
+    int turns = 0;
+    bool ok = true;
+    for (int t = first; t < p.tiles && ok; t += step) {
+      const Tile tile = tile_at(p, t, lane_rank);
+      float sa[16], sb[16];
+      T grad[2][8];
+      const int cols = min(p.bn, p.rows - tile.col0) - c;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sa[8 * h + j] = sb[8 * h + j] = 0.0f;
+          grad[h][j] = from_f32<T>(0.0f);
+        }
+        if (8 * h < cols)
+          grad_rows<T>(p, grad[h], static_cast<int64_t>(tile.col0) + c + 8 * h, min(8, cols - 8 * h),
+                       tile.lane0 + 32 * (e % 4) + static_cast<int>(threadIdx.x % 32));
+      }
+      int kb = k_begin;
+      do {
+        const int half = turns & 1;
+        // One decision per warp: tensor memory loads are executed by whole warps.
+        ok = mbar_wait_warp(&b.acc_full[half], (turns >> 1) & 1, p.wait_ns, abort, p.err);
+        if (!ok) break;
+        tcgen05_fence_after();
+        const uint32_t acc = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2) + c) + (static_cast<uint32_t>(32 * (e % 4)) << 16);
+        if (c < p.bn && p.blocks > 0) {
+          uint32_t r[16];
+          tmem_ld16(acc, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sa[j] += __uint_as_float(r[j]);
+          tmem_ld16(acc + p.tmem_cols / 4, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sb[j] += __uint_as_float(r[j]);
+        }
+        tcgen05_fence_before();
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) {
+          if (PAIR && rank != 0) {
+            mbar_arrive_cluster(cluster_addr(smem_u32(&b.acc_empty[half]), 0));
+          } else {
+            mbar_arrive(&b.acc_empty[half]);
+          }
+        }
+        ++turns;
+        kb += kSumBlocks;
+      } while (kb < k_end);
+      if (ok) held_epilogue_act<T>(p, tile, e, sa, sb, grad);
     }
   } else if (warp >= 4) {
     const int e = warp - 4;
@@ -425,7 +527,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
           for (int j = 0; j < 16; ++j) partial[(c + j) * kLanes + lane] = __uint_as_float(r[j]);
         }
       } else {
-        if constexpr (DUAL) {
+        if constexpr (CHUNKED) {
+        } else if constexpr (DUAL) {
           dual_epilogue_act<T, KIND>(p, tile, acc, e, grad);
         } else {
           plain_epilogue<T, KIND>(p, tile, acc, e);
@@ -529,7 +632,7 @@ using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
 
 template <typename T, Kind KIND>
 Kernel kernel_of(Form form) {
-  if constexpr (KIND == Kind::kGrads) {  // (a tile's sums over rows stay with one CTA)
+  if constexpr (KIND == Kind::kGrads || KIND == Kind::kGradSums) {  // (a tile's sums over rows stay with one CTA)
     return form == Form::kPair ? gated_kernel<T, Form::kPair, KIND> : gated_kernel<T, Form::kOne, KIND>;
   } else {
     return form == Form::kSplit ? gated_kernel<T, Form::kSplit, KIND>
@@ -544,14 +647,15 @@ struct Cut {
 };
 
 // Columns of a tile, at least: sums over rows take space by the tile.
-int narrowest(Kind kind, int64_t rows) { return kind == Kind::kGrads && rows > 1024 ? 64 : 16; }
+int narrowest(Kind kind, int64_t rows) { return kind == Kind::kGradSums && rows > 1024 ? 64 : 16; }
 
 // The cut with the least estimated time, in microseconds: linear.cu's model, with the tile of the second
 // projection where there is one, and this kernel's epilogues.
 Cut best_cut(Kind kind, int64_t n, int64_t rows, int64_t groups, int64_t blocks, int sms, const Resident &held) {
   Cut best = {Form::kOne, kind == Kind::kWeight ? 64 : 16, 1, 0};
   float least = 3.0e38f;
-  const float column = kind == Kind::kGrads ? 0.035f : kind == Kind::kForward ? 0.02f : 0.0085f;
+  const bool grads = kind == Kind::kGrads || kind == Kind::kGradSums;
+  const float column = grads ? 0.035f : kind == Kind::kForward ? 0.02f : 0.0085f;
   const float sums = dual(kind) ? 2.0f : 1.0f;
   auto consider = [&](Form form, int bn, int splits) {
     const bool two = form == Form::kPair;
@@ -583,7 +687,7 @@ Cut best_cut(Kind kind, int64_t n, int64_t rows, int64_t groups, int64_t blocks,
   auto forms = [&](int bn, int unit) {
     consider(Form::kOne, bn, 1);
     if (bn % (2 * unit) == 0) consider(Form::kPair, bn, 1);
-    if (kind == Kind::kGrads) return;
+    if (grads) return;
     for (int s = 2; s <= kMaxSplits && s <= blocks; s *= 2) consider(Form::kSplit, bn, s);
   };
   if (kind == Kind::kWeight) {  // whole boxes of 64 columns a CTA
@@ -591,7 +695,8 @@ Cut best_cut(Kind kind, int64_t n, int64_t rows, int64_t groups, int64_t blocks,
       if (bn == 64 || bn - 64 < rows) forms(bn, 64);
     return best;
   }
-  const int widest = dual(kind) ? 128 : 256;  // both sums twice, or one twice, in 512 columns of tensor memory
+  // Both sums twice, or one twice, in 512 columns of tensor memory; or 16 columns a warp's lanes hold in registers.
+  const int widest = kind == Kind::kGradSums ? 64 : dual(kind) ? 128 : 256;
   const int most = rows < widest ? static_cast<int>(up(rows, 16) * 16) : widest;
   for (int bn = narrowest(kind, rows); bn <= most; bn += bn < 64 ? 16 : 32) forms(bn, 16);
   const int64_t shares = up(rows, widest);
@@ -687,7 +792,7 @@ Plan plan(const lm_gated_args &a, bool backward) {
   if (backward) {
     p.pitch = static_cast<size_t>(up(a.n, 8) * 8);
     p.bytes += padded(static_cast<size_t>(a.rows) * p.pitch * 4);
-    p.parts = static_cast<int>(up(a.rows, narrowest(Kind::kGrads, a.rows)) * kColumnParts);
+    p.parts = static_cast<int>(up(a.rows, narrowest(Kind::kGradSums, a.rows)) * kColumnParts);
     p.bytes += static_cast<size_t>(p.parts) * 8 * static_cast<size_t>(a.n);
   }
   return p;
@@ -751,7 +856,12 @@ lm_status backward(const lm_gated_backward_args &a, Plan pl, void *workspace, co
   p.grad = a.grad;
   p.grad_row = a.grad_row_stride;
   p.columns = a.db_gate || a.db_up ? columns : nullptr;
-  if (lm_status st = run<T, Kind::kGrads>(l, p, 1, pl.gate, pl.up_, pl.x, f.k); st != LM_OK) return st;
+  // (A layer with biases takes it whichever gradients are wanted: each has the same bits then.)
+  if (lm_status st = p.columns || f.b_gate || f.b_up
+                         ? run<T, Kind::kGradSums>(l, p, 1, pl.gate, pl.up_, pl.x, f.k)
+                         : run<T, Kind::kGrads>(l, p, 1, pl.gate, pl.up_, pl.x, f.k);
+      st != LM_OK)
+    return st;
   const Operand both{da, 2, f.rows, plane, static_cast<int64_t>(pl.pitch), false, 0};
   if (a.dx && f.k > 0) {
     GatedParams q = {};
@@ -773,7 +883,7 @@ lm_status backward(const lm_gated_backward_args &a, Plan pl, void *workspace, co
     if (lm_status st = run<T, Kind::kWeight>(l, q, groups, pl.x, pl.x, both, f.rows); st != LM_OK) return st;
   }
   if (p.columns) {
-    const Cut cut = best_cut(Kind::kGrads, f.n, f.rows, 1, up(f.k, kBk), l.dev.sm_count, l.held);
+    const Cut cut = best_cut(Kind::kGradSums, f.n, f.rows, 1, up(f.k, kBk), l.dev.sm_count, l.held);
     const int parts = static_cast<int>(up(f.rows, cut.bn)) * kColumnParts;
     return launch_dependent(columns_kernel<T>, dim3(static_cast<unsigned>(up(2 * f.n, 32))), 256, 0, s, 1,
                             static_cast<const float *>(columns), parts, f.n, a.db_gate, a.db_up, p.bias_f32);

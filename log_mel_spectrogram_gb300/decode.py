@@ -102,7 +102,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor | Weight4, bias: torch.Tensor |
         raise ValueError(f"activation must be one of {[a for a in _ACTIVATIONS if a]} or None")
     if code is None:
         raise ValueError("out_dtype must be x's dtype or float32")
-    if type(weight) is Weight4:
+    if isinstance(weight, Weight4):
         return _checked((_ext or _binding()).linear(x, weight._head(), bias, act, residual, scale, out, code),
                         "lm_linear4")
     return _checked((_ext or _binding()).linear(x, weight, bias, act, residual, scale, out, code), "lm_linear")

@@ -127,7 +127,8 @@ def both(lm, x, wg, wu, bg, bu, g, act="silu"):
 
 SIZES = [(1, 1, 1), (1, 16, 8), (5, 64, 64), (5, 512, 1000), (3, 201, 80), (16, 256, 500), (17, 72, 129), (64, 80, 384),
          (65, 256, 257), (127, 333, 31), (128, 128, 128), (129, 64, 256), (200, 520, 500), (257, 1000, 513), (300, 64, 40),
-         (700, 96, 1024), (1500, 240, 520), (2, 3000, 50), (48, 640, 2001), (2100, 128, 64), (5000, 32, 24)]
+         (700, 96, 1024), (1500, 240, 520), (2, 3000, 50), (48, 640, 2001), (2100, 128, 64), (5000, 32, 24), (5000, 64, 2001),
+         (9000, 72, 520)]
 
 
 @pytest.mark.parametrize("rows,k,n", SIZES)

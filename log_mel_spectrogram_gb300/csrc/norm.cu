@@ -648,7 +648,7 @@ struct Shape {
 // to 1024 elements, because its sums need no barrier.
 Shape forward_shape(int64_t rows, int64_t width, int sms) {
   const bool few = rows <= 4 * sms;
-  auto each = [&](int team) { return width <= 8 * team ? 8 : width <= 16 * team ? 16 : 32; };
+  auto each = [&](int team) { return width <= 8 * team ? 8 : width <= 16 * team ? 16 : team == 32 && width <= 24 * team ? 24 : 32; };
   if (width > 512 * 32) return {0, 0};
   if (width <= 64) return {8, 8};
   if (width <= 128) return {16, 8};
@@ -657,12 +657,14 @@ Shape forward_shape(int64_t rows, int64_t width, int sms) {
   return {512, each(512) < 16 ? 16 : each(512)};
 }
 
-// At most 16 elements a thread: it also holds their sums over rows.
-Shape backward_shape(int64_t width) {
+// At most 24 elements a thread, 16 where rows are off 16-byte boundaries (and wait in registers): it also holds
+// their sums over rows.
+Shape backward_shape(int64_t width, bool vectors) {
   if (width > 512 * 16) return {0, 0};
   if (width <= 64) return {8, 8};
   if (width <= 128) return {16, 8};
   if (width <= 256) return {32, 8};
+  if (vectors && width > 512 && width <= 768) return {32, 24};
   int team = 32;
   while (team * 16 < width) team *= 2;
   return {team, 16};
@@ -716,8 +718,10 @@ lm_status forward_shaped(const NormParams &p, Shape h, int sms, cudaStream_t s) 
   if (h.team == 8) return forward_as<T, 8, 8, VECTORS>(p, sms, s);
   if (h.team == 16) return forward_as<T, 16, 8, VECTORS>(p, sms, s);
   if (h.team == 32)
-    return h.each == 8 ? forward_as<T, 32, 8, VECTORS>(p, sms, s) : h.each == 16 ? forward_as<T, 32, 16, VECTORS>(p, sms, s)
-                                                                                 : forward_as<T, 32, 32, VECTORS>(p, sms, s);
+    return h.each == 8    ? forward_as<T, 32, 8, VECTORS>(p, sms, s)
+           : h.each == 16 ? forward_as<T, 32, 16, VECTORS>(p, sms, s)
+           : h.each == 24 ? forward_as<T, 32, 24, VECTORS>(p, sms, s)
+                          : forward_as<T, 32, 32, VECTORS>(p, sms, s);
   if (h.team == 128)
     return h.each == 8    ? forward_as<T, 128, 8, VECTORS>(p, sms, s)
            : h.each == 16 ? forward_as<T, 128, 16, VECTORS>(p, sms, s)
@@ -730,7 +734,10 @@ lm_status backward_shaped(NormParams &p, Shape h, int sms, cudaStream_t s) {
   switch (h.team) {
     case 8: return backward_as<T, 8, 8, VECTORS>(p, sms, s);
     case 16: return backward_as<T, 16, 8, VECTORS>(p, sms, s);
-    case 32: return h.each == 8 ? backward_as<T, 32, 8, VECTORS>(p, sms, s) : backward_as<T, 32, 16, VECTORS>(p, sms, s);
+    case 32:
+      return h.each == 8    ? backward_as<T, 32, 8, VECTORS>(p, sms, s)
+             : h.each == 16 ? backward_as<T, 32, 16, VECTORS>(p, sms, s)
+                            : backward_as<T, 32, VECTORS ? 24 : 16, VECTORS>(p, sms, s);
     case 64: return backward_as<T, 64, 16, VECTORS>(p, sms, s);
     case 128: return backward_as<T, 128, 16, VECTORS>(p, sms, s);
     case 256: return backward_as<T, 256, 16, VECTORS>(p, sms, s);
@@ -757,11 +764,11 @@ lm_status backward(NormParams p, void *dweight, void *dbias, cudaStream_t s) {
   if (p.rows > 0) {
     DeviceInfo dev;
     if (lm_status st = current_device_info(&dev); st != LM_OK) return st;
-    const Shape h = backward_shape(p.width);
     const int64_t size = sizeof(T);
+    const bool v = p.width * size % 16 == 0 && vectors(p.x, p.x_row, p.rows, size) &&
+                   vectors(p.grad, p.grad_row, p.rows, size) && vectors(p.out, p.out_row, p.rows, size);
+    const Shape h = backward_shape(p.width, v);
     if (h.team != 0) {
-      const bool v = p.width * size % 16 == 0 && vectors(p.x, p.x_row, p.rows, size) &&
-                     vectors(p.grad, p.grad_row, p.rows, size) && vectors(p.out, p.out_row, p.rows, size);
       if (lm_status st = v ? backward_shaped<T, true>(p, h, dev.sm_count, s) : backward_shaped<T, false>(p, h, dev.sm_count, s);
           st != LM_OK)
         return st;

@@ -3,7 +3,8 @@
  *
  * Two operations (and, in sections 4 to 6, what turns their features into
  * text: linear layers, an 8-bit key/value cache with its attention, and beam
- * search):
+ * search; in sections 7 to 9, the rest of such a model's layers: layer norm and
+ * gated linear layers with their gradients, and weights in 4 bits):
  *
  *  1. lm_log_mel_from_stft: Whisper's log-mel spectrogram from a complex
  *     STFT, as defined by the KBench task spec "audio_mel_spectrogram_fused.py"
@@ -740,8 +741,8 @@ lm_status lm_layer_norm(const lm_norm_args *args, lm_stream_t stream);
  *   dbias    device, [width] of bias_dtype, or NULL
  *   workspace  device, >= lm_layer_norm_backward_workspace_size(...), 16-byte
  *            aligned; its contents on entry do not matter.
- * Sums over rows are taken in 32 bits, in an order that depends on the sizes
- * alone, and rounded once.  Outputs meet no input and not one another.
+ * Sums over rows are taken in 32 bits, in an order that depends on the sizes,
+ * the rows' alignment and the device alone, and rounded once.  Outputs meet no input and not one another.
  * Errors as lm_layer_norm, and LM_ERR_WORKSPACE.  rows == 0 sets dweight and
  * dbias to zero.
  */
@@ -810,8 +811,9 @@ lm_status lm_gated_linear(const lm_gated_args *args, void *workspace, size_t wor
  *   da = grad * b * act'(a),   db = grad * act(a)
  *   dx = da Wg + db Wu,  dWg = da^T x,  dWu = db^T x,
  *   dbg, dbu = sums of da, db over rows
- * da and db are computed and, for the biases, summed in 32 bits, and rounded to dtype as operands of
- * the products.  relu's derivative at 0 is 0.
+ * da and db are computed and, for the biases, summed in 32 bits, and rounded to
+ * dtype as operands of the products.  relu's derivative at 0 is 0.  Each
+ * gradient's bits are the same whichever others are wanted.
  *
  *   forward  the inputs and sizes of lm_gated_linear (out and out_row_stride
  *            are not used)

@@ -17,6 +17,12 @@
 //   weight    dWg and dWu: lanes are k, columns n; x and da or db are both summed over rows
 // So no operand is transposed in memory, and consecutive lanes are consecutive outputs.
 //
+// Measured, in a graph: 24000 x 1024 -> 4096 bf16 forward 215 to 222 us (1.8 to 1.87 PFLOP/s; 258 in a long row of calls, at the
+// clock that the power limit allows: 1.56, 91% of the sustained rate); 12000 rows with all gradients 455 to 465 us
+// (540 in a long row: 1.49 PFLOP/s with the second a and b), with biases 567.  5 x 1024 -> 4096 5.8 us for
+// 16.8 MB of weights (k over clusters).  777 x 504 -> 1008 f16 with biases and gradients 31 us, five launches of
+// about 5; 777 x 500 -> 1001 38 to 48, with copies of all operands to 16-byte boundaries in both directions.
+//
 // a and b are computed twice instead of kept: kept in 32 bits they would cost 24 bytes of
 // traffic an element more than computing them costs products up to k of about 1500, kept in 16
 // the biases' gradients would lose their 32 bits; and a training step saves the memory.

@@ -9,8 +9,12 @@
 // k, a group's products in 32 bits and then times its scale; the warps of a CTA share out tiles and
 // k, meet in shared memory, and write whole lines.
 //
-// Many rows: products bound it, and the legacy matrix instruction with them.  The values are expanded into
-// the workspace, rounded to x's type, and linear.cu's kernel takes them.
+// More rows: linear.cu's tiles on tcgen05, with warps that widen W's bytes into the operand, rounded to x's
+// type.  Many rows: the values are expanded into the workspace, and linear.cu's kernel takes them.
+//
+// Measured, in a graph: 5 x 1024 -> 4096 3.3 us; 5 x 1024 -> 50001 10.7 to 10.9 us for 28.8 MB (2.6 TB/s; issue slots 55% full, a
+// hundred instructions a tile), 16 rows 17; 128 rows 18.6 to 20 (16-bit weights: 320 rows 31); 320 x 4096 -> 1024 11.9;
+// 3000 x 1024 -> 4096 22.6, of which the expansion is 3.
 #include <climits>
 #include <type_traits>
 

@@ -187,9 +187,9 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
 // Eight elements of a row from k on, zeros past its end.
 template <typename T>
 __device__ __forceinline__ uint4 load8(const T *row, int k, int end) {
-  if (row && k + 8 <= end) return *reinterpret_cast<const uint4 *>(row + k);
+  if (k + 8 <= end) return *reinterpret_cast<const uint4 *>(row + k);
   uint32_t v[4] = {0, 0, 0, 0};
-  if (row && k < end) {
+  if (k < end) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (k + j < end) v[j / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(row + k + j)) << (16 * (j % 2));
@@ -433,13 +433,13 @@ __device__ __forceinline__ Scale<T> split_scale(float s) {
   return o;
 }
 
-// The eight values of a word, two instructions a pair: q * high + (q * low rounded), rounded once.  In bf16 the
-// parts lose 2^-17 of the value, 2^-8 of the last rounding; in f16, whose least step is 2^-24, 8 * 2^-25 for scales
-// down to 2^-10, a sixteenth of it (smaller scales go through 32 bits).
 __device__ __forceinline__ __half2 as2(uint32_t v, __half) { return *reinterpret_cast<const __half2 *>(&v); }
 __device__ __forceinline__ __nv_bfloat162 as2(uint32_t v, __nv_bfloat16) {
   return *reinterpret_cast<const __nv_bfloat162 *>(&v);
 }
+// The eight values of a word, two instructions a pair: q * high + (q * low rounded), rounded once.  In bf16 the
+// parts lose 2^-17 of the value, 2^-8 of the last rounding; in f16, whose least step is 2^-24, 8 * 2^-25 for scales
+// down to 2^-10, a sixteenth of it (smaller scales go through 32 bits).
 template <typename T>
 __device__ __forceinline__ void widen_scaled(uint32_t word, const Scale<T> &s, uint32_t (&v)[4]) {
   widen<T>(word, v);
@@ -505,12 +505,17 @@ __device__ __forceinline__ void widen_stage(const uint8_t *slot, const float *sc
 // of warps widen as many stages at once, in turn.  A wait tells whether the phase before was the last to
 // end, not which one it was; a group's own last fill shows that what came as many fills before as there are stages
 // has been used, which is enough where there are no more groups than stages.
-template <typename T, bool SPLIT, int GROUPS>
+//
+// KB: blocks of k of a stage.  With two the waits for barriers come half as often (64 x 1024 -> 50001 17.9 us, with
+// one 19.5; 64 x 4096 -> 8192 16.0, 16.8; nowhere slower); from 128 columns of x on there would be room for two
+// stages, too few.  (Of 19.5 us the copies, barriers and three rounds of tiles alone took 13.4, the widening 4.)
+template <typename T, bool SPLIT, int GROUPS, int KB>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap col_map, const TileParams tp) {
-  constexpr int GROUP_WARPS = kWiden / GROUPS, TILES = 8 / GROUP_WARPS;
+  constexpr int GROUP_WARPS = kWiden / GROUPS, TILES = KB * 8 / GROUP_WARPS;
+  static_assert(8 % TILES == 0 && kChunk % KB == 0, "a warp's tiles are of one block, a chunk's stages its own");
   const LinearParams &p = tp.l;
   extern __shared__ __align__(1024) uint8_t ring[];
-  const int stage_bytes = kLanes * 128 + p.bn * 128;
+  const int block_bytes = kLanes * 128 + p.bn * 128, stage_bytes = KB * block_bytes;  // a block: W's tile, then x's
   uint8_t *const raw = ring + p.stages * stage_bytes;
   Barriers &b = *reinterpret_cast<Barriers *>(raw + tp.raw * kSlotBytes);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
@@ -557,13 +562,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     bool ok = true;
     for (int t = first; t < p.tiles && ok; t += step) {
       const Tile tile = tile_at(p, t, 0);
-      for (int kb = k_begin; kb < k_end; ++kb) {
+      for (int kb = k_begin; kb < k_end; kb += KB) {
         if (fills >= p.stages) ok = mbar_wait_warp(&b.empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err);
         if (!ok) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&b.full[s.at], static_cast<uint32_t>(p.bn * 128));
-          tma_load_3d<false>(ring + s.at * stage_bytes + kLanes * 128, &col_map, kb * kBk, tile.col0, tile.group,
-                             smem_u32(&b.full[s.at]));
+          const int count = min(KB, k_end - kb);
+          mbar_arrive_expect_tx(&b.full[s.at], static_cast<uint32_t>(count * p.bn * 128));
+          for (int i = 0; i < count; ++i)
+            tma_load_3d<false>(ring + s.at * stage_bytes + i * block_bytes + kLanes * 128, &col_map, (kb + i) * kBk,
+                               tile.col0, tile.group, smem_u32(&b.full[s.at]));
         }
         __syncwarp();
         ++fills;
@@ -585,7 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         if (fills >= tp.raw) ok = mbar_wait_warp(&b.raw_empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err);
         if (!ok) break;
         if (elect_one()) {
-          const int end = min(kb + kChunk, k_end), g = group_at(tp, kb), g_end = min(group_at(tp, end - 1) + 1 + tp.small, tp.groups);
+          const int end = min(kb + kChunk, k_end), g = group_at(tp, kb);
+          const int g_end = min(group_at(tp, end - 1) + 1 + tp.small, tp.groups);
           const uint32_t size = static_cast<uint32_t>(end - kb) * kBlockBytes, factors = static_cast<uint32_t>(g_end - g) * 512;
           uint8_t *const to = raw + s.at * kSlotBytes;
           mbar_arrive_expect_tx(&b.raw_full[s.at], size + factors);
@@ -609,16 +617,23 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       if (tiles >= 2) ok = mbar_wait_warp(&b.acc_empty[half], ((tiles >> 1) - 1) & 1, p.wait_ns, abort, p.err);
       tcgen05_fence_after();
       const uint32_t d = tmem + static_cast<uint32_t>(half * (p.tmem_cols / 2));
-      for (int kb = k_begin; kb < k_end && ok; ++kb) {
+      for (int kb = k_begin; kb < k_end && ok; kb += KB) {
         ok = mbar_wait_warp(&b.full[s.at], s.phase, p.wait_ns, abort, p.err);
         if (!ok) break;
         tcgen05_fence_after();
         const uint64_t a = smem_desc_k128(ring_a + s.at * stage_bytes);
         const uint64_t c = smem_desc_k128(ring_a + s.at * stage_bytes + kLanes * 128);
+        const bool second = KB == 2 && kb + 1 < k_end;
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kBk / 16; ++i)
             tcgen05_mma_f16<false>(d, a + 2 * i, c + 2 * i, p.idesc, kb > k_begin || i > 0);
+          if (second) {
+            const uint64_t next = static_cast<uint64_t>(block_bytes >> 4);
+#pragma unroll
+            for (int i = 0; i < kBk / 16; ++i)
+              tcgen05_mma_f16<false>(d, a + next + 2 * i, c + next + 2 * i, p.idesc, true);
+          }
           tcgen05_commit<false>(&b.empty[s.at]);
         }
         __syncwarp();
@@ -636,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     // and 4 + c of 16 bytes in a row of 128.  Odd rows store their second chunk first: eight lanes then
     // meet every bank once.
     const int e = warp - 4, group = e / GROUP_WARPS, r = lane / 4, c = lane % 4, odd = r & 1;
-    const int tile0 = e % GROUP_WARPS * TILES;
+    const int tile0 = e % GROUP_WARPS * TILES % 8, block = e % GROUP_WARPS * TILES / 8;  // of the stage's
     const uint32_t low = static_cast<uint32_t>((16 * tile0 + r) * 128 + (((odd ? 4 + c : c) ^ r) * 16));
     const uint32_t high = static_cast<uint32_t>((16 * tile0 + r) * 128 + (((odd ? c : 4 + c) ^ r) * 16));
     const uint32_t ring_a = smem_u32(ring);
@@ -649,8 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       for (int chunk = k_begin; chunk < k_end && ok; chunk += kChunk) {
         ok = mbar_wait_warp(&b.raw_full[q.at], q.phase, p.wait_ns, abort, p.err);
         const int end = min(chunk + kChunk, k_end);
-        for (int kb = chunk; kb < end && ok; ++kb, ++fill) {
+        for (int first_kb = chunk; first_kb < end && ok; first_kb += KB, ++fill) {
           if (fill % GROUPS != group) continue;
+          const int kb = first_kb + block;
           const uint8_t *const slot = raw + q.at * kSlotBytes + (kb - chunk) * kBlockBytes;
           const int g = group_at(tp, kb) - group_at(tp, chunk);
           const float *const scales =
@@ -660,7 +676,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           const bool there = !tp.small || 2 * kb + 1 < tp.groups;
           if (fill >= p.stages) ok = mbar_wait_warp(&b.empty[s.at], s.phase ^ 1, p.wait_ns, abort, p.err);
           if (!ok) break;
-          widen_stage<T, TILES>(slot + tile0 * kTileBytes, scales, other, there, ring_a + s.at * stage_bytes, low, high, odd, lane);
+          if (kb < end)  // (a last stage may have one block)
+            widen_stage<T, TILES>(slot + tile0 * kTileBytes, scales, other, there,
+                                  ring_a + s.at * stage_bytes + block * block_bytes, low, high, odd, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&b.full[s.at]);
@@ -959,21 +977,26 @@ lm_status tiles(const lm_linear_args &a, const Weight &w, const Operand &x, cons
   p.lanes_inside = 0;  // a tile of W's columns go round inside: its bytes come from L2
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.bn) p.tmem_cols *= 2;
-  const int stage_bytes = kLanes * 128 + p.bn * 128;
+  const bool two = p.bn <= 96;  // blocks a stage: see the kernel
+  const int stage_bytes = (two ? 2 : 1) * (kLanes * 128 + p.bn * 128);
   const int room = 227 * 1024 - static_cast<int>(sizeof(Barriers));
   p.stages = (room - 3 * kSlotBytes) / stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   tp.raw = (room - p.stages * stage_bytes) / kSlotBytes;
   if (tp.raw > kMaxRaw) tp.raw = kMaxRaw;
-  const bool four = p.stages >= 4;
+  const bool four = !two && p.stages >= 4;
   if (p.stages < (four ? 4 : 2) || tp.raw < 2) return LM_ERR_UNSUPPORTED;
   p.idesc = idesc_f16(bf16, kLanes, static_cast<uint32_t>(p.bn));
   CUtensorMap cols = {};
   if (lm_status st = make_map(&cols, x, a.k, p.bn, bf16); st != LM_OK) return st;
   const int smem = p.stages * stage_bytes + tp.raw * kSlotBytes + static_cast<int>(sizeof(Barriers));
   const bool split = p.splits > 1;
-  const auto kernel = split ? (four ? tile_kernel<T, true, 4> : tile_kernel<T, true, 2>)
-                            : (four ? tile_kernel<T, false, 4> : tile_kernel<T, false, 2>);
+  const auto kernel = split ? (two    ? tile_kernel<T, true, 2, 2>
+                               : four ? tile_kernel<T, true, 4, 1>
+                                      : tile_kernel<T, true, 2, 1>)
+                            : (two    ? tile_kernel<T, false, 2, 2>
+                               : four ? tile_kernel<T, false, 4, 1>
+                                      : tile_kernel<T, false, 2, 1>);
   if (lm_status st = ensure_smem_attribute(reinterpret_cast<const void *>(kernel), smem); st != LM_OK) return st;
   const int grid = split ? p.tiles * p.splits : p.tiles < dev.sm_count ? p.tiles : dev.sm_count;
   return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), kThreads, static_cast<size_t>(smem), s,

@@ -762,8 +762,8 @@ lm_status view(const lm_weight4 *a, Weight *w) {
 }
 
 // Whether the warps' products take a call: up to 16 rows read the weight once, more read it from L2 for every 16
-// (17 to 32 rows x 1024 -> 4096: 6.0 us, 6.7 on tcgen05; 64 x 4096 -> 1024: 5.5, 8.1; but 48 x 1024 -> 4096 8.9, 7.2, and 32
-// x 1024 -> 50001 29, 19).
+// (17 to 32 rows x 1024 -> 4096: 5.9 to 6.2 us, 6.6 to 6.8 on tcgen05; 64 x 4096 -> 1024: 5.6, 7.9; but 48 x 1024 -> 4096
+// 8.8, 7.5, and 32 x 1024 -> 50001 29, 18; in between, with k of 8192, up to a tenth the wrong way).
 bool few(int64_t rows, int64_t n) { return rows <= 16 || (rows <= 64 && up(rows, 16) * n <= 8192); }
 
 // From this many rows on the products cost more than expanding the weight.
@@ -906,9 +906,9 @@ struct Cut {
   int64_t tiles;
 };
 
-// The cut with the least estimated time, in microseconds: linear.cu's model, with a stage of at least 0.25 for the
-// widening.  Of eleven problems (32 to 700 rows, k 512 to 4096, 512 to 50001 outputs) its choice is within 4% of the best
-// of all cuts.
+// The cut with the least estimated time, in microseconds: linear.cu's model, with what a block's widening takes
+// (in a cluster, too).  Of 24 problems (32 to 768 rows, k 500 to 8192, 512 to 50001 outputs) its choice is within 4% of
+// the best of all cuts (500 x 1024 -> 1024 7.7 us; a cut over k 8.9).
 Cut best_cut(int64_t n, int64_t rows, int64_t groups, int kblocks, bool activation, int sms, const Resident &held) {
   Cut best = {16, 1, 0};
   float least = 3.0e38f;
@@ -917,10 +917,11 @@ Cut best_cut(int64_t n, int64_t rows, int64_t groups, int kblocks, bool activati
     const int64_t tiles = up(n, kLanes) * up(rows, bn) * groups;
     if (splits > 1 && tiles > held.split[splits]) return;
     const int64_t rounds = up(tiles, splits > 1 ? held.split[splits] : sms);
-    const float products = 0.0011f * static_cast<float>(bn), stage = products > 0.25f ? products : 0.25f;
-    const float blocks = static_cast<float>(up(kblocks, splits)) * stage;
-    float t = 3.5f + blocks;
-    t += splits > 1 ? 0.9f + 0.03f * static_cast<float>(bn) / static_cast<float>(splits) + 0.008f * static_cast<float>(bn)
+    const float products = 0.0011f * static_cast<float>(bn);
+    const float widening = splits > 1 ? 0.3f : bn <= 96 ? 0.22f : 0.25f;
+    const float blocks = static_cast<float>(up(kblocks, splits)) * (products > widening ? products : widening);
+    float t = 3.0f + blocks;
+    t += splits > 1 ? 2.0f + 0.03f * static_cast<float>(bn) / static_cast<float>(splits) + 0.008f * static_cast<float>(bn)
                     : column * static_cast<float>(bn);
     const float epi = 0.5f + column * static_cast<float>(bn);
     t += static_cast<float>(rounds - 1) * (blocks > epi ? blocks : epi);

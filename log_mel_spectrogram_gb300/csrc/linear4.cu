@@ -12,8 +12,8 @@
 // More rows: linear.cu's tiles on tcgen05, with warps that widen W's bytes into the operand, rounded to x's
 // type.  Many rows: the values are expanded into the workspace, and linear.cu's kernel takes them.
 //
-// Measured, in a graph: 5 x 1024 -> 4096 3.3 us; 5 x 1024 -> 50001 10.7 to 10.9 us for 28.8 MB (2.6 TB/s; issue slots 55% full, a
-// hundred instructions a tile), 16 rows 17; 128 rows 18.6 to 20 (16-bit weights: 320 rows 31); 320 x 4096 -> 1024 11.9;
+// Measured, in a graph: 5 x 1024 -> 4096 3.3 us; 5 x 1024 -> 50001 10.6 us for 28.8 MB (2.7 TB/s; issue slots 55% full, a
+// hundred instructions a tile), 16 rows 17; 128 rows 18.6 to 20 (16-bit weights: 320 rows 31); 320 x 4096 -> 1024 11.5;
 // 3000 x 1024 -> 4096 22.6, of which the expansion is 3.
 #include <climits>
 #include <type_traits>
@@ -762,9 +762,11 @@ lm_status view(const lm_weight4 *a, Weight *w) {
 }
 
 // Whether the warps' products take a call: up to 16 rows read the weight once, more read it from L2 for every 16
-// (17 to 32 rows x 1024 -> 4096: 5.9 to 6.2 us, 6.6 to 6.8 on tcgen05; 64 x 4096 -> 1024: 5.6, 7.9; but 48 x 1024 -> 4096
-// 8.8, 7.5, and 32 x 1024 -> 50001 29, 18; in between, with k of 8192, up to a tenth the wrong way).
-bool few(int64_t rows, int64_t n) { return rows <= 16 || (rows <= 64 && up(rows, 16) * n <= 8192); }
+// (32 rows x 1024 -> 4096: 4.5 us, 6.7 on tcgen05; 64 x 4096 -> 1024: 5.6, 7.9; 32 x 2048 -> 6000 9.3, 11.6; 64 x 1024 ->
+// 4096 6.7, 7.5; but 48 x 2048 -> 4096 9.1, 8.1, 64 x 1024 -> 6000 10.0, 7.6 and 32 x 1024 -> 50001 29, 18).
+bool few(int64_t rows, int64_t n, int64_t k) {
+  return rows <= 16 || (rows <= 64 && up(rows, 16) * n <= (k <= 1024 ? 16384 : 12000));
+}
 
 // From this many rows on the products cost more than expanding the weight.
 bool expands(int64_t rows, int64_t n, int64_t) { return rows > 768 && n <= 65535 * 128; }
@@ -880,13 +882,32 @@ lm_status sizes(const lm_linear_args &a, size_t *first, size_t *all) {
   return LM_OK;
 }
 
+// Warps that share out the k of a pair of tiles: a warp's time is about its tiles of k and one more, times the rounds
+// in which an SM's 24 warps (16 with two blocks of rows) come by.  Rounds of small CTAs overlap, so
+// that they count half; a CTA of 16 warps has the SM to itself.  Within 5% of the best of all on 74 problems (k 256 to
+// 4096, 512 to 50001 outputs); 16 rows x 512 -> 8192 3.8 us, with two dozen warps an SM as the rule 4.8.
+int best_parts(int64_t ktiles, int64_t pairs, int nt, int sms) {
+  int best = 1;
+  float least = 3.0e38f;
+  for (int parts = 1; parts <= kMostWarps && parts <= ktiles; parts *= 2) {
+    const int64_t room = (nt == 1 && parts <= 8 ? 24ll : 16ll) * sms, warps = pairs * parts;
+    const float whole = static_cast<float>(up(warps, room));
+    const float share = static_cast<float>(warps) / static_cast<float>(room);
+    const float rounds = parts > 8 || share < 1.0f ? whole : 0.5f * (whole + share);
+    const float t = rounds * (1.0f + static_cast<float>(up(ktiles, parts)));
+    if (t < least) {
+      least = t;
+      best = parts;
+    }
+  }
+  return best;
+}
+
 // CTAs of four warps or, where more share out a tile's k, of those: small ones even out over the SMs.
 template <typename T, int NT>
 lm_status product_as(ProductParams p, int sms, cudaStream_t s) {
   const int64_t pairs = up(p.ntiles, kSide), blocks = up(p.rows, 8 * NT);
-  // As many parts of k as give every SM two dozen warps.
-  p.parts = 1;
-  while (p.parts < kMostWarps && 2 * p.parts <= p.w.ktiles && pairs * blocks * p.parts < 24ll * sms) p.parts *= 2;
+  p.parts = best_parts(p.w.ktiles, pairs * blocks, NT, sms);
   const int warps = p.parts > 4 ? p.parts : 4;
   const dim3 grid(static_cast<unsigned>(up(pairs, warps / p.parts)), static_cast<unsigned>(blocks));
   const auto kernel = warps > 8 ? (p.w.group == 32 ? product_kernel<T, NT, true, 16> : product_kernel<T, NT, false, 16>)
@@ -1093,7 +1114,7 @@ lm_status run(const lm_linear_args *args, const lm_weight4 *weight, void *worksp
   p.scale = a.scale;
   DeviceInfo dev;
   if (lm_status st = current_device_info(&dev); st != LM_OK) return st;
-  if (few(rows, a.n) || a.k == 0)
+  if (few(rows, a.n, a.k) || a.k == 0)
     return half ? product<__half>(p, dev.sm_count, s) : product<__nv_bfloat16>(p, dev.sm_count, s);
   return half ? tiles<__half>(a, w, x, dev, workspace, fault, s) : tiles<__nv_bfloat16>(a, w, x, dev, workspace, fault, s);
 }

@@ -262,8 +262,10 @@ constexpr int threads_for(int team, int regs) {
 // elements, whose rows take it all, they are read from the L1 each time.
 template <typename P, int NE>
 constexpr int forward_regs() { return 62 + P::kWords / 2 + NE + (NE == 8 ? 16 : 0); }
+// Several teams of a CTA share the weight and bias.  (Vectors of 32 bits: a CTA of 128 threads, for the room
+// that their rows take.)
 template <typename P, int TEAM, int NE>
-constexpr int forward_threads() { return TEAM <= 32 ? 256 : TEAM; }
+constexpr int forward_threads() { return TEAM <= 32 || (TEAM <= 128 && P::kEach != 4) ? 256 : TEAM < 128 ? 128 : TEAM; }
 template <typename P, int TEAM, int NE>
 constexpr int forward_ctas() {
   const int n = threads_for(32, forward_regs<P, NE>()) / forward_threads<P, TEAM, NE>();
@@ -652,17 +654,22 @@ struct Shape {
   int team, each;
 };
 
-// Few rows are shared out among many threads, for the least time of one; of many, a warp holds up
-// to 1024 elements, because its sums need no barrier.
-Shape forward_shape(int64_t rows, int64_t width, int sms) {
+// Few rows are shared out among many threads, for the least time of one; of many, as few threads as hold one, with
+// 24 or 32 elements each: a team's sums wait for one another, so that more rows at once count for more (bf16, 96 MB in
+// and out: 19660 x 1280 24.4 us, with 128 threads of 16 elements 47; 12288 x 2048 19.5, 33.5; 4096 x 6144 24.6, 36.5
+// with 512 of 16; in f32 above 4096 those are the faster, because a CTA's rows take an SM's shared memory).
+Shape forward_shape(int64_t rows, int64_t width, int64_t size, int sms) {
   const bool few = rows <= 4 * sms;
-  auto each = [&](int team) { return width <= 8 * team ? 8 : width <= 16 * team ? 16 : team == 32 && width <= 24 * team ? 24 : 32; };
   if (width > 512 * 32) return {0, 0};
   if (width <= 64) return {8, 8};
   if (width <= 128) return {16, 8};
-  if (width <= (few ? 256 : 1024)) return {32, each(32)};
-  if (width <= (few ? 1024 : 4096)) return {128, each(128)};
-  return {512, each(512) < 16 ? 16 : each(512)};
+  if (width <= 256) return {32, 8};
+  if (few) return width <= 1024 ? Shape{128, 8} : Shape{512, width <= 4096 ? 8 : width <= 8192 ? 16 : 32};
+  if (width <= 512) return {32, 16};
+  int team = 32;
+  while (team * 32 < width) team *= 2;
+  if (team == 512 || (team == 256 && size == 4)) return {512, width <= 8192 ? 16 : 32};
+  return {team, width <= 24 * team ? 24 : 32};
 }
 
 // At most 24 elements a thread, 16 where rows are off 16-byte boundaries (and wait in registers): it also holds
@@ -730,11 +737,17 @@ lm_status forward_shaped(const NormParams &p, Shape h, int sms, cudaStream_t s) 
            : h.each == 16 ? forward_as<T, 32, 16, VECTORS>(p, sms, s)
            : h.each == 24 ? forward_as<T, 32, 24, VECTORS>(p, sms, s)
                           : forward_as<T, 32, 32, VECTORS>(p, sms, s);
+  if (h.team == 64) return h.each == 24 ? forward_as<T, 64, 24, VECTORS>(p, sms, s) : forward_as<T, 64, 32, VECTORS>(p, sms, s);
   if (h.team == 128)
     return h.each == 8    ? forward_as<T, 128, 8, VECTORS>(p, sms, s)
-           : h.each == 16 ? forward_as<T, 128, 16, VECTORS>(p, sms, s)
+           : h.each == 24 ? forward_as<T, 128, 24, VECTORS>(p, sms, s)
                           : forward_as<T, 128, 32, VECTORS>(p, sms, s);
-  return h.each == 16 ? forward_as<T, 512, 16, VECTORS>(p, sms, s) : forward_as<T, 512, 32, VECTORS>(p, sms, s);
+  if constexpr (sizeof(T) == 2)
+    if (h.team == 256)
+      return h.each == 24 ? forward_as<T, 256, 24, VECTORS>(p, sms, s) : forward_as<T, 256, 32, VECTORS>(p, sms, s);
+  return h.each == 8    ? forward_as<T, 512, 8, VECTORS>(p, sms, s)
+         : h.each == 16 ? forward_as<T, 512, 16, VECTORS>(p, sms, s)
+                        : forward_as<T, 512, 32, VECTORS>(p, sms, s);
 }
 
 template <typename T, bool VECTORS>
@@ -757,7 +770,7 @@ template <typename T>
 lm_status forward(const NormParams &p, cudaStream_t s) {
   DeviceInfo dev;
   if (lm_status st = current_device_info(&dev); st != LM_OK) return st;
-  const Shape h = forward_shape(p.rows, p.width, dev.sm_count);
+  const Shape h = forward_shape(p.rows, p.width, sizeof(T), dev.sm_count);
   if (h.team == 0)
     return launch_dependent(norm_rows_loop<T>, dim3(static_cast<unsigned>(p.rows)), kLoopThreads, 0, s, 1, p);
   const int64_t size = sizeof(T);

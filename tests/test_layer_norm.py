@@ -106,6 +106,18 @@ def test_sizes(lm, rows, width, dtype):
     both(lm, x, w, b, g)
 
 
+MANY = [(700, 1025), (1300, 1280), (650, 1536), (700, 2047), (1301, 2048), (620, 2560), (620, 3001), (650, 4096), (610, 4104),
+        (620, 5120), (609, 6150), (650, 8192), (640, 8200), (620, 9001)]
+
+
+@pytest.mark.parametrize("rows,width", MANY)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_wide_rows(lm, rows, width, dtype):
+    """Teams of fewer threads than few rows have."""
+    x, w, b, g = inputs(rows, width, dtype, torch.float32, seed=rows + width)
+    both(lm, x, w, b, g)
+
+
 @pytest.mark.parametrize("dtype", TYPES[1:])
 @pytest.mark.parametrize("width", [1, 100, 1024, 5000])
 def test_parameters_of_the_inputs_type_or_none(lm, dtype, width):

@@ -27,6 +27,9 @@ constexpr size_t kMostKept = 128;         // workspaces; past that the one whose
 // linear has no counters, and needs much where it copies an operand off 16-byte
 // boundaries (128 MB for a weight of 50001 x 1023): what is more than the least is that call's
 // alone, and nothing is cleared.
+//
+// Callers hold the interpreter's lock from here to their last launch: nothing else keeps two threads'
+// launches on one stream, and what they leave for one another in the workspace, apart.
 Tensor workspace(Op op, int dev, cudaStream_t stream, size_t bytes) {
   struct Kept {
     Tensor t;

@@ -72,7 +72,7 @@ inline Tensor make(at::IntArrayRef shape, at::ScalarType type, int dev) {
 
 enum Op { kLinear, kAttend, kBeam, kReorder };
 
-// Scratch of an operation on a stream (binding.cpp).
+// Scratch of an operation on a stream, for callers that hold the interpreter's lock (binding.cpp).
 Tensor workspace(Op op, int dev, cudaStream_t stream, size_t bytes);
 
 inline PyObject *status(int rc) { return PyLong_FromLong(rc); }

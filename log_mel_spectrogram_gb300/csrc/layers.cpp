@@ -81,6 +81,10 @@ lm_stream_t stream_of(int dev) {
   return reinterpret_cast<lm_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());
 }
 
+// Scratch of one backward pass.  It runs on a thread of torch's engine, without the interpreter's lock, so another
+// thread's calls on the stream fall between its launches: what workspace() keeps for the stream may be theirs.
+Tensor own_scratch(int dev, size_t bytes) { return make({static_cast<int64_t>(bytes)}, at::kByte, dev); }
+
 Tensor defined_or_none(const Tensor *t) { return t ? *t : Tensor(); }
 
 // Optional inputs of an autograd node; an absent one has no edge, so a node counts its edges over those there are.
@@ -182,7 +186,7 @@ struct NormFn : public torch::autograd::Function<NormFn> {
     size_t need = 0;
     ok(lm_layer_norm_backward_workspace_size(&p, &need), "lm_layer_norm_backward");
     const cudaStream_t s = c10::cuda::getCurrentCUDAStream(dev).stream();
-    const Tensor ws = workspace(kLinear, dev, s, need);
+    const Tensor ws = own_scratch(dev, need);
     ok(lm_layer_norm_backward(&p, ws.data_ptr(), static_cast<size_t>(ws.numel()), reinterpret_cast<lm_stream_t>(s)),
        "lm_layer_norm_backward");
     return {dx, dw, db, Tensor()};
@@ -312,7 +316,7 @@ struct GatedFn : public torch::autograd::Function<GatedFn> {
     size_t need = 0;
     ok(lm_gated_linear_backward_workspace_size(&p, &need), "lm_gated_linear_backward");
     const cudaStream_t s = c10::cuda::getCurrentCUDAStream(dev).stream();
-    const Tensor ws = workspace(kLinear, dev, s, need);
+    const Tensor ws = own_scratch(dev, need);
     ok(lm_gated_linear_backward(&p, ws.data_ptr(), static_cast<size_t>(ws.numel()), reinterpret_cast<lm_stream_t>(s)),
        "lm_gated_linear_backward");
     return {d[0], d[1], d[2], d[3], d[4], Tensor()};

@@ -428,9 +428,17 @@ template <typename T>
 __device__ __forceinline__ Scale<T> split_scale(float s) {
   Scale<T> o;
   o.high = pack2<T>(s, s);
-  const float rest = s - unpack2<T>(o.high).x, low = fabsf(s) < 3.0e38f ? rest : 0.0f;
+  const float low = s - unpack2<T>(o.high).x;
   o.low = pack2<T>(low, low);
   return o;
+}
+
+// Whether the parts stand for the scale: it is finite in T (of an infinite first part 0 times it is NaN), and in f16,
+// whose steps end at 2^-24, not too small (see widen_scaled).
+template <typename T>
+__device__ __forceinline__ bool splits(float s) {
+  const float a = fabsf(s);
+  return std::is_same<T, __half>::value ? a >= 0x1p-10f && a <= 65504.0f : a <= 0x1.fep127f;
 }
 
 __device__ __forceinline__ __half2 as2(uint32_t v, __half) { return *reinterpret_cast<const __half2 *>(&v); }
@@ -439,7 +447,7 @@ __device__ __forceinline__ __nv_bfloat162 as2(uint32_t v, __nv_bfloat16) {
 }
 // The eight values of a word, two instructions a pair: q * high + (q * low rounded), rounded once.  In bf16 the
 // parts lose 2^-17 of the value, 2^-8 of the last rounding; in f16, whose least step is 2^-24, 8 * 2^-25 for scales
-// down to 2^-10, a sixteenth of it (smaller scales go through 32 bits).
+// down to 2^-10, a sixteenth of it (other scales go through 32 bits).
 template <typename T>
 __device__ __forceinline__ void widen_scaled(uint32_t word, const Scale<T> &s, uint32_t (&v)[4]) {
   widen<T>(word, v);
@@ -450,6 +458,16 @@ __device__ __forceinline__ void widen_scaled(uint32_t word, const Scale<T> &s, u
   }
 }
 
+// ... by whichever way is the scale's.
+template <typename T>
+__device__ __forceinline__ void widen_any(uint32_t word, float s, uint32_t (&v)[4]) {
+  if (splits<T>(s)) {
+    widen_scaled<T>(word, split_scale<T>(s), v);
+  } else {
+    widen_scaled<T>(word, s, v);
+  }
+}
+
 // TILES tiles of 16 rows of a block into the operand at `to`.
 template <typename T, int TILES>
 __device__ __forceinline__ void widen_stage(const uint8_t *slot, const float *scales, int other, bool there, uint32_t to,
@@ -457,7 +475,7 @@ __device__ __forceinline__ void widen_stage(const uint8_t *slot, const float *sc
   // (Odd rows' halves change places here.)
   uint4 v[TILES];
   float f[TILES][2][2];
-  bool tiny = false;
+  bool parts = true;
 #pragma unroll
   for (int j = 0; j < TILES; ++j) {
     const uint4 u = reinterpret_cast<const uint4 *>(slot + j * kTileBytes)[lane];
@@ -467,17 +485,17 @@ __device__ __forceinline__ void widen_stage(const uint8_t *slot, const float *sc
       const float first = scales[16 * j + 8 * h], second = there ? scales[other + 16 * j + 8 * h] : 0.0f;
       f[j][h][0] = odd ? second : first;
       f[j][h][1] = odd ? first : second;
-      tiny = tiny || fabsf(f[j][h][0]) < 0x1p-10f || fabsf(f[j][h][1]) < 0x1p-10f;
+      parts = parts && splits<T>(f[j][h][0]) && splits<T>(f[j][h][1]);
     }
   }
-  if (std::is_same<T, __half>::value && __any_sync(0xffffffffu, tiny)) {
+  if (!__all_sync(0xffffffffu, parts)) {  // a warp's other rows get the same bits either way
 #pragma unroll 1
     for (int h = 0; h < 2 * TILES; ++h) {
       const uint4 u = reinterpret_cast<const uint4 *>(slot + h / 2 * kTileBytes)[lane];
       const float first = scales[8 * h], second = there ? scales[other + 8 * h] : 0.0f;
       uint32_t x[4], y[4];
-      widen_scaled<T>(h % 2 ? u.z : u.x, first, x);
-      widen_scaled<T>(h % 2 ? u.w : u.y, second, y);
+      widen_any<T>(h % 2 ? u.z : u.x, first, x);
+      widen_any<T>(h % 2 ? u.w : u.y, second, y);
       const uint32_t at = to + h * 1024;
       sts_v4(at + (odd ? high : low), x[0], x[1], x[2], x[3]);
       sts_v4(at + (odd ? low : high), y[0], y[1], y[2], y[3]);

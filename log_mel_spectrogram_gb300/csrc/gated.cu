@@ -779,17 +779,17 @@ lm_status run(const Launch &l, GatedParams p, int64_t groups, const Operand &lan
                           l.stream, cluster, a, b, c, p);
 }
 
-// The inputs as the kernels fetch them, and where copies of them and the gradients lie in the workspace.
+// The inputs as the kernels fetch them, and where copies of them, the gradients and (columns) the tiles' sums of
+// them lie in the workspace.
 struct Plan {
   Operand x, gate, up_;
   size_t pitch;          // elements a row of da and db
   size_t copies, grads, bytes;
-  int parts;             // most column tiles' parts
 };
 
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
-Plan plan(const lm_gated_args &a, bool backward) {
+Plan plan(const lm_gated_args &a, bool backward = false, bool columns = false) {
   Plan p = {};
   p.x = operand(a.x, 1, a.rows, a.k, 0, a.x_row_stride);
   p.gate = operand(a.w_gate, 1, a.n, a.k, 0, a.gate_row_stride);
@@ -800,11 +800,14 @@ Plan plan(const lm_gated_args &a, bool backward) {
   if (backward) {
     p.pitch = static_cast<size_t>(up(a.n, 8) * 8);
     p.bytes += padded(static_cast<size_t>(a.rows) * p.pitch * 4);
-    p.parts = static_cast<int>(up(a.rows, narrowest(Kind::kGradSums, a.rows)) * kColumnParts);
-    p.bytes += static_cast<size_t>(p.parts) * 8 * static_cast<size_t>(a.n);
   }
+  if (columns)
+    p.bytes += static_cast<size_t>(up(a.rows, narrowest(Kind::kGradSums, a.rows)) * kColumnParts) * 8 *
+               static_cast<size_t>(a.n);
   return p;
 }
+
+Plan plan(const lm_gated_backward_args &a) { return plan(a.forward, true, a.db_gate || a.db_up); }
 
 template <typename T>
 GatedParams params(const lm_gated_args &a) {
@@ -907,7 +910,7 @@ lm_status run_forward(const lm_gated_args *args, void *workspace, size_t workspa
   if (!a.out) return LM_ERR_INVALID_ARG;
   if (lm_status st = check_pointers(a, workspace); st != LM_OK) return st;
   if (!aligned(a.out, 2)) return LM_ERR_MISALIGNED;
-  const Plan pl = plan(a, false);
+  const Plan pl = plan(a);
   if (!workspace || workspace_bytes < pl.bytes) return LM_ERR_WORKSPACE;
   if ((a.rows > 1 && a.out_row_stride < a.n) || meets_inputs(a, {a.out, a.rows, a.out_row_stride * 2, a.n * 2}))
     return LM_ERR_INVALID_ARG;
@@ -943,7 +946,7 @@ lm_status run_backward(const lm_gated_backward_args *args, void *workspace, size
     for (int j = 0; j < i; ++j)
       if (outs[j] && rows_meet(out, {outs[j], 1, 0, sizes[j]})) return LM_ERR_INVALID_ARG;
   }
-  const Plan pl = plan(f, true);
+  const Plan pl = plan(a);
   return f.dtype == LM_F16 ? backward<__half>(a, pl, workspace, fault, s)
                            : backward<__nv_bfloat16>(a, pl, workspace, fault, s);
 }
@@ -957,7 +960,7 @@ lm_status gated_error(uint32_t *value, bool clear, cudaStream_t s) { return read
 extern "C" lm_status lm_gated_linear_workspace_size(const lm_gated_args *args, size_t *bytes) {
   if (!bytes) return LM_ERR_INVALID_ARG;
   if (lm_status st = lm::check(args); st != LM_OK) return st;
-  *bytes = lm::plan(*args, false).bytes;
+  *bytes = lm::plan(*args).bytes;
   return LM_OK;
 }
 
@@ -970,7 +973,7 @@ extern "C" lm_status lm_gated_linear_backward_workspace_size(const lm_gated_back
   if (!args || !bytes || args->grad_row_stride < 0) return LM_ERR_INVALID_ARG;
   if (lm_status st = lm::check(&args->forward); st != LM_OK) return st;
   if (args->grad_row_stride > (1ll << 38)) return LM_ERR_UNSUPPORTED;
-  *bytes = lm::plan(args->forward, true).bytes;
+  *bytes = lm::plan(*args).bytes;
   return LM_OK;
 }
 

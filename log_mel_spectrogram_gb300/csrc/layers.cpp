@@ -4,10 +4,12 @@
 
 #include <cmath>
 #include <optional>
+#include <unordered_set>
 #include <vector>
 
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/graph_task.h>
 #include <torch/csrc/autograd/variable.h>
 
 namespace lm_binding {
@@ -54,21 +56,52 @@ bool capturing(cudaStream_t s) {
   return cs != cudaStreamCaptureStatusNone;
 }
 
-// A leaf's gradient is taken by a node that is made on the stream of the first graph over it, and that
-// lives as long as one does.  Where that is the default stream, a backward pass that is being captured would make
-// that stream wait for the captured one, which ends the capture and with it the process: refused here, while
-// the forward pass is captured.
+// A node of a graph runs on the stream that it was made on, a leaf's on that of the first graph over it, and
+// that one lives as long as such a graph does.  Where that is the default stream, a backward pass that is being captured
+// would make that stream wait for the captured one, which ends the capture and with it the process.  It is refused
+// while the forward pass is captured, for leaves among the inputs, and for what lies behind them when the gradients
+// are taken.
+bool on_default_stream(torch::autograd::Node &node) {
+  const auto stream = node.stream();
+  return stream && c10::cuda::CUDAStream(*stream).stream() == nullptr;
+}
+
+[[noreturn]] void refuse_capture() {
+  throw std::runtime_error("log_mel_spectrogram_gb300: a graph of the default stream over the same leaf is alive; a "
+                           "backward pass cannot be captured beside it (delete its outputs first, or run it on a "
+                           "side stream)");
+}
+
 void no_eager_graph(std::initializer_list<const Tensor *> ts, int dev) {
   if (!capturing(c10::cuda::getCurrentCUDAStream(dev).stream())) return;
   for (const Tensor *t : ts) {
     if (!t || !t->defined() || !t->requires_grad() || t->grad_fn()) continue;
     const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
-    if (!node) continue;
-    const auto stream = node->stream();
-    if (stream && c10::cuda::CUDAStream(*stream).stream() == nullptr)
-      throw std::runtime_error("log_mel_spectrogram_gb300: a graph of the default stream over the same leaf is alive; a "
-                               "backward pass cannot be captured beside it (delete its outputs first, or run it on a "
-                               "side stream)");
+    if (node && on_default_stream(*node)) refuse_capture();
+  }
+}
+
+// ... of the nodes that the pass will come to after this one.
+void no_eager_nodes(int dev) {
+  if (!capturing(c10::cuda::getCurrentCUDAStream(dev).stream())) return;
+  const auto *const info = torch::autograd::get_current_graph_task_exec_info();  // (empty: all of them)
+  const auto here = torch::autograd::get_current_node();
+  std::vector<torch::autograd::Node *> todo;
+  std::unordered_set<torch::autograd::Node *> seen;
+  if (here) todo.push_back(here.get());
+  while (!todo.empty()) {
+    const torch::autograd::Node *const node = todo.back();
+    todo.pop_back();
+    for (const torch::autograd::Edge &e : node->next_edges()) {
+      torch::autograd::Node *const next = e.function.get();
+      if (!next || !seen.insert(next).second) continue;
+      if (info && !info->empty()) {
+        const auto at = info->find(next);
+        if (at == info->end() || !at->second.should_execute()) continue;
+      }
+      if (on_default_stream(*next)) refuse_capture();
+      todo.push_back(next);
+    }
   }
 }
 
@@ -161,6 +194,7 @@ struct NormFn : public torch::autograd::Function<NormFn> {
     const int64_t bias = ctx->saved_data["bias"].toInt();
     const int dev = x.get_device();
     const c10::cuda::OptionalCUDAGuard guard(x.device());
+    no_eager_nodes(dev);
     const int64_t width = x.size(-1);
     const Tensor g = as_rows(grads[0]);
     Tensor dx, dw, db;
@@ -299,6 +333,7 @@ struct GatedFn : public torch::autograd::Function<GatedFn> {
     const Tensor &x = saved[0], &wg = saved[1], &wu = saved[2], &bg = saved[3], &bu = saved[4];
     const int dev = x.get_device();
     const c10::cuda::OptionalCUDAGuard guard(x.device());
+    no_eager_nodes(dev);
     const Tensor g = as_rows(grads[0]);
     lm_gated_backward_args p = {};
     p.forward = gated_args(x, wg, wu, bg, bu, ctx->saved_data["act"].toInt());

@@ -90,7 +90,7 @@ PyObject *linear(PyObject *const *a) {
   } else if (!w) {
     refuse("weight must be a CUDA tensor");
   }
-  no_grad({&x, w, bias, res, given});
+  no_grad({&x, w, bias, res, given, four ? &w4.scale : nullptr});
   const int64_t dims = x.dim(), k = x.size(-1);
   if (four ? w4.code != code || w4.c.k != k
            : w->scalar_type() != x.scalar_type() || w->dim() != 2 || w->size(1) != k)

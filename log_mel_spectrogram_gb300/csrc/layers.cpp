@@ -467,6 +467,7 @@ PyObject *weight4_values(PyObject *const *a) {
   const Weight4 w = weight4_of(a[0]);
   const int code = static_cast<int>(PyLong_AsLong(a[1]));
   if (PyErr_Occurred()) return nullptr;
+  no_grad({&w.scale});
   const c10::cuda::OptionalCUDAGuard guard(w.packed.device());
   const Tensor out = make({w.c.n, w.c.k}, type_of(code), w.dev);
   if (const int rc = lm_weight4_values(&w.c, out.data_ptr(), w.c.k, code, stream_of(w.dev)); rc != LM_OK)

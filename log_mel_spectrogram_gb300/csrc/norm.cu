@@ -406,7 +406,10 @@ __global__ void __launch_bounds__(backward_threads<Part<T, TEAM, NE, VECTORS>, T
   for (int i = 0; i < Rows::kAhead; ++i) push();
   float mean = 0.0f, off = 0.0f, r = 0.0f;
   auto load_stats = [&](int64_t row) {
-    if (row >= p.rows) return;
+    if (row >= p.rows) {  // (a warp's other teams have one: zeros for n here, which the last row's mean need not give)
+      mean = off = r = 0.0f;
+      return;
+    }
     mean = p.stats[row];
     off = p.stats[p.rows + row];
     r = p.stats[2 * p.rows + row];

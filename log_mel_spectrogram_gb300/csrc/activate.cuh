@@ -105,15 +105,4 @@ __device__ __forceinline__ float activate_any(float z, int act) {
   }
 }
 
-__device__ __forceinline__ float activate_slope_any(float z, int act, float &slope) {
-  switch (act) {
-    case LM_ACT_RELU: return activate_slope<LM_ACT_RELU>(z, slope);
-    case LM_ACT_GELU: return activate_slope<LM_ACT_GELU>(z, slope);
-    case LM_ACT_GELU_TANH: return activate_slope<LM_ACT_GELU_TANH>(z, slope);
-    case LM_ACT_SILU: return activate_slope<LM_ACT_SILU>(z, slope);
-    case LM_ACT_SIGMOID: return activate_slope<LM_ACT_SIGMOID>(z, slope);
-    default: return activate_slope<LM_ACT_NONE>(z, slope);
-  }
-}
-
 }  // namespace lm

@@ -710,6 +710,7 @@ lm_status lm_kv_reorder(const lm_kv_cache *cache, const int32_t *parents, int32_
  *   eps      >= 0
  * Sums are held in 32 bits, the deviations' taken about the rounded mean and put
  * right by theirs; y is rounded once.  A NaN or infinity in a row makes the row NaN.
+ * Where the sum of a row's squared deviations passes 3.4e38 its y is bias, or NaN.
  *
  * Errors: LM_ERR_INVALID_ARG, LM_ERR_UNSUPPORTED (dtypes, sizes of 2^31 and
  * more), LM_ERR_MISALIGNED (pointers are aligned to their element), LM_ERR_CUDA.
@@ -812,8 +813,9 @@ lm_status lm_gated_linear(const lm_gated_args *args, void *workspace, size_t wor
  *   dx = da Wg + db Wu,  dWg = da^T x,  dWu = db^T x,
  *   dbg, dbu = sums of da, db over rows
  * da and db are computed and, for the biases, summed in 32 bits, and rounded to
- * dtype as operands of the products.  relu's derivative at 0 is 0.  Each
- * gradient's bits are the same whichever others are wanted.
+ * dtype as operands of the products (in f16 one past 65504 is infinite).  relu's
+ * derivative at 0 is 0.  Each gradient's bits are the same whichever others are
+ * wanted (but for db_gate and db_up where b_gate and b_up are both NULL).
  *
  *   forward  the inputs and sizes of lm_gated_linear (out and out_row_stride
  *            are not used)
@@ -894,8 +896,8 @@ lm_status lm_weight4_values(const lm_weight4 *w, void *out, int64_t row_stride, 
 /*
  * lm_linear with such a weight: args as there, but for weight and
  * weight_row_stride, which are not used; args->n and args->k are the weight's.
- * For few rows (up to 16; up to 64 where n is small) a group's products q * x
- * are summed in 32 bits and the sums multiplied by its scale.  For more the
+ * For few rows (up to 16; up to 64 where ceil(rows / 16) * n is at most 16384, 12000 for
+ * k above 1024) a group's products q * x are summed in 32 bits and the sums multiplied by its scale.  For more the
  * values are rounded to dtype on their way into the products (to within 17/16
  * of half a step: the scale is taken in two parts of dtype); for many
  * (lm_linear4_expands) they are expanded into the workspace for lm_linear.

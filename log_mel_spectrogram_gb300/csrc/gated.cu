@@ -23,9 +23,10 @@
 // 16.8 MB of weights (k over clusters).  777 x 504 -> 1008 f16 with biases and gradients 31 us, five launches of
 // about 5; 777 x 500 -> 1001 38 to 48, with copies of all operands to 16-byte boundaries in both directions.
 //
-// a and b are computed twice instead of kept: kept in 32 bits they would cost 24 bytes of
-// traffic an element more than computing them costs products up to k of about 1500, kept in 16
-// the biases' gradients would lose their 32 bits; and a training step saves the memory.
+// a and b are computed twice instead of kept: a training step keeps nothing but its inputs.  In 32 bits they would be
+// 8 bytes of memory an element, and 16 of traffic (written and read; the gradient, da and db pass either way), as much
+// time as computing them anew takes products at a k of about 1000 to 1100 (4 k operations an element, at 1710 to 1911
+// TFLOP/s): above that it is the slower way, taken for the memory.  In 16 bits the biases' gradients would lose their 32.
 #include <climits>
 
 #include "activate.cuh"
@@ -54,7 +55,10 @@ constexpr int epi_warps(Form f) { return f == Form::kSplit ? 8 : 16; }
 constexpr int threads_of(Form f) { return 128 + 32 * epi_warps(f); }
 // Blocks of k after which sums that have to be right to 32 bits go from tensor memory into registers: it loses a
 // little towards zero with each of its additions (measured at k = 912: 7e-7 of the result, systematically, where
-// additions that round are 2e-7 off), which a sum of thousands of da keeps.
+// additions that round are 2e-7 off), which a sum of thousands of da keeps.  All other sums stay in tensor memory and end
+// in 16 bits, to half a step of 2^-11 or 2^-8 of them: of products of one sign they lose 7e-10 a product (linear with f32
+// outputs 1.1e-5 at k = 16384, 1.9e-4 at 262144), of random signs a fifth of that, which a weight's gradient does not show
+// (512 x 256 in f16, over 4096 rows 2.94e-4 off in the norm, over 200000 2.95e-4).
 constexpr int kSumBlocks = 4;
 // Parts of a tile's columns whose sums of da and db are kept apart.
 constexpr int kColumnParts = epi_warps(Form::kOne) / 4;

@@ -4,8 +4,8 @@
 // Few rows of x: the weight's bytes bound the call.  They are laid out so that a lane's 16 bytes of
 // a tile are its operands of four m16n8k16 products with W as the 16 rows, and 16 bytes of x twice the
 // other operand: neither goes through shared memory, and a nibble becomes a 16-bit float by an OR into
-// the mantissa of 1024 (f16) or 128 (bf16) and an exact subtraction.  (tcgen05 takes no operand that has to
-// be converted first without a pass through shared memory.)  A warp sums a tile of 16 outputs over a part of
+// the mantissa of 1024 (f16) or 128 (bf16) and an exact subtraction.  (For tcgen05 a converted operand has to be
+// written to shared or tensor memory first.)  A warp sums a tile of 16 outputs over a part of
 // k, a group's products in 32 bits and then times its scale; the warps of a CTA share out tiles and
 // k, meet in shared memory, and write whole lines.
 //
@@ -786,7 +786,11 @@ bool few(int64_t rows, int64_t n, int64_t k) {
   return rows <= 16 || (rows <= 64 && up(rows, 16) * n <= (k <= 1024 ? 16384 : 12000));
 }
 
-// From this many rows on the products cost more than expanding the weight.
+// From this many rows on the products cost more than expanding the weight.  (us, tiles and expanded: 768 rows x 1024 -> 4096
+// 9.7, 11.3, 3000 rows 24.1, 20.8; 4096 -> 4096 23.9, 23.9 and 74.6, 59.3; 2048 -> 8192 24.7, 23.7 and 77.8, 60.4; 1024 ->
+// 50001 60.3, 71.3 and 234, 208.  Of nine weights seven cross between 256 and 2048 rows, whatever n and k, and the smallest,
+// 512 -> 512 and 256 -> 1024, stay 2 to 12% apart.  The rule's choice is up to 18% slower than the other at 768 and 1024 rows
+// (8192 -> 2048 31.5, 26.6; 1024 -> 4096 13.2, 11.3), 8% elsewhere, and 30% at 512 x 4096 -> 4096 (25.7, 19.7).)
 bool expands(int64_t rows, int64_t n, int64_t) { return rows > 768 && n <= 65535 * 128; }
 
 // ... of a weight with contents.

@@ -424,21 +424,31 @@ struct Scale {
   uint32_t high, low;
 };
 
+// Both of a number, rounded; of bf16 at most its largest value.
+template <typename T>
+__device__ __forceinline__ uint32_t first_part(float s) {
+  if (std::is_same<T, __half>::value) return pack2<T>(s, s);
+  uint32_t r;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(s));
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ Scale<T> split_scale(float s) {
   Scale<T> o;
-  o.high = pack2<T>(s, s);
+  o.high = first_part<T>(s);
   const float low = s - unpack2<T>(o.high).x;
   o.low = pack2<T>(low, low);
   return o;
 }
 
-// Whether the parts stand for the scale: it is finite in T (of an infinite first part 0 times it is NaN), and in f16,
-// whose steps end at 2^-24, not too small (see widen_scaled).
+// Whether the parts stand for the scale.  Those of f16 do up to its largest value (past it the second may be infinite, and
+// 0 times it NaN) and, because its steps end at 2^-24, down to 2^-10 (see widen_scaled).  Those of bf16 always do: a
+// finite scale leaves a finite second part, an infinite one an infinite, and 0 times the scale is 0 or NaN.
 template <typename T>
 __device__ __forceinline__ bool splits(float s) {
   const float a = fabsf(s);
-  return std::is_same<T, __half>::value ? a >= 0x1p-10f && a <= 65504.0f : a <= 0x1.fep127f;
+  return !std::is_same<T, __half>::value || (a >= 0x1p-10f && a <= 65504.0f);
 }
 
 __device__ __forceinline__ __half2 as2(uint32_t v, __half) { return *reinterpret_cast<const __half2 *>(&v); }
@@ -488,7 +498,7 @@ __device__ __forceinline__ void widen_stage(const uint8_t *slot, const float *sc
       parts = parts && splits<T>(f[j][h][0]) && splits<T>(f[j][h][1]);
     }
   }
-  if (!__all_sync(0xffffffffu, parts)) {  // a warp's other rows get the same bits either way
+  if (std::is_same<T, __half>::value && !__all_sync(0xffffffffu, parts)) {  // a warp's other rows get the same bits either way
 #pragma unroll 1
     for (int h = 0; h < 2 * TILES; ++h) {
       const uint4 u = reinterpret_cast<const uint4 *>(slot + h / 2 * kTileBytes)[lane];

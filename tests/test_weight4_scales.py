@@ -69,3 +69,23 @@ def test_other_outputs_keep_their_bits(lm, dtype, rows, odd):
     got = lm.linear(x, lm.Weight4.pack(q, s, group=32, dtype=dtype))
     keep = [i for i in range(150) if i not in (7, 100)]
     assert torch.equal(got[:, keep], want[:, keep])
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scales_that_are_not_finite(lm, dtype, rows):
+    """As values() says: q times infinity is infinite, or NaN where q is 0, and so is what x adds up to."""
+    q, s = numbers(150, 300, 32, seed=5)
+    q[7], q[9] = 1, -1  # no zeros: the sums are infinite
+    q[11, 70] = 0
+    s[7, 2], s[9, 5], s[11, 2], s[13, 1] = float("inf"), float("inf"), float("inf"), float("nan")
+    w4 = lm.Weight4.pack(q, s, group=32, dtype=dtype)
+    v = w4.values()
+    assert (v[7, 64:96] == float("inf")).all() and (v[9, 160:192] == -float("inf")).all()
+    assert v[11, 70].isnan() and v[13, 32:64].isnan().all()
+    x = torch.rand((rows, 300), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(dtype) + 0.25
+    y = lm.linear(x, w4)
+    assert (y[:, 7] == float("inf")).all() and (y[:, 9] == -float("inf")).all()
+    assert not y[:, 11].isfinite().any() and y[:, 13].isnan().all()
+    keep = [i for i in range(150) if i not in (7, 9, 11, 13)]
+    assert y[:, keep].isfinite().all()

@@ -37,7 +37,7 @@ MELS, TAPS = 80, 3
 class Layer:
     """Weights of one block: attention (and, in a decoder, attention over the encoder), feed-forward."""
 
-    def __init__(self, width: int, cross: bool, rand, gated: bool):
+    def __init__(self, width: int, cross: bool, rand, gated: bool = False):
         def dense(n, k):
             return rand(n, k) / math.sqrt(k)
         self.qkv, self.qkv_bias = dense(3 * width, width), torch.zeros(3 * width, device="cuda")

@@ -1,6 +1,6 @@
 """Calls that are a host thread's first to CUDA.
 
-Tensor maps are made by the driver, which wants the thread to have a context; CUDA's runtime, which the library uses
+Tensor maps are made by the CUDA driver, which wants the thread to have a context; CUDA's runtime, which the library uses
 otherwise, gives a thread one at its first call.  The thread of torch's engine that runs backward passes is such a
 thread, and a program's own threads are.  The operands here need no copies, which would be launches before the maps.
 """
